@@ -83,6 +83,21 @@ extern "C" {
 #define MOE_Q4_CODEC_AFFINE8_G64 4 /* 8-bit affine, bf16 scale + bias per 64 inputs                      */
 #define MOE_Q4_CODEC_MXFP8 5       /* FP8 E4M3 elements, one E8M0 scale byte per 32 inputs             */
 
+/* ---- element types (the operators beside the expert layer; the first two are the MOE_Q4_OUT_* values) ---- */
+#define MOE_Q4_DTYPE_BF16 0
+#define MOE_Q4_DTYPE_F32 1
+#define MOE_Q4_DTYPE_F16 2
+
+/* ---- router scores ---- */
+#define MOE_Q4_SCORE_SOFTMAX 0
+#define MOE_Q4_SCORE_SIGMOID 1
+
+/* ---- limits of the operators beside the expert layer ---- */
+#define MOE_Q4_ROUTER_MAX_K 64       /* routes per token of moe_router_topk                    */
+#define MOE_Q4_BALANCE_MAX_SEQS 65535 /* sequences of one moe_balance_loss call                 */
+#define MOE_Q4_LINEAR_MAX_L 1048560  /* tokens of one moe_linear_codec_forward call            */
+#define MOE_Q4_LINEAR_MAX_K 1048576  /* inputs of a row of moe_linear_codec_forward            */
+
 /* ---- forward stages (moe_swiglu_q4_forward_stages) ---- */
 #define MOE_Q4_STAGE_GATEUP 1u   /* union (or sort) + fused gate/up + silu(gate)*up -> workspace  */
 #define MOE_Q4_STAGE_DOWN 2u     /* down projection + router-weighted combine -> out              */
@@ -319,6 +334,107 @@ int moe_sort_pairs_tiles_max(int L, int k, int E, int bm);
 int moe_sort_pairs(const int32_t *topk_ids, int L, int k, int E, int bm, int32_t *offsets,
                    int32_t *perm, int32_t *inv, int32_t *tiles, int tiles_cap, uint32_t *info,
                    int32_t *scratch, hipStream_t stream);
+
+/*
+ * Dense product with 4-bit weights, for the projections around the experts:
+ *
+ *   out[t, n] = sum_c x[t, c] * W[n, c] + bias[n]
+ *
+ * with W in one of the 4-bit codecs (MOE_Q4_CODEC_AFFINE4_G64, _AFFINE4_G32,
+ * _MXFP4, _NVFP4), stored as one expert's matrix of a bank is.
+ *
+ *   x          bf16 or fp16 [L, K] (x_dtype), rows ldx elements apart
+ *              (16-byte aligned, ldx a multiple of 8 where L > 1)
+ *   w          uint32 [N, K/8] codes                          (16-byte aligned)
+ *   s          [N, K/gs] scales: bf16 (affine; 2-byte aligned), uint8 E8M0
+ *              (mxfp4) or uint8 E4M3 (nvfp4; 2-byte aligned)
+ *   b          bf16 [N, K/gs] biases of the affine codecs; ignored otherwise
+ *   bias       fp32 [N], or NULL
+ *   L, N, K    tokens, outputs, inputs; K a multiple of 64 for AFFINE4_G64, of
+ *              32 otherwise; L and N are any
+ *   out        [L, N] in out_dtype (MOE_Q4_DTYPE_*), rows ldo elements apart,
+ *              fully overwritten; must not overlap an input or the workspace
+ *   workspace  moe_linear_codec_workspace_bytes bytes (256-byte aligned, no
+ *              initialisation; NULL where that is 0); not shared by calls that
+ *              may run at the same time
+ *
+ * Products are exact, sums are fp32 and rounded once to out_dtype; results are
+ * deterministic.  L == 0 returns MOE_Q4_OK without touching the GPU.  Needs
+ * L <= MOE_Q4_LINEAR_MAX_L and K <= MOE_Q4_LINEAR_MAX_K.
+ */
+int moe_linear_codec_forward(int codec, const void *x, int x_dtype, long long ldx, const uint32_t *w,
+                             const void *s, const void *b, const float *bias, int L, int N, int K,
+                             void *out, int out_dtype, long long ldo, void *workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of moe_linear_codec_forward; 0 also for an invalid or unsupported shape.  Host only. */
+size_t moe_linear_codec_workspace_bytes(int codec, int L, int N, int K);
+
+/*
+ * The router's selection: topk_ids and topk_weights of the layer from router
+ * logits.
+ *
+ *   logits      [T, E] in logits_dtype, rows ld elements apart
+ *   select_bias fp32 [E] or NULL: added to the scores for the choice only
+ *   score       MOE_Q4_SCORE_SOFTMAX: p = softmax(z) over the row;
+ *               MOE_Q4_SCORE_SIGMOID: p = sigmoid(z)
+ *   topk_ids    int32 [T, k]: the k experts with the largest z (with
+ *               select_bias: the largest p + select_bias), in falling order
+ *   topk_weights fp32 [T, k]: scale * p_j / (sum of the chosen p) with
+ *               renormalize = 1, scale * p_j with 0
+ *
+ * Equal values go to the lower expert; scores with a bias that fp32 cannot
+ * tell apart are compared in 64 bits.  A logit of -inf (a masked expert) has
+ * score 0; so do all experts of a row of nothing else, whose weights are 0
+ * and whose ids are the lowest.  NaN logits rank below -inf.  ids are always
+ * k different experts.  1 <= k <= MOE_Q4_ROUTER_MAX_K, E <= MOE_Q4_MAX_E.
+ */
+int moe_router_topk(const void *logits, int logits_dtype, long long ld, const float *select_bias, int T,
+                    int k, int E, int score, int renormalize, float scale, int32_t *topk_ids,
+                    float *topk_weights, hipStream_t stream);
+
+/*
+ * Gradient of moe_router_topk's weights, the choice held fixed: dlogits
+ * [T, E] (logits_dtype, rows ldd elements apart, fully overwritten) from
+ * dweights fp32 [T, k].  An id outside [0, E) is left out; a repeated one
+ * counts each time.
+ */
+int moe_router_topk_backward(const void *logits, int logits_dtype, long long ld, const int32_t *topk_ids,
+                             const float *dweights, int T, int k, int E, int score, int renormalize,
+                             float scale, void *dlogits, long long ldd, hipStream_t stream);
+
+/*
+ * Balance loss and route counts of S sequences of T tokens each.  With n
+ * unmasked tokens in a sequence, c_e routes of theirs to expert e and P_e the
+ * mean over them of p (softmax(z), or sigmoid(z) over its row sum):
+ *
+ *   loss = coef * E / (k * n) * sum_e c_e P_e
+ *
+ *   logits     [S * T, E] in logits_dtype, rows ld elements apart
+ *   topk_ids   int32 [S * T, k]; ids outside [0, E) count nowhere
+ *   token_mask uint8 [S * T] or NULL: 0 leaves a token out (padding)
+ *   loss       fp32 [S] (0 for a sequence without tokens)
+ *   counts     int32 [S, E];  tokens int32 [S]: c_e and n
+ *   workspace  moe_balance_loss_workspace_bytes(S, T, E) bytes (256-byte
+ *              aligned, no initialisation)
+ *
+ * Sums are fp32 in a fixed order.  S <= MOE_Q4_BALANCE_MAX_SEQS.
+ */
+int moe_balance_loss(const void *logits, int logits_dtype, long long ld, const int32_t *topk_ids,
+                     const uint8_t *token_mask, int S, int T, int k, int E, int score, float coef,
+                     float *loss, int32_t *counts, int32_t *tokens, void *workspace,
+                     size_t workspace_bytes, hipStream_t stream);
+size_t moe_balance_loss_workspace_bytes(int S, int T, int E);
+
+/*
+ * Gradient of moe_balance_loss with the counts held fixed: dlogits [S * T, E]
+ * (logits_dtype, rows ldd elements apart, fully overwritten; 0 for masked
+ * tokens) from dloss fp32 [S] and the forward's counts and tokens.
+ */
+int moe_balance_loss_backward(const void *logits, int logits_dtype, long long ld, const uint8_t *token_mask,
+                              const int32_t *counts, const int32_t *tokens, const float *dloss, int S,
+                              int T, int k, int E, int score, float coef, void *dlogits, long long ldd,
+                              hipStream_t stream);
 
 /*
  * Reads the device status word (MOE_Q4_DEV_* bits) that the last forward

@@ -45,10 +45,24 @@ MOE_Q4_CODEC_MXFP8 = 5
 CODECS = {"affine4_g64": (MOE_Q4_CODEC_AFFINE4_G64, 64, 4), "affine4_g32": (MOE_Q4_CODEC_AFFINE4_G32, 32, 4),
           "mxfp4": (MOE_Q4_CODEC_MXFP4, 32, 4), "nvfp4": (MOE_Q4_CODEC_NVFP4, 16, 4),
           "affine8_g64": (MOE_Q4_CODEC_AFFINE8_G64, 64, 8), "mxfp8": (MOE_Q4_CODEC_MXFP8, 32, 8)}
+#: MOE_Q4_CODEC_* of the 4-bit codecs -> inputs per scale group, whether it has biases
+_LINEAR_CODECS = {MOE_Q4_CODEC_AFFINE4_G64: (64, True), MOE_Q4_CODEC_AFFINE4_G32: (32, True),
+                  MOE_Q4_CODEC_MXFP4: (32, False), MOE_Q4_CODEC_NVFP4: (16, False)}
+MOE_Q4_DTYPE_BF16 = 0
+MOE_Q4_DTYPE_F32 = 1
+MOE_Q4_DTYPE_F16 = 2
+MOE_Q4_SCORE_SOFTMAX = 0
+MOE_Q4_SCORE_SIGMOID = 1
+#: score names of the router's selection and the balance loss -> MOE_Q4_SCORE_*
+SCORES = {"softmax": MOE_Q4_SCORE_SOFTMAX, "sigmoid": MOE_Q4_SCORE_SIGMOID}
 MOE_Q4_UNION_MAX_L = 32
 MOE_Q4_MAX_PAIRS = 1024
 MOE_Q4_CODEC_MAX_L = 65535
 MOE_Q4_NOALLOC_SCRATCH_BYTES = 16 << 20
+MOE_Q4_ROUTER_MAX_K = 64
+MOE_Q4_BALANCE_MAX_SEQS = 65535
+MOE_Q4_LINEAR_MAX_L = 1048560
+MOE_Q4_LINEAR_MAX_K = 1048576
 
 EXPORTS = (
     "moe_swiglu_q4_workspace_bytes",
@@ -65,6 +79,13 @@ EXPORTS = (
     "moe_route_union",
     "moe_sort_pairs_tiles_max",
     "moe_sort_pairs",
+    "moe_linear_codec_workspace_bytes",
+    "moe_linear_codec_forward",
+    "moe_router_topk",
+    "moe_router_topk_backward",
+    "moe_balance_loss_workspace_bytes",
+    "moe_balance_loss",
+    "moe_balance_loss_backward",
     "moe_q4_read_device_status",
     "moe_q4_clear_device_status",
     "moe_q4_status_string",
@@ -121,6 +142,21 @@ def lib() -> ctypes.CDLL:
     L.moe_sort_pairs_tiles_max.restype = I32
     L.moe_sort_pairs.argtypes = [P, I32, I32, I32, I32, P, P, P, P, I32, P, P, P]
     L.moe_sort_pairs.restype = I32
+    LL, F32 = ctypes.c_longlong, ctypes.c_float
+    L.moe_linear_codec_workspace_bytes.argtypes = [I32] * 4
+    L.moe_linear_codec_workspace_bytes.restype = SZ
+    L.moe_linear_codec_forward.argtypes = [I32, P, I32, LL, P, P, P, P, I32, I32, I32, P, I32, LL, P, SZ, P]
+    L.moe_linear_codec_forward.restype = I32
+    L.moe_router_topk.argtypes = [P, I32, LL, P, I32, I32, I32, I32, I32, F32, P, P, P]
+    L.moe_router_topk.restype = I32
+    L.moe_router_topk_backward.argtypes = [P, I32, LL, P, P, I32, I32, I32, I32, I32, F32, P, LL, P]
+    L.moe_router_topk_backward.restype = I32
+    L.moe_balance_loss_workspace_bytes.argtypes = [I32] * 3
+    L.moe_balance_loss_workspace_bytes.restype = SZ
+    L.moe_balance_loss.argtypes = [P, I32, LL, P, P, I32, I32, I32, I32, I32, F32, P, P, P, P, SZ, P]
+    L.moe_balance_loss.restype = I32
+    L.moe_balance_loss_backward.argtypes = [P, I32, LL, P, P, P, P, I32, I32, I32, I32, I32, F32, P, LL, P]
+    L.moe_balance_loss_backward.restype = I32
     L.moe_q4_read_device_status.argtypes = [P, P, P, P]
     L.moe_q4_read_device_status.restype = I32
     L.moe_q4_clear_device_status.argtypes = [P, P]
@@ -529,3 +565,10 @@ def moe_q4_stream_read(buf: torch.Tensor, sink: torch.Tensor, stream=None) -> No
     st = lib().moe_q4_stream_read(_dev_ptr(buf, (buf.dtype,), "buf"), buf.numel() * buf.element_size(),
                                   _dev_ptr(sink, _I32, "sink"), sink.numel(), _stream_ptr(stream))
     _check(st, "moe_q4_stream_read")
+
+
+# ---- operators beside the expert layer ----
+
+from .dense import PreparedLinear, moe_linear_codec_forward, moe_linear_codec_workspace_bytes  # noqa: E402
+from .router import (moe_balance_loss, moe_balance_loss_backward, moe_balance_loss_workspace_bytes,  # noqa: E402
+                     moe_router_topk, moe_router_topk_backward)

@@ -1,0 +1,352 @@
+// The router's balance loss and the per-expert route counts, with the loss's
+// gradient.  Per sequence of n unmasked tokens:
+//
+//   p = softmax(z), or sigmoid(z) over its row sum;  P_e = sum_t p[t, e] / n;
+//   c_e = number of routes to e;  loss = coef * E / (k * n) * sum_e c_e P_e;
+//   dz = p (a - sum_e a_e p_e) (softmax; times 1 - sigmoid(z) for sigmoid),
+//   a_e = dloss * coef * E * c_e / (k * n^2), the counts held fixed.
+//
+// Forward: a workgroup sums p over its run of tokens in registers (a wave
+// holds whole rows) and its routes in an LDS histogram of integers, and
+// leaves one row of partials in the workspace; a second launch adds the
+// partials in a fixed order.  Nothing depends on an order of atomics.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <stdint.h>
+
+#include "moe_q4.h"
+#include "moe_router_device.h"
+
+namespace moeq4 {
+namespace {
+
+constexpr int kWaves = 4;  // waves of a forward / backward workgroup, one row each at a time (E <= 1024)
+
+struct BalanceArgs {
+  const void* z;
+  const int32_t* ids;
+  const uint8_t* mask;
+  float* psum;      // [S][blocks][E] partial sums of p
+  int32_t* pcount;  // [S][blocks][E] partial route counts
+  int32_t* ptok;    // [S][blocks] unmasked tokens
+  float* loss;
+  int32_t* counts;
+  int32_t* tokens;
+  long long ld;
+  int S, T, k, E, score, vec;
+  int blocks, per;  // workgroups of a sequence, tokens of each
+  float coef;
+};
+
+// p of one row in place of its logits; returns the sigmoid's row factors
+// untouched: v holds p, and `damp` (if asked for) 1 - sigmoid(z).
+template <int EPL, int WPR, bool DAMP>
+__device__ __forceinline__ void row_probabilities(float (&v)[EPL], float (&damp)[EPL], int base, int E, int score,
+                                                  float* red) {
+  float sum = 0.0f;
+  if (score == kRouterScoreSoftmax) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
+    m = row_all<WPR>(m, OpMaxF(), red);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      v[i] = exp_below(v[i], m);
+      sum += v[i];
+      if constexpr (DAMP) damp[i] = 1.0f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const float z = v[i];
+      v[i] = base + i < E ? sigmoid_f32(z) : 0.0f;
+      if constexpr (DAMP) damp[i] = sigmoid_f32(-z);
+      sum += v[i];
+    }
+  }
+  sum = row_all<WPR>(sum, OpSumF(), red);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) v[i] *= inv;
+}
+
+template <class LT, int EPL, int WPR>
+__global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kWaves) void k_balance_partial(BalanceArgs a) {
+  typedef typename LT::mem mem;
+  extern __shared__ unsigned char lds[];
+  float* red = reinterpret_cast<float*>(lds);          // [16]
+  int32_t* ntok = reinterpret_cast<int32_t*>(lds) + 16;  // [1], padded to 16
+  int32_t* hist = reinterpret_cast<int32_t*>(lds) + 32;  // [E]
+  float* sums = reinterpret_cast<float*>(hist + a.E);    // [kWaves][E] (WPR == 1)
+  const int tid = threadIdx.x, nthr = blockDim.x, wave = tid >> 6;
+  const int slot = WPR > 1 ? tid : (tid & 63);
+  const int base = slot * EPL;
+  const int t0 = blockIdx.x * a.per, t1 = min(a.T, t0 + a.per);
+  const size_t seq = (size_t)blockIdx.y * a.T;
+
+  for (int e = tid; e < a.E; e += nthr) hist[e] = 0;
+  if (tid == 0) ntok[0] = 0;
+  __syncthreads();
+  for (int t = t0 + tid; t < t1; t += nthr) {
+    if (a.mask && !a.mask[seq + t]) continue;
+    atomicAdd(ntok, 1);
+    const int32_t* ids = a.ids + (seq + t) * a.k;
+    for (int j = 0; j < a.k; ++j) {
+      const int e = ids[j];
+      if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
+    }
+  }
+
+  float acc[EPL], damp[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
+  for (int t = t0 + (WPR > 1 ? 0 : wave); t < t1; t += WPR > 1 ? 1 : kWaves) {
+    if (a.mask && !a.mask[seq + t]) continue;  // the same for all threads of the row
+    float v[EPL];
+    load_row<LT, EPL>(static_cast<const mem*>(a.z) + (seq + t) * a.ld, base, a.E, a.vec, -__builtin_inff(), v);
+    row_probabilities<EPL, WPR, false>(v, damp, base, a.E, a.score, red);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) acc[i] += v[i];
+  }
+
+  const size_t part = ((size_t)blockIdx.y * a.blocks + blockIdx.x) * a.E;
+  if constexpr (WPR == 1) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (base + i < a.E) sums[wave * a.E + base + i] = acc[i];
+    __syncthreads();
+    for (int e = tid; e < a.E; e += nthr) {
+      float s = sums[e];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) s += sums[w * a.E + e];
+      a.psum[part + e] = s;
+      a.pcount[part + e] = hist[e];
+    }
+  } else {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (base + i < a.E) a.psum[part + base + i] = acc[i];
+    for (int e = tid; e < a.E; e += nthr) a.pcount[part + e] = hist[e];
+  }
+  if (tid == 0) a.ptok[(size_t)blockIdx.y * a.blocks + blockIdx.x] = ntok[0];
+}
+
+// Adds a sequence's partials: counts, token count and loss.
+__global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a) {
+  __shared__ float redf[16];
+  __shared__ int redi[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const size_t part = (size_t)blockIdx.x * a.blocks;
+  int n = 0;
+  for (int b = tid; b < a.blocks; b += 1024) n += a.ptok[part + b];
+  float dot = 0.0f;
+  for (int e = tid; e < a.E; e += 1024) {
+    float s = 0.0f;
+    int c = 0;
+    for (int b = 0; b < a.blocks; ++b) {
+      s += a.psum[(part + b) * a.E + e];
+      c += a.pcount[(part + b) * a.E + e];
+    }
+    a.counts[(size_t)blockIdx.x * a.E + e] = c;
+    dot += (float)c * s;
+  }
+  for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
+  dot = wave_all(dot, OpSumF());
+  if (lane == 0) {
+    redf[wave] = dot;
+    redi[wave] = n;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < 16; ++w) {
+      dot += redf[w];
+      n += redi[w];
+    }
+    a.tokens[blockIdx.x] = n;
+    const float nf = (float)n;
+    a.loss[blockIdx.x] = n ? a.coef * (float)a.E / ((float)a.k * nf) * (dot / nf) : 0.0f;
+  }
+}
+
+struct BalanceBackArgs {
+  const void* z;
+  const uint8_t* mask;
+  const int32_t* counts;
+  const int32_t* tokens;
+  const float* dloss;
+  void* dz;
+  long long ld, ldd;
+  int S, T, k, E, score, vec, vecd;
+  int per;
+  float coef;
+};
+
+template <class LT, int EPL, int WPR>
+__global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kWaves) void k_balance_backward(BalanceBackArgs a) {
+  typedef typename LT::mem mem;
+  __shared__ float red[16];
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int slot = WPR > 1 ? tid : (tid & 63);
+  const int base = slot * EPL;
+  const int t0 = blockIdx.x * a.per, t1 = min(a.T, t0 + a.per);
+  const size_t seq = (size_t)blockIdx.y * a.T;
+  const float n = (float)a.tokens[blockIdx.y];
+  const float f = n > 0.0f ? a.dloss[blockIdx.y] * a.coef * ((float)a.E / ((float)a.k * n)) / n : 0.0f;
+  float w[EPL], v[EPL], damp[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) w[i] = base + i < a.E ? f * (float)a.counts[(size_t)blockIdx.y * a.E + base + i] : 0.0f;
+  for (int t = t0 + (WPR > 1 ? 0 : wave); t < t1; t += WPR > 1 ? 1 : kWaves) {
+    if (a.mask && !a.mask[seq + t]) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = 0.0f;
+    } else {
+      load_row<LT, EPL>(static_cast<const mem*>(a.z) + (seq + t) * a.ld, base, a.E, a.vec, -__builtin_inff(), v);
+      row_probabilities<EPL, WPR, true>(v, damp, base, a.E, a.score, red);
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) dot += w[i] * v[i];
+      dot = row_all<WPR>(dot, OpSumF(), red);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = v[i] * damp[i] * (w[i] - dot);
+    }
+    store_row<LT, EPL>(static_cast<mem*>(a.dz) + (seq + t) * a.ldd, base, a.E, a.vecd, v);
+  }
+}
+
+// Tokens of a workgroup: enough workgroups to fill the card, few enough that
+// the second launch has little to add.
+constexpr int kMaxBlocks = 256;
+int blocks_of(int S, int T, int E) {
+  const int rows = E > 1024 ? 1 : kWaves;
+  const int want = std::max(1, kMaxBlocks / std::max(1, S));
+  return std::max(1, std::min(want, (T + rows - 1) / rows));
+}
+
+struct BalanceWorkspace {
+  size_t psum, pcount, ptok, total;
+};
+size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
+BalanceWorkspace balance_layout(int S, int T, int E) {
+  BalanceWorkspace w{};
+  const size_t rows = (size_t)S * blocks_of(S, T, E);
+  size_t off = 0;
+  w.psum = off;   off = round256(off + rows * E * 4);
+  w.pcount = off; off = round256(off + rows * E * 4);
+  w.ptok = off;   off = round256(off + rows * 4);
+  w.total = off;
+  return w;
+}
+
+int check_balance(int dtype, long long ld, int S, int T, int k, int E, int score) {
+  if (S < 0 || T < 0 || k < 1 || E < 1 || k > E || ld < E) return MOE_Q4_ERR_SHAPE;
+  if (E > MOE_Q4_MAX_E || S > MOE_Q4_BALANCE_MAX_SEQS) return MOE_Q4_ERR_UNSUPPORTED;
+  if (dtype != MOE_Q4_DTYPE_BF16 && dtype != MOE_Q4_DTYPE_F32 && dtype != MOE_Q4_DTYPE_F16) return MOE_Q4_ERR_UNSUPPORTED;
+  if (score != MOE_Q4_SCORE_SOFTMAX && score != MOE_Q4_SCORE_SIGMOID) return MOE_Q4_ERR_UNSUPPORTED;
+  return MOE_Q4_OK;
+}
+
+bool aligned_to(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return na && nb && x < y + nb && y < x + na;
+}
+size_t span(size_t rows, long long ld, int E, size_t es) { return rows ? ((rows - 1) * (size_t)ld + (size_t)E) * es : 0; }
+
+}  // namespace
+}  // namespace moeq4
+
+using namespace moeq4;
+
+extern "C" size_t moe_balance_loss_workspace_bytes(int S, int T, int E) {
+  if (S < 1 || T < 0 || E < 1 || E > MOE_Q4_MAX_E || S > MOE_Q4_BALANCE_MAX_SEQS) return 0;
+  return balance_layout(S, T, E).total;
+}
+
+extern "C" int moe_balance_loss(const void* logits, int logits_dtype, long long ld, const int32_t* topk_ids,
+                                const uint8_t* token_mask, int S, int T, int k, int E, int score, float coef,
+                                float* loss, int32_t* counts, int32_t* tokens, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  const int st = check_balance(logits_dtype, ld, S, T, k, E, score);
+  if (st) return st;
+  if (S == 0) return MOE_Q4_OK;
+  if (!loss || !counts || !tokens || (T > 0 && (!logits || !topk_ids))) return MOE_Q4_ERR_NULL;
+  if (!workspace) return MOE_Q4_ERR_WORKSPACE;
+  const size_t es = logits_dtype == MOE_Q4_DTYPE_F32 ? 4 : 2;
+  if (!aligned_to(logits, es) || !aligned_to(topk_ids, 4) || !aligned_to(loss, 4) || !aligned_to(counts, 4) ||
+      !aligned_to(tokens, 4) || !aligned_to(workspace, 256))
+    return MOE_Q4_ERR_ALIGN;
+  const BalanceWorkspace lay = balance_layout(S, T, E);
+  if (workspace_bytes < lay.total) return MOE_Q4_ERR_WORKSPACE;
+  const size_t rows = (size_t)S * T;
+  const struct { const void* p; size_t n; } ins[] = {{logits, span(rows, ld, E, es)}, {topk_ids, rows * k * 4},
+                                                     {token_mask, token_mask ? rows : 0}, {workspace, lay.total}};
+  const struct { const void* p; size_t n; } outs[] = {{loss, (size_t)S * 4}, {counts, (size_t)S * E * 4},
+                                                      {tokens, (size_t)S * 4}};
+  for (const auto& o : outs)
+    for (const auto& in : ins)
+      if (overlap(o.p, o.n, in.p, in.n)) return MOE_Q4_ERR_ALIAS;
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return MOE_Q4_ERR_ALIAS;
+  const RowPlan plan = row_plan(E);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  BalanceArgs a{};
+  a.z = logits;
+  a.ids = topk_ids;
+  a.mask = token_mask;
+  a.psum = reinterpret_cast<float*>(ws + lay.psum);
+  a.pcount = reinterpret_cast<int32_t*>(ws + lay.pcount);
+  a.ptok = reinterpret_cast<int32_t*>(ws + lay.ptok);
+  a.loss = loss;
+  a.counts = counts;
+  a.tokens = tokens;
+  a.ld = ld;
+  a.S = S; a.T = T; a.k = k; a.E = E;
+  a.score = score;
+  a.vec = row_vec(logits, ld, E, plan.epl, (int)es);
+  a.blocks = blocks_of(S, T, E);
+  a.per = (T + a.blocks - 1) / a.blocks;
+  a.coef = coef;
+  const dim3 grid(a.blocks, S), block(plan.wpr > 1 ? 64 * plan.wpr : 64 * kWaves);
+  const size_t lds = 128 + (size_t)E * 4 + (plan.wpr > 1 ? 0 : (size_t)kWaves * E * 4);
+#define MOE_BALANCE_CALL(LT, EPL, WPR) hipLaunchKernelGGL((k_balance_partial<LT, EPL, WPR>), grid, block, lds, stream, a)
+  MOE_ROW_DISPATCH(logits_dtype, plan, MOE_BALANCE_CALL)
+  if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
+  hipLaunchKernelGGL(k_balance_finish, dim3(S), dim3(1024), 0, stream, a);
+  return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+}
+
+extern "C" int moe_balance_loss_backward(const void* logits, int logits_dtype, long long ld, const uint8_t* token_mask,
+                                         const int32_t* counts, const int32_t* tokens, const float* dloss, int S,
+                                         int T, int k, int E, int score, float coef, void* dlogits, long long ldd,
+                                         hipStream_t stream) {
+  const int st = check_balance(logits_dtype, ld, S, T, k, E, score);
+  if (st) return st;
+  if (ldd < E) return MOE_Q4_ERR_SHAPE;
+  if (S == 0 || T == 0) return MOE_Q4_OK;
+  if (!logits || !counts || !tokens || !dloss || !dlogits) return MOE_Q4_ERR_NULL;
+  const size_t es = logits_dtype == MOE_Q4_DTYPE_F32 ? 4 : 2;
+  if (!aligned_to(logits, es) || !aligned_to(dlogits, es) || !aligned_to(counts, 4) || !aligned_to(tokens, 4) ||
+      !aligned_to(dloss, 4))
+    return MOE_Q4_ERR_ALIGN;
+  const size_t rows = (size_t)S * T, out = span(rows, ldd, E, es);
+  if (overlap(dlogits, out, logits, span(rows, ld, E, es)) || overlap(dlogits, out, token_mask, token_mask ? rows : 0) ||
+      overlap(dlogits, out, counts, (size_t)S * E * 4) || overlap(dlogits, out, tokens, (size_t)S * 4) ||
+      overlap(dlogits, out, dloss, (size_t)S * 4))
+    return MOE_Q4_ERR_ALIAS;
+  const RowPlan plan = row_plan(E);
+  BalanceBackArgs a{logits, token_mask, counts, tokens, dloss, dlogits, ld, ldd, S, T, k, E, score, 0, 0, 0, coef};
+  a.vec = row_vec(logits, ld, E, plan.epl, (int)es);
+  a.vecd = row_vec(dlogits, ldd, E, plan.epl, (int)es);
+  const int unit = plan.wpr > 1 ? 1 : kWaves;
+  const int want = std::max(1, 2048 / S);
+  const int blocks = std::max(1, std::min(want, (T + unit - 1) / unit));
+  a.per = (T + blocks - 1) / blocks;
+  const dim3 grid((T + a.per - 1) / a.per, S), block(plan.wpr > 1 ? 64 * plan.wpr : 64 * kWaves);
+#define MOE_BALANCE_BACK_CALL(LT, EPL, WPR) \
+  hipLaunchKernelGGL((k_balance_backward<LT, EPL, WPR>), grid, block, 0, stream, a)
+  MOE_ROW_DISPATCH(logits_dtype, plan, MOE_BALANCE_BACK_CALL)
+  return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+}

@@ -1,0 +1,130 @@
+// Device helpers of the dense 4-bit product: matrix-core operands out of
+// packed codes.  Internal header.
+//
+// A wave takes 128 inputs of 16 weight rows at a time: lane (n, kb) = (lane %
+// 16, lane / 16) loads 16 bytes (32 codes) of row n at input 32 kb, 64
+// contiguous bytes a row.  v_mfma_f32_16x16x32 sums 32 inputs, eight from
+// each kb; a scale group must not be mixed with another in one sum, so the
+// affine and mxfp4 words are transposed over the four kb (two pairs of
+// register swaps) until register g holds group g's 32 inputs: lane (n, kb)
+// then has inputs 32 g + 8 kb .. + 7.  Tokens are the other operand's rows,
+// and a lane's four sums are four tokens of one weight row, so one scale per
+// lane and group serves them.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "moe_q4_device.h"
+
+namespace moeq4 {
+
+constexpr int kLinAffine64 = 0, kLinAffine32 = 1, kLinMxfp4 = 2, kLinNvfp4 = 3;
+__host__ __device__ constexpr bool lin_affine(int f) { return f == kLinAffine64 || f == kLinAffine32; }
+__host__ __device__ constexpr int lin_group(int f) { return f == kLinAffine64 ? 64 : f == kLinNvfp4 ? 16 : 32; }
+constexpr int kLinStep = 128;  // inputs of one 16-byte load per lane
+// 32-bit words of one row's scales (biases) in a step
+__host__ __device__ constexpr int lin_scale_words(int f) { return f == kLinAffine32 ? 2 : 1; }
+
+typedef __bf16 lin_bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 lin_f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 lin_f16x2 __attribute__((ext_vector_type(2)));
+typedef float lin_f32x2 __attribute__((ext_vector_type(2)));
+typedef float lin_f32x4 __attribute__((ext_vector_type(4)));
+
+template <bool F16>
+__device__ __forceinline__ lin_f32x4 lin_mfma(uint4 a, uint4 b, lin_f32x4 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(lin_f16x8, a), __builtin_bit_cast(lin_f16x8, b), c,
+                                                  0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(lin_bf16x8, a), __builtin_bit_cast(lin_bf16x8, b),
+                                                   c, 0, 0, 0);
+}
+
+// 16 + q for the eight codes of a word, as pairs (q0,q4) (q1,q5) (q2,q6)
+// (q3,q7): a code in the top mantissa bits under the exponent of 16.  The
+// smallest offset that one mask and one or can give keeps the fp32 sums
+// near the size of the codes' own (128 + q would cost three more bits).
+template <bool F16>
+__device__ __forceinline__ uint4 lin_codes16(uint32_t w) {
+  constexpr uint32_t kMask = F16 ? 0x03C003C0u : 0x00780078u, kBase = F16 ? 0x4C004C00u : 0x41804180u;
+  if constexpr (F16)
+    return make_uint4(((w << 6) & kMask) | kBase, ((w << 2) & kMask) | kBase, ((w >> 2) & kMask) | kBase,
+                      ((w >> 6) & kMask) | kBase);
+  else
+    return make_uint4(((w << 3) & kMask) | kBase, ((w >> 1) & kMask) | kBase, ((w >> 5) & kMask) | kBase,
+                      ((w >> 9) & kMask) | kBase);
+}
+
+// Eight activations in the order lin_codes16 gives the codes.
+__device__ __forceinline__ uint4 lin_pair_order(uint4 v) {
+  return make_uint4((v.x & 0xFFFFu) | (v.z << 16), (v.x >> 16) | (v.z & 0xFFFF0000u), (v.y & 0xFFFFu) | (v.w << 16),
+                    (v.y >> 16) | (v.w & 0xFFFF0000u));
+}
+
+// E2M1 values of a word's codes, natural order, exact.
+template <bool F16>
+__device__ __forceinline__ uint4 lin_fp4(uint32_t w) {
+  if constexpr (F16)
+    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3)));
+  else
+    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3)));
+}
+
+// E2M1 values times an E4M3 scale: at most 2 + 4 significant bits and an
+// exponent both types hold, so the product is exact in bf16 and in fp16.
+template <bool F16>
+__device__ __forceinline__ uint4 lin_fp4_scaled(uint32_t w, float s) {
+  if constexpr (F16) {
+    const lin_f16x2 h = {(_Float16)s, (_Float16)s};
+    uint4 v = lin_fp4<true>(w);
+    v.x = __builtin_bit_cast(uint32_t, __builtin_bit_cast(lin_f16x2, v.x) * h);
+    v.y = __builtin_bit_cast(uint32_t, __builtin_bit_cast(lin_f16x2, v.y) * h);
+    v.z = __builtin_bit_cast(uint32_t, __builtin_bit_cast(lin_f16x2, v.z) * h);
+    v.w = __builtin_bit_cast(uint32_t, __builtin_bit_cast(lin_f16x2, v.w) * h);
+    return v;
+  } else {
+    auto two = [&](lin_f32x2 p) {  // the high halves of two fp32 are their exact bf16
+      return __builtin_amdgcn_perm(__float_as_uint(p.y * s), __float_as_uint(p.x * s), 0x07060302u);
+    };
+    return make_uint4(two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0)),
+                      two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1)),
+                      two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2)),
+                      two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3)));
+  }
+}
+
+// 2^(e - 127) of an E8M0 byte: the byte in fp32's exponent field, the
+// subnormal 2^-127 for 0 and NaN for 255.
+__device__ __forceinline__ float lin_e8m0(uint32_t e) {
+  const uint32_t v = e == 0 ? 0x00400000u : e << 23;
+  return __uint_as_float(e == 255u ? 0x7FC00000u : v);
+}
+
+// Transposes the 4 x 4 words of four 16-lane rows: w[j] of row kb goes to
+// w[kb] of row j.
+__device__ __forceinline__ void lin_transpose(uint32_t (&w)[4]) {
+  auto s = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  w[0] = s[0]; w[2] = s[1];
+  s = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  w[1] = s[0]; w[3] = s[1];
+  s = __builtin_amdgcn_permlane16_swap(w[0], w[1], false, false);
+  w[0] = s[0]; w[1] = s[1];
+  s = __builtin_amdgcn_permlane16_swap(w[2], w[3], false, false);
+  w[2] = s[0]; w[3] = s[1];
+}
+
+// Input of operand register g of lane row kb inside a step.
+template <int FMT>
+__device__ __forceinline__ constexpr int lin_input(int g, int kb) {
+  return FMT == kLinNvfp4 ? 32 * kb + 8 * g : 32 * g + 8 * kb;
+}
+
+}  // namespace moeq4

@@ -1,0 +1,228 @@
+"""The router's selection and the balance loss, with their gradients
+(``moe_router_topk``, ``moe_balance_loss`` and their ``_backward``)."""
+
+from __future__ import annotations
+
+from typing import Tuple
+
+import torch
+
+import quantized_expert_gather_amd as _q
+
+from ._args import DTYPES, array, matrix, on_device, stream_of, used_on
+
+
+def _score(score) -> int:
+    if isinstance(score, str):
+        if score not in _q.SCORES:
+            raise ValueError(f"unknown score {score!r}, expected one of {tuple(_q.SCORES)}")
+        return _q.SCORES[score]
+    return int(score)
+
+
+def _output(t, dtype, shape, name, device):
+    """(tensor, pointer, tensor if it was made here)."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr(), t
+    return t, array(t, dtype, shape, name, device), None
+
+
+def _gradient(logits, dlogits):
+    """(tensor, pointer, row stride, tensor if it was made here) of a gradient like `logits`."""
+    if dlogits is None:
+        d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        return d, d.data_ptr(), logits.shape[1], d
+    p, ldd = matrix(dlogits, (logits.dtype,), "dlogits")
+    if dlogits.shape != logits.shape or dlogits.device != logits.device:
+        raise ValueError("dlogits must have the shape and device of logits")
+    return dlogits, p, ldd, None
+
+
+def _topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weights, stream):
+    zp, ld = matrix(logits, DTYPES, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    k = int(k)
+    if not 1 <= k <= E:
+        raise _q.MoeQ4Error(_q.MOE_Q4_ERR_SHAPE, "moe_router_topk")
+    bp = 0 if select_bias is None else array(select_bias, torch.float32, (E,), "select_bias", dev)
+    ids, ip, made_i = _output(topk_ids, torch.int32, (T, k), "topk_ids", dev)
+    w, wp, made_w = _output(topk_weights, torch.float32, (T, k), "topk_weights", dev)
+    handle, side = stream_of(stream, dev)
+    with on_device(dev):
+        _q._check(_q.lib().moe_router_topk(zp, DTYPES[logits.dtype], ld, bp, T, k, E, _score(score), int(bool(renormalize)),
+                                           float(scale), ip, wp, handle), "moe_router_topk")
+    if side is not None:
+        used_on(side, made_i, made_w)
+    return ids, w
+
+
+class _TopkFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, select_bias, score, renormalize, scale):
+        ids, w = _topk(logits, k, select_bias, score, renormalize, scale, None, None, None)
+        ctx.mark_non_differentiable(ids)
+        ctx.save_for_backward(logits, ids)
+        ctx.how = (score, renormalize, scale)
+        return ids, w
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _dids, dweights):
+        logits, ids = ctx.saved_tensors
+        score, renormalize, scale = ctx.how
+        dz = moe_router_topk_backward(logits, ids, dweights.float().contiguous(), score=score, renormalize=renormalize,
+                                      scale=scale)
+        return dz, None, None, None, None, None
+
+
+def moe_router_topk(logits, k: int, select_bias=None, score="softmax", renormalize: bool = True, scale: float = 1.0,
+                    topk_ids=None, topk_weights=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The k experts of each token and their weights (see include/moe_q4.h).
+
+    logits [T, E] bf16, fp16 or fp32 with contiguous rows; select_bias fp32
+    [E], added to the scores for the choice only.  Returns (topk_ids int32 [T,
+    k], topk_weights fp32 [T, k]) as :func:`moe_swiglu_q4_forward` takes them.
+
+    The weights carry a gradient to logits where logits requires one and no
+    output tensors or stream are given; a step recorded into a graph calls
+    :func:`moe_router_topk_backward` itself.
+    """
+    if topk_ids is None and topk_weights is None and stream is None and isinstance(logits, torch.Tensor) and \
+            logits.requires_grad and torch.is_grad_enabled():
+        return _TopkFunction.apply(logits, k, select_bias, score, renormalize, scale)
+    return _topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weights, stream)
+
+
+def moe_router_topk_backward(logits, topk_ids, dweights, score="softmax", renormalize: bool = True, scale: float = 1.0,
+                             dlogits=None, stream=None) -> torch.Tensor:
+    """Gradient of :func:`moe_router_topk`'s weights with respect to logits, the
+    choice held fixed: dweights fp32 [T, k] -> dlogits [T, E] in logits' type."""
+    zp, ld = matrix(logits, DTYPES, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
+        raise ValueError("topk_ids [T, k] expected")
+    k = topk_ids.shape[1]
+    ip = array(topk_ids, torch.int32, (T, k), "topk_ids", dev)
+    gp = array(dweights, torch.float32, (T, k), "dweights", dev)
+    d, dp, ldd, made = _gradient(logits, dlogits)
+    handle, side = stream_of(stream, dev)
+    with on_device(dev):
+        _q._check(_q.lib().moe_router_topk_backward(zp, DTYPES[logits.dtype], ld, ip, gp, T, k, E, _score(score),
+                                                    int(bool(renormalize)), float(scale), dp, ldd, handle),
+                  "moe_router_topk_backward")
+    if side is not None:
+        used_on(side, made)
+    return d
+
+
+def moe_balance_loss_workspace_bytes(S: int, T: int, E: int) -> int:
+    return int(_q.lib().moe_balance_loss_workspace_bytes(S, T, E))
+
+
+def _tokens_of(logits, seqs):
+    seqs = int(seqs)
+    if seqs < 1 or logits.shape[0] % seqs:
+        raise ValueError(f"{logits.shape[0]} tokens are not {seqs} sequences of equal length")
+    return seqs, logits.shape[0] // seqs
+
+
+def _mask_ptr(token_mask, rows, device):
+    if token_mask is None:
+        return 0
+    if isinstance(token_mask, torch.Tensor):
+        token_mask = token_mask.reshape(-1) if token_mask.is_contiguous() else token_mask
+    return array(token_mask, (torch.bool, torch.uint8), (rows,), "token_mask", device)
+
+
+def _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace, stream):
+    zp, ld = matrix(logits, DTYPES, "logits")
+    rows, E = logits.shape
+    dev = logits.device
+    S, T = _tokens_of(logits, seqs)
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
+        raise ValueError("topk_ids [tokens, k] expected")
+    k = topk_ids.shape[1]
+    ip = array(topk_ids, torch.int32, (rows, k), "topk_ids", dev)
+    mp = _mask_ptr(token_mask, rows, dev)
+    lib = _q.lib()
+    loss = torch.empty(S, dtype=torch.float32, device=dev)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    tokens = torch.empty(S, dtype=torch.int32, device=dev)
+    scratch = None
+    if workspace is None:
+        scratch = workspace = torch.empty(max(256, lib.moe_balance_loss_workspace_bytes(S, T, E)), dtype=torch.uint8,
+                                          device=dev)
+    wsn = workspace.numel()
+    wsp = array(workspace, torch.uint8, (wsn,), "workspace", dev)
+    handle, side = stream_of(stream, dev)
+    with on_device(dev):
+        _q._check(lib.moe_balance_loss(zp, DTYPES[logits.dtype], ld, ip, mp, S, T, k, E, _score(score), float(coef),
+                                       loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(), wsp, wsn, handle),
+                  "moe_balance_loss")
+    if side is not None:
+        used_on(side, loss, counts, tokens, scratch)
+    return loss, counts, tokens
+
+
+class _BalanceFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, topk_ids, coef, score, seqs, token_mask, workspace):
+        loss, counts, tokens = _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace, None)
+        ctx.mark_non_differentiable(counts, tokens)
+        ctx.save_for_backward(logits, counts, tokens, token_mask)
+        ctx.how = (topk_ids.shape[1], coef, score)
+        return loss, counts, tokens
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss, _dcounts, _dtokens):
+        logits, counts, tokens, token_mask = ctx.saved_tensors
+        k, coef, score = ctx.how
+        dz = moe_balance_loss_backward(logits, counts, tokens, dloss.float().contiguous(), k, coef=coef, score=score,
+                                       token_mask=token_mask)
+        return dz, None, None, None, None, None, None
+
+
+def moe_balance_loss(logits, topk_ids, coef: float = 1.0, score="softmax", seqs: int = 1, token_mask=None,
+                     workspace=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Balance loss and route counts of ``seqs`` sequences of equal length (see
+    include/moe_q4.h): logits [seqs * T, E] bf16, fp16 or fp32 with contiguous
+    rows, topk_ids int32 [seqs * T, k], token_mask bool or uint8 [seqs * T] (0
+    leaves a token out).
+
+    Returns (loss fp32 [seqs], counts int32 [seqs, E], tokens int32 [seqs]).
+    The loss carries a gradient to logits where logits requires one and no
+    stream is given; a step recorded into a graph calls
+    :func:`moe_balance_loss_backward` itself.
+    """
+    if stream is None and isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
+        return _BalanceFunction.apply(logits, topk_ids, coef, score, seqs, token_mask, workspace)
+    return _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace, stream)
+
+
+def moe_balance_loss_backward(logits, counts, tokens, dloss, k: int, coef: float = 1.0, score="softmax",
+                              token_mask=None, dlogits=None, stream=None) -> torch.Tensor:
+    """Gradient of :func:`moe_balance_loss`, the counts held fixed: dloss fp32
+    [seqs] and the forward's counts and tokens -> dlogits in logits' type."""
+    zp, ld = matrix(logits, DTYPES, "logits")
+    rows, E = logits.shape
+    dev = logits.device
+    if not isinstance(counts, torch.Tensor) or counts.dim() != 2:
+        raise ValueError("counts [seqs, E] expected")
+    S, T = _tokens_of(logits, counts.shape[0])
+    cp = array(counts, torch.int32, (S, E), "counts", dev)
+    np_ = array(tokens, torch.int32, (S,), "tokens", dev)
+    gp = array(dloss, torch.float32, (S,), "dloss", dev)
+    mp = _mask_ptr(token_mask, rows, dev)
+    d, dp, ldd, made = _gradient(logits, dlogits)
+    handle, side = stream_of(stream, dev)
+    with on_device(dev):
+        _q._check(_q.lib().moe_balance_loss_backward(zp, DTYPES[logits.dtype], ld, mp, cp, np_, gp, S, T, int(k), E,
+                                                     _score(score), float(coef), dp, ldd, handle),
+                  "moe_balance_loss_backward")
+    if side is not None:
+        used_on(side, made)
+    return d
