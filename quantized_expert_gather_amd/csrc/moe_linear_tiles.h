@@ -1,0 +1,487 @@
+// Dense 4-bit product for many tokens: tiles of 16 MT tokens x 64 NT weight
+// rows on the matrix cores, K in steps of 128.  Internal header.
+//
+// Every weight is made one exact 16-bit operand, so the products add up over
+// all of K in the accumulators with no work per scale group:
+//   nvfp4    e2m1 * e4m3, exact in both types;
+//   mxfp4    e2m1 * 2^e: exact in bf16; in fp16 with e counted from the row's
+//            largest, whose power of two multiplies the row's result;
+//   affine   s * (q - 8): 8 + 3 significant bits, exact in fp16's 11, with s
+//            divided by a power of two near its row's largest.  bf16 tokens
+//            are divided by a power of two near their largest value likewise
+//            and held in fp16.  What lies 2^-34 (weights) or 2^-39 (tokens)
+//            below the largest of its row loses bits, far below fp32's own
+//            rounding of the sum.
+// The affine rest, sum over groups of (b + 8 s) X with X = sum of the group's
+// x, is a product over K / group columns; it starts the accumulators, with b
+// and s as they are and X as two or three bf16 terms.
+//
+// A wave holds 16 NT rows' codes in registers, one step ahead; the tokens'
+// step is copied into LDS without passing registers, 16-byte pieces of a row
+// XORed with the row so that the 16 rows of an operand read fall in
+// different banks.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "moe_linear_device.h"
+#include "moe_q4.h"
+
+namespace moeq4 {
+
+struct TilesArgs {
+  const uint16_t* x;       // tokens in operand type and order
+  const uint32_t* w;
+  const unsigned char* s;  // scales as given (nvfp4, mxfp4)
+  const uint16_t* sh;      // affine: fp16 scales over their row's power of two [N][G]
+  const uint16_t* sraw;    // affine: bf16 scales and biases as given
+  const uint16_t* braw;
+  const uint16_t* xsum;    // affine: bf16 terms of the group sums [3][L][Gp]
+  const int32_t* xexp;     // power of two of each token (affine with bf16 tokens), or NULL
+  const int32_t* wexp;     // power of two of each row (affine; mxfp4 with fp16 tokens), or NULL
+  const float* bias;
+  void* out;
+  float* part;             // split K: [splits][L][N] partial sums
+  long long ldx, ldo;
+  int L, N, K, G, Gp;
+  int out_dtype;
+  int terms;               // bf16 terms of X that are used
+  int bvec;                // biases and scales can be read 8 groups at a time
+  int splits, steps_per;   // steps of 128 inputs of each split
+  int row_tiles, tok_tiles;
+};
+
+typedef unsigned int lin_u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ lin_f16x2 lin_h2(uint32_t v) { return __builtin_bit_cast(lin_f16x2, v); }
+__device__ __forceinline__ uint32_t lin_u(lin_f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+
+// s * (q - 8) of a word's codes in fp16: one fused multiply-add a pair, its
+// addend -24 s exact (9 significant bits) and its result too.
+__device__ __forceinline__ uint4 lin_affine_f16(uint32_t w, lin_f16x2 s, lin_f16x2 m24s) {
+  const uint4 c = lin_codes16<true>(w);
+  return make_uint4(lin_u(__builtin_elementwise_fma(lin_h2(c.x), s, m24s)), lin_u(__builtin_elementwise_fma(lin_h2(c.y), s, m24s)),
+                    lin_u(__builtin_elementwise_fma(lin_h2(c.z), s, m24s)), lin_u(__builtin_elementwise_fma(lin_h2(c.w), s, m24s)));
+}
+
+// mxfp4 codes times the power of two in the exponent of `s`.
+template <bool F16>
+__device__ __forceinline__ uint4 lin_fp4_pow2(uint32_t w, float s) {
+  if constexpr (F16)
+    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3)));
+  else
+    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3)));
+}
+
+// The scale of a row's 32 inputs from k on (nvfp4: two scales), as stored.
+template <int FMT>
+__device__ __forceinline__ uint32_t tile_scale(const unsigned char* row, int k) {
+  if constexpr (FMT == kLinMxfp4)
+    return row[k / 32];
+  else if constexpr (FMT == kLinNvfp4)
+    return *reinterpret_cast<const uint16_t*>(row + k / 16);
+  else
+    return *reinterpret_cast<const uint16_t*>(row + 2 * (k / lin_group(FMT)));
+}
+
+// Stores the first `left` (at least one) of four neighbours.
+template <class T>
+__device__ __forceinline__ void store4(T* p, int left, T a, T b, T c, T d) {
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  if (left >= 4 && ((uintptr_t)p & (sizeof(t4) - 1)) == 0) {
+    *reinterpret_cast<t4*>(p) = t4{a, b, c, d};
+  } else {
+    p[0] = a;
+    if (left > 1) p[1] = b;
+    if (left > 2) p[2] = c;
+    if (left > 3) p[3] = d;
+  }
+}
+
+template <int FMT, bool F16, int MT, int NT>
+__global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
+  constexpr int kTok = 16 * MT, kRows = 64 * NT;
+  extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];  // [2][kTok][256 B]
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n16 = lane & 15, kb = lane >> 4;
+
+  // Workgroups b, b + 8, ... share an XCD (and its L2): each XCD takes a
+  // contiguous run of the tiles, tokens fastest, so it reads an eighth of the
+  // weights.
+  const int tiles = a.row_tiles * a.tok_tiles;
+  int tile = blockIdx.x;
+  {
+    const int per = tiles / 8, rest = tiles % 8, xcd = tile & 7, at = tile >> 3;
+    tile = xcd * per + min(xcd, rest) + at;
+  }
+  const int tok0 = (tile % a.tok_tiles) * kTok;
+  const int row0 = (tile / a.tok_tiles) * kRows + wave * 16 * NT;
+  const int split = blockIdx.y;
+  const int all = (a.K + kLinStep - 1) / kLinStep;
+  const int step0 = split * a.steps_per, step1 = min(all, step0 + a.steps_per);
+
+  size_t row[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) row[nt] = min(row0 + 16 * nt + n16, a.N - 1);
+
+  lin_f32x4 acc[MT][NT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = lin_f32x4{0, 0, 0, 0};
+
+  constexpr bool kScaled = lin_affine(FMT) || (FMT == kLinMxfp4 && F16);
+  int wexp[NT];
+  if constexpr (lin_affine(FMT) || (FMT == kLinMxfp4 && F16)) {  // the same lanes' rows as the codes'
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) wexp[nt] = a.wexp[row[nt]];
+  }
+
+  if constexpr (lin_affine(FMT)) {
+    if (split == 0) {
+      // sum over groups of s X, times 8, plus that of b X
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        const uint16_t* src = pass ? a.braw : a.sraw;
+#pragma unroll 1
+        for (int g0 = 0; g0 < a.G; g0 += 32) {
+          const int g = g0 + 8 * kb;
+          uint4 bf[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint16_t* p = src + row[nt] * a.G + g;
+            if (a.bvec) {
+              bf[nt] = g < a.G ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+            } else {
+              bf[nt] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+              for (int i = 7; i >= 0; --i) {  // shifts the groups in, the last one first
+                bf[nt].w = bf[nt].w << 16 | bf[nt].z >> 16;
+                bf[nt].z = bf[nt].z << 16 | bf[nt].y >> 16;
+                bf[nt].y = bf[nt].y << 16 | bf[nt].x >> 16;
+                bf[nt].x = bf[nt].x << 16 | (g + i < a.G ? p[i] : 0);
+              }
+            }
+          }
+#pragma unroll 1
+          for (int term = 0; term < a.terms; ++term) {
+            uint4 xf[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const size_t t = min(tok0 + 16 * mt + n16, a.L - 1);
+              xf[mt] = *reinterpret_cast<const uint4*>(a.xsum + ((size_t)term * a.L + t) * a.Gp + g);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = lin_mfma<false>(bf[nt], xf[mt], acc[mt][nt]);
+          }
+        }
+        if (pass == 0) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) acc[mt][nt] *= 8.0f;
+        }
+      }
+      // into the operands' units
+      int we[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) we[nt][i] = __shfl(wexp[nt], 4 * kb + i, 64);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int xe = a.xexp ? a.xexp[min(tok0 + 16 * mt + n16, a.L - 1)] : 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[mt][nt][i] = __builtin_amdgcn_ldexpf(acc[mt][nt][i], -xe - we[nt][i]);
+      }
+    }
+  }
+
+  // pieces of a step's tokens: LDS slot i holds piece (i % 16) ^ (row % 16) of token i / 16
+  constexpr int kCopies = kTok / 16;
+  const int piece = (tid & 15) ^ ((tid >> 4) & 15);
+  const uint16_t* xrow[kCopies];
+#pragma unroll
+  for (int c = 0; c < kCopies; ++c) xrow[c] = a.x + (size_t)min(tok0 + 16 * c + (tid >> 4), a.L - 1) * a.ldx;
+  auto stage = [&](int step, int buf) {
+    const int k = min(step * kLinStep + piece * 8, a.K - 8);
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      // a wave's 64 pieces go to 1 KB of LDS from its first slot on
+      unsigned char* dst = lds + buf * (kTok * 256) + (c * 256 + wave * 64) * 16;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(xrow[c] + k),
+                                       (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+    }
+  };
+  const unsigned char* wrow[NT];
+  const unsigned char* srow[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    wrow[nt] = reinterpret_cast<const unsigned char*>(a.w) + row[nt] * ((size_t)a.K / 2);
+    srow[nt] = lin_affine(FMT) ? reinterpret_cast<const unsigned char*>(a.sh) + row[nt] * a.G * 2 : a.s + row[nt] * a.G;
+  }
+  auto load = [&](int step, lin_u32x4 (&cw)[NT], uint32_t (&sw)[NT]) {
+    const int k = min(step * kLinStep + 32 * kb, a.K - 32);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      cw[nt] = *reinterpret_cast<const lin_u32x4*>(wrow[nt] + k / 2);
+      sw[nt] = tile_scale<FMT>(srow[nt], k);
+    }
+  };
+
+  lin_u32x4 cw[NT];
+  uint32_t sw[NT];
+  if (step0 < step1) {
+    stage(step0, 0);
+    load(step0, cw, sw);
+  }
+
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  for (int step = step0, buf = 0; step < step1; ++step, buf ^= 1) {
+    lin_u32x4 cn[NT];
+    uint32_t sn[NT];
+    if (step + 1 < step1) {
+      stage(step + 1, buf ^ 1);
+      load(step + 1, cn, sn);
+    }
+    const bool dead = step * kLinStep + 32 * kb >= a.K;  // past the row's end
+    float sf[NT][2];
+    lin_f16x2 sv[NT], sm[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if constexpr (FMT == kLinNvfp4) {
+        sf[nt][0] = dead ? 0.0f : e4m3_to_f32(sw[nt] & 255u);
+        sf[nt][1] = dead ? 0.0f : e4m3_to_f32(sw[nt] >> 8);
+      } else if constexpr (FMT == kLinMxfp4) {
+        if (dead) cw[nt] = lin_u32x4{0, 0, 0, 0};
+        if constexpr (F16) {  // counted from the row's largest exponent; 255 stands for NaN
+          const int e = max((int)sw[nt] - 127 - wexp[nt], -126);
+          sf[nt][0] = sw[nt] == 255u ? __builtin_nanf("") : __int_as_float((e + 127) << 23);
+        } else {
+          sf[nt][0] = lin_e8m0(sw[nt]);
+        }
+      } else {
+        sv[nt] = lin_h2(dead ? 0u : sw[nt] | sw[nt] << 16);
+        sm[nt] = sv[nt] * lin_f16x2{(_Float16)-24.0f, (_Float16)-24.0f};
+      }
+    }
+    const unsigned char* xb = lds + buf * (kTok * 256);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint4 wf[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (FMT == kLinNvfp4)
+          wf[nt] = lin_fp4_scaled<F16>(cw[nt][j], sf[nt][j >> 1]);
+        else if constexpr (FMT == kLinMxfp4)
+          wf[nt] = lin_fp4_pow2<F16>(cw[nt][j], sf[nt][0]);
+        else
+          wf[nt] = lin_affine_f16(cw[nt][j], sv[nt], sm[nt]);
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const uint4 xf = *reinterpret_cast<const uint4*>(xb + (16 * mt + n16) * 256 + (((4 * kb + j) ^ n16) << 4));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = lin_mfma<lin_affine(FMT) || F16>(wf[nt], xf, acc[mt][nt]);
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      cw[nt] = cn[nt];
+      sw[nt] = sn[nt];
+    }
+  }
+
+  // Lane (n16, kb) holds token n16 of each token tile and rows 4 kb .. + 3 of
+  // each row tile.  Through LDS (the waves' own quarters, four token tiles at
+  // a time) it comes to hold four neighbouring rows of a token whose other
+  // rows the next lanes hold.
+  constexpr int kPass = MT < 4 ? MT : 4, kQuads = 4 * NT;  // token tiles of a pass, 16-byte pieces of a token's rows
+  unsigned char* mine = lds + wave * (kPass * 16 * kQuads * 16);
+#pragma unroll
+  for (int m0 = 0; m0 < MT; m0 += kPass) {
+#pragma unroll
+    for (int mt = 0; mt < kPass; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        *reinterpret_cast<lin_f32x4*>(mine + ((16 * mt + n16) * kQuads + ((4 * nt + kb) ^ (n16 & (kQuads - 1)))) * 16) =
+            acc[m0 + mt][nt];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 1
+    for (int i = lane; i < kPass * 16 * kQuads; i += 64) {
+      const int tt = i / kQuads, quad = i & (kQuads - 1);
+      const int t = tok0 + 16 * m0 + tt, n = row0 + 4 * quad;
+      const lin_f32x4 v4 = *reinterpret_cast<const lin_f32x4*>(mine + (tt * kQuads + (quad ^ (tt & 15 & (kQuads - 1)))) * 16);
+      if (t >= a.L || n >= a.N) continue;
+      float v[4] = {v4[0], v4[1], v4[2], v4[3]};
+      if constexpr (kScaled) {
+        const int xe = lin_affine(FMT) && a.xexp ? a.xexp[t] : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_ldexpf(v[e], xe + a.wexp[min(n + e, a.N - 1)]);
+      }
+      if (a.splits > 1) {
+        store4<float>(a.part + ((size_t)split * a.L + t) * a.N + n, a.N - n, v[0], v[1], v[2], v[3]);
+        continue;
+      }
+      if (a.bias) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += a.bias[min(n + e, a.N - 1)];
+      }
+      const size_t at = (size_t)t * a.ldo + n;
+      if (a.out_dtype == MOE_Q4_DTYPE_F32)
+        store4<float>(static_cast<float*>(a.out) + at, a.N - n, v[0], v[1], v[2], v[3]);
+      else if (a.out_dtype == MOE_Q4_DTYPE_BF16)
+        store4<uint16_t>(static_cast<uint16_t*>(a.out) + at, a.N - n, (uint16_t)f32_to_bf16_rne(v[0]),
+                         (uint16_t)f32_to_bf16_rne(v[1]), (uint16_t)f32_to_bf16_rne(v[2]), (uint16_t)f32_to_bf16_rne(v[3]));
+      else
+        store4<_Float16>(static_cast<_Float16*>(a.out) + at, a.N - n, (_Float16)v[0], (_Float16)v[1], (_Float16)v[2],
+                         (_Float16)v[3]);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+// Lays out what the tiles read besides codes and tokens.  One workgroup a
+// token (affine): its power of two, the fp16 copy in the codes' pair order
+// and the group sums' bf16 terms.  One wave a weight row (affine, and mxfp4
+// with fp16 tokens): its power of two and the fp16 scales.
+struct PrepareArgs {
+  const uint16_t* x;
+  const unsigned char* s;
+  uint16_t* xq;
+  uint16_t* xsum;
+  int32_t* xexp;
+  uint16_t* sh;
+  int32_t* wexp;
+  long long ldx;
+  int L, N, K, G, Gp;
+  int tok_blocks;
+};
+
+template <int FMT, bool F16>
+__global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
+  __shared__ uint32_t red[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if ((int)blockIdx.x < a.tok_blocks) {
+    if constexpr (lin_affine(FMT)) {
+      const int t = blockIdx.x;
+      const uint16_t* x = a.x + (size_t)t * a.ldx;
+      int e = 0;
+      if constexpr (!F16) {
+        uint32_t m = 0;
+        for (int c = 8 * tid; c < a.K; c += 2048) {
+          const uint4 v = *reinterpret_cast<const uint4*>(x + c);
+          const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m = max(m, max(q[i] & 0x7FFFu, (q[i] >> 16) & 0x7FFFu));
+        }
+        for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+        if (lane == 0) red[wave] = m;
+        __syncthreads();
+        m = max(max(red[0], red[1]), max(red[2], red[3]));
+        e = m ? min(max((int)(m >> 7), 1), 254) - 127 - 14 : 0;  // the largest falls in [2^14, 2^15)
+        if (tid == 0) a.xexp[t] = e;
+      }
+      constexpr int kLanes = lin_group(FMT) / 8;  // lanes of a group
+      for (int c0 = 0; c0 < a.K; c0 += 2048) {
+        const int c = c0 + 8 * tid;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (c < a.K) v = *reinterpret_cast<const uint4*>(x + c);
+        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (F16) {
+            const lin_f16x2 h = lin_h2(q[i]);
+            f[2 * i] = (float)h.x;
+            f[2 * i + 1] = (float)h.y;
+          } else {
+            f[2 * i] = bf16_lo_to_f32(q[i]);
+            f[2 * i + 1] = bf16_hi_to_f32(q[i]);
+          }
+        }
+        float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+        if constexpr (!F16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const lin_f16x2 h = {(_Float16)__builtin_amdgcn_ldexpf(f[2 * i], -e), (_Float16)__builtin_amdgcn_ldexpf(f[2 * i + 1], -e)};
+            (&v.x)[i] = lin_u(h);
+          }
+        }
+        if (c < a.K) *reinterpret_cast<uint4*>(a.xq + (size_t)t * a.K + c) = lin_pair_order(v);
+        sum += __shfl_xor(sum, 1, 64);
+        sum += __shfl_xor(sum, 2, 64);
+        if constexpr (kLanes == 8) sum += __shfl_xor(sum, 4, 64);
+        if (c < a.K && (tid & (kLanes - 1)) == 0) {
+          const uint32_t hi = f32_to_bf16_rne(sum);
+          const float r = sum - bf16_lo_to_f32(hi);
+          const uint32_t mid = f32_to_bf16_rne(r);
+          const uint32_t lo = f32_to_bf16_rne(r - bf16_lo_to_f32(mid));
+          const size_t at = (size_t)t * a.Gp + c / lin_group(FMT), plane = (size_t)a.L * a.Gp;
+          a.xsum[at] = (uint16_t)hi;
+          a.xsum[at + plane] = (uint16_t)mid;
+          a.xsum[at + 2 * plane] = (uint16_t)lo;
+        }
+      }
+      if (a.G + tid < a.Gp) {
+        for (int p = 0; p < 3; ++p) a.xsum[((size_t)p * a.L + t) * a.Gp + a.G + tid] = 0;
+      }
+    }
+    return;
+  }
+  const size_t n = (size_t)(blockIdx.x - a.tok_blocks) * 4 + wave;
+  if (n >= (size_t)a.N) return;
+  int m = 0;
+  if constexpr (FMT == kLinMxfp4) {
+    for (int g = lane; g < a.G; g += 64) {
+      const int e = a.s[n * a.G + g];
+      m = max(m, e == 255 ? 0 : e);
+    }
+    for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o, 64));
+    if (lane == 0) a.wexp[n] = m - 127 - 12;  // the largest block's elements reach 6 * 2^12
+  } else if constexpr (lin_affine(FMT)) {
+    const uint16_t* s = reinterpret_cast<const uint16_t*>(a.s) + n * a.G;
+    for (int g = lane; g < a.G; g += 64) m = max(m, (int)(s[g] & 0x7FFFu));
+    for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o, 64));
+    const int e = m ? min(max(m >> 7, 1), 254) - 127 - 8 : 0;  // the largest falls in [2^8, 2^9): 24 s in 2^14
+    for (int g = lane; g < a.G; g += 64)
+      a.sh[n * a.G + g] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(bf16_to_f32(s[g]), -e));
+    if (lane == 0) a.wexp[n] = e;
+  }
+}
+
+// Adds the splits of K in ascending order, the bias, and rounds.
+__global__ __launch_bounds__(256) void k_linear_join(const float* __restrict__ part, const float* __restrict__ bias,
+                                                     void* out, long long ldo, int L, int N, int splits, int dtype) {
+  const size_t all = (size_t)L * N;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (size_t)gridDim.x * 256) {
+    float v = part[i];
+    for (int z = 1; z < splits; ++z) v += part[(size_t)z * all + i];
+    const size_t t = i / N, n = i - t * N;
+    if (bias) v += bias[n];
+    const size_t at = t * ldo + n;
+    if (dtype == MOE_Q4_DTYPE_F32)
+      static_cast<float*>(out)[at] = v;
+    else if (dtype == MOE_Q4_DTYPE_BF16)
+      static_cast<uint16_t*>(out)[at] = (uint16_t)f32_to_bf16_rne(v);
+    else
+      static_cast<_Float16*>(out)[at] = (_Float16)v;
+  }
+}
+
+}  // namespace moeq4
