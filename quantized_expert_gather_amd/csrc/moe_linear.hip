@@ -218,7 +218,7 @@ TilesPlan tiles_plan(int L, int N, int K) {
   p.mt = L <= 32 ? 2 : L <= 64 ? 4 : 8;
   p.tok_tiles = (L + 16 * p.mt - 1) / (16 * p.mt);
   const int steps = (K + kLinStep - 1) / kLinStep;
-  for (p.nt = 4;; p.nt /= 2) {
+  for (p.nt = 3;; --p.nt) {
     p.row_tiles = (N + 64 * p.nt - 1) / (64 * p.nt);
     if (p.nt == 1 || (long)p.row_tiles * p.tok_tiles >= 256) break;
   }
@@ -240,7 +240,7 @@ TilesWorkspace tiles_layout(int fmt, int L, int N, int K) {
   const size_t G = K / lin_group(fmt), Gp = (G + 31) / 32 * 32;
   const bool affine = lin_affine(fmt);
   size_t off = 0;
-  w.xq = off;   off = round256(off + (affine ? (size_t)L * K * 2 : 0));
+  w.xq = off;   off = round256(off + (affine ? (size_t)p.tok_tiles * p.mt * 16 * ((K + kLinStep - 1) / kLinStep * kLinStep) * 2 : 0));
   w.xsum = off; off = round256(off + (affine ? 3 * (size_t)L * Gp * 2 : 0));
   w.xexp = off; off = round256(off + (affine ? (size_t)L * 4 : 0));
   w.sh = off;   off = round256(off + (affine ? (size_t)N * G * 2 : 0));
@@ -253,11 +253,10 @@ TilesWorkspace tiles_layout(int fmt, int L, int N, int K) {
 template <int FMT, bool F16, int MT>
 void launch_tiles_mt(const TilesArgs& a, const TilesPlan& p, hipStream_t stream) {
   const dim3 grid(p.row_tiles * p.tok_tiles, p.splits), block(256);
-  const size_t lds = 2 * (size_t)(16 * MT) * 256;
   switch (p.nt) {
-    case 4: hipLaunchKernelGGL((k_linear_tiles<FMT, F16, MT, 4>), grid, block, lds, stream, a); break;
-    case 2: hipLaunchKernelGGL((k_linear_tiles<FMT, F16, MT, 2>), grid, block, lds, stream, a); break;
-    default: hipLaunchKernelGGL((k_linear_tiles<FMT, F16, MT, 1>), grid, block, lds, stream, a); break;
+    case 3: hipLaunchKernelGGL((k_linear_tiles<FMT, F16, MT, 3>), grid, block, 0, stream, a); break;
+    case 2: hipLaunchKernelGGL((k_linear_tiles<FMT, F16, MT, 2>), grid, block, 0, stream, a); break;
+    default: hipLaunchKernelGGL((k_linear_tiles<FMT, F16, MT, 1>), grid, block, 0, stream, a); break;
   }
 }
 
@@ -276,6 +275,7 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
   a.terms = l.out_dtype == MOE_Q4_DTYPE_F32 ? 3 : 2;
   a.bvec = a.G % 8 == 0 && (uintptr_t)l.s % 16 == 0 && (uintptr_t)l.b % 16 == 0;
   a.splits = p.splits; a.steps_per = p.steps_per;
+  a.stagger = std::max(1, p.steps_per / p.tok_tiles);
   a.row_tiles = p.row_tiles; a.tok_tiles = p.tok_tiles;
   a.part = reinterpret_cast<float*>(ws + lay.part);
   constexpr bool kRowsScaled = lin_affine(FMT) || (FMT == kLinMxfp4 && F16);
@@ -292,7 +292,7 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
       q.xexp = reinterpret_cast<int32_t*>(ws + lay.xexp);
       q.sh = reinterpret_cast<uint16_t*>(ws + lay.sh);
       q.tok_blocks = l.L;
-      a.x = q.xq; a.ldx = l.K;
+      a.x = q.xq;
       a.xsum = q.xsum;
       a.xexp = F16 ? nullptr : q.xexp;
       a.sh = q.sh;

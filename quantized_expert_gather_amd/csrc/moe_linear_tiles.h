@@ -17,7 +17,8 @@
 // and s as they are and X as two or three bf16 terms.
 //
 // A wave holds 16 NT rows' codes in registers, one step ahead; the tokens'
-// step is copied into LDS without passing registers, 16-byte pieces of a row
+// step (of affine weights: blocks of 16 tokens x 128 inputs, laid out first)
+// is copied into LDS without passing registers, 16-byte pieces of a row
 // XORed with the row so that the 16 rows of an operand read fall in
 // different banks.
 #pragma once
@@ -49,6 +50,7 @@ struct TilesArgs {
   int terms;               // bf16 terms of X that are used
   int bvec;                // biases and scales can be read 8 groups at a time
   int splits, steps_per;   // steps of 128 inputs of each split
+  int stagger;             // steps between the token tiles' first ones
   int row_tiles, tok_tiles;
 };
 
@@ -82,13 +84,13 @@ __device__ __forceinline__ uint4 lin_fp4_pow2(uint32_t w, float s) {
 
 // The scale of a row's 32 inputs from k on (nvfp4: two scales), as stored.
 template <int FMT>
-__device__ __forceinline__ uint32_t tile_scale(const unsigned char* row, int k) {
+__device__ __forceinline__ uint32_t tile_scale(const unsigned char* base, uint32_t row, int k) {
   if constexpr (FMT == kLinMxfp4)
-    return row[k / 32];
+    return base[row + (uint32_t)(k / 32)];
   else if constexpr (FMT == kLinNvfp4)
-    return *reinterpret_cast<const uint16_t*>(row + k / 16);
+    return *reinterpret_cast<const uint16_t*>(base + (row + (uint32_t)(k / 16)));
   else
-    return *reinterpret_cast<const uint16_t*>(row + 2 * (k / lin_group(FMT)));
+    return *reinterpret_cast<const uint16_t*>(base + (row + 2u * (uint32_t)(k / lin_group(FMT))));
 }
 
 // Stores the first `left` (at least one) of four neighbours.
@@ -108,7 +110,10 @@ __device__ __forceinline__ void store4(T* p, int left, T a, T b, T c, T d) {
 template <int FMT, bool F16, int MT, int NT>
 __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
   constexpr int kTok = 16 * MT, kRows = 64 * NT;
-  extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];  // [2][kTok][256 B]
+  constexpr bool kTiledX = lin_affine(FMT);  // the laid-out copy
+  // Two objects, each named where it is used: the compiler then knows that
+  // reads of one do not wait for the copies into the other.
+  __shared__ __attribute__((aligned(1024))) unsigned char lds0[kTok * 256], lds1[kTok * 256];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int n16 = lane & 15, kb = lane >> 4;
 
@@ -137,6 +142,13 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = lin_f32x4{0, 0, 0, 0};
 
+  if constexpr (!lin_affine(FMT)) {
+    // hides the zeros: as known constants the compiler carries them through the loop in registers of their own
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) asm volatile("" : "+v"(acc[mt][nt]));
+  }
   constexpr bool kScaled = lin_affine(FMT) || (FMT == kLinMxfp4 && F16);
   int wexp[NT];
   if constexpr (lin_affine(FMT) || (FMT == kLinMxfp4 && F16)) {  // the same lanes' rows as the codes'
@@ -209,53 +221,75 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
     }
   }
 
-  // pieces of a step's tokens: LDS slot i holds piece (i % 16) ^ (row % 16) of token i / 16
+  // Pieces of a step's tokens: LDS slot i holds piece (i % 16) ^ (row % 16) of
+  // token i / 16.  Addresses are a base that the wave shares and 32-bit
+  // offsets, which take half the registers of pointers.
   constexpr int kCopies = kTok / 16;
   const int piece = (tid & 15) ^ ((tid >> 4) & 15);
-  const uint16_t* xrow[kCopies];
+  const unsigned char* xbase = reinterpret_cast<const unsigned char*>(a.x) +
+                               (kTiledX ? (size_t)(tok0 / 16) * all * (16 * kLinStep * 2) : (size_t)tok0 * a.ldx * 2);
+  uint32_t xoff[kTiledX ? 1 : kCopies];
+  if constexpr (kTiledX) {
+    xoff[0] = (tid >> 4) * (kLinStep * 2) + piece * 16;
+  } else {
 #pragma unroll
-  for (int c = 0; c < kCopies; ++c) xrow[c] = a.x + (size_t)min(tok0 + 16 * c + (tid >> 4), a.L - 1) * a.ldx;
-  auto stage = [&](int step, int buf) {
-    const int k = min(step * kLinStep + piece * 8, a.K - 8);
+    for (int c = 0; c < kCopies; ++c) xoff[c] = (uint32_t)(min(tok0 + 16 * c + (tid >> 4), a.L - 1) - tok0) * (uint32_t)(2 * a.ldx);
+  }
+  auto stage = [&](int step, unsigned char* buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < kCopies; ++c) {
+      const unsigned char* src;
+      if constexpr (kTiledX)
+        src = xbase + ((size_t)c * all + step) * (16 * kLinStep * 2) + xoff[0];
+      else
+        src = xbase + (xoff[c] + 2u * (uint32_t)min(step * kLinStep + piece * 8, a.K - 8));
       // a wave's 64 pieces go to 1 KB of LDS from its first slot on
-      unsigned char* dst = lds + buf * (kTok * 256) + (c * 256 + wave * 64) * 16;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(xrow[c] + k),
+      unsigned char* dst = buf + (c * 256 + wave * 64) * 16;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                        (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
     }
   };
-  const unsigned char* wrow[NT];
-  const unsigned char* srow[NT];
+  const int rows0 = __builtin_amdgcn_readfirstlane(min(row0, a.N - 1));
+  constexpr int kScaleBytes = lin_affine(FMT) ? 2 : 1;
+  const unsigned char* wbase = reinterpret_cast<const unsigned char*>(a.w) + (size_t)rows0 * ((size_t)a.K / 2);
+  const unsigned char* sbase = (lin_affine(FMT) ? reinterpret_cast<const unsigned char*>(a.sh) : a.s) + (size_t)rows0 * a.G * kScaleBytes;
+  uint32_t woff[NT], soff[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    wrow[nt] = reinterpret_cast<const unsigned char*>(a.w) + row[nt] * ((size_t)a.K / 2);
-    srow[nt] = lin_affine(FMT) ? reinterpret_cast<const unsigned char*>(a.sh) + row[nt] * a.G * 2 : a.s + row[nt] * a.G;
+    woff[nt] = (uint32_t)((int)row[nt] - rows0) * (uint32_t)(a.K / 2);
+    soff[nt] = (uint32_t)((int)row[nt] - rows0) * (uint32_t)(a.G * kScaleBytes);
   }
-  auto load = [&](int step, lin_u32x4 (&cw)[NT], uint32_t (&sw)[NT]) {
+  auto load = [&](int step, lin_u32x4 (&cw)[NT], uint32_t (&sw)[NT]) __attribute__((always_inline)) {
     const int k = min(step * kLinStep + 32 * kb, a.K - 32);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      cw[nt] = *reinterpret_cast<const lin_u32x4*>(wrow[nt] + k / 2);
-      sw[nt] = tile_scale<FMT>(srow[nt], k);
+      cw[nt] = *reinterpret_cast<const lin_u32x4*>(wbase + (woff[nt] + (uint32_t)(k / 2)));
+      sw[nt] = tile_scale<FMT>(sbase, soff[nt], k);
     }
   };
 
   lin_u32x4 cw[NT];
   uint32_t sw[NT];
-  if (step0 < step1) {
-    stage(step0, 0);
-    load(step0, cw, sw);
+  // Rows whose length is a power of two put one step's pieces of all rows on
+  // a few memory channels: token tiles start at different steps, round the
+  // end to the beginning, so the tiles that run together read different ones.
+  const int count = step1 - step0;
+  int step = count > 0 ? step0 + (tile % a.tok_tiles) * a.stagger % count : 0;
+  if (count > 0) {
+    stage(step, lds0);
+    load(step, cw, sw);
   }
 
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  for (int step = step0, buf = 0; step < step1; ++step, buf ^= 1) {
+  int i = 0;
+  auto body = [&](unsigned char* xb, unsigned char* other) __attribute__((always_inline)) {
     lin_u32x4 cn[NT];
     uint32_t sn[NT];
-    if (step + 1 < step1) {
-      stage(step + 1, buf ^ 1);
-      load(step + 1, cn, sn);
+    const int next = step + 1 < step1 ? step + 1 : step0;
+    if (i + 1 < count) {
+      stage(next, other);
+      load(next, cn, sn);
     }
     const bool dead = step * kLinStep + 32 * kb >= a.K;  // past the row's end
     float sf[NT][2];
@@ -278,7 +312,6 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
         sm[nt] = sv[nt] * lin_f16x2{(_Float16)-24.0f, (_Float16)-24.0f};
       }
     }
-    const unsigned char* xb = lds + buf * (kTok * 256);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint4 wf[NT];
@@ -300,33 +333,42 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
     }
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
+    step = next;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       cw[nt] = cn[nt];
       sw[nt] = sn[nt];
     }
+    ++i;
+  };
+  while (i < count) {
+    body(lds0, lds1);
+    if (i >= count) break;
+    body(lds1, lds0);
   }
 
   // Lane (n16, kb) holds token n16 of each token tile and rows 4 kb .. + 3 of
-  // each row tile.  Through LDS (the waves' own quarters, four token tiles at
+  // each row tile.  Through LDS (the waves' own shares, some token tiles at
   // a time) it comes to hold four neighbouring rows of a token whose other
   // rows the next lanes hold.
-  constexpr int kPass = MT < 4 ? MT : 4, kQuads = 4 * NT;  // token tiles of a pass, 16-byte pieces of a token's rows
-  unsigned char* mine = lds + wave * (kPass * 16 * kQuads * 16);
+  // token tiles of a pass, 16-byte pieces of a token's rows; two waves' share fits each buffer
+  constexpr int kHalf = NT > 2 ? MT / 2 : MT, kPass = kHalf < 4 ? kHalf : 4, kQuads = 4 * NT;
+  static_assert(2 * kPass * 16 * kQuads * 16 <= kTok * 256, "the waves' output fits the token buffers");
+  unsigned char* mine = (wave < 2 ? lds0 : lds1) + (wave & 1) * (kPass * 16 * kQuads * 16);
 #pragma unroll
   for (int m0 = 0; m0 < MT; m0 += kPass) {
 #pragma unroll
     for (int mt = 0; mt < kPass; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<lin_f32x4*>(mine + ((16 * mt + n16) * kQuads + ((4 * nt + kb) ^ (n16 & (kQuads - 1)))) * 16) =
+        *reinterpret_cast<lin_f32x4*>(mine + ((16 * mt + n16) * kQuads + (4 * nt + kb + n16) % kQuads) * 16) =
             acc[m0 + mt][nt];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll 1
     for (int i = lane; i < kPass * 16 * kQuads; i += 64) {
-      const int tt = i / kQuads, quad = i & (kQuads - 1);
+      const int tt = i / kQuads, quad = i % kQuads;
       const int t = tok0 + 16 * m0 + tt, n = row0 + 4 * quad;
-      const lin_f32x4 v4 = *reinterpret_cast<const lin_f32x4*>(mine + (tt * kQuads + (quad ^ (tt & 15 & (kQuads - 1)))) * 16);
+      const lin_f32x4 v4 = *reinterpret_cast<const lin_f32x4*>(mine + (tt * kQuads + (quad + (tt & 15)) % kQuads) * 16);
       if (t >= a.L || n >= a.N) continue;
       float v[4] = {v4[0], v4[1], v4[2], v4[3]};
       if constexpr (kScaled) {
@@ -423,7 +465,10 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
             (&v.x)[i] = lin_u(h);
           }
         }
-        if (c < a.K) *reinterpret_cast<uint4*>(a.xq + (size_t)t * a.K + c) = lin_pair_order(v);
+        // zeros past the row's end fill its last step
+        if (c < (a.K + kLinStep - 1) / kLinStep * kLinStep)
+          *reinterpret_cast<uint4*>(a.xq + (((size_t)(t >> 4) * ((a.K + kLinStep - 1) / kLinStep) + c / kLinStep) * 16 + (t & 15)) * kLinStep +
+                                    c % kLinStep) = lin_pair_order(v);
         sum += __shfl_xor(sum, 1, 64);
         sum += __shfl_xor(sum, 2, 64);
         if constexpr (kLanes == 8) sum += __shfl_xor(sum, 4, 64);

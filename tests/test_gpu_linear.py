@@ -68,6 +68,12 @@ def test_many_tokens(codec, L, N, K):
 
 
 @pytest.mark.parametrize("codec", CODECS)
+@pytest.mark.parametrize("L,N,K", [(20, 16500, 64), (40, 33000, 128), (64, 16401, 192), (150, 8200, 320), (260, 5003, 448)])
+def test_many_tokens_and_many_outputs(codec, L, N, K):
+    run(codec, L, N, K, BF16 if N % 2 else F16, F16 if N % 2 else F32, bias=True)
+
+
+@pytest.mark.parametrize("codec", CODECS)
 @pytest.mark.parametrize("xt", [BF16, F16])
 @pytest.mark.parametrize("ot", [BF16, F16, F32])
 def test_types(codec, xt, ot):
