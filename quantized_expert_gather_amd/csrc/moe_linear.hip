@@ -111,6 +111,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
       }
     }
   };
+  const LinCode code = lin_code<F16>();
   if (a.chunks == 1) load_x(0);
 
   int buf = 0;
@@ -162,7 +163,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
               if (32 * kPer * q >= left) break;
               lin_f32x4 c = {0, 0, 0, 0};
 #pragma unroll
-              for (int g = q * kPer; g < (q + 1) * kPer; ++g) c = lin_mfma<F16>(xf[st][g], lin_codes16<F16>(w4[g]), c);
+              for (int g = q * kPer; g < (q + 1) * kPer; ++g) c = lin_mfma<F16>(xf[st][g], lin_codes16<F16>(w4[g], code), c);
               const float s = q & 1 ? bf16_hi_to_f32(sw[st][q / 2]) : bf16_lo_to_f32(sw[st][q / 2]);
               const float b = q & 1 ? bf16_hi_to_f32(bw[st][q / 2]) : bf16_lo_to_f32(bw[st][q / 2]);
               const float off = __builtin_fmaf(-16.0f, s, b);
@@ -231,7 +232,7 @@ TilesPlan tiles_plan(int L, int N, int K) {
 }
 
 struct TilesWorkspace {
-  size_t xq, xsum, xexp, sh, wexp, part, total;
+  size_t xq, xsum, tsum, xexp, sh, wexp, part, total;
 };
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 TilesWorkspace tiles_layout(int fmt, int L, int N, int K) {
@@ -242,6 +243,7 @@ TilesWorkspace tiles_layout(int fmt, int L, int N, int K) {
   size_t off = 0;
   w.xq = off;   off = round256(off + (affine ? (size_t)p.tok_tiles * p.mt * 16 * ((K + kLinStep - 1) / kLinStep * kLinStep) * 2 : 0));
   w.xsum = off; off = round256(off + (affine ? 3 * (size_t)L * Gp * 2 : 0));
+  w.tsum = off; off = round256(off + (affine ? 3 * (size_t)N * Gp * 2 : 0));
   w.xexp = off; off = round256(off + (affine ? (size_t)L * 4 : 0));
   w.sh = off;   off = round256(off + (affine ? (size_t)N * G * 2 : 0));
   w.wexp = off; off = round256(off + (affine || fmt == kLinMxfp4 ? (size_t)N * 4 : 0));
@@ -273,7 +275,6 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
   a.Gp = (a.G + 31) / 32 * 32;
   a.out_dtype = l.out_dtype;
   a.terms = l.out_dtype == MOE_Q4_DTYPE_F32 ? 3 : 2;
-  a.bvec = a.G % 8 == 0 && (uintptr_t)l.s % 16 == 0 && (uintptr_t)l.b % 16 == 0;
   a.splits = p.splits; a.steps_per = p.steps_per;
   a.stagger = std::max(1, p.steps_per / p.tok_tiles);
   a.row_tiles = p.row_tiles; a.tok_tiles = p.tok_tiles;
@@ -282,7 +283,7 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
   if constexpr (kRowsScaled) {
     a.wexp = reinterpret_cast<int32_t*>(ws + lay.wexp);
     PrepareArgs q{};
-    q.x = l.x; q.s = l.s;
+    q.x = l.x; q.s = l.s; q.b = l.b;
     q.wexp = reinterpret_cast<int32_t*>(ws + lay.wexp);
     q.ldx = l.ldx;
     q.L = l.L; q.N = l.N; q.K = l.K; q.G = a.G; q.Gp = a.Gp;
@@ -296,8 +297,8 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
       a.xsum = q.xsum;
       a.xexp = F16 ? nullptr : q.xexp;
       a.sh = q.sh;
-      a.sraw = reinterpret_cast<const uint16_t*>(l.s);
-      a.braw = reinterpret_cast<const uint16_t*>(l.b);
+      q.tsum = reinterpret_cast<uint16_t*>(ws + lay.tsum);
+      a.tsum = q.tsum;
     }
     hipLaunchKernelGGL((k_linear_prepare<FMT, F16>), dim3(q.tok_blocks + (l.N + 3) / 4), dim3(256), 0, stream, q);
     if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;

@@ -46,15 +46,24 @@ __device__ __forceinline__ lin_f32x4 lin_mfma(uint4 a, uint4 b, lin_f32x4 c) {
 // (q3,q7): a code in the top mantissa bits under the exponent of 16.  The
 // smallest offset that one mask and one or can give keeps the fp32 sums
 // near the size of the codes' own (128 + q would cost three more bits).
+// Mask and base come in registers (one scalar, one vector: what a
+// three-operand instruction may read), so each pair is a shift and one
+// v_and_or; as literals they would be two instructions.
+struct LinCode {
+  uint32_t mask, base;
+};
 template <bool F16>
-__device__ __forceinline__ uint4 lin_codes16(uint32_t w) {
-  constexpr uint32_t kMask = F16 ? 0x03C003C0u : 0x00780078u, kBase = F16 ? 0x4C004C00u : 0x41804180u;
-  if constexpr (F16)
-    return make_uint4(((w << 6) & kMask) | kBase, ((w << 2) & kMask) | kBase, ((w >> 2) & kMask) | kBase,
-                      ((w >> 6) & kMask) | kBase);
-  else
-    return make_uint4(((w << 3) & kMask) | kBase, ((w >> 1) & kMask) | kBase, ((w >> 5) & kMask) | kBase,
-                      ((w >> 9) & kMask) | kBase);
+__device__ __forceinline__ LinCode lin_code() {
+  LinCode c{F16 ? 0x03C003C0u : 0x00780078u, F16 ? 0x4C004C00u : 0x41804180u};
+  asm("" : "+s"(c.mask));
+  asm("" : "+v"(c.base));
+  return c;
+}
+template <bool F16>
+__device__ __forceinline__ uint4 lin_codes16(uint32_t w, LinCode c) {
+  constexpr int kUp = F16 ? 6 : 3;  // from a word's lowest code to the mantissa's top
+  return make_uint4(((w << kUp) & c.mask) | c.base, ((F16 ? w << 2 : w >> 1) & c.mask) | c.base,
+                    ((w >> (8 - kUp)) & c.mask) | c.base, ((w >> (12 - kUp)) & c.mask) | c.base);
 }
 
 // Eight activations in the order lin_codes16 gives the codes.

@@ -13,8 +13,8 @@
 //            below the largest of its row loses bits, far below fp32's own
 //            rounding of the sum.
 // The affine rest, sum over groups of (b + 8 s) X with X = sum of the group's
-// x, is a product over K / group columns; it starts the accumulators, with b
-// and s as they are and X as two or three bf16 terms.
+// x, is a product over K / group columns; it starts the accumulators, both
+// factors as two or three bf16 terms.
 //
 // A wave holds 16 NT rows' codes in registers, one step ahead; the tokens'
 // step (of affine weights: blocks of 16 tokens x 128 inputs, laid out first)
@@ -36,8 +36,7 @@ struct TilesArgs {
   const uint32_t* w;
   const unsigned char* s;  // scales as given (nvfp4, mxfp4)
   const uint16_t* sh;      // affine: fp16 scales over their row's power of two [N][G]
-  const uint16_t* sraw;    // affine: bf16 scales and biases as given
-  const uint16_t* braw;
+  const uint16_t* tsum;    // affine: bf16 terms of b + 8 s [3][N][Gp]
   const uint16_t* xsum;    // affine: bf16 terms of the group sums [3][L][Gp]
   const int32_t* xexp;     // power of two of each token (affine with bf16 tokens), or NULL
   const int32_t* wexp;     // power of two of each row (affine; mxfp4 with fp16 tokens), or NULL
@@ -47,8 +46,7 @@ struct TilesArgs {
   long long ldx, ldo;
   int L, N, K, G, Gp;
   int out_dtype;
-  int terms;               // bf16 terms of X that are used
-  int bvec;                // biases and scales can be read 8 groups at a time
+  int terms;               // how many bf16 terms are used: 3, or 2 (2^-17 of |t X|) for 16-bit results
   int splits, steps_per;   // steps of 128 inputs of each split
   int stagger;             // steps between the token tiles' first ones
   int row_tiles, tok_tiles;
@@ -61,8 +59,8 @@ __device__ __forceinline__ uint32_t lin_u(lin_f16x2 v) { return __builtin_bit_ca
 
 // s * (q - 8) of a word's codes in fp16: one fused multiply-add a pair, its
 // addend -24 s exact (9 significant bits) and its result too.
-__device__ __forceinline__ uint4 lin_affine_f16(uint32_t w, lin_f16x2 s, lin_f16x2 m24s) {
-  const uint4 c = lin_codes16<true>(w);
+__device__ __forceinline__ uint4 lin_affine_f16(uint32_t w, LinCode code, lin_f16x2 s, lin_f16x2 m24s) {
+  const uint4 c = lin_codes16<true>(w, code);
   return make_uint4(lin_u(__builtin_elementwise_fma(lin_h2(c.x), s, m24s)), lin_u(__builtin_elementwise_fma(lin_h2(c.y), s, m24s)),
                     lin_u(__builtin_elementwise_fma(lin_h2(c.z), s, m24s)), lin_u(__builtin_elementwise_fma(lin_h2(c.w), s, m24s)));
 }
@@ -158,49 +156,36 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
 
   if constexpr (lin_affine(FMT)) {
     if (split == 0) {
-      // sum over groups of s X, times 8, plus that of b X
+      // sum over groups of t X, t = b + 8 s, by their bf16 terms: the products
+      // whose terms' places add up to less than `terms`
 #pragma unroll 1
-      for (int pass = 0; pass < 2; ++pass) {
-        const uint16_t* src = pass ? a.braw : a.sraw;
-#pragma unroll 1
-        for (int g0 = 0; g0 < a.G; g0 += 32) {
-          const int g = g0 + 8 * kb;
-          uint4 bf[NT];
+      for (int g = 8 * kb; g < a.Gp; g += 32) {
+        uint4 tf[3][NT], xf[3][MT];
+        auto load_t = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint16_t* p = src + row[nt] * a.G + g;
-            if (a.bvec) {
-              bf[nt] = g < a.G ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-            } else {
-              bf[nt] = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-              for (int i = 7; i >= 0; --i) {  // shifts the groups in, the last one first
-                bf[nt].w = bf[nt].w << 16 | bf[nt].z >> 16;
-                bf[nt].z = bf[nt].z << 16 | bf[nt].y >> 16;
-                bf[nt].y = bf[nt].y << 16 | bf[nt].x >> 16;
-                bf[nt].x = bf[nt].x << 16 | (g + i < a.G ? p[i] : 0);
-              }
-            }
-          }
-#pragma unroll 1
-          for (int term = 0; term < a.terms; ++term) {
-            uint4 xf[MT];
+          for (int nt = 0; nt < NT; ++nt) tf[i][nt] = *reinterpret_cast<const uint4*>(a.tsum + ((size_t)i * a.N + row[nt]) * a.Gp + g);
+        };
+        auto load_x = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const size_t t = min(tok0 + 16 * mt + n16, a.L - 1);
-              xf[mt] = *reinterpret_cast<const uint4*>(a.xsum + ((size_t)term * a.L + t) * a.Gp + g);
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = lin_mfma<false>(bf[nt], xf[mt], acc[mt][nt]);
-          }
-        }
-        if (pass == 0) {
+          for (int mt = 0; mt < MT; ++mt)
+            xf[i][mt] = *reinterpret_cast<const uint4*>(a.xsum + ((size_t)i * a.L + min(tok0 + 16 * mt + n16, a.L - 1)) * a.Gp + g);
+        };
+        auto add = [&](int i, int j) __attribute__((always_inline)) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[mt][nt] *= 8.0f;
+            for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = lin_mfma<false>(tf[i][nt], xf[j][mt], acc[mt][nt]);
+        };
+        load_t(0); load_t(1); load_x(0);
+        add(0, 0); add(1, 0);
+        load_x(1);
+        add(0, 1);
+        if (a.terms == 3) {  // kept in this order: all terms at once would not fit the registers
+          add(1, 1);
+          __builtin_amdgcn_sched_barrier(0);
+          load_t(2); add(2, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          load_x(2); add(0, 2);
         }
       }
       // into the operands' units
@@ -282,6 +267,7 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
 
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
+  const LinCode code = lin_code<true>();
   int i = 0;
   auto body = [&](unsigned char* xb, unsigned char* other) __attribute__((always_inline)) {
     lin_u32x4 cn[NT];
@@ -322,7 +308,7 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
         else if constexpr (FMT == kLinMxfp4)
           wf[nt] = lin_fp4_pow2<F16>(cw[nt][j], sf[nt][0]);
         else
-          wf[nt] = lin_affine_f16(cw[nt][j], sv[nt], sm[nt]);
+          wf[nt] = lin_affine_f16(cw[nt][j], code, sv[nt], sm[nt]);
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -398,15 +384,27 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
   }
 }
 
+// v as three bf16 terms, hi + mid + lo, at `at` of three planes.
+__device__ __forceinline__ void store_terms(uint16_t* p, size_t at, size_t plane, float v) {
+  const uint32_t hi = f32_to_bf16_rne(v);
+  const float r = v - bf16_lo_to_f32(hi);
+  const uint32_t mid = f32_to_bf16_rne(r);
+  p[at] = (uint16_t)hi;
+  p[at + plane] = (uint16_t)mid;
+  p[at + 2 * plane] = (uint16_t)f32_to_bf16_rne(r - bf16_lo_to_f32(mid));
+}
+
 // Lays out what the tiles read besides codes and tokens.  One workgroup a
 // token (affine): its power of two, the fp16 copy in the codes' pair order
 // and the group sums' bf16 terms.  One wave a weight row (affine, and mxfp4
-// with fp16 tokens): its power of two and the fp16 scales.
+// with fp16 tokens): its power of two, the fp16 scales and b + 8 s in bf16 terms.
 struct PrepareArgs {
   const uint16_t* x;
   const unsigned char* s;
+  const unsigned char* b;
   uint16_t* xq;
   uint16_t* xsum;
+  uint16_t* tsum;
   int32_t* xexp;
   uint16_t* sh;
   int32_t* wexp;
@@ -473,14 +471,7 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
         sum += __shfl_xor(sum, 2, 64);
         if constexpr (kLanes == 8) sum += __shfl_xor(sum, 4, 64);
         if (c < a.K && (tid & (kLanes - 1)) == 0) {
-          const uint32_t hi = f32_to_bf16_rne(sum);
-          const float r = sum - bf16_lo_to_f32(hi);
-          const uint32_t mid = f32_to_bf16_rne(r);
-          const uint32_t lo = f32_to_bf16_rne(r - bf16_lo_to_f32(mid));
-          const size_t at = (size_t)t * a.Gp + c / lin_group(FMT), plane = (size_t)a.L * a.Gp;
-          a.xsum[at] = (uint16_t)hi;
-          a.xsum[at + plane] = (uint16_t)mid;
-          a.xsum[at + 2 * plane] = (uint16_t)lo;
+          store_terms(a.xsum, (size_t)t * a.Gp + c / lin_group(FMT), (size_t)a.L * a.Gp, sum);
         }
       }
       if (a.G + tid < a.Gp) {
@@ -504,8 +495,16 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
     for (int g = lane; g < a.G; g += 64) m = max(m, (int)(s[g] & 0x7FFFu));
     for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o, 64));
     const int e = m ? min(max(m >> 7, 1), 254) - 127 - 8 : 0;  // the largest falls in [2^8, 2^9): 24 s in 2^14
-    for (int g = lane; g < a.G; g += 64)
-      a.sh[n * a.G + g] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(bf16_to_f32(s[g]), -e));
+    const uint16_t* b = reinterpret_cast<const uint16_t*>(a.b) + n * a.G;
+    for (int g = lane; g < a.Gp; g += 64) {
+      float t = 0.0f;
+      if (g < a.G) {
+        const float v = bf16_to_f32(s[g]);
+        a.sh[n * a.G + g] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(v, -e));
+        t = __builtin_fmaf(8.0f, v, bf16_to_f32(b[g]));
+      }
+      store_terms(a.tsum, n * a.Gp + g, (size_t)a.N * a.Gp, t);
+    }
     if (lane == 0) a.wexp[n] = e;
   }
 }
