@@ -1,15 +1,5 @@
 // Device helpers of the dense 4-bit product: matrix-core operands out of
 // packed codes.  Internal header.
-//
-// A wave takes 128 inputs of 16 weight rows at a time: lane (n, kb) = (lane %
-// 16, lane / 16) loads 16 bytes (32 codes) of row n at input 32 kb, 64
-// contiguous bytes a row.  v_mfma_f32_16x16x32 sums 32 inputs, eight from
-// each kb; a scale group must not be mixed with another in one sum, so the
-// affine and mxfp4 words are transposed over the four kb (two pairs of
-// register swaps) until register g holds group g's 32 inputs: lane (n, kb)
-// then has inputs 32 g + 8 kb .. + 7.  Tokens are the other operand's rows,
-// and a lane's four sums are four tokens of one weight row, so one scale per
-// lane and group serves them.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -22,9 +12,11 @@ namespace moeq4 {
 constexpr int kLinAffine64 = 0, kLinAffine32 = 1, kLinMxfp4 = 2, kLinNvfp4 = 3;
 __host__ __device__ constexpr bool lin_affine(int f) { return f == kLinAffine64 || f == kLinAffine32; }
 __host__ __device__ constexpr int lin_group(int f) { return f == kLinAffine64 ? 64 : f == kLinNvfp4 ? 16 : 32; }
-constexpr int kLinStep = 128;  // inputs of one 16-byte load per lane
-// 32-bit words of one row's scales (biases) in a step
-__host__ __device__ constexpr int lin_scale_words(int f) { return f == kLinAffine32 ? 2 : 1; }
+// A wave takes weights 128 inputs (a step) of 16 rows at a time: lane (n, kb) =
+// (lane % 16, lane / 16) loads 16 bytes of row n, the 32 codes from input 32 kb,
+// so a row's 64 bytes are contiguous.  v_mfma_f32_16x16x32 sums the eight
+// inputs of a word over the four kb.
+constexpr int kLinStep = 128;
 
 typedef __bf16 lin_bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 lin_f16x8 __attribute__((ext_vector_type(8)));
@@ -87,6 +79,27 @@ __device__ __forceinline__ uint4 lin_fp4(uint32_t w) {
                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3)));
 }
 
+// mxfp4 codes times the power of two in the exponent of `s`.
+template <bool F16>
+__device__ __forceinline__ uint4 lin_fp4_pow2(uint32_t w, float s) {
+  if constexpr (F16)
+    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3)));
+  else
+    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3)));
+}
+
+// Value of byte B of a word of E4M3 bytes.
+template <int B>
+__device__ __forceinline__ float lin_e4m3(uint32_t w) {
+  return __builtin_amdgcn_cvt_f32_fp8((int)w, B);
+}
+
 // E2M1 values times an E4M3 scale: at most 2 + 4 significant bits and an
 // exponent both types hold, so the product is exact in bf16 and in fp16.
 template <bool F16>
@@ -128,12 +141,6 @@ __device__ __forceinline__ void lin_transpose(uint32_t (&w)[4]) {
   w[0] = s[0]; w[1] = s[1];
   s = __builtin_amdgcn_permlane16_swap(w[2], w[3], false, false);
   w[2] = s[0]; w[3] = s[1];
-}
-
-// Input of operand register g of lane row kb inside a step.
-template <int FMT>
-__device__ __forceinline__ constexpr int lin_input(int g, int kb) {
-  return FMT == kLinNvfp4 ? 32 * kb + 8 * g : 32 * g + 8 * kb;
 }
 
 }  // namespace moeq4

@@ -65,21 +65,6 @@ __device__ __forceinline__ uint4 lin_affine_f16(uint32_t w, LinCode code, lin_f1
                     lin_u(__builtin_elementwise_fma(lin_h2(c.z), s, m24s)), lin_u(__builtin_elementwise_fma(lin_h2(c.w), s, m24s)));
 }
 
-// mxfp4 codes times the power of two in the exponent of `s`.
-template <bool F16>
-__device__ __forceinline__ uint4 lin_fp4_pow2(uint32_t w, float s) {
-  if constexpr (F16)
-    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3)));
-  else
-    return make_uint4(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
-                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3)));
-}
-
 // The scale of a row's 32 inputs from k on (nvfp4: two scales), as stored.
 template <int FMT>
 __device__ __forceinline__ uint32_t tile_scale(const unsigned char* base, uint32_t row, int k) {
@@ -510,7 +495,7 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
 }
 
 // Adds the splits of K in ascending order, the bias, and rounds.
-__global__ __launch_bounds__(256) void k_linear_join(const float* __restrict__ part, const float* __restrict__ bias,
+static __global__ __launch_bounds__(256) void k_linear_join(const float* __restrict__ part, const float* __restrict__ bias,
                                                      void* out, long long ldo, int L, int N, int splits, int dtype) {
   const size_t all = (size_t)L * N;
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (size_t)gridDim.x * 256) {
