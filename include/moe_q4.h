@@ -97,6 +97,7 @@ extern "C" {
 #define MOE_Q4_BALANCE_MAX_SEQS 65535 /* sequences of one moe_balance_loss call                 */
 #define MOE_Q4_LINEAR_MAX_L 1048560  /* tokens of one moe_linear_codec_forward call            */
 #define MOE_Q4_LINEAR_MAX_K 1048576  /* inputs of a row of moe_linear_codec_forward            */
+#define MOE_Q4_LINEAR_MAX_LDX 16777216 /* distance of its x rows                              */
 
 /* ---- forward stages (moe_swiglu_q4_forward_stages) ---- */
 #define MOE_Q4_STAGE_GATEUP 1u   /* union (or sort) + fused gate/up + silu(gate)*up -> workspace  */
@@ -360,7 +361,7 @@ int moe_sort_pairs(const int32_t *topk_ids, int L, int k, int E, int bm, int32_t
  *
  * Products are exact, sums are fp32 and rounded once to out_dtype; results are
  * deterministic.  L == 0 returns MOE_Q4_OK without touching the GPU.  Needs
- * L <= MOE_Q4_LINEAR_MAX_L and K <= MOE_Q4_LINEAR_MAX_K.
+ * L <= MOE_Q4_LINEAR_MAX_L, K <= MOE_Q4_LINEAR_MAX_K, ldx <= MOE_Q4_LINEAR_MAX_LDX.
  */
 int moe_linear_codec_forward(int codec, const void *x, int x_dtype, long long ldx, const uint32_t *w,
                              const void *s, const void *b, const float *bias, int L, int N, int K,

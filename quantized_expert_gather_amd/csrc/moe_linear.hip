@@ -44,8 +44,8 @@ using namespace moeq4;
 
 extern "C" size_t moe_linear_codec_workspace_bytes(int codec, int L, int N, int K) {
   const int fmt = linear_fmt(codec);
-  if (linear_shape_status(fmt, L, N, K) || L < kTilesFrom) return 0;
-  return tiles_layout(fmt, L, N, K).total;
+  if (linear_shape_status(fmt, L, N, K) || L == 0) return 0;
+  return L < kTilesFrom ? rows_workspace(fmt, L, N, K) : tiles_layout(fmt, L, N, K).total;
 }
 
 extern "C" int moe_linear_codec_forward(int codec, const void* x, int x_dtype, long long ldx, const uint32_t* w,
@@ -56,6 +56,7 @@ extern "C" int moe_linear_codec_forward(int codec, const void* x, int x_dtype, l
   const int st = linear_shape_status(fmt, L, N, K);
   if (st) return st;
   if (ldx < K || ldo < N) return MOE_Q4_ERR_SHAPE;
+  if (L > 1 && ldx > MOE_Q4_LINEAR_MAX_LDX) return MOE_Q4_ERR_UNSUPPORTED;
   if (x_dtype != MOE_Q4_DTYPE_BF16 && x_dtype != MOE_Q4_DTYPE_F16) return MOE_Q4_ERR_UNSUPPORTED;
   if (out_dtype != MOE_Q4_DTYPE_BF16 && out_dtype != MOE_Q4_DTYPE_F32 && out_dtype != MOE_Q4_DTYPE_F16)
     return MOE_Q4_ERR_UNSUPPORTED;
@@ -77,7 +78,7 @@ extern "C" int moe_linear_codec_forward(int codec, const void* x, int x_dtype, l
   for (const auto& in : ins)
     if (overlap(out, on, in.p, in.n)) return MOE_Q4_ERR_ALIAS;
   const LinearArgs a{static_cast<const uint16_t*>(x), w, static_cast<const unsigned char*>(s),
-               static_cast<const unsigned char*>(b), bias, out, ldx, ldo, L, N, K, out_dtype, 1};
+               affine ? static_cast<const unsigned char*>(b) : nullptr, bias, out, ldx, ldo, L, N, K, out_dtype, nullptr, 0};
   const bool f16 = x_dtype == MOE_Q4_DTYPE_F16;
   unsigned char* wsb = static_cast<unsigned char*>(workspace);
   switch (fmt) {

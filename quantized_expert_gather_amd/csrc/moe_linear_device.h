@@ -24,8 +24,10 @@ typedef _Float16 lin_f16x2 __attribute__((ext_vector_type(2)));
 typedef float lin_f32x2 __attribute__((ext_vector_type(2)));
 typedef float lin_f32x4 __attribute__((ext_vector_type(4)));
 
-template <bool F16>
-__device__ __forceinline__ lin_f32x4 lin_mfma(uint4 a, uint4 b, lin_f32x4 c) {
+typedef unsigned int lin_u32x4 __attribute__((ext_vector_type(4)));
+
+template <bool F16, class A, class B>
+__device__ __forceinline__ lin_f32x4 lin_mfma(A a, B b, lin_f32x4 c) {
   if constexpr (F16)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(lin_f16x8, a), __builtin_bit_cast(lin_f16x8, b), c,
                                                   0, 0, 0);
@@ -128,6 +130,14 @@ __device__ __forceinline__ uint4 lin_fp4_scaled(uint32_t w, float s) {
 __device__ __forceinline__ float lin_e8m0(uint32_t e) {
   const uint32_t v = e == 0 ? 0x00400000u : e << 23;
   return __uint_as_float(e == 255u ? 0x7FC00000u : v);
+}
+
+// Buffer loads of one or two bytes with a wave-uniform offset beside the lane's.
+__device__ __forceinline__ uint32_t bld1s(rsrc_t r, uint32_t off, int soff) {
+  return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(r, off, soff, 0);
+}
+__device__ __forceinline__ uint32_t bld2s(rsrc_t r, uint32_t off, int soff) {
+  return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, soff, 0);
 }
 
 // Transposes the 4 x 4 words of four 16-lane rows: w[j] of row kb goes to

@@ -62,7 +62,25 @@ inline TilesWorkspace tiles_layout(int fmt, int L, int N, int K) {
   return w;
 }
 
+// Whether the scale arrays can be read by words.
+inline bool linear_words(const LinearArgs& a) { return (uintptr_t)a.s % 4 == 0 && (uintptr_t)a.b % 4 == 0; }
+
+// Bytes of partial sums of a call with few tokens, whatever its x and the
+// alignment of its scales.
+inline size_t rows_workspace(int fmt, int L, int N, int K) {
+  if (K < kLinStep) return 0;
+  const int s = std::max({rows_plan(fmt, false, K, true).splits, rows_plan(fmt, true, K, true).splits,
+                          rows_plan(fmt, false, K, false).splits});
+  return s > 1 ? lin_round256((size_t)s * L * N * 4) : 0;
+}
+
 #ifdef MOE_LINEAR_INST
+inline void launch_linear_join(const LinearArgs& l, const float* part, int splits, hipStream_t stream) {
+  const size_t all = (size_t)l.L * l.N;
+  hipLaunchKernelGGL(k_linear_join, dim3((unsigned)std::min<size_t>((all + 255) / 256, 4096)), dim3(256), 0, stream, part,
+                     l.bias, l.out, l.ldo, l.L, l.N, splits, l.out_dtype);
+}
+
 template <int FMT, bool F16, int MT>
 void launch_tiles_mt(const TilesArgs& a, const TilesPlan& p, hipStream_t stream) {
   const dim3 grid(p.row_tiles * p.tok_tiles, p.splits), block(256);
@@ -120,11 +138,7 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
     default: launch_tiles_mt<FMT, F16, 8>(a, p, stream); break;
   }
   if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
-  if (p.splits > 1) {
-    const size_t all = (size_t)l.L * l.N;
-    hipLaunchKernelGGL(k_linear_join, dim3((unsigned)std::min<size_t>((all + 255) / 256, 4096)), dim3(256), 0, stream, a.part,
-                       l.bias, l.out, l.ldo, l.L, l.N, p.splits, l.out_dtype);
-  }
+  if (p.splits > 1) launch_linear_join(l, a.part, p.splits, stream);
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }
 
@@ -137,11 +151,14 @@ int linear_launch(bool f16, const LinearArgs& a, unsigned char* ws, hipStream_t 
       hipLaunchKernelGGL((k_linear_short<FMT, true>), grid, dim3(256), 0, stream, a);
     else
       hipLaunchKernelGGL((k_linear_short<FMT, false>), grid, dim3(256), 0, stream, a);
-  } else if (f16) {
-    launch_linear_rows<FMT, true>(a, stream);
-  } else {
-    launch_linear_rows<FMT, false>(a, stream);
+    return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
   }
+  const RowsPlan p = rows_plan(FMT, f16, a.K, linear_words(a));
+  LinearArgs l = a;
+  if (p.splits > 1) l.part = reinterpret_cast<float*>(ws);
+  f16 ? launch_linear_rows<FMT, true>(l, p, stream) : launch_linear_rows<FMT, false>(l, p, stream);
+  if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
+  if (p.splits > 1) launch_linear_join(l, l.part, p.splits, stream);
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }
 #endif

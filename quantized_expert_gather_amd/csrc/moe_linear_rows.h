@@ -2,8 +2,8 @@
 //
 // A workgroup takes 16 weight rows at a time, its W waves splitting K; wave
 // w's S steps of 128 inputs of x stay in its registers over all the rows it
-// meets (longer K is taken in passes), and the next rows' codes are on their
-// way while these are multiplied.  A lane (n, kb) loads 16 bytes of row n, the
+// meets, and D tiles of rows are on their way at a time (K beyond W S steps
+// is split over workgroups).  A lane (n, kb) loads 16 bytes of row n, the
 // 32 codes from input 32 kb of the step; a matrix product of their words with
 // x sums over n's four lanes, which hold different scale groups.  So
 //   mxfp4       the block's power of two goes into the bf16 operand, exact
@@ -36,7 +36,8 @@ struct LinearArgs {
   long long ldx, ldo;
   int L, N, K;
   int out_dtype;
-  int passes;  // passes over K that the waves' registers take
+  float* part;        // K split over workgroups: [splits][L][N] partial sums, else NULL
+  int split_steps;    // steps of each
 };
 
 __device__ __forceinline__ void lin_store(void* out, size_t at, int dtype, float v) {
@@ -48,8 +49,8 @@ __device__ __forceinline__ void lin_store(void* out, size_t at, int dtype, float
     static_cast<_Float16*>(out)[at] = (_Float16)v;
 }
 
-// Bytes of a row's scales in a step, and of those a lane reads: all of them
-// where it scales sums, its own block's where it scales operands.
+// Bytes of a row's scales in a step, and the words of those a lane reads: all
+// of them where it scales sums, its own block's where it scales operands.
 template <int FMT, bool FEW>
 struct LinScales {
   static constexpr bool kOwn = FMT == kLinMxfp4 || (FMT == kLinNvfp4 && !FEW);
@@ -57,12 +58,12 @@ struct LinScales {
   static constexpr int kWords = !kOwn && kStep == 8 ? 2 : 1;
 };
 
-// Reads them.  A row's scales may start at any byte, and the last step of a
-// row may be short: it is read from its end back (K >= 128) and shifted down,
-// which leaves zeros for what is not there.
+// Reads a lane's scales of a step where rows of scales may start at any byte
+// or end inside a step: a short last step is read from its end back (K >= 128)
+// and shifted down, which leaves zeros for what is not there.
 template <int FMT, bool FEW>
-__device__ __forceinline__ void lin_scales(const unsigned char* row, int step, int kb, int row_bytes, bool ragged,
-                                           uint32_t (&v)[LinScales<FMT, FEW>::kWords]) {
+__device__ __forceinline__ void lin_scales_any(const unsigned char* row, int step, int kb, int row_bytes,
+                                               uint32_t (&v)[LinScales<FMT, FEW>::kWords]) {
   typedef LinScales<FMT, FEW> Sc;
   if constexpr (Sc::kOwn) {
     constexpr int kBytes = Sc::kStep / 4;
@@ -72,27 +73,24 @@ __device__ __forceinline__ void lin_scales(const unsigned char* row, int step, i
     else
       v[0] = *reinterpret_cast<const uint16_t*>(row + at);
   } else {
-    int at = step * Sc::kStep, shift = 0;
-    if (ragged) {
-      const int last = row_bytes - Sc::kStep;
-      shift = 8 * max(at - last, 0);
-      at = min(at, last);
-    }
+    const int last = row_bytes - Sc::kStep, at = min(step * Sc::kStep, last);
+    const int shift = 8 * (step * Sc::kStep - at);
     if constexpr (Sc::kStep == 4) {
       uint32_t u;
       __builtin_memcpy(&u, row + at, 4);
-      v[0] = u >> shift;
+      v[0] = shift > 31 ? 0u : u >> shift;
     } else {
       uint64_t u;
       __builtin_memcpy(&u, row + at, 8);
-      u >>= shift;
+      u = shift > 63 ? 0u : u >> shift;
       v[0] = (uint32_t)u;
       v[1] = (uint32_t)(u >> 32);
     }
   }
 }
 
-template <int FMT, bool F16, bool FEW, int S, int W>
+// PLAIN: K in whole steps, scale arrays on words.
+template <int FMT, bool F16, bool FEW, bool PLAIN, int S, int W>
 __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
   typedef LinScales<FMT, FEW> Sc;
   constexpr bool kAffine = lin_affine(FMT);
@@ -102,86 +100,115 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
   constexpr int kX = kTerms ? 2 : 1;
   constexpr int kGroups = FMT == kLinAffine64 ? 2 : 4;  // group sums of x a step (affine)
   constexpr int kAcc = kSep ? 1 : 4;
+  constexpr int kDeep = S == 1 ? 4 : S == 2 ? 3 : 2;    // tiles on their way
   __shared__ float red[2][W][kAcc * 64];
   __shared__ __attribute__((aligned(16))) float xsum[kAffine ? W * S * kGroups * 16 : 1];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int n16 = lane & 15, kb = lane >> 4;
   const int t0 = blockIdx.y * 16;
-  const int steps = (a.K + kLinStep - 1) / kLinStep;
-  const bool ragged = a.K % kLinStep != 0;
+  const int steps = min((a.K + kLinStep - 1) / kLinStep, ((int)blockIdx.z + 1) * a.split_steps);
+  const int first = blockIdx.z * a.split_steps + wave * S;  // this wave's first step
   const int tiles = (a.N + 15) / 16;
   const int wrow = a.K / 2, srow = a.K / lin_group(FMT) * (kAffine ? 2 : 1);
   const LinCode code = lin_code<F16>();
 
-  struct Rows {  // a pass over 16 rows, as loaded
-    uint4 c[S];
+  struct Rows {  // 16 rows, as loaded
+    lin_u32x4 c[S];
     uint32_t s[S][Sc::kWords], b[kAffine ? S : 1][Sc::kWords];
   };
-  auto load = [&](int tile, int pass, Rows& r) __attribute__((always_inline)) {
-    const size_t row = min(tile * 16 + n16, a.N - 1);
-    const int first = (pass * W + wave) * S;
-    const unsigned char* w = reinterpret_cast<const unsigned char*>(a.w) + row * wrow;
+  // Rows past N lie past the buffers' ranges and read as zero.
+  const uint32_t woff = n16 * wrow + 16 * kb, soff = n16 * srow + (Sc::kOwn ? kb * (Sc::kStep / 4) : 0);
+  auto load = [&](int tile, Rows& r) __attribute__((always_inline)) {
+    const int rows = min(a.N - tile * 16, 16);
+    const rsrc_t wr = make_rsrc(reinterpret_cast<const unsigned char*>(a.w) + (size_t)tile * 16 * wrow, rows * wrow);
 #pragma unroll
     for (int st = 0; st < S; ++st) {
       if (first + st >= steps) break;
-      const int at = (first + st) * (kLinStep / 2) + 16 * kb;
-      r.c[st] = *reinterpret_cast<const uint4*>(w + (ragged ? min(at, wrow - 16) : at));
+      // a short last step's missing codes are those of the row's end: x is zero there
+      const uint32_t at = PLAIN ? woff : woff + min(0, wrow - 64 - (first + st) * 64 + 48 - 16 * kb);
+      r.c[st] = __builtin_bit_cast(lin_u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, at + st * 64, first * 64, 0));
     }
-#pragma unroll
-    for (int st = 0; st < S; ++st) {
-      if (first + st >= steps) break;
-      lin_scales<FMT, FEW>(a.s + row * srow, first + st, kb, srow, ragged, r.s[st]);
-      if constexpr (kAffine) lin_scales<FMT, FEW>(a.b + row * srow, first + st, kb, srow, ragged, r.b[st]);
-    }
-  };
-
-  uint4 xf[S][4][kX];
-  auto load_x = [&](int pass) __attribute__((always_inline)) {
-    const int first = (pass * W + wave) * S;
-    const int t = t0 + (kSep ? n16 >> 2 : n16);
-    const bool live = t < a.L && (!kSep || (n16 & 3) == kb);
-    const uint16_t* x = a.x + (size_t)min(t, a.L - 1) * a.ldx + first * kLinStep;
-#pragma unroll
-    for (int st = 0; st < S; ++st)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) xf[st][j][0] = make_uint4(0, 0, 0, 0);
-    if (live) {
+    if constexpr (PLAIN) {
+      const rsrc_t sr = make_rsrc(a.s + (size_t)tile * 16 * srow, rows * srow);
+      const rsrc_t br = make_rsrc(a.b + (kAffine ? (size_t)tile * 16 * srow : 0), kAffine ? rows * srow : 0);
+      auto get = [&](rsrc_t p, int st, uint32_t (&v)[Sc::kWords]) __attribute__((always_inline)) {
+        if constexpr (Sc::kOwn && FMT == kLinMxfp4) {
+          v[0] = bld1s(p, soff + st * Sc::kStep, first * Sc::kStep);
+        } else if constexpr (Sc::kOwn) {
+          v[0] = bld2s(p, soff + st * Sc::kStep, first * Sc::kStep);
+        } else if constexpr (Sc::kStep == 4) {
+          v[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(p, soff + st * Sc::kStep, first * Sc::kStep, 0);
+        } else {
+          const auto u = __builtin_amdgcn_raw_buffer_load_b64(p, soff + st * Sc::kStep, first * Sc::kStep, 0);
+          v[0] = (uint32_t)u[0];
+          v[1] = (uint32_t)u[1];
+        }
+      };
 #pragma unroll
       for (int st = 0; st < S; ++st) {
         if (first + st >= steps) break;
+        get(sr, st, r.s[st]);
+        if constexpr (kAffine) get(br, st, r.b[st]);
+      }
+    } else {
+      const size_t row = min(tile * 16 + n16, a.N - 1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // operand register j: after the transpose block j's inputs, else word j of block kb
-          const int c = st * kLinStep + (kTurn ? 32 * j + 8 * kb : 32 * kb + 8 * j);
-          if (!ragged || first * kLinStep + c < a.K) xf[st][j][0] = *reinterpret_cast<const uint4*>(x + c);
-        }
+      for (int st = 0; st < S; ++st) {
+        if (first + st >= steps) break;
+        lin_scales_any<FMT, FEW>(a.s + row * srow, first + st, kb, srow, r.s[st]);
+        if constexpr (kAffine) lin_scales_any<FMT, FEW>(a.b + row * srow, first + st, kb, srow, r.b[st]);
+      }
+    }
+  };
+
+  lin_u32x4 xf[S][4][kX];
+  auto load_x = [&]() __attribute__((always_inline)) {
+    const int t = t0 + (kSep ? n16 >> 2 : n16);
+    const bool live = t < a.L && (!kSep || (n16 & 3) == kb);
+    // reads past the range give zeros: dead lanes' offsets lie there
+    const int rows = min(a.L - t0, 16);
+    const rsrc_t xr = make_rsrc(a.x + (size_t)t0 * a.ldx, (uint32_t)((rows - 1) * (uint32_t)a.ldx + a.K) * 2u);
+    const uint32_t off = live ? (uint32_t)(t - t0) * (uint32_t)a.ldx * 2u + (kTurn ? 16 * kb : 64 * kb) : 0x80000000u;
+#pragma unroll
+    for (int st = 0; st < S; ++st) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // operand register j: after the transpose block j's inputs, else word j of block kb
+        const int c = st * kLinStep + (kTurn ? 32 * j : 8 * j);
+        uint32_t at = off + 2 * c;
+        // steps past the split's end, and inputs past the row's, count as zero
+        if (first + st >= steps) at = 0x80000000u;
+        if (!PLAIN && first * kLinStep + c + (kTurn ? 8 : 32) * kb >= a.K) at = 0x80000000u;
+        xf[st][j][0] = __builtin_bit_cast(lin_u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, at, first * kLinStep * 2, 0));
       }
     }
 #pragma unroll
     for (int st = 0; st < S; ++st)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (kAffine) xf[st][j][0] = lin_pair_order(xf[st][j][0]);
+        const lin_u32x4 v = xf[st][j][0];
+        if constexpr (kAffine) {  // the codes' pair order
+          xf[st][j][0] = lin_u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
+                                   __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
+        }
         if constexpr (kTerms) {
-          uint32_t q[4] = {xf[st][j][0].x, xf[st][j][0].y, xf[st][j][0].z, xf[st][j][0].w}, hi[4], lo[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // 11 bits as 8 + 3, both exact
-            const lin_f16x2 h = __builtin_bit_cast(lin_f16x2, q[i]);
+            const uint32_t word = v[i];
+            const lin_f16x2 h = __builtin_bit_cast(lin_f16x2, word);
             const float f0 = (float)h.x, f1 = (float)h.y;
             const uint32_t h0 = __float_as_uint(f0) & 0xFFFF0000u, h1 = __float_as_uint(f1) & 0xFFFF0000u;
-            hi[i] = h0 >> 16 | h1;
             // (an infinite or NaN x has no second term)
             const float r0 = f0 - __uint_as_float(h0), r1 = f1 - __uint_as_float(h1);
-            lo[i] = (r0 == r0 ? __float_as_uint(r0) >> 16 : 0u) | (r1 == r1 ? __float_as_uint(r1) & 0xFFFF0000u : 0u);
+            xf[st][j][0][i] = h0 >> 16 | h1;
+            xf[st][j][kX - 1][i] = (r0 == r0 ? __float_as_uint(r0) >> 16 : 0u) | (r1 == r1 ? __float_as_uint(r1) & 0xFFFF0000u : 0u);
           }
-          xf[st][j][0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          xf[st][j][kX - 1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
     if constexpr (kAffine) {  // x times ones is the group sums, in the layout of the products
       const uint32_t one = F16 ? 0x3C003C00u : 0x3F803F80u;
-      const uint4 ones = make_uint4(one, one, one, one);
+      const lin_u32x4 ones = {one, one, one, one};
 #pragma unroll
       for (int st = 0; st < S; ++st) {
         float* to = xsum + (wave * S + st) * kGroups * 16;
@@ -211,15 +238,13 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
   };
 
   lin_f32x4 acc = {0, 0, 0, 0};
-  auto multiply = [&](const Rows& r, int pass) __attribute__((always_inline)) {
-    const int first = (pass * W + wave) * S;
+  auto multiply = [&](const Rows& r) __attribute__((always_inline)) {
 #pragma unroll
     for (int st = 0; st < S; ++st) {
       if (first + st >= steps) break;
-      uint32_t w4[4] = {r.c[st].x, r.c[st].y, r.c[st].z, r.c[st].w};
+      uint32_t w4[4] = {r.c[st][0], r.c[st][1], r.c[st][2], r.c[st][3]};
       const float* xs = xsum + (wave * S + st) * kGroups * 16;
       if constexpr (FMT == kLinMxfp4) {
-        // past a row's end x is zero, and the codes and scales are the row's own last ones
         const float s = lin_e8m0(r.s[st][0]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -278,94 +303,107 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
 
   // The waves' sums of a tile, in ascending order of the waves.  The two
   // buffers alternate: a wave is at most one barrier ahead of the readers.
-  auto finish = [&](int tile, int buf) __attribute__((always_inline)) {
+  constexpr int kParts = W / 4;  // threads of an output, four waves' sums each
+  const int o = threadIdx.x / kParts, part = threadIdx.x % kParts;
+  const int at = 4 * part * kAcc * 64 + (kSep ? o : 4 * ((o & 15) + 16 * (o >> 6)) + ((o >> 4) & 3));
+  const int ot = t0 + (o >> 4);
+  const bool writes = part == 0 && ot < a.L;
+  auto finish = [&](int tile, float* buf) __attribute__((always_inline)) {
     if constexpr (kSep)
-      red[buf][wave][lane] = acc[0];
+      buf[wave * 64 + lane] = acc[0];
     else
-      *reinterpret_cast<lin_f32x4*>(&red[buf][wave][4 * lane]) = acc;
+      *reinterpret_cast<lin_f32x4*>(buf + wave * 256 + 4 * lane) = acc;
     acc = lin_f32x4{0, 0, 0, 0};
     __syncthreads();
-    constexpr int kParts = W / 4;  // threads of an output, four waves' sums each
-    const int o = threadIdx.x / kParts, part = threadIdx.x % kParts;
-    const int n = tile * 16 + (o & 15), t = t0 + (o >> 4);
     if (kSep && o >= 64) return;  // whole waves
-    const float* r = &red[buf][4 * part][kSep ? o : 4 * ((o & 15) + 16 * (o >> 6)) + ((o >> 4) & 3)];
+    const float* r = buf + at;
     constexpr int kWave = kAcc * 64;
     float v = (r[0] + r[kWave]) + (r[2 * kWave] + r[3 * kWave]);
     if constexpr (kParts >= 2) v += dpp_f32<0xB1>(v);  // lane ^ 1
     if constexpr (kParts >= 4) v += dpp_f32<0x4E>(v);  // lane ^ 2
-    if (part == 0 && t < a.L && n < a.N) {
-      if (a.bias) v += a.bias[n];
-      lin_store(a.out, (size_t)t * a.ldo + n, a.out_dtype, v);
+    const int n = tile * 16 + (o & 15);
+    if (writes && n < a.N) {
+      if (a.part) {
+        a.part[((size_t)blockIdx.z * a.L + ot) * a.N + n] = v;
+      } else {
+        if (a.bias) v += a.bias[n];
+        lin_store(a.out, (size_t)ot * a.ldo + n, a.out_dtype, v);
+      }
     }
   };
 
-  int tile = blockIdx.x, pass = 0, buf = 0;
-  auto body = [&](Rows& cur, Rows& nxt) __attribute__((always_inline)) {
-    int tile2 = tile, pass2 = pass + 1;
-    if (pass2 == a.passes) {
-      pass2 = 0;
-      tile2 += gridDim.x;
-    }
-    if (tile2 < tiles) load(tile2, pass2, nxt);
-    multiply(cur, pass);
-    if (pass2 == 0) {
-      finish(tile, buf);
-      buf ^= 1;
-    }
-    if (a.passes > 1 && tile2 < tiles) load_x(pass2);
-    tile = tile2;
-    pass = pass2;
-  };
-  Rows one, two;
-  load(tile, 0, one);
-  load_x(0);
+  Rows ring[kDeep];
+  int tile = blockIdx.x;
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d)
+    if (tile + d * (int)gridDim.x < tiles) load(tile + d * gridDim.x, ring[d]);
+  load_x();
+  float *buf = &red[0][0][0], *other = &red[1][0][0];
   while (true) {
-    body(one, two);
-    if (tile >= tiles) break;
-    body(two, one);
-    if (tile >= tiles) break;
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      multiply(ring[d]);
+      if (tile + kDeep * (int)gridDim.x < tiles) load(tile + kDeep * gridDim.x, ring[d]);
+      finish(tile, buf);
+      float* const t = buf;
+      buf = other;
+      other = t;
+      tile += gridDim.x;
+      if (tile >= tiles) return;
+    }
   }
 }
 
+struct RowsPlan {
+  int W, S, splits, split_steps;
+  bool plain;
+};
+// The longest K of one workgroup is 16 waves x 3 steps (2 where x takes two
+// operands); longer ones are split evenly.
+inline RowsPlan rows_plan(int fmt, bool f16, int K, bool words) {
+  RowsPlan p{};
+  p.plain = K % kLinStep == 0 && words;
+  const int steps = (K + kLinStep - 1) / kLinStep;
+  const int most = !p.plain ? 1 : fmt == kLinMxfp4 && f16 ? 2 : 3;
+  p.W = p.plain && steps <= 8 ? 8 : 16;
+  p.splits = (steps + 16 * most - 1) / (16 * most);
+  p.split_steps = (steps + p.splits - 1) / p.splits;
+  p.splits = (steps + p.split_steps - 1) / p.split_steps;
+  p.S = (p.split_steps + p.W - 1) / p.W;
+  return p;
+}
+
 template <int FMT, bool F16>
-void launch_linear_rows(const LinearArgs& args, hipStream_t stream) {
+void launch_linear_rows(const LinearArgs& args, const RowsPlan& p, hipStream_t stream) {
   LinearArgs a = args;
-  const int steps = (a.K + kLinStep - 1) / kLinStep;
-  const bool wide = steps > 12;  // 16 waves, else 8
-  const int W = wide ? 16 : 8;
-  constexpr int kMost = FMT == kLinMxfp4 && F16 ? 2 : 3;  // steps of x that fit a wave's registers
-  a.passes = (steps + kMost * W - 1) / (kMost * W);
-  const int S = (steps + a.passes * W - 1) / (a.passes * W);
+  a.split_steps = p.split_steps;
   const int tiles = (a.N + 15) / 16;
-  const int most = wide ? 256 : 512;  // workgroups that run at once
-  const int rounds = (tiles + most - 1) / most;
-  const dim3 grid((tiles + rounds - 1) / rounds, (a.L + 15) / 16), block(64 * W);
-  const bool few = a.L <= 4 && FMT != kLinMxfp4;
-#define MOE_LINEAR_ROWS(FEW, S)                                                                         \
-  if (wide)                                                                                             \
-    hipLaunchKernelGGL((k_linear_rows<FMT, F16, FEW, S, 16>), grid, block, 0, stream, a);               \
-  else                                                                                                  \
-    hipLaunchKernelGGL((k_linear_rows<FMT, F16, FEW, S, 8>), grid, block, 0, stream, a)
+  const int most = p.W == 16 ? 256 : 512;  // workgroups that run at once
+  const int rounds = (int)(((long)tiles * p.splits + most - 1) / most);
+  const dim3 grid((tiles + rounds - 1) / rounds, (a.L + 15) / 16, p.splits), block(64 * p.W);
+  const bool few = a.L <= 4;
+#define MOE_LINEAR_ROWS(FEW, PLAIN, S, W) \
+  hipLaunchKernelGGL((k_linear_rows<FMT, F16, FEW, PLAIN, S, W>), grid, block, 0, stream, a)
+#define MOE_LINEAR_ROWS_S(FEW)                         \
+  if (!p.plain) {                                      \
+    MOE_LINEAR_ROWS(FEW, false, 1, 16);                \
+  } else if (p.W == 8) {                               \
+    MOE_LINEAR_ROWS(FEW, true, 1, 8);                  \
+  } else if (p.S == 1) {                               \
+    MOE_LINEAR_ROWS(FEW, true, 1, 16);                 \
+  } else if (p.S == 2) {                               \
+    MOE_LINEAR_ROWS(FEW, true, 2, 16);                 \
+  } else if constexpr (!(FMT == kLinMxfp4 && F16)) {   \
+    MOE_LINEAR_ROWS(FEW, true, 3, 16);                 \
+  }
   if constexpr (FMT != kLinMxfp4) {
     if (few) {
-      switch (S) {
-        case 1: MOE_LINEAR_ROWS(true, 1); break;
-        case 2: MOE_LINEAR_ROWS(true, 2); break;
-        default: MOE_LINEAR_ROWS(true, 3); break;
-      }
+      MOE_LINEAR_ROWS_S(true)
       return;
     }
   }
-  switch (S) {
-    case 1: MOE_LINEAR_ROWS(false, 1); break;
-    case 2: MOE_LINEAR_ROWS(false, 2); break;
-    default:
-      if constexpr (kMost >= 3) {
-        MOE_LINEAR_ROWS(false, 3);
-      }
-      break;
-  }
+  MOE_LINEAR_ROWS_S(false)
+#undef MOE_LINEAR_ROWS_S
 #undef MOE_LINEAR_ROWS
 }
 

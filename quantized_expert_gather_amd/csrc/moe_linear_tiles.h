@@ -52,8 +52,6 @@ struct TilesArgs {
   int row_tiles, tok_tiles;
 };
 
-typedef unsigned int lin_u32x4 __attribute__((ext_vector_type(4)));
-
 __device__ __forceinline__ lin_f16x2 lin_h2(uint32_t v) { return __builtin_bit_cast(lin_f16x2, v); }
 __device__ __forceinline__ uint32_t lin_u(lin_f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
 

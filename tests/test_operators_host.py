@@ -38,6 +38,7 @@ def linear(codec=0, x=None, xd=0, ldx=None, w=None, s=None, b=None, bias=0, L=2,
     (dict(od=3), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(L=q.MOE_Q4_LINEAR_MAX_L + 1), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(K=q.MOE_Q4_LINEAR_MAX_K + 64), q.MOE_Q4_ERR_UNSUPPORTED),
+    (dict(ldx=q.MOE_Q4_LINEAR_MAX_LDX + 8), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(x=0), q.MOE_Q4_ERR_NULL),
     (dict(w=0), q.MOE_Q4_ERR_NULL),
     (dict(s=0), q.MOE_Q4_ERR_NULL),
