@@ -132,12 +132,23 @@ __device__ __forceinline__ float lin_e8m0(uint32_t e) {
   return __uint_as_float(e == 255u ? 0x7FC00000u : v);
 }
 
-// Buffer loads of one or two bytes with a wave-uniform offset beside the lane's.
-__device__ __forceinline__ uint32_t bld1s(rsrc_t r, uint32_t off, int soff) {
-  return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(r, off, soff, 0);
-}
-__device__ __forceinline__ uint32_t bld2s(rsrc_t r, uint32_t off, int soff) {
-  return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, soff, 0);
+// The values of the first S 16-lane rows, each to all four rows.
+template <int S>
+__device__ __forceinline__ void lin_spread(uint32_t v, uint32_t (&out)[S]) {
+  static_assert(S >= 1 && S <= 4, "rows of a wave");
+  if constexpr (S == 1) {
+    out[0] = v;
+  } else {
+    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // rows 0 1 0 1, rows 2 3 2 3
+    const auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    out[0] = lo[0];
+    out[1] = lo[1];
+    if constexpr (S > 2) {
+      const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+      out[2] = hi[0];
+      if constexpr (S > 3) out[3] = hi[1];
+    }
+  }
 }
 
 // Transposes the 4 x 4 words of four 16-lane rows: w[j] of row kb goes to

@@ -103,6 +103,8 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
   constexpr int kDeep = S == 1 ? 4 : S == 2 ? 3 : 2;    // tiles on their way
   __shared__ float red[2][W][kAcc * 64];
   __shared__ __attribute__((aligned(16))) float xsum[kAffine ? W * S * kGroups * 16 : 1];
+  constexpr int kStageSteps = kSep ? S : 1, kStageTokens = kSep ? 4 : 16;  // of x in LDS at a time
+  __shared__ lin_u32x4 xstage[W][kStageTokens * kStageSteps * 16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int n16 = lane & 15, kb = lane >> 4;
@@ -113,12 +115,16 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
   const int wrow = a.K / 2, srow = a.K / lin_group(FMT) * (kAffine ? 2 : 1);
   const LinCode code = lin_code<F16>();
 
+  // Scales: one load a tile, lane (n, kb) taking those of row n and step kb
+  // (every load of 16 rows' few bytes costs as much as one of their codes);
+  // row moves spread them when they are used.
+  constexpr int kRec = PLAIN ? Sc::kStep / 4 : Sc::kWords;
   struct Rows {  // 16 rows, as loaded
     lin_u32x4 c[S];
-    uint32_t s[S][Sc::kWords], b[kAffine ? S : 1][Sc::kWords];
+    uint32_t s[kRec], b[kAffine ? kRec : 1];
   };
   // Rows past N lie past the buffers' ranges and read as zero.
-  const uint32_t woff = n16 * wrow + 16 * kb, soff = n16 * srow + (Sc::kOwn ? kb * (Sc::kStep / 4) : 0);
+  const uint32_t woff = n16 * wrow + 16 * kb, soff = n16 * srow + min(kb, S - 1) * Sc::kStep;
   auto load = [&](int tile, Rows& r) __attribute__((always_inline)) {
     const int rows = min(a.N - tile * 16, 16);
     const rsrc_t wr = make_rsrc(reinterpret_cast<const unsigned char*>(a.w) + (size_t)tile * 16 * wrow, rows * wrow);
@@ -129,70 +135,70 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
       const uint32_t at = PLAIN ? woff : woff + min(0, wrow - 64 - (first + st) * 64 + 48 - 16 * kb);
       r.c[st] = __builtin_bit_cast(lin_u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, at + st * 64, first * 64, 0));
     }
+    if (first >= steps) return;
     if constexpr (PLAIN) {
       const rsrc_t sr = make_rsrc(a.s + (size_t)tile * 16 * srow, rows * srow);
       const rsrc_t br = make_rsrc(a.b + (kAffine ? (size_t)tile * 16 * srow : 0), kAffine ? rows * srow : 0);
-      auto get = [&](rsrc_t p, int st, uint32_t (&v)[Sc::kWords]) __attribute__((always_inline)) {
-        if constexpr (Sc::kOwn && FMT == kLinMxfp4) {
-          v[0] = bld1s(p, soff + st * Sc::kStep, first * Sc::kStep);
-        } else if constexpr (Sc::kOwn) {
-          v[0] = bld2s(p, soff + st * Sc::kStep, first * Sc::kStep);
-        } else if constexpr (Sc::kStep == 4) {
-          v[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(p, soff + st * Sc::kStep, first * Sc::kStep, 0);
+      auto get = [&](rsrc_t p, uint32_t* v) __attribute__((always_inline)) {
+        if constexpr (kRec == 1) {
+          v[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(p, soff, first * Sc::kStep, 0);
         } else {
-          const auto u = __builtin_amdgcn_raw_buffer_load_b64(p, soff + st * Sc::kStep, first * Sc::kStep, 0);
+          const auto u = __builtin_amdgcn_raw_buffer_load_b64(p, soff, first * Sc::kStep, 0);
           v[0] = (uint32_t)u[0];
           v[1] = (uint32_t)u[1];
         }
       };
-#pragma unroll
-      for (int st = 0; st < S; ++st) {
-        if (first + st >= steps) break;
-        get(sr, st, r.s[st]);
-        if constexpr (kAffine) get(br, st, r.b[st]);
-      }
+      get(sr, r.s);
+      if constexpr (kAffine) get(br, r.b);
     } else {
       const size_t row = min(tile * 16 + n16, a.N - 1);
-#pragma unroll
-      for (int st = 0; st < S; ++st) {
-        if (first + st >= steps) break;
-        lin_scales_any<FMT, FEW>(a.s + row * srow, first + st, kb, srow, r.s[st]);
-        if constexpr (kAffine) lin_scales_any<FMT, FEW>(a.b + row * srow, first + st, kb, srow, r.b[st]);
-      }
+      lin_scales_any<FMT, FEW>(a.s + row * srow, first, kb, srow, r.s);
+      if constexpr (kAffine) lin_scales_any<FMT, FEW>(a.b + row * srow, first, kb, srow, r.b);
     }
   };
 
+  // x comes through LDS: contiguous 16-byte pieces in, operands out (each
+  // wave its own inputs).
   lin_u32x4 xf[S][4][kX];
   auto load_x = [&]() __attribute__((always_inline)) {
-    const int t = t0 + (kSep ? n16 >> 2 : n16);
-    const bool live = t < a.L && (!kSep || (n16 & 3) == kb);
-    // reads past the range give zeros: dead lanes' offsets lie there
-    const int rows = min(a.L - t0, 16);
+    // reads past the range give zeros: inputs past the row's end or this split's lie there
+    const int rows = min(a.L - t0, kSep ? 4 : 16);
     const rsrc_t xr = make_rsrc(a.x + (size_t)t0 * a.ldx, (uint32_t)((rows - 1) * (uint32_t)a.ldx + a.K) * 2u);
-    const uint32_t off = live ? (uint32_t)(t - t0) * (uint32_t)a.ldx * 2u + (kTurn ? 16 * kb : 64 * kb) : 0x80000000u;
+    const int room = min(a.K, steps * kLinStep) - first * kLinStep;  // inputs of this wave's steps that count
+    lin_u32x4* const mine = xstage[wave];
+    constexpr int kPieces = kStageSteps * 16;  // of a token
 #pragma unroll
-    for (int st = 0; st < S; ++st) {
+    for (int s0 = 0; s0 < S; s0 += kStageSteps) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // operand register j: after the transpose block j's inputs, else word j of block kb
-        const int c = st * kLinStep + (kTurn ? 32 * j : 8 * j);
-        uint32_t at = off + 2 * c;
-        // steps past the split's end, and inputs past the row's, count as zero
-        if (first + st >= steps) at = 0x80000000u;
-        if (!PLAIN && first * kLinStep + c + (kTurn ? 8 : 32) * kb >= a.K) at = 0x80000000u;
-        xf[st][j][0] = __builtin_bit_cast(lin_u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, at, first * kLinStep * 2, 0));
+      for (int i0 = 0; i0 < kStageTokens * kPieces; i0 += 64) {
+        if (i0 >= rows * kPieces) break;
+        const int i = i0 + lane, t = i / kPieces, c = s0 * kLinStep + (i - t * kPieces) * 8;
+        const uint32_t at = t < rows && c < room ? ((uint32_t)t * (uint32_t)a.ldx + c) * 2u : 0x80000000u;
+        lin_u32x4 v = __builtin_bit_cast(lin_u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, at, first * kLinStep * 2, 0));
+        if constexpr (kAffine)  // the codes' pair order
+          v = lin_u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
+                        __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
+        if (i < kStageTokens * kPieces) mine[i] = v;
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const int t = kSep ? n16 >> 2 : n16;
+      const bool live = t < rows && (!kSep || (n16 & 3) == kb);
+#pragma unroll
+      for (int st = s0; st < s0 + kStageSteps; ++st)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // operand register j: after the transpose block j's inputs, else word j of block kb
+          const int piece = t * kPieces + (st - s0) * 16 + (kTurn ? 4 * j + kb : 4 * kb + j);
+          xf[st][j][0] = live ? mine[piece] : lin_u32x4{0, 0, 0, 0};
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 #pragma unroll
     for (int st = 0; st < S; ++st)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const lin_u32x4 v = xf[st][j][0];
-        if constexpr (kAffine) {  // the codes' pair order
-          xf[st][j][0] = lin_u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
-                                   __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
-        }
         if constexpr (kTerms) {
+          const lin_u32x4 v = xf[st][j][0];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // 11 bits as 8 + 3, both exact
             const uint32_t word = v[i];
@@ -239,13 +245,40 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
 
   lin_f32x4 acc = {0, 0, 0, 0};
   auto multiply = [&](const Rows& r) __attribute__((always_inline)) {
+    // this lane's scales of each step
+    uint32_t sv[S][Sc::kWords], bv[kAffine ? S : 1][Sc::kWords];
+    auto spread = [&](const uint32_t* rec, uint32_t (*v)[Sc::kWords]) __attribute__((always_inline)) {
+      uint32_t u[S][kRec];
+#pragma unroll
+      for (int w = 0; w < kRec; ++w) {
+        uint32_t one[S];
+        lin_spread<PLAIN ? S : 1>(rec[w], one);
+#pragma unroll
+        for (int st = 0; st < S; ++st) u[st][w] = one[st];
+      }
+#pragma unroll
+      for (int st = 0; st < S; ++st) {
+        if constexpr (!PLAIN || !Sc::kOwn) {
+#pragma unroll
+          for (int w = 0; w < Sc::kWords; ++w) v[st][w] = u[st][w];
+        } else if constexpr (kRec == 1) {
+          v[st][0] = (u[st][0] >> (8 * kb)) & 255u;
+        } else {
+          v[st][0] = (kb & 2 ? u[st][kRec - 1] : u[st][0]) >> (16 * (kb & 1));
+        }
+      }
+    };
+    if (first < steps) {
+      spread(r.s, sv);
+      if constexpr (kAffine) spread(r.b, bv);
+    }
 #pragma unroll
     for (int st = 0; st < S; ++st) {
       if (first + st >= steps) break;
       uint32_t w4[4] = {r.c[st][0], r.c[st][1], r.c[st][2], r.c[st][3]};
       const float* xs = xsum + (wave * S + st) * kGroups * 16;
       if constexpr (FMT == kLinMxfp4) {
-        const float s = lin_e8m0(r.s[st][0]);
+        const float s = lin_e8m0(sv[st][0]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint4 w = lin_fp4_pow2<false>(w4[j], s);
@@ -253,7 +286,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
           for (int i = 0; i < kX; ++i) acc = lin_mfma<false>(xf[st][j][i], w, acc);
         }
       } else if constexpr (FMT == kLinNvfp4 && !FEW) {
-        const float s0 = lin_e4m3<0>(r.s[st][0]), s1 = lin_e4m3<1>(r.s[st][0]);
+        const float s0 = lin_e4m3<0>(sv[st][0]), s1 = lin_e4m3<1>(sv[st][0]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc = lin_mfma<F16>(xf[st][j][0], lin_fp4_scaled<F16>(w4[j], j < 2 ? s0 : s1), acc);
       } else if constexpr (FMT == kLinNvfp4) {
@@ -262,7 +295,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
         c1 = lin_mfma<F16>(xf[st][2][0], lin_fp4<F16>(w4[2]), c1);
         c0 = lin_mfma<F16>(xf[st][1][0], lin_fp4<F16>(w4[1]), c0);
         c1 = lin_mfma<F16>(xf[st][3][0], lin_fp4<F16>(w4[3]), c1);
-        const uint32_t s0 = r.s[st][0], s1 = r.s[st][1];
+        const uint32_t s0 = sv[st][0], s1 = sv[st][1];
         acc[0] = __builtin_fmaf(lin_e4m3<0>(s0), c0[0], acc[0]);
         acc[0] = __builtin_fmaf(lin_e4m3<1>(s0), c1[0], acc[0]);
         acc[0] = __builtin_fmaf(lin_e4m3<2>(s0), c0[1], acc[0]);
@@ -279,7 +312,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
           for (int j = 0; j < 4; ++j) c = lin_mfma<F16>(xf[st][j][0], lin_codes16<F16>(w4[j], code), c);
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) {
-            const float s = half(r.s[st], g), off = __builtin_fmaf(-16.0f, s, half(r.b[st], g));
+            const float s = half(sv[st], g), off = __builtin_fmaf(-16.0f, s, half(bv[st], g));
             const float v = kGroups == 2 ? c[2 * g] + c[2 * g + 1] : c[g];
             acc[0] = __builtin_fmaf(off, xs[kGroups * kb + g], __builtin_fmaf(s, v, acc[0]));
           }
@@ -291,7 +324,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
             lin_f32x4 c = {0, 0, 0, 0};
 #pragma unroll
             for (int j = g * kPer; j < (g + 1) * kPer; ++j) c = lin_mfma<F16>(xf[st][j][0], lin_codes16<F16>(w4[j], code), c);
-            const float s = half(r.s[st], g), off = __builtin_fmaf(-16.0f, s, half(r.b[st], g));
+            const float s = half(sv[st], g), off = __builtin_fmaf(-16.0f, s, half(bv[st], g));
             const lin_f32x4 x4 = *reinterpret_cast<const lin_f32x4*>(xs + g * 16 + 4 * kb);
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(off, x4[i], __builtin_fmaf(s, c[i], acc[i]));
