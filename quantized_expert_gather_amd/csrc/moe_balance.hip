@@ -21,7 +21,12 @@
 namespace moeq4 {
 namespace {
 
-constexpr int kWaves = 4;  // waves of a forward / backward workgroup, one row each at a time (E <= 1024)
+// Waves of a workgroup, each taking kRows rows at a time (E <= 1024): their
+// loads are all on their way before the first is used, and their reductions
+// interleave.
+constexpr int kPartialWaves = 16, kBackWaves = 8;
+template <int EPL, int WPR>
+constexpr int kRows = WPR > 1 ? 1 : EPL <= 4 ? 4 : EPL == 8 ? 2 : 1;
 
 struct BalanceArgs {
   const void* z;
@@ -39,75 +44,101 @@ struct BalanceArgs {
   float coef;
 };
 
-// p of one row in place of its logits; returns the sigmoid's row factors
-// untouched: v holds p, and `damp` (if asked for) 1 - sigmoid(z).
-template <int EPL, int WPR, bool DAMP>
-__device__ __forceinline__ void row_probabilities(float (&v)[EPL], float (&damp)[EPL], int base, int E, int score,
-                                                  float* red) {
-  float sum = 0.0f;
+// p of R rows in place of their logits, and 1 - sigmoid(z) in `damp` (DAMP).
+template <int EPL, int WPR, int R, bool DAMP>
+__device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&damp)[DAMP ? R : 1][EPL], int base, int E,
+                                                  int score, float* red) {
+  float sum[R];
   if (score == kRouterScoreSoftmax) {
-    float m = v[0];
+    float m[R];
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
-    m = row_all<WPR>(m, OpMaxF(), red);
+    for (int r = 0; r < R; ++r) {
+      m[r] = v[r][0];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      v[i] = exp_below(v[i], m);
-      sum += v[i];
-      if constexpr (DAMP) damp[i] = 1.0f;
+      for (int i = 1; i < EPL; ++i) m[r] = fmaxf(m[r], v[r][i]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) m[r] = row_all<WPR>(m[r], OpMaxF(), red);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sum[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        v[r][i] = exp_below(v[r][i], m[r]);
+        sum[r] += v[r][i];
+        if constexpr (DAMP) damp[r][i] = 1.0f;
+      }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const float z = v[i];
-      v[i] = base + i < E ? sigmoid_f32(z) : 0.0f;
-      if constexpr (DAMP) damp[i] = sigmoid_f32(-z);
-      sum += v[i];
+    for (int r = 0; r < R; ++r) {
+      sum[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const float z = v[r][i];
+        v[r][i] = base + i < E ? sigmoid_f32(z) : 0.0f;
+        if constexpr (DAMP) damp[r][i] = sigmoid_f32(-z);
+        sum[r] += v[r][i];
+      }
     }
   }
-  sum = row_all<WPR>(sum, OpSumF(), red);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) v[i] *= inv;
+  for (int r = 0; r < R; ++r) sum[r] = row_all<WPR>(sum[r], OpSumF(), red);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float inv = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[r][i] *= inv;
+  }
 }
 
 template <class LT, int EPL, int WPR>
-__global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kWaves) void k_balance_partial(BalanceArgs a) {
+__global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceArgs a) {
   typedef typename LT::mem mem;
+  constexpr int R = kRows<EPL, WPR>, kStride = WPR > 1 ? 1 : kPartialWaves;
   extern __shared__ unsigned char lds[];
-  float* red = reinterpret_cast<float*>(lds);          // [16]
+  float* red = reinterpret_cast<float*>(lds);            // [16]
   int32_t* ntok = reinterpret_cast<int32_t*>(lds) + 16;  // [1], padded to 16
   int32_t* hist = reinterpret_cast<int32_t*>(lds) + 32;  // [E]
-  float* sums = reinterpret_cast<float*>(hist + a.E);    // [kWaves][E] (WPR == 1)
-  const int tid = threadIdx.x, nthr = blockDim.x, wave = tid >> 6;
-  const int slot = WPR > 1 ? tid : (tid & 63);
-  const int base = slot * EPL;
+  float* sums = reinterpret_cast<float*>(hist + a.E);    // [kPartialWaves][E] (WPR == 1)
+  const int tid = threadIdx.x, nthr = 64 * kPartialWaves;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int base = (WPR > 1 ? tid : (tid & 63)) * EPL;
   const int t0 = blockIdx.x * a.per, t1 = min(a.T, t0 + a.per);
   const size_t seq = (size_t)blockIdx.y * a.T;
 
   for (int e = tid; e < a.E; e += nthr) hist[e] = 0;
   if (tid == 0) ntok[0] = 0;
   __syncthreads();
-  for (int t = t0 + tid; t < t1; t += nthr) {
-    if (a.mask && !a.mask[seq + t]) continue;
-    atomicAdd(ntok, 1);
-    const int32_t* ids = a.ids + (seq + t) * a.k;
-    for (int j = 0; j < a.k; ++j) {
-      const int e = ids[j];
-      if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
+  {
+    const int32_t* ids = a.ids + (seq + t0) * a.k;
+    const int n = max(t1 - t0, 0) * a.k;
+    for (int i = tid; i < n; i += nthr) {
+      const int e = ids[i];
+      if (e >= 0 && e < a.E && !(a.mask && !a.mask[seq + t0 + i / a.k])) atomicAdd(&hist[e], 1);
     }
+    int live = 0;
+    for (int t = t0 + tid; t < t1; t += nthr) live += !(a.mask && !a.mask[seq + t]);
+    for (int o = 32; o > 0; o >>= 1) live += __shfl_xor(live, o, 64);
+    if ((tid & 63) == 0 && live) atomicAdd(ntok, live);
   }
 
-  float acc[EPL], damp[EPL];
+  float acc[EPL], v[R][EPL], none[1][EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
-  for (int t = t0 + (WPR > 1 ? 0 : wave); t < t1; t += WPR > 1 ? 1 : kWaves) {
-    if (a.mask && !a.mask[seq + t]) continue;  // the same for all threads of the row
-    float v[EPL];
-    load_row<LT, EPL>(static_cast<const mem*>(a.z) + (seq + t) * a.ld, base, a.E, a.vec, -__builtin_inff(), v);
-    row_probabilities<EPL, WPR, false>(v, damp, base, a.E, a.score, red);
+  for (int t = t0 + (WPR > 1 ? 0 : wave); t < t1; t += R * kStride) {
+    bool live[R];  // the same for all threads of a row
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) acc[i] += v[i];
+    for (int r = 0; r < R; ++r) {
+      const int tr = t + r * kStride;
+      live[r] = tr < t1 && !(a.mask && !a.mask[seq + tr]);
+      load_row<LT, EPL>(static_cast<const mem*>(a.z) + (seq + min(tr, t1 - 1)) * a.ld, base, a.E, a.vec, -__builtin_inff(), v[r]);
+    }
+    row_probabilities<EPL, WPR, R, false>(v, none, base, a.E, a.score, red);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) acc[i] += live[r] ? v[r][i] : 0.0f;
   }
 
   const size_t part = ((size_t)blockIdx.y * a.blocks + blockIdx.x) * a.E;
@@ -119,7 +150,7 @@ __global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kWaves) void k_balance_pa
     for (int e = tid; e < a.E; e += nthr) {
       float s = sums[e];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) s += sums[w * a.E + e];
+      for (int w = 1; w < kPartialWaves; ++w) s += sums[w * a.E + e];
       a.psum[part + e] = s;
       a.pcount[part + e] = hist[e];
     }
@@ -133,24 +164,43 @@ __global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kWaves) void k_balance_pa
   if (tid == 0) a.ptok[(size_t)blockIdx.y * a.blocks + blockIdx.x] = ntok[0];
 }
 
-// Adds a sequence's partials: counts, token count and loss.
-__global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a) {
-  __shared__ float redf[16];
-  __shared__ int redi[16];
+// Adds a sequence's partials: counts, token count and loss.  Where there are
+// fewer experts than threads, 1024 / cols threads share an expert's partials.
+__global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a, int cols) {
+  __shared__ float redf[1024];
+  __shared__ int redi[1024];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const size_t part = (size_t)blockIdx.x * a.blocks;
+  const int slices = 1024 / cols, slice = tid / cols, col = tid & (cols - 1);
   int n = 0;
   for (int b = tid; b < a.blocks; b += 1024) n += a.ptok[part + b];
   float dot = 0.0f;
-  for (int e = tid; e < a.E; e += 1024) {
+  for (int e0 = 0; e0 < a.E; e0 += cols) {
+    const int e = e0 + col;
     float s = 0.0f;
     int c = 0;
-    for (int b = 0; b < a.blocks; ++b) {
-      s += a.psum[(part + b) * a.E + e];
-      c += a.pcount[(part + b) * a.E + e];
+    if (e < a.E) {
+#pragma unroll 8
+      for (int b = slice; b < a.blocks; b += slices) {
+        s += a.psum[(part + b) * a.E + e];
+        c += a.pcount[(part + b) * a.E + e];
+      }
     }
-    a.counts[(size_t)blockIdx.x * a.E + e] = c;
-    dot += (float)c * s;
+    if (slices > 1) {
+      redf[tid] = s;
+      redi[tid] = c;
+      __syncthreads();
+      if (slice == 0)
+        for (int q = 1; q < slices; ++q) {
+          s += redf[q * cols + col];
+          c += redi[q * cols + col];
+        }
+      __syncthreads();
+    }
+    if (slice == 0 && e < a.E) {
+      a.counts[(size_t)blockIdx.x * a.E + e] = c;
+      dot += (float)c * s;
+    }
   }
   for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
   dot = wave_all(dot, OpSumF());
@@ -184,42 +234,52 @@ struct BalanceBackArgs {
 };
 
 template <class LT, int EPL, int WPR>
-__global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kWaves) void k_balance_backward(BalanceBackArgs a) {
+__global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kBackWaves) void k_balance_backward(BalanceBackArgs a) {
   typedef typename LT::mem mem;
+  constexpr int R = kRows<EPL, WPR>, kStride = WPR > 1 ? 1 : kBackWaves;
   __shared__ float red[16];
-  const int tid = threadIdx.x, wave = tid >> 6;
-  const int slot = WPR > 1 ? tid : (tid & 63);
-  const int base = slot * EPL;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int base = (WPR > 1 ? tid : (tid & 63)) * EPL;
   const int t0 = blockIdx.x * a.per, t1 = min(a.T, t0 + a.per);
   const size_t seq = (size_t)blockIdx.y * a.T;
   const float n = (float)a.tokens[blockIdx.y];
   const float f = n > 0.0f ? a.dloss[blockIdx.y] * a.coef * ((float)a.E / ((float)a.k * n)) / n : 0.0f;
-  float w[EPL], v[EPL], damp[EPL];
+  float w[EPL], v[R][EPL], damp[R][EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) w[i] = base + i < a.E ? f * (float)a.counts[(size_t)blockIdx.y * a.E + base + i] : 0.0f;
-  for (int t = t0 + (WPR > 1 ? 0 : wave); t < t1; t += WPR > 1 ? 1 : kWaves) {
-    if (a.mask && !a.mask[seq + t]) {
+  for (int t = t0 + (WPR > 1 ? 0 : wave); t < t1; t += R * kStride) {
+    bool live[R];
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) v[i] = 0.0f;
-    } else {
-      load_row<LT, EPL>(static_cast<const mem*>(a.z) + (seq + t) * a.ld, base, a.E, a.vec, -__builtin_inff(), v);
-      row_probabilities<EPL, WPR, true>(v, damp, base, a.E, a.score, red);
-      float dot = 0.0f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) dot += w[i] * v[i];
-      dot = row_all<WPR>(dot, OpSumF(), red);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) v[i] = v[i] * damp[i] * (w[i] - dot);
+    for (int r = 0; r < R; ++r) {
+      const int tr = t + r * kStride;
+      live[r] = tr < t1 && !(a.mask && !a.mask[seq + tr]);
+      load_row<LT, EPL>(static_cast<const mem*>(a.z) + (seq + min(tr, t1 - 1)) * a.ld, base, a.E, a.vec, -__builtin_inff(), v[r]);
     }
-    store_row<LT, EPL>(static_cast<mem*>(a.dz) + (seq + t) * a.ldd, base, a.E, a.vecd, v);
+    row_probabilities<EPL, WPR, R, true>(v, damp, base, a.E, a.score, red);
+    float dot[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      dot[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) dot[r] += w[i] * v[r][i];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) dot[r] = row_all<WPR>(dot[r], OpSumF(), red);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int tr = t + r * kStride;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[r][i] = live[r] ? v[r][i] * damp[r][i] * (w[i] - dot[r]) : 0.0f;
+      if (tr < t1) store_row<LT, EPL>(static_cast<mem*>(a.dz) + (seq + tr) * a.ldd, base, a.E, a.vecd, v[r]);
+    }
   }
 }
 
 // Tokens of a workgroup: enough workgroups to fill the card, few enough that
 // the second launch has little to add.
-constexpr int kMaxBlocks = 256;
+constexpr int kMaxBlocks = 128;
 int blocks_of(int S, int T, int E) {
-  const int rows = E > 1024 ? 1 : kWaves;
+  const int rows = E > 1024 ? 1 : kPartialWaves;
   const int want = std::max(1, kMaxBlocks / std::max(1, S));
   return std::max(1, std::min(want, (T + rows - 1) / rows));
 }
@@ -309,12 +369,14 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, long long 
   a.blocks = blocks_of(S, T, E);
   a.per = (T + a.blocks - 1) / a.blocks;
   a.coef = coef;
-  const dim3 grid(a.blocks, S), block(plan.wpr > 1 ? 64 * plan.wpr : 64 * kWaves);
-  const size_t lds = 128 + (size_t)E * 4 + (plan.wpr > 1 ? 0 : (size_t)kWaves * E * 4);
+  const dim3 grid(a.blocks, S), block(64 * kPartialWaves);
+  const size_t lds = 128 + (size_t)E * 4 + (plan.wpr > 1 ? 0 : (size_t)kPartialWaves * E * 4);
 #define MOE_BALANCE_CALL(LT, EPL, WPR) hipLaunchKernelGGL((k_balance_partial<LT, EPL, WPR>), grid, block, lds, stream, a)
   MOE_ROW_DISPATCH(logits_dtype, plan, MOE_BALANCE_CALL)
   if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
-  hipLaunchKernelGGL(k_balance_finish, dim3(S), dim3(1024), 0, stream, a);
+  int cols = 1;
+  while (cols < E && cols < 1024) cols *= 2;
+  hipLaunchKernelGGL(k_balance_finish, dim3(S), dim3(1024), 0, stream, a, cols);
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }
 
@@ -340,11 +402,11 @@ extern "C" int moe_balance_loss_backward(const void* logits, int logits_dtype, l
   BalanceBackArgs a{logits, token_mask, counts, tokens, dloss, dlogits, ld, ldd, S, T, k, E, score, 0, 0, 0, coef};
   a.vec = row_vec(logits, ld, E, plan.epl, (int)es);
   a.vecd = row_vec(dlogits, ldd, E, plan.epl, (int)es);
-  const int unit = plan.wpr > 1 ? 1 : kWaves;
-  const int want = std::max(1, 2048 / S);
+  const int unit = plan.wpr > 1 ? 1 : kBackWaves;
+  const int want = std::max(1, 1024 / S);
   const int blocks = std::max(1, std::min(want, (T + unit - 1) / unit));
   a.per = (T + blocks - 1) / blocks;
-  const dim3 grid((T + a.per - 1) / a.per, S), block(plan.wpr > 1 ? 64 * plan.wpr : 64 * kWaves);
+  const dim3 grid((T + a.per - 1) / a.per, S), block(plan.wpr > 1 ? 64 * plan.wpr : 64 * kBackWaves);
 #define MOE_BALANCE_BACK_CALL(LT, EPL, WPR) \
   hipLaunchKernelGGL((k_balance_backward<LT, EPL, WPR>), grid, block, 0, stream, a)
   MOE_ROW_DISPATCH(logits_dtype, plan, MOE_BALANCE_BACK_CALL)

@@ -51,14 +51,12 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
 // What one round of the selection found.
 struct Pick {
   int key, id;
-  float z, b;
 };
 
 // The largest key among the row's threads, lowest expert first, and takes it
-// out.  With a selection bias the pick's logit and bias come along.
-template <int EPL, int WPR, bool BIAS>
-__device__ __forceinline__ Pick take_largest(int (&key)[EPL], const float (&z)[EPL], const float (&b)[EPL],
-                                             Pick* red) {
+// out.
+template <int EPL, int WPR>
+__device__ __forceinline__ Pick take_largest(int (&key)[EPL], Pick* red) {
   const int lane = threadIdx.x & 63;
   int lm = key[0];
 #pragma unroll
@@ -66,22 +64,11 @@ __device__ __forceinline__ Pick take_largest(int (&key)[EPL], const float (&z)[E
   const int m = wave_all(lm, OpMaxI());
   const int owner = __ffsll((unsigned long long)__ballot(lm == m)) - 1;
   int at = 0;
-  float zs = 0.0f, bs = 0.0f;
 #pragma unroll
-  for (int i = EPL - 1; i >= 0; --i) {
-    const bool hit = key[i] == m;
-    at = hit ? i : at;
-    if constexpr (BIAS) {
-      zs = hit ? z[i] : zs;
-      bs = hit ? b[i] : bs;
-    }
-  }
+  for (int i = EPL - 1; i >= 0; --i) at = key[i] == m ? i : at;
   Pick p;
   p.key = m;
-  p.id = lane_value((int)threadIdx.x * EPL + at, owner);
-  if constexpr (WPR == 1) p.id -= (int)(threadIdx.x - lane) * EPL;
-  p.z = BIAS ? lane_value(zs, owner) : key_value(m);
-  p.b = BIAS ? lane_value(bs, owner) : 0.0f;
+  p.id = lane_value((WPR > 1 ? (int)threadIdx.x : lane) * EPL + at, owner);
   bool mine = lane == owner;
   if constexpr (WPR > 1) {
     __syncthreads();
@@ -98,6 +85,40 @@ __device__ __forceinline__ Pick take_largest(int (&key)[EPL], const float (&z)[E
   for (int i = 0; i < EPL; ++i)
     if (mine && at == i) key[i] = kKeyTaken;
   return p;
+}
+
+// 16-bit logits without a bias: order and expert fit one word, so keys differ
+// and each thread can keep its own in falling order.  A round is a maximum
+// over the threads' first keys; its owner moves up.
+template <class LT>
+__device__ __forceinline__ int packed_key(float v, int e) {
+  const int b = (int)(int16_t)__builtin_bit_cast(uint16_t, LT::store(v + 0.0f));
+  const int o = v != v ? -32767 : b ^ ((b >> 31) & 0x7FFF);  // NaN below -inf
+  return (int)((uint32_t)o << 16) | (0xFFFF - e);
+}
+template <class LT>
+__device__ __forceinline__ float packed_value(int key) {
+  const int o = key >> 16;
+  if (o == -32767) return __builtin_nanf("");
+  return LT::load(__builtin_bit_cast(typename LT::mem, (uint16_t)(o ^ ((o >> 31) & 0x7FFF))));
+}
+template <int EPL>
+__device__ __forceinline__ void sort_falling(int (&k)[EPL]) {  // odd-even merges
+#pragma unroll
+  for (int p = 1; p < EPL; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < EPL; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i) {
+          const int x = i + j, y = i + j + q;
+          if (y < EPL && x / (2 * p) == y / (2 * p)) {
+            const int hi = k[x] > k[y] ? k[x] : k[y], lo = k[x] > k[y] ? k[y] : k[x];
+            k[x] = hi;
+            k[y] = lo;
+          }
+        }
 }
 
 // The same selection with the scores in 64 bits, for the rows whose 32-bit
@@ -215,16 +236,20 @@ __device__ __forceinline__ float chosen_weight(float z, bool live, int score, in
 
 template <class LT, int EPL, int WPR, bool BIAS>
 __global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kRowsPerBlock) void k_router_topk(TopkArgs a) {
+  constexpr bool kPacked = !BIAS && WPR == 1 && sizeof(typename LT::mem) == 2;
+  typedef typename LT::mem mem;
   __shared__ Pick red[WPR];
   __shared__ float redf[WPR];
   __shared__ double redd[WPR];
   __shared__ int redi[2 * WPR];
-  const int slot = WPR > 1 ? (int)threadIdx.x : (int)(threadIdx.x & 63);
-  const int t = WPR > 1 ? (int)blockIdx.x : (int)blockIdx.x * kRowsPerBlock + (int)(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int slot = WPR > 1 ? (int)threadIdx.x : lane;
+  const int t = __builtin_amdgcn_readfirstlane(WPR > 1 ? (int)blockIdx.x : (int)blockIdx.x * kRowsPerBlock + (int)(threadIdx.x >> 6));
   if (t >= a.T) return;  // whole rows only
   const int base = slot * EPL;
-  float z[EPL], b[EPL];
-  load_row<LT, EPL>(static_cast<const typename LT::mem*>(a.z) + (size_t)t * a.ld, base, a.E, a.vec, -__builtin_inff(), z);
+  const mem* row = static_cast<const mem*>(a.z) + (size_t)t * a.ld;
+  float z[EPL];
+  load_row<LT, EPL>(row, base, a.E, a.vec, -__builtin_inff(), z);
 
   // softmax statistics, where the whole row counts
   float row_max = 0.0f, row_sum = 1.0f;
@@ -243,41 +268,79 @@ __global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kRowsPerBlock) void k_rou
     row_sum = row_all<WPR>(row_sum, OpSumF(), redf);
   }
 
-  int key[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    float v = z[i];
-    b[i] = 0.0f;
-    if constexpr (BIAS) {
-      b[i] = base + i < a.E ? a.bias[base + i] : 0.0f;
-      v = (a.score == kRouterScoreSoftmax ? (row_sum == 0.0f ? 0.0f : e[i] / row_sum) : sigmoid_f32(z[i])) + b[i];
-    }
-    key[i] = base + i < a.E ? order_key(v) : kKeyTaken;
-  }
-
   int my_id = 0;
   float my_z = 0.0f;
-  bool close = false;
-  Pick prev{};
-  const int rounds = BIAS && a.k < a.E ? a.k + 1 : a.k;
-  for (int j = 0; j < rounds; ++j) {
-    const Pick p = take_largest<EPL, WPR, BIAS>(key, z, b, red);
-    if (slot == j && j < a.k) {
-      my_id = p.id;
-      my_z = p.z;
+  int key[EPL];
+  if constexpr (kPacked) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = base + i < a.E ? packed_key<LT>(z[i], base + i) : kKeyTaken;
+    sort_falling<EPL>(key);
+    int mine = 0;
+    for (int j = 0; j < a.k; ++j) {
+      const int m = wave_all(key[0], OpMaxI());
+      if (lane == j) mine = m;
+      const bool own = key[0] == m;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) key[i] = own ? (i + 1 < EPL ? key[i + 1] : kKeyTaken) : key[i];
+    }
+    my_id = 0xFFFF - (mine & 0xFFFF);
+    my_z = packed_value<LT>(mine);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      float v = z[i];
+      if constexpr (BIAS) {
+        const float b = base + i < a.E ? a.bias[base + i] : 0.0f;
+        v = (a.score == kRouterScoreSoftmax ? (row_sum == 0.0f ? 0.0f : e[i] / row_sum) : sigmoid_f32(z[i])) + b;
+      }
+      key[i] = base + i < a.E ? order_key(v) : kKeyTaken;
+    }
+    int my_key = 0, last_key = 0, last_id = 0;
+    const int rounds = BIAS && a.k < a.E ? a.k + 1 : a.k;
+    for (int j = 0; j < rounds; ++j) {
+      const Pick p = take_largest<EPL, WPR>(key, red);
+      if (slot == j) {
+        my_id = p.id;
+        my_key = p.key;
+      }
+      last_key = p.key;
+      last_id = p.id;
     }
     if constexpr (BIAS) {
-      // Two scores of different logits or biases that fp32 cannot tell apart:
-      // a score is off by at most about 2e-6 p + 2^-24 |score| (the exponential's
-      // argument and value, the division, the sum with the bias), p <= 1.
-      const float s1 = key_value(prev.key), s0 = key_value(p.key);
-      const bool same = p.z == prev.z && p.b == prev.b;
-      if (j > 0 && !same && !(s1 - s0 > 8e-6f + 5e-7f * fabsf(s1))) close = true;
-      prev = p;
+      // Two neighbours in the order of different logits or biases that fp32
+      // cannot tell apart: a score is off by at most about 5e-6 p + 2^-24
+      // |score| (the exponential, its sum, the quotient, the sum with the
+      // bias), p <= 1.  The first wave holds the picks.
+      bool close = false;
+      if (WPR == 1 || threadIdx.x < 64) {
+        const bool last = lane == rounds - 1 || lane == 63;
+        const int id2 = lane == 63 ? last_id : __shfl_down(my_id, 1, 64);
+        const int key2 = lane == 63 ? last_key : __shfl_down(my_key, 1, 64);
+        const bool pair = lane < rounds - 1 && (!last || (lane == 63 && rounds == 65));
+        if (lane < a.k) my_z = LT::load(row[my_id]);
+        if (pair) {
+          const float s1 = key_value(my_key), s0 = key_value(key2);
+          if (!(s1 - s0 > 8e-6f + 5e-7f * fabsf(s1)))
+            close = !(LT::load(row[id2]) == my_z && a.bias[id2] == a.bias[my_id]);
+        }
+        close = __any(close);
+      }
+      if constexpr (WPR > 1) {
+        __syncthreads();
+        if (threadIdx.x == 0) redi[0] = close;
+        __syncthreads();
+        close = redi[0];
+        __syncthreads();
+      }
+      if (close) {
+        float b[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) b[i] = base + i < a.E ? a.bias[base + i] : 0.0f;
+        select_in_64<EPL, WPR>(z, b, base, a.E, a.k, a.score, redd, redi, my_id, my_z);
+      }
+    } else {
+      my_z = key_value(my_key);
     }
-  }
-  if constexpr (BIAS) {
-    if (close) select_in_64<EPL, WPR>(z, b, base, a.E, a.k, a.score, redd, redi, my_id, my_z);
   }
 
   if (WPR > 1 && threadIdx.x >= 64) return;  // k <= 64: the picks lie in the first wave
@@ -300,15 +363,17 @@ struct TopkBackArgs {
 };
 
 // dz of one row per wave (16 waves above 1024 experts): the first wave's
-// lanes j < k form their pick's term, every thread adds the terms that fall
-// on its values, in ascending j.
+// lanes j < k form their pick's term; the terms reach the threads that hold
+// their experts through an LDS row, in ascending j where an expert repeats.
 template <class LT, int EPL, int WPR>
 __global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kRowsPerBlock) void k_router_topk_backward(TopkBackArgs a) {
   typedef typename LT::mem mem;
   __shared__ float redf[WPR];
+  __shared__ __attribute__((aligned(16))) float rows[WPR > 1 ? 1 : kRowsPerBlock][WPR > 1 ? 4 : 64 * EPL];
   const int lane = threadIdx.x & 63;
   const int slot = WPR > 1 ? (int)threadIdx.x : lane;
-  const int t = WPR > 1 ? (int)blockIdx.x : (int)blockIdx.x * kRowsPerBlock + (int)(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int t = WPR > 1 ? (int)blockIdx.x : (int)blockIdx.x * kRowsPerBlock + wave;
   if (t >= a.T) return;
   const int base = slot * EPL;
   const mem* row = static_cast<const mem*>(a.z) + (size_t)t * a.ld;
@@ -324,15 +389,14 @@ __global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kRowsPerBlock) void k_rou
   const bool live = id >= 0;
   float out[EPL], term;
   if (a.score == kRouterScoreSoftmax && !a.norm) {
-    float v[EPL];
-    load_row<LT, EPL>(row, base, a.E, a.vec, -__builtin_inff(), v);
-    float m = v[0], sum = 0.0f;
+    load_row<LT, EPL>(row, base, a.E, a.vec, -__builtin_inff(), out);
+    float m = out[0], sum = 0.0f;
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
+    for (int i = 1; i < EPL; ++i) m = fmaxf(m, out[i]);
     m = row_all<WPR>(m, OpMaxF(), redf);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      out[i] = exp_below(v[i], m);
+      out[i] = exp_below(out[i], m);
       sum += out[i];
     }
     sum = row_all<WPR>(sum, OpSumF(), redf);
@@ -359,11 +423,31 @@ __global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kRowsPerBlock) void k_rou
     }
     term = live ? a.scale * p * g * damp : 0.0f;
   }
-  for (int j = 0; j < a.k; ++j) {
-    const int at = __builtin_amdgcn_readlane(id, j) - base;
-    const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(term), j));
+  bool repeats = true;
+  if constexpr (WPR == 1) {
+    float* mine = rows[wave];
+    // does an expert repeat?  each pick leaves its lane and looks whether it stayed
+    if (live) mine[id] = __int_as_float(lane);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    repeats = __any(live && __float_as_int(mine[live ? id : 0]) != lane);
+    if (!repeats) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) out[i] += at == i ? v : 0.0f;
+      for (int i = 0; i < EPL; ++i) mine[base + i] = 0.0f;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (live) mine[id] = term;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) out[i] += mine[base + i];
+    }
+  }
+  if (repeats) {
+    for (int j = 0; j < a.k; ++j) {
+      const int at = __builtin_amdgcn_readlane(id, j) - base;
+      const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(term), j));
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) out[i] += at == i ? v : 0.0f;
+    }
   }
   store_row<LT, EPL>(static_cast<mem*>(a.dz) + (size_t)t * a.ldd, base, a.E, a.vecd, out);
 }

@@ -40,7 +40,7 @@ struct OpMaxI { __device__ __forceinline__ int operator()(int a, int b) const { 
 
 template <int CTRL, class V>
 __device__ __forceinline__ V dpp_move(V v) {
-  return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+  return __builtin_bit_cast(V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
 
 // op over the 64 lanes of a wave; every lane receives it.  Inside 16-lane
@@ -136,13 +136,26 @@ __device__ __forceinline__ void store_row(typename LT::mem* __restrict__ row, in
   }
 }
 
+// 1 / v by the hardware's reciprocal (one step off at most) and one Newton
+// step, for v >= 1 (infinity included).
+__device__ __forceinline__ float recip_f32(float v) {
+  const float r = __builtin_amdgcn_rcpf(v);
+  const float e = __builtin_fmaf(-v, r, 1.0f);
+  return v == __builtin_inff() ? r : __builtin_fmaf(e, r, r);
+}
+
+// exp(d) as 2^(d log2 e): the product is off by 2^-24 of itself and so, with
+// the constant's own rounding, exp(d) by 2^-24 (1.5 |d|) and the two steps
+// of v_exp_f32.  d = -inf gives 0.
+__device__ __forceinline__ float exp_f32(float d) { return __builtin_amdgcn_exp2f(d * 1.44269504f); }
+
 // sigmoid(z) and 1 - sigmoid(z) = sigmoid(-z), each without cancellation.
-__device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + expf(-z)); }
+__device__ __forceinline__ float sigmoid_f32(float z) { return recip_f32(1.0f + exp_f32(-z)); }
 
 // exp(z - m) with exp of a masked value (-inf) 0 also where the whole row is
 // masked (m = -inf), whose softmax is taken as zero.
 __device__ __forceinline__ float exp_below(float z, float m) {
-  return m == -__builtin_inff() ? 0.0f : expf(z - m);
+  return m == -__builtin_inff() ? 0.0f : exp_f32(z - m);
 }
 
 // Host side: values per thread and waves per row for E experts, and whether

@@ -1,11 +1,12 @@
 """The router's selection and the balance loss on the GPU against 64-bit
 references (needs an MI355X).
 
-Bounds.  An exponential of a difference d of fp32 numbers is off by at most
-2^-24 |d| (the difference's rounding) and two steps of its own; sums over a
-row take at most 64 / 64 + 4 + 6 + 16 roundings on a path (a thread's values, the
-lanes, the waves) and quotients two more.  With 2 D for a quotient's two
-exponentials a probability is off by at most 2^-24 (2 D + 80) of itself, D the
+Bounds.  An exponential of a difference d of fp32 numbers is 2^(d log2 e): off by
+at most 2^-24 |d| for the difference's rounding, as much for the product's and
+half of it for the constant's, and two steps of its own; sums over a
+row take at most 16 + 6 + 16 roundings on a path (a thread's values, the
+lanes, the waves) and quotients two more.  With 5 D for a quotient's two
+exponentials a probability is off by at most 2^-24 (5 D + 80) of itself, D the
 largest difference; a gradient multiplies three such numbers at most."""
 
 import numpy as np
@@ -26,7 +27,7 @@ def logits(T, E, dtype, seed=0, spread=2.0):
 
 def rel(z):
     f = z[np.isfinite(z)]
-    return 2.0 ** -24 * (2 * (f.max() - f.min() if f.size else 0) + 80)
+    return 2.0 ** -24 * (5 * (f.max() - f.min() if f.size else 0) + 80)
 
 
 def check_topk(z, k, bias, score, norm, scale=1.5):
