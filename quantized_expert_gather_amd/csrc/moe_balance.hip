@@ -21,12 +21,12 @@
 namespace moeq4 {
 namespace {
 
-// Waves of a workgroup, each taking kRows rows at a time (E <= 1024): their
+// Waves of a workgroup, each thread group taking kRows rows at a time: their
 // loads are all on their way before the first is used, and their reductions
 // interleave.
-constexpr int kPartialWaves = 16, kBackWaves = 8;
-template <int EPL, int WPR>
-constexpr int kRows = WPR > 1 ? 1 : EPL <= 4 ? 4 : EPL == 8 ? 2 : 1;
+constexpr int kPartialWaves = 16, kBackWaves = 4;
+template <int EPL, int LPR>
+constexpr int kRows = LPR > 64 ? 1 : EPL == 4 ? 4 : EPL == 8 ? 2 : 1;
 
 struct BalanceArgs {
   const void* z;
@@ -44,9 +44,10 @@ struct BalanceArgs {
   float coef;
 };
 
-// p of R rows in place of their logits, and 1 - sigmoid(z) in `damp` (DAMP).
-template <int EPL, int WPR, int R, bool DAMP>
-__device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&damp)[DAMP ? R : 1][EPL], int base, int E,
+// p of R rows in place of their logits, and 1 - sigmoid(z) in `damp` (DAMP,
+// sigmoid scores only).
+template <class LT, int EPL, int LPR, int R, bool DAMP>
+__device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&damp)[DAMP ? R : 1][EPL], int slot, int E,
                                                   int score, float* red) {
   float sum[R];
   if (score == kRouterScoreSoftmax) {
@@ -58,15 +59,14 @@ __device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&da
       for (int i = 1; i < EPL; ++i) m[r] = fmaxf(m[r], v[r][i]);
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) m[r] = row_all<WPR>(m[r], OpMaxF(), red);
+    for (int r = 0; r < R; ++r) m[r] = exp_base(row_all<LPR>(m[r], OpMaxF(), red));
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       sum[r] = 0.0f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        v[r][i] = exp_below(v[r][i], m[r]);
+        v[r][i] = exp_f32(v[r][i] - m[r]);
         sum[r] += v[r][i];
-        if constexpr (DAMP) damp[r][i] = 1.0f;
       }
     }
   } else {
@@ -74,16 +74,17 @@ __device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&da
     for (int r = 0; r < R; ++r) {
       sum[r] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const float z = v[r][i];
-        v[r][i] = base + i < E ? sigmoid_f32(z) : 0.0f;
-        if constexpr (DAMP) damp[r][i] = sigmoid_f32(-z);
+      for (int i = 0; i < EPL; ++i) {  // past E the logits are -inf, their sigmoid 0
+        if constexpr (DAMP)
+          v[r][i] = sigmoid_pair(v[r][i], damp[r][i]);
+        else
+          v[r][i] = sigmoid_f32(v[r][i]);
         sum[r] += v[r][i];
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r) sum[r] = row_all<WPR>(sum[r], OpSumF(), red);
+  for (int r = 0; r < R; ++r) sum[r] = row_all<LPR>(sum[r], OpSumF(), red);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const float inv = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];
@@ -92,21 +93,29 @@ __device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&da
   }
 }
 
-template <class LT, int EPL, int WPR>
+template <class LT, int EPL, int LPR>
 __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceArgs a) {
   typedef typename LT::mem mem;
-  constexpr int R = kRows<EPL, WPR>, kStride = WPR > 1 ? 1 : kPartialWaves;
+  constexpr int R = kRows<EPL, LPR>, kGroups = 64 * kPartialWaves / LPR;  // rows at a time
   extern __shared__ unsigned char lds[];
   float* red = reinterpret_cast<float*>(lds);            // [16]
   int32_t* ntok = reinterpret_cast<int32_t*>(lds) + 16;  // [1], padded to 16
   int32_t* hist = reinterpret_cast<int32_t*>(lds) + 32;  // [E]
-  float* sums = reinterpret_cast<float*>(hist + a.E);    // [kPartialWaves][E] (WPR == 1)
+  float* sums = reinterpret_cast<float*>(hist + a.E);    // [kPartialWaves][E] (LPR <= 64)
   const int tid = threadIdx.x, nthr = 64 * kPartialWaves;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int base = (WPR > 1 ? tid : (tid & 63)) * EPL;
+  const int wave = tid >> 6, group = tid / LPR, slot = tid % LPR;
   const int t0 = blockIdx.x * a.per, t1 = min(a.T, t0 + a.per);
   const size_t seq = (size_t)blockIdx.y * a.T;
 
+  // the rows after the ones at hand are on their way
+  float acc[EPL], v[R][EPL], next[R][EPL], none[1][EPL];
+  auto load = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      load_row<LT, EPL, LPR>(static_cast<const mem*>(a.z) + (seq + min(t + r * kGroups + group, t1 - 1)) * a.ld, slot, a.E, a.vec,
+                             -__builtin_inff(), next[r]);
+  };
+  if (t0 < t1) load(t0);
   for (int e = tid; e < a.E; e += nthr) hist[e] = 0;
   if (tid == 0) ntok[0] = 0;
   __syncthreads();
@@ -123,18 +132,20 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
     if ((tid & 63) == 0 && live) atomicAdd(ntok, live);
   }
 
-  float acc[EPL], v[R][EPL], none[1][EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
-  for (int t = t0 + (WPR > 1 ? 0 : wave); t < t1; t += R * kStride) {
-    bool live[R];  // the same for all threads of a row
+  // whole waves go round as long as one of their rows is left
+  for (int t = t0; t < t1; t += R * kGroups) {
+    bool live[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int tr = t + r * kStride;
+      const int tr = t + r * kGroups + group;
       live[r] = tr < t1 && !(a.mask && !a.mask[seq + tr]);
-      load_row<LT, EPL>(static_cast<const mem*>(a.z) + (seq + min(tr, t1 - 1)) * a.ld, base, a.E, a.vec, -__builtin_inff(), v[r]);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[r][i] = next[r][i];
     }
-    row_probabilities<EPL, WPR, R, false>(v, none, base, a.E, a.score, red);
+    if (t + R * kGroups < t1) load(t + R * kGroups);
+    row_probabilities<LT, EPL, LPR, R, false>(v, none, slot, a.E, a.score, red);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -142,10 +153,28 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
   }
 
   const size_t part = ((size_t)blockIdx.y * a.blocks + blockIdx.x) * a.E;
-  if constexpr (WPR == 1) {
+  if constexpr (LPR <= 64) {
+    // a wave's rows, then the waves', in a fixed order
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (base + i < a.E) sums[wave * a.E + base + i] = acc[i];
+    for (int i = 0; i < EPL; ++i) {
+      if constexpr (LPR <= 16) {
+        const uint32_t u = __float_as_uint(acc[i]);
+        const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        acc[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+      }
+      if constexpr (LPR <= 32) {
+        const uint32_t u = __float_as_uint(acc[i]);
+        const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        acc[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+      }
+    }
+    if ((tid & 63) < LPR) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = row_expert<LT, EPL, LPR>(slot, i);
+        if (e < a.E) sums[wave * a.E + e] = acc[i];
+      }
+    }
     __syncthreads();
     for (int e = tid; e < a.E; e += nthr) {
       float s = sums[e];
@@ -157,8 +186,10 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
   } else {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (base + i < a.E) a.psum[part + base + i] = acc[i];
+    for (int i = 0; i < EPL; ++i) {
+      const int e = row_expert<LT, EPL, LPR>(slot, i);
+      if (e < a.E) a.psum[part + e] = acc[i];
+    }
     for (int e = tid; e < a.E; e += nthr) a.pcount[part + e] = hist[e];
   }
   if (tid == 0) a.ptok[(size_t)blockIdx.y * a.blocks + blockIdx.x] = ntok[0];
@@ -203,7 +234,7 @@ __global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a, int cols
     }
   }
   for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
-  dot = wave_all(dot, OpSumF());
+  dot = row_all<64>(dot, OpSumF());
   if (lane == 0) {
     redf[wave] = dot;
     redi[wave] = n;
@@ -233,29 +264,37 @@ struct BalanceBackArgs {
   float coef;
 };
 
-template <class LT, int EPL, int WPR>
-__global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kBackWaves) void k_balance_backward(BalanceBackArgs a) {
+template <class LT, int EPL, int LPR>
+__global__ __launch_bounds__(LPR > 64 ? LPR : 64 * kBackWaves) void k_balance_backward(BalanceBackArgs a) {
   typedef typename LT::mem mem;
-  constexpr int R = kRows<EPL, WPR>, kStride = WPR > 1 ? 1 : kBackWaves;
+  constexpr int R = kRows<EPL, LPR>, kGroups = (LPR > 64 ? LPR : 64 * kBackWaves) / LPR;
   __shared__ float red[16];
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int base = (WPR > 1 ? tid : (tid & 63)) * EPL;
+  const int tid = threadIdx.x, group = tid / LPR, slot = tid % LPR;
   const int t0 = blockIdx.x * a.per, t1 = min(a.T, t0 + a.per);
   const size_t seq = (size_t)blockIdx.y * a.T;
+  float v[R][EPL], next[R][EPL], damp[R][EPL];
+  auto load = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      load_row<LT, EPL, LPR>(static_cast<const mem*>(a.z) + (seq + min(t + r * kGroups + group, t1 - 1)) * a.ld, slot, a.E, a.vec,
+                             -__builtin_inff(), next[r]);
+  };
+  load(t0);
   const float n = (float)a.tokens[blockIdx.y];
   const float f = n > 0.0f ? a.dloss[blockIdx.y] * a.coef * ((float)a.E / ((float)a.k * n)) / n : 0.0f;
-  float w[EPL], v[R][EPL], damp[R][EPL];
+  float w[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) w[i] = base + i < a.E ? f * (float)a.counts[(size_t)blockIdx.y * a.E + base + i] : 0.0f;
-  for (int t = t0 + (WPR > 1 ? 0 : wave); t < t1; t += R * kStride) {
-    bool live[R];
+  for (int i = 0; i < EPL; ++i) {
+    const int e = row_expert<LT, EPL, LPR>(slot, i);
+    w[i] = e < a.E ? f * (float)a.counts[(size_t)blockIdx.y * a.E + e] : 0.0f;
+  }
+  for (int t = t0; t < t1; t += R * kGroups) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int tr = t + r * kStride;
-      live[r] = tr < t1 && !(a.mask && !a.mask[seq + tr]);
-      load_row<LT, EPL>(static_cast<const mem*>(a.z) + (seq + min(tr, t1 - 1)) * a.ld, base, a.E, a.vec, -__builtin_inff(), v[r]);
-    }
-    row_probabilities<EPL, WPR, R, true>(v, damp, base, a.E, a.score, red);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[r][i] = next[r][i];
+    if (t + R * kGroups < t1) load(t + R * kGroups);
+    row_probabilities<LT, EPL, LPR, R, true>(v, damp, slot, a.E, a.score, red);
     float dot[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -264,13 +303,21 @@ __global__ __launch_bounds__(WPR > 1 ? 64 * WPR : 64 * kBackWaves) void k_balanc
       for (int i = 0; i < EPL; ++i) dot[r] += w[i] * v[r][i];
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) dot[r] = row_all<WPR>(dot[r], OpSumF(), red);
+    for (int r = 0; r < R; ++r) dot[r] = row_all<LPR>(dot[r], OpSumF(), red);
+    if (a.score != kRouterScoreSoftmax) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) v[r][i] *= damp[r][i];
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int tr = t + r * kStride;
+      const int tr = t + r * kGroups + group;
+      if (tr >= t1) continue;
+      const bool live = !(a.mask && !a.mask[seq + tr]);
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) v[r][i] = live[r] ? v[r][i] * damp[r][i] * (w[i] - dot[r]) : 0.0f;
-      if (tr < t1) store_row<LT, EPL>(static_cast<mem*>(a.dz) + (seq + tr) * a.ldd, base, a.E, a.vecd, v[r]);
+      for (int i = 0; i < EPL; ++i) v[r][i] = live ? v[r][i] * (w[i] - dot[r]) : 0.0f;
+      store_row<LT, EPL, LPR>(static_cast<mem*>(a.dz) + (seq + tr) * a.ldd, slot, a.E, a.vecd, v[r]);
     }
   }
 }
@@ -350,7 +397,7 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, long long 
   for (int i = 0; i < 3; ++i)
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return MOE_Q4_ERR_ALIAS;
-  const RowPlan plan = row_plan(E);
+  const RowPlan plan = row_plan(E, 1, false);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   BalanceArgs a{};
   a.z = logits;
@@ -370,8 +417,8 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, long long 
   a.per = (T + a.blocks - 1) / a.blocks;
   a.coef = coef;
   const dim3 grid(a.blocks, S), block(64 * kPartialWaves);
-  const size_t lds = 128 + (size_t)E * 4 + (plan.wpr > 1 ? 0 : (size_t)kPartialWaves * E * 4);
-#define MOE_BALANCE_CALL(LT, EPL, WPR) hipLaunchKernelGGL((k_balance_partial<LT, EPL, WPR>), grid, block, lds, stream, a)
+  const size_t lds = 128 + (size_t)E * 4 + (plan.lpr > 64 ? 0 : (size_t)kPartialWaves * E * 4);
+#define MOE_BALANCE_CALL(LT, EPL, LPR) hipLaunchKernelGGL((k_balance_partial<LT, EPL, LPR>), grid, block, lds, stream, a)
   MOE_ROW_DISPATCH(logits_dtype, plan, MOE_BALANCE_CALL)
   if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
   int cols = 1;
@@ -398,17 +445,19 @@ extern "C" int moe_balance_loss_backward(const void* logits, int logits_dtype, l
       overlap(dlogits, out, counts, (size_t)S * E * 4) || overlap(dlogits, out, tokens, (size_t)S * 4) ||
       overlap(dlogits, out, dloss, (size_t)S * 4))
     return MOE_Q4_ERR_ALIAS;
-  const RowPlan plan = row_plan(E);
+  const RowPlan plan = row_plan(E, 1, false);
   BalanceBackArgs a{logits, token_mask, counts, tokens, dloss, dlogits, ld, ldd, S, T, k, E, score, 0, 0, 0, coef};
   a.vec = row_vec(logits, ld, E, plan.epl, (int)es);
   a.vecd = row_vec(dlogits, ldd, E, plan.epl, (int)es);
-  const int unit = plan.wpr > 1 ? 1 : kBackWaves;
+  // a workgroup's rows at a time, and few enough workgroups that each goes round a few times
+  const int threads = plan.lpr > 64 ? plan.lpr : 64 * kBackWaves;
+  const int unit = threads / plan.lpr * (plan.lpr > 64 ? 1 : plan.epl == 4 ? 4 : plan.epl == 8 ? 2 : 1);
   const int want = std::max(1, 1024 / S);
-  const int blocks = std::max(1, std::min(want, (T + unit - 1) / unit));
-  a.per = (T + blocks - 1) / blocks;
-  const dim3 grid((T + a.per - 1) / a.per, S), block(plan.wpr > 1 ? 64 * plan.wpr : 64 * kBackWaves);
-#define MOE_BALANCE_BACK_CALL(LT, EPL, WPR) \
-  hipLaunchKernelGGL((k_balance_backward<LT, EPL, WPR>), grid, block, 0, stream, a)
+  a.per = std::max((T + want - 1) / want, unit);
+  a.per = (a.per + unit - 1) / unit * unit;
+  const dim3 grid((T + a.per - 1) / a.per, S), block(threads);
+#define MOE_BALANCE_BACK_CALL(LT, EPL, LPR) \
+  hipLaunchKernelGGL((k_balance_backward<LT, EPL, LPR>), grid, block, 0, stream, a)
   MOE_ROW_DISPATCH(logits_dtype, plan, MOE_BALANCE_BACK_CALL)
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }

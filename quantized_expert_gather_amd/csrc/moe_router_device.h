@@ -1,10 +1,12 @@
-// Device helpers of the router's selection and of the balance loss: one row
-// of E router values lies in the registers of one wave, or of one 16-wave
-// workgroup where E is large.  Internal header.
+// Device helpers of the router's selection and of the balance loss.  Internal
+// header.
 //
-// Layout: thread i of the row's threads holds the EPL consecutive values
-// i * EPL .. i * EPL + EPL - 1, so a lower thread always holds lower experts
-// and ties go to the lowest set bit of a ballot.
+// LPR threads hold one row of E router values in their registers: 16, 32 or
+// 64 lanes of a wave (so a wave works on four, two or one rows at a time, and
+// a reduction's steps serve all of them), or a workgroup of 1024 threads where
+// E is large.  Thread i of a row holds EPL values, in chunks of V neighbours:
+// value j is expert (j / V) * LPR * V + i * V + j % V, so that a load takes
+// neighbouring bytes in neighbouring threads, and j rises with the expert.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -21,7 +23,8 @@ constexpr int kRouterScoreSigmoid = 1;
 struct LogitBf16 {
   typedef uint16_t mem;
   static __device__ __forceinline__ float load(mem v) { return bf16_to_f32(v); }
-  static __device__ __forceinline__ mem store(float v) { return (mem)f32_to_bf16_rne(v); }
+  // gfx950 converts in hardware: to nearest even, NaN stays NaN
+  static __device__ __forceinline__ mem store(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 };
 struct LogitF32 {
   typedef float mem;
@@ -36,6 +39,7 @@ struct LogitF16 {
 
 struct OpMaxF { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
 struct OpSumF { __device__ __forceinline__ float operator()(float a, float b) const { return a + b; } };
+struct OpMinI { __device__ __forceinline__ int operator()(int a, int b) const { return a < b ? a : b; } };
 struct OpMaxI { __device__ __forceinline__ int operator()(int a, int b) const { return a > b ? a : b; } };
 
 template <int CTRL, class V>
@@ -43,96 +47,105 @@ __device__ __forceinline__ V dpp_move(V v) {
   return __builtin_bit_cast(V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
 
-// op over the 64 lanes of a wave; every lane receives it.  Inside 16-lane
-// rows the steps are DPP lane permutes, across rows gfx950's row swaps, so
-// nothing goes through the LDS pipe.  The tree is fixed: sums are the same
-// from run to run.
-template <class OP, class V>
-__device__ __forceinline__ V wave_all(V v, OP op) {
+// op over the LPR threads of each row; every thread receives its row's.
+// Inside 16-lane rows the steps are DPP lane permutes, across them gfx950's
+// row swaps, so nothing goes through the LDS pipe (but for LPR = 1024, whose
+// waves meet in `red`, 16 words; all threads must call it then).  The tree is
+// fixed: sums are the same from run to run.
+template <int LPR, class OP, class V>
+__device__ __forceinline__ V row_all(V v, OP op, V* red = nullptr) {
   v = op(v, dpp_move<0xB1>(v));   // lane ^ 1
   v = op(v, dpp_move<0x4E>(v));   // lane ^ 2
   v = op(v, dpp_move<0x141>(v));  // half-row mirror
   v = op(v, dpp_move<0x140>(v));  // row mirror
-  const uint32_t a = __builtin_bit_cast(uint32_t, v);
-  const auto s16 = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-  v = op(__builtin_bit_cast(V, (uint32_t)s16[0]), __builtin_bit_cast(V, (uint32_t)s16[1]));
-  const uint32_t b = __builtin_bit_cast(uint32_t, v);
-  const auto s32 = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return op(__builtin_bit_cast(V, (uint32_t)s32[0]), __builtin_bit_cast(V, (uint32_t)s32[1]));
-}
-
-// op over all threads of a row: WPR waves, through `red` (LDS, 16 words)
-// where WPR > 1.  Every thread of the workgroup must call it then.
-template <int WPR, class OP, class V>
-__device__ __forceinline__ V row_all(V v, OP op, V* red) {
-  v = wave_all(v, op);
-  if constexpr (WPR > 1) {
+  if constexpr (LPR >= 32) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    const auto s = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    const uint32_t s0 = s[0], s1 = s[1];
+    v = op(__builtin_bit_cast(V, s0), __builtin_bit_cast(V, s1));
+  }
+  if constexpr (LPR >= 64) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    const auto s = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    const uint32_t s0 = s[0], s1 = s[1];
+    v = op(__builtin_bit_cast(V, s0), __builtin_bit_cast(V, s1));
+  }
+  if constexpr (LPR > 64) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
     v = red[0];
 #pragma unroll
-    for (int w = 1; w < WPR; ++w) v = op(v, red[w]);
+    for (int w = 1; w < LPR / 64; ++w) v = op(v, red[w]);
   }
   return v;
 }
 
-template <int N>
-struct alignas(N) Bytes {
-  unsigned char b[N];
-};
-
-// Values base .. base + EPL - 1 of a row as fp32, `fill` past E.  `vec`: the
-// row starts on a boundary of the widest load below and E is a multiple of
-// EPL, so a thread's values are all inside the row or all outside.
+// Neighbouring values of a thread: a 16-byte load's, or all of them.
 template <class LT, int EPL>
-__device__ __forceinline__ void load_row(const typename LT::mem* __restrict__ row, int base, int E, bool vec,
-                                         float fill, float (&v)[EPL]) {
+constexpr int row_chunk() {
+  return EPL < 16 / (int)sizeof(typename LT::mem) ? EPL : 16 / (int)sizeof(typename LT::mem);
+}
+// Expert of value j of thread `slot`.
+template <class LT, int EPL, int LPR>
+__device__ __forceinline__ int row_expert(int slot, int j) {
+  constexpr int V = row_chunk<LT, EPL>();
+  return (j / V) * (LPR * V) + slot * V + j % V;
+}
+
+// A thread's values of a row as fp32, `fill` past E.  `vec`: rows start on
+// chunk boundaries and E is a multiple of the chunk.
+template <class LT, int EPL, int LPR>
+__device__ __forceinline__ void load_row(const typename LT::mem* __restrict__ row, int slot, int E, bool vec, float fill,
+                                         float (&v)[EPL]) {
   typedef typename LT::mem mem;
-  constexpr int kBytes = EPL * (int)sizeof(mem);
-  constexpr int kLoad = kBytes < 16 ? kBytes : 16;
-  constexpr int kPer = kLoad / (int)sizeof(mem);
+  constexpr int V = row_chunk<LT, EPL>();
   if (vec) {
-    if (base < E) {
+    typedef mem vt __attribute__((ext_vector_type(V)));
 #pragma unroll
-      for (int c = 0; c < EPL / kPer; ++c) {
-        typedef mem vt __attribute__((ext_vector_type(kPer)));
-        const vt x = *reinterpret_cast<const vt*>(row + base + c * kPer);
+    for (int c = 0; c < EPL / V; ++c) {
+      const int e = row_expert<LT, EPL, LPR>(slot, c * V);
+      if (e < E) {
+        const vt x = *reinterpret_cast<const vt*>(row + e);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) v[c * kPer + j] = LT::load(x[j]);
+        for (int j = 0; j < V; ++j) v[c * V + j] = LT::load(x[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[c * V + j] = fill;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) v[i] = fill;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) v[i] = base + i < E ? LT::load(row[base + i]) : fill;
+    for (int j = 0; j < EPL; ++j) {
+      const int e = row_expert<LT, EPL, LPR>(slot, j);
+      v[j] = e < E ? LT::load(row[e]) : fill;
+    }
   }
 }
 
-template <class LT, int EPL>
-__device__ __forceinline__ void store_row(typename LT::mem* __restrict__ row, int base, int E, bool vec,
+template <class LT, int EPL, int LPR>
+__device__ __forceinline__ void store_row(typename LT::mem* __restrict__ row, int slot, int E, bool vec,
                                           const float (&v)[EPL]) {
   typedef typename LT::mem mem;
-  constexpr int kBytes = EPL * (int)sizeof(mem);
-  constexpr int kStore = kBytes < 16 ? kBytes : 16;
-  constexpr int kPer = kStore / (int)sizeof(mem);
+  constexpr int V = row_chunk<LT, EPL>();
   if (vec) {
-    if (base < E) {
+    typedef mem vt __attribute__((ext_vector_type(V)));
 #pragma unroll
-      for (int c = 0; c < EPL / kPer; ++c) {
-        typedef mem vt __attribute__((ext_vector_type(kPer)));
+    for (int c = 0; c < EPL / V; ++c) {
+      const int e = row_expert<LT, EPL, LPR>(slot, c * V);
+      if (e < E) {
         vt x;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) x[j] = LT::store(v[c * kPer + j]);
-        *reinterpret_cast<vt*>(row + base + c * kPer) = x;
+        for (int j = 0; j < V; ++j) x[j] = LT::store(v[c * V + j]);
+        *reinterpret_cast<vt*>(row + e) = x;
       }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (base + i < E) row[base + i] = LT::store(v[i]);
+    for (int j = 0; j < EPL; ++j) {
+      const int e = row_expert<LT, EPL, LPR>(slot, j);
+      if (e < E) row[e] = LT::store(v[j]);
+    }
   }
 }
 
@@ -152,53 +165,73 @@ __device__ __forceinline__ float exp_f32(float d) { return __builtin_amdgcn_exp2
 // sigmoid(z) and 1 - sigmoid(z) = sigmoid(-z), each without cancellation.
 __device__ __forceinline__ float sigmoid_f32(float z) { return recip_f32(1.0f + exp_f32(-z)); }
 
-// exp(z - m) with exp of a masked value (-inf) 0 also where the whole row is
-// masked (m = -inf), whose softmax is taken as zero.
-__device__ __forceinline__ float exp_below(float z, float m) {
-  return m == -__builtin_inff() ? 0.0f : exp_f32(z - m);
+// sigmoid(z) and 1 - sigmoid(z) = e^-z sigmoid(z) together, neither by a
+// difference; below -80 the second is 1 (and e^-z may be infinite).
+__device__ __forceinline__ float sigmoid_pair(float z, float& rest) {
+  const float e = exp_f32(-z), s = recip_f32(1.0f + e);
+  rest = z < -80.0f ? 1.0f : e * s;
+  return s;
 }
 
-// Host side: values per thread and waves per row for E experts, and whether
-// a row of this layout can be read and written with vector accesses.
+// What a row's exponentials count from: its maximum, or 0 where all of it is
+// masked (-inf): exp(-inf - 0) = 0, a softmax of zeros.
+__device__ __forceinline__ float exp_base(float row_max) { return row_max == -__builtin_inff() ? 0.0f : row_max; }
+
+// Host side: threads per row and values per thread for E experts and k
+// picks (one thread each), and whether rows of this layout can be read and
+// written by chunks.  Few threads a row share a reduction's steps among more
+// rows; many (`wide`) have less to do one after the other.
 struct RowPlan {
-  int epl, wpr;
+  int lpr, epl;
 };
-inline RowPlan row_plan(int E) {
-  RowPlan p{1, 1};
-  if (E > 1024) p.wpr = 16;
-  while (64 * p.wpr * p.epl < E) p.epl *= 2;
+inline RowPlan row_plan(int E, int k, bool wide) {
+  RowPlan p{wide ? 64 : 16, 0};
+  if (E > 1024) {
+    p.lpr = 1024;
+  } else {
+    while (16 * p.lpr < E || p.lpr < k) p.lpr *= 2;
+  }
+  const int need = (E + p.lpr - 1) / p.lpr;
+  p.epl = need <= 4 ? 4 : need <= 8 && (p.lpr == 16 || p.lpr == 64) ? 8 : 16;
   return p;
 }
 inline bool row_vec(const void* base, long long ld, int E, int epl, int elem) {
-  const int bytes = epl * elem < 16 ? epl * elem : 16;
-  return E % epl == 0 && (uintptr_t)base % bytes == 0 && (ld * elem) % bytes == 0;
+  const int chunk = epl * elem < 16 ? epl : 16 / elem;
+  return E % chunk == 0 && (uintptr_t)base % (chunk * elem) == 0 && ld % chunk == 0;
 }
 
 }  // namespace moeq4
 
-// Calls F<LT, EPL, WPR>(...) for a logits type and a RowPlan.
-#define MOE_ROW_DISPATCH_EPL(LT, plan, CALL)                       \
-  if ((plan).wpr == 1) {                                           \
-    switch ((plan).epl) {                                          \
-      case 1: CALL(LT, 1, 1); break;                               \
-      case 2: CALL(LT, 2, 1); break;                               \
-      case 4: CALL(LT, 4, 1); break;                               \
-      case 8: CALL(LT, 8, 1); break;                               \
-      default: CALL(LT, 16, 1); break;                             \
-    }                                                              \
-  } else {                                                         \
-    switch ((plan).epl) {                                          \
-      case 2: CALL(LT, 2, 16); break;                              \
-      case 4: CALL(LT, 4, 16); break;                              \
-      case 8: CALL(LT, 8, 16); break;                              \
-      default: CALL(LT, 16, 16); break;                            \
-    }                                                              \
+// Expands CALL(LT, EPL, LPR) for a logits type and a RowPlan.
+#define MOE_ROW_DISPATCH_EPL(LT, plan, CALL)         \
+  if ((plan).lpr == 16) {                            \
+    switch ((plan).epl) {                            \
+      case 4: CALL(LT, 4, 16); break;                \
+      case 8: CALL(LT, 8, 16); break;                \
+      default: CALL(LT, 16, 16); break;              \
+    }                                                \
+  } else if ((plan).lpr == 32) {                     \
+    if ((plan).epl == 4) {                           \
+      CALL(LT, 4, 32);                               \
+    } else {                                         \
+      CALL(LT, 16, 32);                              \
+    }                                                \
+  } else if ((plan).lpr == 64) {                     \
+    switch ((plan).epl) {                            \
+      case 4: CALL(LT, 4, 64); break;                \
+      case 8: CALL(LT, 8, 64); break;                \
+      default: CALL(LT, 16, 64); break;              \
+    }                                                \
+  } else if ((plan).epl == 4) {                      \
+    CALL(LT, 4, 1024);                               \
+  } else {                                           \
+    CALL(LT, 16, 1024);                              \
   }
-#define MOE_ROW_DISPATCH(dtype, plan, CALL)                        \
-  if ((dtype) == MOE_Q4_DTYPE_BF16) {                              \
-    MOE_ROW_DISPATCH_EPL(LogitBf16, plan, CALL)                    \
-  } else if ((dtype) == MOE_Q4_DTYPE_F32) {                        \
-    MOE_ROW_DISPATCH_EPL(LogitF32, plan, CALL)                     \
-  } else {                                                         \
-    MOE_ROW_DISPATCH_EPL(LogitF16, plan, CALL)                     \
+#define MOE_ROW_DISPATCH(dtype, plan, CALL)          \
+  if ((dtype) == MOE_Q4_DTYPE_BF16) {                \
+    MOE_ROW_DISPATCH_EPL(LogitBf16, plan, CALL)      \
+  } else if ((dtype) == MOE_Q4_DTYPE_F32) {          \
+    MOE_ROW_DISPATCH_EPL(LogitF32, plan, CALL)       \
+  } else {                                           \
+    MOE_ROW_DISPATCH_EPL(LogitF16, plan, CALL)       \
   }
