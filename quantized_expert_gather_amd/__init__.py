@@ -45,9 +45,6 @@ MOE_Q4_CODEC_MXFP8 = 5
 CODECS = {"affine4_g64": (MOE_Q4_CODEC_AFFINE4_G64, 64, 4), "affine4_g32": (MOE_Q4_CODEC_AFFINE4_G32, 32, 4),
           "mxfp4": (MOE_Q4_CODEC_MXFP4, 32, 4), "nvfp4": (MOE_Q4_CODEC_NVFP4, 16, 4),
           "affine8_g64": (MOE_Q4_CODEC_AFFINE8_G64, 64, 8), "mxfp8": (MOE_Q4_CODEC_MXFP8, 32, 8)}
-#: MOE_Q4_CODEC_* of the 4-bit codecs -> inputs per scale group, whether it has biases
-_LINEAR_CODECS = {MOE_Q4_CODEC_AFFINE4_G64: (64, True), MOE_Q4_CODEC_AFFINE4_G32: (32, True),
-                  MOE_Q4_CODEC_MXFP4: (32, False), MOE_Q4_CODEC_NVFP4: (16, False)}
 MOE_Q4_DTYPE_BF16 = 0
 MOE_Q4_DTYPE_F32 = 1
 MOE_Q4_DTYPE_F16 = 2

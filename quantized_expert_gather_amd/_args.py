@@ -1,15 +1,15 @@
-"""Argument checks that the operators beside the expert layer share."""
+"""Argument checks and the call that the operators beside the expert layer
+share.  A checked call costs a few microseconds of host time, most of it the
+launch, so checks read attributes once and build messages only on failure."""
 
 from __future__ import annotations
-
-import contextlib
 
 import torch
 
 #: torch dtype -> MOE_Q4_DTYPE_*
 DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
-_same_device = contextlib.nullcontext()
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
 def matrix(t, dtypes, name: str):
@@ -26,48 +26,59 @@ def matrix(t, dtypes, name: str):
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if rows <= 1 or ld < cols:
+    if ld < cols:
         if rows > 1:
             raise ValueError(f"{name} has overlapping rows")
         ld = cols
-    return t.data_ptr(), ld
+    return t.data_ptr(), ld if rows > 1 else cols
 
 
 def array(t, dtype, shape, name: str, device) -> int:
-    """Pointer of a contiguous device tensor of this type, shape and device."""
+    """Pointer of a contiguous device tensor of this type (one of these types), shape and device."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.device == device and t.is_contiguous() and \
+            (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
 
 
-def on_device(device):
-    """The tensors' device made the current one, if it is not."""
-    return _same_device if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def new(shape, strides, dtype, device):
+    """An uninitialised contiguous tensor (with its strides given, torch takes a shorter way)."""
+    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
-def stream_of(stream, device):
-    """(HIP stream handle, torch stream or None): the caller's stream, or the
-    device's current one."""
+def stream_handle(stream, device) -> int:
+    """HIP stream handle of a call: the caller's stream, or the device's current one."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream, None
-    if isinstance(stream, torch.cuda.Stream):
-        return stream.cuda_stream, stream
-    handle = int(stream)
-    return handle, torch.cuda.ExternalStream(handle, device=device)
+        if _raw_stream is not None:
+            return _raw_stream(device.index)
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def used_on(side, *tensors) -> None:
-    """Tensors that were allocated here and are used on another stream keep
-    their memory until that stream has passed the work enqueued so far."""
-    if side is not None:
-        for t in tensors:
+def call(fn, args, device, stream, made) -> int:
+    """Runs fn(*args, stream) with the tensors' device current; returns its status.
+
+    Tensors that were allocated here (``made``; None entries skipped) and are
+    used on another stream than the current one keep their memory until that
+    stream has passed the work enqueued so far.
+    """
+    handle = stream_handle(stream, device)
+    if torch._C._cuda_getDevice() == device.index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if stream is not None:
+        side = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
+        for t in made:
             if t is not None:
                 t.record_stream(side)
+    return st

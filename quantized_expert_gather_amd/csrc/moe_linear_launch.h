@@ -65,12 +65,10 @@ inline TilesWorkspace tiles_layout(int fmt, int L, int N, int K) {
 // Whether the scale arrays can be read by words.
 inline bool linear_words(const LinearArgs& a) { return (uintptr_t)a.s % 4 == 0 && (uintptr_t)a.b % 4 == 0; }
 
-// Bytes of partial sums of a call with few tokens, whatever its x and the
-// alignment of its scales.
+// Bytes of partial sums of a call with few tokens, whatever its x.
 inline size_t rows_workspace(int fmt, int L, int N, int K) {
   if (K < kLinStep) return 0;
-  const int s = std::max({rows_plan(fmt, false, K, true).splits, rows_plan(fmt, true, K, true).splits,
-                          rows_plan(fmt, false, K, false).splits});
+  const int s = std::max(rows_plan(fmt, false, K, true).splits, rows_plan(fmt, true, K, true).splits);
   return s > 1 ? lin_round256((size_t)s * L * N * 4) : 0;
 }
 

@@ -6,10 +6,16 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, matrix, on_device, stream_of, used_on
+from ._args import DTYPES, array, call, matrix, new, stream_handle
 
 _X = (torch.bfloat16, torch.float16)
 _CODES = (torch.int32, getattr(torch, "uint32", torch.int32))
+#: 4-bit codec (name or MOE_Q4_CODEC_*) -> MOE_Q4_CODEC_*, inputs per scale, scale type, whether it has biases
+_SPECS = {}
+for _name, (_code, _gs, _bits) in _q.CODECS.items():
+    if _bits == 4:
+        _affine = _name.startswith("affine")
+        _SPECS[_name] = _SPECS[_code] = (_code, _gs, torch.bfloat16 if _affine else torch.uint8, _affine)
 
 
 def moe_linear_codec_workspace_bytes(codec, L: int, N: int, K: int) -> int:
@@ -17,12 +23,11 @@ def moe_linear_codec_workspace_bytes(codec, L: int, N: int, K: int) -> int:
 
 
 def _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace):
-    """Checked arguments of a call up to the stream, and the tensors made here."""
-    code = _q._codec_id(codec)
-    spec = _q._LINEAR_CODECS.get(code)
+    """Checked arguments of a call up to the stream, out, and the tensors made here."""
+    spec = _SPECS.get(codec)
     if spec is None:
         raise ValueError(f"codec {codec!r} has no 4-bit dense product")
-    gs, affine = spec
+    code, gs, scale_type, affine = spec
     xp, ldx = matrix(x, _X, "x")
     L, K = x.shape
     dev = x.device
@@ -31,33 +36,37 @@ def _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace):
     N = w.shape[0]
     if K % gs:
         raise _q.MoeQ4Error(_q.MOE_Q4_ERR_UNSUPPORTED, "moe_linear_codec_forward")
-    scale_type = torch.bfloat16 if affine else torch.uint8
-    wp = array(w, _CODES, (N, K // 8), "w", dev)
-    sp = array(s, scale_type, (N, K // gs), "s", dev)
-    bp = array(b, torch.bfloat16, (N, K // gs), "b", dev) if affine else 0
+    if w.dtype in _CODES and w.shape[1] == K // 8 and w.device == dev and w.is_contiguous():
+        wp = w.data_ptr()
+    else:
+        wp = array(w, _CODES, (N, K // 8), "w", dev)
+    rows = (N, K // gs)
+    sp = array(s, scale_type, rows, "s", dev)
+    bp = array(b, torch.bfloat16, rows, "b", dev) if affine else 0
     ap = 0 if bias is None else array(bias, torch.float32, (N,), "bias", dev)
     made = None
     if out is None:
         od = x.dtype if out_dtype is None else out_dtype
         if od not in DTYPES:
             raise TypeError(f"out_dtype {od} is not one of {tuple(DTYPES)}")
-        out = made = torch.empty((L, N), dtype=od, device=dev)
+        out = made = new((L, N), (N, 1), od, dev)
         op, ldo = out.data_ptr(), N
     else:
         op, ldo = matrix(out, DTYPES, "out")
-        if out.shape != (L, N) or out.device != dev or out_dtype not in (None, out.dtype):
+        od = out.dtype
+        if out.shape != (L, N) or out.device != dev or out_dtype not in (None, od):
             raise ValueError(f"out must be [{L}, {N}] on {dev}, of out_dtype")
-    need = _q.lib().moe_linear_codec_workspace_bytes(code, L, N, K)
+    need = _q.lib().moe_linear_codec_workspace_bytes(code, L, N, K) if workspace is None else 0
     scratch = None
-    wsp, wsn = 0, 0
+    wsp = wsn = 0
     if workspace is not None:
         wsn = workspace.numel()
         wsp = array(workspace, torch.uint8, (wsn,), "workspace", dev)
     elif need:
-        scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+        scratch = new((need,), (1,), torch.uint8, dev)
         wsp, wsn = scratch.data_ptr(), need
-    args = (code, xp, DTYPES[x.dtype], ldx, wp, sp, bp, ap, L, N, K, op, DTYPES[out.dtype], ldo, wsp, wsn)
-    return args, out, made, scratch
+    args = (code, xp, DTYPES[x.dtype], ldx, wp, sp, bp, ap, L, N, K, op, DTYPES[od], ldo, wsp, wsn)
+    return args, out, (made, scratch)
 
 
 def moe_linear_codec_forward(codec, x, w, s, b=None, bias=None, out=None, out_dtype=None, workspace=None,
@@ -70,12 +79,10 @@ def moe_linear_codec_forward(codec, x, w, s, b=None, bias=None, out=None, out_dt
     uint8; b bf16 [N, K/group] (affine codecs only); bias fp32 [N].  Returns
     out [L, N] in ``out_dtype`` (bf16, fp16 or fp32; x's type if not given).
     """
-    args, out, made, scratch = _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace)
-    handle, side = stream_of(stream, x.device)
-    with on_device(x.device):
-        _q._check(_q.lib().moe_linear_codec_forward(*args, handle), "moe_linear_codec_forward")
-    if side is not None:
-        used_on(side, made, scratch)
+    args, out, made = _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace)
+    st = call(_q.lib().moe_linear_codec_forward, args, x.device, stream, made)
+    if st:
+        raise _q.MoeQ4Error(st, "moe_linear_codec_forward")
     return out
 
 
@@ -88,16 +95,19 @@ class PreparedLinear:
     of their own (each makes its own if none is given)."""
 
     def __init__(self, codec, x, w, s, b=None, bias=None, out=None, out_dtype=None, workspace=None, stream=None):
-        args, out, _, scratch = _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace)
+        args, out, made = _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace)
         self.out = out
-        self._keep = (x, w, s, b, bias, workspace, scratch, stream)
-        self._args = (*args, stream_of(stream, x.device)[0])
+        self._keep = (x, w, s, b, bias, workspace, made, stream)
+        self._args = (*args, stream_handle(stream, x.device))
         self._fn = _q.lib().moe_linear_codec_forward
         self._device = x.device
 
     def __call__(self) -> torch.Tensor:
-        with on_device(self._device):
+        if torch._C._cuda_getDevice() == self._device.index:
             st = self._fn(*self._args)
+        else:
+            with torch.cuda.device(self._device):
+                st = self._fn(*self._args)
         if st:
             raise _q.MoeQ4Error(st, "moe_linear_codec_forward")
         return self.out

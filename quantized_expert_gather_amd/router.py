@@ -9,30 +9,24 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, matrix, on_device, stream_of, used_on
+from ._args import DTYPES, array, call, matrix, new
 
 
 def _score(score) -> int:
+    code = _q.SCORES.get(score)
+    if code is not None:
+        return code
     if isinstance(score, str):
-        if score not in _q.SCORES:
-            raise ValueError(f"unknown score {score!r}, expected one of {tuple(_q.SCORES)}")
-        return _q.SCORES[score]
+        raise ValueError(f"unknown score {score!r}, expected one of {tuple(_q.SCORES)}")
     return int(score)
-
-
-def _output(t, dtype, shape, name, device):
-    """(tensor, pointer, tensor if it was made here)."""
-    if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        return t, t.data_ptr(), t
-    return t, array(t, dtype, shape, name, device), None
 
 
 def _gradient(logits, dlogits):
     """(tensor, pointer, row stride, tensor if it was made here) of a gradient like `logits`."""
     if dlogits is None:
-        d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        return d, d.data_ptr(), logits.shape[1], d
+        E = logits.shape[1]
+        d = new(logits.shape, (E, 1), logits.dtype, logits.device)
+        return d, d.data_ptr(), E, d
     p, ldd = matrix(dlogits, (logits.dtype,), "dlogits")
     if dlogits.shape != logits.shape or dlogits.device != logits.device:
         raise ValueError("dlogits must have the shape and device of logits")
@@ -47,15 +41,22 @@ def _topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weig
     if not 1 <= k <= E:
         raise _q.MoeQ4Error(_q.MOE_Q4_ERR_SHAPE, "moe_router_topk")
     bp = 0 if select_bias is None else array(select_bias, torch.float32, (E,), "select_bias", dev)
-    ids, ip, made_i = _output(topk_ids, torch.int32, (T, k), "topk_ids", dev)
-    w, wp, made_w = _output(topk_weights, torch.float32, (T, k), "topk_weights", dev)
-    handle, side = stream_of(stream, dev)
-    with on_device(dev):
-        _q._check(_q.lib().moe_router_topk(zp, DTYPES[logits.dtype], ld, bp, T, k, E, _score(score), int(bool(renormalize)),
-                                           float(scale), ip, wp, handle), "moe_router_topk")
-    if side is not None:
-        used_on(side, made_i, made_w)
-    return ids, w
+    made_i = made_w = None
+    if topk_ids is None:
+        topk_ids = made_i = new((T, k), (k, 1), torch.int32, dev)
+        ip = topk_ids.data_ptr()
+    else:
+        ip = array(topk_ids, torch.int32, (T, k), "topk_ids", dev)
+    if topk_weights is None:
+        topk_weights = made_w = new((T, k), (k, 1), torch.float32, dev)
+        wp = topk_weights.data_ptr()
+    else:
+        wp = array(topk_weights, torch.float32, (T, k), "topk_weights", dev)
+    args = (zp, DTYPES[logits.dtype], ld, bp, T, k, E, _score(score), 1 if renormalize else 0, scale, ip, wp)
+    st = call(_q.lib().moe_router_topk, args, dev, stream, (made_i, made_w))
+    if st:
+        raise _q.MoeQ4Error(st, "moe_router_topk")
+    return topk_ids, topk_weights
 
 
 class _TopkFunction(torch.autograd.Function):
@@ -108,13 +109,10 @@ def moe_router_topk_backward(logits, topk_ids, dweights, score="softmax", renorm
     ip = array(topk_ids, torch.int32, (T, k), "topk_ids", dev)
     gp = array(dweights, torch.float32, (T, k), "dweights", dev)
     d, dp, ldd, made = _gradient(logits, dlogits)
-    handle, side = stream_of(stream, dev)
-    with on_device(dev):
-        _q._check(_q.lib().moe_router_topk_backward(zp, DTYPES[logits.dtype], ld, ip, gp, T, k, E, _score(score),
-                                                    int(bool(renormalize)), float(scale), dp, ldd, handle),
-                  "moe_router_topk_backward")
-    if side is not None:
-        used_on(side, made)
+    args = (zp, DTYPES[logits.dtype], ld, ip, gp, T, k, E, _score(score), 1 if renormalize else 0, scale, dp, ldd)
+    st = call(_q.lib().moe_router_topk_backward, args, dev, stream, (made,))
+    if st:
+        raise _q.MoeQ4Error(st, "moe_router_topk_backward")
     return d
 
 
@@ -148,22 +146,21 @@ def _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace, stream)
     ip = array(topk_ids, torch.int32, (rows, k), "topk_ids", dev)
     mp = _mask_ptr(token_mask, rows, dev)
     lib = _q.lib()
-    loss = torch.empty(S, dtype=torch.float32, device=dev)
-    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-    tokens = torch.empty(S, dtype=torch.int32, device=dev)
+    loss, tokens = new((S,), (1,), torch.float32, dev), new((S,), (1,), torch.int32, dev)
+    counts = new((S, E), (E, 1), torch.int32, dev)
     scratch = None
     if workspace is None:
-        scratch = workspace = torch.empty(max(256, lib.moe_balance_loss_workspace_bytes(S, T, E)), dtype=torch.uint8,
-                                          device=dev)
-    wsn = workspace.numel()
-    wsp = array(workspace, torch.uint8, (wsn,), "workspace", dev)
-    handle, side = stream_of(stream, dev)
-    with on_device(dev):
-        _q._check(lib.moe_balance_loss(zp, DTYPES[logits.dtype], ld, ip, mp, S, T, k, E, _score(score), float(coef),
-                                       loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(), wsp, wsn, handle),
-                  "moe_balance_loss")
-    if side is not None:
-        used_on(side, loss, counts, tokens, scratch)
+        wsn = lib.moe_balance_loss_workspace_bytes(S, T, E)
+        scratch = new((wsn,), (1,), torch.uint8, dev)
+        wsp = scratch.data_ptr()
+    else:
+        wsn = workspace.numel()
+        wsp = array(workspace, torch.uint8, (wsn,), "workspace", dev)
+    args = (zp, DTYPES[logits.dtype], ld, ip, mp, S, T, k, E, _score(score), coef, loss.data_ptr(), counts.data_ptr(),
+            tokens.data_ptr(), wsp, wsn)
+    st = call(lib.moe_balance_loss, args, dev, stream, (loss, counts, tokens, scratch))
+    if st:
+        raise _q.MoeQ4Error(st, "moe_balance_loss")
     return loss, counts, tokens
 
 
@@ -218,11 +215,8 @@ def moe_balance_loss_backward(logits, counts, tokens, dloss, k: int, coef: float
     gp = array(dloss, torch.float32, (S,), "dloss", dev)
     mp = _mask_ptr(token_mask, rows, dev)
     d, dp, ldd, made = _gradient(logits, dlogits)
-    handle, side = stream_of(stream, dev)
-    with on_device(dev):
-        _q._check(_q.lib().moe_balance_loss_backward(zp, DTYPES[logits.dtype], ld, mp, cp, np_, gp, S, T, int(k), E,
-                                                     _score(score), float(coef), dp, ldd, handle),
-                  "moe_balance_loss_backward")
-    if side is not None:
-        used_on(side, made)
+    args = (zp, DTYPES[logits.dtype], ld, mp, cp, np_, gp, S, T, int(k), E, _score(score), coef, dp, ldd)
+    st = call(_q.lib().moe_balance_loss_backward, args, dev, stream, (made,))
+    if st:
+        raise _q.MoeQ4Error(st, "moe_balance_loss_backward")
     return d
