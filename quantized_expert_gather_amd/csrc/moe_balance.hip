@@ -25,6 +25,7 @@ namespace {
 // loads are all on their way before the first is used, and their reductions
 // interleave.
 constexpr int kPartialWaves = 16, kBackWaves = 4;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <int EPL, int LPR>
 constexpr int kRows = LPR > 64 ? 1 : EPL == 4 ? 4 : EPL == 8 ? 2 : 1;
 
@@ -35,19 +36,22 @@ struct BalanceArgs {
   float* psum;      // [S][blocks][E] partial sums of p
   int32_t* pcount;  // [S][blocks][E] partial route counts
   int32_t* ptok;    // [S][blocks] unmasked tokens
+  float* pdot;      // [S][chunks] sums of c_e p_e over a chunk of experts
+  int32_t* ticket;  // [S] chunks done
   float* loss;
   int32_t* counts;
   int32_t* tokens;
   long long ld;
   int S, T, k, E, score, vec;
   int blocks, per;  // workgroups of a sequence, tokens of each
+  int chunks;
   float coef;
 };
 
-// p of R rows in place of their logits, and 1 - sigmoid(z) in `damp` (DAMP,
-// sigmoid scores only).
+// p of R rows but for their factor `inv`, in place of their logits, and
+// 1 - sigmoid(z) in `damp` (DAMP, sigmoid scores only).
 template <class LT, int EPL, int LPR, int R, bool DAMP>
-__device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&damp)[DAMP ? R : 1][EPL], int slot, int E,
+__device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&damp)[DAMP ? R : 1][EPL], float (&inv)[R],
                                                   int score, float* red) {
   float sum[R];
   if (score == kRouterScoreSoftmax) {
@@ -86,11 +90,7 @@ __device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&da
 #pragma unroll
   for (int r = 0; r < R; ++r) sum[r] = row_all<LPR>(sum[r], OpSumF(), red);
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const float inv = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) v[r][i] *= inv;
-  }
+  for (int r = 0; r < R; ++r) inv[r] = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];
 }
 
 template <class LT, int EPL, int LPR>
@@ -100,8 +100,9 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
   extern __shared__ unsigned char lds[];
   float* red = reinterpret_cast<float*>(lds);            // [16]
   int32_t* ntok = reinterpret_cast<int32_t*>(lds) + 16;  // [1], padded to 16
-  int32_t* hist = reinterpret_cast<int32_t*>(lds) + 32;  // [E]
-  float* sums = reinterpret_cast<float*>(hist + a.E);    // [kPartialWaves][E] (LPR <= 64)
+  int32_t* hist = reinterpret_cast<int32_t*>(lds) + 32;  // [E], padded to 4
+  float* sums = reinterpret_cast<float*>(hist + (a.E + 3) / 4 * 4);  // [kPartialWaves][kWide] (LPR <= 64)
+  constexpr int kWide = EPL * LPR;
   const int tid = threadIdx.x, nthr = 64 * kPartialWaves;
   const int wave = tid >> 6, group = tid / LPR, slot = tid % LPR;
   const int t0 = blockIdx.x * a.per, t1 = min(a.T, t0 + a.per);
@@ -145,11 +146,14 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
       for (int i = 0; i < EPL; ++i) v[r][i] = next[r][i];
     }
     if (t + R * kGroups < t1) load(t + R * kGroups);
-    row_probabilities<LT, EPL, LPR, R, false>(v, none, slot, a.E, a.score, red);
+    float inv[R];
+    row_probabilities<LT, EPL, LPR, R, false>(v, none, inv, a.score, red);
 #pragma unroll
     for (int r = 0; r < R; ++r)
+      if (live[r]) {  // (a masked row may hold anything)
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) acc[i] += live[r] ? v[r][i] : 0.0f;
+        for (int i = 0; i < EPL; ++i) acc[i] = __builtin_fmaf(v[r][i], inv[r], acc[i]);
+      }
   }
 
   const size_t part = ((size_t)blockIdx.y * a.blocks + blockIdx.x) * a.E;
@@ -170,16 +174,15 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
     }
     if ((tid & 63) < LPR) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = row_expert<LT, EPL, LPR>(slot, i);
-        if (e < a.E) sums[wave * a.E + e] = acc[i];
-      }
+      for (int i = 0; i < EPL; i += 4)
+        *reinterpret_cast<f32x4*>(sums + wave * kWide + row_expert<LT, EPL, LPR>(slot, i)) =
+            f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
     }
     __syncthreads();
     for (int e = tid; e < a.E; e += nthr) {
       float s = sums[e];
 #pragma unroll
-      for (int w = 1; w < kPartialWaves; ++w) s += sums[w * a.E + e];
+      for (int w = 1; w < kPartialWaves; ++w) s += sums[w * kWide + e];
       a.psum[part + e] = s;
       a.pcount[part + e] = hist[e];
     }
@@ -192,63 +195,68 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
     }
     for (int e = tid; e < a.E; e += nthr) a.pcount[part + e] = hist[e];
   }
-  if (tid == 0) a.ptok[(size_t)blockIdx.y * a.blocks + blockIdx.x] = ntok[0];
+  if (tid == 0) {
+    a.ptok[(size_t)blockIdx.y * a.blocks + blockIdx.x] = ntok[0];
+    if (blockIdx.x == 0) a.ticket[blockIdx.y] = 0;
+  }
 }
 
-// Adds a sequence's partials: counts, token count and loss.  Where there are
-// fewer experts than threads, 1024 / cols threads share an expert's partials.
-__global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a, int cols) {
-  __shared__ float redf[1024];
-  __shared__ int redi[1024];
+// Adds a sequence's partials: counts, token count and loss.  A workgroup takes
+// kCols experts, 1024 / kCols threads sharing an expert's partials; the last
+// one to finish adds the workgroups' sums in ascending order.
+constexpr int kCols = 32;
+__global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a) {
+  constexpr int kSlices = 1024 / kCols;
+  __shared__ float redf[kSlices][kCols + 1];
+  __shared__ int redi[kSlices][kCols + 1];
+  __shared__ int redn[16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const size_t part = (size_t)blockIdx.x * a.blocks;
-  const int slices = 1024 / cols, slice = tid / cols, col = tid & (cols - 1);
+  const int seq = blockIdx.y;
+  const size_t part = (size_t)seq * a.blocks;
+  const int slice = tid / kCols, col = tid % kCols;
   int n = 0;
   for (int b = tid; b < a.blocks; b += 1024) n += a.ptok[part + b];
-  float dot = 0.0f;
-  for (int e0 = 0; e0 < a.E; e0 += cols) {
-    const int e = e0 + col;
-    float s = 0.0f;
-    int c = 0;
-    if (e < a.E) {
+  const int e = blockIdx.x * kCols + col;
+  float s = 0.0f;
+  int c = 0;
+  if (e < a.E) {
 #pragma unroll 8
-      for (int b = slice; b < a.blocks; b += slices) {
-        s += a.psum[(part + b) * a.E + e];
-        c += a.pcount[(part + b) * a.E + e];
-      }
-    }
-    if (slices > 1) {
-      redf[tid] = s;
-      redi[tid] = c;
-      __syncthreads();
-      if (slice == 0)
-        for (int q = 1; q < slices; ++q) {
-          s += redf[q * cols + col];
-          c += redi[q * cols + col];
-        }
-      __syncthreads();
-    }
-    if (slice == 0 && e < a.E) {
-      a.counts[(size_t)blockIdx.x * a.E + e] = c;
-      dot += (float)c * s;
+    for (int b = slice; b < a.blocks; b += kSlices) {
+      s += a.psum[(part + b) * a.E + e];
+      c += a.pcount[(part + b) * a.E + e];
     }
   }
+  redf[slice][col] = s;
+  redi[slice][col] = c;
   for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
-  dot = row_all<64>(dot, OpSumF());
-  if (lane == 0) {
-    redf[wave] = dot;
-    redi[wave] = n;
-  }
+  if (lane == 0) redn[wave] = n;
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < 16; ++w) {
-      dot += redf[w];
-      n += redi[w];
-    }
-    a.tokens[blockIdx.x] = n;
-    const float nf = (float)n;
-    a.loss[blockIdx.x] = n ? a.coef * (float)a.E / ((float)a.k * nf) * (dot / nf) : 0.0f;
+  if (wave > 0) return;
+  // lanes 0..31 and 32..63 add half the slices each
+  constexpr int kHalf = kSlices / 2;
+  s = 0.0f;
+  c = 0;
+#pragma unroll
+  for (int q = 0; q < kHalf; ++q) {
+    s += redf[(lane / kCols) * kHalf + q][col];
+    c += redi[(lane / kCols) * kHalf + q][col];
   }
+  s += __shfl_xor(s, kCols, 64);
+  c += __shfl_xor(c, kCols, 64);
+  if (lane < kCols && e < a.E) a.counts[(size_t)seq * a.E + e] = c;
+  float dot = row_all<64>(lane < kCols ? (float)c * s : 0.0f, OpSumF());
+  n = row_all<64>(lane < 16 ? redn[lane & 15] : 0, [](int x, int y) { return x + y; });
+  if (lane > 0) return;
+  if (a.chunks > 1) {
+    float* dots = a.pdot + (size_t)seq * a.chunks;
+    __hip_atomic_store(dots + blockIdx.x, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__hip_atomic_fetch_add(a.ticket + seq, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) != a.chunks - 1) return;
+    dot = 0.0f;
+    for (int q = 0; q < a.chunks; ++q) dot += __hip_atomic_load(dots + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  a.tokens[seq] = n;
+  const float nf = (float)n;
+  a.loss[seq] = n ? a.coef * (float)a.E / ((float)a.k * nf) * (dot / nf) : 0.0f;
 }
 
 struct BalanceBackArgs {
@@ -269,6 +277,7 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : 64 * kBackWaves) void k_balance_ba
   typedef typename LT::mem mem;
   constexpr int R = kRows<EPL, LPR>, kGroups = (LPR > 64 ? LPR : 64 * kBackWaves) / LPR;
   __shared__ float red[16];
+  __shared__ __attribute__((aligned(16))) float factors[EPL * LPR];
   const int tid = threadIdx.x, group = tid / LPR, slot = tid % LPR;
   const int t0 = blockIdx.x * a.per, t1 = min(a.T, t0 + a.per);
   const size_t seq = (size_t)blockIdx.y * a.T;
@@ -282,11 +291,15 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : 64 * kBackWaves) void k_balance_ba
   load(t0);
   const float n = (float)a.tokens[blockIdx.y];
   const float f = n > 0.0f ? a.dloss[blockIdx.y] * a.coef * ((float)a.E / ((float)a.k * n)) / n : 0.0f;
+  // the counts through LDS: neighbouring threads read neighbouring ones, each then its own
+  for (int e = tid; e < EPL * LPR; e += blockDim.x) factors[e] = e < a.E ? f * (float)a.counts[(size_t)blockIdx.y * a.E + e] : 0.0f;
+  __syncthreads();
   float w[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = row_expert<LT, EPL, LPR>(slot, i);
-    w[i] = e < a.E ? f * (float)a.counts[(size_t)blockIdx.y * a.E + e] : 0.0f;
+  for (int i = 0; i < EPL; i += 4) {
+    const f32x4 u = *reinterpret_cast<const f32x4*>(factors + row_expert<LT, EPL, LPR>(slot, i));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[i + j] = u[j];
   }
   for (int t = t0; t < t1; t += R * kGroups) {
 #pragma unroll
@@ -294,11 +307,13 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : 64 * kBackWaves) void k_balance_ba
 #pragma unroll
       for (int i = 0; i < EPL; ++i) v[r][i] = next[r][i];
     if (t + R * kGroups < t1) load(t + R * kGroups);
-    row_probabilities<LT, EPL, LPR, R, true>(v, damp, slot, a.E, a.score, red);
-    float dot[R];
+    float dot[R], inv[R];
+    row_probabilities<LT, EPL, LPR, R, true>(v, damp, inv, a.score, red);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       dot[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[r][i] *= inv[r];
 #pragma unroll
       for (int i = 0; i < EPL; ++i) dot[r] += w[i] * v[r][i];
     }
@@ -324,7 +339,7 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : 64 * kBackWaves) void k_balance_ba
 
 // Tokens of a workgroup: enough workgroups to fill the card, few enough that
 // the second launch has little to add.
-constexpr int kMaxBlocks = 128;
+constexpr int kMaxBlocks = 256;
 int blocks_of(int S, int T, int E) {
   const int rows = E > 1024 ? 1 : kPartialWaves;
   const int want = std::max(1, kMaxBlocks / std::max(1, S));
@@ -332,7 +347,7 @@ int blocks_of(int S, int T, int E) {
 }
 
 struct BalanceWorkspace {
-  size_t psum, pcount, ptok, total;
+  size_t psum, pcount, ptok, pdot, ticket, total;
 };
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 BalanceWorkspace balance_layout(int S, int T, int E) {
@@ -342,6 +357,8 @@ BalanceWorkspace balance_layout(int S, int T, int E) {
   w.psum = off;   off = round256(off + rows * E * 4);
   w.pcount = off; off = round256(off + rows * E * 4);
   w.ptok = off;   off = round256(off + rows * 4);
+  w.pdot = off;   off = round256(off + (size_t)S * ((E + kCols - 1) / kCols) * 4);
+  w.ticket = off; off = round256(off + (size_t)S * 4);
   w.total = off;
   return w;
 }
@@ -406,6 +423,9 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, long long 
   a.psum = reinterpret_cast<float*>(ws + lay.psum);
   a.pcount = reinterpret_cast<int32_t*>(ws + lay.pcount);
   a.ptok = reinterpret_cast<int32_t*>(ws + lay.ptok);
+  a.pdot = reinterpret_cast<float*>(ws + lay.pdot);
+  a.ticket = reinterpret_cast<int32_t*>(ws + lay.ticket);
+  a.chunks = (E + kCols - 1) / kCols;
   a.loss = loss;
   a.counts = counts;
   a.tokens = tokens;
@@ -417,13 +437,11 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, long long 
   a.per = (T + a.blocks - 1) / a.blocks;
   a.coef = coef;
   const dim3 grid(a.blocks, S), block(64 * kPartialWaves);
-  const size_t lds = 128 + (size_t)E * 4 + (plan.lpr > 64 ? 0 : (size_t)kPartialWaves * E * 4);
+  const size_t lds = 128 + ((size_t)E + 3) / 4 * 16 + (plan.lpr > 64 ? 0 : (size_t)kPartialWaves * plan.epl * plan.lpr * 4);
 #define MOE_BALANCE_CALL(LT, EPL, LPR) hipLaunchKernelGGL((k_balance_partial<LT, EPL, LPR>), grid, block, lds, stream, a)
   MOE_ROW_DISPATCH(logits_dtype, plan, MOE_BALANCE_CALL)
   if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
-  int cols = 1;
-  while (cols < E && cols < 1024) cols *= 2;
-  hipLaunchKernelGGL(k_balance_finish, dim3(S), dim3(1024), 0, stream, a, cols);
+  hipLaunchKernelGGL(k_balance_finish, dim3(a.chunks, S), dim3(1024), 0, stream, a);
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }
 
