@@ -21,24 +21,49 @@ int linear_launch(bool f16, const LinearArgs& a, unsigned char* workspace, hipSt
 // Tokens from which the tiles take over.
 constexpr int kTilesFrom = 17;
 
+// Tile shape and split of K.  A compute unit holds two workgroups, so they
+// run in rounds of 512, and what a round takes per 1024 inputs was measured
+// (us; 4096 x 4096 weights and other shapes of exactly 256 and 512 workgroups,
+// the formats' mean): wide tiles do more per byte of LDS, narrow ones leave
+// fewer compute units idle in the last round.  Splits add their partial sums'
+// way through memory and a launch.  The plan is the one with the least sum;
+// against the widest tiles that give 256 workgroups, mxfp4 1536 x 4096 x 4096
+// goes from 84 to 60 us and 16384 outputs of 24 tokens from 24 to 17.
 struct TilesPlan {
   int mt, nt, row_tiles, tok_tiles, splits, steps_per;
 };
 inline TilesPlan tiles_plan(int L, int N, int K) {
-  TilesPlan p{};
-  p.mt = L <= 32 ? 2 : L <= 64 ? 4 : 8;
-  p.tok_tiles = (L + 16 * p.mt - 1) / (16 * p.mt);
+  static const float kFull[3][3] = {{6.0f, 9.5f, 13.5f}, {7.5f, 12.0f, 16.5f}, {13.0f, 18.0f, 26.0f}};
+  static const float kHalf[3][3] = {{5.5f, 7.5f, 9.8f}, {6.5f, 8.7f, 11.5f}, {9.5f, 12.5f, 17.0f}};
   const int steps = (K + kLinStep - 1) / kLinStep;
-  for (p.nt = 3;; --p.nt) {
-    p.row_tiles = (N + 64 * p.nt - 1) / (64 * p.nt);
-    if (p.nt == 1 || (long)p.row_tiles * p.tok_tiles >= 256) break;
+  const float out_us = (float)L * (float)N * (8.0f / 6e6f);  // a split's sums written and read
+  TilesPlan best{};
+  float least = 0.0f;
+  for (int m = 0; m < 3; ++m) {
+    const int mt = 2 << m, tok_tiles = (L + 16 * mt - 1) / (16 * mt);
+    if (m && 8 * mt >= (L + 15) / 16 * 16) break;  // half the tile would be empty
+    for (int nt = 3; nt >= 1; --nt) {
+      const int row_tiles = (N + 64 * nt - 1) / (64 * nt);
+      const long tiles = (long)row_tiles * tok_tiles;
+      int tried = 0;
+      for (int fill = 0; fill <= 512; fill += 256) {
+        const int s = (int)std::max(1L, std::min<long>(std::min(16, steps / 4), fill / tiles));
+        if (s == tried) continue;
+        tried = s;
+        const int per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
+        const long n = tiles * splits, rounds = n / 512, rest = n % 512;
+        const float k = (float)per / 8.0f, end = 0.6f * (float)(mt * nt);
+        float us = (float)rounds * (k * kFull[m][nt - 1] + end);
+        if (rest) us += k * (rest > 256 ? kFull : kHalf)[m][nt - 1] + end;
+        if (splits > 1) us += 2.5f + (float)splits * out_us;
+        if (best.mt == 0 || us < least) {
+          best = TilesPlan{mt, nt, row_tiles, tok_tiles, splits, per};
+          least = us;
+        }
+      }
+    }
   }
-  const long tiles = (long)p.row_tiles * p.tok_tiles;
-  p.splits = 1;
-  if (tiles < 256) p.splits = (int)std::max(1L, std::min<long>(std::min(16, steps / 4), 512 / tiles));
-  p.steps_per = (steps + p.splits - 1) / p.splits;
-  p.splits = (steps + p.steps_per - 1) / p.steps_per;
-  return p;
+  return best;
 }
 
 struct TilesWorkspace {

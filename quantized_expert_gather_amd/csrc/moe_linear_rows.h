@@ -169,16 +169,21 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
     constexpr int kPieces = kStageSteps * 16;  // of a token
 #pragma unroll
     for (int s0 = 0; s0 < S; s0 += kStageSteps) {
+      constexpr int kLoads = (kStageTokens * kPieces + 63) / 64;
+      lin_u32x4 in[kLoads];  // all on their way before the first is used
 #pragma unroll
-      for (int i0 = 0; i0 < kStageTokens * kPieces; i0 += 64) {
-        if (i0 >= rows * kPieces) break;
-        const int i = i0 + lane, t = i / kPieces, c = s0 * kLinStep + (i - t * kPieces) * 8;
+      for (int l = 0; l < kLoads; ++l) {
+        const int i = 64 * l + lane, t = i / kPieces, c = s0 * kLinStep + (i - t * kPieces) * 8;
         const uint32_t at = t < rows && c < room ? ((uint32_t)t * (uint32_t)a.ldx + c) * 2u : 0x80000000u;
-        lin_u32x4 v = __builtin_bit_cast(lin_u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, at, first * kLinStep * 2, 0));
+        in[l] = __builtin_bit_cast(lin_u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, at, first * kLinStep * 2, 0));
+      }
+#pragma unroll
+      for (int l = 0; l < kLoads; ++l) {
+        lin_u32x4 v = in[l];
         if constexpr (kAffine)  // the codes' pair order
           v = lin_u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
                         __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
-        if (i < kStageTokens * kPieces) mine[i] = v;
+        if (64 * l + lane < kStageTokens * kPieces) mine[64 * l + lane] = v;
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       const int t = kSep ? n16 >> 2 : n16;
@@ -264,7 +269,9 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
         } else if constexpr (kRec == 1) {
           v[st][0] = (u[st][0] >> (8 * kb)) & 255u;
         } else {
-          v[st][0] = (kb & 2 ? u[st][kRec - 1] : u[st][0]) >> (16 * (kb & 1));
+          // (a selection between the two would become an indexed array in memory)
+          const uint32_t upper = 0u - (uint32_t)(kb >> 1);
+          v[st][0] = ((u[st][kRec - 1] & upper) | (u[st][0] & ~upper)) >> (16 * (kb & 1));
         }
       }
     };
