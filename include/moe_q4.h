@@ -97,7 +97,9 @@ extern "C" {
 #define MOE_Q4_BALANCE_MAX_SEQS 65535 /* sequences of one moe_balance_loss call                 */
 #define MOE_Q4_LINEAR_MAX_L 1048560  /* tokens of one moe_linear_codec_forward call            */
 #define MOE_Q4_LINEAR_MAX_K 1048576  /* inputs of a row of moe_linear_codec_forward            */
+#define MOE_Q4_LINEAR_MAX_N 268435456 /* its outputs                                           */
 #define MOE_Q4_LINEAR_MAX_LDX 16777216 /* distance of its x rows                              */
+#define MOE_Q4_ROUTER_MAX_T 1073741824 /* tokens of one router or balance loss call           */
 
 /* ---- forward stages (moe_swiglu_q4_forward_stages) ---- */
 #define MOE_Q4_STAGE_GATEUP 1u   /* union (or sort) + fused gate/up + silu(gate)*up -> workspace  */
@@ -358,12 +360,22 @@ int moe_sort_pairs(const int32_t *topk_ids, int L, int k, int E, int bm, int32_t
  *   out        [L, N] in out_dtype (MOE_Q4_DTYPE_*), rows ldo elements apart,
  *              fully overwritten; must not overlap an input or the workspace
  *   workspace  moe_linear_codec_workspace_bytes bytes (256-byte aligned, no
- *              initialisation; NULL where that is 0); not shared by calls that
- *              may run at the same time
+ *              initialisation; NULL where that is 0; no overlap with an
+ *              input); not shared by calls, or graphs, that may run at the
+ *              same time
  *
  * Products are exact, sums are fp32 and rounded once to out_dtype; results are
- * deterministic.  L == 0 returns MOE_Q4_OK without touching the GPU.  Needs
- * L <= MOE_Q4_LINEAR_MAX_L, K <= MOE_Q4_LINEAR_MAX_K, ldx <= MOE_Q4_LINEAR_MAX_LDX.
+ * deterministic.  Outside the usual range: an infinite or NaN x gives its own
+ * token's outputs as infinities or NaN (not always the one the sum itself
+ * gives); an E8M0 or E4M3 NaN scale its own row's.  mxfp4 products of elements
+ * below 2^-126 are taken as 0, and with more than 16 tokens so are fp16 ones
+ * 2^-126 below their row's largest block; sums may be infinite where |x| times
+ * a code's 31 is past fp32.  With more than 16 tokens affine scales 2^-34
+ * below the largest of their row, and bf16 x 2^-39 below the largest of their
+ * token, lose bits.
+ * L == 0 returns MOE_Q4_OK without touching the GPU.  Needs
+ * L <= MOE_Q4_LINEAR_MAX_L, N <= MOE_Q4_LINEAR_MAX_N, K <= MOE_Q4_LINEAR_MAX_K,
+ * ldx <= MOE_Q4_LINEAR_MAX_LDX.
  */
 int moe_linear_codec_forward(int codec, const void *x, int x_dtype, long long ldx, const uint32_t *w,
                              const void *s, const void *b, const float *bias, int L, int N, int K,
@@ -390,7 +402,8 @@ size_t moe_linear_codec_workspace_bytes(int codec, int L, int N, int K);
  * tell apart are compared in 64 bits.  A logit of -inf (a masked expert) has
  * score 0; so do all experts of a row of nothing else, whose weights are 0
  * and whose ids are the lowest.  NaN logits rank below -inf.  ids are always
- * k different experts.  1 <= k <= MOE_Q4_ROUTER_MAX_K, E <= MOE_Q4_MAX_E.
+ * k different experts.  1 <= k <= MOE_Q4_ROUTER_MAX_K, E <= MOE_Q4_MAX_E,
+ * T <= MOE_Q4_ROUTER_MAX_T.
  */
 int moe_router_topk(const void *logits, int logits_dtype, long long ld, const float *select_bias, int T,
                     int k, int E, int score, int renormalize, float scale, int32_t *topk_ids,
@@ -419,9 +432,11 @@ int moe_router_topk_backward(const void *logits, int logits_dtype, long long ld,
  *   loss       fp32 [S] (0 for a sequence without tokens)
  *   counts     int32 [S, E];  tokens int32 [S]: c_e and n
  *   workspace  moe_balance_loss_workspace_bytes(S, T, E) bytes (256-byte
- *              aligned, no initialisation)
+ *              aligned, no initialisation, no overlap with an input; not
+ *              shared by calls, or graphs, that may run at the same time)
  *
- * Sums are fp32 in a fixed order.  S <= MOE_Q4_BALANCE_MAX_SEQS.
+ * Sums are fp32 in a fixed order.  S <= MOE_Q4_BALANCE_MAX_SEQS, E <= MOE_Q4_MAX_E,
+ * T <= MOE_Q4_ROUTER_MAX_T.
  */
 int moe_balance_loss(const void *logits, int logits_dtype, long long ld, const int32_t *topk_ids,
                      const uint8_t *token_mask, int S, int T, int k, int E, int score, float coef,

@@ -60,7 +60,9 @@ MOE_Q4_ROUTER_MAX_K = 64
 MOE_Q4_BALANCE_MAX_SEQS = 65535
 MOE_Q4_LINEAR_MAX_L = 1048560
 MOE_Q4_LINEAR_MAX_K = 1048576
+MOE_Q4_LINEAR_MAX_N = 268435456
 MOE_Q4_LINEAR_MAX_LDX = 16777216
+MOE_Q4_ROUTER_MAX_T = 1073741824
 
 EXPORTS = (
     "moe_swiglu_q4_workspace_bytes",

@@ -9,8 +9,6 @@ import torch
 #: torch dtype -> MOE_Q4_DTYPE_*
 DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
-
 
 def matrix(t, dtypes, name: str):
     """A device matrix with contiguous rows: (pointer, row stride in elements)."""
@@ -54,31 +52,27 @@ def new(shape, strides, dtype, device):
     return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
-def stream_handle(stream, device) -> int:
-    """HIP stream handle of a call: the caller's stream, or the device's current one."""
-    if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(device.index)
-        return torch.cuda.current_stream(device).cuda_stream
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+def on_stream(stream, tensor):
+    """Context of a call on a stream of the caller's (a torch stream or a HIP
+    handle): what the call allocates belongs to that stream too, so neither
+    earlier work on the current stream nor later work there shares its memory."""
+    device = tensor.device
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
-def call(fn, args, device, stream, made) -> int:
-    """Runs fn(*args, stream) with the tensors' device current; returns its status.
+def current_handle(device) -> int:
+    """HIP handle of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
-    Tensors that were allocated here (``made``; None entries skipped) and are
-    used on another stream than the current one keep their memory until that
-    stream has passed the work enqueued so far.
-    """
-    handle = stream_handle(stream, device)
+
+def call(fn, args, device, handle) -> int:
+    """Runs fn(*args, handle) with the tensors' device current; returns its status."""
     if torch._C._cuda_getDevice() == device.index:
-        st = fn(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, handle)
-    if stream is not None:
-        side = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=device)
-        for t in made:
-            if t is not None:
-                t.record_stream(side)
-    return st
+        return fn(*args, handle)
+    with torch.cuda.device(device):
+        return fn(*args, handle)

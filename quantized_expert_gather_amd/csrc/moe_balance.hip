@@ -365,7 +365,7 @@ BalanceWorkspace balance_layout(int S, int T, int E) {
 
 int check_balance(int dtype, long long ld, int S, int T, int k, int E, int score) {
   if (S < 0 || T < 0 || k < 1 || E < 1 || k > E || ld < E) return MOE_Q4_ERR_SHAPE;
-  if (E > MOE_Q4_MAX_E || S > MOE_Q4_BALANCE_MAX_SEQS) return MOE_Q4_ERR_UNSUPPORTED;
+  if (E > MOE_Q4_MAX_E || S > MOE_Q4_BALANCE_MAX_SEQS || T > MOE_Q4_ROUTER_MAX_T) return MOE_Q4_ERR_UNSUPPORTED;
   if (dtype != MOE_Q4_DTYPE_BF16 && dtype != MOE_Q4_DTYPE_F32 && dtype != MOE_Q4_DTYPE_F16) return MOE_Q4_ERR_UNSUPPORTED;
   if (score != MOE_Q4_SCORE_SOFTMAX && score != MOE_Q4_SCORE_SIGMOID) return MOE_Q4_ERR_UNSUPPORTED;
   return MOE_Q4_OK;
@@ -384,7 +384,7 @@ size_t span(size_t rows, long long ld, int E, size_t es) { return rows ? ((rows 
 using namespace moeq4;
 
 extern "C" size_t moe_balance_loss_workspace_bytes(int S, int T, int E) {
-  if (S < 1 || T < 0 || E < 1 || E > MOE_Q4_MAX_E || S > MOE_Q4_BALANCE_MAX_SEQS) return 0;
+  if (S < 1 || T < 0 || E < 1 || E > MOE_Q4_MAX_E || S > MOE_Q4_BALANCE_MAX_SEQS || T > MOE_Q4_ROUTER_MAX_T) return 0;
   return balance_layout(S, T, E).total;
 }
 
@@ -411,6 +411,8 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, long long 
   for (const auto& o : outs)
     for (const auto& in : ins)
       if (overlap(o.p, o.n, in.p, in.n)) return MOE_Q4_ERR_ALIAS;
+  for (int i = 0; i < 3; ++i)
+    if (overlap(workspace, lay.total, ins[i].p, ins[i].n)) return MOE_Q4_ERR_ALIAS;
   for (int i = 0; i < 3; ++i)
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return MOE_Q4_ERR_ALIAS;

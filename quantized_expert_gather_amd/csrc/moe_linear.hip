@@ -24,7 +24,7 @@ int linear_fmt(int codec) {
 int linear_shape_status(int fmt, int L, int N, int K) {
   if (L < 0 || N < 1 || K < 1) return MOE_Q4_ERR_SHAPE;
   const int grp = fmt == kLinAffine64 ? 64 : 32;
-  if (fmt < 0 || K % grp || L > MOE_Q4_LINEAR_MAX_L || K > MOE_Q4_LINEAR_MAX_K) return MOE_Q4_ERR_UNSUPPORTED;
+  if (fmt < 0 || K % grp || L > MOE_Q4_LINEAR_MAX_L || N > MOE_Q4_LINEAR_MAX_N || K > MOE_Q4_LINEAR_MAX_K) return MOE_Q4_ERR_UNSUPPORTED;
   return MOE_Q4_OK;
 }
 
@@ -79,7 +79,7 @@ extern "C" int moe_linear_codec_forward(int codec, const void* x, int x_dtype, l
                                                      {bias, bias ? (size_t)N * 4 : 0}, {workspace, need}};
   const size_t on = span(L, ldo, N, os);
   for (const auto& in : ins)
-    if (overlap(out, on, in.p, in.n)) return MOE_Q4_ERR_ALIAS;
+    if (overlap(out, on, in.p, in.n) || (&in != &ins[5] && overlap(workspace, need, in.p, in.n))) return MOE_Q4_ERR_ALIAS;
   const LinearArgs a{static_cast<const uint16_t*>(x), w, static_cast<const unsigned char*>(s),
                affine ? static_cast<const unsigned char*>(b) : nullptr, bias, out, ldx, ldo, L, N, K, out_dtype, nullptr, 0};
   const bool f16 = x_dtype == MOE_Q4_DTYPE_F16;

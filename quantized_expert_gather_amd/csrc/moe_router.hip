@@ -444,7 +444,7 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : kTopkThreads) void k_router_topk_b
 
 int check_router(int dtype, long long ld, int T, int k, int E, int score, int norm) {
   if (T < 0 || k < 1 || E < 1 || k > E || ld < E) return MOE_Q4_ERR_SHAPE;
-  if (E > MOE_Q4_MAX_E || k > MOE_Q4_ROUTER_MAX_K) return MOE_Q4_ERR_UNSUPPORTED;
+  if (E > MOE_Q4_MAX_E || k > MOE_Q4_ROUTER_MAX_K || T > MOE_Q4_ROUTER_MAX_T) return MOE_Q4_ERR_UNSUPPORTED;
   if (dtype != MOE_Q4_DTYPE_BF16 && dtype != MOE_Q4_DTYPE_F32 && dtype != MOE_Q4_DTYPE_F16) return MOE_Q4_ERR_UNSUPPORTED;
   if (score != MOE_Q4_SCORE_SOFTMAX && score != MOE_Q4_SCORE_SIGMOID) return MOE_Q4_ERR_UNSUPPORTED;
   if (norm != 0 && norm != 1) return MOE_Q4_ERR_UNSUPPORTED;

@@ -6,7 +6,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, matrix, new, stream_handle
+from ._args import DTYPES, array, call, current_handle, matrix, new, on_stream
 
 _X = (torch.bfloat16, torch.float16)
 _CODES = (torch.int32, getattr(torch, "uint32", torch.int32))
@@ -23,7 +23,7 @@ def moe_linear_codec_workspace_bytes(codec, L: int, N: int, K: int) -> int:
 
 
 def _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace):
-    """Checked arguments of a call up to the stream, out, and the tensors made here."""
+    """Checked arguments of a call up to the stream, out, and the workspace made here."""
     spec = _SPECS.get(codec)
     if spec is None:
         raise ValueError(f"codec {codec!r} has no 4-bit dense product")
@@ -44,12 +44,11 @@ def _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace):
     sp = array(s, scale_type, rows, "s", dev)
     bp = array(b, torch.bfloat16, rows, "b", dev) if affine else 0
     ap = 0 if bias is None else array(bias, torch.float32, (N,), "bias", dev)
-    made = None
     if out is None:
         od = x.dtype if out_dtype is None else out_dtype
         if od not in DTYPES:
             raise TypeError(f"out_dtype {od} is not one of {tuple(DTYPES)}")
-        out = made = new((L, N), (N, 1), od, dev)
+        out = new((L, N), (N, 1), od, dev)
         op, ldo = out.data_ptr(), N
     else:
         op, ldo = matrix(out, DTYPES, "out")
@@ -66,7 +65,7 @@ def _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace):
         scratch = new((need,), (1,), torch.uint8, dev)
         wsp, wsn = scratch.data_ptr(), need
     args = (code, xp, DTYPES[x.dtype], ldx, wp, sp, bp, ap, L, N, K, op, DTYPES[od], ldo, wsp, wsn)
-    return args, out, (made, scratch)
+    return args, out, scratch
 
 
 def moe_linear_codec_forward(codec, x, w, s, b=None, bias=None, out=None, out_dtype=None, workspace=None,
@@ -77,10 +76,15 @@ def moe_linear_codec_forward(codec, x, w, s, b=None, bias=None, out=None, out_dt
     x bf16 or fp16 [L, K] (contiguous rows; row stride a multiple of 8);
     w int32 (uint32 bits) [N, K/8]; s [N, K/group] bf16 (affine codecs) or
     uint8; b bf16 [N, K/group] (affine codecs only); bias fp32 [N].  Returns
-    out [L, N] in ``out_dtype`` (bf16, fp16 or fp32; x's type if not given).
+    out [L, N] in ``out_dtype`` (bf16, fp16 or fp32; x's type if not given),
+    with no gradient.  ``stream`` (a torch stream or a HIP handle) is as
+    ``with torch.cuda.stream(stream)`` around the call.
     """
-    args, out, made = _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace)
-    st = call(_q.lib().moe_linear_codec_forward, args, x.device, stream, made)
+    if stream is not None and isinstance(x, torch.Tensor):
+        with on_stream(stream, x):
+            return moe_linear_codec_forward(codec, x, w, s, b, bias, out, out_dtype, workspace)
+    args, out, _scratch = _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace)
+    st = call(_q.lib().moe_linear_codec_forward, args, x.device, current_handle(x.device))
     if st:
         raise _q.MoeQ4Error(st, "moe_linear_codec_forward")
     return out
@@ -95,19 +99,22 @@ class PreparedLinear:
     of their own (each makes its own if none is given)."""
 
     def __init__(self, codec, x, w, s, b=None, bias=None, out=None, out_dtype=None, workspace=None, stream=None):
-        args, out, made = _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace)
+        if stream is not None and isinstance(x, torch.Tensor):
+            with on_stream(stream, x):
+                args, out, scratch = _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace)
+                handle = current_handle(x.device)
+        else:
+            args, out, scratch = _linear_args(codec, x, w, s, b, bias, out, out_dtype, workspace)
+            handle = current_handle(x.device)
         self.out = out
-        self._keep = (x, w, s, b, bias, workspace, made, stream)
-        self._args = (*args, stream_handle(stream, x.device))
+        self._keep = (x, w, s, b, bias, workspace, scratch, stream)
+        self._args = args
+        self._handle = handle
         self._fn = _q.lib().moe_linear_codec_forward
         self._device = x.device
 
     def __call__(self) -> torch.Tensor:
-        if torch._C._cuda_getDevice() == self._device.index:
-            st = self._fn(*self._args)
-        else:
-            with torch.cuda.device(self._device):
-                st = self._fn(*self._args)
+        st = call(self._fn, self._args, self._device, self._handle)
         if st:
             raise _q.MoeQ4Error(st, "moe_linear_codec_forward")
         return self.out

@@ -9,7 +9,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, matrix, new
+from ._args import DTYPES, array, call, current_handle, matrix, new, on_stream
 
 
 def _score(score) -> int:
@@ -21,19 +21,25 @@ def _score(score) -> int:
     return int(score)
 
 
+def _not_captured(name):
+    # torch's accumulation of a captured gradient into a leaf that an eager graph still holds ends the process
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError(f"backward() of a graph-captured step: call {name} itself")
+
+
 def _gradient(logits, dlogits):
-    """(tensor, pointer, row stride, tensor if it was made here) of a gradient like `logits`."""
+    """(tensor, pointer, row stride) of a gradient like `logits`."""
     if dlogits is None:
         E = logits.shape[1]
         d = new(logits.shape, (E, 1), logits.dtype, logits.device)
-        return d, d.data_ptr(), E, d
+        return d, d.data_ptr(), E
     p, ldd = matrix(dlogits, (logits.dtype,), "dlogits")
     if dlogits.shape != logits.shape or dlogits.device != logits.device:
         raise ValueError("dlogits must have the shape and device of logits")
-    return dlogits, p, ldd, None
+    return dlogits, p, ldd
 
 
-def _topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weights, stream):
+def _topk(logits, k, select_bias, score, renormalize, scale, topk_ids=None, topk_weights=None):
     zp, ld = matrix(logits, DTYPES, "logits")
     T, E = logits.shape
     dev = logits.device
@@ -41,19 +47,18 @@ def _topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weig
     if not 1 <= k <= E:
         raise _q.MoeQ4Error(_q.MOE_Q4_ERR_SHAPE, "moe_router_topk")
     bp = 0 if select_bias is None else array(select_bias, torch.float32, (E,), "select_bias", dev)
-    made_i = made_w = None
     if topk_ids is None:
-        topk_ids = made_i = new((T, k), (k, 1), torch.int32, dev)
+        topk_ids = new((T, k), (k, 1), torch.int32, dev)
         ip = topk_ids.data_ptr()
     else:
         ip = array(topk_ids, torch.int32, (T, k), "topk_ids", dev)
     if topk_weights is None:
-        topk_weights = made_w = new((T, k), (k, 1), torch.float32, dev)
+        topk_weights = new((T, k), (k, 1), torch.float32, dev)
         wp = topk_weights.data_ptr()
     else:
         wp = array(topk_weights, torch.float32, (T, k), "topk_weights", dev)
     args = (zp, DTYPES[logits.dtype], ld, bp, T, k, E, _score(score), 1 if renormalize else 0, scale, ip, wp)
-    st = call(_q.lib().moe_router_topk, args, dev, stream, (made_i, made_w))
+    st = call(_q.lib().moe_router_topk, args, dev, current_handle(dev))
     if st:
         raise _q.MoeQ4Error(st, "moe_router_topk")
     return topk_ids, topk_weights
@@ -62,7 +67,7 @@ def _topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weig
 class _TopkFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, k, select_bias, score, renormalize, scale):
-        ids, w = _topk(logits, k, select_bias, score, renormalize, scale, None, None, None)
+        ids, w = _topk(logits, k, select_bias, score, renormalize, scale)
         ctx.mark_non_differentiable(ids)
         ctx.save_for_backward(logits, ids)
         ctx.how = (score, renormalize, scale)
@@ -71,6 +76,7 @@ class _TopkFunction(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, _dids, dweights):
+        _not_captured("moe_router_topk_backward")
         logits, ids = ctx.saved_tensors
         score, renormalize, scale = ctx.how
         dz = moe_router_topk_backward(logits, ids, dweights.float().contiguous(), score=score, renormalize=renormalize,
@@ -88,18 +94,26 @@ def moe_router_topk(logits, k: int, select_bias=None, score="softmax", renormali
 
     The weights carry a gradient to logits where logits requires one and no
     output tensors or stream are given; a step recorded into a graph calls
-    :func:`moe_router_topk_backward` itself.
+    :func:`moe_router_topk_backward` itself (backward() refuses there).
+    ``stream`` (a torch stream or a HIP handle) is as ``with
+    torch.cuda.stream(stream)`` around the call.
     """
     if topk_ids is None and topk_weights is None and stream is None and isinstance(logits, torch.Tensor) and \
             logits.requires_grad and torch.is_grad_enabled():
         return _TopkFunction.apply(logits, k, select_bias, score, renormalize, scale)
-    return _topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weights, stream)
+    if stream is not None and isinstance(logits, torch.Tensor):
+        with on_stream(stream, logits):
+            return _topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weights)
+    return _topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weights)
 
 
 def moe_router_topk_backward(logits, topk_ids, dweights, score="softmax", renormalize: bool = True, scale: float = 1.0,
                              dlogits=None, stream=None) -> torch.Tensor:
     """Gradient of :func:`moe_router_topk`'s weights with respect to logits, the
     choice held fixed: dweights fp32 [T, k] -> dlogits [T, E] in logits' type."""
+    if stream is not None and isinstance(logits, torch.Tensor):
+        with on_stream(stream, logits):
+            return moe_router_topk_backward(logits, topk_ids, dweights, score, renormalize, scale, dlogits)
     zp, ld = matrix(logits, DTYPES, "logits")
     T, E = logits.shape
     dev = logits.device
@@ -108,9 +122,9 @@ def moe_router_topk_backward(logits, topk_ids, dweights, score="softmax", renorm
     k = topk_ids.shape[1]
     ip = array(topk_ids, torch.int32, (T, k), "topk_ids", dev)
     gp = array(dweights, torch.float32, (T, k), "dweights", dev)
-    d, dp, ldd, made = _gradient(logits, dlogits)
+    d, dp, ldd = _gradient(logits, dlogits)
     args = (zp, DTYPES[logits.dtype], ld, ip, gp, T, k, E, _score(score), 1 if renormalize else 0, scale, dp, ldd)
-    st = call(_q.lib().moe_router_topk_backward, args, dev, stream, (made,))
+    st = call(_q.lib().moe_router_topk_backward, args, dev, current_handle(dev))
     if st:
         raise _q.MoeQ4Error(st, "moe_router_topk_backward")
     return d
@@ -135,7 +149,7 @@ def _mask_ptr(token_mask, rows, device):
     return array(token_mask, (torch.bool, torch.uint8), (rows,), "token_mask", device)
 
 
-def _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace, stream):
+def _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace):
     zp, ld = matrix(logits, DTYPES, "logits")
     rows, E = logits.shape
     dev = logits.device
@@ -158,7 +172,7 @@ def _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace, stream)
         wsp = array(workspace, torch.uint8, (wsn,), "workspace", dev)
     args = (zp, DTYPES[logits.dtype], ld, ip, mp, S, T, k, E, _score(score), coef, loss.data_ptr(), counts.data_ptr(),
             tokens.data_ptr(), wsp, wsn)
-    st = call(lib.moe_balance_loss, args, dev, stream, (loss, counts, tokens, scratch))
+    st = call(lib.moe_balance_loss, args, dev, current_handle(dev))
     if st:
         raise _q.MoeQ4Error(st, "moe_balance_loss")
     return loss, counts, tokens
@@ -167,7 +181,7 @@ def _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace, stream)
 class _BalanceFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, topk_ids, coef, score, seqs, token_mask, workspace):
-        loss, counts, tokens = _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace, None)
+        loss, counts, tokens = _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace)
         ctx.mark_non_differentiable(counts, tokens)
         ctx.save_for_backward(logits, counts, tokens, token_mask)
         ctx.how = (topk_ids.shape[1], coef, score)
@@ -176,6 +190,7 @@ class _BalanceFunction(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dloss, _dcounts, _dtokens):
+        _not_captured("moe_balance_loss_backward")
         logits, counts, tokens, token_mask = ctx.saved_tensors
         k, coef, score = ctx.how
         dz = moe_balance_loss_backward(logits, counts, tokens, dloss.float().contiguous(), k, coef=coef, score=score,
@@ -193,17 +208,23 @@ def moe_balance_loss(logits, topk_ids, coef: float = 1.0, score="softmax", seqs:
     Returns (loss fp32 [seqs], counts int32 [seqs, E], tokens int32 [seqs]).
     The loss carries a gradient to logits where logits requires one and no
     stream is given; a step recorded into a graph calls
-    :func:`moe_balance_loss_backward` itself.
+    :func:`moe_balance_loss_backward` itself (backward() refuses there).
     """
     if stream is None and isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
         return _BalanceFunction.apply(logits, topk_ids, coef, score, seqs, token_mask, workspace)
-    return _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace, stream)
+    if stream is not None and isinstance(logits, torch.Tensor):
+        with on_stream(stream, logits):
+            return _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace)
+    return _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace)
 
 
 def moe_balance_loss_backward(logits, counts, tokens, dloss, k: int, coef: float = 1.0, score="softmax",
                               token_mask=None, dlogits=None, stream=None) -> torch.Tensor:
     """Gradient of :func:`moe_balance_loss`, the counts held fixed: dloss fp32
     [seqs] and the forward's counts and tokens -> dlogits in logits' type."""
+    if stream is not None and isinstance(logits, torch.Tensor):
+        with on_stream(stream, logits):
+            return moe_balance_loss_backward(logits, counts, tokens, dloss, k, coef, score, token_mask, dlogits)
     zp, ld = matrix(logits, DTYPES, "logits")
     rows, E = logits.shape
     dev = logits.device
@@ -214,9 +235,9 @@ def moe_balance_loss_backward(logits, counts, tokens, dloss, k: int, coef: float
     np_ = array(tokens, torch.int32, (S,), "tokens", dev)
     gp = array(dloss, torch.float32, (S,), "dloss", dev)
     mp = _mask_ptr(token_mask, rows, dev)
-    d, dp, ldd, made = _gradient(logits, dlogits)
+    d, dp, ldd = _gradient(logits, dlogits)
     args = (zp, DTYPES[logits.dtype], ld, mp, cp, np_, gp, S, T, int(k), E, _score(score), coef, dp, ldd)
-    st = call(_q.lib().moe_balance_loss_backward, args, dev, stream, (made,))
+    st = call(_q.lib().moe_balance_loss_backward, args, dev, current_handle(dev))
     if st:
         raise _q.MoeQ4Error(st, "moe_balance_loss_backward")
     return d

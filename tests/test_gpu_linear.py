@@ -217,6 +217,49 @@ def test_other_streams(L):
     assert all(torch.equal(o, ref) for o in outs)
 
 
+@pytest.mark.parametrize("L", [2, 40])
+def test_a_streams_outputs_share_no_memory_with_pending_work(L):
+    x, w, s, b, _ = problem("affine4_g64", L, 300, 512, BF16, False)
+    a = [t.cuda() for t in (x, w[0], s[0], b[0])]
+    ref = q.moe_linear_codec_forward("affine4_g64", *a)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for make in (lambda: q.moe_linear_codec_forward("affine4_g64", *a, stream=side),
+                 lambda: q.PreparedLinear("affine4_g64", *a, stream=side)()):
+        old = [torch.empty_like(ref) for _ in range(4)]
+        torch.cuda._sleep(20_000_000)
+        for t in old:
+            t.fill_(float("nan"))  # still to come when the call below is made
+        del old, t
+        out = make()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+
+
+def test_a_stream_of_another_device_is_refused():
+    x, w, s, b, _ = problem("mxfp4", 1, 16, 128, BF16, False)
+
+    class Elsewhere(torch.cuda.Stream):
+        device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="stream"):
+        q.moe_linear_codec_forward("mxfp4", x.cuda(), w[0].cuda(), s[0].cuda(), stream=Elsewhere())
+
+
+@pytest.mark.parametrize("codec", CODECS)
+@pytest.mark.parametrize("L", [3, 12, 40, 200])
+def test_infinite_activations_reach_their_token_only(codec, L):
+    x, w, s, b, _ = problem(codec, L, 40, 256, BF16, False)
+    x[1, 30] = float("inf")
+    x[2, 200] = float("-inf")
+    a = [t.cuda() for t in (w[0], s[0])] + [b[0].cuda() if b is not None else None]
+    out = q.moe_linear_codec_forward(codec, x.cuda(), *a)
+    bad = ~torch.isfinite(out).any(1)
+    assert bad.nonzero().flatten().tolist() == [1, 2]
+    x[1:3] = 0
+    keep = [t for t in range(L) if t not in (1, 2)]
+    assert torch.equal(out[keep], q.moe_linear_codec_forward(codec, x.cuda(), *a)[keep])
+
+
 @pytest.mark.parametrize("L", [1, 48, 260])
 def test_replays_in_graphs(L):
     x, w, s, b, _ = problem("affine4_g64", L, 200, 1024, BF16, False)

@@ -325,6 +325,18 @@ def test_autograd(score):
     assert (wd.grad.cpu().double() - w64.grad).abs().max() <= 2e-5 * w64.grad.abs().max()
 
 
+def test_backward_of_a_captured_step_is_refused(monkeypatch):
+    z = logits(8, 16, F32).cuda().requires_grad_()
+    ids, w = q.moe_router_topk(z, 2)
+    loss, _, _ = q.moe_balance_loss(z, ids)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="moe_router_topk_backward"):
+        w.sum().backward()
+    with pytest.raises(RuntimeError, match="moe_balance_loss_backward"):
+        loss.sum().backward()
+    assert z.grad is None
+
+
 def test_autograd_does_not_touch_plain_calls():
     z = logits(4, 8, F32).cuda().requires_grad_()
     with torch.no_grad():

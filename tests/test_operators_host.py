@@ -39,6 +39,10 @@ def linear(codec=0, x=None, xd=0, ldx=None, w=None, s=None, b=None, bias=0, L=2,
     (dict(L=q.MOE_Q4_LINEAR_MAX_L + 1), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(K=q.MOE_Q4_LINEAR_MAX_K + 64), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(ldx=q.MOE_Q4_LINEAR_MAX_LDX + 8), q.MOE_Q4_ERR_UNSUPPORTED),
+    (dict(N=q.MOE_Q4_LINEAR_MAX_N + 1), q.MOE_Q4_ERR_UNSUPPORTED),
+    (dict(L=40, ws=fake(0)), q.MOE_Q4_ERR_ALIAS),
+    (dict(L=40, ws=fake(2)), q.MOE_Q4_ERR_ALIAS),
+    (dict(L=40, ws=fake(4, 256), bias=fake(4, 512)), q.MOE_Q4_ERR_ALIAS),
     (dict(x=0), q.MOE_Q4_ERR_NULL),
     (dict(w=0), q.MOE_Q4_ERR_NULL),
     (dict(s=0), q.MOE_Q4_ERR_NULL),
@@ -99,6 +103,7 @@ def topk(z=None, dt=1, ld=None, bias=0, T=4, k=3, E=10, score=0, norm=1, ids=Non
     (dict(dt=3), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(score=2), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(norm=2), q.MOE_Q4_ERR_UNSUPPORTED),
+    (dict(T=q.MOE_Q4_ROUTER_MAX_T + 1, E=1, k=1), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(z=0), q.MOE_Q4_ERR_NULL),
     (dict(ids=0), q.MOE_Q4_ERR_NULL),
     (dict(w=0), q.MOE_Q4_ERR_NULL),
@@ -126,6 +131,7 @@ def topk_back(z=None, dt=1, ld=None, T=4, k=3, E=10, score=0, norm=1, ids=None, 
     (dict(T=-1), q.MOE_Q4_ERR_SHAPE), (dict(k=0), q.MOE_Q4_ERR_SHAPE), (dict(ldd=9), q.MOE_Q4_ERR_SHAPE),
     (dict(ld=9), q.MOE_Q4_ERR_SHAPE), (dict(k=65, E=70), q.MOE_Q4_ERR_UNSUPPORTED), (dict(dt=9), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(g=0), q.MOE_Q4_ERR_NULL), (dict(d=0), q.MOE_Q4_ERR_NULL), (dict(d=fake(4, 2)), q.MOE_Q4_ERR_ALIGN),
+    (dict(T=q.MOE_Q4_ROUTER_MAX_T + 1, k=1), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(d=fake(0)), q.MOE_Q4_ERR_ALIAS), (dict(d=fake(3, 44)), q.MOE_Q4_ERR_ALIAS), (dict(d=fake(2)), q.MOE_Q4_ERR_ALIAS),
     (dict(T=0), q.MOE_Q4_OK),
 ])
@@ -149,7 +155,9 @@ def balance(z=None, dt=1, ld=None, ids=None, mask=0, S=2, T=5, k=2, E=8, score=0
     (dict(ws=0), q.MOE_Q4_ERR_WORKSPACE), (dict(wn=64), q.MOE_Q4_ERR_WORKSPACE), (dict(ws=fake(6, 128)), q.MOE_Q4_ERR_ALIGN),
     (dict(z=fake(0, 2)), q.MOE_Q4_ERR_ALIGN), (dict(counts=fake(0, 64)), q.MOE_Q4_ERR_ALIAS),
     (dict(loss=fake(6)), q.MOE_Q4_ERR_ALIAS), (dict(tokens=fake(4, 60)), q.MOE_Q4_ERR_ALIAS),
-    (dict(mask=fake(2), loss=fake(2, 8)), q.MOE_Q4_ERR_ALIAS), (dict(S=0), q.MOE_Q4_OK),
+    (dict(mask=fake(2), loss=fake(2, 8)), q.MOE_Q4_ERR_ALIAS),
+    (dict(T=q.MOE_Q4_ROUTER_MAX_T + 1), q.MOE_Q4_ERR_UNSUPPORTED), (dict(ws=fake(0)), q.MOE_Q4_ERR_ALIAS),
+    (dict(ws=fake(1)), q.MOE_Q4_ERR_ALIAS), (dict(ws=fake(2), mask=fake(2, 8)), q.MOE_Q4_ERR_ALIAS), (dict(S=0), q.MOE_Q4_OK),
 ])
 def test_balance_refusals(kw, status):
     assert balance(**kw) == status
@@ -170,6 +178,15 @@ def balance_back(z=None, dt=1, ld=None, mask=0, counts=None, tokens=None, g=None
 ])
 def test_balance_backward_refusals(kw, status):
     assert balance_back(**kw) == status
+
+
+def test_tile_plans_keep_their_sums_small():
+    # (nvfp4 needs room for nothing but the sums of a split K: 16 at most)
+    for L in (17, 33, 65, 129, 300, 1000, 5000):
+        for N in (1, 63, 64, 500, 4096, 20000):
+            for K in (32, 128, 160, 2048, 14336):
+                n = q.moe_linear_codec_workspace_bytes("nvfp4", L, N, K)
+                assert n % 256 == 0 and n <= 16 * L * N * 4 + 256, (L, N, K)
 
 
 def test_balance_workspace_grows_with_experts():
