@@ -352,8 +352,7 @@ int moe_sort_pairs(const int32_t *topk_ids, int L, int k, int E, int bm, int32_t
  *   s          [N, K/gs] scales: bf16 (affine; 2-byte aligned), uint8 E8M0
  *              (mxfp4) or uint8 E4M3 (nvfp4; 2-byte aligned)
  *   b          bf16 [N, K/gs] biases of the affine codecs (2-byte aligned);
- *              ignored otherwise.  With L <= 16 and K > 2048 a multiple of 128, s
- *              and b must be 4-byte aligned
+ *              ignored otherwise
  *   bias       fp32 [N], or NULL
  *   L, N, K    tokens, outputs, inputs; K a multiple of 64 for AFFINE4_G64, of
  *              32 otherwise; L and N are any

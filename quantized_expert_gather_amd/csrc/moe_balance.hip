@@ -42,7 +42,7 @@ struct BalanceArgs {
   int32_t* counts;
   int32_t* tokens;
   long long ld;
-  int S, T, k, E, score, vec;
+  int S, T, k, E, score;
   int blocks, per;  // workgroups of a sequence, tokens of each
   int chunks;
   float coef;
@@ -93,6 +93,13 @@ __device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&da
   for (int r = 0; r < R; ++r) inv[r] = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];
 }
 
+// dot = sum_e c_e sum_t p[t, e]
+__device__ __forceinline__ void store_loss(const BalanceArgs& a, int seq, int n, float dot) {
+  const float nf = (float)n;
+  a.tokens[seq] = n;
+  a.loss[seq] = n ? a.coef * (float)a.E / ((float)a.k * nf) * (dot / nf) : 0.0f;
+}
+
 template <class LT, int EPL, int LPR>
 __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceArgs a) {
   typedef typename LT::mem mem;
@@ -113,8 +120,7 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
   auto load = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      load_row<LT, EPL, LPR>(static_cast<const mem*>(a.z) + (seq + min(t + r * kGroups + group, t1 - 1)) * a.ld, slot, a.E, a.vec,
-                             -__builtin_inff(), next[r]);
+      load_row<LT, EPL, LPR>(static_cast<const mem*>(a.z) + (seq + min(t + r * kGroups + group, t1 - 1)) * a.ld, slot, a.E, -__builtin_inff(), next[r]);
   };
   if (t0 < t1) load(t0);
   for (int e = tid; e < a.E; e += nthr) hist[e] = 0;
@@ -156,7 +162,19 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
       }
   }
 
-  const size_t part = ((size_t)blockIdx.y * a.blocks + blockIdx.x) * a.E;
+  // few tokens: one workgroup finishes by itself
+  const bool alone = a.blocks == 1;
+  float dot = 0.0f;
+  auto leave = [&](int e, float s) __attribute__((always_inline)) {
+    if (alone) {
+      a.counts[(size_t)blockIdx.y * a.E + e] = hist[e];
+      dot += (float)hist[e] * s;
+    } else {
+      const size_t part = ((size_t)blockIdx.y * a.blocks + blockIdx.x) * a.E;
+      a.psum[part + e] = s;
+      a.pcount[part + e] = hist[e];
+    }
+  };
   if constexpr (LPR <= 64) {
     // a wave's rows, then the waves', in a fixed order
 #pragma unroll
@@ -183,19 +201,20 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
       float s = sums[e];
 #pragma unroll
       for (int w = 1; w < kPartialWaves; ++w) s += sums[w * kWide + e];
-      a.psum[part + e] = s;
-      a.pcount[part + e] = hist[e];
+      leave(e, s);
     }
   } else {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const int e = row_expert<LT, EPL, LPR>(slot, i);
-      if (e < a.E) a.psum[part + e] = acc[i];
+      if (e < a.E) leave(e, acc[i]);
     }
-    for (int e = tid; e < a.E; e += nthr) a.pcount[part + e] = hist[e];
   }
-  if (tid == 0) {
+  if (alone) {
+    dot = row_all<1024>(dot, OpSumF(), red);
+    if (tid == 0) store_loss(a, blockIdx.y, ntok[0], dot);
+  } else if (tid == 0) {
     a.ptok[(size_t)blockIdx.y * a.blocks + blockIdx.x] = ntok[0];
     if (blockIdx.x == 0) a.ticket[blockIdx.y] = 0;
   }
@@ -254,9 +273,7 @@ __global__ __launch_bounds__(1024) void k_balance_finish(BalanceArgs a) {
     dot = 0.0f;
     for (int q = 0; q < a.chunks; ++q) dot += __hip_atomic_load(dots + q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  a.tokens[seq] = n;
-  const float nf = (float)n;
-  a.loss[seq] = n ? a.coef * (float)a.E / ((float)a.k * nf) * (dot / nf) : 0.0f;
+  store_loss(a, seq, n, dot);
 }
 
 struct BalanceBackArgs {
@@ -267,7 +284,7 @@ struct BalanceBackArgs {
   const float* dloss;
   void* dz;
   long long ld, ldd;
-  int S, T, k, E, score, vec, vecd;
+  int S, T, k, E, score;
   int per;
   float coef;
 };
@@ -285,8 +302,7 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : 64 * kBackWaves) void k_balance_ba
   auto load = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      load_row<LT, EPL, LPR>(static_cast<const mem*>(a.z) + (seq + min(t + r * kGroups + group, t1 - 1)) * a.ld, slot, a.E, a.vec,
-                             -__builtin_inff(), next[r]);
+      load_row<LT, EPL, LPR>(static_cast<const mem*>(a.z) + (seq + min(t + r * kGroups + group, t1 - 1)) * a.ld, slot, a.E, -__builtin_inff(), next[r]);
   };
   load(t0);
   const float n = (float)a.tokens[blockIdx.y];
@@ -332,15 +348,18 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : 64 * kBackWaves) void k_balance_ba
       const bool live = !(a.mask && !a.mask[seq + tr]);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) v[r][i] = live ? v[r][i] * (w[i] - dot[r]) : 0.0f;
-      store_row<LT, EPL, LPR>(static_cast<mem*>(a.dz) + (seq + tr) * a.ldd, slot, a.E, a.vecd, v[r]);
+      store_row<LT, EPL, LPR>(static_cast<mem*>(a.dz) + (seq + tr) * a.ldd, slot, a.E, v[r]);
     }
   }
 }
 
-// Tokens of a workgroup: enough workgroups to fill the card, few enough that
-// the second launch has little to add.
+// Workgroups of a sequence: enough of them to fill the card; one, which
+// needs no second launch, where a sequence has few values (512 x 64 fp32:
+// 7.5 us, against 9.2 with two launches; 1000 x 64: 12.3 against 8.7).
 constexpr int kMaxBlocks = 256;
+constexpr long kAloneValues = 32768;
 int blocks_of(int S, int T, int E) {
+  if ((long)T * std::max(E, 64) <= kAloneValues) return 1;
   const int rows = E > 1024 ? 1 : kPartialWaves;
   const int want = std::max(1, kMaxBlocks / std::max(1, S));
   return std::max(1, std::min(want, (T + rows - 1) / rows));
@@ -434,7 +453,6 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, long long 
   a.ld = ld;
   a.S = S; a.T = T; a.k = k; a.E = E;
   a.score = score;
-  a.vec = row_vec(logits, ld, E, plan.epl, (int)es);
   a.blocks = blocks_of(S, T, E);
   a.per = (T + a.blocks - 1) / a.blocks;
   a.coef = coef;
@@ -443,7 +461,7 @@ extern "C" int moe_balance_loss(const void* logits, int logits_dtype, long long 
 #define MOE_BALANCE_CALL(LT, EPL, LPR) hipLaunchKernelGGL((k_balance_partial<LT, EPL, LPR>), grid, block, lds, stream, a)
   MOE_ROW_DISPATCH(logits_dtype, plan, MOE_BALANCE_CALL)
   if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
-  hipLaunchKernelGGL(k_balance_finish, dim3(a.chunks, S), dim3(1024), 0, stream, a);
+  if (a.blocks > 1) hipLaunchKernelGGL(k_balance_finish, dim3(a.chunks, S), dim3(1024), 0, stream, a);
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }
 
@@ -466,9 +484,7 @@ extern "C" int moe_balance_loss_backward(const void* logits, int logits_dtype, l
       overlap(dlogits, out, dloss, (size_t)S * 4))
     return MOE_Q4_ERR_ALIAS;
   const RowPlan plan = row_plan(E, 1, false);
-  BalanceBackArgs a{logits, token_mask, counts, tokens, dloss, dlogits, ld, ldd, S, T, k, E, score, 0, 0, 0, coef};
-  a.vec = row_vec(logits, ld, E, plan.epl, (int)es);
-  a.vecd = row_vec(dlogits, ldd, E, plan.epl, (int)es);
+  BalanceBackArgs a{logits, token_mask, counts, tokens, dloss, dlogits, ld, ldd, S, T, k, E, score, 0, coef};
   // a workgroup's rows at a time, and few enough workgroups that each goes round a few times
   const int threads = plan.lpr > 64 ? plan.lpr : 64 * kBackWaves;
   const int unit = threads / plan.lpr * (plan.lpr > 64 ? 1 : plan.epl == 4 ? 4 : plan.epl == 8 ? 2 : 1);

@@ -67,9 +67,6 @@ extern "C" int moe_linear_codec_forward(int codec, const void* x, int x_dtype, l
   if (!aligned_to(x, 16) || (L > 1 && ldx % 8) || !aligned_to(w, 16) || !aligned_to(s, sa) || (affine && !aligned_to(b, 2)) ||
       !aligned_to(bias, 4) || !aligned_to(out, os))
     return MOE_Q4_ERR_ALIGN;
-  // rows of whole steps are read by words unless one workgroup takes them whole
-  if (L < kTilesFrom && K % kLinStep == 0 && K > 16 * kLinStep && (!aligned_to(s, 4) || (affine && !aligned_to(b, 4))))
-    return MOE_Q4_ERR_ALIGN;
   const size_t need = moe_linear_codec_workspace_bytes(codec, L, N, K);
   if (need && (!workspace || workspace_bytes < need)) return MOE_Q4_ERR_WORKSPACE;
   if (need && !aligned_to(workspace, 256)) return MOE_Q4_ERR_ALIGN;

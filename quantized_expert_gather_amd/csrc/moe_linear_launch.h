@@ -80,7 +80,7 @@ inline TilesWorkspace tiles_layout(int fmt, int L, int N, int K) {
   w.xsum = off; off = lin_round256(off + (affine ? 3 * (size_t)L * Gp * 2 : 0));
   w.tsum = off; off = lin_round256(off + (affine ? 3 * (size_t)N * Gp * 2 : 0));
   w.xexp = off; off = lin_round256(off + (affine ? (size_t)L * 4 : 0));
-  w.sh = off;   off = lin_round256(off + (affine ? (size_t)N * G * 2 : 0));
+  w.sh = off;   off = lin_round256(off + (affine ? (size_t)N * Gp * 2 : 0));
   w.wexp = off; off = lin_round256(off + (affine || fmt == kLinMxfp4 ? (size_t)N * 4 : 0));
   w.part = off; off = lin_round256(off + (p.splits > 1 ? (size_t)p.splits * L * N * 4 : 0));
   w.total = off;
@@ -139,6 +139,10 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
     q.wexp = reinterpret_cast<int32_t*>(ws + lay.wexp);
     q.ldx = l.ldx;
     q.L = l.L; q.N = l.N; q.K = l.K; q.G = a.G; q.Gp = a.Gp;
+    q.terms = a.terms;
+    q.row_lanes = 4;
+    while (q.row_lanes < 64 && 8 * q.row_lanes < a.G) q.row_lanes *= 2;
+    const int row_blocks = (int)(((size_t)l.N * q.row_lanes + 255) / 256);
     if constexpr (lin_affine(FMT)) {
       q.xq = reinterpret_cast<uint16_t*>(ws + lay.xq);
       q.xsum = reinterpret_cast<uint16_t*>(ws + lay.xsum);
@@ -152,7 +156,7 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
       q.tsum = reinterpret_cast<uint16_t*>(ws + lay.tsum);
       a.tsum = q.tsum;
     }
-    hipLaunchKernelGGL((k_linear_prepare<FMT, F16>), dim3(q.tok_blocks + (l.N + 3) / 4), dim3(256), 0, stream, q);
+    hipLaunchKernelGGL((k_linear_prepare<FMT, F16>), dim3(q.tok_blocks + row_blocks), dim3(256), 0, stream, q);
     if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
   }
   switch (p.mt) {

@@ -58,34 +58,23 @@ struct LinScales {
   static constexpr int kWords = !kOwn && kStep == 8 ? 2 : 1;
 };
 
-// Reads a lane's scales of a step where rows of scales may start at any byte
-// or end inside a step: a short last step is read from its end back (K >= 128)
-// and shifted down, which leaves zeros for what is not there.
-template <int FMT, bool FEW>
-__device__ __forceinline__ void lin_scales_any(const unsigned char* row, int step, int kb, int row_bytes,
-                                               uint32_t (&v)[LinScales<FMT, FEW>::kWords]) {
-  typedef LinScales<FMT, FEW> Sc;
-  if constexpr (Sc::kOwn) {
-    constexpr int kBytes = Sc::kStep / 4;
-    const int at = min(step * Sc::kStep + kb * kBytes, row_bytes - kBytes);
-    if constexpr (kBytes == 1)
-      v[0] = row[at];
-    else
-      v[0] = *reinterpret_cast<const uint16_t*>(row + at);
+// A row's scales of a step where rows of scales may start at any byte or end
+// inside a step: a short last step is read from its end back (K >= 128) and
+// shifted down, which leaves zeros for what is not there.
+template <int WORDS>
+__device__ __forceinline__ void lin_scales_any(const unsigned char* row, int step, int row_bytes, uint32_t (&v)[WORDS]) {
+  const int last = row_bytes - 4 * WORDS, at = min(step * 4 * WORDS, last);
+  const int shift = 8 * (step * 4 * WORDS - at);
+  if constexpr (WORDS == 1) {
+    uint32_t u;
+    __builtin_memcpy(&u, row + at, 4);
+    v[0] = shift > 31 ? 0u : u >> shift;
   } else {
-    const int last = row_bytes - Sc::kStep, at = min(step * Sc::kStep, last);
-    const int shift = 8 * (step * Sc::kStep - at);
-    if constexpr (Sc::kStep == 4) {
-      uint32_t u;
-      __builtin_memcpy(&u, row + at, 4);
-      v[0] = shift > 31 ? 0u : u >> shift;
-    } else {
-      uint64_t u;
-      __builtin_memcpy(&u, row + at, 8);
-      u = shift > 63 ? 0u : u >> shift;
-      v[0] = (uint32_t)u;
-      v[1] = (uint32_t)(u >> 32);
-    }
+    uint64_t u;
+    __builtin_memcpy(&u, row + at, 8);
+    u = shift > 63 ? 0u : u >> shift;
+    v[0] = (uint32_t)u;
+    v[1] = (uint32_t)(u >> 32);
   }
 }
 
@@ -118,7 +107,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
   // Scales: one load a tile, lane (n, kb) taking those of row n and step kb
   // (every load of 16 rows' few bytes costs as much as one of their codes);
   // row moves spread them when they are used.
-  constexpr int kRec = PLAIN ? Sc::kStep / 4 : Sc::kWords;
+  constexpr int kRec = Sc::kStep / 4;
   struct Rows {  // 16 rows, as loaded
     lin_u32x4 c[S];
     uint32_t s[kRec], b[kAffine ? kRec : 1];
@@ -152,8 +141,9 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
       if constexpr (kAffine) get(br, r.b);
     } else {
       const size_t row = min(tile * 16 + n16, a.N - 1);
-      lin_scales_any<FMT, FEW>(a.s + row * srow, first, kb, srow, r.s);
-      if constexpr (kAffine) lin_scales_any<FMT, FEW>(a.b + row * srow, first, kb, srow, r.b);
+      const int step = first + min(kb, S - 1);
+      lin_scales_any<kRec>(a.s + row * srow, step, srow, r.s);
+      if constexpr (kAffine) lin_scales_any<kRec>(a.b + row * srow, step, srow, r.b);
     }
   };
 
@@ -257,13 +247,13 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
 #pragma unroll
       for (int w = 0; w < kRec; ++w) {
         uint32_t one[S];
-        lin_spread<PLAIN ? S : 1>(rec[w], one);
+        lin_spread<S>(rec[w], one);
 #pragma unroll
         for (int st = 0; st < S; ++st) u[st][w] = one[st];
       }
 #pragma unroll
       for (int st = 0; st < S; ++st) {
-        if constexpr (!PLAIN || !Sc::kOwn) {
+        if constexpr (!Sc::kOwn) {
 #pragma unroll
           for (int w = 0; w < Sc::kWords; ++w) v[st][w] = u[st][w];
         } else if constexpr (kRec == 1) {
@@ -398,14 +388,15 @@ struct RowsPlan {
   int W, S, splits, split_steps;
   bool plain;
 };
-// The longest K of one workgroup is 16 waves x 3 steps (2 where x takes two
-// operands); longer ones are split evenly.
+// As many waves as there are steps, up to 16; the longest K of one workgroup
+// is 16 waves x 3 steps (2 where x takes two operands), longer ones are split
+// evenly.  (10 x 54483 x 320 takes 9.4 us with 4 waves, 17.6 with 16.)
 inline RowsPlan rows_plan(int fmt, bool f16, int K, bool words) {
   RowsPlan p{};
   p.plain = K % kLinStep == 0 && words;
   const int steps = (K + kLinStep - 1) / kLinStep;
-  const int most = !p.plain ? 1 : fmt == kLinMxfp4 && f16 ? 2 : 3;
-  p.W = p.plain && steps <= 8 ? 8 : 16;
+  const int most = fmt == kLinMxfp4 && f16 ? 2 : 3;
+  p.W = steps <= 4 ? 4 : steps <= 8 && p.plain ? 8 : 16;
   p.splits = (steps + 16 * most - 1) / (16 * most);
   p.split_steps = (steps + p.splits - 1) / p.splits;
   p.splits = (steps + p.split_steps - 1) / p.split_steps;
@@ -418,31 +409,39 @@ void launch_linear_rows(const LinearArgs& args, const RowsPlan& p, hipStream_t s
   LinearArgs a = args;
   a.split_steps = p.split_steps;
   const int tiles = (a.N + 15) / 16;
-  const int most = p.W == 16 ? 256 : 512;  // workgroups that run at once
+  const int most = 4096 / p.W;  // workgroups that run at once
   const int rounds = (int)(((long)tiles * p.splits + most - 1) / most);
   const dim3 grid((tiles + rounds - 1) / rounds, (a.L + 15) / 16, p.splits), block(64 * p.W);
   const bool few = a.L <= 4;
 #define MOE_LINEAR_ROWS(FEW, PLAIN, S, W) \
   hipLaunchKernelGGL((k_linear_rows<FMT, F16, FEW, PLAIN, S, W>), grid, block, 0, stream, a)
-#define MOE_LINEAR_ROWS_S(FEW)                         \
-  if (!p.plain) {                                      \
-    MOE_LINEAR_ROWS(FEW, false, 1, 16);                \
-  } else if (p.W == 8) {                               \
+#define MOE_LINEAR_ROWS_S(FEW, PLAIN)                  \
+  if (p.W == 4) {                                      \
+    MOE_LINEAR_ROWS(FEW, PLAIN, 1, 4);                 \
+  } else if (PLAIN && p.W == 8) {                      \
     MOE_LINEAR_ROWS(FEW, true, 1, 8);                  \
   } else if (p.S == 1) {                               \
-    MOE_LINEAR_ROWS(FEW, true, 1, 16);                 \
+    MOE_LINEAR_ROWS(FEW, PLAIN, 1, 16);                \
   } else if (p.S == 2) {                               \
-    MOE_LINEAR_ROWS(FEW, true, 2, 16);                 \
+    MOE_LINEAR_ROWS(FEW, PLAIN, 2, 16);                \
   } else if constexpr (!(FMT == kLinMxfp4 && F16)) {   \
-    MOE_LINEAR_ROWS(FEW, true, 3, 16);                 \
+    MOE_LINEAR_ROWS(FEW, PLAIN, 3, 16);                \
   }
   if constexpr (FMT != kLinMxfp4) {
     if (few) {
-      MOE_LINEAR_ROWS_S(true)
+      if (p.plain) {
+        MOE_LINEAR_ROWS_S(true, true)
+      } else {
+        MOE_LINEAR_ROWS_S(true, false)
+      }
       return;
     }
   }
-  MOE_LINEAR_ROWS_S(false)
+  if (p.plain) {
+    MOE_LINEAR_ROWS_S(false, true)
+  } else {
+    MOE_LINEAR_ROWS_S(false, false)
+  }
 #undef MOE_LINEAR_ROWS_S
 #undef MOE_LINEAR_ROWS
 }

@@ -35,7 +35,7 @@ struct TilesArgs {
   const uint16_t* x;       // tokens in operand type and order
   const uint32_t* w;
   const unsigned char* s;  // scales as given (nvfp4, mxfp4)
-  const uint16_t* sh;      // affine: fp16 scales over their row's power of two [N][G]
+  const uint16_t* sh;      // affine: fp16 scales over their row's power of two [N][Gp]
   const uint16_t* tsum;    // affine: bf16 terms of b + 8 s [3][N][Gp]
   const uint16_t* xsum;    // affine: bf16 terms of the group sums [3][L][Gp]
   const int32_t* xexp;     // power of two of each token (affine with bf16 tokens), or NULL
@@ -218,14 +218,14 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
     }
   };
   const int rows0 = __builtin_amdgcn_readfirstlane(min(row0, a.N - 1));
-  constexpr int kScaleBytes = lin_affine(FMT) ? 2 : 1;
+  const uint32_t scale_row = lin_affine(FMT) ? 2 * a.Gp : a.G;  // bytes
   const unsigned char* wbase = reinterpret_cast<const unsigned char*>(a.w) + (size_t)rows0 * ((size_t)a.K / 2);
-  const unsigned char* sbase = (lin_affine(FMT) ? reinterpret_cast<const unsigned char*>(a.sh) : a.s) + (size_t)rows0 * a.G * kScaleBytes;
+  const unsigned char* sbase = (lin_affine(FMT) ? reinterpret_cast<const unsigned char*>(a.sh) : a.s) + (size_t)rows0 * scale_row;
   uint32_t woff[NT], soff[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     woff[nt] = (uint32_t)((int)row[nt] - rows0) * (uint32_t)(a.K / 2);
-    soff[nt] = (uint32_t)((int)row[nt] - rows0) * (uint32_t)(a.G * kScaleBytes);
+    soff[nt] = (uint32_t)((int)row[nt] - rows0) * scale_row;
   }
   auto load = [&](int step, lin_u32x4 (&cw)[NT], uint32_t (&sw)[NT]) __attribute__((always_inline)) {
     const int k = min(step * kLinStep + 32 * kb, a.K - 32);
@@ -367,20 +367,20 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
   }
 }
 
-// v as three bf16 terms, hi + mid + lo, at `at` of three planes.
-__device__ __forceinline__ void store_terms(uint16_t* p, size_t at, size_t plane, float v) {
-  const uint32_t hi = f32_to_bf16_rne(v);
-  const float r = v - bf16_lo_to_f32(hi);
-  const uint32_t mid = f32_to_bf16_rne(r);
-  p[at] = (uint16_t)hi;
-  p[at + plane] = (uint16_t)mid;
-  p[at + 2 * plane] = (uint16_t)f32_to_bf16_rne(r - bf16_lo_to_f32(mid));
+// v as bf16 terms, hi + mid + lo.
+__device__ __forceinline__ void split_terms(float v, uint32_t (&t)[3]) {
+  t[0] = f32_to_bf16_rne(v);
+  const float r = v - bf16_lo_to_f32(t[0]);
+  t[1] = f32_to_bf16_rne(r);
+  t[2] = f32_to_bf16_rne(r - bf16_lo_to_f32(t[1]));
 }
 
 // Lays out what the tiles read besides codes and tokens.  One workgroup a
 // token (affine): its power of two, the fp16 copy in the codes' pair order
-// and the group sums' bf16 terms.  One wave a weight row (affine, and mxfp4
-// with fp16 tokens): its power of two, the fp16 scales and b + 8 s in bf16 terms.
+// and the group sums' bf16 terms.  row_lanes threads a weight row (affine, and
+// mxfp4 with fp16 tokens), eight groups each at a time: its power of two, the
+// fp16 scales and b + 8 s in bf16 terms (112843 rows of 12 groups: 11.3 us;
+// 29.8 with a wave a row and a group a lane).
 struct PrepareArgs {
   const uint16_t* x;
   const unsigned char* s;
@@ -393,6 +393,8 @@ struct PrepareArgs {
   int32_t* wexp;
   long long ldx;
   int L, N, K, G, Gp;
+  int terms;
+  int row_lanes;  // a power of two, 64 at most
   int tok_blocks;
 };
 
@@ -421,10 +423,13 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
         if (tid == 0) a.xexp[t] = e;
       }
       constexpr int kLanes = lin_group(FMT) / 8;  // lanes of a group
+      uint4 next = make_uint4(0, 0, 0, 0);  // a step ahead
+      if (8 * tid < a.K) next = *reinterpret_cast<const uint4*>(x + 8 * tid);
       for (int c0 = 0; c0 < a.K; c0 += 2048) {
         const int c = c0 + 8 * tid;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c < a.K) v = *reinterpret_cast<const uint4*>(x + c);
+        uint4 v = next;
+        next = make_uint4(0, 0, 0, 0);
+        if (c + 2048 < a.K) next = *reinterpret_cast<const uint4*>(x + c + 2048);
         const uint32_t q[4] = {v.x, v.y, v.z, v.w};
         float f[8];
 #pragma unroll
@@ -454,41 +459,68 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
         sum += __shfl_xor(sum, 2, 64);
         if constexpr (kLanes == 8) sum += __shfl_xor(sum, 4, 64);
         if (c < a.K && (tid & (kLanes - 1)) == 0) {
-          store_terms(a.xsum, (size_t)t * a.Gp + c / lin_group(FMT), (size_t)a.L * a.Gp, sum);
+          uint32_t term[3];
+          split_terms(sum, term);
+          uint16_t* to = a.xsum + (size_t)t * a.Gp + c / lin_group(FMT);
+          for (int p = 0; p < a.terms; ++p) to[(size_t)p * a.L * a.Gp] = (uint16_t)term[p];
         }
       }
       if (a.G + tid < a.Gp) {
-        for (int p = 0; p < 3; ++p) a.xsum[((size_t)p * a.L + t) * a.Gp + a.G + tid] = 0;
+        for (int p = 0; p < a.terms; ++p) a.xsum[((size_t)p * a.L + t) * a.Gp + a.G + tid] = 0;
       }
     }
     return;
   }
-  const size_t n = (size_t)(blockIdx.x - a.tok_blocks) * 4 + wave;
-  if (n >= (size_t)a.N) return;
+  const int P = a.row_lanes, sub = tid & (P - 1);
+  const size_t n = ((size_t)(blockIdx.x - a.tok_blocks) * 256 + tid) / P;
+  if (n >= (size_t)a.N) return;  // a row's threads together
   int m = 0;
   if constexpr (FMT == kLinMxfp4) {
-    for (int g = lane; g < a.G; g += 64) {
+    for (int g = sub; g < a.G; g += P) {
       const int e = a.s[n * a.G + g];
       m = max(m, e == 255 ? 0 : e);
     }
-    for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o, 64));
-    if (lane == 0) a.wexp[n] = m - 127 - 12;  // the largest block's elements reach 6 * 2^12
+    for (int o = P / 2; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o, 64));
+    if (sub == 0) a.wexp[n] = m - 127 - 12;  // the largest block's elements reach 6 * 2^12
   } else if constexpr (lin_affine(FMT)) {
-    const uint16_t* s = reinterpret_cast<const uint16_t*>(a.s) + n * a.G;
-    for (int g = lane; g < a.G; g += 64) m = max(m, (int)(s[g] & 0x7FFFu));
-    for (int o = 32; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o, 64));
-    const int e = m ? min(max(m >> 7, 1), 254) - 127 - 8 : 0;  // the largest falls in [2^8, 2^9): 24 s in 2^14
-    const uint16_t* b = reinterpret_cast<const uint16_t*>(a.b) + n * a.G;
-    for (int g = lane; g < a.Gp; g += 64) {
-      float t = 0.0f;
-      if (g < a.G) {
-        const float v = bf16_to_f32(s[g]);
-        a.sh[n * a.G + g] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_ldexpf(v, -e));
-        t = __builtin_fmaf(8.0f, v, bf16_to_f32(b[g]));
+    // eight bf16 from group g on, zeros past the row (whose start has any alignment)
+    auto eight = [&](const unsigned char* base, int g, uint16_t (&v)[8]) __attribute__((always_inline)) {
+      const uint16_t* from = reinterpret_cast<const uint16_t*>(base) + n * a.G + g;
+      if (g + 8 <= a.G) {
+        __builtin_memcpy(v, from, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = g + i < a.G ? from[i] : (uint16_t)0;
       }
-      store_terms(a.tsum, n * a.Gp + g, (size_t)a.N * a.Gp, t);
+    };
+    uint16_t s[8], b[8];
+    for (int g = 8 * sub; g < a.G; g += 8 * P) {
+      eight(a.s, g, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, (int)(s[i] & 0x7FFFu));
     }
-    if (lane == 0) a.wexp[n] = e;
+    for (int o = P / 2; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o, 64));
+    const int e = m ? min(max(m >> 7, 1), 254) - 127 - 8 : 0;  // the largest falls in [2^8, 2^9): 24 s in 2^14
+    for (int g = 8 * sub; g < a.Gp; g += 8 * P) {
+      eight(a.s, g, s);
+      eight(a.b, g, b);
+      uint32_t h[4], t[3][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t term[2][3];
+        const float s0 = bf16_to_f32(s[2 * i]), s1 = bf16_to_f32(s[2 * i + 1]);
+        h[i] = lin_u(lin_f16x2{(_Float16)__builtin_amdgcn_ldexpf(s0, -e), (_Float16)__builtin_amdgcn_ldexpf(s1, -e)});
+        split_terms(__builtin_fmaf(8.0f, s0, bf16_to_f32(b[2 * i])), term[0]);
+        split_terms(__builtin_fmaf(8.0f, s1, bf16_to_f32(b[2 * i + 1])), term[1]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) t[p][i] = term[0][p] | term[1][p] << 16;
+      }
+      *reinterpret_cast<uint4*>(a.sh + n * a.Gp + g) = make_uint4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        if (p < a.terms) *reinterpret_cast<uint4*>(a.tsum + ((size_t)p * a.N + n) * a.Gp + g) = make_uint4(t[p][0], t[p][1], t[p][2], t[p][3]);
+    }
+    if (sub == 0) a.wexp[n] = e;
   }
 }
 

@@ -25,7 +25,7 @@ struct TopkArgs {
   int32_t* ids;
   float* w;
   long long ld;
-  int T, k, E, score, norm, vec;
+  int T, k, E, score, norm;
   float scale;
 };
 
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : kTopkThreads) void k_router_topk(T
   const int want = blockIdx.x * kGroups + tid / LPR, t = min(want, a.T - 1);  // rows past T do the last one's work
   const mem* row = static_cast<const mem*>(a.z) + (size_t)t * a.ld;
   float z[EPL];
-  load_row<LT, EPL, LPR>(row, slot, a.E, a.vec, -__builtin_inff(), z);
+  load_row<LT, EPL, LPR>(row, slot, a.E, -__builtin_inff(), z);
 
   // softmax statistics, where the whole row counts
   float row_base = 0.0f, row_sum = 1.0f;
@@ -347,7 +347,7 @@ struct TopkBackArgs {
   const float* dw;
   void* dz;
   long long ld, ldd;
-  int T, k, E, score, norm, vec, vecd;
+  int T, k, E, score, norm;
   float scale;
 };
 
@@ -375,7 +375,7 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : kTopkThreads) void k_router_topk_b
   const bool live = id >= 0;
   float out[EPL], term;
   if (a.score == kRouterScoreSoftmax && !a.norm) {
-    load_row<LT, EPL, LPR>(row, slot, a.E, a.vec, -__builtin_inff(), out);
+    load_row<LT, EPL, LPR>(row, slot, a.E, -__builtin_inff(), out);
     float m = out[0], sum = 0.0f;
 #pragma unroll
     for (int i = 1; i < EPL; ++i) m = fmaxf(m, out[i]);
@@ -439,7 +439,7 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : kTopkThreads) void k_router_topk_b
       for (int i = 0; i < EPL; ++i) out[i] += row_expert<LT, EPL, LPR>(slot, i) == e ? v : 0.0f;
     }
   }
-  if (want < a.T) store_row<LT, EPL, LPR>(static_cast<mem*>(a.dz) + (size_t)t * a.ldd, slot, a.E, a.vecd, out);
+  if (want < a.T) store_row<LT, EPL, LPR>(static_cast<mem*>(a.dz) + (size_t)t * a.ldd, slot, a.E, out);
 }
 
 int check_router(int dtype, long long ld, int T, int k, int E, int score, int norm) {
@@ -482,8 +482,7 @@ extern "C" int moe_router_topk(const void* logits, int logits_dtype, long long l
     return MOE_Q4_ERR_ALIAS;
   // Narrow rows where keys are packed and there are rows enough to fill the card with them.
   const RowPlan plan = row_plan(E, k, select_bias || logits_dtype == MOE_Q4_DTYPE_F32 || T <= 2048);
-  TopkArgs a{logits, select_bias, topk_ids, topk_weights, ld, T, k, E, score, renormalize, 0, scale};
-  a.vec = row_vec(logits, ld, E, plan.epl, (int)es);
+  TopkArgs a{logits, select_bias, topk_ids, topk_weights, ld, T, k, E, score, renormalize, scale};
   const int threads = plan.lpr > 64 ? plan.lpr : kTopkThreads, per = threads / plan.lpr;
   const dim3 grid((T + per - 1) / per), block(threads);
 #define MOE_TOPK_CALL(LT, EPL, LPR)                                                                    \
@@ -511,9 +510,7 @@ extern "C" int moe_router_topk_backward(const void* logits, int logits_dtype, lo
       overlap(dlogits, out, dweights, pairs))
     return MOE_Q4_ERR_ALIAS;
   const RowPlan plan = row_plan(E, k, T <= 2048);
-  TopkBackArgs a{logits, topk_ids, dweights, dlogits, ld, ldd, T, k, E, score, renormalize, 0, 0, scale};
-  a.vec = row_vec(logits, ld, E, plan.epl, (int)es);
-  a.vecd = row_vec(dlogits, ldd, E, plan.epl, (int)es);
+  TopkBackArgs a{logits, topk_ids, dweights, dlogits, ld, ldd, T, k, E, score, renormalize, scale};
   const int threads = plan.lpr > 64 ? plan.lpr : kTopkThreads, per = threads / plan.lpr;
   const dim3 grid((T + per - 1) / per), block(threads);
 #define MOE_TOPK_BACK_CALL(LT, EPL, LPR) \

@@ -93,58 +93,49 @@ __device__ __forceinline__ int row_expert(int slot, int j) {
   return (j / V) * (LPR * V) + slot * V + j % V;
 }
 
-// A thread's values of a row as fp32, `fill` past E.  `vec`: rows start on
-// chunk boundaries and E is a multiple of the chunk.
+// A thread's values of a row as fp32, `fill` past E.  Rows may start at any
+// element: loads of a whole chunk need no alignment, and only the chunk that E
+// ends in goes by elements (against elements throughout, 5 x 16525 rows of 93
+// bf16 values went from 18.6 to 14.3 us in the balance loss, from 27.6 to 17.6
+// in its gradient).
 template <class LT, int EPL, int LPR>
-__device__ __forceinline__ void load_row(const typename LT::mem* __restrict__ row, int slot, int E, bool vec, float fill,
+__device__ __forceinline__ void load_row(const typename LT::mem* __restrict__ row, int slot, int E, float fill,
                                          float (&v)[EPL]) {
   typedef typename LT::mem mem;
   constexpr int V = row_chunk<LT, EPL>();
-  if (vec) {
-    typedef mem vt __attribute__((ext_vector_type(V)));
+  typedef mem vt __attribute__((ext_vector_type(V)));
 #pragma unroll
-    for (int c = 0; c < EPL / V; ++c) {
-      const int e = row_expert<LT, EPL, LPR>(slot, c * V);
-      if (e < E) {
-        const vt x = *reinterpret_cast<const vt*>(row + e);
+  for (int c = 0; c < EPL / V; ++c) {
+    const int e = row_expert<LT, EPL, LPR>(slot, c * V);
+    if (e + V <= E) {
+      vt x;
+      __builtin_memcpy(&x, row + e, sizeof(vt));
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[c * V + j] = LT::load(x[j]);
-      } else {
+      for (int j = 0; j < V; ++j) v[c * V + j] = LT::load(x[j]);
+    } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[c * V + j] = fill;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const int e = row_expert<LT, EPL, LPR>(slot, j);
-      v[j] = e < E ? LT::load(row[e]) : fill;
+      for (int j = 0; j < V; ++j) v[c * V + j] = e + j < E ? LT::load(row[e + j]) : fill;
     }
   }
 }
 
 template <class LT, int EPL, int LPR>
-__device__ __forceinline__ void store_row(typename LT::mem* __restrict__ row, int slot, int E, bool vec,
-                                          const float (&v)[EPL]) {
+__device__ __forceinline__ void store_row(typename LT::mem* __restrict__ row, int slot, int E, const float (&v)[EPL]) {
   typedef typename LT::mem mem;
   constexpr int V = row_chunk<LT, EPL>();
-  if (vec) {
-    typedef mem vt __attribute__((ext_vector_type(V)));
+  typedef mem vt __attribute__((ext_vector_type(V)));
 #pragma unroll
-    for (int c = 0; c < EPL / V; ++c) {
-      const int e = row_expert<LT, EPL, LPR>(slot, c * V);
-      if (e < E) {
-        vt x;
+  for (int c = 0; c < EPL / V; ++c) {
+    const int e = row_expert<LT, EPL, LPR>(slot, c * V);
+    if (e + V <= E) {
+      vt x;
 #pragma unroll
-        for (int j = 0; j < V; ++j) x[j] = LT::store(v[c * V + j]);
-        *reinterpret_cast<vt*>(row + e) = x;
-      }
-    }
-  } else {
+      for (int j = 0; j < V; ++j) x[j] = LT::store(v[c * V + j]);
+      __builtin_memcpy(row + e, &x, sizeof(vt));
+    } else {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const int e = row_expert<LT, EPL, LPR>(slot, j);
-      if (e < E) row[e] = LT::store(v[j]);
+      for (int j = 0; j < V; ++j)
+        if (e + j < E) row[e + j] = LT::store(v[c * V + j]);
     }
   }
 }
@@ -178,8 +169,7 @@ __device__ __forceinline__ float sigmoid_pair(float z, float& rest) {
 __device__ __forceinline__ float exp_base(float row_max) { return row_max == -__builtin_inff() ? 0.0f : row_max; }
 
 // Host side: threads per row and values per thread for E experts and k
-// picks (one thread each), and whether rows of this layout can be read and
-// written by chunks.  Few threads a row share a reduction's steps among more
+// picks (one thread each).  Few threads a row share a reduction's steps among more
 // rows; many (`wide`) have less to do one after the other.
 struct RowPlan {
   int lpr, epl;
@@ -195,11 +185,6 @@ inline RowPlan row_plan(int E, int k, bool wide) {
   p.epl = need <= 4 ? 4 : need <= 8 && (p.lpr == 16 || p.lpr == 64) ? 8 : 16;
   return p;
 }
-inline bool row_vec(const void* base, long long ld, int E, int epl, int elem) {
-  const int chunk = epl * elem < 16 ? epl : 16 / elem;
-  return E % chunk == 0 && (uintptr_t)base % (chunk * elem) == 0 && ld % chunk == 0;
-}
-
 }  // namespace moeq4
 
 // Expands CALL(LT, EPL, LPR) for a logits type and a RowPlan.

@@ -75,6 +75,31 @@ def test_many_tokens_and_many_outputs(codec, L, N, K):
 
 @pytest.mark.parametrize("codec", CODECS)
 @pytest.mark.parametrize("xt", [BF16, F16])
+@pytest.mark.parametrize("L,N,K", [(1, 40, 384), (4, 3000, 320), (16, 70, 448), (3, 100, 2240), (9, 50, 4160), (2, 33, 6208),
+                                   (6, 20, 8256)])
+def test_few_tokens_of_long_and_odd_inputs(codec, xt, L, N, K):
+    run(codec, L, N, K, xt, F32)
+
+
+@pytest.mark.parametrize("codec", CODECS)
+@pytest.mark.parametrize("L,K", [(2, 4224), (7, 6144), (3, 8320)])
+def test_unaligned_scale_rows_of_long_inputs(codec, L, K):
+    x, w, s, b, _ = problem(codec, L, 21, K, BF16, False)
+    ref, bound = R.linear_reference(codec, x, w, s, b, None)
+
+    def shifted(t):
+        if t is None:
+            return None
+        skip = 2 if codec == "nvfp4" else 1
+        room = torch.zeros(t.numel() + skip, dtype=t.dtype, device="cuda")
+        room[skip:] = t.flatten().cuda()
+        return room[skip:].view(t.shape[1:])
+    out = q.moe_linear_codec_forward(codec, x.cuda(), w[0].cuda(), shifted(s), shifted(b), out_dtype=F32)
+    check(out, ref, bound, L, 21, F32)
+
+
+@pytest.mark.parametrize("codec", CODECS)
+@pytest.mark.parametrize("xt", [BF16, F16])
 @pytest.mark.parametrize("ot", [BF16, F16, F32])
 def test_types(codec, xt, ot):
     for L in (1, 6, 50, 200):

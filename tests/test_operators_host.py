@@ -54,9 +54,6 @@ def linear(codec=0, x=None, xd=0, ldx=None, w=None, s=None, b=None, bias=0, L=2,
     (dict(s=fake(2, 1)), q.MOE_Q4_ERR_ALIGN),
     (dict(b=fake(3, 1)), q.MOE_Q4_ERR_ALIGN),
     (dict(codec=3, s=fake(2, 1)), q.MOE_Q4_ERR_ALIGN),
-    (dict(K=2176, s=fake(2, 2)), q.MOE_Q4_ERR_ALIGN),
-    (dict(K=2176, b=fake(3, 2)), q.MOE_Q4_ERR_ALIGN),
-    (dict(codec=2, K=4096, s=fake(2, 1)), q.MOE_Q4_ERR_ALIGN),
     (dict(bias=fake(4, 2)), q.MOE_Q4_ERR_ALIGN),
     (dict(out=fake(5, 1)), q.MOE_Q4_ERR_ALIGN),
     (dict(od=1, out=fake(5, 2)), q.MOE_Q4_ERR_ALIGN),
