@@ -138,11 +138,15 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
   }
 
   if constexpr (lin_affine(FMT)) {
-    if (split == 0) {
+    // This split's share of the groups (all of them in the first split: 262 x
+    // 728 x 12288 takes 42 us, the shares 31).
+    const int chunks = a.Gp / 32;
+    const int g0 = 32 * (int)((long)chunks * split / a.splits), g1 = 32 * (int)((long)chunks * (split + 1) / a.splits);
+    if (g0 < g1) {
       // sum over groups of t X, t = b + 8 s, by their bf16 terms: the products
       // whose terms' places add up to less than `terms`
 #pragma unroll 1
-      for (int g = 8 * kb; g < a.Gp; g += 32) {
+      for (int g = g0 + 8 * kb; g < g1; g += 32) {
         uint4 tf[3][NT], xf[3][MT];
         auto load_t = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
