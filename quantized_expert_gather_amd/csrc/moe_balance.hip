@@ -6,6 +6,12 @@
 //   dz = p (a - sum_e a_e p_e) (softmax; times 1 - sigmoid(z) for sigmoid),
 //   a_e = dloss * coef * E * c_e / (k * n^2), the counts held fixed.
 //
+// What it has to move is z, once each way, and dz: 32768 x 256 bf16 takes
+// 9.6 + 4.8 us forward (16.8 MB) and 10.5 us backward (33.6 MB).  A launch
+// here takes about 3.5 us whatever it does; the rest is the exponentials'
+// vector work and the latency of a workgroup's first rows, which 256
+// workgroups of 16 waves, one a compute unit, pay once (128 of them: 12.9 us).
+//
 // Forward: a workgroup sums p over its run of tokens in registers (a wave
 // holds whole rows) and its routes in an LDS histogram of integers, and
 // leaves one row of partials in the workspace; a second launch adds the
@@ -289,6 +295,10 @@ struct BalanceBackArgs {
   float coef;
 };
 
+// Rows as in the forward; a row's p is formed again, which costs less than
+// keeping it (four times the bytes of bf16 logits).  The counts are the same
+// for all rows of a workgroup: through LDS once, then registers (read by each
+// thread for itself from memory: 16.7 us instead of 10.5).
 template <class LT, int EPL, int LPR>
 __global__ __launch_bounds__(LPR > 64 ? LPR : 64 * kBackWaves) void k_balance_backward(BalanceBackArgs a) {
   typedef typename LT::mem mem;

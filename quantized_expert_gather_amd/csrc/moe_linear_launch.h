@@ -126,7 +126,7 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
   a.G = l.K / lin_group(FMT);
   a.Gp = (a.G + 31) / 32 * 32;
   a.out_dtype = l.out_dtype;
-  a.terms = l.out_dtype == MOE_Q4_DTYPE_F32 ? 3 : 2;
+  a.terms = l.out_dtype == MOE_Q4_DTYPE_BF16 ? 2 : 3;
   a.splits = p.splits; a.steps_per = p.steps_per;
   a.stagger = std::max(1, p.steps_per / p.tok_tiles);
   a.row_tiles = p.row_tiles; a.tok_tiles = p.tok_tiles;

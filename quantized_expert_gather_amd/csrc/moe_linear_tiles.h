@@ -46,7 +46,10 @@ struct TilesArgs {
   long long ldx, ldo;
   int L, N, K, G, Gp;
   int out_dtype;
-  int terms;               // how many bf16 terms are used: 3, or 2 (2^-17 of |t X|) for 16-bit results
+  // How many bf16 terms are used: 3, whose error is fp32's, or 2 where the
+  // result is rounded to bf16 anyway (together off by 2^-16 |t X|, 2^-8 of
+  // the result's own half step unless the sum cancels; a sixth of the products).
+  int terms;
   int splits, steps_per;   // steps of 128 inputs of each split
   int stagger;             // steps between the token tiles' first ones
   int row_tiles, tok_tiles;

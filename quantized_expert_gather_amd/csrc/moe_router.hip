@@ -6,6 +6,14 @@
 //
 // The threads of a row take its largest value k times: each thread's largest,
 // the row's, and the lowest expert that has it.  z is read once.
+//
+// Bound by a launch where there are few tokens (4 x 256 fp32, k = 8, with a
+// bias: 3.6 us) and by vector instructions where there are many: 16384 x 256
+// bf16, k = 8 takes 9.0 us, its 8.4 MB two.  16-bit logits without a bias
+// make order and expert one word, so a thread's keys can be sorted once and a
+// round is one reduction and a shift (8.3 us of a captured run; 9.8 with a
+// maximum, the lowest expert that has it and its removal each round); the
+// reductions stay in registers.
 #include <hip/hip_runtime.h>
 
 #include <limits.h>
@@ -303,9 +311,12 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : kTopkThreads) void k_router_topk(T
     }
     if constexpr (BIAS) {
       // Two neighbours in the order of different logits or biases that fp32
-      // cannot tell apart: a score is off by at most about 5e-6 p + 2^-24
-      // |score| (the exponential, its sum, the quotient, the sum with the
-      // bias), p <= 1.  Lanes j < k hold the picks and compare with the next.
+      // cannot tell apart: with |d| the distance from the row's maximum, a
+      // softmax p is off by at most 2^-24 (1.5 |d| + 80) p (the exponential,
+      // its sum, the quotient), |d| <= 88 where p is not 0 and p |d| <= 0.4: by
+      // 1.3e-5 p and by 4e-6 in any case.  A sigmoid is off by 2^-24 (1.5 |z|
+      // (1 - p) + 5) p: by 8.2e-6 p and by 4e-7.  The sum with the bias adds
+      // 2^-24 of itself.  Lanes j < k hold the picks and compare with the next.
       bool close = false;
       if (LPR <= 64 || tid < 64) {
         const bool end = slot == a.k - 1;  // its neighbour is the pick after the k-th
@@ -314,8 +325,11 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : kTopkThreads) void k_router_topk(T
         if (slot < a.k) {
           my_z = LT::load(row[my_id]);
           const float s1 = key_value(my_key), s0 = key_value(key2);
-          if ((!end || rounds > a.k) && !(s1 - s0 > 8e-6f + 5e-7f * fabsf(s1)))
-            close = !(LT::load(row[id2]) == my_z && a.bias[id2] == a.bias[my_id]);
+          if ((!end || rounds > a.k) && !(s1 - s0 > 8e-6f + 5e-7f * fabsf(s1))) {
+            const float b1 = a.bias[my_id], b0 = a.bias[id2], p = fabsf(s1 - b1) + fabsf(s0 - b0);
+            const float off = a.score == kRouterScoreSoftmax ? fminf(8e-6f, 1.3e-5f * p) : fminf(8e-7f, 8.2e-6f * p);
+            close = !(s1 - s0 > off + 5e-7f * fabsf(s1)) && !(LT::load(row[id2]) == my_z && b0 == b1);
+          }
         }
         close = __any(close);
       }
@@ -351,6 +365,12 @@ struct TopkBackArgs {
   float scale;
 };
 
+// w_j's gradient g_j, in the logits: renormalised p_j (g_j - sum_i p_i g_i)
+// at the chosen only (times 1 - sigmoid(z_j) for sigmoid scores), else the
+// softmax's over the whole row, which is read for that alone.  Bound by the
+// gradient it writes: 16384 x 256 bf16, k = 8: 5.0 us for 9.5 MB, most of it
+// zeros; 5003 x 288 fp32 over the whole row: 5.5 us for 11.8 MB.
+//
 // dz of rows as the selection holds them: a row's lanes j < k form their
 // pick's term; the terms reach the threads that hold their experts through an
 // LDS row, in ascending j where an expert repeats.
@@ -480,8 +500,11 @@ extern "C" int moe_router_topk(const void* logits, int logits_dtype, long long l
       overlap(topk_ids, pairs, topk_weights, pairs) || overlap(topk_ids, pairs, select_bias, select_bias ? (size_t)E * 4 : 0) ||
       overlap(topk_weights, pairs, select_bias, select_bias ? (size_t)E * 4 : 0))
     return MOE_Q4_ERR_ALIAS;
-  // Narrow rows where keys are packed and there are rows enough to fill the card with them.
-  const RowPlan plan = row_plan(E, k, select_bias || logits_dtype == MOE_Q4_DTYPE_F32 || T <= 2048);
+  // Few lanes a row where there are rows enough to fill the card with them
+  // (k = 8 of 256, us over 16 lanes and over 64: 16384 fp32 rows 9.9 and 15.0,
+  // bf16 8.3 and 9.6, 4096 4.7 and 4.1, 1000 4.5 and 3.0); with a bias, whose
+  // scores are formed for all of a row, many (31.9 and 30.3).
+  const RowPlan plan = row_plan(E, k, select_bias || T <= 6144);
   TopkArgs a{logits, select_bias, topk_ids, topk_weights, ld, T, k, E, score, renormalize, scale};
   const int threads = plan.lpr > 64 ? plan.lpr : kTopkThreads, per = threads / plan.lpr;
   const dim3 grid((T + per - 1) / per), block(threads);
@@ -509,6 +532,7 @@ extern "C" int moe_router_topk_backward(const void* logits, int logits_dtype, lo
   if (overlap(dlogits, out, logits, span(T, ld, E, es)) || overlap(dlogits, out, topk_ids, pairs) ||
       overlap(dlogits, out, dweights, pairs))
     return MOE_Q4_ERR_ALIAS;
+  // 2048 x 256 bf16: 2.9 us over 16 lanes a row, 2.7 over 64; 4096: 3.1 and 3.4
   const RowPlan plan = row_plan(E, k, T <= 2048);
   TopkBackArgs a{logits, topk_ids, dweights, dlogits, ld, ldd, T, k, E, score, renormalize, scale};
   const int threads = plan.lpr > 64 ? plan.lpr : kTopkThreads, per = threads / plan.lpr;

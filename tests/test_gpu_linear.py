@@ -153,6 +153,19 @@ def test_scales_at_the_ends_of_their_range(codec, L):
     assert (np.abs(got - ref) <= bound + R.HALF_STEP[F32] * np.abs(ref) + K * 2.0 ** -126).all()
 
 
+@pytest.mark.parametrize("codec", ["affine4_g64", "affine4_g32"])
+@pytest.mark.parametrize("L", [2, 9, 40, 200])
+@pytest.mark.parametrize("ot", [F16, F32])
+def test_biases_far_above_the_scales(codec, L, ot):
+    x, w, s, b, _ = problem(codec, L, 70, 256, BF16, False)
+    g = torch.Generator().manual_seed(3)
+    b = torch.randn(b.shape, generator=g).to(BF16)
+    s = s / 64
+    ref, bound = R.linear_reference(codec, x, w, s, b, None)
+    out = q.moe_linear_codec_forward(codec, x.cuda(), w[0].cuda(), s[0].cuda(), b[0].cuda(), out_dtype=ot)
+    check(out, ref, bound, L, 70, ot)
+
+
 @pytest.mark.parametrize("codec,nan", [("mxfp4", 255), ("nvfp4", 0x7F)])
 @pytest.mark.parametrize("L", [1, 20, 150])
 def test_nan_scales_reach_their_row_only(codec, nan, L):
