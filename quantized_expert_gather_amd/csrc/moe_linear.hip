@@ -45,7 +45,7 @@ using namespace moeq4;
 extern "C" size_t moe_linear_codec_workspace_bytes(int codec, int L, int N, int K) {
   const int fmt = linear_fmt(codec);
   if (linear_shape_status(fmt, L, N, K) || L == 0) return 0;
-  return L < kTilesFrom ? rows_workspace(fmt, L, N, K) : tiles_layout(fmt, L, N, K).total;
+  return linear_by_tiles(fmt, L, N, K) ? tiles_layout(fmt, L, N, K).total : rows_workspace(fmt, L, N, K);
 }
 
 extern "C" int moe_linear_codec_forward(int codec, const void* x, int x_dtype, long long ldx, const uint32_t* w,

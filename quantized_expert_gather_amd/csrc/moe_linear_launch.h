@@ -18,8 +18,19 @@ namespace moeq4 {
 template <int FMT>
 int linear_launch(bool f16, const LinearArgs& a, unsigned char* workspace, hipStream_t stream);
 
-// Tokens from which the tiles take over.
-constexpr int kTilesFrom = 17;
+// Whether the tiles take a call.  The rows' kernel takes 16 tokens at a time,
+// reading all weights for each 16, but needs neither a preparation (affine)
+// nor splits of K to fill the card, so it keeps small products of any number
+// of tokens (us, rows against tiles: affine4_g64 128 x 256 x 4096 7.4 and
+// 15.7, 32 x 4096 x 4096 13.8 and 16.2, 32 x 8192 x 4096 19.0 and 18.4, 128 x
+// 4096 x 4096 47 and 23; mxfp4 64 x 1024 x 4096 6.3 and 10.1, 64 x 8192 x 512
+// 5.7 and 5.1, 32 x 4096 x 4096 12.0 and 10.3).
+inline bool linear_by_tiles(int fmt, int L, int N, int K) {
+  if (L <= 16) return false;
+  const bool affine = lin_affine(fmt);
+  const long read = (long)((L + 15) / 16) * N * K;  // codes of all passes
+  return K < (affine ? kLinStep : 1024) || read > (affine ? 1L << 25 : 1L << 24);
+}
 
 // Tile shape and split of K.  A compute unit holds two workgroups, so they
 // run in rounds of 512, and what a round takes per 1024 inputs was measured
@@ -171,7 +182,7 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
 
 template <int FMT>
 int linear_launch(bool f16, const LinearArgs& a, unsigned char* ws, hipStream_t stream) {
-  if (a.L >= kTilesFrom) return f16 ? launch_tiles<FMT, true>(a, ws, stream) : launch_tiles<FMT, false>(a, ws, stream);
+  if (linear_by_tiles(FMT, a.L, a.N, a.K)) return f16 ? launch_tiles<FMT, true>(a, ws, stream) : launch_tiles<FMT, false>(a, ws, stream);
   if (a.K < kLinStep) {
     const dim3 grid((unsigned)(((size_t)a.L * a.N + 255) / 256));
     if (f16)

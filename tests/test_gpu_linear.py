@@ -340,3 +340,98 @@ def test_more_codes_than_32_bits_of_bytes():
         want[:, -3:] = 100.0
         want[:, 0] = 100.0
         assert torch.equal(out, want)
+
+
+# ---- affine products that are large enough for the tiles (small ones of any number of tokens take the few tokens' way) ----
+
+AFFINE = ["affine4_g64", "affine4_g32"]
+
+
+@pytest.mark.parametrize("codec", AFFINE)
+@pytest.mark.parametrize("xt", [BF16, F16])
+@pytest.mark.parametrize("L,N,K", [(17, 4099, 4160), (33, 2900, 4160), (50, 2100, 5184), (70, 1700, 4224), (130, 1000, 4160),
+                                   (200, 701, 4160), (600, 250, 4160), (1500, 100, 4224), (129, 2003, 2112), (40, 6000, 2240),
+                                   (300, 14, 131072)])
+def test_affine_tiles(codec, xt, L, N, K):
+    run(codec, L, N, K, xt, F32, bias=N % 3 == 0)
+
+
+@pytest.mark.parametrize("codec", AFFINE)
+@pytest.mark.parametrize("L,N", [(20, 66000), (60, 33003), (200, 10501)])
+@pytest.mark.parametrize("ot", [BF16, F16])
+def test_affine_tiles_of_short_inputs(codec, L, N, ot):
+    run(codec, L, N, 256, ot, ot, bias=True)
+
+
+@pytest.mark.parametrize("codec", AFFINE)
+@pytest.mark.parametrize("ot", [F16, F32])
+def test_affine_tiles_with_extreme_rows(codec, ot):
+    L, N, K = 150, 13203, 256
+    x, w, s, b, _ = problem(codec, L, N, K, BF16, False)
+    s[0, 1] = 0.0
+    s[0, 2, ::2] = -s[0, 2, ::2]
+    if ot == F32:
+        s[0, 3] *= 2.0 ** -90
+        b[0, 3] *= 2.0 ** -90
+        s[0, 4] *= 2.0 ** 90
+        b[0, 4] *= 2.0 ** 90
+        x[5] *= 2.0 ** 20
+        x[6] *= 2.0 ** -60
+    b[0, 7] = b[0, 7] * 64
+    x[8] = 0
+    ref, bound = R.linear_reference(codec, x, w, s, b, None)
+    out = q.moe_linear_codec_forward(codec, x.cuda(), w[0].cuda(), s[0].cuda(), b[0].cuda(), out_dtype=ot)
+    check(out, ref, bound + K * 2.0 ** -126, L, N, ot)
+
+
+@pytest.mark.parametrize("codec", AFFINE)
+@pytest.mark.parametrize("xt", [BF16, F16])
+def test_affine_tiles_keep_bad_tokens_and_rows_apart(codec, xt):
+    L, N, K = 150, 13203, 256
+    x, w, s, b, _ = problem(codec, L, N, K, xt, False)
+    x[1, 70] = float("nan")
+    x[2, 3] = float("inf")
+    x[149, 255] = float("-inf")
+    s[0, 17, 1] = float("nan")
+    b[0, 40, 0] = float("inf")
+    out = q.moe_linear_codec_forward(codec, x.cuda(), w[0].cuda(), s[0].cuda(), b[0].cuda(), out_dtype=F32).cpu()
+    rows, cols = [1, 2, 149], [17, 40]
+    assert not torch.isfinite(out[rows]).any() and not torch.isfinite(out[:, cols]).any()
+    x[rows] = 0
+    s[0, 17, 1] = 1.0
+    b[0, 40, 0] = 0.0
+    ref, bound = R.linear_reference(codec, x, w, s, b, None)
+    keep_r, keep_c = np.setdiff1d(np.arange(L), rows), np.setdiff1d(np.arange(N), cols)
+    got = out.double().numpy()[np.ix_(keep_r, keep_c)]
+    r, bd = ref[np.ix_(keep_r, keep_c)], bound[np.ix_(keep_r, keep_c)]
+    assert (np.abs(got - r) <= bd + R.HALF_STEP[F32] * (np.abs(r) + bd)).all()
+
+
+@pytest.mark.parametrize("codec", AFFINE)
+def test_affine_tiles_strided_runs_and_replays(codec):
+    L, N, K = 150, 13203, 256
+    x, w, s, b, _ = problem(codec, L, N, K, BF16, False)
+    ref, bound = R.linear_reference(codec, x, w, s, b, None)
+    wide = torch.full((L, K + 24), float("nan"), dtype=BF16, device="cuda")
+    wide[:, 8:8 + K] = x.cuda()
+    room = torch.full((L + 2, N + 9), 7.0, device="cuda")
+    out = room[1:L + 1, 4:4 + N]
+    a = (wide[:, 8:8 + K], w[0].cuda(), s[0].cuda(), b[0].cuda())
+    q.moe_linear_codec_forward(codec, *a, out=out)
+    check(out, ref, bound, L, N, F32)
+    first = out.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    p = q.PreparedLinear(codec, *a, out=out, stream=side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        p()
+    for _ in range(3):
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+        assert torch.equal(q.moe_linear_codec_forward(codec, *a, out_dtype=F32), first)
+    room[1:L + 1, 4:4 + N] = 7.0
+    assert (room == 7.0).all()

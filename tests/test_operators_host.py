@@ -40,9 +40,9 @@ def linear(codec=0, x=None, xd=0, ldx=None, w=None, s=None, b=None, bias=0, L=2,
     (dict(K=q.MOE_Q4_LINEAR_MAX_K + 64), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(ldx=q.MOE_Q4_LINEAR_MAX_LDX + 8), q.MOE_Q4_ERR_UNSUPPORTED),
     (dict(N=q.MOE_Q4_LINEAR_MAX_N + 1), q.MOE_Q4_ERR_UNSUPPORTED),
-    (dict(L=40, ws=fake(0)), q.MOE_Q4_ERR_ALIAS),
-    (dict(L=40, ws=fake(2)), q.MOE_Q4_ERR_ALIAS),
-    (dict(L=40, ws=fake(4, 256), bias=fake(4, 512)), q.MOE_Q4_ERR_ALIAS),
+    (dict(L=40, K=64, ws=fake(0)), q.MOE_Q4_ERR_ALIAS),
+    (dict(L=40, K=64, ws=fake(2)), q.MOE_Q4_ERR_ALIAS),
+    (dict(L=40, K=64, ws=fake(4, 256), bias=fake(4, 512)), q.MOE_Q4_ERR_ALIAS),
     (dict(x=0), q.MOE_Q4_ERR_NULL),
     (dict(w=0), q.MOE_Q4_ERR_NULL),
     (dict(s=0), q.MOE_Q4_ERR_NULL),
