@@ -104,7 +104,7 @@ inline bool linear_words(const LinearArgs& a) { return (uintptr_t)a.s % 4 == 0 &
 // Bytes of partial sums of a call with few tokens, whatever its x.
 inline size_t rows_workspace(int fmt, int L, int N, int K) {
   if (K < kLinStep) return 0;
-  const int s = std::max(rows_plan(fmt, false, K, true).splits, rows_plan(fmt, true, K, true).splits);
+  const int s = std::max(rows_plan(fmt, false, N, K, true).splits, rows_plan(fmt, true, N, K, true).splits);
   return s > 1 ? lin_round256((size_t)s * L * N * 4) : 0;
 }
 
@@ -191,7 +191,7 @@ int linear_launch(bool f16, const LinearArgs& a, unsigned char* ws, hipStream_t 
       hipLaunchKernelGGL((k_linear_short<FMT, false>), grid, dim3(256), 0, stream, a);
     return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
   }
-  const RowsPlan p = rows_plan(FMT, f16, a.K, linear_words(a));
+  const RowsPlan p = rows_plan(FMT, f16, a.N, a.K, linear_words(a));
   LinearArgs l = a;
   if (p.splits > 1) l.part = reinterpret_cast<float*>(ws);
   f16 ? launch_linear_rows<FMT, true>(l, p, stream) : launch_linear_rows<FMT, false>(l, p, stream);

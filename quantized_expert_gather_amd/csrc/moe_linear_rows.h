@@ -16,6 +16,18 @@
 // token t takes operand rows 4 t .. 4 t + 3, row 4 t + b holding its x in
 // lanes kb = b only, so a lane (n, t) receives the four blocks' sums of row n
 // and token t separately, and multiplies them by the row's scales.
+//
+// What it has to move is the weights.  Large ones stream at 5.2 TB/s (mxfp4 4
+// x 131072 x 4096: 54 us for 287 MB; affine4_g64 1 x 131072 x 6144: 88 us; a
+// kernel that only reads reaches 7.1): neighbouring lanes hold different rows,
+// as the operand wants them, so a load touches 16 pieces of 64 bytes and takes
+// 30 to 50 cycles to issue, and 16 waves a compute unit share that pipe.  A
+// tile's codes are one load a step and its scales one a tile for that reason.
+// Loads with a streaming hint were slower (60 us).  Small products take what a
+// launch, x's way through LDS to registers, one round of weights and the
+// waves' reduction take in sequence: 1 x 256 x 6144 5.9 us, 1 x 6144 x 6144 (21
+// MB) 10.0, 7 x 4099 x 4096 11.0, 16 x 4096 x 4096 6.3 (mxfp4) to 8.0
+// (affine4_g64).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -89,7 +101,10 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
   constexpr int kX = kTerms ? 2 : 1;
   constexpr int kGroups = FMT == kLinAffine64 ? 2 : 4;  // group sums of x a step (affine)
   constexpr int kAcc = kSep ? 1 : 4;
-  constexpr int kDeep = S == 1 ? 4 : S == 2 ? 3 : 2;    // tiles on their way
+  // Tiles on their way, in 128 registers a lane (which 16 waves a compute unit
+  // have) with x and the scales.  Deeper rings change little: two tiles instead
+  // of four at S = 1 take 38.3 us for 39.5 (mxfp4 4 x 131072 x 2048, 16 waves).
+  constexpr int kDeep = S == 1 ? 4 : S == 2 ? 3 : 2;
   __shared__ float red[2][W][kAcc * 64];
   __shared__ __attribute__((aligned(16))) float xsum[kAffine ? W * S * kGroups * 16 : 1];
   constexpr int kStageSteps = kSep ? S : 1, kStageTokens = kSep ? 4 : 16;  // of x in LDS at a time
@@ -388,15 +403,20 @@ struct RowsPlan {
   int W, S, splits, split_steps;
   bool plain;
 };
-// As many waves as there are steps, up to 16; the longest K of one workgroup
-// is 16 waves x 3 steps (2 where x takes two operands), longer ones are split
-// evenly.  (10 x 54483 x 320 takes 9.4 us with 4 waves, 17.6 with 16.)
-inline RowsPlan rows_plan(int fmt, bool f16, int K, bool words) {
+// The longest K of one workgroup is 16 waves x 3 steps (2 where x takes two
+// operands), longer ones are split evenly.  Where a workgroup has a tile of
+// rows or two, as many waves as there are steps; where it has many, so few
+// that each wave has two or three steps, and several workgroups share a
+// compute unit, whose barriers then overlap (mxfp4 1 x 131072 x 2048 28.8 us,
+// 37.0 with 16 waves; 9000 rows of 2944 inputs 8.2 with three steps a wave,
+// 7.1 with 16 waves of two).
+inline RowsPlan rows_plan(int fmt, bool f16, int N, int K, bool words) {
   RowsPlan p{};
   p.plain = K % kLinStep == 0 && words;
   const int steps = (K + kLinStep - 1) / kLinStep;
   const int most = fmt == kLinMxfp4 && f16 ? 2 : 3;
-  p.W = steps <= 4 ? 4 : steps <= 8 && p.plain ? 8 : 16;
+  const int per = N <= 12288 ? 1 : N <= 32768 ? 2 : most;  // steps of a wave
+  p.W = steps <= 4 * per ? 4 : steps <= 8 * per && p.plain ? 8 : 16;
   p.splits = (steps + 16 * most - 1) / (16 * most);
   p.split_steps = (steps + p.splits - 1) / p.splits;
   p.splits = (steps + p.split_steps - 1) / p.split_steps;
@@ -415,17 +435,21 @@ void launch_linear_rows(const LinearArgs& args, const RowsPlan& p, hipStream_t s
   const bool few = a.L <= 4;
 #define MOE_LINEAR_ROWS(FEW, PLAIN, S, W) \
   hipLaunchKernelGGL((k_linear_rows<FMT, F16, FEW, PLAIN, S, W>), grid, block, 0, stream, a)
+#define MOE_LINEAR_ROWS_W(FEW, PLAIN, W)               \
+  if (p.S == 1) {                                      \
+    MOE_LINEAR_ROWS(FEW, PLAIN, 1, W);                 \
+  } else if (p.S == 2) {                               \
+    MOE_LINEAR_ROWS(FEW, PLAIN, 2, W);                 \
+  } else if constexpr (!(FMT == kLinMxfp4 && F16)) {   \
+    MOE_LINEAR_ROWS(FEW, PLAIN, 3, W);                 \
+  }
 #define MOE_LINEAR_ROWS_S(FEW, PLAIN)                  \
   if (p.W == 4) {                                      \
-    MOE_LINEAR_ROWS(FEW, PLAIN, 1, 4);                 \
+    MOE_LINEAR_ROWS_W(FEW, PLAIN, 4)                   \
   } else if (PLAIN && p.W == 8) {                      \
-    MOE_LINEAR_ROWS(FEW, true, 1, 8);                  \
-  } else if (p.S == 1) {                               \
-    MOE_LINEAR_ROWS(FEW, PLAIN, 1, 16);                \
-  } else if (p.S == 2) {                               \
-    MOE_LINEAR_ROWS(FEW, PLAIN, 2, 16);                \
-  } else if constexpr (!(FMT == kLinMxfp4 && F16)) {   \
-    MOE_LINEAR_ROWS(FEW, PLAIN, 3, 16);                \
+    MOE_LINEAR_ROWS_W(FEW, true, 8)                    \
+  } else {                                             \
+    MOE_LINEAR_ROWS_W(FEW, PLAIN, 16)                  \
   }
   if constexpr (FMT != kLinMxfp4) {
     if (few) {
@@ -443,10 +467,12 @@ void launch_linear_rows(const LinearArgs& args, const RowsPlan& p, hipStream_t s
     MOE_LINEAR_ROWS_S(false, false)
   }
 #undef MOE_LINEAR_ROWS_S
+#undef MOE_LINEAR_ROWS_W
 #undef MOE_LINEAR_ROWS
 }
 
-// Inputs shorter than a step: one thread an output.
+// Inputs shorter than a step: one thread an output (1 x 16 x 64 4.9 us, 16 x
+// 4096 x 64 6.0; 16 x 65536 x 64 67, bound by its vector instructions).
 template <int FMT, bool F16>
 __global__ __launch_bounds__(256) void k_linear_short(LinearArgs a) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
