@@ -48,8 +48,9 @@ struct LinCode {
 };
 template <bool F16>
 __device__ __forceinline__ LinCode lin_code() {
-  LinCode c{F16 ? 0x03C003C0u : 0x00780078u, F16 ? 0x4C004C00u : 0x41804180u};
-  asm("" : "+s"(c.mask));
+  LinCode c;
+  asm("s_mov_b32 %0, %1" : "=s"(c.mask) : "i"(F16 ? 0x03C003C0 : 0x00780078));
+  c.base = F16 ? 0x4C004C00u : 0x41804180u;
   asm("" : "+v"(c.base));
   return c;
 }
