@@ -212,6 +212,52 @@ __device__ void select_in_64(const float (&z)[EPL], const float (&b)[EPL], int s
   }
 }
 
+// Puts the picks that lanes j < held hold in order by their scores in 64 bits
+// (they are the row's first `held` already).  `base`: the row's exp_base.
+// Every lane of the wave calls it.
+template <int EPL, int LPR>
+__device__ void order_in_64(const float (&z)[EPL], const float* bias, int slot, int held, int score, float base, int& my_id,
+                            float& my_z) {
+  double s = 0.0, sum = 0.0;
+  if (score == kRouterScoreSoftmax) {
+#pragma unroll 1
+    for (int i = 0; i < EPL; ++i) {
+      float zi = z[0];
+#pragma unroll
+      for (int j = 1; j < EPL; ++j) zi = i == j ? z[j] : zi;
+      sum += exp((double)zi - (double)base);  // 0 past E
+    }
+    for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  }
+  if (slot < held) {
+    if (score == kRouterScoreSoftmax)
+      s = sum > 0.0 ? exp((double)my_z - (double)base) / sum : 0.0;
+    else
+      s = 1.0 / (1.0 + exp(-(double)my_z));
+    s += (double)bias[my_id];
+  }
+  // neighbours change places, even and odd pairs in turn, until none does
+  int still = 0;
+  for (int r = 0; r <= held + 1 && still < 2; ++r) {
+    const int other = r & 1 ? ((slot + 1) ^ 1) - 1 : slot ^ 1;
+    const bool pair = slot < held && other >= 0 && other < held;
+    const int from = (threadIdx.x & 63) + (pair ? other - slot : 0);
+    const double s2 = __shfl(s, from, 64);
+    const int id2 = __shfl(my_id, from, 64);
+    const float z2 = __shfl(my_z, from, 64);
+    // numbers before NaN, the larger, the lower expert
+    const bool n1 = s != s, n2 = s2 != s2;
+    const bool first = n1 != n2 ? n2 : !n1 && s != s2 ? s > s2 : my_id < id2;
+    const bool swap = pair && (slot < other) != first;
+    if (swap) {
+      s = s2;
+      my_id = id2;
+      my_z = z2;
+    }
+    still = __any(swap) ? 0 : still + 1;
+  }
+}
+
 // Weights of the chosen: thread j < k of the row holds logit z of pick j.
 // Every thread of the wave calls it; the sums run over the row's lanes (the
 // first wave's).
@@ -301,7 +347,10 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : kTopkThreads) void k_router_topk(T
     }
     int my_key = 0;
     Pick last{};
-    const int rounds = BIAS && a.k < a.E ? a.k + 1 : a.k;
+    // with a bias one pick more than the lanes hold, for the comparison; they
+    // hold the pick after the k-th too where there is a lane for it
+    const bool spare = BIAS && LPR <= 64 && a.k < LPR;
+    const int held = BIAS ? min(a.E, a.k + spare) : a.k, rounds = BIAS ? min(a.E, a.k + spare + 1) : a.k;
     for (int j = 0; j < rounds; ++j) {
       last = take_largest<LT, EPL, LPR>(key, slot, red);
       if (slot == j) {
@@ -316,31 +365,40 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : kTopkThreads) void k_router_topk(T
       // its sum, the quotient), |d| <= 88 where p is not 0 and p |d| <= 0.4: by
       // 1.3e-5 p and by 4e-6 in any case.  A sigmoid is off by 2^-24 (1.5 |z|
       // (1 - p) + 5) p: by 8.2e-6 p and by 4e-7.  The sum with the bias adds
-      // 2^-24 of itself.  Lanes j < k hold the picks and compare with the next.
-      bool close = false;
+      // 2^-24 of itself.  Lanes hold the picks and compare with the next.  The
+      // rest of the row, whose errors are at most those of its largest p, lies
+      // at the last pick or below: the first k are among the picks held
+      // unless that one is close to the k-th.
+      bool close = false, open = false;
       if (LPR <= 64 || tid < 64) {
-        const bool end = slot == a.k - 1;  // its neighbour is the pick after the k-th
-        const int id2 = end ? last.id : __shfl_down(my_id, 1, 64);
-        const int key2 = end ? last.key : __shfl_down(my_key, 1, 64);
-        if (slot < a.k) {
+        const int id2 = __shfl_down(my_id, 1, 64), key2 = __shfl_down(my_key, 1, 64);
+        const bool softmax = a.score == kRouterScoreSoftmax;
+        if (slot < held) {
           my_z = LT::load(row[my_id]);
-          const float s1 = key_value(my_key), s0 = key_value(key2);
-          if ((!end || rounds > a.k) && !(s1 - s0 > 8e-6f + 5e-7f * fabsf(s1))) {
+          const float s1 = key_value(my_key), s0 = key_value(key2), step = 5e-7f * fabsf(s1);
+          if (slot + 1 < held && !(s1 - s0 > 8e-6f + step)) {
             const float b1 = a.bias[my_id], b0 = a.bias[id2], p = fabsf(s1 - b1) + fabsf(s0 - b0);
-            const float off = a.score == kRouterScoreSoftmax ? fminf(8e-6f, 1.3e-5f * p) : fminf(8e-7f, 8.2e-6f * p);
-            close = !(s1 - s0 > off + 5e-7f * fabsf(s1)) && !(LT::load(row[id2]) == my_z && b0 == b1);
+            const float off = softmax ? fminf(8e-6f, 1.3e-5f * p) : fminf(8e-7f, 8.2e-6f * p);
+            close = !(s1 - s0 > off + step) && !(LT::load(row[id2]) == my_z && b0 == b1);
           }
+          if (slot == a.k - 1 && rounds > held)
+            open = !(s1 - key_value(last.key) > (softmax ? fminf(8e-6f, 2.6e-5f / row_sum) : 8e-7f) + step);
         }
+        open = __any(open);
         close = __any(close);
       }
       if constexpr (LPR > 64) {
         __syncthreads();
-        if (tid == 0) redi[0] = close;
+        if (tid == 0) redi[0] = open || close;
         __syncthreads();
-        close = redi[0];
+        open = redi[0];
         __syncthreads();
       }
-      if (close) select_in_64<LT, EPL, LPR>(z, b, slot, a.E, a.k, a.score, redd, redi, my_id, my_z);
+      if (open)
+        select_in_64<LT, EPL, LPR>(z, b, slot, a.E, a.k, a.score, redd, redi, my_id, my_z);
+      else if constexpr (LPR <= 64) {
+        if (close) order_in_64<EPL, LPR>(z, a.bias, slot, held, a.score, row_base, my_id, my_z);
+      }
     } else {
       my_z = key_value(my_key);
     }

@@ -80,6 +80,29 @@ def test_topk_scores_that_fp32_cannot_tell_apart(score):
     check_topk(z, 8, b, score, True)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(64, 4), (64, 16), (256, 7), (256, 8), (288, 31), (1024, 64), (1500, 8), (9, 8), (8, 8)])
+def test_topk_close_pairs_at_every_place(score, E, k):
+    # biases that bring experts' scores within a few steps of one another, in
+    # pairs and in runs, at places that differ from row to row
+    g = torch.Generator().manual_seed(E + k)
+    T = 96
+    z = torch.randn(T, E, generator=g)
+    n = min(E, 48)
+    z[:, :n] = z[0, :n]                        # the same logits in every row
+    b = 0.05 * torch.randn(E, generator=g)
+    total = 1.0 if score == "sigmoid" else None
+    p = torch.sigmoid(z[0].double()) if total else torch.softmax(z[0].double(), -1)
+    for i in range(0, n - 3, 4):               # experts i, i + 1 close; in every third group i + 2 and i + 3 too
+        for j in range(1, 4 if i % 12 == 0 else 2):
+            b[i + j] = (p[i] + b[i].double() - p[i + j]).float()
+    if score == "softmax":
+        z = z[:1].repeat(T, 1)                 # close scores need the same sum: rows differ by a shift
+        z = z + torch.randint(-3, 4, (T, 1), generator=g).float()
+    check_topk(z, k, b, score, True)
+    check_topk(z, k, b, score, False)
+
+
 def test_topk_masked_experts_and_nan():
     inf = float("inf")
     z = logits(9, 130, F32, seed=4)
