@@ -560,9 +560,9 @@ extern "C" int moe_router_topk(const void* logits, int logits_dtype, long long l
     return MOE_Q4_ERR_ALIAS;
   // Few lanes a row where there are rows enough to fill the card with them
   // (k = 8 of 256, us over 16 lanes and over 64: 16384 fp32 rows 9.9 and 15.0,
-  // bf16 8.3 and 9.6, 4096 4.7 and 4.1, 1000 4.5 and 3.0); with a bias, whose
-  // scores are formed for all of a row, many (31.9 and 30.3).
-  const RowPlan plan = row_plan(E, k, select_bias || T <= 6144);
+  // with a bias 16.7 and 20.0, bf16 8.3 and 9.6; 8192 with a bias 9.5 and
+  // 12.2, 4096 8.7 and 7.8, bf16 4.7 and 4.1; 1000 4.5 and 3.0).
+  const RowPlan plan = row_plan(E, k, T <= 6144);
   TopkArgs a{logits, select_bias, topk_ids, topk_weights, ld, T, k, E, score, renormalize, scale};
   const int threads = plan.lpr > 64 ? plan.lpr : kTopkThreads, per = threads / plan.lpr;
   const dim3 grid((T + per - 1) / per), block(threads);

@@ -135,6 +135,27 @@ def test_topk_masked_experts_and_nan():
     check_topk(logits(20, 130, F32, seed=8), 9, b, "sigmoid", True)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [40, 130, 1500])
+@pytest.mark.parametrize("T", [9, 7000])
+def test_topk_choice_of_bad_rows_with_a_bias(score, E, T):
+    inf = float("inf")
+    z = logits(T, E, F32, seed=4)
+    z[0, 10] = float("nan")
+    z[1, :] = -inf
+    z[2, :] = float("nan")
+    z[3, 5] = inf
+    z[4, 3:] = -inf
+    z[5, :] = 0.25
+    b = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(E))
+    b[7] = -inf
+    for bias in (b, torch.zeros(E)):
+        ids, _ = R.route(z.double().numpy(), 6, bias.double().numpy(), score, True, 1.0)
+        gi, gw = q.moe_router_topk(z.cuda(), 6, select_bias=bias.cuda(), score=score)
+        assert np.array_equal(gi.cpu().numpy(), ids)
+        assert torch.isfinite(gw[6:]).all()
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("E", [64, 100, 1500])
 def test_topk_strided_logits(dtype, E):
