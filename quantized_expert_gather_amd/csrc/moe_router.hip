@@ -148,11 +148,12 @@ __device__ void select_in_64(const float (&z)[EPL], const float (&b)[EPL], int s
       if (((open >> i) & 1u) && (double)z[i] > m) m = (double)z[i];
     m = all(m, true);
     for (int i = 0; i < EPL; ++i) {
-      s[i] = ((open >> i) & 1u) && m > -__builtin_inf() ? exp((double)z[i] - m) : 0.0;
+      // (NaN stays NaN, also in a row of nothing else)
+      s[i] = !((open >> i) & 1u) ? 0.0 : z[i] != z[i] || m > -__builtin_inf() ? exp((double)z[i] - m) : 0.0;
       sum += s[i];
     }
     sum = all(sum, false);
-    for (int i = 0; i < EPL; ++i) s[i] = (m > -__builtin_inf() ? s[i] / sum : 0.0) + (double)b[i];
+    for (int i = 0; i < EPL; ++i) s[i] = (sum == 0.0 ? 0.0 : s[i] / sum) + (double)b[i];
   } else {
     for (int i = 0; i < EPL; ++i) s[i] = 1.0 / (1.0 + exp(-(double)z[i])) + (double)b[i];
   }
