@@ -367,12 +367,12 @@ int moe_sort_pairs(const int32_t *topk_ids, int L, int k, int E, int bm, int32_t
  * deterministic.  Outside the usual range: an infinite or NaN x gives its own
  * token's outputs as infinities or NaN (not always the one the sum itself
  * gives); an E8M0 or E4M3 NaN scale its own row's.  mxfp4 products of elements
- * below 2^-126 are taken as 0, and with more than 16 tokens so are fp16 ones
+ * below 2^-126 are taken as 0, and with more than 16 tokens so may be fp16 ones
  * 2^-126 below their row's largest block; sums may be infinite where |x| times
  * a code's 31 is past fp32.  With more than 16 tokens affine scales 2^-34
  * below the largest of their row, and bf16 x 2^-39 below the largest of their
- * token, lose bits, and for bf16 results the groups' b + 8 s and sums of x
- * count to 16 bits each.
+ * token, may lose bits, and for bf16 results the groups' b + 8 s and sums of x
+ * may count to 16 bits each.
  * L == 0 returns MOE_Q4_OK without touching the GPU.  Needs
  * L <= MOE_Q4_LINEAR_MAX_L, N <= MOE_Q4_LINEAR_MAX_N, K <= MOE_Q4_LINEAR_MAX_K,
  * ldx <= MOE_Q4_LINEAR_MAX_LDX.
