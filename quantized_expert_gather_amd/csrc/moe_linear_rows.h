@@ -26,7 +26,7 @@
 // Loads with a streaming hint were slower (60 us).  Small products take what a
 // launch, x's way through LDS to registers, one round of weights and the
 // waves' reduction take in sequence: 1 x 256 x 6144 5.9 us, 1 x 6144 x 6144 (21
-// MB) 10.0, 7 x 4099 x 4096 11.0, 16 x 4096 x 4096 6.3 (mxfp4) to 8.0
+// MB) 10.0, 7 x 4099 x 4096 9.2, 16 x 4096 x 4096 6.3 (mxfp4) to 8.0
 // (affine4_g64).
 #pragma once
 
