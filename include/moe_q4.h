@@ -367,8 +367,8 @@ int moe_sort_pairs(const int32_t *topk_ids, int L, int k, int E, int bm, int32_t
  * deterministic.  Outside the usual range: an infinite or NaN x gives its own
  * token's outputs as infinities or NaN (not always the one the sum itself
  * gives); an E8M0 or E4M3 NaN scale its own row's.  mxfp4 products of elements
- * below 2^-126 are taken as 0, and with more than 16 tokens so may be fp16 ones
- * 2^-126 below their row's largest block; sums may be infinite where |x| times
+ * below 2^-126 are taken as 0, and elements of 2^128 and more may be infinite;
+ * sums may be infinite where |x| times
  * a code's 31 is past fp32.  With more than 16 tokens affine scales 2^-34
  * below the largest of their row, and bf16 x 2^-39 below the largest of their
  * token, may lose bits, and for bf16 results the groups' b + 8 s and sums of x

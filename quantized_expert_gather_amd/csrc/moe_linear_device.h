@@ -97,6 +97,21 @@ __device__ __forceinline__ uint4 lin_fp4_pow2(uint32_t w, float s) {
                       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3)));
 }
 
+// fp16 values as two bf16 terms, hi + lo: 11 bits as 8 + 3, both exact.
+__device__ __forceinline__ void lin_two_terms(lin_u32x4 v, lin_u32x4& hi, lin_u32x4& lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t word = v[i];
+    const lin_f16x2 h = __builtin_bit_cast(lin_f16x2, word);
+    const float f0 = (float)h.x, f1 = (float)h.y;
+    const uint32_t h0 = __float_as_uint(f0) & 0xFFFF0000u, h1 = __float_as_uint(f1) & 0xFFFF0000u;
+    // (an infinite or NaN value has no second term)
+    const float r0 = f0 - __uint_as_float(h0), r1 = f1 - __uint_as_float(h1);
+    hi[i] = h0 >> 16 | h1;
+    lo[i] = (r0 == r0 ? __float_as_uint(r0) >> 16 : 0u) | (r1 == r1 ? __float_as_uint(r1) & 0xFFFF0000u : 0u);
+  }
+}
+
 // Value of byte B of a word of E4M3 bytes.
 template <int B>
 __device__ __forceinline__ float lin_e4m3(uint32_t w) {

@@ -146,7 +146,7 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
   if constexpr (kRowsScaled) {
     a.wexp = reinterpret_cast<int32_t*>(ws + lay.wexp);
     PrepareArgs q{};
-    q.x = l.x; q.s = l.s; q.b = l.b;
+    q.x = l.x; q.w = l.w; q.s = l.s; q.b = l.b;
     q.wexp = reinterpret_cast<int32_t*>(ws + lay.wexp);
     q.ldx = l.ldx;
     q.L = l.L; q.N = l.N; q.K = l.K; q.G = a.G; q.Gp = a.Gp;

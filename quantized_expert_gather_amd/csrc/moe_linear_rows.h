@@ -208,20 +208,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_rows(LinearArgs a) {
     for (int st = 0; st < S; ++st)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (kTerms) {
-          const lin_u32x4 v = xf[st][j][0];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // 11 bits as 8 + 3, both exact
-            const uint32_t word = v[i];
-            const lin_f16x2 h = __builtin_bit_cast(lin_f16x2, word);
-            const float f0 = (float)h.x, f1 = (float)h.y;
-            const uint32_t h0 = __float_as_uint(f0) & 0xFFFF0000u, h1 = __float_as_uint(f1) & 0xFFFF0000u;
-            // (an infinite or NaN x has no second term)
-            const float r0 = f0 - __uint_as_float(h0), r1 = f1 - __uint_as_float(h1);
-            xf[st][j][0][i] = h0 >> 16 | h1;
-            xf[st][j][kX - 1][i] = (r0 == r0 ? __float_as_uint(r0) >> 16 : 0u) | (r1 == r1 ? __float_as_uint(r1) & 0xFFFF0000u : 0u);
-          }
-        }
+        if constexpr (kTerms) lin_two_terms(xf[st][j][0], xf[st][j][0], xf[st][j][kX - 1]);
       }
     if constexpr (kAffine) {  // x times ones is the group sums, in the layout of the products
       const uint32_t one = F16 ? 0x3C003C00u : 0x3F803F80u;

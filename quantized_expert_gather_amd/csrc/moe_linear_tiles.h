@@ -5,7 +5,9 @@
 // all of K in the accumulators with no work per scale group:
 //   nvfp4    e2m1 * e4m3, exact in both types;
 //   mxfp4    e2m1 * 2^e: exact in bf16; in fp16 with e counted from the row's
-//            largest, whose power of two multiplies the row's result;
+//            largest, whose power of two multiplies the row's result (exact
+//            for the 35 powers of two below it; tiles with a wide row, one
+//            with other codes than 0 below these, see `wide`);
 //   affine   s * (q - 8): 8 + 3 significant bits, exact in fp16's 11, with s
 //            divided by a power of two near its row's largest.  bf16 tokens
 //            are divided by a power of two near their largest value likewise
@@ -47,7 +49,7 @@ struct TilesArgs {
   const uint16_t* tsum;    // affine: bf16 terms of b + 8 s [3][N][Gp]
   const uint16_t* xsum;    // affine: bf16 terms of the group sums [3][L][Gp]
   const int32_t* xexp;     // power of two of each token (affine with bf16 tokens), or NULL
-  const int32_t* wexp;     // power of two of each row (affine; mxfp4 with fp16 tokens), or NULL
+  const int32_t* wexp;     // power of two of each row (affine; mxfp4 with fp16 tokens) and kLinWide, or NULL
   const float* bias;
   void* out;
   float* part;             // split K: [splits][L][N] partial sums
@@ -62,6 +64,10 @@ struct TilesArgs {
   int stagger;             // steps between the token tiles' first ones
   int row_tiles, tok_tiles;
 };
+
+// A row's power of two is the low half of its word, the marks lie above.
+constexpr int kLinWide = 1 << 16;  // one fp16 power of two does not fit the row
+__device__ __forceinline__ int lin_exponent(int v) { return (int)(int16_t)v; }
 
 __device__ __forceinline__ lin_f16x2 lin_h2(uint32_t v) { return __builtin_bit_cast(lin_f16x2, v); }
 __device__ __forceinline__ uint32_t lin_u(lin_f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
@@ -103,6 +109,7 @@ template <int FMT, bool F16, int MT, int NT>
 __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
   constexpr int kTok = 16 * MT, kRows = 64 * NT;
   constexpr bool kTiledX = lin_affine(FMT);  // the laid-out copy
+  __shared__ int wide_waves[4];
   // Two objects, each named where it is used: the compiler then knows that
   // reads of one do not wait for the copies into the other.
   __shared__ __attribute__((aligned(1024))) unsigned char lds0[kTok * 256], lds1[kTok * 256];
@@ -143,9 +150,14 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
   }
   constexpr bool kScaled = lin_affine(FMT) || (FMT == kLinMxfp4 && F16);
   int wexp[NT];
-  if constexpr (lin_affine(FMT) || (FMT == kLinMxfp4 && F16)) {  // the same lanes' rows as the codes'
+  bool wide = false;
+  if constexpr (kScaled) {  // the same lanes' rows as the codes'
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) wexp[nt] = a.wexp[row[nt]];
+    for (int nt = 0; nt < NT; ++nt) {
+      wexp[nt] = a.wexp[row[nt]];
+      wide |= (wexp[nt] & kLinWide) != 0;
+      wexp[nt] = lin_exponent(wexp[nt]);
+    }
   }
 
   if constexpr (lin_affine(FMT)) {
@@ -263,8 +275,13 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
     load(step, cw, sw);
   }
 
+  if constexpr (kScaled) {
+    wide = __any(wide);
+    if (lane == 0) wide_waves[wave] = wide;
+  }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
+  if constexpr (kScaled) wide = (wide_waves[0] | wide_waves[1] | wide_waves[2] | wide_waves[3]) != 0;
   const LinCode code = lin_code<true>();
   int i = 0;
   auto body = [&](unsigned char* xb, unsigned char* other) __attribute__((always_inline)) {
@@ -325,6 +342,45 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
     }
     ++i;
   };
+  // A workgroup with a wide row: the rows' own powers of two in bf16 operands,
+  // tokens from memory as two bf16 terms.  Every product is exact as before;
+  // twice the matrix instructions and none of the staging (2048 x 6144 x 4096
+  // with such a row in every tile: 410 us, 102 with none).
+  if constexpr (FMT == kLinMxfp4 && F16) {
+    if (wide) {
+      uint32_t from[MT];  // (the last token's rows stand for those past it)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) from[mt] = (uint32_t)(min(tok0 + 16 * mt + n16, a.L - 1) - tok0) * (uint32_t)(2 * a.ldx);
+      const unsigned char* xrow = reinterpret_cast<const unsigned char*>(a.x) + (size_t)tok0 * a.ldx * 2;
+#pragma unroll 1
+      for (int s = step0; s < step1; ++s) {
+        load(s, cw, sw);
+        const int k = s * kLinStep + 32 * kb;
+        const bool dead = k >= a.K;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          uint4 wf[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t c01 = j & 1 ? cw[nt][1] : cw[nt][0], c23 = j & 1 ? cw[nt][3] : cw[nt][2];
+            wf[nt] = lin_fp4_pow2<false>(dead ? 0u : j & 2 ? c23 : c01, lin_e8m0(sw[nt]));
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            lin_u32x4 x = {0, 0, 0, 0}, hi, lo;
+            if (!dead) x = *reinterpret_cast<const lin_u32x4*>(xrow + (from[mt] + 2u * (uint32_t)(k + 8 * j)));
+            lin_two_terms(x, hi, lo);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              acc[mt][nt] = lin_mfma<false>(wf[nt], hi, acc[mt][nt]);
+              acc[mt][nt] = lin_mfma<false>(wf[nt], lo, acc[mt][nt]);
+            }
+          }
+        }
+      }
+      i = count;
+    }
+  }
   while (i < count) {
     body(lds0, lds1);
     if (i >= count) break;
@@ -338,6 +394,7 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
   // token tiles of a pass, 16-byte pieces of a token's rows; two waves' share fits each buffer
   constexpr int kHalf = NT > 2 ? MT / 2 : MT, kPass = kHalf < 4 ? kHalf : 4, kQuads = 4 * NT;
   static_assert(2 * kPass * 16 * kQuads * 16 <= kTok * 256, "the waves' output fits the token buffers");
+  const int units = wide ? 0 : -1;  // (a mask: a branch here would part the loads below)
   unsigned char* mine = (wave < 2 ? lds0 : lds1) + (wave & 1) * (kPass * 16 * kQuads * 16);
 #pragma unroll
   for (int m0 = 0; m0 < MT; m0 += kPass) {
@@ -358,7 +415,8 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
       if constexpr (kScaled) {
         const int xe = lin_affine(FMT) && a.xexp ? a.xexp[t] : 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_ldexpf(v[e], xe + a.wexp[min(n + e, a.N - 1)]);
+        for (int e = 0; e < 4; ++e)
+          v[e] = __builtin_amdgcn_ldexpf(v[e], (xe + lin_exponent(a.wexp[min(n + e, a.N - 1)])) & units);
       }
       if (a.splits > 1) {
         store4<float>(a.part + ((size_t)split * a.L + t) * a.N + n, a.N - n, v[0], v[1], v[2], v[3]);
@@ -398,6 +456,7 @@ __device__ __forceinline__ void split_terms(float v, uint32_t (&t)[3]) {
 // 29.8 with a wave a row and a group a lane).
 struct PrepareArgs {
   const uint16_t* x;
+  const uint32_t* w;
   const unsigned char* s;
   const unsigned char* b;
   uint16_t* xq;
@@ -491,12 +550,25 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
   if (n >= (size_t)a.N) return;  // a row's threads together
   int m = 0;
   if constexpr (FMT == kLinMxfp4) {
+    int least = 255;
     for (int g = sub; g < a.G; g += P) {
       const int e = a.s[n * a.G + g];
       m = max(m, e == 255 ? 0 : e);
+      least = min(least, e);
     }
     for (int o = P / 2; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o, 64));
-    if (sub == 0) a.wexp[n] = m - 127 - 12;  // the largest block's elements reach 6 * 2^12
+    // The largest block's elements reach 6 * 2^12, the smallest, 0.5 of a
+    // block 2^35 below, fp16's smallest number 2^-24; further down only zeros are exact.
+    int wide = 0;
+    if (least < m - 35) {
+      for (int g = sub; g < a.G; g += P) {
+        if (a.s[n * a.G + g] >= m - 35) continue;
+        const uint4 c = *reinterpret_cast<const uint4*>(a.w + n * (a.K / 8) + 4 * (size_t)g);
+        wide |= ((c.x | c.y | c.z | c.w) & 0x77777777u) != 0;
+      }
+    }
+    for (int o = P / 2; o > 0; o >>= 1) wide |= __shfl_xor(wide, o, 64);
+    if (sub == 0) a.wexp[n] = ((m - 127 - 12) & 0xFFFF) | (wide ? kLinWide : 0);
   } else if constexpr (lin_affine(FMT)) {
     // eight bf16 from group g on, zeros past the row (whose start has any alignment)
     auto eight = [&](const unsigned char* base, int g, uint16_t (&v)[8]) __attribute__((always_inline)) {
@@ -535,7 +607,7 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
       for (int p = 0; p < 3; ++p)
         if (p < a.terms) *reinterpret_cast<uint4*>(a.tsum + ((size_t)p * a.N + n) * a.Gp + g) = make_uint4(t[p][0], t[p][1], t[p][2], t[p][3]);
     }
-    if (sub == 0) a.wexp[n] = e;
+    if (sub == 0) a.wexp[n] = e & 0xFFFF;
   }
 }
 

@@ -1,0 +1,81 @@
+"""Dense 4-bit products whose scales, biases or activations span a wide range,
+on both sides of the rule that gives a call to the few tokens' or the many
+tokens' kernel (needs an MI355X).
+
+The bound is operator_refs.linear_reference's: fp32 sums of exact products,
+relative to the magnitudes that meet.  Where the large scales meet zeros of x
+(or the large x zeros of the weights) these magnitudes are the small ones', so
+nothing may be lost beside a row's or a token's largest value."""
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_expert_gather_amd as q
+from tests import operator_refs as R
+
+pytestmark = pytest.mark.gpu
+
+AFFINE = ["affine4_g64", "affine4_g32"]
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+# affine sizes that are past the rule (many groups; split K) and one short input
+AFFINE_TILES = [(1500, 1400, 256), (300, 110, 16448), (40, 50, 64)]
+
+
+def by_tiles(codec, L, N, K):
+    """Whether an affine call goes to the many tokens' kernel, by the room for its copy of the tokens."""
+    return q.moe_linear_codec_workspace_bytes(codec, L, N, K) >= 2 * L * K
+
+
+def forward(codec, x, w, s, b, ot=F32, bias=None):
+    return q.moe_linear_codec_forward(codec, x.cuda(), w[0].cuda(), s[0].cuda(), None if b is None else b[0].cuda(),
+                                      bias=bias, out_dtype=ot)
+
+
+def check(out, ref, bound, dtype=F32):
+    got = out.double().cpu().numpy()
+    lim = bound + R.HALF_STEP[dtype] * (np.abs(ref) + bound) + R.HALF_TINY[dtype]
+    bad = ~(np.abs(got - ref) <= lim)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), got[bad][:4], ref[bad][:4])
+
+
+def activations(L, K, dtype, seed=7):
+    return torch.randn(L, K, generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+# ---- mxfp4 with fp16 tokens: block exponents far apart in one row ----
+
+@pytest.mark.parametrize("xt", [F16, BF16])
+@pytest.mark.parametrize("L,N,K", [(16, 48, 256), (17, 48, 256), (300, 300, 4160), (200, 131, 288)])
+def test_mxfp4_blocks_far_below_their_rows_largest(xt, L, N, K):
+    print("[case] mxfp4 blocks far apart", xt, L, N, K, flush=True)
+    w, s, _ = R.linear_weights("mxfp4", N, K, 31)
+    x = activations(L, K, xt)
+    x[:, :32] = 0                       # nothing meets the large block
+    for i, d in enumerate((30, 34, 35, 36, 37, 40, 48, 60, 100)):
+        s[0, i, :] = 120
+        s[0, i, 0] = 120 + d
+        s[0, i + 9, 1:] = 120           # the small block in the middle
+        s[0, i + 9, 2] = 120 - d
+    s[0, 20, 0], s[0, 20, 3], s[0, 20, 4] = 200, 150, 110
+    s[0, 21, 1:] = 0                    # 2^-127 under zero codes, as for a block of zeros
+    w[0, 21, 4:] = 0
+    s[0, 22, 5] = 0
+    w[0, 22, 20:24] = int(np.uint32(0x88888888).view(np.int32))  # and minus zeros
+    ref, bound = R.linear_reference("mxfp4", x, w, s, None, None)
+    check(forward("mxfp4", x, w, s, None), ref, bound + K * 2.0 ** -126)
+
+
+def test_mxfp4_large_block_meets_some_tokens_only():
+    L, N, K = 150, 70, 512
+    w, s, _ = R.linear_weights("mxfp4", N, K, 32)
+    x = activations(L, K, F16)
+    x[::2, :32] = 0
+    s[0, 3, 0] = 180
+    s[0, 3, 1:] = 121
+    s[0, 69, 0] = 171
+    s[0, 69, 7] = 255                   # a NaN beside it stays its row's
+    ref, bound = R.linear_reference("mxfp4", x, w, s, None, None)
+    out = forward("mxfp4", x, w, s, None)
+    assert torch.isnan(out[:, 69]).all()
+    check(out[:, :69], ref[:, :69], bound[:, :69])
