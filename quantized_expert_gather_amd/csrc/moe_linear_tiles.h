@@ -581,16 +581,33 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
       }
     };
     uint16_t s[8], b[8];
-    for (int g = 8 * sub; g < a.G; g += 8 * P) {
-      eight(a.s, g, s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, (int)(s[i] & 0x7FFFu));
-    }
-    for (int o = P / 2; o > 0; o >>= 1) m = max(m, __shfl_xor(m, o, 64));
-    const int e = m ? min(max(m >> 7, 1), 254) - 127 - 8 : 0;  // the largest falls in [2^8, 2^9): 24 s in 2^14
+    int mb = 0;  // the largest finite bias
     for (int g = 8 * sub; g < a.Gp; g += 8 * P) {
       eight(a.s, g, s);
       eight(a.b, g, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m = max(m, (int)(s[i] & 0x7FFFu));
+        const int v = b[i] & 0x7FFFu;
+        mb = max(mb, v < 0x7F80 ? v : 0);
+      }
+    }
+    for (int o = P / 2; o > 0; o >>= 1) {
+      m = max(m, __shfl_xor(m, o, 64));
+      mb = max(mb, __shfl_xor(mb, o, 64));
+    }
+    // The largest scale falls in [2^8, 2^9), 24 s in 2^14; with biases 2^68 and
+    // more above the scales, lower: the rest, at most K 2^16 (|b| + 8 |s|) in its
+    // token's units, then stays below 2^110 in the row's.  (A scale that loses
+    // bits there counts 2^-85 of the bias.)
+    const int es = min(max(m >> 7, 1), 254) - 127 - 8, eb = (mb >> 7) - 127 - 68;
+    const int e = m == 0 ? max(eb, 0) : max(es, eb);
+    const bool again = a.Gp > 8 * P;  // else they are at hand
+    for (int g = 8 * sub; g < a.Gp; g += 8 * P) {
+      if (again) {
+        eight(a.s, g, s);
+        eight(a.b, g, b);
+      }
       uint32_t h[4], t[3][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

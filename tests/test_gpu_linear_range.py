@@ -79,3 +79,29 @@ def test_mxfp4_large_block_meets_some_tokens_only():
     out = forward("mxfp4", x, w, s, None)
     assert torch.isnan(out[:, 69]).all()
     check(out[:, :69], ref[:, :69], bound[:, :69])
+
+
+# ---- affine: scales far below the biases, and far apart in a row ----
+
+@pytest.mark.parametrize("codec", AFFINE)
+@pytest.mark.parametrize("xt", [BF16, F16])
+@pytest.mark.parametrize("L,N,K", AFFINE_TILES + [(5, 50, 256)])
+def test_affine_scales_far_below_the_biases(codec, xt, L, N, K):
+    print("[case] affine scales far below biases", codec, xt, L, N, K, flush=True)
+    assert by_tiles(codec, L, N, K) == (L > 5)
+    w, s, b = R.linear_weights(codec, N, K, 33)
+    x = activations(L, K, xt)
+    g = torch.Generator().manual_seed(3)
+    rb = torch.randn(b[0].shape, generator=g)
+    for i, e in enumerate((-126, -120, -110, -100, -90, -70, -60, -50, -40, -24)):
+        s[0, i] = 2.0 ** e              # a row of constants whose scale was kept from being zero
+        b[0, i] = rb[i].to(BF16)
+    s[0, 10] = 0.0
+    b[0, 10] = rb[10].to(BF16)
+    s[0, 11] = 0.0
+    b[0, 11] = (rb[11] * 2.0 ** 75).to(BF16)
+    b[0, 12] = (rb[12] * 2.0 ** 80).to(BF16)
+    s[0, 13] = 2.0 ** -100
+    b[0, 13] = (rb[13] * 2.0 ** -20).to(BF16)
+    ref, bound = R.linear_reference(codec, x, w, s, b, None)
+    check(forward(codec, x, w, s, b), ref, bound + K * 2.0 ** -126)
