@@ -130,7 +130,7 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
   const TilesPlan p = tiles_plan(l.L, l.N, l.K);
   const TilesWorkspace lay = tiles_layout(FMT, l.L, l.N, l.K);
   TilesArgs a{};
-  a.x = l.x; a.w = l.w; a.s = l.s;
+  a.x = a.xraw = l.x; a.w = l.w; a.s = l.s; a.b = l.b;
   a.bias = l.bias; a.out = l.out;
   a.ldx = l.ldx; a.ldo = l.ldo;
   a.L = l.L; a.N = l.N; a.K = l.K;

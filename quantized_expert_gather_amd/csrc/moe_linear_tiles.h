@@ -9,11 +9,10 @@
 //            for the 35 powers of two below it; tiles with a wide row, one
 //            with other codes than 0 below these, see `wide`);
 //   affine   s * (q - 8): 8 + 3 significant bits, exact in fp16's 11, with s
-//            divided by a power of two near its row's largest.  bf16 tokens
+//            divided by a power of two near its row's largest (down to 2^-26
+//            of that; rows with smaller scales are wide too).  bf16 tokens
 //            are divided by a power of two near their largest value likewise
-//            and held in fp16.  What lies 2^-34 (weights) or 2^-39 (tokens)
-//            below the largest of its row loses bits, far below fp32's own
-//            rounding of the sum.
+//            and held in fp16, where values 2^-32 below it lose bits.
 // The affine rest, sum over groups of (b + 8 s) X with X = sum of the group's
 // x, is a product over K / group columns; it starts the accumulators, both
 // factors as two or three bf16 terms.
@@ -43,8 +42,10 @@ namespace moeq4 {
 
 struct TilesArgs {
   const uint16_t* x;       // tokens in operand type and order
+  const uint16_t* xraw;    // tokens as given, ldx apart
   const uint32_t* w;
-  const unsigned char* s;  // scales as given (nvfp4, mxfp4)
+  const unsigned char* s;  // scales as given
+  const unsigned char* b;  // biases as given (affine)
   const uint16_t* sh;      // affine: fp16 scales over their row's power of two [N][Gp]
   const uint16_t* tsum;    // affine: bf16 terms of b + 8 s [3][N][Gp]
   const uint16_t* xsum;    // affine: bf16 terms of the group sums [3][L][Gp]
@@ -73,11 +74,26 @@ __device__ __forceinline__ lin_f16x2 lin_h2(uint32_t v) { return __builtin_bit_c
 __device__ __forceinline__ uint32_t lin_u(lin_f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
 
 // s * (q - 8) of a word's codes in fp16: one fused multiply-add a pair, its
-// addend -24 s exact (9 significant bits) and its result too.
+// addend -24 s exact (10 significant bits) and its result too.
 __device__ __forceinline__ uint4 lin_affine_f16(uint32_t w, LinCode code, lin_f16x2 s, lin_f16x2 m24s) {
   const uint4 c = lin_codes16<true>(w, code);
   return make_uint4(lin_u(__builtin_elementwise_fma(lin_h2(c.x), s, m24s)), lin_u(__builtin_elementwise_fma(lin_h2(c.y), s, m24s)),
                     lin_u(__builtin_elementwise_fma(lin_h2(c.z), s, m24s)), lin_u(__builtin_elementwise_fma(lin_h2(c.w), s, m24s)));
+}
+
+// q - 8 of a word's codes, exact, in lin_codes16's order.
+template <bool F16>
+__device__ __forceinline__ uint4 lin_centred(uint32_t w, LinCode code) {
+  if constexpr (F16) {
+    const lin_f16x2 one = {(_Float16)1.0f, (_Float16)1.0f}, m24 = {(_Float16)-24.0f, (_Float16)-24.0f};
+    return lin_affine_f16(w, code, one, m24);
+  } else {
+    const uint4 c = lin_codes16<false>(w, code);
+    auto two = [](uint32_t v) {
+      return __builtin_amdgcn_perm(__float_as_uint(bf16_hi_to_f32(v) - 24.0f), __float_as_uint(bf16_lo_to_f32(v) - 24.0f), 0x07060302u);
+    };
+    return make_uint4(two(c.x), two(c.y), two(c.z), two(c.w));
+  }
 }
 
 // The scale of a row's 32 inputs from k on (nvfp4: two scales), as stored.
@@ -149,13 +165,12 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
       for (int nt = 0; nt < NT; ++nt) asm volatile("" : "+v"(acc[mt][nt]));
   }
   constexpr bool kScaled = lin_affine(FMT) || (FMT == kLinMxfp4 && F16);
-  int wexp[NT];
-  bool wide = false;
+  int wexp[NT], marks = 0;
   if constexpr (kScaled) {  // the same lanes' rows as the codes'
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       wexp[nt] = a.wexp[row[nt]];
-      wide |= (wexp[nt] & kLinWide) != 0;
+      marks |= wexp[nt];
       wexp[nt] = lin_exponent(wexp[nt]);
     }
   }
@@ -276,12 +291,11 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
   }
 
   if constexpr (kScaled) {
-    wide = __any(wide);
-    if (lane == 0) wide_waves[wave] = wide;
+    const int wide_rows = __any(marks & kLinWide);
+    if (lane == 0) wide_waves[wave] = wide_rows;
   }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if constexpr (kScaled) wide = (wide_waves[0] | wide_waves[1] | wide_waves[2] | wide_waves[3]) != 0;
   const LinCode code = lin_code<true>();
   int i = 0;
   auto body = [&](unsigned char* xb, unsigned char* other) __attribute__((always_inline)) {
@@ -342,49 +356,112 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
     }
     ++i;
   };
-  // A workgroup with a wide row: the rows' own powers of two in bf16 operands,
-  // tokens from memory as two bf16 terms.  Every product is exact as before;
-  // twice the matrix instructions and none of the staging (2048 x 6144 x 4096
-  // with such a row in every tile: 410 us, 102 with none).
-  if constexpr (FMT == kLinMxfp4 && F16) {
-    if (wide) {
-      uint32_t from[MT];  // (the last token's rows stand for those past it)
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) from[mt] = (uint32_t)(min(tok0 + 16 * mt + n16, a.L - 1) - tok0) * (uint32_t)(2 * a.ldx);
-      const unsigned char* xrow = reinterpret_cast<const unsigned char*>(a.x) + (size_t)tok0 * a.ldx * 2;
-#pragma unroll 1
-      for (int s = step0; s < step1; ++s) {
-        load(s, cw, sw);
-        const int k = s * kLinStep + 32 * kb;
-        const bool dead = k >= a.K;
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          uint4 wf[NT];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t c01 = j & 1 ? cw[nt][1] : cw[nt][0], c23 = j & 1 ? cw[nt][3] : cw[nt][2];
-            wf[nt] = lin_fp4_pow2<false>(dead ? 0u : j & 2 ? c23 : c01, lin_e8m0(sw[nt]));
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            lin_u32x4 x = {0, 0, 0, 0}, hi, lo;
-            if (!dead) x = *reinterpret_cast<const lin_u32x4*>(xrow + (from[mt] + 2u * (uint32_t)(k + 8 * j)));
-            lin_two_terms(x, hi, lo);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              acc[mt][nt] = lin_mfma<false>(wf[nt], hi, acc[mt][nt]);
-              acc[mt][nt] = lin_mfma<false>(wf[nt], lo, acc[mt][nt]);
-            }
-          }
-        }
-      }
-      i = count;
-    }
-  }
   while (i < count) {
     body(lds0, lds1);
     if (i >= count) break;
     body(lds1, lds0);
+  }
+
+  // A workgroup with a wide row starts again: its tokens from memory as they
+  // are, every product exact, and the sums in their own units.  mxfp4: the
+  // blocks' powers of two in bf16 operands, x as two bf16 terms.  Affine: the
+  // words transposed over the lanes, so that a product is one group's, and
+  // its fp32 sum times the scale, plus b + 8 s times the group's sum of x.
+  // (2048 x 6144 x 4096 with such a row in every tile: mxfp4 476 us, 102 with
+  // none; affine4_g64 826 and 137, 128 tokens x 4096 x 4096 53 and 23.)
+  bool wide = false;
+  if constexpr (kScaled) {
+    wide = (wide_waves[0] | wide_waves[1] | wide_waves[2] | wide_waves[3]) != 0;
+    if (wide) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          acc[mt][nt] = lin_f32x4{0, 0, 0, 0};
+          asm volatile("" : "+v"(acc[mt][nt]));  // (hides the zeros, as above)
+        }
+      uint32_t from[MT];  // (the last token's rows stand for those past it)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) from[mt] = (uint32_t)(min(tok0 + 16 * mt + n16, a.L - 1) - tok0) * (uint32_t)(2 * a.ldx);
+      const unsigned char* xrow = reinterpret_cast<const unsigned char*>(a.xraw) + (size_t)tok0 * a.ldx * 2;
+      auto piece_at = [&](int mt, int k) __attribute__((always_inline)) {  // eight inputs of token n16 of a tile
+        return *reinterpret_cast<const lin_u32x4*>(xrow + (from[mt] + 2u * (uint32_t)k));
+      };
+      if constexpr (lin_affine(FMT)) {
+        constexpr int kPer = lin_group(FMT) / 32, kGroups = 4 / kPer;  // blocks of a group, groups of a step
+        const LinCode own = lin_code<F16>();
+        const uint32_t one = F16 ? 0x3C003C00u : 0x3F803F80u;
+        const uint4 ones = make_uint4(one, one, one, one);
+#pragma unroll 1
+        for (int s = step0; s < step1; ++s) {
+          load(s, cw, sw);
+          // one row tile at a time, and its tokens again: what that takes fits the registers beside the sums
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t words[4] = {cw[nt][0], cw[nt][1], cw[nt][2], cw[nt][3]};
+            lin_transpose(words);
+#pragma unroll 1
+            for (int g = 0; g < kGroups; ++g) {
+              const int group = s * kGroups + g;
+              if (group >= a.G) break;
+              uint4 wf[kPer];
+#pragma unroll
+              for (int p = 0; p < kPer; ++p) wf[p] = lin_centred<F16>(words[p], own);
+#pragma unroll
+              for (int j = 0; j + kPer < 4; ++j) words[j] = words[j + kPer];  // the next group's
+              float scale[4], rest[4];  // s and b + 8 s of the rows whose sums the lane holds
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const size_t at = (size_t)min(row0 + 16 * nt + 4 * kb + e, a.N - 1) * a.G + group;
+                scale[e] = bf16_to_f32(reinterpret_cast<const uint16_t*>(a.s)[at]);
+                rest[e] = __builtin_fmaf(8.0f, scale[e], bf16_to_f32(reinterpret_cast<const uint16_t*>(a.b)[at]));
+              }
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                lin_f32x4 c = {0, 0, 0, 0}, sum = {0, 0, 0, 0};  // sum: of the token's x, the same in all four
+#pragma unroll
+                for (int p = 0; p < kPer; ++p) {
+                  const uint4 xf = lin_pair_order(__builtin_bit_cast(uint4, piece_at(mt, s * kLinStep + 32 * (g * kPer + p) + 8 * kb)));
+                  c = lin_mfma<F16>(wf[p], xf, c);
+                  sum = lin_mfma<F16>(ones, xf, sum);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  acc[mt][nt][e] = __builtin_fmaf(scale[e], c[e], __builtin_fmaf(rest[e], sum[e], acc[mt][nt][e]));
+                if (mt % 2) __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int s = step0; s < step1; ++s) {
+          load(s, cw, sw);
+          const int k = s * kLinStep + 32 * kb;
+          const bool dead = k >= a.K;
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {
+            uint4 wf[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t c01 = j & 1 ? cw[nt][1] : cw[nt][0], c23 = j & 1 ? cw[nt][3] : cw[nt][2];
+              wf[nt] = lin_fp4_pow2<false>(dead ? 0u : j & 2 ? c23 : c01, lin_e8m0(sw[nt]));
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              lin_u32x4 x = {0, 0, 0, 0}, hi, lo;
+              if (!dead) x = piece_at(mt, k + 8 * j);
+              lin_two_terms(x, hi, lo);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                acc[mt][nt] = lin_mfma<false>(wf[nt], hi, acc[mt][nt]);
+                acc[mt][nt] = lin_mfma<false>(wf[nt], lo, acc[mt][nt]);
+              }
+            }
+          }
+        }
+      }
+    }
   }
 
   // Lane (n16, kb) holds token n16 of each token tile and rows 4 kb .. + 3 of
@@ -581,25 +658,26 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
       }
     };
     uint16_t s[8], b[8];
-    int mb = 0;  // the largest finite bias
+    int mb = 0, least = 0x7FFF;  // the largest finite bias, the least scale of 2^-96 and more
     for (int g = 8 * sub; g < a.Gp; g += 8 * P) {
       eight(a.s, g, s);
       eight(a.b, g, b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        m = max(m, (int)(s[i] & 0x7FFFu));
-        const int v = b[i] & 0x7FFFu;
+        const int u = s[i] & 0x7FFFu, v = b[i] & 0x7FFFu;
+        m = max(m, u);
+        least = min(least, u >= (127 - 96) << 7 ? u : 0x7FFF);
         mb = max(mb, v < 0x7F80 ? v : 0);
       }
     }
     for (int o = P / 2; o > 0; o >>= 1) {
       m = max(m, __shfl_xor(m, o, 64));
       mb = max(mb, __shfl_xor(mb, o, 64));
+      least = min(least, __shfl_xor(least, o, 64));
     }
     // The largest scale falls in [2^8, 2^9), 24 s in 2^14; with biases 2^68 and
     // more above the scales, lower: the rest, at most K 2^16 (|b| + 8 |s|) in its
-    // token's units, then stays below 2^110 in the row's.  (A scale that loses
-    // bits there counts 2^-85 of the bias.)
+    // token's units, then stays below 2^110 in the row's.
     const int es = min(max(m >> 7, 1), 254) - 127 - 8, eb = (mb >> 7) - 127 - 68;
     const int e = m == 0 ? max(eb, 0) : max(es, eb);
     const bool again = a.Gp > 8 * P;  // else they are at hand
@@ -624,7 +702,10 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
       for (int p = 0; p < 3; ++p)
         if (p < a.terms) *reinterpret_cast<uint4*>(a.tsum + ((size_t)p * a.N + n) * a.Gp + g) = make_uint4(t[p][0], t[p][1], t[p][2], t[p][3]);
     }
-    if (sub == 0) a.wexp[n] = e & 0xFFFF;
+    // the last of a scale's eight bits has to reach fp16's smallest number, 2^-24
+    // (a row with an infinity or NaN is lost anyway)
+    const bool wide = m < 0x7F80 && (least >> 7) - 127 - 7 < e - 24;
+    if (sub == 0) a.wexp[n] = (e & 0xFFFF) | (wide ? kLinWide : 0);
   }
 }
 

@@ -105,3 +105,22 @@ def test_affine_scales_far_below_the_biases(codec, xt, L, N, K):
     b[0, 13] = (rb[13] * 2.0 ** -20).to(BF16)
     ref, bound = R.linear_reference(codec, x, w, s, b, None)
     check(forward(codec, x, w, s, b), ref, bound + K * 2.0 ** -126)
+
+
+@pytest.mark.parametrize("codec", AFFINE)
+@pytest.mark.parametrize("xt", [BF16, F16])
+@pytest.mark.parametrize("L,N,K", AFFINE_TILES[:2] + [(16, 50, 256)])
+def test_affine_scales_far_below_their_rows_largest(codec, xt, L, N, K):
+    print("[case] affine scales far apart", codec, xt, L, N, K, flush=True)
+    assert by_tiles(codec, L, N, K) == (L > 16)
+    w, s, b = R.linear_weights(codec, N, K, 34)
+    gs = R.GROUPS[codec]
+    x = activations(L, K, xt)
+    x[:, :gs] = 0                       # nothing meets the large scale
+    for i, d in enumerate(range(20, 40)):
+        s[0, i, 1:] = (s[0, i, 1:].float() * 2.0 ** -d).to(BF16)
+        b[0, i, 1:] = (b[0, i, 1:].float() * 2.0 ** -d).to(BF16)
+    s[0, 20, 2] = 2.0 ** -126
+    b[0, 20, 2] = 0.0
+    ref, bound = R.linear_reference(codec, x, w, s, b, None)
+    check(forward(codec, x, w, s, b), ref, bound + K * 2.0 ** -126)
