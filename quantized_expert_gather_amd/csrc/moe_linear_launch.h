@@ -162,7 +162,7 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
       q.tok_blocks = l.L;
       a.x = q.xq;
       a.xsum = q.xsum;
-      a.xexp = F16 ? nullptr : q.xexp;
+      a.xexp = q.xexp;
       a.sh = q.sh;
       q.tsum = reinterpret_cast<uint16_t*>(ws + lay.tsum);
       a.tsum = q.tsum;

@@ -12,7 +12,12 @@
 //            divided by a power of two near its row's largest (down to 2^-26
 //            of that; rows with smaller scales are wide too).  bf16 tokens
 //            are divided by a power of two near their largest value likewise
-//            and held in fp16, where values 2^-32 below it lose bits.
+//            and held in fp16.  Their values 2^-32 below it lose bits, 2^-25
+//            each where the largest is at least 2^14: with the operands' 8 s
+//            2^-39 of what a row's largest scale gives the largest value.  In
+//            rows whose scales lie within 2^12 of one another that is 2^-27
+//            of what the largest value does give, below fp32's own rounding;
+//            tiles with another row and such a token go the wide rows' way.
 // The affine rest, sum over groups of (b + 8 s) X with X = sum of the group's
 // x, is a product over K / group columns; it starts the accumulators, both
 // factors as two or three bf16 terms.
@@ -49,8 +54,8 @@ struct TilesArgs {
   const uint16_t* sh;      // affine: fp16 scales over their row's power of two [N][Gp]
   const uint16_t* tsum;    // affine: bf16 terms of b + 8 s [3][N][Gp]
   const uint16_t* xsum;    // affine: bf16 terms of the group sums [3][L][Gp]
-  const int32_t* xexp;     // power of two of each token (affine with bf16 tokens), or NULL
-  const int32_t* wexp;     // power of two of each row (affine; mxfp4 with fp16 tokens) and kLinWide, or NULL
+  const int32_t* xexp;     // power of two of each token (affine with bf16 tokens) and kLinWide, or NULL
+  const int32_t* wexp;     // power of two of each row (affine; mxfp4 with fp16 tokens), kLinWide and kLinUneven, or NULL
   const float* bias;
   void* out;
   float* part;             // split K: [splits][L][N] partial sums
@@ -67,7 +72,8 @@ struct TilesArgs {
 };
 
 // A row's power of two is the low half of its word, the marks lie above.
-constexpr int kLinWide = 1 << 16;  // one fp16 power of two does not fit the row
+constexpr int kLinWide = 1 << 16;    // one fp16 power of two does not fit the row (or token)
+constexpr int kLinUneven = 1 << 17;  // scales 2^-12 and more below the row's largest
 __device__ __forceinline__ int lin_exponent(int v) { return (int)(int16_t)v; }
 
 __device__ __forceinline__ lin_f16x2 lin_h2(uint32_t v) { return __builtin_bit_cast(lin_f16x2, v); }
@@ -164,7 +170,7 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) asm volatile("" : "+v"(acc[mt][nt]));
   }
-  constexpr bool kScaled = lin_affine(FMT) || (FMT == kLinMxfp4 && F16);
+  constexpr bool kScaled = lin_affine(FMT) || (FMT == kLinMxfp4 && F16), kTokens = lin_affine(FMT) && !F16;  // have powers of two
   int wexp[NT], marks = 0;
   if constexpr (kScaled) {  // the same lanes' rows as the codes'
 #pragma unroll
@@ -221,7 +227,8 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
         for (int i = 0; i < 4; ++i) we[nt][i] = __shfl(wexp[nt], 4 * kb + i, 64);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const int xe = a.xexp ? a.xexp[min(tok0 + 16 * mt + n16, a.L - 1)] : 0;
+        int xe = 0;
+        if constexpr (kTokens) xe = lin_exponent(a.xexp[min(tok0 + 16 * mt + n16, a.L - 1)]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -285,16 +292,22 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
   // end to the beginning, so the tiles that run together read different ones.
   const int count = step1 - step0;
   int step = count > 0 ? step0 + (tile % a.tok_tiles) * a.stagger % count : 0;
+  int token_marks = 0, more_marks = 0;
+  if constexpr (kTokens) {
+    token_marks = a.xexp[min(tok0 + lane, a.L - 1)];
+    if constexpr (kTok > 64) more_marks = a.xexp[min(tok0 + 64 + lane, a.L - 1)];
+  }
   if (count > 0) {
     stage(step, lds0);
     load(step, cw, sw);
   }
 
-  if constexpr (kScaled) {
-    const int wide_rows = __any(marks & kLinWide);
-    if (lane == 0) wide_waves[wave] = wide_rows;
-  }
   __builtin_amdgcn_s_waitcnt(0);
+  if constexpr (kScaled) {
+    const int wide_wave = __any(marks & kLinWide) || (__any(marks & kLinUneven) && __any((token_marks | more_marks) & kLinWide));
+    if (lane == 0) wide_waves[wave] = wide_wave;
+    __builtin_amdgcn_s_waitcnt(0);
+  }
   __syncthreads();
   const LinCode code = lin_code<true>();
   int i = 0;
@@ -362,8 +375,8 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
     body(lds1, lds0);
   }
 
-  // A workgroup with a wide row starts again: its tokens from memory as they
-  // are, every product exact, and the sums in their own units.  mxfp4: the
+  // A workgroup with a wide row, or an uneven row and a wide token, starts
+  // again: its tokens from memory as they are, every product exact, and the sums in their own units.  mxfp4: the
   // blocks' powers of two in bf16 operands, x as two bf16 terms.  Affine: the
   // words transposed over the lanes, so that a product is one group's, and
   // its fp32 sum times the scale, plus b + 8 s times the group's sum of x.
@@ -490,7 +503,8 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
       if (t >= a.L || n >= a.N) continue;
       float v[4] = {v4[0], v4[1], v4[2], v4[3]};
       if constexpr (kScaled) {
-        const int xe = lin_affine(FMT) && a.xexp ? a.xexp[t] : 0;
+        int xe = 0;
+        if constexpr (kTokens) xe = lin_exponent(a.xexp[t]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           v[e] = __builtin_amdgcn_ldexpf(v[e], (xe + lin_exponent(a.wexp[min(n + e, a.N - 1)])) & units);
@@ -523,6 +537,23 @@ __device__ __forceinline__ void split_terms(float v, uint32_t (&t)[3]) {
   const float r = v - bf16_lo_to_f32(t[0]);
   t[1] = f32_to_bf16_rne(r);
   t[2] = f32_to_bf16_rne(r - bf16_lo_to_f32(t[1]));
+}
+
+// Largest and smallest of pairs of 16-bit numbers.
+typedef unsigned short lin_u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t lin_max2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(lin_u16x2, a), __builtin_bit_cast(lin_u16x2, b)));
+}
+__device__ __forceinline__ uint32_t lin_min2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(lin_u16x2, a), __builtin_bit_cast(lin_u16x2, b)));
+}
+__device__ __forceinline__ uint32_t lin_sub2(uint32_t a, uint32_t b) {  // each wraps for itself
+  return __builtin_bit_cast(uint32_t, (lin_u16x2)(__builtin_bit_cast(lin_u16x2, a) - __builtin_bit_cast(lin_u16x2, b)));
+}
+// A pair's largest and the inverse of another's smallest as one pair, whose
+// reduction by lin_max2 serves both.
+__device__ __forceinline__ uint32_t lin_ends(uint32_t most, uint32_t least) {
+  return max(most & 0xFFFFu, most >> 16) << 16 | (0xFFFFu - min(least & 0xFFFFu, least >> 16));
 }
 
 // Lays out what the tiles read besides codes and tokens.  One workgroup a
@@ -559,19 +590,26 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
       const uint16_t* x = a.x + (size_t)t * a.ldx;
       int e = 0;
       if constexpr (!F16) {
-        uint32_t m = 0;
+        uint32_t most = 0, lows = ~0u;  // the largest, and the least but 0, each less 1 (0 itself wraps)
         for (int c = 8 * tid; c < a.K; c += 2048) {
           const uint4 v = *reinterpret_cast<const uint4*>(x + c);
           const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) m = max(m, max(q[i] & 0x7FFFu, (q[i] >> 16) & 0x7FFFu));
+          for (int i = 0; i < 4; ++i) {
+            most = lin_max2(most, q[i] & 0x7FFF7FFFu);
+            lows = lin_min2(lows, lin_sub2(q[i] & 0x7FFF7FFFu, 0x00010001u));
+          }
         }
-        for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
-        if (lane == 0) red[wave] = m;
+        uint32_t ends = lin_ends(most, lows);
+        for (int o = 32; o > 0; o >>= 1) ends = lin_max2(ends, (uint32_t)__shfl_xor((int)ends, o, 64));
+        if (lane == 0) red[wave] = ends;
         __syncthreads();
-        m = max(max(red[0], red[1]), max(red[2], red[3]));
+        ends = lin_max2(lin_max2(red[0], red[1]), lin_max2(red[2], red[3]));
+        const uint32_t m = ends >> 16, least = (0x10000u - (ends & 0xFFFFu)) & 0xFFFFu;  // 0 where all are
         e = m ? min(max((int)(m >> 7), 1), 254) - 127 - 14 : 0;  // the largest falls in [2^14, 2^15)
-        if (tid == 0) a.xexp[t] = e;
+        // the last of a value's eight bits has to reach fp16's smallest number, 2^-24 (an infinity's token is lost anyway)
+        const bool wide = least && m < 0x7F80u && max((int)(least >> 7), 1) - 127 - 7 < e - 24;
+        if (tid == 0) a.xexp[t] = (e & 0xFFFF) | (wide ? kLinWide : 0);
       }
       constexpr int kLanes = lin_group(FMT) / 8;  // lanes of a group
       uint4 next = make_uint4(0, 0, 0, 0);  // a step ahead
@@ -658,23 +696,28 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
       }
     };
     uint16_t s[8], b[8];
-    int mb = 0, least = 0x7FFF;  // the largest finite bias, the least scale of 2^-96 and more
+    constexpr uint32_t kFloor = (127 - 96) << 7;  // 2^-96
+    // the largest scale and bias; the least scale, and the least from kFloor on (less kFloor: those below wrap)
+    uint32_t most_s = 0, most_b = 0, lows = ~0u, floored = ~0u;
     for (int g = 8 * sub; g < a.Gp; g += 8 * P) {
       eight(a.s, g, s);
       eight(a.b, g, b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int u = s[i] & 0x7FFFu, v = b[i] & 0x7FFFu;
-        m = max(m, u);
-        least = min(least, u >= (127 - 96) << 7 ? u : 0x7FFF);
-        mb = max(mb, v < 0x7F80 ? v : 0);
+      for (int i = 0; i < 8; i += 2) {
+        const uint32_t u = (s[i] | (uint32_t)s[i + 1] << 16) & 0x7FFF7FFFu;
+        most_s = lin_max2(most_s, u);
+        most_b = lin_max2(most_b, (b[i] | (uint32_t)b[i + 1] << 16) & 0x7FFF7FFFu);
+        lows = lin_min2(lows, u | (g + i < a.G ? 0u : 0x7FFFu) | (g + i + 1 < a.G ? 0u : 0x7FFF0000u));
+        floored = lin_min2(floored, lin_sub2(u, kFloor << 16 | kFloor));
       }
     }
+    uint32_t ends_s = lin_ends(most_s, lows), ends_b = lin_ends(most_b, floored);
     for (int o = P / 2; o > 0; o >>= 1) {
-      m = max(m, __shfl_xor(m, o, 64));
-      mb = max(mb, __shfl_xor(mb, o, 64));
-      least = min(least, __shfl_xor(least, o, 64));
+      ends_s = lin_max2(ends_s, (uint32_t)__shfl_xor((int)ends_s, o, 64));
+      ends_b = lin_max2(ends_b, (uint32_t)__shfl_xor((int)ends_b, o, 64));
     }
+    m = ends_s >> 16;
+    const int mb = ends_b >> 16, lowest = 0xFFFF - (ends_s & 0xFFFFu), least = 0xFFFF - (int)(ends_b & 0xFFFFu) + (int)kFloor;
     // The largest scale falls in [2^8, 2^9), 24 s in 2^14; with biases 2^68 and
     // more above the scales, lower: the rest, at most K 2^16 (|b| + 8 |s|) in its
     // token's units, then stays below 2^110 in the row's.
@@ -704,8 +747,9 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
     }
     // the last of a scale's eight bits has to reach fp16's smallest number, 2^-24
     // (a row with an infinity or NaN is lost anyway)
-    const bool wide = m < 0x7F80 && (least >> 7) - 127 - 7 < e - 24;
-    if (sub == 0) a.wexp[n] = (e & 0xFFFF) | (wide ? kLinWide : 0);
+    const bool wide = m < 0x7F80 && mb < 0x7F80 && (least >> 7) - 127 - 7 < e - 24;
+    const bool uneven = (lowest >> 7) < (m >> 7) - 12;
+    if (sub == 0) a.wexp[n] = (e & 0xFFFF) | (wide ? kLinWide : 0) | (uneven ? kLinUneven : 0);
   }
 }
 

@@ -124,3 +124,22 @@ def test_affine_scales_far_below_their_rows_largest(codec, xt, L, N, K):
     b[0, 20, 2] = 0.0
     ref, bound = R.linear_reference(codec, x, w, s, b, None)
     check(forward(codec, x, w, s, b), ref, bound + K * 2.0 ** -126)
+
+
+@pytest.mark.parametrize("codec", AFFINE)
+@pytest.mark.parametrize("L,N,K", AFFINE_TILES[:2] + [(16, 50, 256)])
+def test_bf16_activations_far_below_their_tokens_largest(codec, L, N, K):
+    print("[case] tokens far apart", codec, L, N, K, flush=True)
+    assert by_tiles(codec, L, N, K) == (L > 16)
+    w, s, b = R.linear_weights(codec, N, K, 35)
+    gs = R.GROUPS[codec]
+    x = activations(L, K, BF16)
+    for i, d in enumerate(range(22, 46)):
+        t = i % L
+        x[t, :gs] = (x[t, :gs].float() * 2.0 ** d).to(BF16)
+    s[0, ::2, 0] = 0.0                  # half of the rows do not look at the large ones
+    b[0, ::2, 0] = 0.0
+    s[0, 4, 0] = s[0, 4, 1] * 2.0 ** -20
+    b[0, 4, 0] = b[0, 4, 1] * 2.0 ** -20
+    ref, bound = R.linear_reference(codec, x, w, s, b, None)
+    check(forward(codec, x, w, s, b), ref, bound)
