@@ -371,8 +371,7 @@ int moe_sort_pairs(const int32_t *topk_ids, int L, int k, int E, int bm, int32_t
  * sums may be infinite where |x| times
  * a code's 31 is past fp32.  With more than 16 tokens affine scales below
  * 2^-96 may count as 0 beside scales 2^25, or biases 2^84, above them in their
- * row, and for bf16 results the groups' b + 8 s and sums of x may count to 16
- * bits each.
+ * row.
  * L == 0 returns MOE_Q4_OK without touching the GPU.  Needs
  * L <= MOE_Q4_LINEAR_MAX_L, N <= MOE_Q4_LINEAR_MAX_N, K <= MOE_Q4_LINEAR_MAX_K,
  * ldx <= MOE_Q4_LINEAR_MAX_LDX.

@@ -89,7 +89,7 @@ inline TilesWorkspace tiles_layout(int fmt, int L, int N, int K) {
   size_t off = 0;
   w.xq = off;   off = lin_round256(off + (affine ? (size_t)p.tok_tiles * p.mt * 16 * ((K + kLinStep - 1) / kLinStep * kLinStep) * 2 : 0));
   w.xsum = off; off = lin_round256(off + (affine ? 3 * (size_t)L * Gp * 2 : 0));
-  w.tsum = off; off = lin_round256(off + (affine ? 3 * (size_t)N * Gp * 2 : 0));
+  w.tsum = off; off = lin_round256(off + (affine ? 2 * (size_t)N * Gp * 2 : 0));
   w.xexp = off; off = lin_round256(off + (affine ? (size_t)L * 4 : 0));
   w.sh = off;   off = lin_round256(off + (affine ? (size_t)N * Gp * 2 : 0));
   w.wexp = off; off = lin_round256(off + (affine || fmt == kLinMxfp4 ? (size_t)N * 4 : 0));
@@ -137,7 +137,6 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
   a.G = l.K / lin_group(FMT);
   a.Gp = (a.G + 31) / 32 * 32;
   a.out_dtype = l.out_dtype;
-  a.terms = l.out_dtype == MOE_Q4_DTYPE_BF16 ? 2 : 3;
   a.splits = p.splits; a.steps_per = p.steps_per;
   a.stagger = std::max(1, p.steps_per / p.tok_tiles);
   a.row_tiles = p.row_tiles; a.tok_tiles = p.tok_tiles;
@@ -150,7 +149,6 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
     q.wexp = reinterpret_cast<int32_t*>(ws + lay.wexp);
     q.ldx = l.ldx;
     q.L = l.L; q.N = l.N; q.K = l.K; q.G = a.G; q.Gp = a.Gp;
-    q.terms = a.terms;
     q.row_lanes = 4;
     while (q.row_lanes < 64 && 8 * q.row_lanes < a.G) q.row_lanes *= 2;
     const int row_blocks = (int)(((size_t)l.N * q.row_lanes + 255) / 256);

@@ -19,8 +19,13 @@
 //            of what the largest value does give, below fp32's own rounding;
 //            tiles with another row and such a token go the wide rows' way.
 // The affine rest, sum over groups of (b + 8 s) X with X = sum of the group's
-// x, is a product over K / group columns; it starts the accumulators, both
-// factors as two or three bf16 terms.
+// x, is a product over K / group columns in bf16 terms; it starts the
+// accumulators.  b + 8 s is two terms, exact to fp32's rounding: of two
+// numbers of 8 bits, d powers of two apart, the sum has at most 9 + d bits
+// and what is left of it beside its first 8 at most 8, or, further apart, is
+// the smaller one.  X is three terms, fp32's 24 bits (two would leave it 16
+// and save 6 of 110 us for affine4_g32 2048 x 4096 x 4096, bf16, and at most
+// 1 of 134 for affine4_g64 2048 x 6144 x 4096).
 //
 // Bound by matrix instructions with the decoding beside them: 2048 x 6144 x
 // 4096 takes 96 us for mxfp4 (1073 TFLOP/s; 4 conversions per 8 weights), 115
@@ -52,7 +57,7 @@ struct TilesArgs {
   const unsigned char* s;  // scales as given
   const unsigned char* b;  // biases as given (affine)
   const uint16_t* sh;      // affine: fp16 scales over their row's power of two [N][Gp]
-  const uint16_t* tsum;    // affine: bf16 terms of b + 8 s [3][N][Gp]
+  const uint16_t* tsum;    // affine: bf16 terms of b + 8 s [2][N][Gp]
   const uint16_t* xsum;    // affine: bf16 terms of the group sums [3][L][Gp]
   const int32_t* xexp;     // power of two of each token (affine with bf16 tokens) and kLinWide, or NULL
   const int32_t* wexp;     // power of two of each row (affine; mxfp4 with fp16 tokens), kLinWide and kLinUneven, or NULL
@@ -62,10 +67,6 @@ struct TilesArgs {
   long long ldx, ldo;
   int L, N, K, G, Gp;
   int out_dtype;
-  // How many bf16 terms are used: 3, whose error is fp32's, or 2 where the
-  // result is rounded to bf16 anyway (together off by 2^-16 |t X|, 2^-8 of
-  // the result's own half step unless the sum cancels; a sixth of the products).
-  int terms;
   int splits, steps_per;   // steps of 128 inputs of each split
   int stagger;             // steps between the token tiles' first ones
   int row_tiles, tok_tiles;
@@ -187,11 +188,11 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
     const int chunks = a.Gp / 32;
     const int g0 = 32 * (int)((long)chunks * split / a.splits), g1 = 32 * (int)((long)chunks * (split + 1) / a.splits);
     if (g0 < g1) {
-      // sum over groups of t X, t = b + 8 s, by their bf16 terms: the products
-      // whose terms' places add up to less than `terms`
+      // sum over groups of t X, t = b + 8 s, by their bf16 terms (the last of
+      // t times the last of X is below fp32's rounding)
 #pragma unroll 1
       for (int g = g0 + 8 * kb; g < g1; g += 32) {
-        uint4 tf[3][NT], xf[3][MT];
+        uint4 tf[2][NT], xf[3][MT];
         auto load_t = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) tf[i][nt] = *reinterpret_cast<const uint4*>(a.tsum + ((size_t)i * a.N + row[nt]) * a.Gp + g);
@@ -211,13 +212,10 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
         add(0, 0); add(1, 0);
         load_x(1);
         add(0, 1);
-        if (a.terms == 3) {  // kept in this order: all terms at once would not fit the registers
-          add(1, 1);
-          __builtin_amdgcn_sched_barrier(0);
-          load_t(2); add(2, 0);
-          __builtin_amdgcn_sched_barrier(0);
-          load_x(2); add(0, 2);
-        }
+        add(1, 1);
+        __builtin_amdgcn_sched_barrier(0);  // all of X at once would not fit the registers
+        load_x(2);
+        add(0, 2);
       }
       // into the operands' units
       int we[NT][4];
@@ -531,12 +529,14 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
   }
 }
 
-// v as bf16 terms, hi + mid + lo.
-__device__ __forceinline__ void split_terms(float v, uint32_t (&t)[3]) {
-  t[0] = f32_to_bf16_rne(v);
-  const float r = v - bf16_lo_to_f32(t[0]);
-  t[1] = f32_to_bf16_rne(r);
-  t[2] = f32_to_bf16_rne(r - bf16_lo_to_f32(t[1]));
+// v as bf16 terms, each the nearest to what the ones before leave.
+template <int N>
+__device__ __forceinline__ void split_terms(float v, uint32_t (&t)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    t[i] = f32_to_bf16_rne(v);
+    v -= bf16_lo_to_f32(t[i]);
+  }
 }
 
 // Largest and smallest of pairs of 16-bit numbers.
@@ -575,7 +575,6 @@ struct PrepareArgs {
   int32_t* wexp;
   long long ldx;
   int L, N, K, G, Gp;
-  int terms;
   int row_lanes;  // a power of two, 64 at most
   int tok_blocks;
 };
@@ -651,11 +650,12 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
           uint32_t term[3];
           split_terms(sum, term);
           uint16_t* to = a.xsum + (size_t)t * a.Gp + c / lin_group(FMT);
-          for (int p = 0; p < a.terms; ++p) to[(size_t)p * a.L * a.Gp] = (uint16_t)term[p];
+#pragma unroll
+          for (int p = 0; p < 3; ++p) to[(size_t)p * a.L * a.Gp] = (uint16_t)term[p];
         }
       }
       if (a.G + tid < a.Gp) {
-        for (int p = 0; p < a.terms; ++p) a.xsum[((size_t)p * a.L + t) * a.Gp + a.G + tid] = 0;
+        for (int p = 0; p < 3; ++p) a.xsum[((size_t)p * a.L + t) * a.Gp + a.G + tid] = 0;
       }
     }
     return;
@@ -729,21 +729,21 @@ __global__ __launch_bounds__(256) void k_linear_prepare(PrepareArgs a) {
         eight(a.s, g, s);
         eight(a.b, g, b);
       }
-      uint32_t h[4], t[3][4];
+      uint32_t h[4], t[2][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t term[2][3];
+        uint32_t term[2][2];
         const float s0 = bf16_to_f32(s[2 * i]), s1 = bf16_to_f32(s[2 * i + 1]);
         h[i] = lin_u(lin_f16x2{(_Float16)__builtin_amdgcn_ldexpf(s0, -e), (_Float16)__builtin_amdgcn_ldexpf(s1, -e)});
         split_terms(__builtin_fmaf(8.0f, s0, bf16_to_f32(b[2 * i])), term[0]);
         split_terms(__builtin_fmaf(8.0f, s1, bf16_to_f32(b[2 * i + 1])), term[1]);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) t[p][i] = term[0][p] | term[1][p] << 16;
+        for (int p = 0; p < 2; ++p) t[p][i] = term[0][p] | term[1][p] << 16;
       }
       *reinterpret_cast<uint4*>(a.sh + n * a.Gp + g) = make_uint4(h[0], h[1], h[2], h[3]);
 #pragma unroll
-      for (int p = 0; p < 3; ++p)
-        if (p < a.terms) *reinterpret_cast<uint4*>(a.tsum + ((size_t)p * a.N + n) * a.Gp + g) = make_uint4(t[p][0], t[p][1], t[p][2], t[p][3]);
+      for (int p = 0; p < 2; ++p)
+        *reinterpret_cast<uint4*>(a.tsum + ((size_t)p * a.N + n) * a.Gp + g) = make_uint4(t[p][0], t[p][1], t[p][2], t[p][3]);
     }
     // the last of a scale's eight bits has to reach fp16's smallest number, 2^-24
     // (a row with an infinity or NaN is lost anyway)

@@ -143,3 +143,20 @@ def test_bf16_activations_far_below_their_tokens_largest(codec, L, N, K):
     b[0, 4, 0] = b[0, 4, 1] * 2.0 ** -20
     ref, bound = R.linear_reference(codec, x, w, s, b, None)
     check(forward(codec, x, w, s, b), ref, bound)
+
+
+@pytest.mark.parametrize("codec", AFFINE)
+@pytest.mark.parametrize("xt", [BF16, F16])
+@pytest.mark.parametrize("ot", [BF16, F16, F32])
+@pytest.mark.parametrize("L", [9, 40])
+def test_group_sums_count_in_full(codec, xt, ot, L):
+    # codes and biases of 0: every weight is 0 and so is the result.  The sum of a group's x, 985089, takes three bf16
+    # terms; every partial sum is a whole number of at most 8 * 985089 < 2^24, exact in fp32.
+    N, K = 20, 64
+    w = torch.zeros(1, N, K // 8, dtype=torch.int32)
+    s, b = torch.ones(1, N, K // R.GROUPS[codec], dtype=BF16), torch.zeros(1, N, K // R.GROUPS[codec], dtype=BF16)
+    x = torch.zeros(L, K)
+    x[:, :30] = 32768.0
+    x[:, 30], x[:, 31] = 2048.0, 1.0
+    out = forward(codec, x.to(xt), w, s, b, ot=ot)
+    assert (out == 0).all(), out.unique()
