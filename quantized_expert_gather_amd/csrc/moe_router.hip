@@ -16,6 +16,7 @@
 // reductions stay in registers.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <limits.h>
 #include <stdint.h>
 
@@ -564,16 +565,21 @@ extern "C" int moe_router_topk(const void* logits, int logits_dtype, long long l
   // with a bias 16.7 and 20.0, bf16 8.3 and 9.6; 8192 with a bias 9.5 and
   // 12.2, 4096 8.7 and 7.8, bf16 4.7 and 4.1; 1000 4.5 and 3.0).
   const RowPlan plan = row_plan(E, k, T <= 6144);
-  TopkArgs a{logits, select_bias, topk_ids, topk_weights, ld, T, k, E, score, renormalize, scale};
-  const int threads = plan.lpr > 64 ? plan.lpr : kTopkThreads, per = threads / plan.lpr;
-  const dim3 grid((T + per - 1) / per), block(threads);
+  const int threads = plan.lpr > 64 ? plan.lpr : kTopkThreads, per = threads / plan.lpr, most = rows_of_launch(plan.lpr);
 #define MOE_TOPK_CALL(LT, EPL, LPR)                                                                    \
   if (select_bias)                                                                                     \
     hipLaunchKernelGGL((k_router_topk<LT, EPL, LPR, true>), grid, block, 0, stream, a);                \
   else                                                                                                 \
     hipLaunchKernelGGL((k_router_topk<LT, EPL, LPR, false>), grid, block, 0, stream, a)
-  MOE_ROW_DISPATCH(logits_dtype, plan, MOE_TOPK_CALL)
-  return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+  for (int t = 0; t < T; t += most) {
+    const int n = std::min(most, T - t);
+    const TopkArgs a{static_cast<const unsigned char*>(logits) + (size_t)t * ld * es, select_bias, topk_ids + (size_t)t * k,
+                     topk_weights + (size_t)t * k, ld, n, k, E, score, renormalize, scale};
+    const dim3 grid((n + per - 1) / per), block(threads);
+    MOE_ROW_DISPATCH(logits_dtype, plan, MOE_TOPK_CALL)
+    if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
+  }
+  return MOE_Q4_OK;
 }
 
 extern "C" int moe_router_topk_backward(const void* logits, int logits_dtype, long long ld, const int32_t* topk_ids,
@@ -593,11 +599,17 @@ extern "C" int moe_router_topk_backward(const void* logits, int logits_dtype, lo
     return MOE_Q4_ERR_ALIAS;
   // 2048 x 256 bf16: 2.9 us over 16 lanes a row, 2.7 over 64; 4096: 3.1 and 3.4
   const RowPlan plan = row_plan(E, k, T <= 2048);
-  TopkBackArgs a{logits, topk_ids, dweights, dlogits, ld, ldd, T, k, E, score, renormalize, scale};
-  const int threads = plan.lpr > 64 ? plan.lpr : kTopkThreads, per = threads / plan.lpr;
-  const dim3 grid((T + per - 1) / per), block(threads);
+  const int threads = plan.lpr > 64 ? plan.lpr : kTopkThreads, per = threads / plan.lpr, most = rows_of_launch(plan.lpr);
 #define MOE_TOPK_BACK_CALL(LT, EPL, LPR) \
   hipLaunchKernelGGL((k_router_topk_backward<LT, EPL, LPR>), grid, block, 0, stream, a)
-  MOE_ROW_DISPATCH(logits_dtype, plan, MOE_TOPK_BACK_CALL)
-  return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+  for (int t = 0; t < T; t += most) {
+    const int n = std::min(most, T - t);
+    const TopkBackArgs a{static_cast<const unsigned char*>(logits) + (size_t)t * ld * es, topk_ids + (size_t)t * k,
+                         dweights + (size_t)t * k, static_cast<unsigned char*>(dlogits) + (size_t)t * ldd * es, ld, ldd, n, k, E,
+                         score, renormalize, scale};
+    const dim3 grid((n + per - 1) / per), block(threads);
+    MOE_ROW_DISPATCH(logits_dtype, plan, MOE_TOPK_BACK_CALL)
+    if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
+  }
+  return MOE_Q4_OK;
 }

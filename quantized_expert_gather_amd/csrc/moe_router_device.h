@@ -185,6 +185,11 @@ inline RowPlan row_plan(int E, int k, bool wide) {
   p.epl = need <= 4 ? 4 : need <= 8 && (p.lpr == 16 || p.lpr == 64) ? 8 : 16;
   return p;
 }
+
+// Rows of one launch: a grid holds fewer than 2^32 threads, so the longest
+// inputs take several.
+constexpr size_t kLaunchThreads = size_t(1) << 31;
+inline int rows_of_launch(int lpr) { return (int)(kLaunchThreads / lpr); }
 }  // namespace moeq4
 
 // Expands CALL(LT, EPL, LPR) for a logits type and a RowPlan.
