@@ -150,7 +150,8 @@ int launch_tiles(const LinearArgs& l, unsigned char* ws, hipStream_t stream) {
     q.ldx = l.ldx;
     q.L = l.L; q.N = l.N; q.K = l.K; q.G = a.G; q.Gp = a.Gp;
     q.row_lanes = 4;
-    while (q.row_lanes < 64 && 8 * q.row_lanes < a.G) q.row_lanes *= 2;
+    // (a launch holds fewer than 2^32 threads)
+    while (q.row_lanes < 64 && 8 * q.row_lanes < a.G && (size_t)l.N * q.row_lanes <= size_t(1) << 30) q.row_lanes *= 2;
     const int row_blocks = (int)(((size_t)l.N * q.row_lanes + 255) / 256);
     if constexpr (lin_affine(FMT)) {
       q.xq = reinterpret_cast<uint16_t*>(ws + lay.xq);
@@ -182,12 +183,20 @@ template <int FMT>
 int linear_launch(bool f16, const LinearArgs& a, unsigned char* ws, hipStream_t stream) {
   if (linear_by_tiles(FMT, a.L, a.N, a.K)) return f16 ? launch_tiles<FMT, true>(a, ws, stream) : launch_tiles<FMT, false>(a, ws, stream);
   if (a.K < kLinStep) {
-    const dim3 grid((unsigned)(((size_t)a.L * a.N + 255) / 256));
-    if (f16)
-      hipLaunchKernelGGL((k_linear_short<FMT, true>), grid, dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL((k_linear_short<FMT, false>), grid, dim3(256), 0, stream, a);
-    return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+    const int most = (int)std::min<size_t>(a.L, (size_t(1) << 31) / a.N);  // tokens whose outputs fit a launch's threads
+    LinearArgs l = a;
+    for (int t = 0; t < a.L; t += most) {
+      l.L = std::min(most, a.L - t);
+      l.x = a.x + (size_t)t * a.ldx;
+      l.out = static_cast<unsigned char*>(a.out) + (size_t)t * a.ldo * (a.out_dtype == MOE_Q4_DTYPE_F32 ? 4 : 2);
+      const dim3 grid((unsigned)(((size_t)l.L * l.N + 255) / 256));
+      if (f16)
+        hipLaunchKernelGGL((k_linear_short<FMT, true>), grid, dim3(256), 0, stream, l);
+      else
+        hipLaunchKernelGGL((k_linear_short<FMT, false>), grid, dim3(256), 0, stream, l);
+      if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
+    }
+    return MOE_Q4_OK;
   }
   const RowsPlan p = rows_plan(FMT, f16, a.N, a.K, linear_words(a));
   LinearArgs l = a;

@@ -29,3 +29,19 @@ def test_selection_of_more_rows_than_a_launch_holds(T, E, step):
     others = torch.ones(T, dtype=torch.bool, device="cuda")
     others[rows] = False
     assert bool(((dz[:, 0] == 0.25) == others).all()) and int((dz[:, 1] != 0).sum()) == 0
+
+
+def test_short_products_of_more_outputs_than_a_launch_holds():
+    # 16 tokens x 2^28 outputs of 32 inputs: 2^32 outputs
+    L, N, K = 16, q.MOE_Q4_LINEAR_MAX_N, 32
+    print("[case] short product", L, N, K, flush=True)
+    w = torch.zeros(N, K // 8, dtype=torch.int32, device="cuda")
+    s = torch.full((N, 1), 127, dtype=torch.uint8, device="cuda")
+    cols = torch.tensor([0, 1, 255, 256, (1 << 27) - 1, 1 << 27, N - 256, N - 1], device="cuda")
+    w[cols, 0] = 0x22222222   # E2M1 1.0, eight inputs
+    x = torch.arange(1, L + 1, device="cuda").to(BF16).view(L, 1).expand(L, K).contiguous()
+    out = q.moe_linear_codec_forward("mxfp4", x, w, s)
+    want = (8.0 * torch.arange(1, L + 1, device="cuda")).to(BF16)
+    for t in range(L):
+        assert (out[t, cols] == want[t]).all(), t
+        assert int((out[t] != 0).sum()) == len(cols), t
