@@ -260,6 +260,21 @@ __device__ void order_in_64(const float (&z)[EPL], const float* bias, int slot, 
   }
 }
 
+// Sigmoid scores of a row's picks (z of the lanes that are live) over their sum.
+// Every lane of the wave calls it.
+template <int LANES>
+__device__ __forceinline__ float chosen_sigmoid(float z, bool live) {
+  float s = live ? sigmoid_f32(z) : 0.0f, sum = row_all<LANES>(s, OpSumF());
+  const bool low = sum < kLowSum;
+  if (__any(low)) {
+    const float base = exp_base(row_all<LANES>(live ? z : -__builtin_inff(), OpMaxF()));
+    const float u = live ? sigmoid_from(z, low ? base : 0.0f) : 0.0f, all = row_all<LANES>(u, OpSumF());
+    s = low ? u : s;
+    sum = low ? all : sum;
+  }
+  return sum == 0.0f ? 0.0f : s / sum;
+}
+
 // Weights of the chosen: thread j < k of the row holds logit z of pick j.
 // Every thread of the wave calls it; the sums run over the row's lanes (the
 // first wave's).
@@ -276,10 +291,8 @@ __device__ __forceinline__ float chosen_weight(float z, bool live, int score, in
     }
     return row_sum == 0.0f ? 0.0f : scale * (exp_f32(z - row_base) / row_sum);
   }
-  const float s = live ? sigmoid_f32(z) : 0.0f;
-  if (!norm) return scale * s;
-  const float sum = row_all<kLanes>(s, OpSumF());
-  return sum == 0.0f ? 0.0f : scale * (s / sum);
+  if (!norm) return scale * (live ? sigmoid_f32(z) : 0.0f);
+  return scale * chosen_sigmoid<kLanes>(z, live);
 }
 
 template <class LT, int EPL, int LPR, bool BIAS>
@@ -475,18 +488,16 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : kTopkThreads) void k_router_topk_b
 #pragma unroll
     for (int i = 0; i < EPL; ++i) out[i] = 0.0f;
     float p, damp = 1.0f;
-    if (a.score == kRouterScoreSoftmax) {
+    if (a.score == kRouterScoreSoftmax) {  // (renormalised: else above)
       const float m = exp_base(row_all<kLanes>(live ? z : -__builtin_inff(), OpMaxF()));
       p = live ? exp_f32(z - m) : 0.0f;
-    } else {
-      p = live ? sigmoid_f32(z) : 0.0f;
-      damp = sigmoid_f32(-z);
-    }
-    if (a.norm) {
       const float sum = row_all<kLanes>(p, OpSumF());
       p = sum == 0.0f ? 0.0f : p / sum;
-      g -= row_all<kLanes>(live ? p * g : 0.0f, OpSumF());
+    } else {
+      p = a.norm ? chosen_sigmoid<kLanes>(z, live) : live ? sigmoid_f32(z) : 0.0f;
+      damp = sigmoid_f32(-z);
     }
+    if (a.norm) g -= row_all<kLanes>(live ? p * g : 0.0f, OpSumF());
     term = live ? a.scale * p * g * damp : 0.0f;
   }
   bool repeats = true;

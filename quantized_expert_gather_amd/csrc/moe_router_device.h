@@ -164,6 +164,13 @@ __device__ __forceinline__ float sigmoid_pair(float z, float& rest) {
   return s;
 }
 
+// Scores whose row's sum is below this (every logit below -16) are formed
+// again from the row's maximum where they are divided by that sum: fp32 holds
+// no sigmoid below -87, the ratios of these are ordinary numbers.
+constexpr float kLowSum = 0x1p-24f;
+// sigmoid(z) e^-base, for z <= base <= 0.
+__device__ __forceinline__ float sigmoid_from(float z, float base) { return exp_f32(z - base) * recip_f32(1.0f + exp_f32(z)); }
+
 // What a row's exponentials count from: its maximum, or 0 where all of it is
 // masked (-inf): exp(-inf - 0) = 0, a softmax of zeros.
 __device__ __forceinline__ float exp_base(float row_max) { return row_max == -__builtin_inff() ? 0.0f : row_max; }

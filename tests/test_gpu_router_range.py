@@ -1,6 +1,8 @@
 """The router's selection and the balance loss with sigmoid scores of very
 negative logits (needs an MI355X): fp32 holds none of the scores, their
-ratios are ordinary numbers.  Bounds as in test_gpu_router."""
+ratios are ordinary numbers.  Bounds as in test_gpu_router; a score below
+2^-126, fp32's smallest normal number, may be 0, so a weight that is such a
+score times `scale` is off by scale * 2^-126 at most."""
 
 import numpy as np
 import pytest
@@ -25,13 +27,22 @@ def low_logits(rows, E, dtype, seed=0):
     return z.to(dtype)
 
 
+def check_topk(z, k, bias, norm, scale=1.5):
+    z64 = z.double().numpy()
+    ids, w = R.route(z64, k, None if bias is None else bias.double().numpy(), "sigmoid", norm, scale)
+    gi, gw = q.moe_router_topk(z.cuda(), k, select_bias=None if bias is None else bias.cuda(), score="sigmoid", renormalize=norm,
+                               scale=scale)
+    assert np.array_equal(gi.cpu().numpy(), ids)
+    assert (np.abs(gw.double().cpu().numpy() - w) <= T.rel(z64) * np.abs(w) + scale * 2.0 ** -126).all()
+
+
 @pytest.mark.parametrize("E,k", [(8, 2), (64, 6), (256, 8), (300, 40), (1024, 8), (1500, 8)])
 def test_topk_of_low_logits(E, k):
     for dtype in (F32, BF16, F16):
         z = low_logits(24, E, dtype, seed=E)
         for bias in (None, 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(4)), torch.zeros(E)):
             for norm in (True, False):
-                T.check_topk(z, k, bias, "sigmoid", norm)
+                check_topk(z, k, bias, norm)
 
 
 @pytest.mark.parametrize("E,k", [(8, 2), (64, 6), (256, 8), (1500, 8)])
