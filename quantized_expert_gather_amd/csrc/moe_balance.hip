@@ -55,10 +55,11 @@ struct BalanceArgs {
 };
 
 // p of R rows but for their factor `inv`, in place of their logits, and
-// 1 - sigmoid(z) in `damp` (DAMP, sigmoid scores only).
-template <class LT, int EPL, int LPR, int R, bool DAMP>
+// 1 - sigmoid(z) in `damp` (DAMP, sigmoid scores only).  reload(r, u) reads row
+// r's logits again.
+template <class LT, int EPL, int LPR, int R, bool DAMP, class RELOAD>
 __device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&damp)[DAMP ? R : 1][EPL], float (&inv)[R],
-                                                  int score, float* red) {
+                                                  int score, float* red, RELOAD reload) {
   float sum[R];
   if (score == kRouterScoreSoftmax) {
     float m[R];
@@ -95,6 +96,27 @@ __device__ __forceinline__ void row_probabilities(float (&v)[R][EPL], float (&da
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) sum[r] = row_all<LPR>(sum[r], OpSumF(), red);
+  if (score != kRouterScoreSoftmax) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool low = sum[r] < kLowSum;  // (the same in a workgroup that holds one row)
+      if (!__any(low)) continue;
+      float u[EPL];
+      reload(r, u);
+      float m = u[0], all = 0.0f;
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) m = fmaxf(m, u[i]);
+      m = exp_base(row_all<LPR>(m, OpMaxF(), red));
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        u[i] = sigmoid_from(u[i], low ? m : 0.0f);
+        all += u[i];
+        v[r][i] = low ? u[i] : v[r][i];
+      }
+      all = row_all<LPR>(all, OpSumF(), red);
+      sum[r] = low ? all : sum[r];
+    }
+  }
 #pragma unroll
   for (int r = 0; r < R; ++r) inv[r] = sum[r] == 0.0f ? 0.0f : 1.0f / sum[r];
 }
@@ -123,10 +145,12 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
 
   // the rows after the ones at hand are on their way
   float acc[EPL], v[R][EPL], next[R][EPL], none[1][EPL];
+  auto load_one = [&](int t, int r, float (&to)[EPL]) __attribute__((always_inline)) {
+    load_row<LT, EPL, LPR>(static_cast<const mem*>(a.z) + (seq + min(t + r * kGroups + group, t1 - 1)) * a.ld, slot, a.E, -__builtin_inff(), to);
+  };
   auto load = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      load_row<LT, EPL, LPR>(static_cast<const mem*>(a.z) + (seq + min(t + r * kGroups + group, t1 - 1)) * a.ld, slot, a.E, -__builtin_inff(), next[r]);
+    for (int r = 0; r < R; ++r) load_one(t, r, next[r]);
   };
   if (t0 < t1) load(t0);
   for (int e = tid; e < a.E; e += nthr) hist[e] = 0;
@@ -159,7 +183,7 @@ __global__ __launch_bounds__(64 * kPartialWaves) void k_balance_partial(BalanceA
     }
     if (t + R * kGroups < t1) load(t + R * kGroups);
     float inv[R];
-    row_probabilities<LT, EPL, LPR, R, false>(v, none, inv, a.score, red);
+    row_probabilities<LT, EPL, LPR, R, false>(v, none, inv, a.score, red, [&](int r, float (&u)[EPL]) { load_one(t, r, u); });
 #pragma unroll
     for (int r = 0; r < R; ++r)
       if (live[r]) {  // (a masked row may hold anything)
@@ -310,10 +334,12 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : 64 * kBackWaves) void k_balance_ba
   const int t0 = blockIdx.x * a.per, t1 = min(a.T, t0 + a.per);
   const size_t seq = (size_t)blockIdx.y * a.T;
   float v[R][EPL], next[R][EPL], damp[R][EPL];
+  auto load_one = [&](int t, int r, float (&to)[EPL]) __attribute__((always_inline)) {
+    load_row<LT, EPL, LPR>(static_cast<const mem*>(a.z) + (seq + min(t + r * kGroups + group, t1 - 1)) * a.ld, slot, a.E, -__builtin_inff(), to);
+  };
   auto load = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      load_row<LT, EPL, LPR>(static_cast<const mem*>(a.z) + (seq + min(t + r * kGroups + group, t1 - 1)) * a.ld, slot, a.E, -__builtin_inff(), next[r]);
+    for (int r = 0; r < R; ++r) load_one(t, r, next[r]);
   };
   load(t0);
   const float n = (float)a.tokens[blockIdx.y];
@@ -335,7 +361,7 @@ __global__ __launch_bounds__(LPR > 64 ? LPR : 64 * kBackWaves) void k_balance_ba
       for (int i = 0; i < EPL; ++i) v[r][i] = next[r][i];
     if (t + R * kGroups < t1) load(t + R * kGroups);
     float dot[R], inv[R];
-    row_probabilities<LT, EPL, LPR, R, true>(v, damp, inv, a.score, red);
+    row_probabilities<LT, EPL, LPR, R, true>(v, damp, inv, a.score, red, [&](int r, float (&u)[EPL]) { load_one(t, r, u); });
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       dot[r] = 0.0f;
