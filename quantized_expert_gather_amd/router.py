@@ -92,18 +92,19 @@ def moe_router_topk(logits, k: int, select_bias=None, score="softmax", renormali
     [E], added to the scores for the choice only.  Returns (topk_ids int32 [T,
     k], topk_weights fp32 [T, k]) as :func:`moe_swiglu_q4_forward` takes them.
 
-    The weights carry a gradient to logits where logits requires one and no
-    output tensors or stream are given; a step recorded into a graph calls
-    :func:`moe_router_topk_backward` itself (backward() refuses there).
+    The weights carry a gradient to logits where logits requires one; output
+    tensors, which cannot, are refused then.  A step recorded into a graph
+    calls :func:`moe_router_topk_backward` itself (backward() refuses there).
     ``stream`` (a torch stream or a HIP handle) is as ``with
     torch.cuda.stream(stream)`` around the call.
     """
-    if topk_ids is None and topk_weights is None and stream is None and isinstance(logits, torch.Tensor) and \
-            logits.requires_grad and torch.is_grad_enabled():
-        return _TopkFunction.apply(logits, k, select_bias, score, renormalize, scale)
     if stream is not None and isinstance(logits, torch.Tensor):
         with on_stream(stream, logits):
-            return _topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weights)
+            return moe_router_topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weights)
+    if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
+        if topk_ids is not None or topk_weights is not None:
+            raise RuntimeError("moe_router_topk: given output tensors carry no gradient, but logits requires one")
+        return _TopkFunction.apply(logits, k, select_bias, score, renormalize, scale)
     return _topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weights)
 
 
@@ -206,15 +207,15 @@ def moe_balance_loss(logits, topk_ids, coef: float = 1.0, score="softmax", seqs:
     leaves a token out).
 
     Returns (loss fp32 [seqs], counts int32 [seqs, E], tokens int32 [seqs]).
-    The loss carries a gradient to logits where logits requires one and no
-    stream is given; a step recorded into a graph calls
-    :func:`moe_balance_loss_backward` itself (backward() refuses there).
+    The loss carries a gradient to logits where logits requires one; a step
+    recorded into a graph calls :func:`moe_balance_loss_backward` itself
+    (backward() refuses there).  ``stream`` is as :func:`moe_router_topk`'s.
     """
-    if stream is None and isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
-        return _BalanceFunction.apply(logits, topk_ids, coef, score, seqs, token_mask, workspace)
     if stream is not None and isinstance(logits, torch.Tensor):
         with on_stream(stream, logits):
-            return _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace)
+            return moe_balance_loss(logits, topk_ids, coef, score, seqs, token_mask, workspace)
+    if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
+        return _BalanceFunction.apply(logits, topk_ids, coef, score, seqs, token_mask, workspace)
     return _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace)
 
 

@@ -71,3 +71,22 @@ def test_balance_of_low_logits(S, rows, E, k):
     mask = torch.ones(S * rows, dtype=torch.bool)
     mask[2:7] = False
     T.check_balance(S, rows, E, k, F32, "sigmoid", z=low_logits(S * rows, E, F32), mask=mask)
+
+
+def test_a_call_on_a_given_stream_carries_its_gradient():
+    z = T.logits(40, 24, F32, seed=3).cuda()
+    c = torch.randn(40, 4, generator=torch.Generator().manual_seed(1)).cuda()
+    grads = []
+    for side in (None, torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        zi = z.clone().requires_grad_()
+        torch.cuda.synchronize()
+        ids, w = q.moe_router_topk(zi, 4, stream=side)
+        loss, _, _ = q.moe_balance_loss(zi, ids, stream=side)
+        assert w.requires_grad and loss.requires_grad and not ids.requires_grad
+        torch.cuda.synchronize()
+        torch.autograd.backward([w, loss], [c, torch.ones_like(loss)])
+        torch.cuda.synchronize()
+        grads.append(zi.grad)
+    assert torch.equal(grads[0], grads[1]) and torch.equal(grads[0], grads[2]) and grads[0].abs().max() > 0
+    with torch.no_grad():
+        assert not q.moe_router_topk(zi, 4, stream=torch.cuda.Stream())[1].requires_grad

@@ -207,6 +207,16 @@ def test_bindings_refuse_host_tensors():
         q.moe_balance_loss(z, torch.zeros(4, 2, dtype=torch.int32))
 
 
+def test_given_outputs_are_refused_where_a_gradient_is_due():
+    z = torch.zeros(4, 8, requires_grad=True)
+    ids, w = torch.empty(4, 2, dtype=torch.int32), torch.empty(4, 2)
+    for kw in (dict(topk_ids=ids), dict(topk_weights=w), dict(topk_ids=ids, topk_weights=w)):
+        with pytest.raises(RuntimeError, match="gradient"):
+            q.moe_router_topk(z, 2, **kw)
+        with torch.no_grad(), pytest.raises(ValueError, match="device"):  # past that check
+            q.moe_router_topk(z, 2, **kw)
+
+
 # ---- the references themselves ----
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
