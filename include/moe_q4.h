@@ -398,7 +398,10 @@ size_t moe_linear_codec_workspace_bytes(int codec, int L, int N, int K);
  *               renormalize = 1, scale * p_j with 0
  *
  * Equal values go to the lower expert; scores with a bias that fp32 cannot
- * tell apart are compared in 64 bits.  A logit of -inf (a masked expert) has
+ * tell apart are compared in 64 bits.  Weights are fp32: an exponential of a
+ * difference d is off by up to 2^-24 (2.5 |d| + 4) of itself, |d| at most the
+ * logits' range, scores below 2^-126 may be 0 (renormalised ones keep their
+ * ratios), and the gradients carry the same.  A logit of -inf (a masked expert) has
  * score 0; so do all experts of a row of nothing else, whose weights are 0
  * and whose ids are the lowest.  NaN logits rank below -inf.  ids are always
  * k different experts.  1 <= k <= MOE_Q4_ROUTER_MAX_K, E <= MOE_Q4_MAX_E,
@@ -434,7 +437,7 @@ int moe_router_topk_backward(const void *logits, int logits_dtype, long long ld,
  *              aligned, no initialisation, no overlap with an input; not
  *              shared by calls, or graphs, that may run at the same time)
  *
- * Sums are fp32 in a fixed order.  S <= MOE_Q4_BALANCE_MAX_SEQS, E <= MOE_Q4_MAX_E,
+ * Sums are fp32 in a fixed order, of p as the selection forms it.  S <= MOE_Q4_BALANCE_MAX_SEQS, E <= MOE_Q4_MAX_E,
  * T <= MOE_Q4_ROUTER_MAX_T.
  */
 int moe_balance_loss(const void *logits, int logits_dtype, long long ld, const int32_t *topk_ids,

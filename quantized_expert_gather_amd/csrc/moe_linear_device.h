@@ -151,7 +151,7 @@ __device__ __forceinline__ float lin_e8m0(uint32_t e) {
 // The values of the first S 16-lane rows, each to all four rows.
 template <int S>
 __device__ __forceinline__ void lin_spread(uint32_t v, uint32_t (&out)[S]) {
-  static_assert(S >= 1 && S <= 4, "rows of a wave");
+  static_assert(S >= 1 && S <= 3, "steps of a wave");
   if constexpr (S == 1) {
     out[0] = v;
   } else {
@@ -160,9 +160,7 @@ __device__ __forceinline__ void lin_spread(uint32_t v, uint32_t (&out)[S]) {
     out[0] = lo[0];
     out[1] = lo[1];
     if constexpr (S > 2) {
-      const auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
-      out[2] = hi[0];
-      if constexpr (S > 3) out[3] = hi[1];
+      out[2] = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false)[0];
     }
   }
 }

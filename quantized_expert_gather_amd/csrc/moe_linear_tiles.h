@@ -27,13 +27,13 @@
 // and save 6 of 110 us for affine4_g32 2048 x 4096 x 4096, bf16, and at most
 // 1 of 134 for affine4_g64 2048 x 6144 x 4096).
 //
-// Bound by matrix instructions with the decoding beside them: 2048 x 6144 x
-// 4096 takes 96 us for mxfp4 (1073 TFLOP/s; 4 conversions per 8 weights), 115
-// for nvfp4 (894; 16 more multiplications and packings), 131 to 143 from card to card
-// for affine4_g64 (11 instructions per 8 weights, 11 of these us the
+// Bound by matrix instructions with the decoding beside them: in a row of
+// calls 2048 x 6144 x 4096 takes 97 us for mxfp4 (1065 TFLOP/s; 4 conversions per 8 weights), 117
+// for nvfp4 (880; 16 more multiplications and packings), 134 to 139 from card to card
+// for affine4_g64 (11 instructions per 8 weights, 10 of these us the
 // preparation); a bf16 library product of these sizes takes 87.  With few
 // tiles the latency of a step's loads, one step ahead, bounds it: 96 x 2050 x
-// 4096 nvfp4 10.5 us and 3 for joining the splits.
+// 4096 nvfp4 11.3 us and 3.9 for joining the splits (12.4 in a row of calls).
 //
 // A wave holds 16 NT rows' codes in registers, one step ahead; the tokens'
 // step (of affine weights: blocks of 16 tokens x 128 inputs, laid out first)
@@ -560,8 +560,8 @@ __device__ __forceinline__ uint32_t lin_ends(uint32_t most, uint32_t least) {
 // token (affine): its power of two, the fp16 copy in the codes' pair order
 // and the group sums' bf16 terms.  row_lanes threads a weight row (affine, and
 // mxfp4 with fp16 tokens), eight groups each at a time: its power of two, the
-// fp16 scales and b + 8 s in bf16 terms (112843 rows of 12 groups: 11.3 us;
-// 29.8 with a wave a row and a group a lane).
+// fp16 scales and b + 8 s in bf16 terms (112843 rows of 24 groups: 9.7 us;
+// of 12 groups, with a wave a row and a group a lane, 29.8).
 struct PrepareArgs {
   const uint16_t* x;
   const uint32_t* w;

@@ -8,7 +8,7 @@
 // the row's, and the lowest expert that has it.  z is read once.
 //
 // Bound by a launch where there are few tokens (4 x 256 fp32, k = 8, with a
-// bias: 3.6 us) and by vector instructions where there are many: 16384 x 256
+// bias: 3.8 us) and by vector instructions where there are many: 16384 x 256
 // bf16, k = 8 takes 9.0 us, its 8.4 MB two.  16-bit logits without a bias
 // make order and expert one word, so a thread's keys can be sorted once and a
 // round is one reduction and a shift (8.3 us of a captured run; 9.8 with a
