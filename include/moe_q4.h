@@ -368,10 +368,9 @@ int moe_sort_pairs(const int32_t *topk_ids, int L, int k, int E, int bm, int32_t
  * token's outputs as infinities or NaN (not always the one the sum itself
  * gives); an E8M0 or E4M3 NaN scale its own row's.  mxfp4 products of elements
  * below 2^-126 are taken as 0, and elements of 2^128 and more may be infinite;
- * sums may be infinite where |x| times
- * a code's 31 is past fp32.  With more than 16 tokens affine scales below
- * 2^-96 may count as 0 beside scales 2^25, or biases 2^84, above them in their
- * row.
+ * sums may be infinite where |x| times a code's 31 is past fp32.  With more
+ * than 16 tokens affine scales below 2^-96 may count as 0 beside scales 2^25,
+ * or biases 2^84, above them in their row.
  * L == 0 returns MOE_Q4_OK without touching the GPU.  Needs
  * L <= MOE_Q4_LINEAR_MAX_L, N <= MOE_Q4_LINEAR_MAX_N, K <= MOE_Q4_LINEAR_MAX_K,
  * ldx <= MOE_Q4_LINEAR_MAX_LDX.
@@ -401,9 +400,9 @@ size_t moe_linear_codec_workspace_bytes(int codec, int L, int N, int K);
  * tell apart are compared in 64 bits.  Weights are fp32: an exponential of a
  * difference d is off by up to 2^-24 (2.5 |d| + 4) of itself, |d| at most the
  * logits' range, scores below 2^-126 may be 0 (renormalised ones keep their
- * ratios), and the gradients carry the same.  A logit of -inf (a masked expert) has
- * score 0; so do all experts of a row of nothing else, whose weights are 0
- * and whose ids are the lowest.  NaN logits rank below -inf.  ids are always
+ * ratios), and the gradients carry the same.  A logit of -inf (a masked
+ * expert) has score 0; so do all experts of a row of nothing else, whose
+ * weights are 0 and whose ids are the lowest.  NaN logits rank below -inf.  ids are always
  * k different experts.  1 <= k <= MOE_Q4_ROUTER_MAX_K, E <= MOE_Q4_MAX_E,
  * T <= MOE_Q4_ROUTER_MAX_T.
  */

@@ -28,12 +28,13 @@
 // 1 of 134 for affine4_g64 2048 x 6144 x 4096).
 //
 // Bound by matrix instructions with the decoding beside them: in a row of
-// calls 2048 x 6144 x 4096 takes 97 us for mxfp4 (1065 TFLOP/s; 4 conversions per 8 weights), 117
-// for nvfp4 (880; 16 more multiplications and packings), 134 to 139 from card to card
-// for affine4_g64 (11 instructions per 8 weights, 10 of these us the
-// preparation); a bf16 library product of these sizes takes 87.  With few
-// tiles the latency of a step's loads, one step ahead, bounds it: 96 x 2050 x
-// 4096 nvfp4 11.3 us and 3.9 for joining the splits (12.4 in a row of calls).
+// calls 2048 x 6144 x 4096 takes 97 us for mxfp4 (1065 TFLOP/s; 4 conversions
+// per 8 weights), 117 for nvfp4 (880; 16 more multiplications and packings),
+// 134 to 139 from card to card for affine4_g64 (11 instructions per 8 weights,
+// 10 of these us the preparation); a bf16 library product of these sizes takes
+// 87.  With few tiles the latency of a step's loads, one step ahead, bounds
+// it: 96 x 2050 x 4096 nvfp4 11.3 us and 3.9 for joining the splits (12.4 in a
+// row of calls).
 //
 // A wave holds 16 NT rows' codes in registers, one step ahead; the tokens'
 // step (of affine weights: blocks of 16 tokens x 128 inputs, laid out first)
@@ -171,7 +172,8 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) asm volatile("" : "+v"(acc[mt][nt]));
   }
-  constexpr bool kScaled = lin_affine(FMT) || (FMT == kLinMxfp4 && F16), kTokens = lin_affine(FMT) && !F16;  // have powers of two
+  // whether rows, and tokens, have powers of two
+  constexpr bool kScaled = lin_affine(FMT) || (FMT == kLinMxfp4 && F16), kTokens = lin_affine(FMT) && !F16;
   int wexp[NT], marks = 0;
   if constexpr (kScaled) {  // the same lanes' rows as the codes'
 #pragma unroll
@@ -374,12 +376,14 @@ __global__ __launch_bounds__(256, 2) void k_linear_tiles(TilesArgs a) {
   }
 
   // A workgroup with a wide row, or an uneven row and a wide token, starts
-  // again: its tokens from memory as they are, every product exact, and the sums in their own units.  mxfp4: the
-  // blocks' powers of two in bf16 operands, x as two bf16 terms.  Affine: the
-  // words transposed over the lanes, so that a product is one group's, and
-  // its fp32 sum times the scale, plus b + 8 s times the group's sum of x.
-  // (2048 x 6144 x 4096 with such a row in every tile: mxfp4 476 us, 102 with
-  // none; affine4_g64 826 and 137, 128 tokens x 4096 x 4096 53 and 23.)
+  // again: its tokens from memory as they are, every product exact, and the
+  // sums in their own units.  mxfp4: the blocks' powers of two in bf16
+  // operands, x as two bf16 terms.  Affine: the words transposed over the
+  // lanes, so that a product is one group's, and its fp32 sum times the scale,
+  // plus b + 8 s times the group's sum of x.  Here and not in place of the
+  // loop above, whose registers it would share.  (2048 x 6144 x 4096 with such
+  // a row in every tile: mxfp4 476 us, 102 with none; affine4_g64 826 and 137,
+  // 128 tokens x 4096 x 4096 53 and 23.)
   bool wide = false;
   if constexpr (kScaled) {
     wide = (wide_waves[0] | wide_waves[1] | wide_waves[2] | wide_waves[3]) != 0;
