@@ -63,6 +63,8 @@ MOE_Q4_LINEAR_MAX_K = 1048576
 MOE_Q4_LINEAR_MAX_N = 268435456
 MOE_Q4_LINEAR_MAX_LDX = 16777216
 MOE_Q4_ROUTER_MAX_T = 1073741824
+MOE_Q4_NORM_MAX_H = 16384
+MOE_Q4_GLU_MAX_LD = 8388608
 
 EXPORTS = (
     "moe_swiglu_q4_workspace_bytes",
@@ -86,6 +88,16 @@ EXPORTS = (
     "moe_balance_loss_workspace_bytes",
     "moe_balance_loss",
     "moe_balance_loss_backward",
+    "moe_rms_norm",
+    "moe_rms_norm_backward",
+    "moe_rms_norm_backward_workspace_bytes",
+    "moe_quantize_fp8",
+    "moe_linear_fp8_forward",
+    "moe_linear_fp8_workspace_bytes",
+    "moe_glu_forward",
+    "moe_glu_workspace_bytes",
+    "moe_glu_backward",
+    "moe_glu_backward_workspace_bytes",
     "moe_q4_read_device_status",
     "moe_q4_clear_device_status",
     "moe_q4_status_string",
@@ -157,6 +169,26 @@ def lib() -> ctypes.CDLL:
     L.moe_balance_loss.restype = I32
     L.moe_balance_loss_backward.argtypes = [P, I32, LL, P, P, P, P, I32, I32, I32, I32, I32, F32, P, LL, P]
     L.moe_balance_loss_backward.restype = I32
+    L.moe_rms_norm.argtypes = [P, I32, LL, P, I32, LL, P, I32, I32, I32, F32, P, LL, P, I32, LL, P, LL, P, P]
+    L.moe_rms_norm.restype = I32
+    L.moe_rms_norm_backward.argtypes = [P, I32, LL, P, I32, P, I32, LL, P, LL, I32, I32, F32, P, LL, P, P, SZ, P]
+    L.moe_rms_norm_backward.restype = I32
+    L.moe_rms_norm_backward_workspace_bytes.argtypes = [I32, I32]
+    L.moe_rms_norm_backward_workspace_bytes.restype = SZ
+    L.moe_quantize_fp8.argtypes = [P, I32, LL, I32, I32, I32, P, LL, P, P]
+    L.moe_quantize_fp8.restype = I32
+    L.moe_linear_fp8_forward.argtypes = [P, LL, P, P, P, P, I32, I32, I32, P, I32, LL, P, SZ, P]
+    L.moe_linear_fp8_forward.restype = I32
+    L.moe_linear_fp8_workspace_bytes.argtypes = [I32] * 3
+    L.moe_linear_fp8_workspace_bytes.restype = SZ
+    L.moe_glu_forward.argtypes = [I32, P, LL, P, P, LL, I32, I32, I32, P, LL, P, P, SZ, P]
+    L.moe_glu_forward.restype = I32
+    L.moe_glu_workspace_bytes.argtypes = [I32] * 3
+    L.moe_glu_workspace_bytes.restype = SZ
+    L.moe_glu_backward.argtypes = [I32, P, LL, P, P, LL, P, LL, P, I32, I32, I32, P, LL, P, P, P, SZ, P]
+    L.moe_glu_backward.restype = I32
+    L.moe_glu_backward_workspace_bytes.argtypes = [I32] * 4
+    L.moe_glu_backward_workspace_bytes.restype = SZ
     L.moe_q4_read_device_status.argtypes = [P, P, P, P]
     L.moe_q4_read_device_status.restype = I32
     L.moe_q4_clear_device_status.argtypes = [P, P]
@@ -572,3 +604,10 @@ def moe_q4_stream_read(buf: torch.Tensor, sink: torch.Tensor, stream=None) -> No
 from .dense import PreparedLinear, moe_linear_codec_forward, moe_linear_codec_workspace_bytes  # noqa: E402
 from .router import (moe_balance_loss, moe_balance_loss_backward, moe_balance_loss_workspace_bytes,  # noqa: E402
                      moe_router_topk, moe_router_topk_backward)
+
+# ---- operators around the expert layer ----
+
+from .fp8 import moe_linear_fp8_forward, moe_linear_fp8_workspace_bytes  # noqa: E402
+from .glu import moe_glu, moe_glu_backward, moe_glu_backward_workspace_bytes, moe_glu_workspace_bytes  # noqa: E402
+from .norm import (moe_quantize_fp8, moe_rms_norm, moe_rms_norm_backward,  # noqa: E402
+                   moe_rms_norm_backward_workspace_bytes, moe_rms_norm_fp8)

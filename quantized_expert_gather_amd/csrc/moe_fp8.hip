@@ -1,0 +1,207 @@
+// Product in 8 bits with a scale for each block of 128:
+//   out[t, n] = sum_b sx[t, b] sw[n / 128, b] (sum over c in block b of x[t, c] w[n, c]) + bias[n]
+// A block of 128 inputs is one step of the matrix cores: its sum comes out of
+// one instruction and enters the fp32 accumulator by one multiply-add with
+// sx sw.  fp32 results, and those of few tokens, which memory bounds either
+// way, multiply the codes as bf16 (kGemmFp8Wide).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <stdint.h>
+
+#include "moe_args.h"
+#include "moe_gemm_device.h"
+#include "moe_gemm_plan.h"
+#include "moe_q4.h"
+
+namespace moeq4 {
+namespace {
+
+struct Fp8Args {
+  const unsigned char* x;
+  const float* sx;
+  const unsigned char* w;
+  const float* sw;
+  const float* bias;
+  void* out;
+  float* part;  // split K: [splits][L][N]
+  long long ldx, ldo;
+  int L, N, K, G, out_dtype;
+  int tok_tiles, row_tiles, steps_per;
+};
+
+// Eight neighbours of a row of the results, or of a split's partial sums.
+__device__ __forceinline__ void fp8_store(const Fp8Args& a, int t, int n, int split, float (&v)[8]) {
+  if (a.part) {
+    norm_store8(a.part + ((size_t)split * a.L + t) * a.N + n, a.N - n, v);
+  } else {
+    if (a.bias) {
+      float b[8];
+      norm_load8(a.bias + n, a.N - n, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += b[i];
+    }
+    norm_store8_as(a.out, a.out_dtype, (long)t * a.ldo + n, a.N - n, v);
+  }
+}
+
+template <int KIND, int MT, int NT, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_fp8_tiles(Fp8Args a) {
+  using S = GemmShape<KIND, MT, NT, WM, WN>;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds0[S::kBuffer], lds1[S::kBuffer];
+  __shared__ float scl0[S::kTok], scl1[S::kTok];
+  int tt, rt;
+  gemm_place(blockIdx.x, a.tok_tiles, a.row_tiles, tt, rt);
+  const int tok0 = tt * S::kTok, row0 = rt * S::kRows;
+  const int wave = threadIdx.x >> 6, wm = wave % WM, wn = wave / WM;
+  const int step0 = blockIdx.y * a.steps_per, step1 = min(a.G, step0 + a.steps_per);
+  gemm_f32x4 acc[MT][NT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = gemm_zero();
+  const int wrow = row0 + wn * NT * 16;
+  const unsigned char* wbase = a.w + (size_t)row0 * a.K;
+  gemm_tile<S>(
+      lds0, lds1, scl0, scl1, a.K, step0, step1, a.x + (size_t)tok0 * a.ldx,
+      [&](int r) { return (uint32_t)min(r, a.L - 1 - tok0) * (uint32_t)a.ldx; }, [&](int) { return wbase; },
+      [&](int r) { return (uint32_t)min(r, a.N - 1 - row0) * (uint32_t)a.K; },
+      a.sx + (size_t)min(tok0 + (int)threadIdx.x, a.L - 1) * a.G,
+      a.sw + (size_t)__builtin_amdgcn_readfirstlane(min(wrow, a.N - 1) / 128) * a.G, acc);
+  __syncthreads();  // the last step's operands have been read
+  constexpr int kWaves = WM * WN, kBytes = 2 * S::kBuffer / kWaves;
+  unsigned char* mine = wave < kWaves / 2 ? lds0 + wave * kBytes : lds1 + (wave - kWaves / 2) * kBytes;
+  gemm_out<MT, NT, kBytes>(reinterpret_cast<float*>(mine), [&](int mt, int nt) { return acc[mt][nt]; }, [&](int r, int c, float (&v)[8]) {
+    const int t = tok0 + wm * MT * 16 + r, n = wrow + c;
+    if (t < a.L && n < a.N) fp8_store(a, t, n, blockIdx.y, v);
+  });
+}
+
+// 16 rows of w a workgroup, their inputs spread over its waves.
+template <int MT, int WAVES, int U>
+__global__ __launch_bounds__(64 * WAVES) void k_fp8_rows(Fp8Args a) {
+  __shared__ gemm_f32x4 lds[WAVES][MT][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, kb = lane >> 4;
+  const int row0 = blockIdx.x * 16;
+  const unsigned char* tok[MT];
+  const float* sx[MT];
+  gemm_f32x4 acc[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const size_t t = min(mt * 16 + n16, a.L - 1);
+    tok[mt] = a.x + t * a.ldx;
+    sx[mt] = a.sx + t * a.G;
+    acc[mt] = gemm_f32x4{0, 0, 0, 0};
+  }
+  gemm_rows<kGemmFp8Wide, MT, U>(a.w + (size_t)min(row0 + n16, a.N - 1) * a.K, tok, a.K, wave, WAVES, a.G,
+                             a.sw + (size_t)(row0 / 128) * a.G, sx, acc);
+  gemm_f32x4 v = gemm_join_waves<MT, WAVES>(lds, acc);
+  const int t = wave * 16 + n16, n = row0 + 4 * kb;
+  if (wave >= MT || t >= a.L || n >= a.N) return;
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += a.bias[min(n + i, a.N - 1)];
+  }
+  float out[8] = {v[0], v[1], v[2], v[3], 0, 0, 0, 0};
+  norm_store8_as(a.out, a.out_dtype, (long)t * a.ldo + n, min(a.N - n, 4), out);
+}
+
+// Partial sums of a split K, added in their order.
+__global__ __launch_bounds__(256) void k_fp8_join(const float* part, const float* bias, void* out, long long ldo, int L, int N,
+                                                  int splits, int dtype) {
+  const size_t all = (size_t)L * N;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (size_t)gridDim.x * 256) {
+    const size_t t = i / N;
+    const int n = (int)(i - t * N);
+    float s = part[i];
+    for (int p = 1; p < splits; ++p) s += part[p * all + i];
+    if (bias) s += bias[n];
+    const size_t at = t * ldo + n;
+    if (dtype == MOE_Q4_DTYPE_F32)
+      static_cast<float*>(out)[at] = s;
+    else if (dtype == MOE_Q4_DTYPE_BF16)
+      static_cast<__bf16*>(out)[at] = (__bf16)s;
+    else
+      static_cast<_Float16*>(out)[at] = (_Float16)s;
+  }
+}
+
+int fp8_status(int L, int N, int K) {
+  if (L < 0 || N < 1 || K < 1) return MOE_Q4_ERR_SHAPE;
+  if (K % 16 || L > MOE_Q4_LINEAR_MAX_L || N > MOE_Q4_LINEAR_MAX_N || K > MOE_Q4_LINEAR_MAX_K) return MOE_Q4_ERR_UNSUPPORTED;
+  return MOE_Q4_OK;
+}
+
+bool fp8_by_rows(int L) { return L <= 32; }
+GemmPlan fp8_plan(int L, int N, int K, bool wide) { return gemm_plan(L, N, (K + 127) / 128, wide ? 1 : 0); }
+size_t fp8_part(int L, int N, int K, bool wide) {
+  const GemmPlan p = fp8_plan(L, N, K, wide);
+  return p.splits > 1 ? ((size_t)p.splits * L * N * 4 + 255) & ~size_t(255) : 0;
+}
+
+}  // namespace
+}  // namespace moeq4
+
+using namespace moeq4;
+
+extern "C" size_t moe_linear_fp8_workspace_bytes(int L, int N, int K) {
+  if (fp8_status(L, N, K) || L == 0 || fp8_by_rows(L)) return 0;
+  return std::max(fp8_part(L, N, K, false), fp8_part(L, N, K, true));
+}
+
+extern "C" int moe_linear_fp8_forward(const uint8_t* x, long long ldx, const float* sx, const uint8_t* w, const float* sw,
+                                      const float* bias, int L, int N, int K, void* out, int out_dtype, long long ldo,
+                                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int st = fp8_status(L, N, K);
+  if (st) return st;
+  if (ldx < K || ldo < N) return MOE_Q4_ERR_SHAPE;
+  const size_t os = args_size(out_dtype);
+  if (!os || (L > 1 && ldx > MOE_Q4_LINEAR_MAX_LDX)) return MOE_Q4_ERR_UNSUPPORTED;
+  if (L == 0) return MOE_Q4_OK;
+  if (!x || !sx || !w || !sw || !out) return MOE_Q4_ERR_NULL;
+  if (!args_aligned(x, 16) || (L > 1 && ldx % 16) || !args_aligned(w, 16) || !args_aligned(sx, 4) || !args_aligned(sw, 4) ||
+      !args_aligned(bias, 4) || !args_aligned(out, os))
+    return MOE_Q4_ERR_ALIGN;
+  const size_t need = moe_linear_fp8_workspace_bytes(L, N, K);
+  if (need && (!workspace || workspace_bytes < need)) return MOE_Q4_ERR_WORKSPACE;
+  if (need && !args_aligned(workspace, 256)) return MOE_Q4_ERR_ALIGN;
+  const int G = (K + 127) / 128;
+  const ArgSpan ins[] = {{x, args_span(L, ldx, K, 1)}, {sx, (size_t)L * G * 4}, {w, (size_t)N * K},
+                         {sw, ((size_t)N + 127) / 128 * G * 4}, {bias, bias ? (size_t)N * 4 : 0}};
+  const ArgSpan outs[] = {{out, args_span(L, ldo, N, os)}, {need ? workspace : nullptr, need}};
+  if (args_alias(outs, ins)) return MOE_Q4_ERR_ALIAS;
+  Fp8Args a{x, sx, w, sw, bias, out, nullptr, ldx, ldo, L, N, K, G, out_dtype, 0, 0, 0};
+  if (fp8_by_rows(L)) {
+    const dim3 grid((N + 15) / 16);
+    if (L <= 16)
+      hipLaunchKernelGGL((k_fp8_rows<1, 8, 4>), grid, dim3(512), 0, stream, a);
+    else
+      hipLaunchKernelGGL((k_fp8_rows<2, 8, 4>), grid, dim3(512), 0, stream, a);
+    return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+  }
+  const GemmPlan p = fp8_plan(L, N, K, out_dtype == MOE_Q4_DTYPE_F32);
+  a.tok_tiles = p.tok_tiles;
+  a.row_tiles = p.row_tiles;
+  a.steps_per = p.steps_per;
+  if (p.splits > 1) a.part = static_cast<float*>(workspace);
+  const dim3 grid((unsigned)(p.tok_tiles * p.row_tiles), p.splits);
+  if (out_dtype == MOE_Q4_DTYPE_F32) {
+    if (p.shape == kGemm128x128)
+      hipLaunchKernelGGL((k_fp8_tiles<kGemmFp8Wide, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL((k_fp8_tiles<kGemmFp8Wide, 4, 2, 1, 4>), grid, dim3(256), 0, stream, a);
+  } else {
+    switch (p.shape) {
+      case kGemm256x256: hipLaunchKernelGGL((k_fp8_tiles<kGemmFp8, 8, 4, 2, 4>), grid, dim3(512), 0, stream, a); break;
+      case kGemm128x128: hipLaunchKernelGGL((k_fp8_tiles<kGemmFp8, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
+      default: hipLaunchKernelGGL((k_fp8_tiles<kGemmFp8, 4, 2, 1, 4>), grid, dim3(256), 0, stream, a); break;
+    }
+  }
+  if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
+  if (p.splits > 1) {
+    const size_t all = (size_t)L * N;
+    hipLaunchKernelGGL(k_fp8_join, dim3((unsigned)std::min<size_t>((all + 255) / 256, 4096)), dim3(256), 0, stream, a.part,
+                       bias, out, ldo, L, N, p.splits, out_dtype);
+  }
+  return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+}

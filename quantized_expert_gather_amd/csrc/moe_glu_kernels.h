@@ -1,0 +1,327 @@
+// Kernels of the gated feed-forward block and its gradient, for 16-bit types.
+// Each type is instantiated in a source of its own (moe_glu_inst_*.hip).
+// Internal header.
+//
+//   forward   g = x Wg^T, u = x Wu^T, h = silu(g) u: one product whose tile takes
+//             the same rows of Wg and Wu, so that a lane holds g and u of a result
+//   backward  dg = dh u silu'(g), du = dh silu(g), side by side as D [T, 2I];
+//             dx = D [Wg; Wu], [dWg; dWu] = D^T x
+// The backward's products have their sums along the operands' other axis:
+// transposed copies of D, x and the weights make them the same product.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "moe_gemm_device.h"
+#include "moe_gemm_plan.h"
+#include "moe_q4.h"
+
+namespace moeq4 {
+
+struct GluArgs {
+  const unsigned char *x, *wg, *wu;  // rows ldx, ldw bytes apart
+  void* h;                           // or NULL
+  float* saved;                      // [2][T][I], or NULL
+  float* part;                       // split K: [splits][2][T][I]
+  long long ldx, ldw, ldh;           // ldh in elements
+  int T, H, I;
+  int tok_tiles, row_tiles, steps_per, steps;
+};
+
+// C [M, N] = A B^T over K elements; rows of C from `cut` on go to out1.
+struct GluMmArgs {
+  const unsigned char *a, *b;  // rows lda, ldb bytes apart
+  void *out0, *out1;
+  float* part;                 // split K: [splits][M][N]
+  long long lda, ldb, ldo;     // ldo in elements
+  int M, N, kbytes, cut;
+  int tok_tiles, row_tiles, steps_per, steps;
+};
+
+// Launches for each type; MOE_Q4_* status.
+int glu_forward_bf16(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t stream);
+int glu_forward_f16(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t stream);
+int glu_mm_bf16(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream);
+int glu_mm_f16(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream);
+// D [T][2I] and its transpose [2I][Tp] (zeros from T on) from g, u and dh
+// (lddh elements apart); either may be NULL.
+int glu_grad_bf16(const float* saved, const void* dh, long long lddh, int T, int I, int Tp, void* d, void* dt, hipStream_t stream);
+int glu_grad_f16(const float* saved, const void* dh, long long lddh, int T, int I, int Tp, void* d, void* dt, hipStream_t stream);
+
+// Writes the transpose of a workgroup's 64 x 64 numbers in LDS: rows c0 + c (to
+// C) of dst from column r0 on, a multiple of 64 (to Rp, a multiple of 8).
+constexpr int kGluPad = 64 + 8;
+__device__ __forceinline__ void glu_put_transposed(const uint16_t (&tile)[64][kGluPad], uint16_t* dst, long long ldd, int c0,
+                                                   int C, int r0, int Rp) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = threadIdx.x / 8 + 32 * i, r = (threadIdx.x % 8) * 8;
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = tile[r + 2 * j][c] | (uint32_t)tile[r + 2 * j + 1][c] << 16;
+    if (c0 + c < C && r0 + r < Rp) *reinterpret_cast<uint4*>(dst + (size_t)(c0 + c) * ldd + r0 + r) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+#ifdef MOE_GLU_INST
+
+template <int KIND> struct GluType;
+template <> struct GluType<kGemmBf16> { typedef __bf16 type; };
+template <> struct GluType<kGemmF16> { typedef _Float16 type; };
+
+// 1 / (1 + e^-g): the exponential of the hardware's 2^x is off by about
+// 2^-24 |g| of itself, far below a 16-bit result's half step.
+__device__ __forceinline__ float glu_sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+
+template <int KIND, int MT, int NT, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_glu_tiles(GluArgs a) {
+  using S = GemmShape<KIND, MT, NT, WM, WN>;
+  typedef typename GluType<KIND>::type T16;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds0[S::kBuffer], lds1[S::kBuffer];
+  int tt, rt;
+  gemm_place(blockIdx.x, a.tok_tiles, a.row_tiles, tt, rt);
+  constexpr int kHalf = 8 * NT;  // results of a wave: its first rows are Wg's, its others Wu's
+  const int tok0 = tt * S::kTok, n0 = rt * (S::kRows / 2);
+  const int wave = threadIdx.x >> 6, wm = wave % WM, wn = wave / WM;
+  const int step0 = blockIdx.y * a.steps_per, step1 = min(a.steps, step0 + a.steps_per);
+  gemm_f32x4 acc[MT][NT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = gemm_zero();
+  const unsigned char *g0 = a.wg + (size_t)n0 * a.ldw, *u0 = a.wu + (size_t)n0 * a.ldw;
+  gemm_tile<S>(
+      lds0, lds1, nullptr, nullptr, 2 * a.H, step0, step1, a.x + (size_t)tok0 * a.ldx,
+      [&](int r) { return (uint32_t)min(r, a.T - 1 - tok0) * (uint32_t)a.ldx; },
+      [&](int r) { return r % (2 * kHalf) < kHalf ? g0 : u0; },
+      [&](int r) { return (uint32_t)min(r / (2 * kHalf) * kHalf + r % kHalf, a.I - 1 - n0) * (uint32_t)a.ldw; }, nullptr,
+      nullptr, acc);
+  __syncthreads();  // the last step's operands have been read
+  constexpr int kWaves = WM * WN, kBytes = 2 * S::kBuffer / kWaves;
+  float* mine = reinterpret_cast<float*>(wave < kWaves / 2 ? lds0 + wave * kBytes : lds1 + (wave - kWaves / 2) * kBytes);
+  const int t0 = tok0 + wm * MT * 16, c0 = n0 + wn * kHalf;
+  float* keep = a.part ? a.part + (size_t)blockIdx.y * 2 * a.T * a.I : a.saved;
+  if (keep) {
+#pragma unroll
+    for (int up = 0; up < 2; ++up)
+      gemm_out<MT, NT / 2, kBytes>(
+          mine, [&](int mt, int nt) { return acc[mt][nt + up * (NT / 2)]; },
+          [&](int r, int c, float (&v)[8]) {
+            if (t0 + r < a.T && c0 + c < a.I) norm_store8(keep + ((size_t)up * a.T + t0 + r) * a.I + c0 + c, a.I - c0 - c, v);
+          });
+  }
+  if (a.h && !a.part)
+    gemm_out<MT, NT / 2, kBytes>(
+        mine,
+        [&](int mt, int nt) {
+          const gemm_f32x4 g = acc[mt][nt], u = acc[mt][nt + NT / 2];
+          gemm_f32x4 h;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = g[i] * glu_sigmoid(g[i]) * u[i];
+          return h;
+        },
+        [&](int r, int c, float (&v)[8]) {
+          if (t0 + r < a.T && c0 + c < a.I) norm_store8(static_cast<T16*>(a.h) + (size_t)(t0 + r) * a.ldh + c0 + c, a.I - c0 - c, v);
+        });
+}
+
+// Few tokens: 8 rows of Wg and the same of Wu a workgroup, their inputs spread over its waves.
+template <int KIND, int MT, int WAVES, int U>
+__global__ __launch_bounds__(64 * WAVES) void k_glu_rows(GluArgs a) {
+  typedef typename GluType<KIND>::type T16;
+  __shared__ gemm_f32x4 lds[WAVES][MT][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, kb = lane >> 4;
+  const int row0 = blockIdx.x * 8;
+  const unsigned char* tok[MT];
+  const float* none[MT];
+  gemm_f32x4 acc[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    tok[mt] = a.x + (size_t)min(mt * 16 + n16, a.T - 1) * a.ldx;
+    none[mt] = nullptr;
+    acc[mt] = gemm_f32x4{0, 0, 0, 0};
+  }
+  // (I is a multiple of 8: every row is there)
+  const unsigned char* row = (n16 < 8 ? a.wg : a.wu) + (size_t)(row0 + (n16 & 7)) * a.ldw;
+  gemm_rows<KIND, MT, U>(row, tok, 2 * a.H, wave, WAVES, a.steps, nullptr, none, acc);
+  gemm_f32x4 v = gemm_join_waves<MT, WAVES>(lds, acc);
+  // lanes of kb 0 and 1 hold g, those of kb 2 and 3 u of the same results
+  gemm_f32x4 u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = __shfl_xor(v[i], 32);
+  const int t = wave * 16 + n16, n = row0 + 4 * (kb & 1);
+  if (wave >= MT || t >= a.T) return;
+  if (a.saved) *reinterpret_cast<gemm_f32x4*>(a.saved + ((size_t)(kb >> 1) * a.T + t) * a.I + n) = v;
+  if (a.h && kb < 2) {
+    float h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = v[i] * glu_sigmoid(v[i]) * u[i];
+    norm_store8(static_cast<T16*>(a.h) + (size_t)t * a.ldh + n, 4, h);
+  }
+}
+
+// Partial sums of a split K, added in their order: g and u, and h of them.
+template <int KIND>
+__global__ __launch_bounds__(256) void k_glu_join(GluArgs a, int splits) {
+  typedef typename GluType<KIND>::type T16;
+  const size_t all = (size_t)a.T * a.I / 8;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (size_t)gridDim.x * 256) {
+    float s[2][8], v[8];
+#pragma unroll
+    for (int up = 0; up < 2; ++up) {
+      norm_load8(a.part + up * all * 8 + i * 8, 8, s[up]);
+      for (int p = 1; p < splits; ++p) {
+        norm_load8(a.part + (2 * p + up) * all * 8 + i * 8, 8, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[up][j] += v[j];
+      }
+      if (a.saved) norm_store8(a.saved + up * all * 8 + i * 8, 8, s[up]);
+    }
+    if (a.h) {
+      const size_t t = i * 8 / a.I;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = s[0][j] * glu_sigmoid(s[0][j]) * s[1][j];
+      norm_store8(static_cast<T16*>(a.h) + t * a.ldh + (i * 8 - t * a.I), 8, v);
+    }
+  }
+}
+
+template <int KIND, int MT, int NT, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_glu_mm(GluMmArgs a) {
+  using S = GemmShape<KIND, MT, NT, WM, WN>;
+  typedef typename GluType<KIND>::type T16;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds0[S::kBuffer], lds1[S::kBuffer];
+  int tt, rt;
+  gemm_place(blockIdx.x, a.tok_tiles, a.row_tiles, tt, rt);
+  const int tok0 = tt * S::kTok, row0 = rt * S::kRows;
+  const int wave = threadIdx.x >> 6, wm = wave % WM, wn = wave / WM;
+  const int step0 = blockIdx.y * a.steps_per, step1 = min(a.steps, step0 + a.steps_per);
+  gemm_f32x4 acc[MT][NT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = gemm_zero();
+  const unsigned char* b0 = a.b + (size_t)row0 * a.ldb;
+  gemm_tile<S>(
+      lds0, lds1, nullptr, nullptr, a.kbytes, step0, step1, a.a + (size_t)tok0 * a.lda,
+      [&](int r) { return (uint32_t)min(r, a.M - 1 - tok0) * (uint32_t)a.lda; }, [&](int) { return b0; },
+      [&](int r) { return (uint32_t)min(r, a.N - 1 - row0) * (uint32_t)a.ldb; }, nullptr, nullptr, acc);
+  __syncthreads();  // the last step's operands have been read
+  constexpr int kWaves = WM * WN, kBytes = 2 * S::kBuffer / kWaves;
+  float* mine = reinterpret_cast<float*>(wave < kWaves / 2 ? lds0 + wave * kBytes : lds1 + (wave - kWaves / 2) * kBytes);
+  gemm_out<MT, NT, kBytes>(
+      mine, [&](int mt, int nt) { return acc[mt][nt]; },
+      [&](int r, int c, float (&v)[8]) {
+        const int m = tok0 + wm * MT * 16 + r, n = row0 + wn * NT * 16 + c;
+        if (m >= a.M || n >= a.N) return;
+        if (a.part)
+          norm_store8(a.part + ((size_t)blockIdx.y * a.M + m) * a.N + n, a.N - n, v);
+        else
+          norm_store8(static_cast<T16*>(m < a.cut ? a.out0 : a.out1) + (size_t)(m < a.cut ? m : m - a.cut) * a.ldo + n, a.N - n, v);
+      });
+}
+
+// (N is a multiple of 8)
+template <int KIND>
+__global__ __launch_bounds__(256) void k_glu_mm_join(GluMmArgs a, int splits) {
+  typedef typename GluType<KIND>::type T16;
+  const size_t all = (size_t)a.M * a.N / 8;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (size_t)gridDim.x * 256) {
+    float s[8], v[8];
+    norm_load8(a.part + i * 8, 8, s);
+    for (int p = 1; p < splits; ++p) {
+      norm_load8(a.part + (size_t)p * all * 8 + i * 8, 8, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += v[j];
+    }
+    const int m = (int)(i * 8 / a.N), n = (int)(i * 8 - (size_t)m * a.N);
+    norm_store8(static_cast<T16*>(m < a.cut ? a.out0 : a.out1) + (size_t)(m < a.cut ? m : m - a.cut) * a.ldo + n, 8, s);
+  }
+}
+
+// 64 tokens x 64 of the I outputs a workgroup.
+template <int KIND>
+__global__ __launch_bounds__(256) void k_glu_grad(const float* saved, const void* dh, long long lddh, int T, int I, int Tp,
+                                                  void* d, uint16_t* dt) {
+  typedef typename GluType<KIND>::type T16;
+  __shared__ __attribute__((aligned(16))) uint16_t tg[64][kGluPad], tu[64][kGluPad];
+  const int across = (I + 63) / 64, r0 = blockIdx.x / across * 64, c0 = blockIdx.x % across * 64;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = threadIdx.x / 8 + 32 * i, c = (threadIdx.x % 8) * 8;
+    const int n = r0 + r < T ? min(I - c0 - c, 8) : 0;  // (0 or 8)
+    const size_t at = (size_t)min(r0 + r, T - 1) * I + c0 + c;
+    float g[8], u[8], e[8], dg[8], du[8];
+    norm_load8(saved + at, n, g);
+    norm_load8(saved + (size_t)T * I + at, n, u);
+    norm_load8(static_cast<const T16*>(dh) + (size_t)min(r0 + r, T - 1) * lddh + c0 + c, n, e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float s = glu_sigmoid(g[j]);
+      dg[j] = e[j] * u[j] * (s * __builtin_fmaf(g[j], 1.0f - s, 1.0f));
+      du[j] = e[j] * (g[j] * s);
+    }
+    if (d) {
+      T16* to = static_cast<T16*>(d) + (size_t)min(r0 + r, T - 1) * 2 * I + c0 + c;
+      norm_store8(to, n, dg);
+      norm_store8(to + I, n, du);
+    }
+    norm_store8(reinterpret_cast<T16*>(&tg[r][c]), 8, dg);
+    norm_store8(reinterpret_cast<T16*>(&tu[r][c]), 8, du);
+  }
+  if (!dt) return;
+  __syncthreads();
+  glu_put_transposed(tg, dt, Tp, c0, I, r0, Tp);
+  glu_put_transposed(tu, dt + (size_t)I * Tp, Tp, c0, I, r0, Tp);
+}
+
+template <int KIND>
+int glu_forward_kind(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t stream) {
+  if (rows) {
+    const dim3 grid(a.I / 8);
+    if (a.T <= 16)
+      hipLaunchKernelGGL((k_glu_rows<KIND, 1, 16, 3>), grid, dim3(1024), 0, stream, a);
+    else
+      hipLaunchKernelGGL((k_glu_rows<KIND, 2, 16, 2>), grid, dim3(1024), 0, stream, a);
+    return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+  }
+  const dim3 grid((unsigned)(p.tok_tiles * p.row_tiles), p.splits);
+  switch (p.shape) {
+    case kGemm256x256: hipLaunchKernelGGL((k_glu_tiles<KIND, 8, 4, 2, 4>), grid, dim3(512), 0, stream, a); break;
+    case kGemm128x128: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    default: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 2, 1, 4>), grid, dim3(256), 0, stream, a); break;
+  }
+  if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
+  if (p.splits > 1) {
+    const size_t all = (size_t)a.T * a.I / 8;
+    hipLaunchKernelGGL((k_glu_join<KIND>), dim3((unsigned)std::min<size_t>((all + 255) / 256, 4096)), dim3(256), 0, stream, a, p.splits);
+  }
+  return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+}
+
+template <int KIND>
+int glu_mm_kind(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream) {
+  const dim3 grid((unsigned)(p.tok_tiles * p.row_tiles), p.splits);
+  switch (p.shape) {
+    case kGemm256x256: hipLaunchKernelGGL((k_glu_mm<KIND, 8, 4, 2, 4>), grid, dim3(512), 0, stream, a); break;
+    case kGemm128x128: hipLaunchKernelGGL((k_glu_mm<KIND, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    default: hipLaunchKernelGGL((k_glu_mm<KIND, 4, 2, 1, 4>), grid, dim3(256), 0, stream, a); break;
+  }
+  if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
+  if (p.splits > 1) {
+    const size_t all = (size_t)a.M * a.N / 8;
+    hipLaunchKernelGGL((k_glu_mm_join<KIND>), dim3((unsigned)std::min<size_t>((all + 255) / 256, 4096)), dim3(256), 0, stream, a, p.splits);
+  }
+  return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+}
+
+template <int KIND>
+int glu_grad_kind(const float* saved, const void* dh, long long lddh, int T, int I, int Tp, void* d, void* dt, hipStream_t stream) {
+  const dim3 grid((unsigned)(((T + 63) / 64) * ((I + 63) / 64)));
+  hipLaunchKernelGGL((k_glu_grad<KIND>), grid, dim3(256), 0, stream, saved, dh, lddh, T, I, Tp, d, static_cast<uint16_t*>(dt));
+  return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+}
+#endif
+
+}  // namespace moeq4

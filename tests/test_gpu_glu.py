@@ -1,0 +1,188 @@
+"""The gated block and its gradient on the GPU against 64-bit references (needs an MI355X)."""
+
+import pytest
+import torch
+
+import quantized_expert_gather_amd as q
+from tests import around_refs as R
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def problem(T, H, I, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed + 5 * T + 3 * H + I)
+    x = torch.randn(T, H, generator=g).to(dtype)
+    wg, wu = ((torch.randn(I, H, generator=g) / H ** 0.5).to(dtype) for _ in range(2))
+    return x, wg, wu, torch.randn(T, I, generator=g).to(dtype)
+
+
+def check_forward(T, H, I, dtype):
+    print("[case] glu", T, H, I, dtype, flush=True)
+    x, wg, wu, _ = problem(T, H, I, dtype)
+    g, u, h, bg, bu, bh = R.glu(x, wg, wu)
+    saved = torch.full((2, T, I), 9.0, device="cuda")
+    got = q.moe_glu(x.cuda(), wg.cuda(), wu.cuda(), saved=saved)
+    R.check(got, h, bh, dtype)
+    R.check(saved[0], g, bg)
+    R.check(saved[1], u, bu)
+    assert torch.equal(q.moe_glu(x.cuda(), wg.cuda(), wu.cuda()), got)
+
+
+def check_backward(T, H, I, dtype, saved):
+    print("[case] glu backward", T, H, I, dtype, saved, flush=True)
+    x, wg, wu, dh = problem(T, H, I, dtype)
+    refs, bounds = R.glu_backward(x, wg, wu, dh)
+    d = [t.cuda() for t in (x, wg, wu)]
+    keep = None
+    if saved:
+        keep = torch.empty(2, T, I, device="cuda")
+        q.moe_glu(*d, saved=keep)
+    for got, ref, bound in zip(q.moe_glu_backward(*d, dh.cuda(), saved=keep), refs, bounds):
+        R.check(got, ref, bound, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 2, 16, 17, 32, 33, 64, 65, 100, 129, 260])
+@pytest.mark.parametrize("H,I", [(8, 8), (64, 72), (136, 128), (520, 264)])
+def test_forward_sizes(T, H, I):
+    check_forward(T, H, I, BF16)
+
+
+@pytest.mark.parametrize("T,H,I", [(4, 1024, 2048), (48, 2056, 200), (96, 512, 1416), (700, 264, 2600), (1500, 200, 1400)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_forward_larger(T, H, I, dtype):
+    check_forward(T, H, I, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 7, 33, 64, 130])
+@pytest.mark.parametrize("H,I", [(8, 8), (72, 136), (264, 200)])
+@pytest.mark.parametrize("saved", [True, False])
+def test_backward_sizes(T, H, I, saved):
+    check_backward(T, H, I, BF16, saved)
+
+
+@pytest.mark.parametrize("T,H,I", [(40, 1024, 520), (513, 776, 256), (1000, 136, 1032), (300, 2056, 1416)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("saved", [True, False])
+def test_backward_larger(T, H, I, dtype, saved):
+    check_backward(T, H, I, dtype, saved)
+
+
+def test_backward_against_differences():
+    x, wg, wu, dh = problem(5, 16, 8, F16)
+    dx, dwg, dwu = (t.double().cpu() for t in q.moe_glu_backward(x.cuda(), wg.cuda(), wu.cuda(), dh.cuda()))
+    x, wg, wu, dh = (t.double() for t in (x, wg, wu, dh))
+    f = lambda a, b, c: (R.glu(a, b, c)[2] * dh).sum()  # noqa: E731
+    for which, grad in ((0, dx), (1, dwg), (2, dwu)):
+        for i, j in ((0, 0), (3, 11), (4, 15)):
+            a, b = [x.clone(), wg.clone(), wu.clone()], [x.clone(), wg.clone(), wu.clone()]
+            a[which][i, j] += 1e-5
+            b[which][i, j] -= 1e-5
+            # two roundings to fp16 of numbers near 1, the first summed over up to 16
+            assert abs((f(*a) - f(*b)) / 2e-5 - grad[i, j]) < 16 * 2.0 ** -11 * (1 + grad.abs().max())
+
+
+def test_strides_and_given_outputs():
+    for T in (6, 150):
+        x, wg, wu, dh = problem(T, 136, 72, BF16)
+        both = torch.cat((wg, wu)).cuda()  # halves of one matrix
+        xb = torch.zeros(T, 160, dtype=BF16, device="cuda")
+        xb[:, 8:144] = x.cuda()
+        eb = torch.zeros(T, 81, dtype=BF16, device="cuda")
+        eb[:, 5:77] = dh.cuda()
+        out, dxb = torch.full((T, 90), 3.0, dtype=BF16, device="cuda"), torch.full((T, 150), 3.0, dtype=BF16, device="cuda")
+        q.moe_glu(xb[:, 8:144], both[:72], both[72:], out=out[:, 1:73])
+        _, _, h, _, _, bh = R.glu(x, wg, wu)
+        R.check(out[:, 1:73], h, bh)
+        assert (out[:, 0] == 3).all() and (out[:, 73:] == 3).all()
+        grads = torch.empty(2, 72, 136, dtype=BF16, device="cuda")
+        q.moe_glu_backward(xb[:, 8:144], both[:72], both[72:], eb[:, 5:77], dx=dxb[:, 7:143], dwg=grads[0], dwu=grads[1])
+        refs, bounds = R.glu_backward(x, wg, wu, dh)
+        for got, ref, bound in zip((dxb[:, 7:143], grads[0], grads[1]), refs, bounds):
+            R.check(got, ref, bound)
+        assert (dxb[:, :7] == 3).all() and (dxb[:, 143:] == 3).all()
+
+
+@pytest.mark.parametrize("recompute", [False, True])
+@pytest.mark.parametrize("T", [3, 200])
+def test_autograd(recompute, T):
+    x, wg, wu, dh = problem(T, 128, 64, BF16)
+    leaves = [t.cuda().requires_grad_() for t in (x, wg, wu)]
+    q.moe_glu(*leaves, recompute=recompute).backward(dh.cuda())
+    refs, bounds = R.glu_backward(x, wg, wu, dh)
+    for leaf, ref, bound in zip(leaves, refs, bounds):
+        R.check(leaf.grad, ref, bound)
+    for which in range(3):  # one alone
+        one = [t.cuda().requires_grad_(i == which) for i, t in enumerate((x, wg, wu))]
+        q.moe_glu(*one, recompute=recompute).backward(dh.cuda())
+        assert torch.equal(one[which].grad, leaves[which].grad)
+        assert all(t.grad is None for i, t in enumerate(one) if i != which)
+
+
+@pytest.mark.parametrize("T", [5, 140])
+def test_infinities_and_nan_stay_with_their_rows(T):
+    x, wg, wu, _ = problem(T, 200, 64, BF16)
+    _, _, h, _, _, bh = R.glu(x, wg, wu)
+    x, wg = x.clone(), wg.clone()
+    x[1, 199] = float("inf")
+    x[2, 0] = float("nan")
+    wg[63, 199] = float("nan")
+    got = q.moe_glu(x.cuda(), wg.cuda(), wu.cuda()).cpu()
+    assert torch.isnan(got[2]).all() and torch.isnan(got[:, 63]).all()
+    rows = [0] + list(range(3, T))
+    R.check(got[rows][:, :63], h[rows][:, :63], bh[rows][:, :63])
+
+
+def test_large_gates():
+    x, wg, wu, dh = problem(70, 64, 64, BF16)
+    x = x * 60  # gates of a few hundred: the sigmoid is 0 or 1
+    g, u, h, bg, bu, bh = R.glu(x, wg, wu)
+    R.check(q.moe_glu(x.cuda(), wg.cuda(), wu.cuda()), h, bh)
+    refs, bounds = R.glu_backward(x, wg, wu, dh)
+    for got, ref, bound in zip(q.moe_glu_backward(x.cuda(), wg.cuda(), wu.cuda(), dh.cuda()), refs, bounds):
+        R.check(got, ref, bound)
+
+
+def test_no_tokens():
+    x, wg, wu, dh = (t.cuda() for t in problem(2, 64, 40, F16))
+    assert q.moe_glu(x[:0], wg, wu).shape == (0, 40)
+    dx, dwg, dwu = q.moe_glu_backward(x[:0], wg, wu, dh[:0])
+    assert dx.shape == (0, 64) and (dwg == 0).all() and (dwu == 0).all() and dwg.shape == (40, 64)
+
+
+@pytest.mark.parametrize("T", [4, 96, 300])
+def test_graph_stream_and_repeats(T):
+    x, wg, wu, dh = (t.cuda() for t in problem(T, 1024, 512, BF16))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    keep = torch.empty(2, T, 512, device="cuda")
+    h = q.moe_glu(x, wg, wu, saved=keep, stream=side)
+    a = q.moe_glu_backward(x, wg, wu, dh, saved=keep, stream=side)
+    torch.cuda.synchronize()
+    ws = torch.empty(q.moe_glu_backward_workspace_bytes(T, 1024, 512), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    saved = torch.empty(2, T, 512, device="cuda")
+    with torch.cuda.graph(graph):
+        hg = q.moe_glu(x, wg, wu, saved=saved)
+        b = q.moe_glu_backward(x, wg, wu, dh, saved=saved, workspace=ws)
+    for _ in range(3):
+        for t in (hg, saved, *b):
+            t.zero_()
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(hg, h) and all(torch.equal(s, t) for s, t in zip(a, b))
+        c = q.moe_glu_backward(x, wg, wu, dh, saved=keep)
+        assert all(torch.equal(s, t) for s, t in zip(a, c))
+
+
+def test_backward_of_a_captured_step_is_refused(monkeypatch):
+    x, wg, wu, dh = (t.cuda() for t in problem(4, 64, 64, BF16))
+    x.requires_grad_()
+    h = q.moe_glu(x, wg, wu)
+    y = q.moe_rms_norm(x)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="moe_glu_backward"):
+        h.backward(dh)
+    with pytest.raises(RuntimeError, match="moe_rms_norm_backward"):
+        y.backward(x.detach())
