@@ -27,53 +27,64 @@ struct Fp8Args {
   float* part;  // split K: [splits][L][N]
   long long ldx, ldo;
   int L, N, K, G, out_dtype;
-  int tok_tiles, row_tiles, steps_per;
+  GemmTiles tiles;
 };
 
-// Eight neighbours of a row of the results, or of a split's partial sums.
-__device__ __forceinline__ void fp8_store(const Fp8Args& a, int t, int n, int split, float (&v)[8]) {
-  if (a.part) {
-    norm_store8(a.part + ((size_t)split * a.L + t) * a.N + n, a.N - n, v);
-  } else {
-    if (a.bias) {
-      float b[8];
-      norm_load8(a.bias + n, a.N - n, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += b[i];
-    }
-    norm_store8_as(a.out, a.out_dtype, (long)t * a.ldo + n, a.N - n, v);
+template <class S>
+struct Fp8Source {
+  const Fp8Args& a;
+  const unsigned char *tok, *row;
+  const float* scales;
+  int toks, rows;  // the tile's last token and row
+  __device__ __forceinline__ void set(const GemmPlace& p) {
+    const int tok0 = p.tok * S::kTok, row0 = p.row * S::kRows, tid = threadIdx.x;
+    tok = a.x + (size_t)tok0 * a.ldx;
+    row = a.w + (size_t)row0 * a.K;
+    toks = a.L - 1 - tok0;
+    rows = a.N - 1 - row0;
+    scales = tid < S::kTok ? a.sx + (size_t)min(tok0 + tid, a.L - 1) * a.G
+                           : a.sw + (size_t)min(row0 / 128 + tid - S::kTok, (a.N - 1) / 128) * a.G;
   }
-}
+  __device__ __forceinline__ uint32_t tok_off(int r) const { return (uint32_t)min(r, toks) * (uint32_t)a.ldx; }
+  __device__ __forceinline__ const unsigned char* row_base(int) const { return row; }
+  __device__ __forceinline__ uint32_t row_off(int r) const { return (uint32_t)min(r, rows) * (uint32_t)a.K; }
+};
 
 template <int KIND, int MT, int NT, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_fp8_tiles(Fp8Args a) {
   using S = GemmShape<KIND, MT, NT, WM, WN>;
-  __shared__ __attribute__((aligned(1024))) unsigned char lds0[S::kBuffer], lds1[S::kBuffer];
-  __shared__ float scl0[S::kTok], scl1[S::kTok];
-  int tt, rt;
-  gemm_place(blockIdx.x, a.tok_tiles, a.row_tiles, tt, rt);
-  const int tok0 = tt * S::kTok, row0 = rt * S::kRows;
-  const int wave = threadIdx.x >> 6, wm = wave % WM, wn = wave / WM;
-  const int step0 = blockIdx.y * a.steps_per, step1 = min(a.G, step0 + a.steps_per);
-  gemm_f32x4 acc[MT][NT];
+  Fp8Source<S> source{a};
+  gemm_tiles_scaled<S>(a.tiles, a.K, source, [&](const GemmPlace& p, const gemm_f32x4 (&acc)[MT][NT]) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t0 = p.tok * S::kTok + wave % WM * MT * 16, n0 = p.row * S::kRows + wave / WM * NT * 16;
+    const int lane = gemm_opaque(threadIdx.x & 63), n16 = lane & 15, kb = lane >> 4;
+    const bool fp32 = a.part || a.out_dtype == MOE_Q4_DTYPE_F32;
+    float* to = a.part ? a.part + (size_t)p.split * a.L * a.N : static_cast<float*>(a.out);
+    const long long ld = a.part ? a.N : a.ldo;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      const int t = t0 + 16 * mt + n16;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = gemm_zero();
-  const int wrow = row0 + wn * NT * 16;
-  const unsigned char* wbase = a.w + (size_t)row0 * a.K;
-  gemm_tile<S>(
-      lds0, lds1, scl0, scl1, a.K, step0, step1, a.x + (size_t)tok0 * a.ldx,
-      [&](int r) { return (uint32_t)min(r, a.L - 1 - tok0) * (uint32_t)a.ldx; }, [&](int) { return wbase; },
-      [&](int r) { return (uint32_t)min(r, a.N - 1 - row0) * (uint32_t)a.K; },
-      a.sx + (size_t)min(tok0 + (int)threadIdx.x, a.L - 1) * a.G,
-      a.sw + (size_t)__builtin_amdgcn_readfirstlane(min(wrow, a.N - 1) / 128) * a.G, acc);
-  __syncthreads();  // the last step's operands have been read
-  constexpr int kWaves = WM * WN, kBytes = 2 * S::kBuffer / kWaves;
-  unsigned char* mine = wave < kWaves / 2 ? lds0 + wave * kBytes : lds1 + (wave - kWaves / 2) * kBytes;
-  gemm_out<MT, NT, kBytes>(reinterpret_cast<float*>(mine), [&](int mt, int nt) { return acc[mt][nt]; }, [&](int r, int c, float (&v)[8]) {
-    const int t = tok0 + wm * MT * 16 + r, n = wrow + c;
-    if (t < a.L && n < a.N) fp8_store(a, t, n, blockIdx.y, v);
+      for (int nt = 0; nt < NT; nt += 2) {
+        gemm_f32x4 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = n0 + 16 * (nt + h) + 4 * kb;
+          v[h] = gemm_here(acc[mt][nt + h]);
+          if (a.bias && !a.part) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[h][i] += a.bias[min(n + i, a.N - 1)];
+          }
+          if (fp32 && t < a.L) gemm_put32(to + t * ld + n, a.N - n, v[h]);
+        }
+        if (!fp32) {
+          const uint4 q = a.out_dtype == MOE_Q4_DTYPE_BF16 ? gemm_eight16(gemm_pack4<__bf16>(v[0]), gemm_pack4<__bf16>(v[1]))
+                                                           : gemm_eight16(gemm_pack4<_Float16>(v[0]), gemm_pack4<_Float16>(v[1]));
+          const int n = n0 + 16 * nt + 8 * kb;
+          if (t < a.L) gemm_put16(static_cast<uint16_t*>(a.out) + t * ld + n, a.N - n, q);
+        }
+      }
+    }
   });
 }
 
@@ -133,10 +144,10 @@ int fp8_status(int L, int N, int K) {
 }
 
 bool fp8_by_rows(int L) { return L <= 32; }
-GemmPlan fp8_plan(int L, int N, int K, bool wide) { return gemm_plan(L, N, (K + 127) / 128, wide ? 1 : 0); }
+GemmPlan fp8_plan(int L, int N, int K, bool wide) { return gemm_plan(L, N, (K + 127) / 128, wide ? 1 << kGemm128x128 | 1 << kGemm64x128 : ~(1 << kGemm256x192)); }
 size_t fp8_part(int L, int N, int K, bool wide) {
   const GemmPlan p = fp8_plan(L, N, K, wide);
-  return p.splits > 1 ? ((size_t)p.splits * L * N * 4 + 255) & ~size_t(255) : 0;
+  return p.tiles.splits > 1 ? ((size_t)p.tiles.splits * L * N * 4 + 255) & ~size_t(255) : 0;
 }
 
 }  // namespace
@@ -170,7 +181,7 @@ extern "C" int moe_linear_fp8_forward(const uint8_t* x, long long ldx, const flo
                          {sw, ((size_t)N + 127) / 128 * G * 4}, {bias, bias ? (size_t)N * 4 : 0}};
   const ArgSpan outs[] = {{out, args_span(L, ldo, N, os)}, {need ? workspace : nullptr, need}};
   if (args_alias(outs, ins)) return MOE_Q4_ERR_ALIAS;
-  Fp8Args a{x, sx, w, sw, bias, out, nullptr, ldx, ldo, L, N, K, G, out_dtype, 0, 0, 0};
+  Fp8Args a{x, sx, w, sw, bias, out, nullptr, ldx, ldo, L, N, K, G, out_dtype, {}};
   if (fp8_by_rows(L)) {
     const dim3 grid((N + 15) / 16);
     if (L <= 16)
@@ -180,11 +191,9 @@ extern "C" int moe_linear_fp8_forward(const uint8_t* x, long long ldx, const flo
     return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
   }
   const GemmPlan p = fp8_plan(L, N, K, out_dtype == MOE_Q4_DTYPE_F32);
-  a.tok_tiles = p.tok_tiles;
-  a.row_tiles = p.row_tiles;
-  a.steps_per = p.steps_per;
-  if (p.splits > 1) a.part = static_cast<float*>(workspace);
-  const dim3 grid((unsigned)(p.tok_tiles * p.row_tiles), p.splits);
+  a.tiles = p.tiles;
+  if (p.tiles.splits > 1) a.part = static_cast<float*>(workspace);
+  const dim3 grid(p.workgroups);
   if (out_dtype == MOE_Q4_DTYPE_F32) {
     if (p.shape == kGemm128x128)
       hipLaunchKernelGGL((k_fp8_tiles<kGemmFp8Wide, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a);
@@ -198,10 +207,10 @@ extern "C" int moe_linear_fp8_forward(const uint8_t* x, long long ldx, const flo
     }
   }
   if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
-  if (p.splits > 1) {
+  if (p.tiles.splits > 1) {
     const size_t all = (size_t)L * N;
     hipLaunchKernelGGL(k_fp8_join, dim3((unsigned)std::min<size_t>((all + 255) / 256, 4096)), dim3(256), 0, stream, a.part,
-                       bias, out, ldo, L, N, p.splits, out_dtype);
+                       bias, out, ldo, L, N, p.tiles.splits, out_dtype);
   }
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }

@@ -2,8 +2,8 @@
 // with their rows along k: 16-bit numbers, or E4M3 codes with a scale per
 // 128.  A step is 128 bytes of every row (64 or 128 elements).  Internal header.
 //
-//   gemm_tile   many tokens: A's and B's steps are copied into LDS
-//   gemm_rows   few tokens: B is read once, straight into the operands
+//   gemm_tiles, gemm_tiles_scaled   many tokens: steps are copied into LDS
+//   gemm_rows                       few tokens: B straight into the operands
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -26,6 +26,7 @@ constexpr int kGemmStep = 128;  // bytes
 typedef __bf16 gemm_bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 gemm_f16x8 __attribute__((ext_vector_type(8)));
 typedef float gemm_f32x4 __attribute__((ext_vector_type(4)));
+typedef float gemm_f32x16 __attribute__((ext_vector_type(16)));
 typedef int gemm_i32x4 __attribute__((ext_vector_type(4)));
 typedef int gemm_i32x8 __attribute__((ext_vector_type(8)));
 
@@ -43,23 +44,29 @@ __device__ __forceinline__ gemm_bf16x8 gemm_e4m3_bf16(int lo, int hi) {
   return gemm_bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// acc (+)= a b over a step, a's rows along the result's rows (4 kb + i), b's
-// along its columns (lane % 16).  E4M3: the step's sum times f.
+// A step's sums of E4M3 codes, a's rows along the result's rows (4 kb + i),
+// b's along its columns (lane % 16).
 template <int KIND>
-__device__ __forceinline__ void gemm_mfma(const GemmFrag& a, const GemmFrag& b, float f, gemm_f32x4& acc) {
+__device__ __forceinline__ gemm_f32x4 gemm_product(const GemmFrag& a, const GemmFrag& b) {
+  gemm_f32x4 s = {0, 0, 0, 0};
   if constexpr (KIND == kGemmFp8) {
     const gemm_i32x8 x = {a.v[0][0], a.v[0][1], a.v[0][2], a.v[0][3], a.v[1][0], a.v[1][1], a.v[1][2], a.v[1][3]};
     const gemm_i32x8 y = {b.v[0][0], b.v[0][1], b.v[0][2], b.v[0][3], b.v[1][0], b.v[1][1], b.v[1][2], b.v[1][3]};
-    const gemm_f32x4 zero = {0, 0, 0, 0};
-    const gemm_f32x4 s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, zero, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(s[i], f, acc[i]);
-  } else if constexpr (KIND == kGemmFp8Wide) {
-    gemm_f32x4 s = {0, 0, 0, 0};
+    s = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, s, 0, 0, 0, 0, 0, 0);
+  } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(gemm_e4m3_bf16(a.v[j >> 1][2 * (j & 1)], a.v[j >> 1][2 * (j & 1) + 1]),
                                                   gemm_e4m3_bf16(b.v[j >> 1][2 * (j & 1)], b.v[j >> 1][2 * (j & 1) + 1]), s, 0, 0, 0);
+  }
+  return s;
+}
+
+// acc += a b over a step; E4M3: the step's sums times f.
+template <int KIND>
+__device__ __forceinline__ void gemm_step(const GemmFrag& a, const GemmFrag& b, float f, gemm_f32x4& acc) {
+  if constexpr (gemm_scaled(KIND)) {
+    const gemm_f32x4 s = gemm_product<KIND>(a, b);
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(s[i], f, acc[i]);
   } else {
@@ -75,152 +82,398 @@ __device__ __forceinline__ void gemm_mfma(const GemmFrag& a, const GemmFrag& b, 
   }
 }
 
-// Zeros that the compiler does not know: as constants it would carry them
-// through a loop in registers of their own.
-__device__ __forceinline__ gemm_f32x4 gemm_zero() {
-  gemm_f32x4 z = {0, 0, 0, 0};
-  asm volatile("" : "+v"(z));
-  return z;
-}
-
 // ---- many tokens ----
 
-// MT x NT tiles of 16 x 16 a wave, WM x WN waves: 16 MT WM tokens x 16 NT WN rows of B.
+// MT x NT tiles a wave, of 32 x 32 results (16-bit types) or 16 x 16 (E4M3),
+// and WM x WN waves: kTok tokens x kRows rows of B.
 template <int KIND_, int MT_, int NT_, int WM_, int WN_>
 struct GemmShape {
-  static constexpr int KIND = KIND_, MT = MT_, NT = NT_, WM = WM_, WN = WN_;
-  static constexpr int kThreads = 64 * WM * WN, kTok = 16 * MT * WM, kRows = 16 * NT * WN;
-  static constexpr int kBuffer = (kTok + kRows) * kGemmStep;
+  static constexpr int KIND = KIND_, MT = MT_, NT = NT_, WM = WM_, WN = WN_, kTile = gemm_scaled(KIND) ? 16 : 32;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves, kTok = kTile * MT * WM, kRows = kTile * NT * WN;
+  static constexpr int kScaleRows = (kRows + 127) / 128;
 };
 
-// Tile of a workgroup.  Workgroups b, b + 8, ... share an XCD (and its L2):
-// each XCD takes a contiguous run, which goes through 8 token tiles at a time,
-// so the 32 tiles it works on together read 8 + 4 tiles of the operands.
-__device__ __forceinline__ void gemm_place(int block, int tok_tiles, int row_tiles, int& tok, int& row) {
-  const int tiles = tok_tiles * row_tiles;
-  const int per = tiles / 8, rest = tiles % 8, xcd = block & 7, at = block >> 3;
-  const int id = xcd * per + min(xcd, rest) + at;
-  const int group = id / (8 * row_tiles), in = id % (8 * row_tiles), first = group * 8;
-  const int size = min(tok_tiles - first, 8);
-  tok = first + in % size;
-  row = in / size;
+// The tiles of a launch: tok_tiles x row_tiles of them, each in `splits` parts
+// of steps_per steps.  A workgroup takes one after another.  Workgroups b, b +
+// 8, ... share an XCD (and its L2): each XCD takes a contiguous run, which goes
+// through 8 token tiles at a time, so the 32 tiles that it works on together
+// read 8 + 4 tiles of the operands.
+struct GemmTiles {
+  int tok_tiles, row_tiles, splits, steps_per, steps;
+};
+struct GemmPlace {
+  int tok, row, split, step0, count;
+};
+struct GemmQueue {
+  int next, end, stride;
+  __device__ __forceinline__ explicit GemmQueue(const GemmTiles& t) {
+    const int all = t.tok_tiles * t.row_tiles * t.splits, per = all / 8, rest = all % 8, xcd = blockIdx.x & 7;
+    const int first = xcd * per + min(xcd, rest);
+    next = first + (int)(blockIdx.x >> 3);
+    end = first + per + (xcd < rest ? 1 : 0);
+    stride = ((int)gridDim.x - xcd + 7) / 8;
+  }
+  __device__ __forceinline__ bool any() const { return next < end; }
+  __device__ __forceinline__ GemmPlace take(const GemmTiles& t) {
+    const int tiles = t.tok_tiles * t.row_tiles;
+    const int id = next % tiles, split = next / tiles;
+    next += stride;
+    const int group = id / (8 * t.row_tiles), in = id % (8 * t.row_tiles), first = group * 8, size = min(t.tok_tiles - first, 8);
+    GemmPlace p;
+    p.tok = first + in % size;
+    p.row = in / size;
+    p.split = split;
+    p.step0 = split * t.steps_per;
+    p.count = min(t.steps - p.step0, t.steps_per);
+    return p;
+  }
+};
+
+// This wave's LDS reads and all but its last LEFT copies are done, and so are
+// the other waves'.
+template <int LEFT>
+__device__ __forceinline__ void gemm_meet() {
+  static_assert(LEFT < 64, "six bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((LEFT & 15) | (LEFT >> 4) << 14 | 0x70);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
-// Steps step0 .. step1 of a tile into acc.  Row r of the tile begins at
-// tok_base + tok_off(r) in A, row_base(r) + row_off(r) in B (some row within
-// the operand for those past its end); offsets have 32 bits.  kbytes, a
-// multiple of 16, is a row's length.  E4M3: sx_row is the scales of this
-// thread's token tid of the tile, sw those of the wave's rows.
+// A value that the compiler does not know to be the same for every tile: what
+// depends on it would be worked out ahead of the tiles, and held through their
+// loops.
+__device__ __forceinline__ int gemm_opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// 16 bytes a lane from memory into 1 KB of LDS, without passing registers.
+__device__ __forceinline__ void gemm_copy(const unsigned char* from, unsigned char* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
+// Where a tile's rows lie: row r of its tokens at tok + tok_off(r), of B at
+// row_base(r) + row_off(r), rows past the operand's end at some row within;
+// offsets have 32 bits.  scales (E4M3): this thread's row of scales, one a
+// step: thread tid < kTok has the tile's token tid's, the next kScaleRows
+// threads have those of each 128 of B's rows.
+
+// Products of 16-bit numbers: runs the workgroup's tiles, source.set(place)
+// before each and store(place, acc) behind it.  kbytes, a multiple of 16, is a
+// row's length.
 //
-// LDS holds a step of all rows, 128 bytes each, copied without passing
-// registers; chunk c of row r lies at place c ^ (r % 8), so that the 8 rows
-// that are read together fall in different banks.
-template <class S, class TokOff, class RowBase, class RowOff>
-__device__ __forceinline__ void gemm_tile(unsigned char* lds0, unsigned char* lds1, float* scl0, float* scl1, int kbytes,
-                                          int step0, int step1, const unsigned char* tok_base, TokOff tok_off,
-                                          RowBase row_base, RowOff row_off, const float* sx_row, const float* sw,
-                                          gemm_f32x4 (&acc)[S::MT][S::NT]) {
-  constexpr int MT = S::MT, NT = S::NT, KIND = S::KIND;
-  constexpr int kPass = S::kThreads / 8, kTokCopies = S::kTok / kPass, kCopies = (S::kTok + S::kRows) / kPass;
-  static_assert(S::kTok % kPass == 0 && S::kRows % kPass == 0 && S::kTok <= S::kThreads, "copies of whole passes");
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// LDS holds two steps of all rows, 128 bytes each.  Chunk c of row r lies at
+// place c ^ (r / 2 % 8), so that the 16 rows that are read together fall in
+// different banks (of 64).  A wave's 32 x 32 x 16 instructions go through half
+// a step (its chunks 0 to 3 or 4 to 7) at a time, while the next half's
+// operands are on their way into registers; so the waves have read a step when
+// its second half begins, meet there, once a step, and that half carries the
+// copies of the step after the next into the LDS that became free.  Four waves
+// of 128 x 128 results each: their sums fill the accumulator registers, and
+// they read two thirds of what eight of 128 x 64 would.  (16 x 16 x 32
+// instructions read twice the registers, and behind each one's 16 clocks a
+// copy's issue, about 30, shows.)
+template <class S, class Source, class Store>
+__device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, Source& source, Store store) {
+  constexpr int MT = S::MT, NT = S::NT, KIND = S::KIND, kPass = S::kThreads / 8;
+  constexpr int kCb = S::kRows / kPass, kCt = S::kTok / kPass, kCopies = kCb + kCt;
+  constexpr int kReads = 2 * (MT + NT), kMul = 2 * MT * NT;           // of half a step
+  constexpr int kLeast = kReads > kCopies ? kReads : kCopies, kPer = kMul > kLeast ? kMul / kLeast : 1;
+  constexpr int kSlots = (kMul + kPer - 1) / kPer > kLeast ? (kMul + kPer - 1) / kPer : kLeast;
+  static_assert(S::kRows % kPass == 0 && S::kTok % kPass == 0 && kPass % 16 == 0, "copies of whole passes");
+  // each an object of its own: the compiler then knows that reads of one do not wait for copies into another
+  __shared__ __attribute__((aligned(1024))) unsigned char b0[S::kRows * kGemmStep], b1[S::kRows * kGemmStep];
+  __shared__ __attribute__((aligned(1024))) unsigned char t0[S::kTok * kGemmStep], t1[S::kTok * kGemmStep];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n32 = lane & 31, kh = lane >> 5;
+  const int wm = wave % S::WM, wn = wave / S::WM;
+  const int chunk = ((tid & 7) ^ ((tid >> 4) & 7)) * 16;
+  const int tok_at = (wm * MT * 32 + n32) * kGemmStep + ((kh ^ ((n32 >> 1) & 7)) << 4);
+  const int row_at = (wn * NT * 32 + n32) * kGemmStep + ((kh ^ ((n32 >> 1) & 7)) << 4);
+
+  GemmQueue queue(tiles);
+  GemmPlace at, now;
+  uint32_t off[kCopies], k = 0, live = 0;
+  auto place = [&](int i) __attribute__((always_inline)) {
+    k = min((at.step0 + i) * kGemmStep + chunk, kbytes - 16);  // (past the end: never used)
+    live = i < at.count ? ~0u : 0u;                            // past the last step: all of one place
+  };
+  auto copy = [&](int to, int c) __attribute__((always_inline)) {
+    unsigned char* lds = (c < kCb ? (to ? b1 : b0) + c * kPass * kGemmStep : (to ? t1 : t0) + (c - kCb) * kPass * kGemmStep) + wave * 1024;
+    gemm_copy((c < kCb ? source.row_base(c * kPass + tid / 8) : source.tok) + ((off[c] + k) & live), lds);
+  };
+  auto start = [&]() __attribute__((always_inline)) {  // the next tile and its first two steps
+    at = queue.take(tiles);
+    source.set(at);
+    const int mine = gemm_opaque(tid / 8);
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) off[c] = c < kCb ? source.row_off(c * kPass + mine) : source.tok_off((c - kCb) * kPass + mine);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      place(i);
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) copy(i, c);
+    }
+  };
+  // operands of half h, of its instructions' k from 16 s on: chunk 4 h + 2 s + kh of a row
+  gemm_i32x4 w[2][2][NT], x[2][2][MT];
+  gemm_f32x16 acc[MT][NT];
+  auto read = [&](int from, int h, int j) __attribute__((always_inline)) {
+    const int s = j / (MT + NT), r = j % (MT + NT), flip = 64 * h + 32 * s;
+    if (r < NT)
+      w[h][s][r] = *reinterpret_cast<const gemm_i32x4*>((from ? b1 : b0) + (row_at ^ flip) + r * 32 * kGemmStep);
+    else
+      x[h][s][r - NT] = *reinterpret_cast<const gemm_i32x4*>((from ? t1 : t0) + (tok_at ^ flip) + (r - NT) * 32 * kGemmStep);
+  };
+  auto multiply = [&](int h, int j) __attribute__((always_inline)) {
+    const int s = j / (MT * NT), mt = j % (MT * NT) / NT, nt = j % NT;
+    if constexpr (KIND == kGemmBf16)
+      acc[mt][nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(gemm_bf16x8, w[h][s][nt]),
+                                                            __builtin_bit_cast(gemm_bf16x8, x[h][s][mt]), acc[mt][nt], 0, 0, 0);
+    else
+      acc[mt][nt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(gemm_f16x8, w[h][s][nt]),
+                                                           __builtin_bit_cast(gemm_f16x8, x[h][s][mt]), acc[mt][nt], 0, 0, 0);
+  };
+  // half a step, reading the next one, of buffer `from`; the copies into `to` with it (-1: none)
+  auto pass = [&](int h, int from, int to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) {
+      if (q < kReads) read(from, h ^ 1, q);
+      if (to >= 0 && q < kCopies) copy(to, q);
+#pragma unroll
+      for (int j = q * kPer; j < (q + 1) * kPer && j < kMul; ++j) multiply(h, j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto cut = [&](int h, int i) __attribute__((always_inline)) {  // past the rows' end: one operand's zeros
+    const int left = kbytes - (now.step0 + i) * kGemmStep - h * 64;
+    if (left < 64) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          if (kh * 16 + s * 32 >= left) w[h][s][nt] = gemm_i32x4{0, 0, 0, 0};
+    }
+  };
+
+  if (!queue.any()) return;
+  start();
+  while (true) {
+    now = at;
+    gemm_meet<0>();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[mt][nt][e] = 0.0f;
+        asm volatile("" : "+a"(acc[mt][nt]));  // hides the zeros, which the compiler would carry along in registers of their own
+      }
+#pragma unroll
+    for (int j = 0; j < kReads; ++j) read(0, 0, j);
+    cut(0, 0);
+    pass(0, 0, -1);
+    cut(1, 0);
+    gemm_meet<0>();
+    int i = 0;
+    auto body = [&](int buf) __attribute__((always_inline)) {
+      place(i + 2);
+      pass(1, buf ^ 1, buf);
+      ++i;
+      cut(0, i);
+      pass(0, buf ^ 1, -1);
+      cut(1, i);
+      gemm_meet<0>();
+    };
+    while (i + 1 < now.count) {
+      body(0);
+      if (i + 1 >= now.count) break;
+      body(1);
+    }
+    // the last half step, from registers; the LDS is the next tile's
+    const bool more = queue.any();
+    if (more) start();
+#pragma unroll
+    for (int j = 0; j < kMul; ++j) multiply(1, j);
+    store(now, acc);
+    if (!more) break;
+  }
+}
+
+// Products of E4M3 codes with a scale per step, 8 waves of 128 x 64 results
+// (or 4 of fewer).  A step's sums come out of one instruction (or four of
+// kGemmFp8Wide) into registers of their own and enter the accumulators by a
+// multiply-add each, two instructions behind, so that these never wait; the
+// accumulators have to lie among the vector registers for that.
+//
+// LDS holds two steps as above.  A wave reads a token tile two groups of
+// matrix instructions ahead, the next step's too, and its rows of B within a
+// step's last group, each behind its last use.  The waves meet twice a step:
+// once when all have read B and the first half of their token tiles, whose LDS
+// then takes the copies of the step after the next, and once when all have
+// read the second half.  So copies have more than a step's time, and nobody
+// waits for the last ones.  Steps go in pairs, for an odd number of them with
+// one of zeros, since the compiler must see what is on its way at each read:
+// where a loop ends in two places it waits for everything.
+template <class S, class Source, class Store>
+__device__ __forceinline__ void gemm_tiles_scaled(const GemmTiles& tiles, int kbytes, Source& source, Store store) {
+  constexpr int MT = S::MT, NT = S::NT, KIND = S::KIND, kPass = S::kThreads / 8;
+  constexpr int kCb = S::kRows / kPass, kCh = S::kTok / 2 / kPass;  // copies of B, of half the tokens
+  constexpr int kHalf = S::kTok / 2 * kGemmStep;
+  static_assert(S::kRows % kPass == 0 && S::kTok / 2 % kPass == 0 && S::kTok + S::kScaleRows <= S::kThreads, "copies of whole passes");
+  static_assert(MT % 4 == 0, "a ring of four token tiles");
+  __shared__ __attribute__((aligned(1024))) unsigned char b0[S::kRows * kGemmStep], b1[S::kRows * kGemmStep];
+  __shared__ __attribute__((aligned(1024))) unsigned char lo0[kHalf], lo1[kHalf], hi0[kHalf], hi1[kHalf];
+  __shared__ float scale0[S::kTok + 64], scale1[S::kTok + 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n16 = lane & 15, kb = lane >> 4;
   const int wm = wave % S::WM, wn = wave / S::WM;
+  const int chunk = ((tid & 7) ^ ((tid >> 4) & 7)) * 16;
+  const int tok_at = (wm * MT * 8 + n16) * kGemmStep + ((kb ^ (n16 >> 1)) << 4);
+  const int row_at = (wn * NT * 16 + n16) * kGemmStep + ((kb ^ (n16 >> 1)) << 4);
 
-  uint32_t off[kCopies];
-#pragma unroll
-  for (int c = 0; c < kCopies; ++c) {
-    const int r = c * kPass + tid / 8;
-    off[c] = c < kTokCopies ? tok_off(r) : row_off(r - S::kTok);
-  }
-  const int chunk = ((tid & 7) ^ ((tid >> 3) & 7)) * 16;
-  auto stage = [&](int step, unsigned char* buf) __attribute__((always_inline)) {
-    const uint32_t k = min(step * kGemmStep + chunk, kbytes - 16);  // (past the end: never used)
-#pragma unroll
-    for (int c = 0; c < kCopies; ++c) {
-      const unsigned char* base = c < kTokCopies ? tok_base : row_base(c * kPass + tid / 8 - S::kTok);
-      // a wave's 64 chunks go to 1 KB of LDS from its first place on
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + (off[c] + k)),
-                                       (__attribute__((address_space(3))) void*)(buf + (c * S::kThreads + wave * 64) * 16), 16, 0, 0);
-    }
+  GemmQueue queue(tiles);
+  GemmPlace at;
+  uint32_t off_b[kCb], off_t[2][kCh], k = 0, live = 0;
+  auto place = [&](int i) __attribute__((always_inline)) {
+    k = min((at.step0 + i) * kGemmStep + chunk, kbytes - 16);  // (past the end: never used, or times zeros)
+    live = i <= at.count ? ~0u : 0u;
   };
-  const int tok_at = (wm * MT * 16 + n16) * kGemmStep + ((kb ^ (n16 & 7)) << 4);
-  const int row_at = (S::kTok + wn * NT * 16 + n16) * kGemmStep + ((kb ^ (n16 & 7)) << 4);
-  auto read = [&](const unsigned char* buf, int at, int more) __attribute__((always_inline)) {
+  auto copy_lo = [&](int to, int c) __attribute__((always_inline)) {
+    if (c < kCb)
+      gemm_copy(source.row_base(c * kPass + tid / 8) + ((off_b[c] + k) & live), (to ? b1 : b0) + c * kPass * kGemmStep + wave * 1024);
+    else
+      gemm_copy(source.tok + ((off_t[0][c - kCb] + k) & live), (to ? lo1 : lo0) + (c - kCb) * kPass * kGemmStep + wave * 1024);
+  };
+  auto copy_scales = [&](int i, int to) __attribute__((always_inline)) {
+    if (tid < S::kTok + S::kScaleRows)
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(source.scales + at.step0 + min(i, at.count - 1)),
+                                       (__attribute__((address_space(3))) void*)((to ? scale1 : scale0) + wave * 64), 4, 0, 0);
+  };
+  auto copy_hi = [&](int to, int c) __attribute__((always_inline)) {
+    gemm_copy(source.tok + ((off_t[1][c] + k) & live), (to ? hi1 : hi0) + c * kPass * kGemmStep + wave * 1024);
+  };
+  auto copy_all = [&](int i) __attribute__((always_inline)) {
+    place(i);
+#pragma unroll
+    for (int c = 0; c < kCb + kCh; ++c) copy_lo(i, c);
+    copy_scales(i, i);
+#pragma unroll
+    for (int c = 0; c < kCh; ++c) copy_hi(i, c);
+  };
+  GemmFrag x[4], w[NT];
+  float f[4], w_scale = 0.0f, w_next = 0.0f;
+  gemm_f32x4 acc[MT][NT], sum[4];
+  auto read = [&](const unsigned char* lds, int at, int more) __attribute__((always_inline)) {
     GemmFrag r;  // (chunk kb + 4 lies at the place with bit 2 flipped)
-    r.v[0] = *reinterpret_cast<const gemm_i32x4*>(buf + at + more);
-    r.v[1] = *reinterpret_cast<const gemm_i32x4*>(buf + (at ^ 64) + more);
+    r.v[0] = *reinterpret_cast<const gemm_i32x4*>(lds + at + more);
+    r.v[1] = *reinterpret_cast<const gemm_i32x4*>(lds + (at ^ 64) + more);
     return r;
   };
-  auto compute = [&](const unsigned char* buf, const float* scl, float wscale, int left) __attribute__((always_inline)) {
-    GemmFrag w[NT];
+  auto read_x = [&](int from, int mt) __attribute__((always_inline)) {
+    const unsigned char* half = mt < MT / 2 ? (from ? lo1 : lo0) : (from ? hi1 : hi0);
+    x[mt % 4] = read(half, tok_at, mt % (MT / 2) * 16 * kGemmStep);
+    if (mt == 0) w_next = (from ? scale1 : scale0)[S::kTok + wn * NT * 16 / 128];
+    f[mt % 4] = (from ? scale1 : scale0)[(wm * MT + mt) * 16 + n16];
+  };
+  auto read_w = [&](int from, int nt) __attribute__((always_inline)) { w[nt] = read(from ? b1 : b0, row_at, nt * 16 * kGemmStep); };
+  auto cut = [&](int i) __attribute__((always_inline)) {  // past the rows' end, or the last step: one operand's zeros
+    const int left = i < at.count ? kbytes - (at.step0 + i) * kGemmStep : 0;
+    if (left < kGemmStep) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      w[nt] = read(buf, row_at, nt * 16 * kGemmStep);
-      if (left < kGemmStep) {  // past the rows' end: one operand's zeros
-        if (kb * 16 >= left) w[nt].v[0] = gemm_i32x4{0, 0, 0, 0};
-        if (kb * 16 + 64 >= left) w[nt].v[1] = gemm_i32x4{0, 0, 0, 0};
-      }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (kb * 16 + 64 * j >= left) w[nt].v[j] = gemm_i32x4{0, 0, 0, 0};
     }
-    GemmFrag x = read(buf, tok_at, 0);
-    float f = 0.0f;
-    if constexpr (gemm_scaled(KIND)) f = scl[wm * MT * 16 + n16] * wscale;
+  };
+  auto body = [&](int buf, int i) __attribute__((always_inline)) {
+    constexpr int kLo = kCb + kCh, kLoPer = (kLo + MT / 2 - 1) / (MT / 2), kHiPer = (kCh + 1) / 2;
+    float fs[4];  // the factors of the sums that are still to be added
+    w_scale = w_next;
+    auto add = [&](int j) __attribute__((always_inline)) {
+      gemm_f32x4& a = acc[j / NT][j % NT];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] = __builtin_fmaf(sum[j % 4][e], fs[j % 4], a[e]);
+      asm volatile("" : "+v"(a));  // stays here: sunk below, each sum would hold registers of its own
+    };
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      GemmFrag xn;
-      float fn = 0.0f;
-      if (mt + 1 < MT) {
-        xn = read(buf, tok_at, (mt + 1) * 16 * kGemmStep);
-        if constexpr (gemm_scaled(KIND)) fn = scl[(wm * MT + mt + 1) * 16 + n16] * wscale;
+      if (mt == MT / 2 - 2) {  // B and the first half have been read; the second half is there
+        gemm_meet<kCb + 2 * kCh>();
+        place(i + 2);
+      }
+      if (mt + 2 < MT) read_x(buf, mt + 2);
+      if (mt == MT - 2) {  // the second half has been read; the next step's B and first half are there
+        gemm_meet<kCb + 2 * kCh>();
+        copy_scales(i + 2, buf);
+      }
+      if (mt == MT - 1) {
+        read_x(buf ^ 1, 0);
+        read_x(buf ^ 1, 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // reads first: they are a group's time ahead of their use
+      if (mt >= MT / 2 - 2 && mt < MT - 2) {
+#pragma unroll
+        for (int c = (mt - (MT / 2 - 2)) * kLoPer; c < (mt - (MT / 2 - 2) + 1) * kLoPer && c < kLo; ++c) copy_lo(buf, c);
+      }
+      if (mt >= MT - 2) {
+#pragma unroll
+        for (int c = (mt - (MT - 2)) * kHiPer; c < (mt - (MT - 2) + 1) * kHiPer && c < kCh; ++c) copy_hi(buf, c);
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) gemm_mfma<KIND>(w[nt], x, f, acc[mt][nt]);
-      if constexpr (gemm_scaled(KIND)) {  // the sums stay here: sunk below, each would hold registers of its own
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) asm volatile("" : "+v"(acc[mt][nt]));
+      for (int nt = 0; nt < NT; ++nt) {
+        const int j = mt * NT + nt;
+        sum[j % 4] = gemm_product<KIND>(w[nt], x[mt % 4]);
+        fs[j % 4] = f[mt % 4] * w_scale;
+        if (mt == MT - 1) read_w(buf ^ 1, nt);
+        if (j >= 2) add(j - 2);
       }
-      x = xn;
-      f = fn;
+      __builtin_amdgcn_sched_barrier(0);
     }
+    add(MT * NT - 2);
+    add(MT * NT - 1);
+    cut(i + 1);
   };
 
-  const int count = step1 - step0;
-  if (count <= 0) return;
-  const int left = kbytes - (step1 - 1) * kGemmStep;   // bytes of the last step
-  const int full = left < kGemmStep ? count - 1 : count;
-  stage(step0, lds0);
-  float wscale = 0.0f, wnext = 0.0f;
-  if constexpr (gemm_scaled(KIND)) {
-    wscale = sw[step0];
-    if (tid < S::kTok) scl0[tid] = sx_row[step0];
-  }
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  int i = 0;
-  auto body = [&](unsigned char* buf, unsigned char* other, float* scl, float* scl_other) __attribute__((always_inline)) {
-    float s = 0.0f;
-    if (i + 1 < count) {
-      stage(step0 + i + 1, other);
-      if constexpr (gemm_scaled(KIND)) {
-        wnext = sw[step0 + i + 1];
-        if (tid < S::kTok) s = sx_row[step0 + i + 1];
+  while (queue.any()) {
+    at = queue.take(tiles);
+    source.set(at);
+#pragma unroll
+    for (int c = 0; c < kCb; ++c) off_b[c] = source.row_off(c * kPass + tid / 8);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < kCh; ++c) {
+        const int r = c * kPass + tid / 8;
+        off_t[h][c] = source.tok_off(r / (8 * MT) * (16 * MT) + h * (8 * MT) + r % (8 * MT));
       }
-    }
-    compute(buf, scl, wscale, kGemmStep);
-    __builtin_amdgcn_s_waitcnt(0);
-    if constexpr (gemm_scaled(KIND)) {
-      if (tid < S::kTok) scl_other[tid] = s;
-      wscale = wnext;
-    }
-    __syncthreads();
-    ++i;
-  };
-  while (i < full) {
-    body(lds0, lds1, scl0, scl1);
-    if (i >= full) break;
-    body(lds1, lds0, scl1, scl0);
+    copy_all(0);
+    gemm_meet<0>();
+    copy_all(1);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        acc[mt][nt] = gemm_f32x4{0, 0, 0, 0};
+        asm volatile("" : "+v"(acc[mt][nt]));  // hides the zeros, which the compiler would carry along in registers of their own
+      }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) read_w(0, nt);
+    cut(0);
+    read_x(0, 0);
+    read_x(0, 1);
+    int i = 0;
+    do {
+      body(0, i);
+      body(1, i + 1);
+      i += 2;
+    } while (i < at.count);
+    gemm_meet<0>();  // no copy is on its way, and no read, when the next tile's begin
+    store(at, acc);
   }
-  if (full < count) compute(full & 1 ? lds1 : lds0, full & 1 ? scl1 : scl0, wscale, left);
 }
 
 // ---- few tokens ----
@@ -259,7 +512,7 @@ __device__ __forceinline__ void gemm_rows(const unsigned char* row, const unsign
       for (int j = 0; j < 2; ++j)
         if ((kb + 4 * j) * 16 >= left) w[u].v[j] = gemm_i32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) gemm_mfma<KIND>(w[u], x[u][mt], f[u][mt], acc[mt]);
+      for (int mt = 0; mt < MT; ++mt) gemm_step<KIND>(w[u], x[u][mt], f[u][mt], acc[mt]);
     }
   }
 }
@@ -283,39 +536,63 @@ __device__ __forceinline__ gemm_f32x4 gemm_join_waves(gemm_f32x4 (&lds)[WAVES][M
 
 // ---- results ----
 
-// Hands a wave's tile, rows of 16 NT results with get(mt, nt) the lanes' parts,
-// to store(t, n, v) by 8 neighbours v at token t and column n: through `bytes` of
-// LDS that the wave has to itself, so that rows are written in whole lines.
-// (Chunks of 4 results are XORed with the token against bank conflicts.)
-template <int MT, int NT, int BYTES, class Get, class Store>
-__device__ __forceinline__ void gemm_out(float* lds, Get get, Store store) {
-  constexpr int kCols = 16 * NT, kFit = BYTES / (16 * kCols * 4), kRound = kFit < MT ? kFit : MT;
-  constexpr int kLanes = kCols / 8, kRows = 64 / kLanes, kMask = 4 * NT - 1;
-  static_assert(kRound >= 1 && MT % kRound == 0 && (NT & (NT - 1)) == 0, "whole rounds");
-  const int lane = threadIdx.x & 63, n16 = lane & 15, kb = lane >> 4;
+// A lane's sums go straight to memory, four neighbours of a token's results at
+// a time: of a 16 x 16 tile those from 4 (lane / 16) on of token lane % 16, of
+// a 32 x 32 tile those from 8 g + 4 (lane / 32) on of token lane % 32, g = 0 to
+// 3.
+
+// Results in vector registers from here on, and no sooner: of all tiles at
+// once they would not fit beside the accumulator registers.
+__device__ __forceinline__ gemm_f32x4 gemm_here(gemm_f32x4 v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ gemm_f32x4 gemm_four(const gemm_f32x16& v, int g) {
+  return gemm_here(gemm_f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]});
+}
+
+template <class T>
+__device__ __forceinline__ uint2 gemm_pack4(gemm_f32x4 v) {
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(uint2, t4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]});
+}
+
+// Two fours as 16-bit numbers, made eight neighbours of a lane, so that lanes
+// write 16 bytes.  Of 32 x 32 tiles: a's and b's halves, (a0 a1) and (b0 b1),
+// swapped to (a0 b0) and (a1 b1): the lower lanes have a, the upper ones b.
+__device__ __forceinline__ uint4 gemm_eight32(uint2 a, uint2 b) {
+  const auto x = __builtin_amdgcn_permlane32_swap(a.x, b.x, false, false), y = __builtin_amdgcn_permlane32_swap(a.y, b.y, false, false);
+  return make_uint4(x[0], y[0], x[1], y[1]);
+}
+// Of 16 x 16 tiles side by side: rows of 16 lanes (a0 a1 a2 a3) and (b0 b1 b2
+// b3) swapped to (a0 a2 b0 b2) and (a1 a3 b1 b3): eight from 8 (lane / 16) on.
+__device__ __forceinline__ uint4 gemm_eight16(uint2 a, uint2 b) {
+  const auto x = __builtin_amdgcn_permlane32_swap(a.x, b.x, false, false), y = __builtin_amdgcn_permlane32_swap(a.y, b.y, false, false);
+  const auto u = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false), v = __builtin_amdgcn_permlane16_swap(y[0], y[1], false, false);
+  return make_uint4(u[0], v[0], u[1], v[1]);
+}
+
+// The first `left` of eight 16-bit neighbours, or of four fp32, at any element's place.
+__device__ __forceinline__ void gemm_put16(void* p, int left, uint4 v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  typedef u32x4 u32x4_any __attribute__((aligned(2)));
+  if (left >= 8) {
+    *reinterpret_cast<u32x4_any*>(p) = u32x4{v.x, v.y, v.z, v.w};
+  } else {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int m0 = 0; m0 < MT; m0 += kRound) {
+    for (int i = 0; i < 7; ++i)
+      if (i < left) static_cast<uint16_t*>(p)[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
+  }
+}
+__device__ __forceinline__ void gemm_put32(float* p, int left, gemm_f32x4 v) {
+  typedef gemm_f32x4 f32x4_any __attribute__((aligned(4)));
+  if (left >= 4) {
+    *reinterpret_cast<f32x4_any*>(p) = v;
+  } else {
 #pragma unroll
-    for (int m = 0; m < kRound; ++m)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<gemm_f32x4*>(lds + (m * 16 + n16) * kCols + (((4 * nt + kb) ^ (n16 & kMask)) << 2)) = get(m0 + m, nt);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll 2
-    for (int r = lane / kLanes; r < 16 * kRound; r += kRows) {
-      const int c = 2 * (lane % kLanes);
-      float v[8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const gemm_f32x4 q = *reinterpret_cast<const gemm_f32x4*>(lds + r * kCols + (((c + h) ^ (r & 15 & kMask)) << 2));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 * h + i] = q[i];
-      }
-      store(m0 * 16 + r, 4 * c, v);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    for (int i = 0; i < 3; ++i)
+      if (i < left) p[i] = v[i];
   }
 }
 

@@ -43,13 +43,13 @@ int glu_status(int T, int H, int I) {
 
 bool glu_by_rows(int T) { return T <= 32; }
 int glu_steps(long k) { return (int)((2 * k + kGemmStep - 1) / kGemmStep); }
-GemmPlan glu_forward_plan(int T, int H, int I) { return gemm_plan(T, 2 * I, glu_steps(H)); }
+GemmPlan glu_forward_plan(int T, int H, int I) { return gemm_plan(T, 2 * I, glu_steps(H), ~0); }
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
 size_t glu_forward_part(int T, int H, int I) {
   if (glu_by_rows(T)) return 0;
   const GemmPlan p = glu_forward_plan(T, H, I);
-  return p.splits > 1 ? round256((size_t)p.splits * 2 * T * I * 4) : 0;
+  return p.tiles.splits > 1 ? round256((size_t)p.tiles.splits * 2 * T * I * 4) : 0;
 }
 
 struct GluBackLayout {
@@ -60,8 +60,8 @@ struct GluBackLayout {
 GluBackLayout glu_back_layout(int T, int H, int I, bool saved) {
   GluBackLayout w{};
   w.Tp = (T + 63) / 64 * 64;
-  w.dx = gemm_plan(T, H, glu_steps(2L * I));
-  w.dw = gemm_plan(2 * I, H, glu_steps(w.Tp));
+  w.dx = gemm_plan(T, H, glu_steps(2L * I), ~0);
+  w.dw = gemm_plan(2 * I, H, glu_steps(w.Tp), ~0);
   size_t off = 0;
   w.gu = off; off = round256(off + (saved ? 0 : (size_t)2 * T * I * 4));
   w.d = off; off = round256(off + (size_t)T * 2 * I * 2);
@@ -70,8 +70,8 @@ GluBackLayout glu_back_layout(int T, int H, int I, bool saved) {
   w.wt = off; off = round256(off + (size_t)H * 2 * I * 2);
   w.part = off;
   size_t part = saved ? 0 : glu_forward_part(T, H, I);
-  if (w.dx.splits > 1) part = std::max(part, (size_t)w.dx.splits * T * H * 4);
-  if (w.dw.splits > 1) part = std::max(part, (size_t)w.dw.splits * 2 * I * H * 4);
+  if (w.dx.tiles.splits > 1) part = std::max(part, (size_t)w.dx.tiles.splits * T * H * 4);
+  if (w.dw.tiles.splits > 1) part = std::max(part, (size_t)w.dw.tiles.splits * 2 * I * H * 4);
   w.total = round256(off + part);
   return w;
 }
@@ -80,22 +80,14 @@ int glu_forward(bool f16, const GluArgs& given, void* part, hipStream_t stream) 
   GluArgs a = given;
   const bool rows = glu_by_rows(a.T);
   const GemmPlan p = glu_forward_plan(a.T, a.H, a.I);
-  a.steps = glu_steps(a.H);
-  if (!rows) {
-    a.tok_tiles = p.tok_tiles;
-    a.row_tiles = p.row_tiles;
-    a.steps_per = p.steps_per;
-    if (p.splits > 1) a.part = static_cast<float*>(part);
-  }
+  a.tiles = p.tiles;
+  if (!rows && p.tiles.splits > 1) a.part = static_cast<float*>(part);
   return f16 ? glu_forward_f16(a, rows, p, stream) : glu_forward_bf16(a, rows, p, stream);
 }
 
 int glu_mm(bool f16, GluMmArgs a, const GemmPlan& p, void* part, hipStream_t stream) {
-  a.steps = (a.kbytes + kGemmStep - 1) / kGemmStep;
-  a.tok_tiles = p.tok_tiles;
-  a.row_tiles = p.row_tiles;
-  a.steps_per = p.steps_per;
-  a.part = p.splits > 1 ? static_cast<float*>(part) : nullptr;
+  a.tiles = p.tiles;
+  a.part = p.tiles.splits > 1 ? static_cast<float*>(part) : nullptr;
   return f16 ? glu_mm_f16(a, p, stream) : glu_mm_bf16(a, p, stream);
 }
 

@@ -26,7 +26,7 @@ struct GluArgs {
   float* part;                       // split K: [splits][2][T][I]
   long long ldx, ldw, ldh;           // ldh in elements
   int T, H, I;
-  int tok_tiles, row_tiles, steps_per, steps;
+  GemmTiles tiles;
 };
 
 // C [M, N] = A B^T over K elements; rows of C from `cut` on go to out1.
@@ -36,7 +36,7 @@ struct GluMmArgs {
   float* part;                 // split K: [splits][M][N]
   long long lda, ldb, ldo;     // ldo in elements
   int M, N, kbytes, cut;
-  int tok_tiles, row_tiles, steps_per, steps;
+  GemmTiles tiles;
 };
 
 // Launches for each type; MOE_Q4_* status.
@@ -74,56 +74,60 @@ template <> struct GluType<kGemmF16> { typedef _Float16 type; };
 // 2^-24 |g| of itself, far below a 16-bit result's half step.
 __device__ __forceinline__ float glu_sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
+// A tile of 32 of B's rows is 16 of Wg's and the same 16 of Wu's.
+template <class S>
+struct GluSource {
+  const GluArgs& a;
+  const unsigned char *tok, *row;
+  int toks, rows;
+  __device__ __forceinline__ void set(const GemmPlace& p) {
+    tok = a.x + (size_t)p.tok * S::kTok * a.ldx;
+    row = (threadIdx.x / 8 % 32 < 16 ? a.wg : a.wu) + (size_t)p.row * (S::kRows / 2) * a.ldw;  // (a thread's rows are 32 apart)
+    toks = a.T - 1 - p.tok * S::kTok;
+    rows = a.I - 1 - p.row * (S::kRows / 2);
+  }
+  __device__ __forceinline__ uint32_t tok_off(int r) const { return (uint32_t)min(r, toks) * (uint32_t)a.ldx; }
+  __device__ __forceinline__ const unsigned char* row_base(int) const { return row; }
+  __device__ __forceinline__ uint32_t row_off(int r) const { return (uint32_t)min(r / 32 * 16 + r % 16, rows) * (uint32_t)a.ldw; }
+};
+
 template <int KIND, int MT, int NT, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_glu_tiles(GluArgs a) {
   using S = GemmShape<KIND, MT, NT, WM, WN>;
   typedef typename GluType<KIND>::type T16;
-  __shared__ __attribute__((aligned(1024))) unsigned char lds0[S::kBuffer], lds1[S::kBuffer];
-  int tt, rt;
-  gemm_place(blockIdx.x, a.tok_tiles, a.row_tiles, tt, rt);
-  constexpr int kHalf = 8 * NT;  // results of a wave: its first rows are Wg's, its others Wu's
-  const int tok0 = tt * S::kTok, n0 = rt * (S::kRows / 2);
-  const int wave = threadIdx.x >> 6, wm = wave % WM, wn = wave / WM;
-  const int step0 = blockIdx.y * a.steps_per, step1 = min(a.steps, step0 + a.steps_per);
-  gemm_f32x4 acc[MT][NT];
+  static_assert(S::kThreads / 8 == 32, "GluSource's rows");
+  GluSource<S> source{a};
+  gemm_tiles<S>(a.tiles, 2 * a.H, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63), kh = lane >> 5;
+    const int t0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 31), n0 = p.row * (S::kRows / 2) + wave / WM * NT * 16;
+    const bool split = a.tiles.splits > 1;
+    float* keep = split ? a.part + (size_t)p.split * 2 * a.T * a.I : a.saved;
+    T16* h = static_cast<T16*>(a.h);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      const int t = t0 + 32 * mt;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = gemm_zero();
-  const unsigned char *g0 = a.wg + (size_t)n0 * a.ldw, *u0 = a.wu + (size_t)n0 * a.ldw;
-  gemm_tile<S>(
-      lds0, lds1, nullptr, nullptr, 2 * a.H, step0, step1, a.x + (size_t)tok0 * a.ldx,
-      [&](int r) { return (uint32_t)min(r, a.T - 1 - tok0) * (uint32_t)a.ldx; },
-      [&](int r) { return r % (2 * kHalf) < kHalf ? g0 : u0; },
-      [&](int r) { return (uint32_t)min(r / (2 * kHalf) * kHalf + r % kHalf, a.I - 1 - n0) * (uint32_t)a.ldw; }, nullptr,
-      nullptr, acc);
-  __syncthreads();  // the last step's operands have been read
-  constexpr int kWaves = WM * WN, kBytes = 2 * S::kBuffer / kWaves;
-  float* mine = reinterpret_cast<float*>(wave < kWaves / 2 ? lds0 + wave * kBytes : lds1 + (wave - kWaves / 2) * kBytes);
-  const int t0 = tok0 + wm * MT * 16, c0 = n0 + wn * kHalf;
-  float* keep = a.part ? a.part + (size_t)blockIdx.y * 2 * a.T * a.I : a.saved;
-  if (keep) {
+      for (int nt = 0; nt < NT; ++nt) {
+        uint2 out[2];
 #pragma unroll
-    for (int up = 0; up < 2; ++up)
-      gemm_out<MT, NT / 2, kBytes>(
-          mine, [&](int mt, int nt) { return acc[mt][nt + up * (NT / 2)]; },
-          [&](int r, int c, float (&v)[8]) {
-            if (t0 + r < a.T && c0 + c < a.I) norm_store8(keep + ((size_t)up * a.T + t0 + r) * a.I + c0 + c, a.I - c0 - c, v);
-          });
-  }
-  if (a.h && !a.part)
-    gemm_out<MT, NT / 2, kBytes>(
-        mine,
-        [&](int mt, int nt) {
-          const gemm_f32x4 g = acc[mt][nt], u = acc[mt][nt + NT / 2];
-          gemm_f32x4 h;
+        for (int g = 0; g < 2; ++g) {
+          const gemm_f32x4 gate = gemm_four(acc[mt][nt], g), up = gemm_four(acc[mt][nt], g + 2);
+          const int n = n0 + 16 * nt + 8 * g + 4 * kh;  // (I is a multiple of 8: all four are there)
+          if (keep && t < a.T && n < a.I) {
+            gemm_put32(keep + (size_t)t * a.I + n, 4, gate);
+            gemm_put32(keep + ((size_t)a.T + t) * a.I + n, 4, up);
+          }
+          gemm_f32x4 v;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] = g[i] * glu_sigmoid(g[i]) * u[i];
-          return h;
-        },
-        [&](int r, int c, float (&v)[8]) {
-          if (t0 + r < a.T && c0 + c < a.I) norm_store8(static_cast<T16*>(a.h) + (size_t)(t0 + r) * a.ldh + c0 + c, a.I - c0 - c, v);
-        });
+          for (int i = 0; i < 4; ++i) v[i] = gate[i] * glu_sigmoid(gate[i]) * up[i];
+          out[g] = gemm_pack4<T16>(v);
+        }
+        const uint4 q = gemm_eight32(out[0], out[1]);
+        const int n = n0 + 16 * nt + 8 * kh;
+        if (h && !split && t < a.T && n < a.I) gemm_put16(h + (size_t)t * a.ldh + n, 8, q);
+      }
+    }
+  });
 }
 
 // Few tokens: 8 rows of Wg and the same of Wu a workgroup, their inputs spread over its waves.
@@ -144,7 +148,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_glu_rows(GluArgs a) {
   }
   // (I is a multiple of 8: every row is there)
   const unsigned char* row = (n16 < 8 ? a.wg : a.wu) + (size_t)(row0 + (n16 & 7)) * a.ldw;
-  gemm_rows<KIND, MT, U>(row, tok, 2 * a.H, wave, WAVES, a.steps, nullptr, none, acc);
+  gemm_rows<KIND, MT, U>(row, tok, 2 * a.H, wave, WAVES, a.tiles.steps, nullptr, none, acc);
   gemm_f32x4 v = gemm_join_waves<MT, WAVES>(lds, acc);
   // lanes of kb 0 and 1 hold g, those of kb 2 and 3 u of the same results
   gemm_f32x4 u;
@@ -187,39 +191,53 @@ __global__ __launch_bounds__(256) void k_glu_join(GluArgs a, int splits) {
   }
 }
 
+template <class S>
+struct GluMmSource {
+  const GluMmArgs& a;
+  const unsigned char *tok, *row;
+  int toks, rows;
+  __device__ __forceinline__ void set(const GemmPlace& p) {
+    tok = a.a + (size_t)p.tok * S::kTok * a.lda;
+    row = a.b + (size_t)p.row * S::kRows * a.ldb;
+    toks = a.M - 1 - p.tok * S::kTok;
+    rows = a.N - 1 - p.row * S::kRows;
+  }
+  __device__ __forceinline__ uint32_t tok_off(int r) const { return (uint32_t)min(r, toks) * (uint32_t)a.lda; }
+  __device__ __forceinline__ const unsigned char* row_base(int) const { return row; }
+  __device__ __forceinline__ uint32_t row_off(int r) const { return (uint32_t)min(r, rows) * (uint32_t)a.ldb; }
+};
+
 template <int KIND, int MT, int NT, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_glu_mm(GluMmArgs a) {
   using S = GemmShape<KIND, MT, NT, WM, WN>;
   typedef typename GluType<KIND>::type T16;
-  __shared__ __attribute__((aligned(1024))) unsigned char lds0[S::kBuffer], lds1[S::kBuffer];
-  int tt, rt;
-  gemm_place(blockIdx.x, a.tok_tiles, a.row_tiles, tt, rt);
-  const int tok0 = tt * S::kTok, row0 = rt * S::kRows;
-  const int wave = threadIdx.x >> 6, wm = wave % WM, wn = wave / WM;
-  const int step0 = blockIdx.y * a.steps_per, step1 = min(a.steps, step0 + a.steps_per);
-  gemm_f32x4 acc[MT][NT];
+  GluMmSource<S> source{a};
+  gemm_tiles<S>(a.tiles, a.kbytes, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63), kh = lane >> 5;
+    const int m0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 31), n0 = p.row * S::kRows + wave / WM * NT * 32;
+    const bool split = a.tiles.splits > 1;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      const int m = m0 + 32 * mt;
+      T16* to = static_cast<T16*>(m < a.cut ? a.out0 : a.out1) + (long long)(m < a.cut ? m : m - a.cut) * a.ldo;
+      float* part = split ? a.part + ((size_t)p.split * a.M + m) * a.N : nullptr;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = gemm_zero();
-  const unsigned char* b0 = a.b + (size_t)row0 * a.ldb;
-  gemm_tile<S>(
-      lds0, lds1, nullptr, nullptr, a.kbytes, step0, step1, a.a + (size_t)tok0 * a.lda,
-      [&](int r) { return (uint32_t)min(r, a.M - 1 - tok0) * (uint32_t)a.lda; }, [&](int) { return b0; },
-      [&](int r) { return (uint32_t)min(r, a.N - 1 - row0) * (uint32_t)a.ldb; }, nullptr, nullptr, acc);
-  __syncthreads();  // the last step's operands have been read
-  constexpr int kWaves = WM * WN, kBytes = 2 * S::kBuffer / kWaves;
-  float* mine = reinterpret_cast<float*>(wave < kWaves / 2 ? lds0 + wave * kBytes : lds1 + (wave - kWaves / 2) * kBytes);
-  gemm_out<MT, NT, kBytes>(
-      mine, [&](int mt, int nt) { return acc[mt][nt]; },
-      [&](int r, int c, float (&v)[8]) {
-        const int m = tok0 + wm * MT * 16 + r, n = row0 + wn * NT * 16 + c;
-        if (m >= a.M || n >= a.N) return;
-        if (a.part)
-          norm_store8(a.part + ((size_t)blockIdx.y * a.M + m) * a.N + n, a.N - n, v);
-        else
-          norm_store8(static_cast<T16*>(m < a.cut ? a.out0 : a.out1) + (size_t)(m < a.cut ? m : m - a.cut) * a.ldo + n, a.N - n, v);
-      });
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {  // (N is a multiple of 8: all neighbours are there)
+          const gemm_f32x4 v0 = gemm_four(acc[mt][nt], g), v1 = gemm_four(acc[mt][nt], g + 1);
+          const int n = n0 + 32 * nt + 8 * g;
+          if (split) {
+            if (m < a.M && n + 4 * kh < a.N) gemm_put32(part + n + 4 * kh, 4, v0);
+            if (m < a.M && n + 8 + 4 * kh < a.N) gemm_put32(part + n + 8 + 4 * kh, 4, v1);
+          } else {
+            const uint4 q = gemm_eight32(gemm_pack4<T16>(v0), gemm_pack4<T16>(v1));
+            if (m < a.M && n + 8 * kh < a.N) gemm_put16(to + n + 8 * kh, 8, q);
+          }
+        }
+      }
+    }
+  });
 }
 
 // (N is a multiple of 8)
@@ -286,32 +304,34 @@ int glu_forward_kind(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t
       hipLaunchKernelGGL((k_glu_rows<KIND, 2, 16, 2>), grid, dim3(1024), 0, stream, a);
     return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
   }
-  const dim3 grid((unsigned)(p.tok_tiles * p.row_tiles), p.splits);
+  const dim3 grid(p.workgroups);
   switch (p.shape) {
-    case kGemm256x256: hipLaunchKernelGGL((k_glu_tiles<KIND, 8, 4, 2, 4>), grid, dim3(512), 0, stream, a); break;
-    case kGemm128x128: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    default: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 2, 1, 4>), grid, dim3(256), 0, stream, a); break;
+    case kGemm256x256: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm256x192: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x128: hipLaunchKernelGGL((k_glu_tiles<KIND, 2, 2, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    default: hipLaunchKernelGGL((k_glu_tiles<KIND, 2, 1, 1, 4>), grid, dim3(256), 0, stream, a); break;
   }
   if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
-  if (p.splits > 1) {
+  if (p.tiles.splits > 1) {
     const size_t all = (size_t)a.T * a.I / 8;
-    hipLaunchKernelGGL((k_glu_join<KIND>), dim3((unsigned)std::min<size_t>((all + 255) / 256, 4096)), dim3(256), 0, stream, a, p.splits);
+    hipLaunchKernelGGL((k_glu_join<KIND>), dim3((unsigned)std::min<size_t>((all + 255) / 256, 4096)), dim3(256), 0, stream, a, p.tiles.splits);
   }
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }
 
 template <int KIND>
 int glu_mm_kind(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)(p.tok_tiles * p.row_tiles), p.splits);
+  const dim3 grid(p.workgroups);
   switch (p.shape) {
-    case kGemm256x256: hipLaunchKernelGGL((k_glu_mm<KIND, 8, 4, 2, 4>), grid, dim3(512), 0, stream, a); break;
-    case kGemm128x128: hipLaunchKernelGGL((k_glu_mm<KIND, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    default: hipLaunchKernelGGL((k_glu_mm<KIND, 4, 2, 1, 4>), grid, dim3(256), 0, stream, a); break;
+    case kGemm256x256: hipLaunchKernelGGL((k_glu_mm<KIND, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm256x192: hipLaunchKernelGGL((k_glu_mm<KIND, 4, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x128: hipLaunchKernelGGL((k_glu_mm<KIND, 2, 2, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    default: hipLaunchKernelGGL((k_glu_mm<KIND, 2, 1, 1, 4>), grid, dim3(256), 0, stream, a); break;
   }
   if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
-  if (p.splits > 1) {
+  if (p.tiles.splits > 1) {
     const size_t all = (size_t)a.M * a.N / 8;
-    hipLaunchKernelGGL((k_glu_mm_join<KIND>), dim3((unsigned)std::min<size_t>((all + 255) / 256, 4096)), dim3(256), 0, stream, a, p.splits);
+    hipLaunchKernelGGL((k_glu_mm_join<KIND>), dim3((unsigned)std::min<size_t>((all + 255) / 256, 4096)), dim3(256), 0, stream, a, p.tiles.splits);
   }
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }
