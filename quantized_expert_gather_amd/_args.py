@@ -31,6 +31,16 @@ def matrix(t, dtypes, name: str):
     return t.data_ptr(), ld if rows > 1 else cols
 
 
+def plane(t, dtypes, name: str):
+    """As :func:`matrix`, with the shape: (pointer, row stride, shape).  The usual
+    matrix, contiguous and as it should be, is asked least."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2 and t.is_contiguous():
+        shape = t.shape
+        return t.data_ptr(), shape[1], shape
+    p, ld = matrix(t, dtypes, name)
+    return p, ld, t.shape
+
+
 def array(t, dtype, shape, name: str, device) -> int:
     """Pointer of a contiguous device tensor of this type (one of these types), shape and device."""
     if isinstance(t, torch.Tensor) and t.shape == shape and t.device == device and t.is_contiguous() and \

@@ -58,12 +58,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_tiles(Fp8Args a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t0 = p.tok * S::kTok + wave % WM * MT * 16, n0 = p.row * S::kRows + wave / WM * NT * 16;
     const int lane = gemm_opaque(threadIdx.x & 63), n16 = lane & 15, kb = lane >> 4;
-    const bool fp32 = a.part || a.out_dtype == MOE_Q4_DTYPE_F32;
+    const bool fp32 = a.part || a.out_dtype == MOE_Q4_DTYPE_F32, bf16 = a.out_dtype == MOE_Q4_DTYPE_BF16;
     float* to = a.part ? a.part + (size_t)p.split * a.L * a.N : static_cast<float*>(a.out);
     const long long ld = a.part ? a.N : a.ldo;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int t = t0 + 16 * mt + n16;
+      const bool row = t < a.L;
+      float* to32 = to + t * ld + n0 + 4 * kb;
+      uint16_t* to16 = static_cast<uint16_t*>(a.out) + t * ld + n0 + 8 * kb;
 #pragma unroll
       for (int nt = 0; nt < NT; nt += 2) {
         gemm_f32x4 v[2];
@@ -75,46 +78,52 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_tiles(Fp8Args a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[h][i] += a.bias[min(n + i, a.N - 1)];
           }
-          if (fp32 && t < a.L) gemm_put32(to + t * ld + n, a.N - n, v[h]);
+          if (fp32 && row) gemm_put32(to32 + 16 * (nt + h), a.N - n, v[h]);
         }
         if (!fp32) {
-          const uint4 q = a.out_dtype == MOE_Q4_DTYPE_BF16 ? gemm_eight16(gemm_pack4<__bf16>(v[0]), gemm_pack4<__bf16>(v[1]))
-                                                           : gemm_eight16(gemm_pack4<_Float16>(v[0]), gemm_pack4<_Float16>(v[1]));
-          const int n = n0 + 16 * nt + 8 * kb;
-          if (t < a.L) gemm_put16(static_cast<uint16_t*>(a.out) + t * ld + n, a.N - n, q);
+          const uint4 q = bf16 ? gemm_eight16(gemm_pack4<__bf16>(v[0]), gemm_pack4<__bf16>(v[1]))
+                               : gemm_eight16(gemm_pack4<_Float16>(v[0]), gemm_pack4<_Float16>(v[1]));
+          if (row) gemm_put16(to16 + 16 * nt, a.N - n0 - 16 * nt - 8 * kb, q);
         }
       }
     }
   });
 }
 
-// 16 rows of w a workgroup, their inputs spread over its waves.
-template <int MT, int WAVES, int U>
+// 8 J rows of w a workgroup, their inputs spread over its waves; G x 8 tokens.
+template <int J, int G, int WAVES, int U>
 __global__ __launch_bounds__(64 * WAVES) void k_fp8_rows(Fp8Args a) {
-  __shared__ gemm_f32x4 lds[WAVES][MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, kb = lane >> 4;
-  const int row0 = blockIdx.x * 16;
-  const unsigned char* tok[MT];
-  const float* sx[MT];
-  gemm_f32x4 acc[MT];
+  __shared__ float lds[WAVES][J][G][64];
+  const int wave = threadIdx.x >> 6, row0 = blockIdx.x * 8 * J, index = gemm_rows_index();
+  const unsigned char *tok[G], *row[J];
+  const float* sx[G];
+  gemm_f32x4 acc[J][G];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const size_t t = min(mt * 16 + n16, a.L - 1);
-    tok[mt] = a.x + t * a.ldx;
-    sx[mt] = a.sx + t * a.G;
-    acc[mt] = gemm_f32x4{0, 0, 0, 0};
-  }
-  gemm_rows<kGemmFp8Wide, MT, U>(a.w + (size_t)min(row0 + n16, a.N - 1) * a.K, tok, a.K, wave, WAVES, a.G,
-                             a.sw + (size_t)(row0 / 128) * a.G, sx, acc);
-  gemm_f32x4 v = gemm_join_waves<MT, WAVES>(lds, acc);
-  const int t = wave * 16 + n16, n = row0 + 4 * kb;
-  if (wave >= MT || t >= a.L || n >= a.N) return;
-  if (a.bias) {
+  for (int g = 0; g < G; ++g) {
+    const size_t t = min(8 * g + index, a.L - 1);
+    tok[g] = a.x + t * a.ldx;
+    sx[g] = a.sx + t * a.G;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += a.bias[min(n + i, a.N - 1)];
+    for (int j = 0; j < J; ++j) acc[j][g] = gemm_f32x4{0, 0, 0, 0};
   }
-  float out[8] = {v[0], v[1], v[2], v[3], 0, 0, 0, 0};
-  norm_store8_as(a.out, a.out_dtype, (long)t * a.ldo + n, min(a.N - n, 4), out);
+#pragma unroll
+  for (int j = 0; j < J; ++j) row[j] = a.w + (size_t)min(row0 + 8 * j + index, a.N - 1) * a.K;
+  gemm_rows<kGemmFp8Wide, J, G, U>(row, tok, a.K, wave, WAVES, a.G, a.sw + (size_t)(row0 / 128) * a.G, sx, acc);
+  gemm_join_waves<J, G, WAVES>(lds, acc);
+  // neighbours of a token to as many lanes
+  for (int i = threadIdx.x; i < G * 8 * J * 8; i += 64 * WAVES) {
+    const int t = i / (8 * J), r = i % (8 * J), n = row0 + r;
+    if (t >= a.L || n >= a.N) continue;
+    float v = lds[0][r / 8][t / 8][r % 8 / 2 * 16 + t % 8 * 2 + r % 2];
+    if (a.bias) v += a.bias[n];
+    const size_t at = (size_t)t * a.ldo + n;
+    if (a.out_dtype == MOE_Q4_DTYPE_F32)
+      static_cast<float*>(a.out)[at] = v;
+    else if (a.out_dtype == MOE_Q4_DTYPE_BF16)
+      static_cast<__bf16*>(a.out)[at] = (__bf16)v;
+    else
+      static_cast<_Float16*>(a.out)[at] = (_Float16)v;
+  }
 }
 
 // Partial sums of a split K, added in their order.
@@ -183,11 +192,20 @@ extern "C" int moe_linear_fp8_forward(const uint8_t* x, long long ldx, const flo
   if (args_alias(outs, ins)) return MOE_Q4_ERR_ALIAS;
   Fp8Args a{x, sx, w, sw, bias, out, nullptr, ldx, ldo, L, N, K, G, out_dtype, {}};
   if (fp8_by_rows(L)) {
-    const dim3 grid((N + 15) / 16);
-    if (L <= 16)
-      hipLaunchKernelGGL((k_fp8_rows<1, 8, 4>), grid, dim3(512), 0, stream, a);
+    // 32 rows of w share a workgroup's reads of x where that leaves most compute units one (us, 16 and 32 rows:
+    // 16 tokens 6144 x 6144 15.1 and 12.6, 4099 x 4112 9.4 and 10.6; 32 tokens 27 and 19, 16.1 and 13.8)
+    const bool wide = L > 8 && N >= (L > 16 ? 4096 : 6144);
+    const dim3 grid(wide ? (N + 31) / 32 : (N + 15) / 16);
+    if (L <= 8)
+      hipLaunchKernelGGL((k_fp8_rows<2, 1, 8, 6>), grid, dim3(512), 0, stream, a);
+    else if (L <= 16 && wide)
+      hipLaunchKernelGGL((k_fp8_rows<4, 2, 8, 6>), grid, dim3(512), 0, stream, a);
+    else if (L <= 16)
+      hipLaunchKernelGGL((k_fp8_rows<2, 2, 8, 3>), grid, dim3(512), 0, stream, a);
+    else if (wide)
+      hipLaunchKernelGGL((k_fp8_rows<4, 4, 8, 2>), grid, dim3(512), 0, stream, a);
     else
-      hipLaunchKernelGGL((k_fp8_rows<2, 8, 4>), grid, dim3(512), 0, stream, a);
+      hipLaunchKernelGGL((k_fp8_rows<2, 4, 8, 2>), grid, dim3(512), 0, stream, a);
     return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
   }
   const GemmPlan p = fp8_plan(L, N, K, out_dtype == MOE_Q4_DTYPE_F32);

@@ -62,26 +62,6 @@ __device__ __forceinline__ gemm_f32x4 gemm_product(const GemmFrag& a, const Gemm
   return s;
 }
 
-// acc += a b over a step; E4M3: the step's sums times f.
-template <int KIND>
-__device__ __forceinline__ void gemm_step(const GemmFrag& a, const GemmFrag& b, float f, gemm_f32x4& acc) {
-  if constexpr (gemm_scaled(KIND)) {
-    const gemm_f32x4 s = gemm_product<KIND>(a, b);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(s[i], f, acc[i]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if constexpr (KIND == kGemmBf16)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(gemm_bf16x8, a.v[j]),
-                                                      __builtin_bit_cast(gemm_bf16x8, b.v[j]), acc, 0, 0, 0);
-      else
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(gemm_f16x8, a.v[j]),
-                                                     __builtin_bit_cast(gemm_f16x8, b.v[j]), acc, 0, 0, 0);
-    }
-  }
-}
-
 // ---- many tokens ----
 
 // MT x NT tiles a wave, of 32 x 32 results (16-bit types) or 16 x 16 (E4M3),
@@ -478,60 +458,103 @@ __device__ __forceinline__ void gemm_tiles_scaled(const GemmTiles& tiles, int kb
 
 // ---- few tokens ----
 
-// One tile of 16 rows of B (row_ptr gives this lane's) against MT x 16 tokens,
-// steps first, first + stride, ... below `steps`, into acc; U steps' loads are
-// issued together.
-template <int KIND, int MT, int U>
-__device__ __forceinline__ void gemm_rows(const unsigned char* row, const unsigned char* const (&tok)[MT], int kbytes,
-                                          int first, int stride, int steps, const float* sw, const float* const (&sx)[MT],
-                                          gemm_f32x4 (&acc)[MT]) {
-  const int kb = (threadIdx.x & 63) >> 4;
+// J groups of 8 rows of B against G groups of 8 tokens, rows read once.  A
+// load of 16 bytes a lane takes 8 whole lines of 128 bytes, one a row: 16 rows
+// of 64 bytes each, what an operand of 16 rows would take, are read at 3.8 and
+// not 5.5 TB/s (6144 rows of 6144 bytes, the loads alone).  So an operand's row
+// m is row m / 2 of the group, of whose line it holds the chunks 2 kb + m % 2,
+// and tokens likewise: results (m, t) with m % 2 = t % 2 are the sums over one
+// half of the chunks each, the others mean nothing.
+
+// A product of 16 bytes a lane: one instruction of 16-bit numbers onto acc, two
+// of E4M3 codes made bf16, whose sums times f go onto acc.
+template <int KIND>
+__device__ __forceinline__ void gemm_chunk(gemm_i32x4 w, gemm_i32x4 x, float f, gemm_f32x4& acc) {
+  if constexpr (KIND == kGemmFp8Wide) {
+    gemm_f32x4 s = {0, 0, 0, 0};
+    s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(gemm_e4m3_bf16(w[0], w[1]), gemm_e4m3_bf16(x[0], x[1]), s, 0, 0, 0);
+    s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(gemm_e4m3_bf16(w[2], w[3]), gemm_e4m3_bf16(x[2], x[3]), s, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(s[i], f, acc[i]);
+  } else if constexpr (KIND == kGemmBf16) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(gemm_bf16x8, w), __builtin_bit_cast(gemm_bf16x8, x), acc, 0, 0, 0);
+  } else {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(gemm_f16x8, w), __builtin_bit_cast(gemm_f16x8, x), acc, 0, 0, 0);
+  }
+}
+
+// This lane's row of 8, token of 8 and chunk in the above.
+__device__ __forceinline__ int gemm_rows_index() { return (threadIdx.x & 15) >> 1; }
+__device__ __forceinline__ int gemm_rows_chunk() { return 2 * ((threadIdx.x & 63) >> 4) + (threadIdx.x & 1); }
+
+// Steps first, first + stride, ... below `steps` of the lane's rows and tokens
+// into acc; U steps' loads are on their way together.
+template <int KIND, int J, int G, int U>
+__device__ __forceinline__ void gemm_rows(const unsigned char* const (&row)[J], const unsigned char* const (&tok)[G], int kbytes,
+                                          int first, int stride, int steps, const float* sw, const float* const (&sx)[G],
+                                          gemm_f32x4 (&acc)[J][G]) {
+  const int at = gemm_rows_chunk() * 16;
   for (int s = first; s < steps; s += U * stride) {
-    GemmFrag w[U], x[U][MT];
-    float f[U][MT];
+    gemm_i32x4 w[U][J], x[U][G];
+    float f[U][G];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int step = s + u * stride;
+      if (step < steps) {
+        const int k = min(step * kGemmStep + at, kbytes - 16);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int k = min(step * kGemmStep + (kb + 4 * j) * 16, kbytes - 16);
-        w[u].v[j] = __builtin_nontemporal_load(reinterpret_cast<const gemm_i32x4*>(row + k));
+        for (int j = 0; j < J; ++j) w[u][j] = __builtin_nontemporal_load(reinterpret_cast<const gemm_i32x4*>(row[j] + k));
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) x[u][mt].v[j] = *reinterpret_cast<const gemm_i32x4*>(tok[mt] + k);
-      }
-      if constexpr (gemm_scaled(KIND)) {
-        const int g = min(step, steps - 1);
+        for (int g = 0; g < G; ++g) x[u][g] = *reinterpret_cast<const gemm_i32x4*>(tok[g] + k);
+        if constexpr (gemm_scaled(KIND)) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) f[u][mt] = sx[mt][g] * sw[g];
+          for (int g = 0; g < G; ++g) f[u][g] = sx[g][step];
+        }
       }
     }
+    __builtin_amdgcn_sched_barrier(0);  // all are on their way before the first is waited for
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int left = kbytes - (s + u * stride) * kGemmStep;
+      const int step = s + u * stride;
+      if (step >= steps) break;
+      if (step * kGemmStep + at >= kbytes) {  // past the rows' end: one operand's zeros
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if ((kb + 4 * j) * 16 >= left) w[u].v[j] = gemm_i32x4{0, 0, 0, 0};
+        for (int j = 0; j < J; ++j) w[u][j] = gemm_i32x4{0, 0, 0, 0};
+      }
+      float ws = 1.0f;
+      if constexpr (gemm_scaled(KIND)) ws = sw[step];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) gemm_step<KIND>(w[u], x[u][mt], f[u][mt], acc[mt]);
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < J; ++j) gemm_chunk<KIND>(w[u][j], x[u][g], gemm_scaled(KIND) ? f[u][g] * ws : 1.0f, acc[j][g]);
     }
   }
 }
 
-// Sums of the workgroup's waves, in their order: thread i < 64 MT holds lane i
-// % 64's part of token tile i / 64.
-template <int MT, int WAVES>
-__device__ __forceinline__ gemm_f32x4 gemm_join_waves(gemm_f32x4 (&lds)[WAVES][MT][64], const gemm_f32x4 (&acc)[MT]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// The two halves' sums, and those of the workgroup's waves in their order:
+// behind it lds[0][j][g][lane] is the result of row 2 (lane / 16) + lane % 2
+// of group j and token lane % 16 / 2 of group g.
+template <int J, int G, int WAVES>
+__device__ __forceinline__ void gemm_join_waves(float (&lds)[WAVES][J][G][64], const gemm_f32x4 (&acc)[J][G]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, odd = lane & 1;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) lds[wave][mt][lane] = acc[mt];
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      // of its four rows, two rows' halves: a lane keeps the row that is its own and gives the other's
+      const float low = odd ? acc[j][g][1] : acc[j][g][0], high = odd ? acc[j][g][3] : acc[j][g][2];
+      const float mine = odd ? high : low, given = odd ? low : high;
+      lds[wave][j][g][lane] = mine + __shfl_xor(given, 1);
+    }
   __syncthreads();
-  gemm_f32x4 s = {0, 0, 0, 0};
-  if (wave < MT) {
-    s = lds[0][wave][lane];
+  for (int i = threadIdx.x; i < J * G * 64; i += 64 * WAVES) {
+    float* at = &lds[0][0][0][0] + i;
+    float v = at[0];
 #pragma unroll
-    for (int i = 1; i < WAVES; ++i) s += lds[i][wave][lane];
+    for (int k = 1; k < WAVES; ++k) v += at[k * J * G * 64];
+    at[0] = v;  // (read by this thread alone so far)
   }
-  return s;
+  __syncthreads();
 }
 
 // ---- results ----
@@ -564,6 +587,19 @@ __device__ __forceinline__ uint4 gemm_eight32(uint2 a, uint2 b) {
   const auto x = __builtin_amdgcn_permlane32_swap(a.x, b.x, false, false), y = __builtin_amdgcn_permlane32_swap(a.y, b.y, false, false);
   return make_uint4(x[0], y[0], x[1], y[1]);
 }
+// 16 bytes a lane of 32 x 32 tiles, p and q, from two bytes' places of a
+// token's results (the upper lanes' follow the lower lanes'): swapped so that
+// p is of the tokens lane % 16 and q of the 16 after these, at place
+// gemm_place4() of 4.  A token's four lanes write 64 bytes: of 32 each, the
+// writes' number and not their bytes bound the stores (5 us of a tile).
+__device__ __forceinline__ void gemm_spread(uint4& p, uint4& q) {
+  const auto x = __builtin_amdgcn_permlane16_swap(p.x, q.x, false, false), y = __builtin_amdgcn_permlane16_swap(p.y, q.y, false, false);
+  const auto z = __builtin_amdgcn_permlane16_swap(p.z, q.z, false, false), w = __builtin_amdgcn_permlane16_swap(p.w, q.w, false, false);
+  p = make_uint4(x[0], y[0], z[0], w[0]);
+  q = make_uint4(x[1], y[1], z[1], w[1]);
+}
+__device__ __forceinline__ int gemm_place4(int lane) { return (lane >> 4 & 1) * 2 + (lane >> 5); }
+
 // Of 16 x 16 tiles side by side: rows of 16 lanes (a0 a1 a2 a3) and (b0 b1 b2
 // b3) swapped to (a0 a2 b0 b2) and (a1 a3 b1 b3): eight from 8 (lane / 16) on.
 __device__ __forceinline__ uint4 gemm_eight16(uint2 a, uint2 b) {

@@ -98,70 +98,91 @@ __global__ __launch_bounds__(64 * WM * WN) void k_glu_tiles(GluArgs a) {
   static_assert(S::kThreads / 8 == 32, "GluSource's rows");
   GluSource<S> source{a};
   gemm_tiles<S>(a.tiles, 2 * a.H, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63), kh = lane >> 5;
-    const int t0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 31), n0 = p.row * (S::kRows / 2) + wave / WM * NT * 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63);
+    const int place = gemm_place4(lane), t0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 15);
+    const int n0 = p.row * (S::kRows / 2) + wave / WM * NT * 16;
     const bool split = a.tiles.splits > 1;
     float* keep = split ? a.part + (size_t)p.split * 2 * a.T * a.I : a.saved;
-    T16* h = static_cast<T16*>(a.h);
+    T16* h = split ? nullptr : static_cast<T16*>(a.h);
+    // (I is a multiple of 8: neighbours are all there or none)
+    const auto keep4 = [&](size_t row, int t, int n, uint4 v) __attribute__((always_inline)) {
+      if (t < a.T && n < a.I) gemm_put32(keep + (row + t) * a.I + n, 4, __builtin_bit_cast(gemm_f32x4, v));
+    };
+    const auto put8 = [&](int t, int n, uint4 v) __attribute__((always_inline)) {
+      if (t < a.T && n < a.I) gemm_put16(h + (size_t)t * a.ldh + n, 8, v);
+    };
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int t = t0 + 32 * mt;
+      uint4 even = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         uint2 out[2];
+        uint4 kept[2][2];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const gemm_f32x4 gate = gemm_four(acc[mt][nt], g), up = gemm_four(acc[mt][nt], g + 2);
-          const int n = n0 + 16 * nt + 8 * g + 4 * kh;  // (I is a multiple of 8: all four are there)
-          if (keep && t < a.T && n < a.I) {
-            gemm_put32(keep + (size_t)t * a.I + n, 4, gate);
-            gemm_put32(keep + ((size_t)a.T + t) * a.I + n, 4, up);
-          }
+          kept[0][g] = __builtin_bit_cast(uint4, gate);
+          kept[1][g] = __builtin_bit_cast(uint4, up);
           gemm_f32x4 v;
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = gate[i] * glu_sigmoid(gate[i]) * up[i];
           out[g] = gemm_pack4<T16>(v);
         }
-        const uint4 q = gemm_eight32(out[0], out[1]);
-        const int n = n0 + 16 * nt + 8 * kh;
-        if (h && !split && t < a.T && n < a.I) gemm_put16(h + (size_t)t * a.ldh + n, 8, q);
+        if (keep) {
+#pragma unroll
+          for (int up = 0; up < 2; ++up) {
+            gemm_spread(kept[up][0], kept[up][1]);
+            const int n = n0 + 16 * nt + 4 * place;
+            keep4(up ? a.T : 0, t, n, kept[up][0]);
+            keep4(up ? a.T : 0, t + 16, n, kept[up][1]);
+          }
+        }
+        uint4 q = gemm_eight32(out[0], out[1]);
+        if (!h) continue;
+        if (nt % 2 == 0 && nt + 1 < NT) {
+          even = q;
+        } else if (nt % 2) {
+          gemm_spread(even, q);
+          const int n = n0 + 16 * (nt - 1) + 8 * place;
+          put8(t, n, even);
+          put8(t + 16, n, q);
+        } else {  // one tile left
+          put8(t + (lane & 16), n0 + 16 * nt + 8 * (lane >> 5), q);
+        }
       }
     }
   });
 }
 
-// Few tokens: 8 rows of Wg and the same of Wu a workgroup, their inputs spread over its waves.
-template <int KIND, int MT, int WAVES, int U>
+// Few tokens: 8 rows of Wg and the same of Wu a workgroup, their inputs spread
+// over its waves; G x 8 tokens.
+template <int KIND, int G, int WAVES, int U>
 __global__ __launch_bounds__(64 * WAVES) void k_glu_rows(GluArgs a) {
   typedef typename GluType<KIND>::type T16;
-  __shared__ gemm_f32x4 lds[WAVES][MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, kb = lane >> 4;
-  const int row0 = blockIdx.x * 8;
-  const unsigned char* tok[MT];
-  const float* none[MT];
-  gemm_f32x4 acc[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    tok[mt] = a.x + (size_t)min(mt * 16 + n16, a.T - 1) * a.ldx;
-    none[mt] = nullptr;
-    acc[mt] = gemm_f32x4{0, 0, 0, 0};
-  }
+  __shared__ float lds[WAVES][2][G][64];
+  const int wave = threadIdx.x >> 6, row0 = blockIdx.x * 8, index = gemm_rows_index();
   // (I is a multiple of 8: every row is there)
-  const unsigned char* row = (n16 < 8 ? a.wg : a.wu) + (size_t)(row0 + (n16 & 7)) * a.ldw;
-  gemm_rows<KIND, MT, U>(row, tok, 2 * a.H, wave, WAVES, a.tiles.steps, nullptr, none, acc);
-  gemm_f32x4 v = gemm_join_waves<MT, WAVES>(lds, acc);
-  // lanes of kb 0 and 1 hold g, those of kb 2 and 3 u of the same results
-  gemm_f32x4 u;
+  const unsigned char *tok[G], *const row[2] = {a.wg + (size_t)(row0 + index) * a.ldw, a.wu + (size_t)(row0 + index) * a.ldw};
+  const float* none[G];
+  gemm_f32x4 acc[2][G];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) u[i] = __shfl_xor(v[i], 32);
-  const int t = wave * 16 + n16, n = row0 + 4 * (kb & 1);
-  if (wave >= MT || t >= a.T) return;
-  if (a.saved) *reinterpret_cast<gemm_f32x4*>(a.saved + ((size_t)(kb >> 1) * a.T + t) * a.I + n) = v;
-  if (a.h && kb < 2) {
-    float h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = v[i] * glu_sigmoid(v[i]) * u[i];
-    norm_store8(static_cast<T16*>(a.h) + (size_t)t * a.ldh + n, 4, h);
+  for (int g = 0; g < G; ++g) {
+    tok[g] = a.x + (size_t)min(8 * g + index, a.T - 1) * a.ldx;
+    none[g] = nullptr;
+    acc[0][g] = acc[1][g] = gemm_f32x4{0, 0, 0, 0};
+  }
+  gemm_rows<KIND, 2, G, U>(row, tok, 2 * a.H, wave, WAVES, a.tiles.steps, nullptr, none, acc);
+  gemm_join_waves<2, G, WAVES>(lds, acc);
+  for (int i = threadIdx.x; i < G * 8 * 8; i += 64 * WAVES) {  // 8 neighbours of a token to as many lanes
+    const int t = i / 8, r = i % 8, n = row0 + r, at = r / 2 * 16 + t % 8 * 2 + r % 2;
+    if (t >= a.T) continue;
+    const float g = lds[0][0][t / 8][at], u = lds[0][1][t / 8][at];
+    if (a.saved) {
+      a.saved[(size_t)t * a.I + n] = g;
+      a.saved[((size_t)a.T + t) * a.I + n] = u;
+    }
+    if (a.h) static_cast<T16*>(a.h)[(size_t)t * a.ldh + n] = (T16)(g * glu_sigmoid(g) * u);
   }
 }
 
@@ -213,27 +234,41 @@ __global__ __launch_bounds__(64 * WM * WN) void k_glu_mm(GluMmArgs a) {
   typedef typename GluType<KIND>::type T16;
   GluMmSource<S> source{a};
   gemm_tiles<S>(a.tiles, a.kbytes, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63), kh = lane >> 5;
-    const int m0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 31), n0 = p.row * S::kRows + wave / WM * NT * 32;
-    const bool split = a.tiles.splits > 1;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63);
+    const int place = gemm_place4(lane), m0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 15);
+    const int n0 = p.row * S::kRows + wave / WM * NT * 32;
+    float* part = a.tiles.splits > 1 ? a.part + (size_t)p.split * a.M * a.N : nullptr;
+    // (N is a multiple of 8: neighbours are all there or none)
+    const auto put4 = [&](int m, int n, uint4 v) __attribute__((always_inline)) {
+      if (m < a.M && n < a.N) gemm_put32(part + (size_t)m * a.N + n, 4, __builtin_bit_cast(gemm_f32x4, v));
+    };
+    const auto put8 = [&](int m, int n, uint4 v) __attribute__((always_inline)) {
+      if (m < a.M && n < a.N)
+        gemm_put16(static_cast<T16*>(m < a.cut ? a.out0 : a.out1) + (size_t)(m < a.cut ? m : m - a.cut) * a.ldo + n, 8, v);
+    };
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int m = m0 + 32 * mt;
-      T16* to = static_cast<T16*>(m < a.cut ? a.out0 : a.out1) + (long long)(m < a.cut ? m : m - a.cut) * a.ldo;
-      float* part = split ? a.part + ((size_t)p.split * a.M + m) * a.N : nullptr;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        if (part) {
 #pragma unroll
-        for (int g = 0; g < 4; g += 2) {  // (N is a multiple of 8: all neighbours are there)
-          const gemm_f32x4 v0 = gemm_four(acc[mt][nt], g), v1 = gemm_four(acc[mt][nt], g + 1);
-          const int n = n0 + 32 * nt + 8 * g;
-          if (split) {
-            if (m < a.M && n + 4 * kh < a.N) gemm_put32(part + n + 4 * kh, 4, v0);
-            if (m < a.M && n + 8 + 4 * kh < a.N) gemm_put32(part + n + 8 + 4 * kh, 4, v1);
-          } else {
-            const uint4 q = gemm_eight32(gemm_pack4<T16>(v0), gemm_pack4<T16>(v1));
-            if (m < a.M && n + 8 * kh < a.N) gemm_put16(to + n + 8 * kh, 8, q);
+          for (int g = 0; g < 4; g += 2) {
+            uint4 u = __builtin_bit_cast(uint4, gemm_four(acc[mt][nt], g)), v = __builtin_bit_cast(uint4, gemm_four(acc[mt][nt], g + 1));
+            gemm_spread(u, v);
+            const int n = n0 + 32 * nt + 8 * g + 4 * place;
+            put4(m, n, u);
+            put4(m + 16, n, v);
           }
+        } else {
+          uint4 q[2];
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            q[g] = gemm_eight32(gemm_pack4<T16>(gemm_four(acc[mt][nt], 2 * g)), gemm_pack4<T16>(gemm_four(acc[mt][nt], 2 * g + 1)));
+          gemm_spread(q[0], q[1]);
+          const int n = n0 + 32 * nt + 8 * place;
+          put8(m, n, q[0]);
+          put8(m + 16, n, q[1]);
         }
       }
     }
@@ -298,10 +333,12 @@ template <int KIND>
 int glu_forward_kind(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t stream) {
   if (rows) {
     const dim3 grid(a.I / 8);
-    if (a.T <= 16)
-      hipLaunchKernelGGL((k_glu_rows<KIND, 1, 16, 3>), grid, dim3(1024), 0, stream, a);
+    if (a.T <= 8)
+      hipLaunchKernelGGL((k_glu_rows<KIND, 1, 16, 6>), grid, dim3(1024), 0, stream, a);
+    else if (a.T <= 16)
+      hipLaunchKernelGGL((k_glu_rows<KIND, 2, 16, 4>), grid, dim3(1024), 0, stream, a);
     else
-      hipLaunchKernelGGL((k_glu_rows<KIND, 2, 16, 2>), grid, dim3(1024), 0, stream, a);
+      hipLaunchKernelGGL((k_glu_rows<KIND, 4, 16, 3>), grid, dim3(1024), 0, stream, a);
     return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
   }
   const dim3 grid(p.workgroups);

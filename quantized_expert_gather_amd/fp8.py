@@ -6,9 +6,10 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, matrix, new, on_stream
+from ._args import DTYPES, array, call, current_handle, matrix, new, on_stream, plane
 
 F8 = torch.float8_e4m3fn
+_F8S = (F8,)
 
 
 def moe_linear_fp8_workspace_bytes(L: int, N: int, K: int) -> int:
@@ -29,8 +30,8 @@ def moe_linear_fp8_forward(x, sx, w, sw, bias=None, out=None, out_dtype=None, wo
     if stream is not None and isinstance(x, torch.Tensor):
         with on_stream(stream, x):
             return moe_linear_fp8_forward(x, sx, w, sw, bias, out, out_dtype, workspace)
-    xp, ldx = matrix(x, (F8,), "x")
-    L, K = x.shape
+    xp, ldx, shape = plane(x, _F8S, "x")
+    L, K = shape
     dev = x.device
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w [N, K] expected")

@@ -7,7 +7,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, matrix, new, on_stream
+from ._args import DTYPES, array, call, current_handle, new, on_stream, plane
 from .router import _not_captured
 
 _X = (torch.bfloat16, torch.float16)
@@ -21,18 +21,21 @@ def moe_glu_backward_workspace_bytes(T: int, H: int, I: int, saved: bool = True)
     return int(_q.lib().moe_glu_backward_workspace_bytes(T, H, I, 1 if saved else 0))
 
 
+def _wants(t) -> bool:
+    return isinstance(t, torch.Tensor) and t.requires_grad
+
+
 def _operands(x, wg, wu):
     """Checked x and weights: (pointers and strides of a call, T, H, I)."""
-    xp, ldx = matrix(x, _X, "x")
-    T, H = x.shape
-    gp, ldw = matrix(wg, (x.dtype,), "wg")
-    up, ldu = matrix(wu, (x.dtype,), "wu")
-    I = wg.shape[0]
-    if wg.shape != (I, H) or wu.shape != (I, H) or wg.device != x.device or wu.device != x.device:
+    xt = x.dtype if isinstance(x, torch.Tensor) else None
+    xp, ldx, (T, H) = plane(x, _X, "x")
+    gp, ldw, shape = plane(wg, (xt,), "wg")
+    up, ldu, given = plane(wu, (xt,), "wu")
+    if shape[1] != H or given != shape or wg.device != x.device or wu.device != x.device:
         raise ValueError(f"wg and wu must be [I, {H}] on {x.device}")
     if ldw != ldu:
         raise ValueError("wg and wu must have the same row stride")
-    return (DTYPES[x.dtype], xp, ldx, gp, up, ldw), T, H, I
+    return (DTYPES[xt], xp, ldx, gp, up, ldw), T, H, shape[0]
 
 
 def _result(out, shape, dtype, name, device):
@@ -40,8 +43,8 @@ def _result(out, shape, dtype, name, device):
     if out is None:
         out = new(shape, (shape[1], 1), dtype, device)
         return out, out.data_ptr(), shape[1]
-    p, ld = matrix(out, (dtype,), name)
-    if out.shape != shape or out.device != device:
+    p, ld, given = plane(out, (dtype,), name)
+    if given != shape or out.device != device:
         raise ValueError(f"{name} must be {list(shape)} on {device}")
     return out, p, ld
 
@@ -109,7 +112,7 @@ def moe_glu(x, wg, wu, out=None, saved=None, recompute: bool = False, workspace=
     if stream is not None and isinstance(x, torch.Tensor):
         with on_stream(stream, x):
             return moe_glu(x, wg, wu, out, saved, recompute, workspace)
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, wg, wu)):
+    if torch.is_grad_enabled() and (_wants(x) or _wants(wg) or _wants(wu)):
         if out is not None or saved is not None:
             raise RuntimeError("moe_glu: given output tensors carry no gradient, but an input requires one")
         return _GluFunction.apply(x, wg, wu, recompute, workspace)
@@ -119,8 +122,8 @@ def moe_glu(x, wg, wu, out=None, saved=None, recompute: bool = False, workspace=
 def _backward(x, wg, wu, dh, saved, dx, dwg, dwu, workspace, need_x, need_w):
     head, T, H, I = _operands(x, wg, wu)
     dev = x.device
-    ep, lde = matrix(dh, (x.dtype,), "dh")
-    if dh.shape != (T, I) or dh.device != dev:
+    ep, lde, given = plane(dh, (x.dtype,), "dh")
+    if given != (T, I) or dh.device != dev:
         raise ValueError(f"dh must be [{T}, {I}] on {dev}")
     sp = 0 if saved is None else array(saved, torch.float32, (2, T, I), "saved", dev)
     dp = ldd = gp = up = 0

@@ -8,69 +8,76 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, matrix, new, on_stream
+from ._args import DTYPES, array, call, current_handle, new, on_stream, plane
 from .router import _not_captured
 
 F8 = torch.float8_e4m3fn
+_F8S = (F8,)
+_TYPES = tuple(DTYPES)
 
 
 def _weight(weight, H, device):
     """(pointer, MOE_Q4_DTYPE_*) of a norm's weight, or (0, 0)."""
     if weight is None:
         return 0, 0
-    return array(weight, tuple(DTYPES), (H,), "weight", device), DTYPES[weight.dtype]
+    return array(weight, _TYPES, (H,), "weight", device), DTYPES[weight.dtype]
 
 
-def _like(t, out, dtypes, name):
+def _like(t, shape, out, dtypes, name):
     """(tensor, pointer, row stride) of a matrix of t's shape and device, made here where none is given."""
     if out is None:
-        T, H = t.shape
-        out = new((T, H), (H, 1), dtypes[0], t.device)
-        return out, out.data_ptr(), H
-    p, ld = matrix(out, dtypes, name)
-    if out.shape != t.shape or out.device != t.device:
-        raise ValueError(f"{name} must be {list(t.shape)} on {t.device}")
+        out = new(shape, (shape[1], 1), dtypes[0], t.device)
+        return out, out.data_ptr(), shape[1]
+    p, ld, given = plane(out, dtypes, name)
+    if given != shape or out.device != t.device:
+        raise ValueError(f"{name} must be {list(shape)} on {t.device}")
     return out, p, ld
 
 
 def _norm(x, weight, residual, eps, total, y, want_y, codes, scales, want_codes, where):
-    xp, ldx = matrix(x, DTYPES, "x")
-    T, H = x.shape
+    xp, ldx, shape = plane(x, _TYPES, "x")
+    T, H = shape
     dev = x.device
+    xt = x.dtype
     wp, wd = _weight(weight, H, dev)
     rp = ldr = rd = tp = ldt = 0
     if residual is not None:
-        rp, ldr = matrix(residual, (x.dtype, torch.float32), "residual")
-        if residual.shape != x.shape or residual.device != dev:
+        rt = residual.dtype if isinstance(residual, torch.Tensor) else None
+        rp, ldr, given = plane(residual, (xt, torch.float32), "residual")
+        if given != shape or residual.device != dev:
             raise ValueError("residual must have the shape and device of x")
-        rd = DTYPES[residual.dtype]
-        total, tp, ldt = _like(x, total, (residual.dtype,), "total")
+        rd = DTYPES[rt]
+        total, tp, ldt = _like(x, shape, total, (rt,), "total")
     elif total is not None:
         raise ValueError("total without a residual")
     yp = yd = ldy = cp = ldc = sp = 0
     if want_y:
-        y, yp, ldy = _like(x, y, want_y, "out")
+        y, yp, ldy = _like(x, shape, y, want_y, "out")
         yd = DTYPES[y.dtype]
     if want_codes:
-        codes, cp, ldc = _like(x, codes, (F8,), "codes")
+        codes, cp, ldc = _like(x, shape, codes, _F8S, "codes")
         G = (H + 127) // 128
         if scales is None:
             scales = new((T, G), (G, 1), torch.float32, dev)
             sp = scales.data_ptr()
         else:
             sp = array(scales, torch.float32, (T, G), "scales", dev)
-    args = (xp, DTYPES[x.dtype], ldx, rp, rd, ldr, wp, wd, T, H, eps, tp, ldt, yp, yd, ldy, cp, ldc, sp)
-    st = call(_q.lib().moe_rms_norm, args, dev, current_handle(dev))
+    st = call(_q.lib().moe_rms_norm, (xp, DTYPES[xt], ldx, rp, rd, ldr, wp, wd, T, H, eps, tp, ldt, yp, yd, ldy, cp, ldc, sp), dev,
+              current_handle(dev))
     if st:
         raise _q.MoeQ4Error(st, where)
     return y, total, codes, scales
+
+
+def _wants(t) -> bool:
+    return isinstance(t, torch.Tensor) and t.requires_grad
 
 
 def _out_types(x, out, out_dtype):
     if out is not None:
         if out_dtype not in (None, out.dtype):
             raise ValueError("out is not of out_dtype")
-        return tuple(DTYPES)
+        return _TYPES
     od = x.dtype if out_dtype is None else out_dtype
     if od not in DTYPES:
         raise TypeError(f"out_dtype {od} is not one of {tuple(DTYPES)}")
@@ -119,7 +126,7 @@ def moe_rms_norm(x, weight=None, residual=None, eps: float = 1e-6, total=None, o
     if stream is not None and isinstance(x, torch.Tensor):
         with on_stream(stream, x):
             return moe_rms_norm(x, weight, residual, eps, total, out, out_dtype)
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, weight, residual)):
+    if torch.is_grad_enabled() and (_wants(x) or _wants(weight) or _wants(residual)):
         if total is not None or out is not None:
             raise RuntimeError("moe_rms_norm: given output tensors carry no gradient, but an input requires one")
         return _NormFunction.apply(x, weight, residual, eps, out_dtype)
@@ -145,19 +152,19 @@ def moe_rms_norm_backward_workspace_bytes(T: int, H: int) -> int:
 
 
 def _back(total, weight, dy, dtotal, eps, dx, dweight, workspace, want_dweight):
-    rp, ldr = matrix(total, DTYPES, "total")
-    T, H = total.shape
+    rp, ldr, shape = plane(total, _TYPES, "total")
+    T, H = shape
     dev = total.device
     wp, wd = _weight(weight, H, dev)
-    yp, ldy = matrix(dy, DTYPES, "dy")
-    if dy.shape != total.shape or dy.device != dev:
+    yp, ldy, given = plane(dy, _TYPES, "dy")
+    if given != shape or dy.device != dev:
         raise ValueError("dy must have the shape and device of total")
     tp = ldt = 0
     if dtotal is not None:
-        tp, ldt = matrix(dtotal, (total.dtype,), "dtotal")
-        if dtotal.shape != total.shape or dtotal.device != dev:
+        tp, ldt, given = plane(dtotal, (total.dtype,), "dtotal")
+        if given != shape or dtotal.device != dev:
             raise ValueError("dtotal must have the shape and device of total")
-    dx, dp, ldd = _like(total, dx, (total.dtype,), "dx")
+    dx, dp, ldd = _like(total, shape, dx, (total.dtype,), "dx")
     gp = wsp = wsn = 0
     if dweight is not None and not want_dweight:
         raise ValueError("dweight without a weight")
@@ -202,13 +209,13 @@ def moe_quantize_fp8(x, block_rows: int = 1, codes=None, scales=None, stream=Non
     if stream is not None and isinstance(x, torch.Tensor):
         with on_stream(stream, x):
             return moe_quantize_fp8(x, block_rows, codes, scales)
-    xp, ldx = matrix(x, DTYPES, "x")
-    T, K = x.shape
+    xp, ldx, given = plane(x, _TYPES, "x")
+    T, K = given
     dev = x.device
     rows = int(block_rows)
     if rows not in (1, 128):
         raise ValueError(f"block_rows {block_rows} is neither 1 nor 128")
-    codes, cp, ldc = _like(x, codes, (F8,), "codes")
+    codes, cp, ldc = _like(x, given, codes, _F8S, "codes")
     shape = ((T + rows - 1) // rows, (K + 127) // 128)
     if scales is None:
         scales = new(shape, (shape[1], 1), torch.float32, dev)
