@@ -144,18 +144,32 @@ __device__ __forceinline__ void gemm_copy(const unsigned char* from, unsigned ch
 // before each and store(place, acc) behind it.  kbytes, a multiple of 16, is a
 // row's length.
 //
-// LDS holds two steps of all rows, 128 bytes each.  Chunk c of row r lies at
+// LDS holds BUFFERS steps of all rows, 128 bytes each.  Chunk c of row r lies at
 // place c ^ (r / 2 % 8), so that the 16 rows that are read together fall in
 // different banks (of 64).  A wave's 32 x 32 x 16 instructions go through half
 // a step (its chunks 0 to 3 or 4 to 7) at a time, while the next half's
 // operands are on their way into registers; so the waves have read a step when
 // its second half begins, meet there, once a step, and that half carries the
-// copies of the step after the next into the LDS that became free.  Four waves
+// copies of the step BUFFERS on into the LDS that became free.  Four waves
 // of 128 x 128 results each: their sums fill the accumulator registers, and
 // they read two thirds of what eight of 128 x 64 would.  (16 x 16 x 32
 // instructions read twice the registers, and behind each one's 16 clocks a
 // copy's issue, about 30, shows.)
-template <class S, class Source, class Store>
+//
+// Two buffers are enough where a step's instructions take 2048 clocks.  Small
+// tiles have more, since what is on its way must last a memory's latency, about
+// 2000 clocks; there the steps go BUFFERS at a time, past the last one with
+// zeros: the compiler must see what is on its way at each read, and where a
+// loop ends in several places it waits for all of it.
+// LDS buffers of a shape's 16-bit steps: as many as one workgroup a compute
+// unit leaves room for.  A tile of 128 x 128 takes 0.47 us a step with four and
+// 0.86 with two workgroups of two buffers, one of 256 x 256 is bound by its
+// products with two.
+template <class S>
+__host__ __device__ constexpr int gemm_buffers() {
+  return S::kTok == 256 ? 2 : S::kRows > 128 ? 3 : 4;
+}
+template <class S, int BUFFERS, class Source, class Store>
 __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, Source& source, Store store) {
   constexpr int MT = S::MT, NT = S::NT, KIND = S::KIND, kPass = S::kThreads / 8;
   constexpr int kCb = S::kRows / kPass, kCt = S::kTok / kPass, kCopies = kCb + kCt;
@@ -164,8 +178,13 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, S
   constexpr int kSlots = (kMul + kPer - 1) / kPer > kLeast ? (kMul + kPer - 1) / kPer : kLeast;
   static_assert(S::kRows % kPass == 0 && S::kTok % kPass == 0 && kPass % 16 == 0, "copies of whole passes");
   // each an object of its own: the compiler then knows that reads of one do not wait for copies into another
-  __shared__ __attribute__((aligned(1024))) unsigned char b0[S::kRows * kGemmStep], b1[S::kRows * kGemmStep];
-  __shared__ __attribute__((aligned(1024))) unsigned char t0[S::kTok * kGemmStep], t1[S::kTok * kGemmStep];
+  __shared__ __attribute__((aligned(1024))) unsigned char b0[S::kRows * kGemmStep], b1[S::kRows * kGemmStep], b2[S::kRows * kGemmStep],
+      b3[S::kRows * kGemmStep];
+  __shared__ __attribute__((aligned(1024))) unsigned char t0[S::kTok * kGemmStep], t1[S::kTok * kGemmStep], t2[S::kTok * kGemmStep],
+      t3[S::kTok * kGemmStep];
+  static_assert(BUFFERS >= 2 && BUFFERS <= 4, "as many of them are used");
+  auto rows_of = [&](int i) __attribute__((always_inline)) { return i == 0 ? b0 : i == 1 ? b1 : i == 2 ? b2 : b3; };
+  auto toks_of = [&](int i) __attribute__((always_inline)) { return i == 0 ? t0 : i == 1 ? t1 : i == 2 ? t2 : t3; };
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n32 = lane & 31, kh = lane >> 5;
   const int wm = wave % S::WM, wn = wave / S::WM;
@@ -178,20 +197,20 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, S
   uint32_t off[kCopies], k = 0, live = 0;
   auto place = [&](int i) __attribute__((always_inline)) {
     k = min((at.step0 + i) * kGemmStep + chunk, kbytes - 16);  // (past the end: never used)
-    live = i < at.count ? ~0u : 0u;                            // past the last step: all of one place
+    live = i < at.count + BUFFERS - 2 ? ~0u : 0u;              // past the last step: all of one place
   };
   auto copy = [&](int to, int c) __attribute__((always_inline)) {
-    unsigned char* lds = (c < kCb ? (to ? b1 : b0) + c * kPass * kGemmStep : (to ? t1 : t0) + (c - kCb) * kPass * kGemmStep) + wave * 1024;
+    unsigned char* lds = (c < kCb ? rows_of(to) + c * kPass * kGemmStep : toks_of(to) + (c - kCb) * kPass * kGemmStep) + wave * 1024;
     gemm_copy((c < kCb ? source.row_base(c * kPass + tid / 8) : source.tok) + ((off[c] + k) & live), lds);
   };
-  auto start = [&]() __attribute__((always_inline)) {  // the next tile and its first two steps
+  auto start = [&]() __attribute__((always_inline)) {  // the next tile and its first steps
     at = queue.take(tiles);
     source.set(at);
     const int mine = gemm_opaque(tid / 8);
 #pragma unroll
     for (int c = 0; c < kCopies; ++c) off[c] = c < kCb ? source.row_off(c * kPass + mine) : source.tok_off((c - kCb) * kPass + mine);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < BUFFERS; ++i) {
       place(i);
 #pragma unroll
       for (int c = 0; c < kCopies; ++c) copy(i, c);
@@ -203,9 +222,9 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, S
   auto read = [&](int from, int h, int j) __attribute__((always_inline)) {
     const int s = j / (MT + NT), r = j % (MT + NT), flip = 64 * h + 32 * s;
     if (r < NT)
-      w[h][s][r] = *reinterpret_cast<const gemm_i32x4*>((from ? b1 : b0) + (row_at ^ flip) + r * 32 * kGemmStep);
+      w[h][s][r] = *reinterpret_cast<const gemm_i32x4*>(rows_of(from) + (row_at ^ flip) + r * 32 * kGemmStep);
     else
-      x[h][s][r - NT] = *reinterpret_cast<const gemm_i32x4*>((from ? t1 : t0) + (tok_at ^ flip) + (r - NT) * 32 * kGemmStep);
+      x[h][s][r - NT] = *reinterpret_cast<const gemm_i32x4*>(toks_of(from) + (tok_at ^ flip) + (r - NT) * 32 * kGemmStep);
   };
   auto multiply = [&](int h, int j) __attribute__((always_inline)) {
     const int s = j / (MT * NT), mt = j % (MT * NT) / NT, nt = j % NT;
@@ -228,7 +247,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, S
     }
   };
   auto cut = [&](int h, int i) __attribute__((always_inline)) {  // past the rows' end: one operand's zeros
-    const int left = kbytes - (now.step0 + i) * kGemmStep - h * 64;
+    const int left = i < now.count ? kbytes - (now.step0 + i) * kGemmStep - h * 64 : 0;
     if (left < 64) {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
@@ -242,7 +261,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, S
   start();
   while (true) {
     now = at;
-    gemm_meet<0>();
+    gemm_meet<(BUFFERS - 1) * kCopies>();  // the first step is there
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -256,21 +275,33 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, S
     cut(0, 0);
     pass(0, 0, -1);
     cut(1, 0);
-    gemm_meet<0>();
+    constexpr int kOnWay = (BUFFERS - 2) * kCopies;  // copies of later steps than the next
+    gemm_meet<kOnWay>();
     int i = 0;
     auto body = [&](int buf) __attribute__((always_inline)) {
-      place(i + 2);
-      pass(1, buf ^ 1, buf);
+      const int next = (buf + 1) % BUFFERS;
+      place(i + BUFFERS);
+      pass(1, next, buf);
       ++i;
       cut(0, i);
-      pass(0, buf ^ 1, -1);
+      pass(0, next, -1);
       cut(1, i);
-      gemm_meet<0>();
+      gemm_meet<kOnWay>();
     };
-    while (i + 1 < now.count) {
-      body(0);
-      if (i + 1 >= now.count) break;
-      body(1);
+    if constexpr (BUFFERS == 2) {
+      while (i + 1 < now.count) {
+        body(0);
+        if (i + 1 >= now.count) break;
+        body(1);
+      }
+    } else {
+      while (i + 1 < now.count) {
+        body(0);
+        body(1);
+        body(2);
+        if constexpr (BUFFERS > 3) body(3);
+      }
+      gemm_meet<0>();  // nothing is on its way into the next tile's LDS
     }
     // the last half step, from registers; the LDS is the next tile's
     const bool more = queue.any();

@@ -7,35 +7,48 @@
 
 namespace moeq4 {
 
-constexpr int kGemm256x256 = 0, kGemm256x192 = 1, kGemm128x128 = 2, kGemm64x128 = 3;
+// Tile shapes, tokens x rows.
+constexpr int kGemm256x256 = 0, kGemm256x192 = 1, kGemm128x256 = 2, kGemm128x192 = 3, kGemm128x128 = 4, kGemm64x128 = 5, kGemmShapes = 6;
 
 struct GemmPlan {
   int shape, workgroups;
   GemmTiles tiles;
 };
 
-// For M x N results over `steps` steps, with the shapes of `mask` (bits by number).
-inline GemmPlan gemm_plan(int M, int N, int steps, int mask) {
-  static const int kTok[4] = {256, 256, 128, 64}, kRows[4] = {256, 192, 128, 128};
-  static const float kStep[4] = {1.3f, 1.05f, 0.8f, 0.6f};  // us of a step, workgroups that run at once
-  static const int kAtOnce[4] = {256, 256, 512, 768};
+// What a tile of each shape takes, in us: a step of 128 bytes of K where a
+// compute unit has one workgroup, what each further one adds to it, the tile's
+// beginning and end; and how many workgroups a unit holds (0: no such shape).
+struct GemmCosts {
+  float step[kGemmShapes], more[kGemmShapes], end[kGemmShapes];
+  int held[kGemmShapes];
+};
+// 16-bit products, measured with 256 and 1024 tiles of 8, 32 and 128 steps.
+constexpr GemmCosts kGemmCosts16 = {{1.49f, 1.28f, 0.82f, 0.635f, 0.466f, 0.304f}, {}, {5.8f, 3.5f, 7.0f, 5.9f, 3.7f, 2.5f}, {1, 1, 1, 1, 1, 1}};
+
+// For M x N results over `steps` steps: the shape and the split of K with the
+// least sum.  Splits fill the card where the tiles do not; their sums go
+// through memory (8 bytes a result and split at 5 TB/s) and a launch.
+inline GemmPlan gemm_plan(const GemmCosts& costs, int M, int N, int steps) {
+  static const int kTok[kGemmShapes] = {256, 256, 128, 128, 128, 64}, kRows[kGemmShapes] = {256, 192, 256, 192, 128, 128};
   GemmPlan best{};
   float least = 0.0f;
-  for (int i = 0; i < 4; ++i) {
-    if (!(mask >> i & 1)) continue;
+  for (int i = 0; i < kGemmShapes; ++i) {
+    const int held = costs.held[i];
+    if (!held) continue;
     const long tt = (M + kTok[i] - 1) / kTok[i], rt = (N + kRows[i] - 1) / kRows[i], tiles = tt * rt;
-    int tried = 0;
-    for (int fill = 0; fill <= kAtOnce[i]; fill += 256) {
-      const int s = (int)std::max(1L, std::min<long>(std::min(16, steps / 4), fill / tiles));
+    long tried = 0;
+    for (int fill = 0; fill <= held; ++fill) {
+      const long s = std::max(1L, std::min<long>(std::min(16, steps / 4), 256L * fill / tiles));
       if (s == tried) continue;
       tried = s;
-      const int per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
-      const long n = tiles * splits, rounds = (n + kAtOnce[i] - 1) / kAtOnce[i];
-      float us = (float)rounds * ((float)per * kStep[i] + 3.0f);
-      if (splits > 1) us += 2.5f + (float)splits * (float)M * (float)N * (8.0f / 6e6f);
+      const int per = (int)((steps + s - 1) / s), splits = (steps + per - 1) / per;
+      const long n = tiles * splits, rounds = n / (256L * held), rest = (n - rounds * 256 * held + 255) / 256;
+      const auto round = [&](long together) { return together ? (float)per * (costs.step[i] + (float)(together - 1) * costs.more[i]) + costs.end[i] : 0.0f; };
+      float us = (float)rounds * round(held) + round(rest);
+      if (splits > 1) us += 3.0f + (float)splits * (float)M * (float)N * (8.0f / 5e6f);
       if (least == 0.0f || us < least) {
         least = us;
-        best = GemmPlan{i, (int)std::min<long>(n, kAtOnce[i]), GemmTiles{(int)tt, (int)rt, splits, per, steps}};
+        best = GemmPlan{i, (int)std::min<long>(n, 256L * held), GemmTiles{(int)tt, (int)rt, splits, per, steps}};
       }
     }
   }

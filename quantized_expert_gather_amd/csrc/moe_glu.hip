@@ -43,7 +43,7 @@ int glu_status(int T, int H, int I) {
 
 bool glu_by_rows(int T) { return T <= 32; }
 int glu_steps(long k) { return (int)((2 * k + kGemmStep - 1) / kGemmStep); }
-GemmPlan glu_forward_plan(int T, int H, int I) { return gemm_plan(T, 2 * I, glu_steps(H), ~0); }
+GemmPlan glu_forward_plan(int T, int H, int I) { return gemm_plan(kGemmCosts16, T, 2 * I, glu_steps(H)); }
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
 size_t glu_forward_part(int T, int H, int I) {
@@ -60,8 +60,8 @@ struct GluBackLayout {
 GluBackLayout glu_back_layout(int T, int H, int I, bool saved) {
   GluBackLayout w{};
   w.Tp = (T + 63) / 64 * 64;
-  w.dx = gemm_plan(T, H, glu_steps(2L * I), ~0);
-  w.dw = gemm_plan(2 * I, H, glu_steps(w.Tp), ~0);
+  w.dx = gemm_plan(kGemmCosts16, T, H, glu_steps(2L * I));
+  w.dw = gemm_plan(kGemmCosts16, 2 * I, H, glu_steps(w.Tp));
   size_t off = 0;
   w.gu = off; off = round256(off + (saved ? 0 : (size_t)2 * T * I * 4));
   w.d = off; off = round256(off + (size_t)T * 2 * I * 2);

@@ -97,7 +97,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_glu_tiles(GluArgs a) {
   typedef typename GluType<KIND>::type T16;
   static_assert(S::kThreads / 8 == 32, "GluSource's rows");
   GluSource<S> source{a};
-  gemm_tiles<S>(a.tiles, 2 * a.H, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
+  gemm_tiles<S, gemm_buffers<S>()>(a.tiles, 2 * a.H, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63);
     const int place = gemm_place4(lane), t0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 15);
     const int n0 = p.row * (S::kRows / 2) + wave / WM * NT * 16;
@@ -233,7 +233,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_glu_mm(GluMmArgs a) {
   using S = GemmShape<KIND, MT, NT, WM, WN>;
   typedef typename GluType<KIND>::type T16;
   GluMmSource<S> source{a};
-  gemm_tiles<S>(a.tiles, a.kbytes, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
+  gemm_tiles<S, gemm_buffers<S>()>(a.tiles, a.kbytes, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63);
     const int place = gemm_place4(lane), m0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 15);
     const int n0 = p.row * S::kRows + wave / WM * NT * 32;
@@ -345,6 +345,8 @@ int glu_forward_kind(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t
   switch (p.shape) {
     case kGemm256x256: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
     case kGemm256x192: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x256: hipLaunchKernelGGL((k_glu_tiles<KIND, 2, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x192: hipLaunchKernelGGL((k_glu_tiles<KIND, 2, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
     case kGemm128x128: hipLaunchKernelGGL((k_glu_tiles<KIND, 2, 2, 2, 2>), grid, dim3(256), 0, stream, a); break;
     default: hipLaunchKernelGGL((k_glu_tiles<KIND, 2, 1, 1, 4>), grid, dim3(256), 0, stream, a); break;
   }
@@ -362,6 +364,8 @@ int glu_mm_kind(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream) {
   switch (p.shape) {
     case kGemm256x256: hipLaunchKernelGGL((k_glu_mm<KIND, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
     case kGemm256x192: hipLaunchKernelGGL((k_glu_mm<KIND, 4, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x256: hipLaunchKernelGGL((k_glu_mm<KIND, 2, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x192: hipLaunchKernelGGL((k_glu_mm<KIND, 2, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
     case kGemm128x128: hipLaunchKernelGGL((k_glu_mm<KIND, 2, 2, 2, 2>), grid, dim3(256), 0, stream, a); break;
     default: hipLaunchKernelGGL((k_glu_mm<KIND, 2, 1, 1, 4>), grid, dim3(256), 0, stream, a); break;
   }
