@@ -194,14 +194,13 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, S
 
   GemmQueue queue(tiles);
   GemmPlace at, now;
-  uint32_t off[kCopies], k = 0, live = 0;
+  uint32_t off[kCopies], k = 0;
   auto place = [&](int i) __attribute__((always_inline)) {
-    k = min((at.step0 + i) * kGemmStep + chunk, kbytes - 16);  // (past the end: never used)
-    live = i < at.count + BUFFERS - 2 ? ~0u : 0u;              // past the last step: all of one place
+    k = min((at.step0 + min(i, at.count - 1)) * kGemmStep + chunk, kbytes - 16);  // (past the end: of the same rows)
   };
   auto copy = [&](int to, int c) __attribute__((always_inline)) {
     unsigned char* lds = (c < kCb ? rows_of(to) + c * kPass * kGemmStep : toks_of(to) + (c - kCb) * kPass * kGemmStep) + wave * 1024;
-    gemm_copy((c < kCb ? source.row_base(c * kPass + tid / 8) : source.tok) + ((off[c] + k) & live), lds);
+    gemm_copy((c < kCb ? source.row_base(c * kPass + tid / 8) : source.tok) + (off[c] + k), lds);
   };
   auto start = [&]() __attribute__((always_inline)) {  // the next tile and its first steps
     at = queue.take(tiles);
@@ -246,14 +245,17 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, S
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto cut = [&](int h, int i) __attribute__((always_inline)) {  // past the rows' end: one operand's zeros
+  auto cut = [&](int h, int i) __attribute__((always_inline)) {  // past the rows' end: zeros
     const int left = i < now.count ? kbytes - (now.step0 + i) * kGemmStep - h * 64 : 0;
     if (left < 64) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < 2; ++s) {
+        if (kh * 16 + s * 32 < left) continue;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          if (kh * 16 + s * 32 >= left) w[h][s][nt] = gemm_i32x4{0, 0, 0, 0};
+        for (int nt = 0; nt < NT; ++nt) w[h][s][nt] = gemm_i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) x[h][s][mt] = gemm_i32x4{0, 0, 0, 0};
+      }
     }
   };
 
@@ -347,16 +349,16 @@ __device__ __forceinline__ void gemm_tiles_scaled(const GemmTiles& tiles, int kb
 
   GemmQueue queue(tiles);
   GemmPlace at;
-  uint32_t off_b[kCb], off_t[2][kCh], k = 0, live = 0;
+  uint32_t off_b[kCb], off_t[2][kCh], k = 0;
   auto place = [&](int i) __attribute__((always_inline)) {
-    k = min((at.step0 + i) * kGemmStep + chunk, kbytes - 16);  // (past the end: never used, or times zeros)
-    live = i <= at.count ? ~0u : 0u;
+    // past the end: of the same rows, since a NaN times zero stays one
+    k = min((at.step0 + min(i, at.count - 1)) * kGemmStep + chunk, kbytes - 16);
   };
   auto copy_lo = [&](int to, int c) __attribute__((always_inline)) {
     if (c < kCb)
-      gemm_copy(source.row_base(c * kPass + tid / 8) + ((off_b[c] + k) & live), (to ? b1 : b0) + c * kPass * kGemmStep + wave * 1024);
+      gemm_copy(source.row_base(c * kPass + tid / 8) + (off_b[c] + k), (to ? b1 : b0) + c * kPass * kGemmStep + wave * 1024);
     else
-      gemm_copy(source.tok + ((off_t[0][c - kCb] + k) & live), (to ? lo1 : lo0) + (c - kCb) * kPass * kGemmStep + wave * 1024);
+      gemm_copy(source.tok + (off_t[0][c - kCb] + k), (to ? lo1 : lo0) + (c - kCb) * kPass * kGemmStep + wave * 1024);
   };
   auto copy_scales = [&](int i, int to) __attribute__((always_inline)) {
     if (tid < S::kTok + S::kScaleRows)
@@ -364,7 +366,7 @@ __device__ __forceinline__ void gemm_tiles_scaled(const GemmTiles& tiles, int kb
                                        (__attribute__((address_space(3))) void*)((to ? scale1 : scale0) + wave * 64), 4, 0, 0);
   };
   auto copy_hi = [&](int to, int c) __attribute__((always_inline)) {
-    gemm_copy(source.tok + ((off_t[1][c] + k) & live), (to ? hi1 : hi0) + c * kPass * kGemmStep + wave * 1024);
+    gemm_copy(source.tok + (off_t[1][c] + k), (to ? hi1 : hi0) + c * kPass * kGemmStep + wave * 1024);
   };
   auto copy_all = [&](int i) __attribute__((always_inline)) {
     place(i);
@@ -548,9 +550,11 @@ __device__ __forceinline__ void gemm_rows(const unsigned char* const (&row)[J], 
     for (int u = 0; u < U; ++u) {
       const int step = s + u * stride;
       if (step >= steps) break;
-      if (step * kGemmStep + at >= kbytes) {  // past the rows' end: one operand's zeros
+      if (step * kGemmStep + at >= kbytes) {  // past the rows' end: zeros
 #pragma unroll
         for (int j = 0; j < J; ++j) w[u][j] = gemm_i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < G; ++g) x[u][g] = gemm_i32x4{0, 0, 0, 0};
       }
       float ws = 1.0f;
       if constexpr (gemm_scaled(KIND)) ws = sw[step];

@@ -84,6 +84,21 @@ def test_nan_codes_and_scales_stay_with_their_outputs(L):
     R.check(got[rows][:, 128:299], ref[rows][:, 128:299], bound[rows][:, 128:299])
 
 
+@pytest.mark.parametrize("L,N,K", [(4, 300, 144), (30, 4096, 656), (200, 300, 144), (200, 300, 640), (600, 2600, 400), (1300, 2600, 656)])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_a_first_rows_nan_stays_with_it(L, N, K, out):
+    """Odd numbers of steps, and rows that end inside one: what stands in for the rest is no other row's."""
+    x, sx, w, sw = (t.cuda() for t in problem(L, N, K)[:4])
+    clean = q.moe_linear_fp8_forward(x, sx, w, sw, out_dtype=out)
+    bad, wbad = x.clone(), w.clone()
+    bad.view(torch.uint8)[0] = 0x7F
+    wbad.view(torch.uint8)[0] = 0xFF
+    got = q.moe_linear_fp8_forward(bad, sx, w, sw, out_dtype=out)
+    assert torch.isnan(got[0]).all() and torch.equal(got[1:], clean[1:])
+    got = q.moe_linear_fp8_forward(x, sx, wbad, sw, out_dtype=out)
+    assert torch.isnan(got[:, 0]).all() and torch.equal(got[:, 1:], clean[:, 1:])
+
+
 def test_zero_and_subnormal_codes():
     x, sx, w, sw, _ = problem(40, 64, 256)
     x = (x.float() / 2 ** 13).to(R.F8)  # mostly subnormal

@@ -133,6 +133,34 @@ def test_infinities_and_nan_stay_with_their_rows(T):
     R.check(got[rows][:, :63], h[rows][:, :63], bh[rows][:, :63])
 
 
+@pytest.mark.parametrize("T,H,I", [(6, 72, 64), (140, 72, 64), (140, 200, 520), (1500, 328, 1400), (2600, 136, 2600)])
+@pytest.mark.parametrize("odd", [float("nan"), float("inf")])
+def test_a_first_rows_nan_or_infinity_stays_with_it(T, H, I, odd):
+    """Odd numbers of steps, and rows that end inside one: what stands in for the rest is no other row's."""
+    x, wg, wu, dh = (t.cuda() for t in problem(T, H, I, F16))
+    clean = q.moe_glu(x, wg, wu)
+    dclean = q.moe_glu_backward(x, wg, wu, dh)[0]
+    bad, dbad = x.clone(), dh.clone()
+    bad[0], dbad[0, :] = odd, odd
+    got, dx = q.moe_glu(bad, wg, wu), q.moe_glu_backward(x, wg, wu, dbad)[0]
+    assert torch.equal(got[1:], clean[1:]) and torch.equal(dx[1:], dclean[1:])
+    assert not torch.isfinite(got[0]).all() and not torch.isfinite(dx[0]).any()
+    w = wg.clone()
+    w[0] = odd
+    assert torch.equal(q.moe_glu(x, w, wu)[:, 1:], clean[:, 1:])
+
+
+@pytest.mark.parametrize("T", [3, 90])
+def test_an_infinity_gives_one(T):
+    """The last inputs of rows that end inside a step: inf times a weight, not inf times zero."""
+    x, wg, wu, _ = problem(T, 72, 64, BF16)
+    x[1] = 0
+    x[1, 71] = float("inf")
+    wg[:, 71], wu[:, 71] = 1, 2
+    got = q.moe_glu(x.cuda(), wg.cuda(), wu.cuda()).cpu()
+    assert (got[1] == float("inf")).all() and torch.isfinite(got[0]).all() and torch.isfinite(got[2:]).all()
+
+
 def test_large_gates():
     x, wg, wu, dh = problem(70, 64, 64, BF16)
     x = x * 60  # gates of a few hundred: the sigmoid is 0 or 1
