@@ -141,26 +141,38 @@ __device__ __forceinline__ void gemm_copy(const unsigned char* from, unsigned ch
 // threads have those of each 128 of B's rows.
 
 // Products of 16-bit numbers: runs the workgroup's tiles, source.set(place)
-// before each and store(place, acc) behind it.  kbytes, a multiple of 16, is a
-// row's length.
+// before each and store(place, acc) behind it.
+//
+// A source says for each operand whether its memory has the sum's axis along
+// its rows (as above; step s begins at byte source.k(s)) or across them
+// (kTokT, kRowT): then chunk c of 8 of the tile's tokens lies at column
+// tok_col(c), in bytes, of rows tok_ld apart, the step's 64 from tok_at(s) on;
+// columns past the operand's end at some within.  source.left(s) is the number
+// of bytes along the sum's axis from step s on, above 0; a multiple of 16
+// where an operand has that axis along its rows.
 //
 // LDS holds BUFFERS steps of all rows, 128 bytes each.  Chunk c of row r lies at
 // place c ^ (r / 2 % 8), so that the 16 rows that are read together fall in
-// different banks (of 64).  A wave's 32 x 32 x 16 instructions go through half
-// a step (its chunks 0 to 3 or 4 to 7) at a time, while the next half's
-// operands are on their way into registers; so the waves have read a step when
-// its second half begins, meet there, once a step, and that half carries the
-// copies of the step BUFFERS on into the LDS that became free.  Four waves
-// of 128 x 128 results each: their sums fill the accumulator registers, and
-// they read two thirds of what eight of 128 x 64 would.  (16 x 16 x 32
-// instructions read twice the registers, and behind each one's 16 clocks a
-// copy's issue, about 30, shows.)
+// different banks (of 64).  Of an operand with the axis across, it holds the
+// step's 64 rows of 128 bytes (64 tokens) one after another, then the next
+// tokens'; 16 lanes read 4 rows of 32 bytes and get a column of them each
+// (ds_read_b64_tr_b16), 32 lanes 4 rows of 64 bytes, whose halves are swapped
+// in each second pair of rows, for the banks again.
+// A wave's 32 x 32 x 16 instructions go through half a step (its chunks 0 to 3
+// or 4 to 7) at a time, while the next half's operands are on their way into
+// registers; so the waves have read a step when its second half begins, meet
+// there, once a step, and that half carries the copies of the step BUFFERS on
+// into the LDS that became free.  Four waves of 128 x 128 results each: their
+// sums fill the accumulator registers, and they read two thirds of what eight
+// of 128 x 64 would.  (16 x 16 x 32 instructions read twice the registers, and
+// behind each one's 16 clocks a copy's issue, about 30, shows.)
 //
 // Two buffers are enough where a step's instructions take 2048 clocks.  Small
 // tiles have more, since what is on its way must last a memory's latency, about
 // 2000 clocks; there the steps go BUFFERS at a time, past the last one with
 // zeros: the compiler must see what is on its way at each read, and where a
 // loop ends in several places it waits for all of it.
+
 // LDS buffers of a shape's 16-bit steps: as many as one workgroup a compute
 // unit leaves room for.  A tile of 128 x 128 takes 0.47 us a step with four and
 // 0.86 with two workgroups of two buffers, one of 256 x 256 is bound by its
@@ -169,14 +181,23 @@ template <class S>
 __host__ __device__ constexpr int gemm_buffers() {
   return S::kTok == 256 ? 2 : S::kRows > 128 ? 3 : 4;
 }
-template <class S, int BUFFERS, class Source, class Store>
-__device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, Source& source, Store store) {
+
+// Four 16-bit numbers of a column: the 16 lanes' 8 bytes each, 4 rows of 4 lanes.
+__device__ __forceinline__ uint2 gemm_read_column(const unsigned char* lds) {
+  typedef short s4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)lds));
+}
+
+template <class S, class Source, class Store>
+__device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, Source& source, Store store) {
+  constexpr int BUFFERS = gemm_buffers<S>();
+  constexpr bool kTokT = Source::kTokT, kRowT = Source::kRowT;
   constexpr int MT = S::MT, NT = S::NT, KIND = S::KIND, kPass = S::kThreads / 8;
   constexpr int kCb = S::kRows / kPass, kCt = S::kTok / kPass, kCopies = kCb + kCt;
-  constexpr int kReads = 2 * (MT + NT), kMul = 2 * MT * NT;           // of half a step
-  constexpr int kLeast = kReads > kCopies ? kReads : kCopies, kPer = kMul > kLeast ? kMul / kLeast : 1;
-  constexpr int kSlots = (kMul + kPer - 1) / kPer > kLeast ? (kMul + kPer - 1) / kPer : kLeast;
-  static_assert(S::kRows % kPass == 0 && S::kTok % kPass == 0 && kPass % 16 == 0, "copies of whole passes");
+  constexpr int kReadsX = kTokT ? 2 * MT : MT, kReadsW = kRowT ? 2 * NT : NT;
+  constexpr int kReads = 2 * (kReadsX + kReadsW), kMul = 2 * MT * NT;  // of half a step
+  constexpr int kEarly = kMul * 5 / 8;  // instructions that the reads are spread over: the last have a latency's time
+  static_assert(S::kRows % 64 == 0 && S::kTok % 64 == 0 && kPass == 32, "copies of whole passes");
   // each an object of its own: the compiler then knows that reads of one do not wait for copies into another
   __shared__ __attribute__((aligned(1024))) unsigned char b0[S::kRows * kGemmStep], b1[S::kRows * kGemmStep], b2[S::kRows * kGemmStep],
       b3[S::kRows * kGemmStep];
@@ -189,25 +210,71 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, S
   const int n32 = lane & 31, kh = lane >> 5;
   const int wm = wave % S::WM, wn = wave / S::WM;
   const int chunk = ((tid & 7) ^ ((tid >> 4) & 7)) * 16;
-  const int tok_at = (wm * MT * 32 + n32) * kGemmStep + ((kh ^ ((n32 >> 1) & 7)) << 4);
-  const int row_at = (wn * NT * 32 + n32) * kGemmStep + ((kh ^ ((n32 >> 1) & 7)) << 4);
+  const int along = (n32 << 7) + ((kh ^ ((n32 >> 1) & 7)) << 4);
+  const int across = ((8 * kh + (lane >> 2 & 3)) << 7) + ((lane >> 3 & 1) << 6) + ((lane >> 4 & 1) << 5) + ((lane & 3) << 3);
+  // a wave's first tile, and its first two with the axis across: tiles are halves of a row of 64 tokens
+  const auto half = [&](int tile) __attribute__((always_inline)) { return tile / 2 * (64 * kGemmStep) + (across ^ (tile % 2 << 6)); };
+  const int tok_at = wm * MT * 32 * kGemmStep + along, tok_half[2] = {half(wm * MT), half(wm * MT + 1)};
+  const int row_at = wn * NT * 32 * kGemmStep + along, row_half[2] = {half(wn * NT), half(wn * NT + 1)};
 
   GemmQueue queue(tiles);
   GemmPlace at, now;
-  uint32_t off[kCopies], k = 0;
+  // rows' offsets; of an operand with the axis across, two rows' offsets and then columns'
+  uint32_t off_b[kRowT ? kCb / 2 + 2 : kCb], off_t[kTokT ? kCt / 2 + 2 : kCt], k = 0, b_row[2] = {}, t_row[2] = {};
+  const unsigned char *b_from = nullptr, *t_from = nullptr;
   auto place = [&](int i) __attribute__((always_inline)) {
-    k = min((at.step0 + min(i, at.count - 1)) * kGemmStep + chunk, kbytes - 16);  // (past the end: of the same rows)
+    const int s = at.step0 + min(i, at.count - 1), left = source.left(s);  // (past the end: of the same rows)
+    if constexpr (!kTokT || !kRowT) k = source.k(s) + min(chunk, left - 16);
+    const uint32_t last = (uint32_t)(left / 2 - 1);
+    if constexpr (kTokT) {
+      t_from = source.tok_at(s);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) t_row[j] = left >= kGemmStep ? off_t[kCt / 2 + j] : min(off_t[kCt / 2 + j], last * (uint32_t)source.tok_ld());
+    }
+    if constexpr (kRowT) {
+      b_from = source.row_at(s);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) b_row[j] = left >= kGemmStep ? off_b[kCb / 2 + j] : min(off_b[kCb / 2 + j], last * (uint32_t)source.row_ld());
+    }
   };
   auto copy = [&](int to, int c) __attribute__((always_inline)) {
-    unsigned char* lds = (c < kCb ? rows_of(to) + c * kPass * kGemmStep : toks_of(to) + (c - kCb) * kPass * kGemmStep) + wave * 1024;
-    gemm_copy((c < kCb ? source.row_base(c * kPass + tid / 8) : source.tok) + (off[c] + k), lds);
+    if (c < kCb) {
+      unsigned char* lds = rows_of(to) + c * kPass * kGemmStep + wave * 1024;
+      if constexpr (kRowT)
+        gemm_copy(b_from + (off_b[c / 2] + b_row[c % 2]), lds);
+      else
+        gemm_copy(source.row_base(c * kPass + tid / 8) + (off_b[c] + k), lds);
+    } else {
+      c -= kCb;
+      unsigned char* lds = toks_of(to) + c * kPass * kGemmStep + wave * 1024;
+      if constexpr (kTokT)
+        gemm_copy(t_from + (off_t[c / 2] + t_row[c % 2]), lds);
+      else
+        gemm_copy(source.tok + (off_t[c] + k), lds);
+    }
   };
   auto start = [&]() __attribute__((always_inline)) {  // the next tile and its first steps
     at = queue.take(tiles);
     source.set(at);
-    const int mine = gemm_opaque(tid / 8);
+    const int mine = gemm_opaque(tid / 8), column = gemm_opaque((tid & 7) ^ (tid >> 4 & 1) << 2);
+    if constexpr (kRowT) {
 #pragma unroll
-    for (int c = 0; c < kCopies; ++c) off[c] = c < kCb ? source.row_off(c * kPass + mine) : source.tok_off((c - kCb) * kPass + mine);
+      for (int c = 0; c < kCb / 2; ++c) off_b[c] = source.row_col(8 * c + column);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) off_b[kCb / 2 + j] = (uint32_t)(mine + 32 * j) * (uint32_t)source.row_ld();
+    } else {
+#pragma unroll
+      for (int c = 0; c < kCb; ++c) off_b[c] = source.row_off(c * kPass + mine);
+    }
+    if constexpr (kTokT) {
+#pragma unroll
+      for (int c = 0; c < kCt / 2; ++c) off_t[c] = source.tok_col(8 * c + column);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) off_t[kCt / 2 + j] = (uint32_t)(mine + 32 * j) * (uint32_t)source.tok_ld();
+    } else {
+#pragma unroll
+      for (int c = 0; c < kCt; ++c) off_t[c] = source.tok_off(c * kPass + mine);
+    }
 #pragma unroll
     for (int i = 0; i < BUFFERS; ++i) {
       place(i);
@@ -218,12 +285,25 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, S
   // operands of half h, of its instructions' k from 16 s on: chunk 4 h + 2 s + kh of a row
   gemm_i32x4 w[2][2][NT], x[2][2][MT];
   gemm_f32x16 acc[MT][NT];
+  auto read_half = [&](gemm_i32x4& to, const unsigned char* lds, const int (&half)[2], int h, int s, int j) __attribute__((always_inline)) {
+    const int tile = j / 2, part = j % 2;  // (rows 8 kh + 4 part on of the instruction's 16)
+    const uint2 v = gemm_read_column(lds + half[tile % 2] + (tile / 2 * 64 + (2 * h + s) * 16 + part * 4) * kGemmStep);
+    to[2 * part] = (int)v.x;
+    to[2 * part + 1] = (int)v.y;
+  };
   auto read = [&](int from, int h, int j) __attribute__((always_inline)) {
-    const int s = j / (MT + NT), r = j % (MT + NT), flip = 64 * h + 32 * s;
-    if (r < NT)
-      w[h][s][r] = *reinterpret_cast<const gemm_i32x4*>(rows_of(from) + (row_at ^ flip) + r * 32 * kGemmStep);
-    else
-      x[h][s][r - NT] = *reinterpret_cast<const gemm_i32x4*>(toks_of(from) + (tok_at ^ flip) + (r - NT) * 32 * kGemmStep);
+    const int s = j / (kReadsX + kReadsW), r = j % (kReadsX + kReadsW), q = r - kReadsW, flip = 64 * h + 32 * s;
+    if (r < kReadsW) {
+      if constexpr (kRowT)
+        read_half(w[h][s][r / 2], rows_of(from), row_half, h, s, r);
+      else
+        w[h][s][r] = *reinterpret_cast<const gemm_i32x4*>(rows_of(from) + (row_at ^ flip) + r * 32 * kGemmStep);
+    } else {
+      if constexpr (kTokT)
+        read_half(x[h][s][q / 2], toks_of(from), tok_half, h, s, q);
+      else
+        x[h][s][q] = *reinterpret_cast<const gemm_i32x4*>(toks_of(from) + (tok_at ^ flip) + q * 32 * kGemmStep);
+    }
   };
   auto multiply = [&](int h, int j) __attribute__((always_inline)) {
     const int s = j / (MT * NT), mt = j % (MT * NT) / NT, nt = j % NT;
@@ -237,24 +317,32 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, int kbytes, S
   // half a step, reading the next one, of buffer `from`; the copies into `to` with it (-1: none)
   auto pass = [&](int h, int from, int to) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < kSlots; ++q) {
-      if (q < kReads) read(from, h ^ 1, q);
-      if (to >= 0 && q < kCopies) copy(to, q);
+    for (int q = 0; q < kMul; ++q) {
 #pragma unroll
-      for (int j = q * kPer; j < (q + 1) * kPer && j < kMul; ++j) multiply(h, j);
+      for (int j = q * kReads / kEarly; j < (q + 1) * kReads / kEarly && j < kReads; ++j) read(from, h ^ 1, j);
+#pragma unroll
+      for (int j = q * kCopies / kMul; to >= 0 && j < (q + 1) * kCopies / kMul; ++j) copy(to, j);
+      multiply(h, q);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto cut = [&](int h, int i) __attribute__((always_inline)) {  // past the rows' end: zeros
-    const int left = i < now.count ? kbytes - (now.step0 + i) * kGemmStep - h * 64 : 0;
+  auto keep = [&](gemm_i32x4& v, int bytes) __attribute__((always_inline)) {
+    if constexpr (kTokT && kRowT) {  // an end anywhere
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = bytes >= 4 * i + 4 ? v[i] : bytes == 4 * i + 2 ? v[i] & 0xffff : 0;
+    } else if (bytes <= 0) {
+      v = gemm_i32x4{0, 0, 0, 0};
+    }
+  };
+  auto cut = [&](int h, int i) __attribute__((always_inline)) {  // past the axis' end, or the last step: zeros
+    const int left = i < now.count ? source.left(now.step0 + i) - h * 64 : 0;
     if (left < 64) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        if (kh * 16 + s * 32 < left) continue;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) w[h][s][nt] = gemm_i32x4{0, 0, 0, 0};
+        for (int nt = 0; nt < NT; ++nt) keep(w[h][s][nt], left - 32 * s - 16 * kh);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) x[h][s][mt] = gemm_i32x4{0, 0, 0, 0};
+        for (int mt = 0; mt < MT; ++mt) keep(x[h][s][mt], left - 32 * s - 16 * kh);
       }
     }
   };

@@ -12,29 +12,6 @@
 namespace moeq4 {
 namespace {
 
-// dst [C][Rp] = src [R][C]^T, zeros from R to Rp; C a multiple of 8, Rp too.
-__global__ __launch_bounds__(256) void k_glu_transpose(const uint16_t* src, long long lds, int R, int C, int Rp, uint16_t* dst,
-                                                       long long ldd) {
-  __shared__ __attribute__((aligned(16))) uint16_t tile[64][kGluPad];
-  const int across = (C + 63) / 64, r0 = blockIdx.x / across * 64, c0 = blockIdx.x % across * 64;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = threadIdx.x / 8 + 32 * i, c = (threadIdx.x % 8) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r0 + r < R && c0 + c < C) v = *reinterpret_cast<const uint4*>(src + (size_t)(r0 + r) * lds + c0 + c);
-    *reinterpret_cast<uint4*>(&tile[r][c]) = v;
-  }
-  __syncthreads();
-  glu_put_transposed(tile, dst, ldd, c0, C, r0, Rp);
-}
-
-int glu_transpose(const void* src, long long lds, int R, int C, int Rp, void* dst, long long ldd, hipStream_t stream) {
-  const dim3 grid((unsigned)(((Rp + 63) / 64) * ((C + 63) / 64)));
-  hipLaunchKernelGGL(k_glu_transpose, grid, dim3(256), 0, stream, static_cast<const uint16_t*>(src), lds, R, C, Rp,
-                     static_cast<uint16_t*>(dst), ldd);
-  return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
-}
-
 int glu_status(int T, int H, int I) {
   if (T < 0 || H < 1 || I < 1) return MOE_Q4_ERR_SHAPE;
   if (H % 8 || I % 8 || T > MOE_Q4_LINEAR_MAX_L || H > MOE_Q4_LINEAR_MAX_K || I > MOE_Q4_LINEAR_MAX_K) return MOE_Q4_ERR_UNSUPPORTED;
@@ -53,21 +30,16 @@ size_t glu_forward_part(int T, int H, int I) {
 }
 
 struct GluBackLayout {
-  size_t gu, d, dt, xt, wt, part, total;
-  int Tp;
+  size_t gu, d, part, total;
   GemmPlan dx, dw;
 };
 GluBackLayout glu_back_layout(int T, int H, int I, bool saved) {
   GluBackLayout w{};
-  w.Tp = (T + 63) / 64 * 64;
-  w.dx = gemm_plan(kGemmCosts16, T, H, glu_steps(2L * I));
-  w.dw = gemm_plan(kGemmCosts16, 2 * I, H, glu_steps(w.Tp));
+  w.dx = gemm_plan(kGemmCosts16, T, H, 2 * glu_steps(I));
+  w.dw = gemm_plan(kGemmCosts16, 2 * I, H, glu_steps(T));
   size_t off = 0;
   w.gu = off; off = round256(off + (saved ? 0 : (size_t)2 * T * I * 4));
   w.d = off; off = round256(off + (size_t)T * 2 * I * 2);
-  w.dt = off; off = round256(off + (size_t)2 * I * w.Tp * 2);
-  w.xt = off; off = round256(off + (size_t)H * w.Tp * 2);
-  w.wt = off; off = round256(off + (size_t)H * 2 * I * 2);
   w.part = off;
   size_t part = saved ? 0 : glu_forward_part(T, H, I);
   if (w.dx.tiles.splits > 1) part = std::max(part, (size_t)w.dx.tiles.splits * T * H * 4);
@@ -184,35 +156,33 @@ extern "C" int moe_glu_backward(int dtype, const void* x, long long ldx, const v
     if ((st = glu_forward(f16, a, ws + w.part, stream))) return st;
     saved = a.saved;
   }
-  st = (f16 ? glu_grad_f16 : glu_grad_bf16)(saved, dh, lddh, T, I, w.Tp, dx ? ws + w.d : nullptr, dwg ? ws + w.dt : nullptr, stream);
-  if (st) return st;
-  if (dx) {  // dx = D [Wg; Wu], with the weights' rows along 2I
-    if ((st = glu_transpose(wg, ldw, I, H, I, ws + w.wt, 2LL * I, stream))) return st;
-    if ((st = glu_transpose(wu, ldw, I, H, I, ws + w.wt + (size_t)I * 2, 2LL * I, stream))) return st;
-    GluMmArgs m{};
-    m.a = ws + w.d;
-    m.b = ws + w.wt;
+  if ((st = (f16 ? glu_grad_f16 : glu_grad_bf16)(saved, dh, lddh, T, I, ws + w.d, stream))) return st;
+  GluMmArgs m{};
+  m.a = ws + w.d;
+  m.lda = 4LL * I;
+  m.N = H;
+  if (dx) {  // dx = D [Wg; Wu]
+    m.b0 = static_cast<const unsigned char*>(wg);
+    m.b1 = static_cast<const unsigned char*>(wu);
     m.out0 = m.out1 = dx;
-    m.lda = m.ldb = 4LL * I;
+    m.ldb = 2 * ldw;
     m.ldo = lddx;
     m.M = m.cut = T;
-    m.N = H;
-    m.kbytes = 4 * I;
+    m.K = I;
+    m.steps = glu_steps(I);
     if ((st = glu_mm(f16, m, w.dx, ws + w.part, stream))) return st;
   }
-  if (dwg) {  // [dWg; dWu] = D^T x, with the rows along the tokens
-    if ((st = glu_transpose(x, ldx, T, H, w.Tp, ws + w.xt, w.Tp, stream))) return st;
-    GluMmArgs m{};
-    m.a = ws + w.dt;
-    m.b = ws + w.xt;
+  if (dwg) {  // [dWg; dWu] = D^T x
+    m.b0 = static_cast<const unsigned char*>(x);
+    m.b1 = nullptr;
     m.out0 = dwg;
     m.out1 = dwu;
-    m.lda = m.ldb = 2LL * w.Tp;
+    m.ldb = 2 * ldx;
     m.ldo = H;
     m.M = 2 * I;
     m.cut = I;
-    m.N = H;
-    m.kbytes = 2 * w.Tp;
+    m.K = T;
+    m.steps = glu_steps(T);
     if ((st = glu_mm(f16, m, w.dw, ws + w.part, stream))) return st;
   }
   return MOE_Q4_OK;

@@ -6,12 +6,14 @@
 //             the same rows of Wg and Wu, so that a lane holds g and u of a result
 //   backward  dg = dh u silu'(g), du = dh silu(g), side by side as D [T, 2I];
 //             dx = D [Wg; Wu], [dWg; dWu] = D^T x
-// The backward's products have their sums along the operands' other axis:
-// transposed copies of D, x and the weights make them the same product.
+// The backward's products have their sums along the other axis of the weights,
+// or of both D and x, which the tiles read as they are.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "moe_gemm_device.h"
 #include "moe_gemm_plan.h"
@@ -29,13 +31,14 @@ struct GluArgs {
   GemmTiles tiles;
 };
 
-// C [M, N] = A B^T over K elements; rows of C from `cut` on go to out1.
+// dx [M, N] = D [b0; b1], or out [M, N] = D^T b0 (K tokens), whose rows from
+// `cut` on go to out1.
 struct GluMmArgs {
-  const unsigned char *a, *b;  // rows lda, ldb bytes apart
+  const unsigned char *a, *b0, *b1;  // rows lda, ldb bytes apart
   void *out0, *out1;
-  float* part;                 // split K: [splits][M][N]
-  long long lda, ldb, ldo;     // ldo in elements
-  int M, N, kbytes, cut;
+  float* part;                       // split K: [splits][M][N]
+  long long lda, ldb, ldo;           // ldo in elements
+  int M, N, K, steps, cut;           // K and steps of b0
   GemmTiles tiles;
 };
 
@@ -44,25 +47,9 @@ int glu_forward_bf16(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t
 int glu_forward_f16(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t stream);
 int glu_mm_bf16(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream);
 int glu_mm_f16(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream);
-// D [T][2I] and its transpose [2I][Tp] (zeros from T on) from g, u and dh
-// (lddh elements apart); either may be NULL.
-int glu_grad_bf16(const float* saved, const void* dh, long long lddh, int T, int I, int Tp, void* d, void* dt, hipStream_t stream);
-int glu_grad_f16(const float* saved, const void* dh, long long lddh, int T, int I, int Tp, void* d, void* dt, hipStream_t stream);
-
-// Writes the transpose of a workgroup's 64 x 64 numbers in LDS: rows c0 + c (to
-// C) of dst from column r0 on, a multiple of 64 (to Rp, a multiple of 8).
-constexpr int kGluPad = 64 + 8;
-__device__ __forceinline__ void glu_put_transposed(const uint16_t (&tile)[64][kGluPad], uint16_t* dst, long long ldd, int c0,
-                                                   int C, int r0, int Rp) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int c = threadIdx.x / 8 + 32 * i, r = (threadIdx.x % 8) * 8;
-    uint32_t v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = tile[r + 2 * j][c] | (uint32_t)tile[r + 2 * j + 1][c] << 16;
-    if (c0 + c < C && r0 + r < Rp) *reinterpret_cast<uint4*>(dst + (size_t)(c0 + c) * ldd + r0 + r) = make_uint4(v[0], v[1], v[2], v[3]);
-  }
-}
+// D [T][2I] from g, u and dh (lddh elements apart).
+int glu_grad_bf16(const float* saved, const void* dh, long long lddh, int T, int I, void* d, hipStream_t stream);
+int glu_grad_f16(const float* saved, const void* dh, long long lddh, int T, int I, void* d, hipStream_t stream);
 
 #ifdef MOE_GLU_INST
 
@@ -78,8 +65,11 @@ __device__ __forceinline__ float glu_sigmoid(float g) { return __builtin_amdgcn_
 template <class S>
 struct GluSource {
   const GluArgs& a;
+  static constexpr bool kTokT = false, kRowT = false;
   const unsigned char *tok, *row;
   int toks, rows;
+  __device__ __forceinline__ uint32_t k(int s) const { return (uint32_t)s * kGemmStep; }
+  __device__ __forceinline__ int left(int s) const { return 2 * a.H - s * kGemmStep; }
   __device__ __forceinline__ void set(const GemmPlace& p) {
     tok = a.x + (size_t)p.tok * S::kTok * a.ldx;
     row = (threadIdx.x / 8 % 32 < 16 ? a.wg : a.wu) + (size_t)p.row * (S::kRows / 2) * a.ldw;  // (a thread's rows are 32 apart)
@@ -97,7 +87,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_glu_tiles(GluArgs a) {
   typedef typename GluType<KIND>::type T16;
   static_assert(S::kThreads / 8 == 32, "GluSource's rows");
   GluSource<S> source{a};
-  gemm_tiles<S, gemm_buffers<S>()>(a.tiles, 2 * a.H, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
+  gemm_tiles<S>(a.tiles, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63);
     const int place = gemm_place4(lane), t0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 15);
     const int n0 = p.row * (S::kRows / 2) + wave / WM * NT * 16;
@@ -212,28 +202,52 @@ __global__ __launch_bounds__(256) void k_glu_join(GluArgs a, int splits) {
   }
 }
 
+// dx: D's rows, and the weights across; steps of Wg's and then of Wu's rows.
 template <class S>
-struct GluMmSource {
+struct GluDxSource {
   const GluMmArgs& a;
-  const unsigned char *tok, *row;
-  int toks, rows;
+  static constexpr bool kTokT = false, kRowT = true;
+  const unsigned char* tok;
+  int toks, col;
   __device__ __forceinline__ void set(const GemmPlace& p) {
     tok = a.a + (size_t)p.tok * S::kTok * a.lda;
-    row = a.b + (size_t)p.row * S::kRows * a.ldb;
     toks = a.M - 1 - p.tok * S::kTok;
-    rows = a.N - 1 - p.row * S::kRows;
+    col = p.row * S::kRows;
   }
+  __device__ __forceinline__ int part(int s) const { return s >= a.steps ? s - a.steps : s; }
+  __device__ __forceinline__ uint32_t k(int s) const { return (uint32_t)(part(s) * kGemmStep + (s >= a.steps ? 2 * a.K : 0)); }
+  __device__ __forceinline__ int left(int s) const { return 2 * a.K - part(s) * kGemmStep; }
   __device__ __forceinline__ uint32_t tok_off(int r) const { return (uint32_t)min(r, toks) * (uint32_t)a.lda; }
-  __device__ __forceinline__ const unsigned char* row_base(int) const { return row; }
-  __device__ __forceinline__ uint32_t row_off(int r) const { return (uint32_t)min(r, rows) * (uint32_t)a.ldb; }
+  __device__ __forceinline__ const unsigned char* row_at(int s) const { return (s >= a.steps ? a.b1 : a.b0) + (size_t)part(s) * 64 * a.ldb; }
+  __device__ __forceinline__ long long row_ld() const { return a.ldb; }
+  __device__ __forceinline__ uint32_t row_col(int c) const { return 2u * (uint32_t)min(col + 8 * c, a.N - 8); }
 };
 
-template <int KIND, int MT, int NT, int WM, int WN>
+// dWg and dWu: D and x across, steps of tokens.
+template <class S>
+struct GluDwSource {
+  const GluMmArgs& a;
+  static constexpr bool kTokT = true, kRowT = true;
+  int tok, col;
+  __device__ __forceinline__ void set(const GemmPlace& p) {
+    tok = p.tok * S::kTok;
+    col = p.row * S::kRows;
+  }
+  __device__ __forceinline__ int left(int s) const { return 2 * a.K - s * kGemmStep; }
+  __device__ __forceinline__ const unsigned char* tok_at(int s) const { return a.a + (size_t)s * 64 * a.lda; }
+  __device__ __forceinline__ long long tok_ld() const { return a.lda; }
+  __device__ __forceinline__ uint32_t tok_col(int c) const { return 2u * (uint32_t)min(tok + 8 * c, a.M - 8); }
+  __device__ __forceinline__ const unsigned char* row_at(int s) const { return a.b0 + (size_t)s * 64 * a.ldb; }
+  __device__ __forceinline__ long long row_ld() const { return a.ldb; }
+  __device__ __forceinline__ uint32_t row_col(int c) const { return 2u * (uint32_t)min(col + 8 * c, a.N - 8); }
+};
+
+template <int KIND, bool DW, int MT, int NT, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_glu_mm(GluMmArgs a) {
   using S = GemmShape<KIND, MT, NT, WM, WN>;
   typedef typename GluType<KIND>::type T16;
-  GluMmSource<S> source{a};
-  gemm_tiles<S, gemm_buffers<S>()>(a.tiles, a.kbytes, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
+  std::conditional_t<DW, GluDwSource<S>, GluDxSource<S>> source{a};
+  gemm_tiles<S>(a.tiles, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63);
     const int place = gemm_place4(lane), m0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 15);
     const int n0 = p.row * S::kRows + wave / WM * NT * 32;
@@ -293,40 +307,27 @@ __global__ __launch_bounds__(256) void k_glu_mm_join(GluMmArgs a, int splits) {
   }
 }
 
-// 64 tokens x 64 of the I outputs a workgroup.
+// 8 of a token's I a thread.
 template <int KIND>
-__global__ __launch_bounds__(256) void k_glu_grad(const float* saved, const void* dh, long long lddh, int T, int I, int Tp,
-                                                  void* d, uint16_t* dt) {
+__global__ __launch_bounds__(256) void k_glu_grad(const float* saved, const void* dh, long long lddh, int T, int I, void* d) {
   typedef typename GluType<KIND>::type T16;
-  __shared__ __attribute__((aligned(16))) uint16_t tg[64][kGluPad], tu[64][kGluPad];
-  const int across = (I + 63) / 64, r0 = blockIdx.x / across * 64, c0 = blockIdx.x % across * 64;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = threadIdx.x / 8 + 32 * i, c = (threadIdx.x % 8) * 8;
-    const int n = r0 + r < T ? min(I - c0 - c, 8) : 0;  // (0 or 8)
-    const size_t at = (size_t)min(r0 + r, T - 1) * I + c0 + c;
+  const size_t all = (size_t)T * I;
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; i < all; i += (size_t)gridDim.x * 2048) {
+    const size_t t = i / I, n = i - t * I;
     float g[8], u[8], e[8], dg[8], du[8];
-    norm_load8(saved + at, n, g);
-    norm_load8(saved + (size_t)T * I + at, n, u);
-    norm_load8(static_cast<const T16*>(dh) + (size_t)min(r0 + r, T - 1) * lddh + c0 + c, n, e);
+    norm_load8(saved + i, 8, g);
+    norm_load8(saved + all + i, 8, u);
+    norm_load8(static_cast<const T16*>(dh) + t * lddh + n, 8, e);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float s = glu_sigmoid(g[j]);
       dg[j] = e[j] * u[j] * (s * __builtin_fmaf(g[j], 1.0f - s, 1.0f));
       du[j] = e[j] * (g[j] * s);
     }
-    if (d) {
-      T16* to = static_cast<T16*>(d) + (size_t)min(r0 + r, T - 1) * 2 * I + c0 + c;
-      norm_store8(to, n, dg);
-      norm_store8(to + I, n, du);
-    }
-    norm_store8(reinterpret_cast<T16*>(&tg[r][c]), 8, dg);
-    norm_store8(reinterpret_cast<T16*>(&tu[r][c]), 8, du);
+    T16* to = static_cast<T16*>(d) + t * 2 * I + n;
+    norm_store8(to, 8, dg);
+    norm_store8(to + I, 8, du);
   }
-  if (!dt) return;
-  __syncthreads();
-  glu_put_transposed(tg, dt, Tp, c0, I, r0, Tp);
-  glu_put_transposed(tu, dt + (size_t)I * Tp, Tp, c0, I, r0, Tp);
 }
 
 template <int KIND>
@@ -358,17 +359,25 @@ int glu_forward_kind(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }
 
-template <int KIND>
-int glu_mm_kind(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream) {
+template <int KIND, bool DW>
+void glu_mm_launch(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream) {
   const dim3 grid(p.workgroups);
   switch (p.shape) {
-    case kGemm256x256: hipLaunchKernelGGL((k_glu_mm<KIND, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm256x192: hipLaunchKernelGGL((k_glu_mm<KIND, 4, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm128x256: hipLaunchKernelGGL((k_glu_mm<KIND, 2, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm128x192: hipLaunchKernelGGL((k_glu_mm<KIND, 2, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm128x128: hipLaunchKernelGGL((k_glu_mm<KIND, 2, 2, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    default: hipLaunchKernelGGL((k_glu_mm<KIND, 2, 1, 1, 4>), grid, dim3(256), 0, stream, a); break;
+    case kGemm256x256: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm256x192: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 4, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x256: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 2, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x192: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 2, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x128: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 2, 2, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    default: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 2, 1, 1, 4>), grid, dim3(256), 0, stream, a); break;
   }
+}
+
+template <int KIND>
+int glu_mm_kind(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream) {
+  if (a.b1)
+    glu_mm_launch<KIND, false>(a, p, stream);
+  else
+    glu_mm_launch<KIND, true>(a, p, stream);
   if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
   if (p.tiles.splits > 1) {
     const size_t all = (size_t)a.M * a.N / 8;
@@ -378,9 +387,9 @@ int glu_mm_kind(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream) {
 }
 
 template <int KIND>
-int glu_grad_kind(const float* saved, const void* dh, long long lddh, int T, int I, int Tp, void* d, void* dt, hipStream_t stream) {
-  const dim3 grid((unsigned)(((T + 63) / 64) * ((I + 63) / 64)));
-  hipLaunchKernelGGL((k_glu_grad<KIND>), grid, dim3(256), 0, stream, saved, dh, lddh, T, I, Tp, d, static_cast<uint16_t*>(dt));
+int glu_grad_kind(const float* saved, const void* dh, long long lddh, int T, int I, void* d, hipStream_t stream) {
+  const dim3 grid((unsigned)std::min<size_t>(((size_t)T * I + 2047) / 2048, 8192));
+  hipLaunchKernelGGL((k_glu_grad<KIND>), grid, dim3(256), 0, stream, saved, dh, lddh, T, I, d);
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }
 #endif
