@@ -305,24 +305,25 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, Source& sourc
         x[h][s][q] = *reinterpret_cast<const gemm_i32x4*>(toks_of(from) + (tok_at ^ flip) + q * 32 * kGemmStep);
     }
   };
-  auto multiply = [&](int h, int j) __attribute__((always_inline)) {
+  auto multiply = [&](int h, int j, bool first) __attribute__((always_inline)) {
     const int s = j / (MT * NT), mt = j % (MT * NT) / NT, nt = j % NT;
+    const gemm_f32x16 c = first && s == 0 ? gemm_f32x16{} : acc[mt][nt];
     if constexpr (KIND == kGemmBf16)
       acc[mt][nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(gemm_bf16x8, w[h][s][nt]),
-                                                            __builtin_bit_cast(gemm_bf16x8, x[h][s][mt]), acc[mt][nt], 0, 0, 0);
+                                                            __builtin_bit_cast(gemm_bf16x8, x[h][s][mt]), c, 0, 0, 0);
     else
       acc[mt][nt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(gemm_f16x8, w[h][s][nt]),
-                                                           __builtin_bit_cast(gemm_f16x8, x[h][s][mt]), acc[mt][nt], 0, 0, 0);
+                                                           __builtin_bit_cast(gemm_f16x8, x[h][s][mt]), c, 0, 0, 0);
   };
   // half a step, reading the next one, of buffer `from`; the copies into `to` with it (-1: none)
-  auto pass = [&](int h, int from, int to) __attribute__((always_inline)) {
+  auto pass = [&](int h, int from, int to, bool first = false) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < kMul; ++q) {
 #pragma unroll
       for (int j = q * kReads / kEarly; j < (q + 1) * kReads / kEarly && j < kReads; ++j) read(from, h ^ 1, j);
 #pragma unroll
       for (int j = q * kCopies / kMul; to >= 0 && j < (q + 1) * kCopies / kMul; ++j) copy(to, j);
-      multiply(h, q);
+      multiply(h, q, first);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -353,17 +354,9 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, Source& sourc
     now = at;
     gemm_meet<(BUFFERS - 1) * kCopies>();  // the first step is there
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[mt][nt][e] = 0.0f;
-        asm volatile("" : "+a"(acc[mt][nt]));  // hides the zeros, which the compiler would carry along in registers of their own
-      }
-#pragma unroll
     for (int j = 0; j < kReads; ++j) read(0, 0, j);
     cut(0, 0);
-    pass(0, 0, -1);
+    pass(0, 0, -1, true);
     cut(1, 0);
     constexpr int kOnWay = (BUFFERS - 2) * kCopies;  // copies of later steps than the next
     gemm_meet<kOnWay>();
@@ -397,7 +390,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, Source& sourc
     const bool more = queue.any();
     if (more) start();
 #pragma unroll
-    for (int j = 0; j < kMul; ++j) multiply(1, j);
+    for (int j = 0; j < kMul; ++j) multiply(1, j, false);
     store(now, acc);
     if (!more) break;
   }

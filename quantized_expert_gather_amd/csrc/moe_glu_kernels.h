@@ -72,7 +72,8 @@ struct GluSource {
   __device__ __forceinline__ int left(int s) const { return 2 * a.H - s * kGemmStep; }
   __device__ __forceinline__ void set(const GemmPlace& p) {
     tok = a.x + (size_t)p.tok * S::kTok * a.ldx;
-    row = (threadIdx.x / 8 % 32 < 16 ? a.wg : a.wu) + (size_t)p.row * (S::kRows / 2) * a.ldw;  // (a thread's rows are 32 apart)
+    // a thread's rows are 32 apart, a wave's 8 threads of them side by side
+    row = (__builtin_amdgcn_readfirstlane(threadIdx.x) / 8 % 32 < 16 ? a.wg : a.wu) + (size_t)p.row * (S::kRows / 2) * a.ldw;
     toks = a.T - 1 - p.tok * S::kTok;
     rows = a.I - 1 - p.row * (S::kRows / 2);
   }
