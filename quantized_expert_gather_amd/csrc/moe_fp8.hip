@@ -156,7 +156,14 @@ int fp8_status(int L, int N, int K) {
 // 128 steps.
 constexpr GemmCosts kFp8Costs = {{1.62f, 0, 0, 0, 0.64f, 0.41f}, {0, 0, 0, 0, 0.47f, 0.32f}, {8.5f, 0, 0, 0, 4.3f, 3.5f}, {1, 0, 0, 0, 2, 3}};
 constexpr GemmCosts kFp8WideCosts = {{0, 0, 0, 0, 1.02f, 0.69f}, {0, 0, 0, 0, 0.83f, 0.465f}, {0, 0, 0, 0, 7.0f, 5.0f}, {0, 0, 0, 0, 2, 3}};
-bool fp8_by_rows(int L) { return L <= 32; }
+// Few tokens by rows, whose weights then pass the card once at the memory's
+// rate; from 17 tokens on the tiles' matrix instructions are the faster for
+// large weights (us by rows and by tiles, 24 tokens: 2050 x 4096 9.7 and 10.7,
+// 6144 x 6144 17.1 and 14.9, 12288 x 6144 32 and 22; 16 tokens 7.5 and 10.7,
+// 12.5 and 14.9, 23.5 and 21.7).
+bool fp8_by_rows(int L, int N, int K) { return L <= 16 || (L <= 32 && (long)N * K < 1L << 24); }
+// Up to 32 tokens, and fp32 results, with the codes as bf16.
+bool fp8_wide(int L, int out_dtype) { return L <= 32 || out_dtype == MOE_Q4_DTYPE_F32; }
 GemmPlan fp8_plan(int L, int N, int K, bool wide) { return gemm_plan(wide ? kFp8WideCosts : kFp8Costs, L, N, (K + 127) / 128); }
 size_t fp8_part(int L, int N, int K, bool wide) {
   const GemmPlan p = fp8_plan(L, N, K, wide);
@@ -169,7 +176,7 @@ size_t fp8_part(int L, int N, int K, bool wide) {
 using namespace moeq4;
 
 extern "C" size_t moe_linear_fp8_workspace_bytes(int L, int N, int K) {
-  if (fp8_status(L, N, K) || L == 0 || fp8_by_rows(L)) return 0;
+  if (fp8_status(L, N, K) || L == 0 || fp8_by_rows(L, N, K)) return 0;
   return std::max(fp8_part(L, N, K, false), fp8_part(L, N, K, true));
 }
 
@@ -195,7 +202,7 @@ extern "C" int moe_linear_fp8_forward(const uint8_t* x, long long ldx, const flo
   const ArgSpan outs[] = {{out, args_span(L, ldo, N, os)}, {need ? workspace : nullptr, need}};
   if (args_alias(outs, ins)) return MOE_Q4_ERR_ALIAS;
   Fp8Args a{x, sx, w, sw, bias, out, nullptr, ldx, ldo, L, N, K, G, out_dtype, {}};
-  if (fp8_by_rows(L)) {
+  if (fp8_by_rows(L, N, K)) {
     // 32 rows of w share a workgroup's reads of x where that leaves most compute units one (us, 16 and 32 rows:
     // 16 tokens 6144 x 6144 15.1 and 12.6, 4099 x 4112 9.4 and 10.6; 32 tokens 27 and 19, 16.1 and 13.8)
     const bool wide = L > 8 && N >= (L > 16 ? 4096 : 6144);
@@ -212,11 +219,12 @@ extern "C" int moe_linear_fp8_forward(const uint8_t* x, long long ldx, const flo
       hipLaunchKernelGGL((k_fp8_rows<2, 4, 8, 2>), grid, dim3(512), 0, stream, a);
     return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
   }
-  const GemmPlan p = fp8_plan(L, N, K, out_dtype == MOE_Q4_DTYPE_F32);
+  const bool codes_bf16 = fp8_wide(L, out_dtype);
+  const GemmPlan p = fp8_plan(L, N, K, codes_bf16);
   a.tiles = p.tiles;
   if (p.tiles.splits > 1) a.part = static_cast<float*>(workspace);
   const dim3 grid(p.workgroups);
-  if (out_dtype == MOE_Q4_DTYPE_F32) {
+  if (codes_bf16) {
     if (p.shape == kGemm128x128)
       hipLaunchKernelGGL((k_fp8_tiles<kGemmFp8Wide, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a);
     else

@@ -85,7 +85,7 @@ def linear_fp8(x, sx, w, sw, bias, out=torch.float32):
     bound = (160 + x.shape[1] / 128) * U * mag
     if out != torch.float32 and x.shape[0] > 32:
         a, b = X.abs().float(), W.abs().float()
-        cut = torch.zeros(a.shape[0], b.shape[0])
+        cut = torch.zeros(a.shape[0], b.shape[0], device=a.device)
         for k in range(0, x.shape[1], 8):
             most = torch.zeros_like(cut)
             for c in range(k, k + 8):

@@ -68,6 +68,20 @@ def test_strides_and_given_outputs():
         assert (out[:, :3] == 5).all() and (out[:, 134:] == 5).all()
 
 
+# Each tile shape, without and with parts of the inputs, and the products by
+# rows with 16 and 32 of w's rows a workgroup.
+@pytest.mark.parametrize("L,N,K", [(3283, 3795, 64), (5524, 643, 7184), (2322, 2571, 64), (1817, 259, 5488), (51, 67, 2448), (1181, 771, 5408),
+                                   (33, 67, 1680), (9, 6149, 272), (16, 131, 4112), (17, 4099, 400), (32, 4099, 4096), (32, 131, 2064)])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_tile_shapes(L, N, K, out):
+    print("[case] fp8 shapes", L, N, K, out, flush=True)
+    p = [t.cuda() for t in problem(L, N, K, True)]  # (the references, in 64 bits, there too)
+    ref, bound = R.linear_fp8(*p, out)
+    got = q.moe_linear_fp8_forward(*p, out_dtype=out)
+    R.check(got, ref.cpu(), bound.cpu(), out)
+    assert torch.equal(got, q.moe_linear_fp8_forward(*p, out_dtype=out))
+
+
 @pytest.mark.parametrize("L", [4, 200])
 def test_nan_codes_and_scales_stay_with_their_outputs(L):
     x, sx, w, sw, _ = problem(L, 300, 640)

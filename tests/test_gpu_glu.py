@@ -54,6 +54,34 @@ def test_forward_larger(T, H, I, dtype):
     check_forward(T, H, I, dtype)
 
 
+# For each of the products the smallest sizes at which each tile shape was
+# chosen, without and with parts of the sum's axis.
+SHAPES = [(2065, 72, 2704), (131, 8272, 6304), (1537, 64, 1264), (5538, 5760, 144), (1799, 456, 1680), (132, 7976, 3136),
+          (1442, 200, 1416), (612, 4632, 1624), (897, 64, 1104), (2778, 3512, 80), (45, 1480, 64), (3416, 3464, 64),
+          (2739, 672, 5816), (1681, 2360, 64), (5575, 272, 3112), (2720, 2160, 200), (2776, 648, 3112), (1944, 2064, 72),
+          (4287, 136, 2992), (1233, 1544, 64), (2694, 136, 1696), (38, 64, 712), (34, 2136, 2696), (4344, 200, 8208),
+          (39, 1416, 1368), (5932, 144, 5688), (459, 1360, 2112), (5937, 200, 4264), (193, 1168, 1656), (3529, 136, 4232),
+          (37, 904, 1032), (3481, 152, 1432), (1540, 64, 72)]
+
+
+@pytest.mark.parametrize("T,H,I", SHAPES)
+def test_tile_shapes(T, H, I):
+    print("[case] glu shapes", T, H, I, flush=True)
+    dtype = BF16 if T % 2 else F16
+    x, wg, wu, dh = (t.cuda() for t in problem(T, H, I, dtype))  # (the references, in 64 bits, there too)
+    g, u, h, bg, bu, bh = (t.cpu() for t in R.glu(x, wg, wu))
+    saved = torch.full((2, T, I), 9.0, device="cuda")
+    R.check(q.moe_glu(x, wg, wu, saved=saved), h, bh, dtype)
+    R.check(saved[0], g, bg)
+    R.check(saved[1], u, bu)
+    refs, bounds = R.glu_backward(x, wg, wu, dh)
+    got = q.moe_glu_backward(x, wg, wu, dh, saved=saved)
+    for a, ref, bound in zip(got, refs, bounds):
+        R.check(a, ref.cpu(), bound.cpu(), dtype)
+    for a, b in zip(got, q.moe_glu_backward(x, wg, wu, dh, saved=saved)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("T", [1, 7, 33, 64, 130])
 @pytest.mark.parametrize("H,I", [(8, 8), (72, 136), (264, 200)])
 @pytest.mark.parametrize("saved", [True, False])
