@@ -546,9 +546,10 @@ int moe_quantize_fp8(const void *x, int x_dtype, long long ldx, int T, int K, in
  * 16-bit results of more than 32 tokens, each product is cut at 2^-13 of the
  * largest power of two among its 8 neighbours' (inputs 8 i to 8 i + 7) before
  * these are added, as the 8-bit matrix instructions do; fp32 results, and
- * those of fewer tokens, have every product whole.  A NaN code or scale gives NaN in the outputs that it enters.  L == 0 returns
- * MOE_Q4_OK without touching the GPU.  Needs L <= MOE_Q4_LINEAR_MAX_L,
- * N <= MOE_Q4_LINEAR_MAX_N, K <= MOE_Q4_LINEAR_MAX_K, ldx <=
+ * those of fewer tokens, have every product whole.  A NaN code or scale gives
+ * NaN in the outputs that it enters, an infinite scale infinities or NaN.  L ==
+ * 0 returns MOE_Q4_OK without touching the GPU.  Needs L <= MOE_Q4_LINEAR_MAX_L,
+ * N <= MOE_Q4_LINEAR_MAX_N, L * N <= 2^40, K <= MOE_Q4_LINEAR_MAX_K, ldx <=
  * MOE_Q4_LINEAR_MAX_LDX.
  */
 int moe_linear_fp8_forward(const uint8_t *x, long long ldx, const float *sx, const uint8_t *w, const float *sw,

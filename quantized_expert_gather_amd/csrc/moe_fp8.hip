@@ -28,6 +28,7 @@ struct Fp8Args {
   long long ldx, ldo;
   int L, N, K, G, out_dtype;
   GemmTiles tiles;
+  int row0;  // by rows: the launch's first
 };
 
 template <class S>
@@ -94,7 +95,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_fp8_tiles(Fp8Args a) {
 template <int J, int G, int WAVES, int U>
 __global__ __launch_bounds__(64 * WAVES) void k_fp8_rows(Fp8Args a) {
   __shared__ float lds[WAVES][J][G][64];
-  const int wave = threadIdx.x >> 6, row0 = blockIdx.x * 8 * J, index = gemm_rows_index();
+  const int wave = threadIdx.x >> 6, row0 = a.row0 + blockIdx.x * 8 * J, index = gemm_rows_index();
   const unsigned char *tok[G], *row[J];
   const float* sx[G];
   gemm_f32x4 acc[J][G];
@@ -149,6 +150,7 @@ __global__ __launch_bounds__(256) void k_fp8_join(const float* part, const float
 int fp8_status(int L, int N, int K) {
   if (L < 0 || N < 1 || K < 1) return MOE_Q4_ERR_SHAPE;
   if (K % 16 || L > MOE_Q4_LINEAR_MAX_L || N > MOE_Q4_LINEAR_MAX_N || K > MOE_Q4_LINEAR_MAX_K) return MOE_Q4_ERR_UNSUPPORTED;
+  if ((long)L * N > 1L << 40) return MOE_Q4_ERR_UNSUPPORTED;  // (2^31 tiles and more)
   return MOE_Q4_OK;
 }
 
@@ -201,23 +203,28 @@ extern "C" int moe_linear_fp8_forward(const uint8_t* x, long long ldx, const flo
                          {sw, ((size_t)N + 127) / 128 * G * 4}, {bias, bias ? (size_t)N * 4 : 0}};
   const ArgSpan outs[] = {{out, args_span(L, ldo, N, os)}, {need ? workspace : nullptr, need}};
   if (args_alias(outs, ins)) return MOE_Q4_ERR_ALIAS;
-  Fp8Args a{x, sx, w, sw, bias, out, nullptr, ldx, ldo, L, N, K, G, out_dtype, {}};
+  Fp8Args a{x, sx, w, sw, bias, out, nullptr, ldx, ldo, L, N, K, G, out_dtype, {}, 0};
   if (fp8_by_rows(L, N, K)) {
     // 32 rows of w share a workgroup's reads of x where that leaves most compute units one (us, 16 and 32 rows:
     // 16 tokens 6144 x 6144 15.1 and 12.6, 4099 x 4112 9.4 and 10.6; 32 tokens 27 and 19, 16.1 and 13.8)
     const bool wide = L > 8 && N >= (L > 16 ? 4096 : 6144);
-    const dim3 grid(wide ? (N + 31) / 32 : (N + 15) / 16);
-    if (L <= 8)
-      hipLaunchKernelGGL((k_fp8_rows<2, 1, 8, 6>), grid, dim3(512), 0, stream, a);
-    else if (L <= 16 && wide)
-      hipLaunchKernelGGL((k_fp8_rows<4, 2, 8, 6>), grid, dim3(512), 0, stream, a);
-    else if (L <= 16)
-      hipLaunchKernelGGL((k_fp8_rows<2, 2, 8, 3>), grid, dim3(512), 0, stream, a);
-    else if (wide)
-      hipLaunchKernelGGL((k_fp8_rows<4, 4, 8, 2>), grid, dim3(512), 0, stream, a);
-    else
-      hipLaunchKernelGGL((k_fp8_rows<2, 4, 8, 2>), grid, dim3(512), 0, stream, a);
-    return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
+    const int most = 1 << 26;  // rows of a launch, which holds fewer than 2^32 threads
+    for (; a.row0 < N; a.row0 += most) {
+      const int n = std::min(most, N - a.row0);
+      const dim3 grid(wide ? (n + 31) / 32 : (n + 15) / 16);
+      if (L <= 8)
+        hipLaunchKernelGGL((k_fp8_rows<2, 1, 8, 6>), grid, dim3(512), 0, stream, a);
+      else if (L <= 16 && wide)
+        hipLaunchKernelGGL((k_fp8_rows<4, 2, 8, 6>), grid, dim3(512), 0, stream, a);
+      else if (L <= 16)
+        hipLaunchKernelGGL((k_fp8_rows<2, 2, 8, 3>), grid, dim3(512), 0, stream, a);
+      else if (wide)
+        hipLaunchKernelGGL((k_fp8_rows<4, 4, 8, 2>), grid, dim3(512), 0, stream, a);
+      else
+        hipLaunchKernelGGL((k_fp8_rows<2, 4, 8, 2>), grid, dim3(512), 0, stream, a);
+      if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
+    }
+    return MOE_Q4_OK;
   }
   const bool codes_bf16 = fp8_wide(L, out_dtype);
   const GemmPlan p = fp8_plan(L, N, K, codes_bf16);

@@ -34,6 +34,7 @@ struct NormArgs {
   int res_f32;       // residual and total are fp32 (else x's type)
   int w_dtype, y_dtype;
   float eps;
+  long row0;         // the launch's first row
 };
 
 // LANES threads share a row, each with up to C chunks of 8 channels; chunk j
@@ -43,7 +44,7 @@ template <class TX, int LANES, int C>
 __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void k_rms_norm(NormArgs a) {
   constexpr int kThreads = LANES > 256 ? LANES : 256, kRows = kThreads / LANES;
   const int l = threadIdx.x % LANES;
-  const long row = (long)blockIdx.x * kRows + threadIdx.x / LANES;
+  const long row = a.row0 + (long)blockIdx.x * kRows + threadIdx.x / LANES;
   const bool live = row < a.T;
   const long at = live ? row : 0;
   float r[C][8];
@@ -330,16 +331,20 @@ extern "C" int moe_rms_norm(const void* x, int x_dtype, long long ldx, const voi
                           {codes ? scales : nullptr, codes ? (size_t)T * G * 4 : 0}};
   if (args_alias(outs, ins)) return MOE_Q4_ERR_ALIAS;
   NormArgs a{x, residual, weight, total, y, codes, scales, ldx, ldr, ldt, ldy, ldc, T, H, G,
-             residual && residual_dtype == MOE_Q4_DTYPE_F32, weight_dtype, y_dtype, eps};
+             residual && residual_dtype == MOE_Q4_DTYPE_F32, weight_dtype, y_dtype, eps, 0};
   const NormPlan p = norm_plan(T, H);
   const int rows = rows_of(p);
-  const dim3 grid((unsigned)(((long)T + rows - 1) / rows));
-  switch (x_dtype) {
-    case MOE_Q4_DTYPE_BF16: NORM_SWITCH(k_rms_norm, __bf16, p, grid, stream, a) break;
-    case MOE_Q4_DTYPE_F16: NORM_SWITCH(k_rms_norm, _Float16, p, grid, stream, a) break;
-    default: NORM_SWITCH(k_rms_norm, float, p, grid, stream, a) break;
+  const long most = 1L << 21;  // workgroups of a launch, which holds fewer than 2^32 threads
+  for (; a.row0 < T; a.row0 += most * rows) {
+    const dim3 grid((unsigned)std::min(most, (T - a.row0 + rows - 1) / rows));
+    switch (x_dtype) {
+      case MOE_Q4_DTYPE_BF16: NORM_SWITCH(k_rms_norm, __bf16, p, grid, stream, a) break;
+      case MOE_Q4_DTYPE_F16: NORM_SWITCH(k_rms_norm, _Float16, p, grid, stream, a) break;
+      default: NORM_SWITCH(k_rms_norm, float, p, grid, stream, a) break;
+    }
+    if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
   }
-  return launched();
+  return MOE_Q4_OK;
 }
 
 extern "C" size_t moe_rms_norm_backward_workspace_bytes(int T, int H) {

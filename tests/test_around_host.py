@@ -85,6 +85,7 @@ def fp8(x=None, ldx=None, sx=None, w=None, sw=None, bias=0, L=40, N=24, K=144, o
 @pytest.mark.parametrize("kw,status", [
     (dict(L=-1), SHAPE), (dict(N=0), SHAPE), (dict(K=0), SHAPE), (dict(ldx=128), SHAPE), (dict(ldo=23), SHAPE),
     (dict(K=136), UNSUP), (dict(L=q.MOE_Q4_LINEAR_MAX_L + 1), UNSUP), (dict(N=q.MOE_Q4_LINEAR_MAX_N + 1), UNSUP),
+    (dict(L=1 << 19, N=1 << 22, ldo=1 << 22), UNSUP),
     (dict(K=q.MOE_Q4_LINEAR_MAX_K + 16), UNSUP), (dict(ldx=q.MOE_Q4_LINEAR_MAX_LDX + 16), UNSUP), (dict(od=3), UNSUP),
     (dict(x=0), NULL), (dict(sx=0), NULL), (dict(w=0), NULL), (dict(sw=0), NULL), (dict(out=0), NULL), (dict(x=fake(0, 8)), ALIGN),
     (dict(ldx=152), ALIGN), (dict(w=fake(2, 8)), ALIGN), (dict(sx=fake(1, 2)), ALIGN), (dict(sw=fake(3, 2)), ALIGN),

@@ -82,6 +82,32 @@ def test_tile_shapes(L, N, K, out):
     assert torch.equal(got, q.moe_linear_fp8_forward(*p, out_dtype=out))
 
 
+def test_more_outputs_than_a_launch_holds():
+    N = (1 << 26) + 300
+    print("[case] fp8 launches", N, flush=True)
+    x, sx, _, _, _ = problem(2, 64, 16)
+    w = torch.randint(0, 0x7F, (N, 16), device="cuda", dtype=torch.uint8).view(R.F8)  # 0x7f is NaN
+    sw = torch.rand((N + 127) // 128, 1, device="cuda") + 0.5
+    got = q.moe_linear_fp8_forward(x.cuda(), sx.cuda(), w, sw, out_dtype=F32)
+    for a in (0, (1 << 26) - 256, (1 << 26) + 172):  # (from a block's beginning to 128 on)
+        a -= a % 128
+        ref, bound = R.linear_fp8(x, sx, w[a:a + 128].cpu(), sw[a // 128:a // 128 + 1].cpu(), None)
+        R.check(got[:, a:a + 128], ref, bound)
+    assert torch.isfinite(got).all()
+
+
+def test_offsets_past_32_bits():
+    L, K = 600_000, 8192
+    print("[case] fp8 offsets", L, K, flush=True)
+    x = torch.randint(0, 0x7F, (L, K), device="cuda", dtype=torch.uint8).view(R.F8)
+    sx = torch.rand(L, K // 128, device="cuda") + 0.5
+    _, _, w, sw, _ = problem(1, 8, K)
+    got = q.moe_linear_fp8_forward(x, sx, w.cuda(), sw.cuda(), out_dtype=F32)
+    for i in (slice(0, 70), slice(L // 2, L // 2 + 70), slice(L - 70, L)):
+        ref, bound = R.linear_fp8(x[i].cpu(), sx[i].cpu(), w, sw, None)
+        R.check(got[i], ref, bound)
+
+
 @pytest.mark.parametrize("L", [4, 200])
 def test_nan_codes_and_scales_stay_with_their_outputs(L):
     x, sx, w, sw, _ = problem(L, 300, 640)

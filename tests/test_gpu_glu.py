@@ -147,6 +147,64 @@ def test_autograd(recompute, T):
         assert all(t.grad is None for i, t in enumerate(one) if i != which)
 
 
+def test_offsets_past_32_bits():
+    """Rows of x past 4 GB.  dw's sum of 300000 terms a result: (T + 24) 2^-24 of
+    their magnitudes, as everywhere."""
+    T, H, I = 300_000, 8192, 8
+    print("[case] glu offsets", T, H, I, flush=True)
+    _, wg, wu, _ = problem(8, H, I, BF16)
+    x = torch.empty(T, H, device="cuda", dtype=BF16)
+    for i in range(0, T, 20_000):
+        x[i:i + 20_000] = torch.randn(min(20_000, T - i), H, device="cuda")
+    dh = torch.randn(T, I, device="cuda").to(BF16)
+    d = [x, wg.cuda(), wu.cuda()]
+    h = q.moe_glu(*d)
+    dx, dwg, dwu = q.moe_glu_backward(*d, dh)
+    wsum, bsum, mag = [0.0, 0.0], [0.0, 0.0], 0.0
+    for i in range(0, T, 20_000):
+        part = slice(i, min(i + 20_000, T))
+        (rx, *rw), (bx, *bw) = R.glu_backward(x[part], d[1], d[2], dh[part])
+        for k in range(2):
+            wsum[k] = wsum[k] + rw[k]
+            bsum[k] = bsum[k] + bw[k]
+        if i in (0, 140_000, 280_000):
+            R.check(dx[part], rx.cpu(), bx.cpu(), BF16)
+            _, _, rh, _, _, bh = R.glu(x[part], d[1], d[2])
+            R.check(h[part], rh.cpu(), bh.cpu(), BF16)
+        g, u, *_ = R.glu(x[part], d[1], d[2])
+        s = torch.sigmoid(g)
+        for e in (dh[part].double() * u * s * (1 + g * (1 - s)), dh[part].double() * g * s):
+            mag = mag + e.abs().T @ x[part].double().abs()
+    for k, got in enumerate((dwg, dwu)):  # (a part's own bound has its number of tokens' roundings alone)
+        R.check(got, wsum[k].cpu(), (bsum[k] + T * R.U * mag).cpu(), BF16)
+
+
+def test_a_norm_and_the_block_as_they_are_used():
+    """Norm with the residual, the block behind it and the sum carried on, and all
+    gradients through autograd; each step against 64 bits at its own inputs."""
+    T, H, I = 203, 264, 136
+    x, wg, wu, dh = problem(T, H, I, BF16)
+    g = torch.Generator().manual_seed(3)
+    res, w, dtotal = torch.randn(T, H, generator=g), 1 + torch.randn(H, generator=g) / 4, torch.randn(T, H, generator=g)
+    leaves = [t.cuda().requires_grad_() for t in (x, res, w, wg, wu)]
+    y, total = q.moe_rms_norm(leaves[0], leaves[2], leaves[1])
+    y.retain_grad()
+    h = q.moe_glu(y, leaves[3], leaves[4])
+    torch.autograd.backward([h, total], [dh.cuda(), dtotal.cuda()])
+    sums = R.total_of(x, res)
+    assert torch.equal(total.detach().cpu(), sums)
+    R.check(y.detach(), *R.norm(sums, w, 1e-6), BF16)
+    mid = y.detach().cpu()
+    R.check(h.detach(), *(R.glu(mid, wg, wu)[i] for i in (2, 5)), BF16)
+    refs, bounds = R.glu_backward(mid, wg, wu, dh)
+    for t, ref, bound in zip((y, leaves[3], leaves[4]), refs, bounds):
+        R.check(t.grad, ref, bound, BF16)
+    dx, bound, dw, wbound = R.norm_backward(sums, w, y.grad.cpu(), dtotal, 1e-6)
+    R.check(leaves[1].grad, dx, bound)
+    R.check(leaves[0].grad, dx, bound, BF16)
+    R.check(leaves[2].grad, dw, wbound)
+
+
 @pytest.mark.parametrize("T", [5, 140])
 def test_infinities_and_nan_stay_with_their_rows(T):
     x, wg, wu, _ = problem(T, 200, 64, BF16)

@@ -107,6 +107,18 @@ def test_norm_offsets_past_32_bits():
     R.check_codes(codes, scales, v, slack=4 * R.U)
 
 
+def test_norm_of_more_rows_than_a_launch_holds():
+    T = (1 << 25) + 40  # of 8 channels, 16 a workgroup, 2^21 workgroups a launch
+    print("[case] norm launches", T, flush=True)
+    x = torch.randint(1, 5, (T, 8), device="cuda", dtype=torch.int8).to(BF16)
+    got = q.moe_rms_norm(x)
+    for i in (slice(0, 40), slice((1 << 25) - 40, (1 << 25) + 40)):
+        y, bound = R.norm(x[i].cpu(), None, 1e-6)
+        R.check(got[i], y, bound, BF16)
+    v = torch.rsqrt(x.float().square().mean(1) + 1e-6)
+    assert ((got[:, 0].float() - x[:, 0].float() * v).abs() <= 2.0 ** -8 * got[:, 0].float() * 1.01).all()
+
+
 def test_norm_zeros_infinities_and_nan():
     x = rand((6, 384), F32, 5)
     x[1] = 0
