@@ -64,12 +64,12 @@ __device__ __forceinline__ gemm_f32x4 gemm_product(const GemmFrag& a, const Gemm
 
 // ---- many tokens ----
 
-// MT x NT tiles a wave, of 32 x 32 results (16-bit types) or 16 x 16 (E4M3),
-// and WM x WN waves: kTok tokens x kRows rows of B.
+// MT x NT tiles of 16 x 16 results a wave, and WM x WN waves: kTok tokens x
+// kRows rows of B.
 template <int KIND_, int MT_, int NT_, int WM_, int WN_>
 struct GemmShape {
-  static constexpr int KIND = KIND_, MT = MT_, NT = NT_, WM = WM_, WN = WN_, kTile = gemm_scaled(KIND) ? 16 : 32;
-  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves, kTok = kTile * MT * WM, kRows = kTile * NT * WN;
+  static constexpr int KIND = KIND_, MT = MT_, NT = NT_, WM = WM_, WN = WN_;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves, kTok = 16 * MT * WM, kRows = 16 * NT * WN;
   static constexpr int kScaleRows = (kRows + 127) / 128;
 };
 
@@ -156,16 +156,18 @@ __device__ __forceinline__ void gemm_copy(const unsigned char* from, unsigned ch
 // different banks (of 64).  Of an operand with the axis across, it holds the
 // step's 64 rows of 128 bytes (64 tokens) one after another, then the next
 // tokens'; 16 lanes read 4 rows of 32 bytes and get a column of them each
-// (ds_read_b64_tr_b16), 32 lanes 4 rows of 64 bytes, whose halves are swapped
-// in each second pair of rows, for the banks again.
-// A wave's 32 x 32 x 16 instructions go through half a step (its chunks 0 to 3
-// or 4 to 7) at a time, while the next half's operands are on their way into
-// registers; so the waves have read a step when its second half begins, meet
-// there, once a step, and that half carries the copies of the step BUFFERS on
-// into the LDS that became free.  Four waves of 128 x 128 results each: their
-// sums fill the accumulator registers, and they read two thirds of what eight
-// of 128 x 64 would.  (16 x 16 x 32 instructions read twice the registers, and
-// behind each one's 16 clocks a copy's issue, about 30, shows.)
+// (ds_read_b64_tr_b16); 32 lanes read rows k to k + 3 and k + 8 to k + 11, so
+// chunk c of row k lies at place c ^ (k / 2 % 2 * 4 + k / 8 % 2 * 2).
+//
+// A wave's instructions go through half a step (its chunks 0 to 3 or 4 to 7) at
+// a time, while the next half's operands are on their way into registers; so
+// the waves have read a step when its second half begins, meet there, once a
+// step, and that half carries the copies of the step BUFFERS on into the LDS
+// that became free.  Four waves of 128 x 128 results each: their sums fill the
+// accumulator registers, and they read two thirds of what eight of 128 x 64
+// would.  The instruction is of 16 x 16 x 32: one of 32 x 32 x 16 reads and
+// writes twice the sums for a product, and the card's power, which bounds large
+// products, lets it do 1800 and not 2050 TFLOP/s (operands in registers).
 //
 // Two buffers are enough where a step's instructions take 2048 clocks.  Small
 // tiles have more, since what is on its way must last a memory's latency, about
@@ -195,7 +197,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, Source& sourc
   constexpr int MT = S::MT, NT = S::NT, KIND = S::KIND, kPass = S::kThreads / 8;
   constexpr int kCb = S::kRows / kPass, kCt = S::kTok / kPass, kCopies = kCb + kCt;
   constexpr int kReadsX = kTokT ? 2 * MT : MT, kReadsW = kRowT ? 2 * NT : NT;
-  constexpr int kReads = 2 * (kReadsX + kReadsW), kMul = 2 * MT * NT;  // of half a step
+  constexpr int kReads = kReadsX + kReadsW, kMul = MT * NT;  // of half a step
   constexpr int kEarly = kMul * 5 / 8;  // instructions that the reads are spread over: the last have a latency's time
   static_assert(S::kRows % 64 == 0 && S::kTok % 64 == 0 && kPass == 32, "copies of whole passes");
   // each an object of its own: the compiler then knows that reads of one do not wait for copies into another
@@ -207,15 +209,16 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, Source& sourc
   auto rows_of = [&](int i) __attribute__((always_inline)) { return i == 0 ? b0 : i == 1 ? b1 : i == 2 ? b2 : b3; };
   auto toks_of = [&](int i) __attribute__((always_inline)) { return i == 0 ? t0 : i == 1 ? t1 : i == 2 ? t2 : t3; };
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n32 = lane & 31, kh = lane >> 5;
+  const int n16 = lane & 15, kb = lane >> 4;
   const int wm = wave % S::WM, wn = wave / S::WM;
   const int chunk = ((tid & 7) ^ ((tid >> 4) & 7)) * 16;
-  const int along = (n32 << 7) + ((kh ^ ((n32 >> 1) & 7)) << 4);
-  const int across = ((8 * kh + (lane >> 2 & 3)) << 7) + ((lane >> 3 & 1) << 6) + ((lane >> 4 & 1) << 5) + ((lane & 3) << 3);
-  // a wave's first tile, and its first two with the axis across: tiles are halves of a row of 64 tokens
-  const auto half = [&](int tile) __attribute__((always_inline)) { return tile / 2 * (64 * kGemmStep) + (across ^ (tile % 2 << 6)); };
-  const int tok_at = wm * MT * 32 * kGemmStep + along, tok_half[2] = {half(wm * MT), half(wm * MT + 1)};
-  const int row_at = wn * NT * 32 * kGemmStep + along, row_half[2] = {half(wn * NT), half(wn * NT + 1)};
+  const int along = (n16 << 7) + ((kb ^ (n16 >> 1)) << 4);
+  const int across = ((8 * kb + (lane >> 2 & 3)) << 7) + ((lane >> 3 & 1) << 6) + ((kb & 1) << 5) + ((lane & 3) << 3);
+  // a wave's first tile, and its first four with the axis across: tiles are quarters of a row of 64 tokens
+  const auto quarter = [&](int tile) __attribute__((always_inline)) { return tile / 4 * (64 * kGemmStep) + (across ^ (tile % 4 << 5)); };
+  const int tok0 = wm * MT, row0 = wn * NT;
+  const int tok_at = tok0 * 16 * kGemmStep + along, tok_q[4] = {quarter(tok0), quarter(tok0 + 1), quarter(tok0 + 2), quarter(tok0 + 3)};
+  const int row_at = row0 * 16 * kGemmStep + along, row_q[4] = {quarter(row0), quarter(row0 + 1), quarter(row0 + 2), quarter(row0 + 3)};
 
   GemmQueue queue(tiles);
   GemmPlace at, now;
@@ -256,7 +259,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, Source& sourc
   auto start = [&]() __attribute__((always_inline)) {  // the next tile and its first steps
     at = queue.take(tiles);
     source.set(at);
-    const int mine = gemm_opaque(tid / 8), column = gemm_opaque((tid & 7) ^ (tid >> 4 & 1) << 2);
+    const int mine = gemm_opaque(tid / 8), column = gemm_opaque((tid & 7) ^ (tid >> 4 & 1) << 2 ^ (tid >> 6 & 1) << 1);
     if constexpr (kRowT) {
 #pragma unroll
       for (int c = 0; c < kCb / 2; ++c) off_b[c] = source.row_col(8 * c + column);
@@ -282,38 +285,35 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, Source& sourc
       for (int c = 0; c < kCopies; ++c) copy(i, c);
     }
   };
-  // operands of half h, of its instructions' k from 16 s on: chunk 4 h + 2 s + kh of a row
-  gemm_i32x4 w[2][2][NT], x[2][2][MT];
-  gemm_f32x16 acc[MT][NT];
-  auto read_half = [&](gemm_i32x4& to, const unsigned char* lds, const int (&half)[2], int h, int s, int j) __attribute__((always_inline)) {
-    const int tile = j / 2, part = j % 2;  // (rows 8 kh + 4 part on of the instruction's 16)
-    const uint2 v = gemm_read_column(lds + half[tile % 2] + (tile / 2 * 64 + (2 * h + s) * 16 + part * 4) * kGemmStep);
+  gemm_i32x4 w[2][NT], x[2][MT];  // of half h: chunk 4 h + kb of a row
+  gemm_f32x4 acc[MT][NT];
+  auto read_across = [&](gemm_i32x4& to, const unsigned char* lds, const int (&q)[4], int h, int j) __attribute__((always_inline)) {
+    const int tile = j / 2, part = j % 2;  // (rows 8 kb + 4 part on of the half's 32)
+    const uint2 v = gemm_read_column(lds + q[tile % 4] + (tile / 4 * 64 + h * 32 + part * 4) * kGemmStep);
     to[2 * part] = (int)v.x;
     to[2 * part + 1] = (int)v.y;
   };
-  auto read = [&](int from, int h, int j) __attribute__((always_inline)) {
-    const int s = j / (kReadsX + kReadsW), r = j % (kReadsX + kReadsW), q = r - kReadsW, flip = 64 * h + 32 * s;
+  auto read = [&](int from, int h, int r) __attribute__((always_inline)) {
+    const int q = r - kReadsW;
     if (r < kReadsW) {
       if constexpr (kRowT)
-        read_half(w[h][s][r / 2], rows_of(from), row_half, h, s, r);
+        read_across(w[h][r / 2], rows_of(from), row_q, h, r);
       else
-        w[h][s][r] = *reinterpret_cast<const gemm_i32x4*>(rows_of(from) + (row_at ^ flip) + r * 32 * kGemmStep);
+        w[h][r] = *reinterpret_cast<const gemm_i32x4*>(rows_of(from) + (row_at ^ 64 * h) + r * 16 * kGemmStep);
     } else {
       if constexpr (kTokT)
-        read_half(x[h][s][q / 2], toks_of(from), tok_half, h, s, q);
+        read_across(x[h][q / 2], toks_of(from), tok_q, h, q);
       else
-        x[h][s][q] = *reinterpret_cast<const gemm_i32x4*>(toks_of(from) + (tok_at ^ flip) + q * 32 * kGemmStep);
+        x[h][q] = *reinterpret_cast<const gemm_i32x4*>(toks_of(from) + (tok_at ^ 64 * h) + q * 16 * kGemmStep);
     }
   };
   auto multiply = [&](int h, int j, bool first) __attribute__((always_inline)) {
-    const int s = j / (MT * NT), mt = j % (MT * NT) / NT, nt = j % NT;
-    const gemm_f32x16 c = first && s == 0 ? gemm_f32x16{} : acc[mt][nt];
+    const int mt = j / NT, nt = j % NT;
+    const gemm_f32x4 c = first ? gemm_f32x4{} : acc[mt][nt];
     if constexpr (KIND == kGemmBf16)
-      acc[mt][nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(gemm_bf16x8, w[h][s][nt]),
-                                                            __builtin_bit_cast(gemm_bf16x8, x[h][s][mt]), c, 0, 0, 0);
+      acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(gemm_bf16x8, w[h][nt]), __builtin_bit_cast(gemm_bf16x8, x[h][mt]), c, 0, 0, 0);
     else
-      acc[mt][nt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(gemm_f16x8, w[h][s][nt]),
-                                                           __builtin_bit_cast(gemm_f16x8, x[h][s][mt]), c, 0, 0, 0);
+      acc[mt][nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(gemm_f16x8, w[h][nt]), __builtin_bit_cast(gemm_f16x8, x[h][mt]), c, 0, 0, 0);
   };
   // half a step, reading the next one, of buffer `from`; the copies into `to` with it (-1: none)
   auto pass = [&](int h, int from, int to, bool first = false) __attribute__((always_inline)) {
@@ -339,12 +339,9 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, Source& sourc
     const int left = i < now.count ? source.left(now.step0 + i) - h * 64 : 0;
     if (left < 64) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int nt = 0; nt < NT; ++nt) keep(w[h][nt], left - 16 * kb);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) keep(w[h][s][nt], left - 32 * s - 16 * kh);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) keep(x[h][s][mt], left - 32 * s - 16 * kh);
-      }
+      for (int mt = 0; mt < MT; ++mt) keep(x[h][mt], left - 16 * kb);
     }
   };
 
@@ -676,18 +673,13 @@ __device__ __forceinline__ void gemm_join_waves(float (&lds)[WAVES][J][G][64], c
 // ---- results ----
 
 // A lane's sums go straight to memory, four neighbours of a token's results at
-// a time: of a 16 x 16 tile those from 4 (lane / 16) on of token lane % 16, of
-// a 32 x 32 tile those from 8 g + 4 (lane / 32) on of token lane % 32, g = 0 to
-// 3.
+// a time: of a 16 x 16 tile those from 4 (lane / 16) on of token lane % 16.
 
 // Results in vector registers from here on, and no sooner: of all tiles at
 // once they would not fit beside the accumulator registers.
 __device__ __forceinline__ gemm_f32x4 gemm_here(gemm_f32x4 v) {
   asm volatile("" : "+v"(v));
   return v;
-}
-__device__ __forceinline__ gemm_f32x4 gemm_four(const gemm_f32x16& v, int g) {
-  return gemm_here(gemm_f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]});
 }
 
 template <class T>
@@ -696,28 +688,11 @@ __device__ __forceinline__ uint2 gemm_pack4(gemm_f32x4 v) {
   return __builtin_bit_cast(uint2, t4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]});
 }
 
-// Two fours as 16-bit numbers, made eight neighbours of a lane, so that lanes
-// write 16 bytes.  Of 32 x 32 tiles: a's and b's halves, (a0 a1) and (b0 b1),
-// swapped to (a0 b0) and (a1 b1): the lower lanes have a, the upper ones b.
-__device__ __forceinline__ uint4 gemm_eight32(uint2 a, uint2 b) {
-  const auto x = __builtin_amdgcn_permlane32_swap(a.x, b.x, false, false), y = __builtin_amdgcn_permlane32_swap(a.y, b.y, false, false);
-  return make_uint4(x[0], y[0], x[1], y[1]);
-}
-// 16 bytes a lane of 32 x 32 tiles, p and q, from two bytes' places of a
-// token's results (the upper lanes' follow the lower lanes'): swapped so that
-// p is of the tokens lane % 16 and q of the 16 after these, at place
-// gemm_place4() of 4.  A token's four lanes write 64 bytes: of 32 each, the
-// writes' number and not their bytes bound the stores (5 us of a tile).
-__device__ __forceinline__ void gemm_spread(uint4& p, uint4& q) {
-  const auto x = __builtin_amdgcn_permlane16_swap(p.x, q.x, false, false), y = __builtin_amdgcn_permlane16_swap(p.y, q.y, false, false);
-  const auto z = __builtin_amdgcn_permlane16_swap(p.z, q.z, false, false), w = __builtin_amdgcn_permlane16_swap(p.w, q.w, false, false);
-  p = make_uint4(x[0], y[0], z[0], w[0]);
-  q = make_uint4(x[1], y[1], z[1], w[1]);
-}
-__device__ __forceinline__ int gemm_place4(int lane) { return (lane >> 4 & 1) * 2 + (lane >> 5); }
-
-// Of 16 x 16 tiles side by side: rows of 16 lanes (a0 a1 a2 a3) and (b0 b1 b2
-// b3) swapped to (a0 a2 b0 b2) and (a1 a3 b1 b3): eight from 8 (lane / 16) on.
+// Fours of two tiles as 16-bit numbers, made eight neighbours of a lane, so that
+// lanes write 16 bytes and a token's four lanes 64: of 32 each, the writes'
+// number and not their bytes bound the stores (5 us of a tile).  Rows of 16
+// lanes (a0 a1 a2 a3) and (b0 b1 b2 b3) are swapped to (a0 a2 b0 b2) and (a1 a3
+// b1 b3): eight from 8 (lane / 16) on of a's 16 and then b's.
 __device__ __forceinline__ uint4 gemm_eight16(uint2 a, uint2 b) {
   const auto x = __builtin_amdgcn_permlane32_swap(a.x, b.x, false, false), y = __builtin_amdgcn_permlane32_swap(a.y, b.y, false, false);
   const auto u = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false), v = __builtin_amdgcn_permlane16_swap(y[0], y[1], false, false);

@@ -88,58 +88,45 @@ __global__ __launch_bounds__(64 * WM * WN) void k_glu_tiles(GluArgs a) {
   typedef typename GluType<KIND>::type T16;
   static_assert(S::kThreads / 8 == 32, "GluSource's rows");
   GluSource<S> source{a};
-  gemm_tiles<S>(a.tiles, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63);
-    const int place = gemm_place4(lane), t0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 15);
-    const int n0 = p.row * (S::kRows / 2) + wave / WM * NT * 16;
+  gemm_tiles<S>(a.tiles, source, [&](const GemmPlace& p, const gemm_f32x4 (&acc)[MT][NT]) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63), kb = lane >> 4;
+    const int t0 = p.tok * S::kTok + wave % WM * MT * 16 + (lane & 15), n0 = p.row * (S::kRows / 2) + wave / WM * NT * 8;
     const bool split = a.tiles.splits > 1;
     float* keep = split ? a.part + (size_t)p.split * 2 * a.T * a.I : a.saved;
     T16* h = split ? nullptr : static_cast<T16*>(a.h);
     // (I is a multiple of 8: neighbours are all there or none)
-    const auto keep4 = [&](size_t row, int t, int n, uint4 v) __attribute__((always_inline)) {
-      if (t < a.T && n < a.I) gemm_put32(keep + (row + t) * a.I + n, 4, __builtin_bit_cast(gemm_f32x4, v));
+    const auto keep4 = [&](size_t row, int t, int n, gemm_f32x4 v) __attribute__((always_inline)) {
+      if (t < a.T && n < a.I) gemm_put32(keep + (row + t) * a.I + n, 4, v);
     };
     const auto put8 = [&](int t, int n, uint4 v) __attribute__((always_inline)) {
       if (t < a.T && n < a.I) gemm_put16(h + (size_t)t * a.ldh + n, 8, v);
     };
+    uint2 alone = make_uint2(0, 0);  // of an odd number of pairs the last one's, for the next tokens
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const int t = t0 + 32 * mt;
-      uint4 even = make_uint4(0, 0, 0, 0);
+      const int t = t0 + 16 * mt;
+      uint2 before = make_uint2(0, 0);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint2 out[2];
-        uint4 kept[2][2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const gemm_f32x4 gate = gemm_four(acc[mt][nt], g), up = gemm_four(acc[mt][nt], g + 2);
-          kept[0][g] = __builtin_bit_cast(uint4, gate);
-          kept[1][g] = __builtin_bit_cast(uint4, up);
-          gemm_f32x4 v;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = gate[i] * glu_sigmoid(gate[i]) * up[i];
-          out[g] = gemm_pack4<T16>(v);
-        }
+      for (int q = 0; q < NT / 2; ++q) {
+        const gemm_f32x4 gate = gemm_here(acc[mt][2 * q]), up = gemm_here(acc[mt][2 * q + 1]);
         if (keep) {
-#pragma unroll
-          for (int up = 0; up < 2; ++up) {
-            gemm_spread(kept[up][0], kept[up][1]);
-            const int n = n0 + 16 * nt + 4 * place;
-            keep4(up ? a.T : 0, t, n, kept[up][0]);
-            keep4(up ? a.T : 0, t + 16, n, kept[up][1]);
-          }
+          keep4(0, t, n0 + 16 * q + 4 * kb, gate);
+          keep4(a.T, t, n0 + 16 * q + 4 * kb, up);
         }
-        uint4 q = gemm_eight32(out[0], out[1]);
-        if (!h) continue;
-        if (nt % 2 == 0 && nt + 1 < NT) {
-          even = q;
-        } else if (nt % 2) {
-          gemm_spread(even, q);
-          const int n = n0 + 16 * (nt - 1) + 8 * place;
-          put8(t, n, even);
-          put8(t + 16, n, q);
-        } else {  // one tile left
-          put8(t + (lane & 16), n0 + 16 * nt + 8 * (lane >> 5), q);
+        gemm_f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = gate[i] * glu_sigmoid(gate[i]) * up[i];
+        const uint2 out = gemm_pack4<T16>(v);
+        if (q % 2) {
+          const uint4 eight = gemm_eight16(before, out);
+          if (h) put8(t, n0 + 16 * (q - 1) + 8 * kb, eight);
+        } else if (q + 1 < NT / 2) {
+          before = out;
+        } else if (mt % 2) {
+          const uint4 eight = gemm_eight16(alone, out);
+          if (h) put8(t - 16 + 16 * (kb >> 1), n0 + 16 * q + 8 * (kb & 1), eight);
+        } else {
+          alone = out;
         }
       }
     }
@@ -248,42 +235,27 @@ __global__ __launch_bounds__(64 * WM * WN) void k_glu_mm(GluMmArgs a) {
   using S = GemmShape<KIND, MT, NT, WM, WN>;
   typedef typename GluType<KIND>::type T16;
   std::conditional_t<DW, GluDwSource<S>, GluDxSource<S>> source{a};
-  gemm_tiles<S>(a.tiles, source, [&](const GemmPlace& p, const gemm_f32x16 (&acc)[MT][NT]) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63);
-    const int place = gemm_place4(lane), m0 = p.tok * S::kTok + wave % WM * MT * 32 + (lane & 15);
-    const int n0 = p.row * S::kRows + wave / WM * NT * 32;
+  gemm_tiles<S>(a.tiles, source, [&](const GemmPlace& p, const gemm_f32x4 (&acc)[MT][NT]) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63), kb = lane >> 4;
+    const int m0 = p.tok * S::kTok + wave % WM * MT * 16 + (lane & 15), n0 = p.row * S::kRows + wave / WM * NT * 16;
     float* part = a.tiles.splits > 1 ? a.part + (size_t)p.split * a.M * a.N : nullptr;
-    // (N is a multiple of 8: neighbours are all there or none)
-    const auto put4 = [&](int m, int n, uint4 v) __attribute__((always_inline)) {
-      if (m < a.M && n < a.N) gemm_put32(part + (size_t)m * a.N + n, 4, __builtin_bit_cast(gemm_f32x4, v));
-    };
-    const auto put8 = [&](int m, int n, uint4 v) __attribute__((always_inline)) {
-      if (m < a.M && n < a.N)
-        gemm_put16(static_cast<T16*>(m < a.cut ? a.out0 : a.out1) + (size_t)(m < a.cut ? m : m - a.cut) * a.ldo + n, 8, v);
-    };
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const int m = m0 + 32 * mt;
+      const int m = m0 + 16 * mt;
+      const size_t row = (size_t)(m < a.cut ? m : m - a.cut) * a.ldo;
+      T16* to = static_cast<T16*>(m < a.cut ? a.out0 : a.out1) + row;
+      // (N is a multiple of 8: neighbours are all there or none)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; nt += 2) {
+        const gemm_f32x4 u = gemm_here(acc[mt][nt]), v = gemm_here(acc[mt][nt + 1]);
         if (part) {
-#pragma unroll
-          for (int g = 0; g < 4; g += 2) {
-            uint4 u = __builtin_bit_cast(uint4, gemm_four(acc[mt][nt], g)), v = __builtin_bit_cast(uint4, gemm_four(acc[mt][nt], g + 1));
-            gemm_spread(u, v);
-            const int n = n0 + 32 * nt + 8 * g + 4 * place;
-            put4(m, n, u);
-            put4(m + 16, n, v);
-          }
+          const int n = n0 + 16 * nt + 4 * kb;
+          if (m < a.M && n < a.N) gemm_put32(part + (size_t)m * a.N + n, 4, u);
+          if (m < a.M && n + 16 < a.N) gemm_put32(part + (size_t)m * a.N + n + 16, 4, v);
         } else {
-          uint4 q[2];
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-            q[g] = gemm_eight32(gemm_pack4<T16>(gemm_four(acc[mt][nt], 2 * g)), gemm_pack4<T16>(gemm_four(acc[mt][nt], 2 * g + 1)));
-          gemm_spread(q[0], q[1]);
-          const int n = n0 + 32 * nt + 8 * place;
-          put8(m, n, q[0]);
-          put8(m + 16, n, q[1]);
+          const int n = n0 + 16 * nt + 8 * kb;
+          const uint4 q = gemm_eight16(gemm_pack4<T16>(u), gemm_pack4<T16>(v));
+          if (m < a.M && n < a.N) gemm_put16(to + n, 8, q);
         }
       }
     }
@@ -345,12 +317,12 @@ int glu_forward_kind(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t
   }
   const dim3 grid(p.workgroups);
   switch (p.shape) {
-    case kGemm256x256: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm256x192: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm128x256: hipLaunchKernelGGL((k_glu_tiles<KIND, 2, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm128x192: hipLaunchKernelGGL((k_glu_tiles<KIND, 2, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm128x128: hipLaunchKernelGGL((k_glu_tiles<KIND, 2, 2, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    default: hipLaunchKernelGGL((k_glu_tiles<KIND, 2, 1, 1, 4>), grid, dim3(256), 0, stream, a); break;
+    case kGemm256x256: hipLaunchKernelGGL((k_glu_tiles<KIND, 8, 8, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm256x192: hipLaunchKernelGGL((k_glu_tiles<KIND, 8, 6, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x256: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 8, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x192: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 6, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x128: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    default: hipLaunchKernelGGL((k_glu_tiles<KIND, 4, 2, 1, 4>), grid, dim3(256), 0, stream, a); break;
   }
   if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
   if (p.tiles.splits > 1) {
@@ -364,12 +336,12 @@ template <int KIND, bool DW>
 void glu_mm_launch(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream) {
   const dim3 grid(p.workgroups);
   switch (p.shape) {
-    case kGemm256x256: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm256x192: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 4, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm128x256: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 2, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm128x192: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 2, 3, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    case kGemm128x128: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 2, 2, 2, 2>), grid, dim3(256), 0, stream, a); break;
-    default: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 2, 1, 1, 4>), grid, dim3(256), 0, stream, a); break;
+    case kGemm256x256: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 8, 8, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm256x192: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 8, 6, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x256: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 4, 8, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x192: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 4, 6, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    case kGemm128x128: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 4, 4, 2, 2>), grid, dim3(256), 0, stream, a); break;
+    default: hipLaunchKernelGGL((k_glu_mm<KIND, DW, 4, 2, 1, 4>), grid, dim3(256), 0, stream, a); break;
   }
 }
 
