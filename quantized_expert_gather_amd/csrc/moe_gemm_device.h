@@ -198,7 +198,7 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, Source& sourc
   constexpr int kCb = S::kRows / kPass, kCt = S::kTok / kPass, kCopies = kCb + kCt;
   constexpr int kReadsX = kTokT ? 2 * MT : MT, kReadsW = kRowT ? 2 * NT : NT;
   constexpr int kReads = kReadsX + kReadsW, kMul = MT * NT;  // of half a step
-  constexpr int kEarly = kMul * 5 / 8;  // instructions that the reads are spread over: the last have a latency's time
+  constexpr int kEarly = kMul * 7 / 8;  // instructions that the reads are spread over: the last have a latency's time
   static_assert(S::kRows % 64 == 0 && S::kTok % 64 == 0 && kPass == 32, "copies of whole passes");
   // each an object of its own: the compiler then knows that reads of one do not wait for copies into another
   __shared__ __attribute__((aligned(1024))) unsigned char b0[S::kRows * kGemmStep], b1[S::kRows * kGemmStep], b2[S::kRows * kGemmStep],

@@ -22,8 +22,9 @@ struct GemmCosts {
   float step[kGemmShapes], more[kGemmShapes], end[kGemmShapes];
   int held[kGemmShapes];
 };
-// 16-bit products, measured with 256 and 1024 tiles of 8, 32 and 128 steps.
-constexpr GemmCosts kGemmCosts16 = {{1.49f, 1.28f, 0.82f, 0.635f, 0.466f, 0.304f}, {}, {5.8f, 3.5f, 7.0f, 5.9f, 3.7f, 2.5f}, {1, 1, 1, 1, 1, 1}};
+// 16-bit products, measured with 256 and 1024 tiles of 8, 32 and 128 steps (the
+// mean of the forward's and of dx's, which are up to a tenth apart).
+constexpr GemmCosts kGemmCosts16 = {{1.55f, 1.27f, 0.91f, 0.67f, 0.484f, 0.325f}, {}, {4.5f, 3.4f, 4.4f, 3.9f, 2.8f, 2.1f}, {1, 1, 1, 1, 1, 1}};
 
 // For M x N results over `steps` steps: the shape and the split of K with the
 // least sum.  Splits fill the card where the tiles do not; their sums go

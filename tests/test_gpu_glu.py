@@ -61,7 +61,7 @@ SHAPES = [(2065, 72, 2704), (131, 8272, 6304), (1537, 64, 1264), (5538, 5760, 14
           (2739, 672, 5816), (1681, 2360, 64), (5575, 272, 3112), (2720, 2160, 200), (2776, 648, 3112), (1944, 2064, 72),
           (4287, 136, 2992), (1233, 1544, 64), (2694, 136, 1696), (38, 64, 712), (34, 2136, 2696), (4344, 200, 8208),
           (39, 1416, 1368), (5932, 144, 5688), (459, 1360, 2112), (5937, 200, 4264), (193, 1168, 1656), (3529, 136, 4232),
-          (37, 904, 1032), (3481, 152, 1432), (1540, 64, 72)]
+          (37, 904, 1032), (3481, 152, 1432), (1540, 64, 72), (134, 7056, 6496), (5436, 144, 5472)]
 
 
 @pytest.mark.parametrize("T,H,I", SHAPES)
