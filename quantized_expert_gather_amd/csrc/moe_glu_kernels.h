@@ -4,7 +4,7 @@
 //
 //   forward   g = x Wg^T, u = x Wu^T, h = silu(g) u: one product whose tile takes
 //             the same rows of Wg and Wu, so that a lane holds g and u of a result
-//   backward  dg = dh u silu'(g), du = dh silu(g), side by side as D [T, 2I];
+//   backward  dg = dh u silu'(g), du = dh silu(g), side by side as D;
 //             dx = D [Wg; Wu], [dWg; dWu] = D^T x
 // The backward's products have their sums along the other axis of the weights,
 // or of both D and x, which the tiles read as they are.
@@ -38,7 +38,8 @@ struct GluMmArgs {
   void *out0, *out1;
   float* part;                       // split K: [splits][M][N]
   long long lda, ldb, ldo;           // ldo in elements
-  int M, N, K, steps, cut;           // K and steps of b0
+  int M, N, K, steps, cut;           // K of b0, and its steps
+  int ip;                            // of D: du lies ip elements behind dg
   GemmTiles tiles;
 };
 
@@ -47,9 +48,9 @@ int glu_forward_bf16(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t
 int glu_forward_f16(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t stream);
 int glu_mm_bf16(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream);
 int glu_mm_f16(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream);
-// D [T][2I] from g, u and dh (lddh elements apart).
-int glu_grad_bf16(const float* saved, const void* dh, long long lddh, int T, int I, void* d, hipStream_t stream);
-int glu_grad_f16(const float* saved, const void* dh, long long lddh, int T, int I, void* d, hipStream_t stream);
+// D [T][2 ip], dg and du of I each, from g, u and dh (lddh elements apart).
+int glu_grad_bf16(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d, hipStream_t stream);
+int glu_grad_f16(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d, hipStream_t stream);
 
 #ifdef MOE_GLU_INST
 
@@ -203,7 +204,7 @@ struct GluDxSource {
     col = p.row * S::kRows;
   }
   __device__ __forceinline__ int part(int s) const { return s >= a.steps ? s - a.steps : s; }
-  __device__ __forceinline__ uint32_t k(int s) const { return (uint32_t)(part(s) * kGemmStep + (s >= a.steps ? 2 * a.K : 0)); }
+  __device__ __forceinline__ uint32_t k(int s) const { return (uint32_t)(part(s) * kGemmStep + (s >= a.steps ? 2 * a.ip : 0)); }
   __device__ __forceinline__ int left(int s) const { return 2 * a.K - part(s) * kGemmStep; }
   __device__ __forceinline__ uint32_t tok_off(int r) const { return (uint32_t)min(r, toks) * (uint32_t)a.lda; }
   __device__ __forceinline__ const unsigned char* row_at(int s) const { return (s >= a.steps ? a.b1 : a.b0) + (size_t)part(s) * 64 * a.ldb; }
@@ -224,7 +225,10 @@ struct GluDwSource {
   __device__ __forceinline__ int left(int s) const { return 2 * a.K - s * kGemmStep; }
   __device__ __forceinline__ const unsigned char* tok_at(int s) const { return a.a + (size_t)s * 64 * a.lda; }
   __device__ __forceinline__ long long tok_ld() const { return a.lda; }
-  __device__ __forceinline__ uint32_t tok_col(int c) const { return 2u * (uint32_t)min(tok + 8 * c, a.M - 8); }
+  __device__ __forceinline__ uint32_t tok_col(int c) const {
+    const int m = min(tok + 8 * c, a.M - 8);
+    return 2u * (uint32_t)(m < a.cut ? m : m - a.cut + a.ip);
+  }
   __device__ __forceinline__ const unsigned char* row_at(int s) const { return a.b0 + (size_t)s * 64 * a.ldb; }
   __device__ __forceinline__ long long row_ld() const { return a.ldb; }
   __device__ __forceinline__ uint32_t row_col(int c) const { return 2u * (uint32_t)min(col + 8 * c, a.N - 8); }
@@ -282,7 +286,7 @@ __global__ __launch_bounds__(256) void k_glu_mm_join(GluMmArgs a, int splits) {
 
 // 8 of a token's I a thread.
 template <int KIND>
-__global__ __launch_bounds__(256) void k_glu_grad(const float* saved, const void* dh, long long lddh, int T, int I, void* d) {
+__global__ __launch_bounds__(256) void k_glu_grad(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d) {
   typedef typename GluType<KIND>::type T16;
   const size_t all = (size_t)T * I;
   for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; i < all; i += (size_t)gridDim.x * 2048) {
@@ -297,9 +301,9 @@ __global__ __launch_bounds__(256) void k_glu_grad(const float* saved, const void
       dg[j] = e[j] * u[j] * (s * __builtin_fmaf(g[j], 1.0f - s, 1.0f));
       du[j] = e[j] * (g[j] * s);
     }
-    T16* to = static_cast<T16*>(d) + t * 2 * I + n;
+    T16* to = static_cast<T16*>(d) + t * 2 * ip + n;
     norm_store8(to, 8, dg);
-    norm_store8(to + I, 8, du);
+    norm_store8(to + ip, 8, du);
   }
 }
 
@@ -360,9 +364,9 @@ int glu_mm_kind(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream) {
 }
 
 template <int KIND>
-int glu_grad_kind(const float* saved, const void* dh, long long lddh, int T, int I, void* d, hipStream_t stream) {
+int glu_grad_kind(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d, hipStream_t stream) {
   const dim3 grid((unsigned)std::min<size_t>(((size_t)T * I + 2047) / 2048, 8192));
-  hipLaunchKernelGGL((k_glu_grad<KIND>), grid, dim3(256), 0, stream, saved, dh, lddh, T, I, d);
+  hipLaunchKernelGGL((k_glu_grad<KIND>), grid, dim3(256), 0, stream, saved, dh, lddh, T, I, ip, d);
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }
 #endif
