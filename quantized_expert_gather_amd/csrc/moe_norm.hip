@@ -7,7 +7,7 @@
 //   backward: n = r v, a = w dy: dr = v (a - n mean(a n)) + dtotal, dw = sum over tokens of dy n
 //
 // Bound by memory: a row is read once, held in registers as fp32 (8 channels a
-// chunk, up to 4 chunks a thread) through the reduction and written once.
+// chunk, up to 2 chunks a thread) through the reduction and written once.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -112,15 +112,15 @@ struct NormBackArgs {
   const void* dy;
   const void* dtotal;   // or NULL
   void* dx;
-  float* part;          // [groups][H] sums of dy n, or NULL
+  float* part;          // [workgroups][H] sums of dy n, or NULL
   long long ldr, ldy, ldt, ldd;
   int T, H;
   int dy_dtype, w_dtype;
   float eps;
 };
 
-// As above; a group of LANES threads takes rows `groups` apart and keeps its
-// sums of dy n in registers.  All of a row's reads are on their way before its
+// As above; LANES threads take one row after another and keep their sums of dy
+// n in registers.  All of a row's reads are on their way before its
 // sums (dtotal read behind them: 37 and not 34 us of 5003 x 2050).
 template <class TR, int LANES, int C>
 __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void k_rms_norm_back(NormBackArgs a) {
@@ -174,16 +174,27 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void k_rms_norm_back(Nor
       norm_store8(static_cast<TR*>(a.dx) + at * a.ldd + c, n, d[j]);
     }
   }
-  if (a.part) {
+  if (!a.part) return;
+  float* part = a.part + (size_t)blockIdx.x * a.H;
+  if constexpr (kRows > 1) {  // the rows' sums added in their order
+    __shared__ float sums[kRows][LANES * 8];
+    norm_store8(&sums[threadIdx.x / LANES][8 * l], 8, dw[0]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < LANES * 8 && c < a.H; c += kThreads) {
+      float s = sums[0][c];
+      for (int r = 1; r < kRows; ++r) s += sums[r][c];
+      part[c] = s;
+    }
+  } else {
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       const int c = 8 * (j * LANES + l);
-      norm_store8(a.part + first * a.H + c, a.H - c, dw[j]);
+      norm_store8(part + c, a.H - c, dw[j]);
     }
   }
 }
 
-// dw: the groups' sums added in a fixed order, 64 channels a workgroup.
+// dw: the workgroups' sums added in a fixed order, 64 channels a workgroup here.
 __global__ __launch_bounds__(1024) void k_rms_norm_dw(const float* part, int groups, int H, void* dw, int dtype) {
   __shared__ float waves[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -251,8 +262,12 @@ __global__ __launch_bounds__(256) void k_quant_blocks(const TX* x, long long ldx
   if (threadIdx.x == 0) scales[blockIdx.x] = s;
 }
 
-// Threads of a row and chunks of each.  With few rows 1024 threads take a row
-// of more than 2048 channels, which shortens the single row's way.
+// Threads of a row and chunks of each.  1024 threads for more than 4096
+// channels, since 256 with four chunks hold fewer rows in flight (us, 1024 and
+// 256: norm into codes 8192 x 8192 83 and 97, x 6144 72 and 74, x 4104 50 and
+// 46, 1 x 6144 3.1 and 6.9; gradient 8192 x 6144 110 and 127), and with few rows
+// for more than 2048 (1 x 4096 2.9 and 4.8 with two chunks, 256 x 4096 3.9 and
+// 4.2; 1024 x 4096 8.4 and 6.4).
 struct NormPlan {
   int lanes, chunks;
 };
@@ -262,8 +277,7 @@ NormPlan norm_plan(int T, int H) {
   if (n <= 64) return {64, 1};
   if (n <= 256) return {256, 1};
   if (n > 1024) return {1024, 2};
-  if (T <= 512) return {1024, 1};
-  return n <= 512 ? NormPlan{256, 2} : NormPlan{256, 4};
+  return n > 512 || T <= 512 ? NormPlan{1024, 1} : NormPlan{256, 2};
 }
 
 #define NORM_SWITCH(KERNEL, TYPE, PLAN, GRID, STREAM, ARGS)                                                       \
@@ -272,20 +286,20 @@ NormPlan norm_plan(int T, int H) {
     case 64 * 8 + 1: hipLaunchKernelGGL((KERNEL<TYPE, 64, 1>), GRID, dim3(256), 0, STREAM, ARGS); break;          \
     case 256 * 8 + 1: hipLaunchKernelGGL((KERNEL<TYPE, 256, 1>), GRID, dim3(256), 0, STREAM, ARGS); break;        \
     case 256 * 8 + 2: hipLaunchKernelGGL((KERNEL<TYPE, 256, 2>), GRID, dim3(256), 0, STREAM, ARGS); break;        \
-    case 256 * 8 + 4: hipLaunchKernelGGL((KERNEL<TYPE, 256, 4>), GRID, dim3(256), 0, STREAM, ARGS); break;        \
     case 1024 * 8 + 1: hipLaunchKernelGGL((KERNEL<TYPE, 1024, 1>), GRID, dim3(1024), 0, STREAM, ARGS); break;     \
     default: hipLaunchKernelGGL((KERNEL<TYPE, 1024, 2>), GRID, dim3(1024), 0, STREAM, ARGS); break;               \
   }
 
 int rows_of(const NormPlan& p) { return p.lanes >= 256 ? 1 : 256 / p.lanes; }
 
-// Groups of threads of the backward pass, each with a row of sums: as many
-// workgroups as keep the memory busy, few enough that their sums stay small
-// beside the rows.
+// Workgroups of the backward pass, each with a row of sums: as many as the
+// compute units hold at once, by their registers (us with 512, 768 and 1024:
+// 5003 x 2050 fp32 33.2 28.3 35.7, 8192 x 2048 31 26 24; 8192 x 6144, a unit
+// holds one, 110 with 256 and 111 with 512).
 int norm_back_groups(int T, int H) {
   const NormPlan p = norm_plan(T, H);
   const int rows = rows_of(p), blocks = (T + rows - 1) / rows;
-  return std::min(blocks, 512) * rows;
+  return std::min(blocks, p.lanes == 1024 ? 256 : p.chunks == 2 ? 768 : 1024);
 }
 
 int norm_status(int T, int H) {
@@ -379,7 +393,7 @@ extern "C" int moe_rms_norm_backward(const void* total, int total_dtype, long lo
     const NormPlan p = norm_plan(T, H);
     NormBackArgs a{total, weight, dy, dtotal, dx, dweight ? static_cast<float*>(workspace) : nullptr, ldr, ldy, ldt, ldd,
                    T, H, dy_dtype, weight_dtype, eps};
-    const dim3 grid((unsigned)(groups / rows_of(p)));
+    const dim3 grid((unsigned)groups);
     switch (total_dtype) {
       case MOE_Q4_DTYPE_BF16: NORM_SWITCH(k_rms_norm_back, __bf16, p, grid, stream, a) break;
       case MOE_Q4_DTYPE_F16: NORM_SWITCH(k_rms_norm_back, _Float16, p, grid, stream, a) break;

@@ -147,6 +147,12 @@ def test_norm_backward_sizes(T, H):
     check_backward(T, H, BF16, BF16, BF16, True)
 
 
+@pytest.mark.parametrize("T,H", [(20011, 100), (70000, 16), (9001, 500), (3000, 1030), (2500, 4090), (1500, 4104), (600, 9001)])
+def test_norm_backward_many_rows(T, H):
+    print("[case] norm backward rows", T, H, flush=True)
+    check_backward(T, H, F32, BF16, F32, True, seed=5)
+
+
 def check_backward(T, H, r, dy, w, dtotal, seed=0):
     rv, yv = rand((T, H), r, seed), rand((T, H), dy, seed + 1)
     wv = rand((H,), w, seed + 2) if w else None
