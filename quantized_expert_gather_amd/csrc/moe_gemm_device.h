@@ -1,6 +1,7 @@
-// Products C[t, n] = sum_k A[t, k] B[n, k] on the matrix cores, both operands
-// with their rows along k: 16-bit numbers, or E4M3 codes with a scale per
-// 128.  A step is 128 bytes of every row (64 or 128 elements).  Internal header.
+// Products C[t, n] = sum_k A[t, k] B[n, k] on the matrix cores: of 16-bit
+// numbers, the operands' rows along k or across, or of E4M3 codes with a scale
+// per 128.  A step is 128 bytes of every row (64 or 128 elements).  Internal
+// header.
 //
 //   gemm_tiles, gemm_tiles_scaled   many tokens: steps are copied into LDS
 //   gemm_rows                       few tokens: B straight into the operands
@@ -26,7 +27,6 @@ constexpr int kGemmStep = 128;  // bytes
 typedef __bf16 gemm_bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 gemm_f16x8 __attribute__((ext_vector_type(8)));
 typedef float gemm_f32x4 __attribute__((ext_vector_type(4)));
-typedef float gemm_f32x16 __attribute__((ext_vector_type(16)));
 typedef int gemm_i32x4 __attribute__((ext_vector_type(4)));
 typedef int gemm_i32x8 __attribute__((ext_vector_type(8)));
 
@@ -201,10 +201,9 @@ __device__ __forceinline__ void gemm_tiles(const GemmTiles& tiles, Source& sourc
   constexpr int kEarly = kMul * 7 / 8;  // instructions that the reads are spread over: the last have a latency's time
   static_assert(S::kRows % 64 == 0 && S::kTok % 64 == 0 && kPass == 32, "copies of whole passes");
   // each an object of its own: the compiler then knows that reads of one do not wait for copies into another
-  __shared__ __attribute__((aligned(1024))) unsigned char b0[S::kRows * kGemmStep], b1[S::kRows * kGemmStep], b2[S::kRows * kGemmStep],
-      b3[S::kRows * kGemmStep];
-  __shared__ __attribute__((aligned(1024))) unsigned char t0[S::kTok * kGemmStep], t1[S::kTok * kGemmStep], t2[S::kTok * kGemmStep],
-      t3[S::kTok * kGemmStep];
+  constexpr int kRowBytes = S::kRows * kGemmStep, kTokBytes = S::kTok * kGemmStep;
+  __shared__ __attribute__((aligned(1024))) unsigned char b0[kRowBytes], b1[kRowBytes], b2[BUFFERS > 2 ? kRowBytes : 1], b3[BUFFERS > 3 ? kRowBytes : 1];
+  __shared__ __attribute__((aligned(1024))) unsigned char t0[kTokBytes], t1[kTokBytes], t2[BUFFERS > 2 ? kTokBytes : 1], t3[BUFFERS > 3 ? kTokBytes : 1];
   static_assert(BUFFERS >= 2 && BUFFERS <= 4, "as many of them are used");
   auto rows_of = [&](int i) __attribute__((always_inline)) { return i == 0 ? b0 : i == 1 ? b1 : i == 2 ? b2 : b3; };
   auto toks_of = [&](int i) __attribute__((always_inline)) { return i == 0 ? t0 : i == 1 ? t1 : i == 2 ? t2 : t3; };

@@ -8,6 +8,9 @@
 //             dx = D [Wg; Wu], [dWg; dWu] = D^T x
 // The backward's products have their sums along the other axis of the weights,
 // or of both D and x, which the tiles read as they are.
+// 8192 x 6144 x 2048 bf16: forward with g and u kept 310 us (1330 TFLOP/s), dg
+// and du 36, dx 288 (1430), dw 297 (1390), where a large library product reaches
+// 1411; 4 tokens 8.1 us, 6.2 TB/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -309,7 +312,7 @@ __global__ __launch_bounds__(256) void k_glu_grad(const float* saved, const void
 
 template <int KIND>
 int glu_forward_kind(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t stream) {
-  if (rows) {
+  if (rows) {  // as many loads on their way as the registers of 16 waves hold
     const dim3 grid(a.I / 8);
     if (a.T <= 8)
       hipLaunchKernelGGL((k_glu_rows<KIND, 1, 16, 6>), grid, dim3(1024), 0, stream, a);

@@ -54,7 +54,8 @@ def norm_back(r=None, rd=0, ldr=None, w=None, wd=0, dy=None, yd=0, ldy=None, dt=
     (dict(T=-1), SHAPE), (dict(H=0), SHAPE), (dict(ldr=1), SHAPE), (dict(ldy=1), SHAPE), (dict(ldt=1), SHAPE),
     (dict(ldd=1), SHAPE), (dict(eps=-1.0), SHAPE), (dict(H=16385), UNSUP), (dict(rd=5), UNSUP), (dict(yd=5), UNSUP),
     (dict(wd=5), UNSUP), (dict(r=0), NULL), (dict(dy=0), NULL), (dict(dx=0), NULL), (dict(w=0), NULL), (dict(ws=0), WORK),
-    (dict(wn=4 * 200 * 4 - 1), WORK), (dict(ws=fake(6, 128)), ALIGN), (dict(dx=fake(4, 1)), ALIGN), (dict(dw=fake(5, 1)), ALIGN),
+    # one byte less than the documented need, which is a row of sums a workgroup (here one, of 200 floats)
+    (dict(wn=q.moe_rms_norm_backward_workspace_bytes(4, 200) - 1), WORK), (dict(wn=200 * 4 - 1), WORK), (dict(ws=fake(6, 128)), ALIGN), (dict(dx=fake(4, 1)), ALIGN), (dict(dw=fake(5, 1)), ALIGN),
     (dict(dt=fake(3, 1)), ALIGN), (dict(dx=fake(0)), ALIAS), (dict(dx=fake(3)), ALIAS), (dict(dw=fake(1)), ALIAS),
     (dict(ws=fake(2)), ALIAS), (dict(ws=fake(4)), ALIAS), (dict(dw=fake(6, 512)), ALIAS),
 ])
