@@ -711,6 +711,8 @@ __device__ __forceinline__ void gemm_put16(void* p, int left, uint4 v) {
       if (i < left) static_cast<uint16_t*>(p)[i] = (uint16_t)(u[i >> 1] >> (16 * (i & 1)));
   }
 }
+// Past the caches, where a token's four lanes write whole 64 bytes.
+__device__ __forceinline__ void gemm_put32_past(float* p, gemm_f32x4 v) { __builtin_nontemporal_store(v, reinterpret_cast<gemm_f32x4*>(p)); }
 __device__ __forceinline__ void gemm_put32(float* p, int left, gemm_f32x4 v) {
   typedef gemm_f32x4 f32x4_any __attribute__((aligned(4)));
   if (left >= 4) {

@@ -98,9 +98,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_glu_tiles(GluArgs a) {
     const bool split = a.tiles.splits > 1;
     float* keep = split ? a.part + (size_t)p.split * 2 * a.T * a.I : a.saved;
     T16* h = split ? nullptr : static_cast<T16*>(a.h);
+    // g and u are read again by a backward pass at the earliest (8192 x 6144 x 2048 309 us through the caches, 302 past
+    // them; of rows that are no multiple of 64 bytes, 1537 x 2056 x 1416, 31 and 39)
+    const bool past = !split && ((uintptr_t)a.saved | 4 * (uintptr_t)a.I) % 64 == 0;
     // (I is a multiple of 8: neighbours are all there or none)
     const auto keep4 = [&](size_t row, int t, int n, gemm_f32x4 v) __attribute__((always_inline)) {
-      if (t < a.T && n < a.I) gemm_put32(keep + (row + t) * a.I + n, 4, v);
+      if (t >= a.T || n >= a.I) return;
+      float* to = keep + (row + t) * a.I + n;
+      if (past)
+        gemm_put32_past(to, v);
+      else
+        gemm_put32(to, 4, v);
     };
     const auto put8 = [&](int t, int n, uint4 v) __attribute__((always_inline)) {
       if (t < a.T && n < a.I) gemm_put16(h + (size_t)t * a.ldh + n, 8, v);
