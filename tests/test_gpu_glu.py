@@ -290,6 +290,36 @@ def test_graph_stream_and_repeats(T):
         assert all(torch.equal(s, t) for s, t in zip(a, c))
 
 
+def test_saved_projections_at_any_start():
+    for T, I in ((200, 64), (1500, 1408)):  # rows of whole 64 bytes, at a start that is none
+        x, wg, wu, _ = (t.cuda() for t in problem(T, 136, I, BF16))
+        keep, room = torch.empty(2, T, I, device="cuda"), torch.full((2 * T * I + 64,), 7.0, device="cuda")
+        h = q.moe_glu(x, wg, wu, saved=keep)
+        part = room[4:4 + 2 * T * I].view(2, T, I)
+        assert torch.equal(q.moe_glu(x, wg, wu, saved=part), h) and torch.equal(part, keep)
+        assert (room[:4] == 7).all() and (room[4 + 2 * T * I:] == 7).all()
+
+
+def test_two_streams_at_once():
+    """Calls of both streams between each other, each with its own workspace."""
+    p, r = [[t.cuda() for t in problem(T, 1032, 520, F16)] for T in (300, 70)]
+    def run(a):
+        keep = torch.empty(2, a[0].shape[0], 520, device="cuda")
+        return [q.moe_glu(*a[:3], saved=keep), *q.moe_glu_backward(*a, saved=keep)]
+    refs = [run(p), run(r)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(8):
+        for i, a in enumerate((p, r)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(a))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(s, t) for s, t in zip(g, refs[i]))
+
+
 def test_backward_of_a_captured_step_is_refused(monkeypatch):
     x, wg, wu, dh = (t.cuda() for t in problem(4, 64, 64, BF16))
     x.requires_grad_()
