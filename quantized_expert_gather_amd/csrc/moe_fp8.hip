@@ -137,7 +137,14 @@ __global__ __launch_bounds__(256) void k_fp8_join(const float* part, const float
     const size_t t = i / N;
     const int n = (int)(i - t * N);
     float s = part[i];
-    for (int p = 1; p < splits; ++p) s += part[p * all + i];
+    for (int p = 1; p < splits; p += 4) {  // four parts' loads on their way together
+      float v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = part[(size_t)min(p + u, splits - 1) * all + i];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (p + u < splits) s += v[u];
+    }
     if (bias) s += bias[n];
     const size_t at = t * ldo + n;
     if (dtype == MOE_Q4_DTYPE_F32)

@@ -671,6 +671,22 @@ __device__ __forceinline__ void gemm_join_waves(float (&lds)[WAVES][J][G][64], c
 
 // ---- results ----
 
+// Eight neighbours' sums over the parts of a split K, added in their order; four
+// parts' loads are on their way together (15 parts of 16 x 1104: one by one 6.1 us).
+__device__ __forceinline__ void gemm_join8(const float* part, size_t stride, int splits, float (&s)[8]) {
+  norm_load8(part, 8, s);
+  for (int p = 1; p < splits; p += 4) {
+    float v[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) norm_load8(part + (size_t)min(p + u, splits - 1) * stride, 8, v[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (p + u < splits) s[j] += v[u][j];
+  }
+}
+
 // A lane's sums go straight to memory, four neighbours of a token's results at
 // a time: of a 16 x 16 tile those from 4 (lane / 16) on of token lane % 16.
 

@@ -185,12 +185,7 @@ __global__ __launch_bounds__(256) void k_glu_join(GluArgs a, int splits) {
     float s[2][8], v[8];
 #pragma unroll
     for (int up = 0; up < 2; ++up) {
-      norm_load8(a.part + up * all * 8 + i * 8, 8, s[up]);
-      for (int p = 1; p < splits; ++p) {
-        norm_load8(a.part + (2 * p + up) * all * 8 + i * 8, 8, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[up][j] += v[j];
-      }
+      gemm_join8(a.part + up * all * 8 + i * 8, 2 * all * 8, splits, s[up]);
       if (a.saved) norm_store8(a.saved + up * all * 8 + i * 8, 8, s[up]);
     }
     if (a.h) {
@@ -283,13 +278,8 @@ __global__ __launch_bounds__(256) void k_glu_mm_join(GluMmArgs a, int splits) {
   typedef typename GluType<KIND>::type T16;
   const size_t all = (size_t)a.M * a.N / 8;
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (size_t)gridDim.x * 256) {
-    float s[8], v[8];
-    norm_load8(a.part + i * 8, 8, s);
-    for (int p = 1; p < splits; ++p) {
-      norm_load8(a.part + (size_t)p * all * 8 + i * 8, 8, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] += v[j];
-    }
+    float s[8];
+    gemm_join8(a.part + i * 8, all * 8, splits, s);
     const int m = (int)(i * 8 / a.N), n = (int)(i * 8 - (size_t)m * a.N);
     norm_store8(static_cast<T16*>(m < a.cut ? a.out0 : a.out1) + (size_t)(m < a.cut ? m : m - a.cut) * a.ldo + n, 8, s);
   }
