@@ -4,8 +4,8 @@
 // one instruction and enters the fp32 accumulator by one multiply-add with
 // sx sw.  fp32 results, and those of few tokens, which memory bounds either
 // way, multiply the codes as bf16 (kGemmFp8Wide).
-// 8192 x 12288 x 6144: 545 us, 2270 TFLOP/s (a library product with one scale:
-// 468); 1 x 6144 x 6144: 8.2 us, 4.6 TB/s; 96 x 2050 x 4096 in fp32: 10.3 + 2.8.
+// 8192 x 12288 x 6144: 533 us, 2320 TFLOP/s (a library product with one scale:
+// 468); 1 x 6144 x 6144: 8.3 us, 4.5 TB/s; 96 x 2050 x 4096 in fp32: 10.8 + 2.4.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
