@@ -8,9 +8,9 @@
 //
 // Bound by memory: a row is read once, held in registers as fp32 (8 channels a
 // chunk, up to 2 chunks a thread) through the reduction and written once.
-// 8192 x 6144 bf16 with a residual into codes: 354 MB in 71.9 us, 4.9 TB/s, as
+// 8192 x 6144 bf16 with a residual into codes: 354 MB in 73.9 us, 4.8 TB/s, as
 // a large copy; 5003 x 2050 with an fp32 residual 21 us, its gradient 28 and 4;
-// one row of 6144 3.0 us; 12288 x 6144 fp32 in blocks of 128 x 128 68 us.
+// one row of 6144 3.0 us; 12288 x 6144 fp32 in blocks of 128 x 128 69 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -256,11 +256,11 @@ __global__ __launch_bounds__(256) void k_quant_blocks(const TX* x, long long ldx
   if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = most;
   __syncthreads();
   most = fmaxf(fmaxf(waves[0], waves[1]), fmaxf(waves[2], waves[3]));
-  const float s = norm_scale(most), inv = __builtin_amdgcn_rcpf(s);
+  const float s = norm_scale(most);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int row = row0 + 16 * j;
-    if (row < T) norm_store_codes(codes + (size_t)row * ldc + c, K - c, norm_pack8(v[j], inv));
+    if (row < T) norm_store_codes(codes + (size_t)row * ldc + c, K - c, norm_pack8(v[j], s));
   }
   if (threadIdx.x == 0) scales[blockIdx.x] = s;
 }
