@@ -601,8 +601,11 @@ size_t moe_glu_workspace_bytes(int T, int H, int I);
  *              as above
  *
  * dg and du enter the products as 16-bit numbers of `dtype`, rounded once; all
- * sums are fp32 and each gradient is rounded once.  T == 0 gives zero weight
- * gradients.
+ * sums are fp32 and each gradient is rounded once.  fp16 ones are kept over a
+ * power of two that puts the call's largest finite dg or du between 2^14 and
+ * 2^15, so that they neither pass fp16's range nor vanish from it before the
+ * sums: only those below 2^-28 of the largest have fewer bits.  T == 0 gives
+ * zero weight gradients.
  */
 int moe_glu_backward(int dtype, const void *x, long long ldx, const void *wg, const void *wu, long long ldw,
                      const void *dh, long long lddh, const float *saved, int T, int H, int I, void *dx,

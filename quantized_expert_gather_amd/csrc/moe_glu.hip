@@ -32,7 +32,7 @@ size_t glu_forward_part(int T, int H, int I) {
 }
 
 struct GluBackLayout {
-  size_t gu, d, part, total;
+  size_t gu, d, scale, part, total;
   int ip;  // dg's and du's places in a row of D: whole lines, since tiles of other rows' read twice as many
   GemmPlan dx, dw;
 };
@@ -44,6 +44,7 @@ GluBackLayout glu_back_layout(int T, int H, int I, bool saved) {
   size_t off = 0;
   w.gu = off; off = round256(off + (saved ? 0 : (size_t)2 * T * I * 4));
   w.d = off; off = round256(off + (size_t)T * 2 * w.ip * 2);
+  w.scale = off; off = round256(off + kGluScaleBytes);
   w.part = off;
   size_t part = saved ? 0 : glu_forward_part(T, H, I);
   if (w.dx.tiles.splits > 1) part = std::max(part, (size_t)w.dx.tiles.splits * T * H * 4);
@@ -160,11 +161,13 @@ extern "C" int moe_glu_backward(int dtype, const void* x, long long ldx, const v
     if ((st = glu_forward(f16, a, ws + w.part, stream))) return st;
     saved = a.saved;
   }
-  if ((st = (f16 ? glu_grad_f16 : glu_grad_bf16)(saved, dh, lddh, T, I, w.ip, ws + w.d, stream))) return st;
+  float* scale = reinterpret_cast<float*>(ws + w.scale);
+  if ((st = (f16 ? glu_grad_f16 : glu_grad_bf16)(saved, dh, lddh, T, I, w.ip, ws + w.d, scale, stream))) return st;
   GluMmArgs m{};
   m.a = ws + w.d;
   m.lda = 4LL * w.ip;
   m.ip = w.ip;
+  m.back = scale;
   m.N = H;
   if (dx) {  // dx = D [Wg; Wu]
     m.b0 = static_cast<const unsigned char*>(wg);

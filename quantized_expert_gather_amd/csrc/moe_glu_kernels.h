@@ -43,6 +43,7 @@ struct GluMmArgs {
   long long lda, ldb, ldo;           // ldo in elements
   int M, N, K, steps, cut;           // K of b0, and its steps
   int ip;                            // of D: du lies ip elements behind dg
+  const float* back;                 // fp16: what one of D's units is worth
   GemmTiles tiles;
 };
 
@@ -51,9 +52,11 @@ int glu_forward_bf16(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t
 int glu_forward_f16(const GluArgs& a, bool rows, const GemmPlan& p, hipStream_t stream);
 int glu_mm_bf16(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream);
 int glu_mm_f16(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream);
-// D [T][2 ip], dg and du of I each, from g, u and dh (lddh elements apart).
-int glu_grad_bf16(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d, hipStream_t stream);
-int glu_grad_f16(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d, hipStream_t stream);
+// D [T][2 ip], dg and du of I each, from g, u and dh (lddh elements apart);
+// `scale` is of fp16 (kGluScaleBytes): back, and the workgroups' largest.
+int glu_grad_bf16(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d, float* scale, hipStream_t stream);
+int glu_grad_f16(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d, float* scale, hipStream_t stream);
+constexpr int kGluMost = 1024, kGluScaleBytes = 256 + 4 * kGluMost;
 
 #ifdef MOE_GLU_INST
 
@@ -240,11 +243,21 @@ struct GluDwSource {
   __device__ __forceinline__ uint32_t row_col(int c) const { return 2u * (uint32_t)min(col + 8 * c, a.N - 8); }
 };
 
+template <int KIND>
+__device__ __forceinline__ gemm_f32x4 glu_back(gemm_f32x4 v, float back) {
+  if constexpr (KIND == kGemmF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= back;
+  }
+  return v;
+}
+
 template <int KIND, bool DW, int MT, int NT, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void k_glu_mm(GluMmArgs a) {
   using S = GemmShape<KIND, MT, NT, WM, WN>;
   typedef typename GluType<KIND>::type T16;
   std::conditional_t<DW, GluDwSource<S>, GluDxSource<S>> source{a};
+  const float back = KIND == kGemmF16 ? *a.back : 1.0f;
   gemm_tiles<S>(a.tiles, source, [&](const GemmPlace& p, const gemm_f32x4 (&acc)[MT][NT]) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = gemm_opaque(threadIdx.x & 63), kb = lane >> 4;
     const int m0 = p.tok * S::kTok + wave % WM * MT * 16 + (lane & 15), n0 = p.row * S::kRows + wave / WM * NT * 16;
@@ -264,7 +277,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_glu_mm(GluMmArgs a) {
           if (m < a.M && n + 16 < a.N) gemm_put32(part + (size_t)m * a.N + n + 16, 4, v);
         } else {
           const int n = n0 + 16 * nt + 8 * kb;
-          const uint4 q = gemm_eight16(gemm_pack4<T16>(u), gemm_pack4<T16>(v));
+          const uint4 q = gemm_eight16(gemm_pack4<T16>(glu_back<KIND>(u, back)), gemm_pack4<T16>(glu_back<KIND>(v, back)));
           if (m < a.M && n < a.N) gemm_put16(to + n, 8, q);
         }
       }
@@ -280,31 +293,103 @@ __global__ __launch_bounds__(256) void k_glu_mm_join(GluMmArgs a, int splits) {
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (size_t)gridDim.x * 256) {
     float s[8];
     gemm_join8(a.part + i * 8, all * 8, splits, s);
+    if constexpr (KIND == kGemmF16) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] *= *a.back;
+    }
     const int m = (int)(i * 8 / a.N), n = (int)(i * 8 - (size_t)m * a.N);
     norm_store8(static_cast<T16*>(m < a.cut ? a.out0 : a.out1) + (size_t)(m < a.cut ? m : m - a.cut) * a.ldo + n, 8, s);
   }
 }
 
-// 8 of a token's I a thread.
-template <int KIND>
-__global__ __launch_bounds__(256) void k_glu_grad(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d) {
-  typedef typename GluType<KIND>::type T16;
-  const size_t all = (size_t)T * I;
-  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; i < all; i += (size_t)gridDim.x * 2048) {
+// dg and du of 8 neighbours.
+template <class T16>
+struct GluGrad {
+  float g[8], u[8], e[8], dg[8], du[8];
+  __device__ __forceinline__ void load(const float* saved, const void* dh, long long lddh, size_t all, int I, size_t i) {
     const size_t t = i / I, n = i - t * I;
-    float g[8], u[8], e[8], dg[8], du[8];
     norm_load8(saved + i, 8, g);
     norm_load8(saved + all + i, 8, u);
     norm_load8(static_cast<const T16*>(dh) + t * lddh + n, 8, e);
+  }
+  __device__ __forceinline__ void compute() {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float s = glu_sigmoid(g[j]);
       dg[j] = e[j] * u[j] * (s * __builtin_fmaf(g[j], 1.0f - s, 1.0f));
       du[j] = e[j] * (g[j] * s);
     }
+  }
+};
+
+// dg and du enter the matrix cores as 16-bit numbers, rounded once: products of
+// fp32 numbers run at a fraction of that rate, and the gradients' error is 1.4
+// times that of their own rounding alone (bf16 2.35e-3 and 1.66e-3).
+// fp16 has not the range for them, though dh, u and the gradients are of it:
+// with a loss scale, dh = 10^4 and u = 20 give an infinity, and without one,
+// 10^-6 and 0.02 nothing, where the sum over the tokens is an ordinary number.
+// So they are kept over a power of two that puts the call's largest finite one
+// between 2^14 and 2^15: those down to 2^-28 of it have all of fp16's bits.  The
+// sums are multiplied by that power again, before their one rounding.  Finding
+// the largest reads g, u and dh once more (1537 x 1416: 5 us of 99).
+__device__ __forceinline__ float glu_most(float most, float v) { return fabsf(v) < __builtin_inff() ? fmaxf(most, fabsf(v)) : most; }
+__device__ __forceinline__ float glu_most256(float v) {  // of the workgroup's 256 threads
+  __shared__ float waves[4];
+  v = norm_max16(v);
+  v = fmaxf(v, __shfl_xor(v, 16));
+  v = fmaxf(v, __shfl_xor(v, 32));
+  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(waves[0], waves[1]), fmaxf(waves[2], waves[3]));
+}
+template <int KIND>
+__global__ __launch_bounds__(256) void k_glu_most(const float* saved, const void* dh, long long lddh, int T, int I, float* most) {
+  const size_t all = (size_t)T * I;
+  float m = 0.0f;
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8; i < all; i += (size_t)gridDim.x * 2048) {
+    GluGrad<typename GluType<KIND>::type> v;
+    v.load(saved, dh, lddh, all, I, i);
+    v.compute();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = glu_most(glu_most(m, v.dg[j]), v.du[j]);
+  }
+  m = glu_most256(m);
+  if (threadIdx.x == 0) most[blockIdx.x] = m;
+}
+
+// 8 of a token's I a thread.
+template <int KIND>
+__global__ __launch_bounds__(256) void k_glu_grad(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d,
+                                                  float* scale, int groups) {
+  typedef typename GluType<KIND>::type T16;
+  const size_t all = (size_t)T * I;
+  size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  GluGrad<T16> v;
+  if (i < all) v.load(saved, dh, lddh, all, I, i);
+  float up = 1.0f;
+  if constexpr (KIND == kGemmF16) {
+    float m = 0.0f;
+    for (int k = threadIdx.x; k < groups; k += 256) m = fmaxf(m, scale[64 + k]);
+    m = glu_most256(m);
+    // (where the largest is below 2^-86, both gradients are 0 in fp16)
+    up = m > 0.0f ? ldexpf(1.0f, min(14 - ilogbf(m), 100)) : 1.0f;
+    if (blockIdx.x == 0 && threadIdx.x == 0) scale[0] = 1.0f / up;
+  }
+  while (i < all) {
+    v.compute();
+    if constexpr (KIND == kGemmF16) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v.dg[j] *= up;
+        v.du[j] *= up;
+      }
+    }
+    const size_t t = i / I, n = i - t * I;
     T16* to = static_cast<T16*>(d) + t * 2 * ip + n;
-    norm_store8(to, 8, dg);
-    norm_store8(to + ip, 8, du);
+    norm_store8(to, 8, v.dg);
+    norm_store8(to + ip, 8, v.du);
+    i += (size_t)gridDim.x * 2048;
+    if (i < all) v.load(saved, dh, lddh, all, I, i);
   }
 }
 
@@ -365,9 +450,15 @@ int glu_mm_kind(const GluMmArgs& a, const GemmPlan& p, hipStream_t stream) {
 }
 
 template <int KIND>
-int glu_grad_kind(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d, hipStream_t stream) {
-  const dim3 grid((unsigned)std::min<size_t>(((size_t)T * I + 2047) / 2048, 8192));
-  hipLaunchKernelGGL((k_glu_grad<KIND>), grid, dim3(256), 0, stream, saved, dh, lddh, T, I, ip, d);
+int glu_grad_kind(const float* saved, const void* dh, long long lddh, int T, int I, int ip, void* d, float* scale, hipStream_t stream) {
+  const size_t all = ((size_t)T * I + 2047) / 2048;
+  const int groups = (int)std::min<size_t>(all, kGluMost);
+  if constexpr (KIND == kGemmF16) {
+    hipLaunchKernelGGL((k_glu_most<KIND>), dim3((unsigned)groups), dim3(256), 0, stream, saved, dh, lddh, T, I, scale + 64);
+    if (hipGetLastError() != hipSuccess) return MOE_Q4_ERR_LAUNCH;
+  }
+  const dim3 grid((unsigned)std::min<size_t>(all, 8192));
+  hipLaunchKernelGGL((k_glu_grad<KIND>), grid, dim3(256), 0, stream, saved, dh, lddh, T, I, ip, d, scale, groups);
   return hipGetLastError() == hipSuccess ? MOE_Q4_OK : MOE_Q4_ERR_LAUNCH;
 }
 #endif
