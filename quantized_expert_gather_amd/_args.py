@@ -62,6 +62,14 @@ def new(shape, strides, dtype, device):
     return torch.empty_strided(shape, strides, dtype=dtype, device=device)
 
 
+def written(*given):
+    """Marks the output tensors that a caller gave (not None) as changed in place,
+    as torch's own operations do: a backward pass that saved one then raises."""
+    for t in given:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def on_stream(stream, tensor):
     """Context of a call on a stream of the caller's (a torch stream or a HIP
     handle): what the call allocates belongs to that stream too, so neither

@@ -6,7 +6,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, matrix, new, on_stream, plane
+from ._args import DTYPES, array, call, current_handle, matrix, new, on_stream, plane, written
 
 F8 = torch.float8_e4m3fn
 _F8S = (F8,)
@@ -41,6 +41,7 @@ def moe_linear_fp8_forward(x, sx, w, sw, bias=None, out=None, out_dtype=None, wo
     sxp = array(sx, torch.float32, (L, G), "sx", dev)
     swp = array(sw, torch.float32, ((N + 127) // 128, G), "sw", dev)
     bp = 0 if bias is None else array(bias, torch.float32, (N,), "bias", dev)
+    given_output = out
     if out is None:
         od = torch.bfloat16 if out_dtype is None else out_dtype
         if od not in DTYPES:
@@ -66,4 +67,5 @@ def moe_linear_fp8_forward(x, sx, w, sw, bias=None, out=None, out_dtype=None, wo
     st = call(lib.moe_linear_fp8_forward, args, dev, current_handle(dev))
     if st:
         raise _q.MoeQ4Error(st, "moe_linear_fp8_forward")
+    written(given_output)
     return out

@@ -7,7 +7,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, new, on_stream, plane
+from ._args import DTYPES, array, call, current_handle, new, on_stream, plane, written
 from .router import _not_captured
 
 _X = (torch.bfloat16, torch.float16)
@@ -63,6 +63,7 @@ def _scratch(workspace, need, device):
 def _forward(x, wg, wu, out, saved, workspace):
     head, T, H, I = _operands(x, wg, wu)
     dev = x.device
+    given_outputs = out, saved
     out, hp, ldh = _result(out, (T, I), x.dtype, "out", dev)
     sp = 0 if saved is None else array(saved, torch.float32, (2, T, I), "saved", dev)
     lib = _q.lib()
@@ -70,6 +71,7 @@ def _forward(x, wg, wu, out, saved, workspace):
     st = call(lib.moe_glu_forward, (*head, T, H, I, hp, ldh, sp, wsp, wsn), dev, current_handle(dev))
     if st:
         raise _q.MoeQ4Error(st, "moe_glu_forward")
+    written(*given_outputs)
     return out
 
 
@@ -122,6 +124,7 @@ def moe_glu(x, wg, wu, out=None, saved=None, recompute: bool = False, workspace=
 def _backward(x, wg, wu, dh, saved, dx, dwg, dwu, workspace, need_x, need_w):
     head, T, H, I = _operands(x, wg, wu)
     dev = x.device
+    given_outputs = dx, dwg, dwu
     ep, lde, given = plane(dh, (x.dtype,), "dh")
     if given != (T, I) or dh.device != dev:
         raise ValueError(f"dh must be [{T}, {I}] on {dev}")
@@ -140,6 +143,7 @@ def _backward(x, wg, wu, dh, saved, dx, dwg, dwu, workspace, need_x, need_w):
     st = call(lib.moe_glu_backward, (*head, ep, lde, sp, T, H, I, dp, ldd, gp, up, wsp, wsn), dev, current_handle(dev))
     if st:
         raise _q.MoeQ4Error(st, "moe_glu_backward")
+    written(*given_outputs)
     return dx, dwg, dwu
 
 

@@ -8,7 +8,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, new, on_stream, plane
+from ._args import DTYPES, array, call, current_handle, new, on_stream, plane, written
 from .router import _not_captured
 
 F8 = torch.float8_e4m3fn
@@ -35,6 +35,7 @@ def _like(t, shape, out, dtypes, name):
 
 
 def _norm(x, weight, residual, eps, total, y, want_y, codes, scales, want_codes, where):
+    given_outputs = total, y, codes, scales
     xp, ldx, shape = plane(x, _TYPES, "x")
     T, H = shape
     dev = x.device
@@ -66,6 +67,7 @@ def _norm(x, weight, residual, eps, total, y, want_y, codes, scales, want_codes,
               current_handle(dev))
     if st:
         raise _q.MoeQ4Error(st, where)
+    written(*given_outputs)
     return y, total, codes, scales
 
 
@@ -115,7 +117,8 @@ def moe_rms_norm(x, weight=None, residual=None, eps: float = 1e-6, total=None, o
     type or fp32; weight [H] of any of the three, or None.  Returns y in
     ``out_dtype`` (x's type if not given), and with a residual (y, total):
     ``total`` is the sum in the residual's type; passing ``total=residual``
-    adds in place.
+    adds in place.  Autograd sees given tensors as changed: a backward pass
+    that needs what they held raises.
 
     y and total carry gradients to x, weight and residual where one of these
     requires one; given outputs, which cannot, are refused then.  A step
@@ -152,6 +155,7 @@ def moe_rms_norm_backward_workspace_bytes(T: int, H: int) -> int:
 
 
 def _back(total, weight, dy, dtotal, eps, dx, dweight, workspace, want_dweight):
+    given_outputs = dx, dweight
     rp, ldr, shape = plane(total, _TYPES, "total")
     T, H = shape
     dev = total.device
@@ -185,6 +189,7 @@ def _back(total, weight, dy, dtotal, eps, dx, dweight, workspace, want_dweight):
     st = call(_q.lib().moe_rms_norm_backward, args, dev, current_handle(dev))
     if st:
         raise _q.MoeQ4Error(st, "moe_rms_norm_backward")
+    written(*given_outputs)
     return dx, dweight
 
 
@@ -212,6 +217,7 @@ def moe_quantize_fp8(x, block_rows: int = 1, codes=None, scales=None, stream=Non
     xp, ldx, given = plane(x, _TYPES, "x")
     T, K = given
     dev = x.device
+    given_outputs = codes, scales
     rows = int(block_rows)
     if rows not in (1, 128):
         raise ValueError(f"block_rows {block_rows} is neither 1 nor 128")
@@ -225,4 +231,5 @@ def moe_quantize_fp8(x, block_rows: int = 1, codes=None, scales=None, stream=Non
     st = call(_q.lib().moe_quantize_fp8, (xp, DTYPES[x.dtype], ldx, T, K, rows, cp, ldc, sp), dev, current_handle(dev))
     if st:
         raise _q.MoeQ4Error(st, "moe_quantize_fp8")
+    written(*given_outputs)
     return codes, scales
