@@ -138,14 +138,43 @@ def moe_rms_norm(x, weight=None, residual=None, eps: float = 1e-6, total=None, o
     return y if residual is None else (y, total)
 
 
+class _StreamFunction(torch.autograd.Function):
+    """x + residual, which `add` computes beside the codes."""
+
+    @staticmethod
+    def forward(ctx, x, residual, add):
+        ctx.x_dtype = x.dtype
+        return add(x, residual)
+
+    @staticmethod
+    def backward(ctx, dtotal):
+        if torch.cuda.is_current_stream_capturing():  # (as _not_captured)
+            raise RuntimeError("backward() of a graph-captured step: moe_rms_norm_fp8's total has the gradient of x and residual itself")
+        return dtotal.to(ctx.x_dtype), dtotal, None
+
+
 def moe_rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6, total=None, codes=None, scales=None, stream=None):
     """:func:`moe_rms_norm` with an output in 8 bits: returns (codes
     float8_e4m3fn [T, H], scales fp32 [T, ceil(H / 128)]) as
     :func:`moe_linear_fp8_forward` takes them, and with a residual (codes,
-    scales, total).  No gradient."""
+    scales, total).  codes and scales carry no gradient; total, the stream that
+    goes on, carries its own to x and residual where one of these requires one
+    (a given total, which cannot, is refused then)."""
     if stream is not None and isinstance(x, torch.Tensor):
         with on_stream(stream, x):
             return moe_rms_norm_fp8(x, weight, residual, eps, total, codes, scales)
+    if residual is not None and torch.is_grad_enabled() and (_wants(x) or _wants(residual)):
+        if total is not None:
+            raise RuntimeError("moe_rms_norm_fp8: a given total carries no gradient, but x or residual requires one")
+        made = []
+
+        def add(x, residual):
+            _, t, c, s = _norm(x, weight, residual, eps, None, None, (), codes, scales, True, "moe_rms_norm_fp8")
+            made.extend((c, s))
+            return t
+
+        total = _StreamFunction.apply(x, residual, add)
+        return (*made, total)
     _, total, codes, scales = _norm(x, weight, residual, eps, total, None, (), codes, scales, True, "moe_rms_norm_fp8")
     return (codes, scales) if residual is None else (codes, scales, total)
 

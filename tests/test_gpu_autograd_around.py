@@ -63,3 +63,45 @@ def test_given_outputs_count_as_written():
     assert [t._version for t in inputs] == before
     with torch.inference_mode():
         q.moe_rms_norm(x, w, residual=r, total=total, out=e(6, 256))
+
+
+# ---- the residual stream beside codes ----
+
+@pytest.mark.parametrize("res", [BF16, F32])
+@pytest.mark.parametrize("which", ["x", "residual", "both"])
+def test_the_stream_beside_codes_carries_its_gradient(res, which):
+    x, r, w, dt = rand((6, 200)), rand((6, 200), res, 1), rand((200,), seed=2).requires_grad_(), rand((6, 200), res, 3)
+    plain = q.moe_rms_norm_fp8(x, w, residual=r)  # (the weight has none of the stream's gradient)
+    assert not plain[2].requires_grad
+    leaves = [t for t, n in ((x, "x"), (r, "residual")) if which in (n, "both")]
+    for t in leaves:
+        t.requires_grad_()
+    codes, scales, total = q.moe_rms_norm_fp8(x, w, residual=r)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip((codes, scales, total.detach()), plain))
+    assert total.requires_grad and not codes.requires_grad and not scales.requires_grad
+    (2 * total).backward(dt)
+    for t in leaves:
+        assert torch.equal(t.grad, (2 * dt).to(t.dtype))
+    assert w.grad is None
+    # given codes stay possible, a given total does not; without grad mode it does
+    given = torch.zeros(6, 200, dtype=torch.uint8, device="cuda").view(R.F8)
+    got = q.moe_rms_norm_fp8(x, w, residual=r, codes=given)
+    assert got[0] is given and torch.equal(given.view(torch.uint8), codes.view(torch.uint8)) and got[2].requires_grad
+    with pytest.raises(RuntimeError, match="gradient"):
+        q.moe_rms_norm_fp8(x, w, residual=r, total=torch.empty_like(dt))
+    with torch.no_grad():
+        assert not q.moe_rms_norm_fp8(x, w, residual=r, total=torch.empty_like(dt))[2].requires_grad
+    assert not q.moe_rms_norm_fp8(x, w)[0].requires_grad
+
+
+def test_a_layer_around_a_frozen_8_bit_projection():
+    """The stream's gradient past the projection, beside the norm's that follows it."""
+    x, r, w = rand((5, 256)).requires_grad_(), rand((5, 256), seed=1).requires_grad_(), rand((256,), seed=2)
+    wc, ws = q.moe_quantize_fp8(rand((256, 256), seed=3), block_rows=128)
+    codes, scales, total = q.moe_rms_norm_fp8(x, w, residual=r)
+    p = q.moe_linear_fp8_forward(codes, scales, wc, ws)
+    y, _ = q.moe_rms_norm(p, w, residual=total)
+    dy = rand((5, 256), seed=4)
+    y.backward(dy)
+    d, _ = q.moe_rms_norm_backward((p.float() + total.detach().float()).to(BF16), w, dy)
+    assert torch.equal(x.grad, d) and torch.equal(r.grad, d)
