@@ -5,6 +5,7 @@ launch, so checks read attributes once and build messages only on failure."""
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 #: torch dtype -> MOE_Q4_DTYPE_*
 DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
@@ -60,6 +61,15 @@ def array(t, dtype, shape, name: str, device) -> int:
 def new(shape, strides, dtype, device):
     """An uninitialised contiguous tensor (with its strides given, torch takes a shorter way)."""
     return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+
+def no_tangent(where, *tensors):
+    """Refuses dual tensors of forward-mode differentiation, whose tangents a
+    result would lose."""
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise RuntimeError(f"{where} has no forward-mode derivative, but an input has a tangent")
 
 
 def written(*given):

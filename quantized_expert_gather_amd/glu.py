@@ -7,7 +7,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, new, on_stream, plane, written
+from ._args import DTYPES, array, call, current_handle, new, no_tangent, on_stream, plane, written
 from .router import _not_captured
 
 _X = (torch.bfloat16, torch.float16)
@@ -114,6 +114,7 @@ def moe_glu(x, wg, wu, out=None, saved=None, recompute: bool = False, workspace=
     if stream is not None and isinstance(x, torch.Tensor):
         with on_stream(stream, x):
             return moe_glu(x, wg, wu, out, saved, recompute, workspace)
+    no_tangent("moe_glu", x, wg, wu)
     if torch.is_grad_enabled() and (_wants(x) or _wants(wg) or _wants(wu)):
         if out is not None or saved is not None:
             raise RuntimeError("moe_glu: given output tensors carry no gradient, but an input requires one")

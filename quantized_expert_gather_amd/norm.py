@@ -8,7 +8,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, new, on_stream, plane, written
+from ._args import DTYPES, array, call, current_handle, new, no_tangent, on_stream, plane, written
 from .router import _not_captured
 
 F8 = torch.float8_e4m3fn
@@ -129,6 +129,7 @@ def moe_rms_norm(x, weight=None, residual=None, eps: float = 1e-6, total=None, o
     if stream is not None and isinstance(x, torch.Tensor):
         with on_stream(stream, x):
             return moe_rms_norm(x, weight, residual, eps, total, out, out_dtype)
+    no_tangent("moe_rms_norm", x, weight, residual)
     if torch.is_grad_enabled() and (_wants(x) or _wants(weight) or _wants(residual)):
         if total is not None or out is not None:
             raise RuntimeError("moe_rms_norm: given output tensors carry no gradient, but an input requires one")
@@ -163,6 +164,8 @@ def moe_rms_norm_fp8(x, weight=None, residual=None, eps: float = 1e-6, total=Non
     if stream is not None and isinstance(x, torch.Tensor):
         with on_stream(stream, x):
             return moe_rms_norm_fp8(x, weight, residual, eps, total, codes, scales)
+    if residual is not None:
+        no_tangent("moe_rms_norm_fp8", x, residual)
     if residual is not None and torch.is_grad_enabled() and (_wants(x) or _wants(residual)):
         if total is not None:
             raise RuntimeError("moe_rms_norm_fp8: a given total carries no gradient, but x or residual requires one")

@@ -9,7 +9,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, matrix, new, on_stream
+from ._args import DTYPES, array, call, current_handle, matrix, new, no_tangent, on_stream
 
 
 def _score(score) -> int:
@@ -101,6 +101,7 @@ def moe_router_topk(logits, k: int, select_bias=None, score="softmax", renormali
     if stream is not None and isinstance(logits, torch.Tensor):
         with on_stream(stream, logits):
             return moe_router_topk(logits, k, select_bias, score, renormalize, scale, topk_ids, topk_weights)
+    no_tangent("moe_router_topk", logits)
     if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
         if topk_ids is not None or topk_weights is not None:
             raise RuntimeError("moe_router_topk: given output tensors carry no gradient, but logits requires one")
@@ -214,6 +215,7 @@ def moe_balance_loss(logits, topk_ids, coef: float = 1.0, score="softmax", seqs:
     if stream is not None and isinstance(logits, torch.Tensor):
         with on_stream(stream, logits):
             return moe_balance_loss(logits, topk_ids, coef, score, seqs, token_mask, workspace)
+    no_tangent("moe_balance_loss", logits)
     if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
         return _BalanceFunction.apply(logits, topk_ids, coef, score, seqs, token_mask, workspace)
     return _balance(logits, topk_ids, coef, score, seqs, token_mask, workspace)
