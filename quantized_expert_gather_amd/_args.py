@@ -58,6 +58,14 @@ def array(t, dtype, shape, name: str, device) -> int:
     raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
 
 
+def scratch(t, device):
+    """(pointer, bytes) of a given workspace."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    n = t.numel()
+    return array(t, torch.uint8, (n,), "workspace", device), n
+
+
 def new(shape, strides, dtype, device):
     """An uninitialised contiguous tensor (with its strides given, torch takes a shorter way)."""
     return torch.empty_strided(shape, strides, dtype=dtype, device=device)

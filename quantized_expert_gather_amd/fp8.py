@@ -6,7 +6,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, matrix, new, on_stream, plane, written
+from ._args import DTYPES, array, call, current_handle, matrix, new, on_stream, plane, scratch, written
 
 F8 = torch.float8_e4m3fn
 _F8S = (F8,)
@@ -56,8 +56,7 @@ def moe_linear_fp8_forward(x, sx, w, sw, bias=None, out=None, out_dtype=None, wo
     lib = _q.lib()
     wsp = wsn = 0
     if workspace is not None:
-        wsn = workspace.numel()
-        wsp = array(workspace, torch.uint8, (wsn,), "workspace", dev)
+        wsp, wsn = scratch(workspace, dev)
     else:
         wsn = lib.moe_linear_fp8_workspace_bytes(L, N, K)
         if wsn:

@@ -7,7 +7,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, new, no_tangent, on_stream, plane, written
+from ._args import DTYPES, array, call, current_handle, new, no_tangent, on_stream, plane, scratch, written
 from .router import _not_captured
 
 _X = (torch.bfloat16, torch.float16)
@@ -52,18 +52,20 @@ def _result(out, shape, dtype, name, device):
 def _scratch(workspace, need, device):
     """(tensor kept alive, pointer, bytes) of a call's workspace."""
     if workspace is not None:
-        n = workspace.numel()
-        return workspace, array(workspace, torch.uint8, (n,), "workspace", device), n
+        return workspace, *scratch(workspace, device)
     if not need:
         return None, 0, 0
     workspace = new((need,), (1,), torch.uint8, device)
     return workspace, workspace.data_ptr(), need
 
 
-def _forward(x, wg, wu, out, saved, workspace):
+def _forward(x, wg, wu, out, saved, workspace, keep=False):
+    """(h, the projections: `saved`, or made here with `keep`)."""
     head, T, H, I = _operands(x, wg, wu)
     dev = x.device
     given_outputs = out, saved
+    if keep:
+        saved = new((2, T, I), (T * I, I, 1), torch.float32, dev)
     out, hp, ldh = _result(out, (T, I), x.dtype, "out", dev)
     sp = 0 if saved is None else array(saved, torch.float32, (2, T, I), "saved", dev)
     lib = _q.lib()
@@ -72,17 +74,13 @@ def _forward(x, wg, wu, out, saved, workspace):
     if st:
         raise _q.MoeQ4Error(st, "moe_glu_forward")
     written(*given_outputs)
-    return out
+    return out, saved
 
 
 class _GluFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, wg, wu, recompute, workspace):
-        saved = None
-        if not recompute:
-            T, I = x.shape[0], wg.shape[0]
-            saved = new((2, T, I), (T * I, I, 1), torch.float32, x.device)
-        h = _forward(x, wg, wu, None, saved, workspace)
+        h, saved = _forward(x, wg, wu, None, None, workspace, not recompute)
         ctx.save_for_backward(x, wg, wu, saved)
         return h
 
@@ -119,7 +117,7 @@ def moe_glu(x, wg, wu, out=None, saved=None, recompute: bool = False, workspace=
         if out is not None or saved is not None:
             raise RuntimeError("moe_glu: given output tensors carry no gradient, but an input requires one")
         return _GluFunction.apply(x, wg, wu, recompute, workspace)
-    return _forward(x, wg, wu, out, saved, workspace)
+    return _forward(x, wg, wu, out, saved, workspace)[0]
 
 
 def _backward(x, wg, wu, dh, saved, dx, dwg, dwu, workspace, need_x, need_w):

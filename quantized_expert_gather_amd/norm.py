@@ -8,7 +8,7 @@ import torch
 
 import quantized_expert_gather_amd as _q
 
-from ._args import DTYPES, array, call, current_handle, new, no_tangent, on_stream, plane, written
+from ._args import DTYPES, array, call, current_handle, new, no_tangent, on_stream, plane, scratch, written
 from .router import _not_captured
 
 F8 = torch.float8_e4m3fn
@@ -76,7 +76,11 @@ def _wants(t) -> bool:
 
 
 def _out_types(x, out, out_dtype):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
     if out is not None:
+        if not isinstance(out, torch.Tensor):
+            raise TypeError("out must be a torch.Tensor")
         if out_dtype not in (None, out.dtype):
             raise ValueError("out is not of out_dtype")
         return _TYPES
@@ -215,8 +219,7 @@ def _back(total, weight, dy, dtotal, eps, dx, dweight, workspace, want_dweight):
             workspace = new((wsn,), (1,), torch.uint8, dev)
             wsp = workspace.data_ptr()
         else:
-            wsn = workspace.numel()
-            wsp = array(workspace, torch.uint8, (wsn,), "workspace", dev)
+            wsp, wsn = scratch(workspace, dev)
     args = (rp, DTYPES[total.dtype], ldr, wp, wd, yp, DTYPES[dy.dtype], ldy, tp, ldt, T, H, eps, dp, ldd, gp, wsp, wsn)
     st = call(_q.lib().moe_rms_norm_backward, args, dev, current_handle(dev))
     if st:

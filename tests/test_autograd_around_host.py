@@ -36,3 +36,20 @@ def test_forward_mode_is_refused(name):
             call(fw.make_dual(t, torch.ones_like(t)))
         with pytest.raises(ValueError, match="device"):  # without a tangent: the next check's
             call(t)
+
+
+def test_arguments_that_are_no_tensors():
+    x, w, z = arguments()
+    g = torch.zeros(4, 64, dtype=BF16).requires_grad_()
+    codes, s = torch.zeros(4, 64).to(torch.float8_e4m3fn), torch.zeros(4, 1)
+    for call in (lambda: q.moe_rms_norm([1.0]), lambda: q.moe_rms_norm(None), lambda: q.moe_rms_norm([1.0], stream=0),
+                 lambda: q.moe_rms_norm([1.0], w.clone().requires_grad_()), lambda: q.moe_rms_norm_fp8(3),
+                 lambda: q.moe_rms_norm_backward([1.0], None, x), lambda: q.moe_quantize_fp8("x"),
+                 lambda: q.moe_linear_fp8_forward([1], s, codes, s[:1]), lambda: q.moe_glu([1.0], x, x),
+                 lambda: q.moe_glu(3, g, x), lambda: q.moe_glu_backward(None, x, x, x)):
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            call()
+    for call in (lambda: q.moe_glu(g[0, 0], x, x), lambda: q.moe_glu(g, [1.0], x), lambda: q.moe_glu(g, x, None),
+                 lambda: q.moe_rms_norm(x, out=[1.0]), lambda: q.moe_rms_norm(x, out=5, out_dtype=BF16)):
+        with pytest.raises((TypeError, ValueError)):  # (x, on the host here, may be what is refused)
+            call()

@@ -105,3 +105,28 @@ def test_a_layer_around_a_frozen_8_bit_projection():
     y.backward(dy)
     d, _ = q.moe_rms_norm_backward((p.float() + total.detach().float()).to(BF16), w, dy)
     assert torch.equal(x.grad, d) and torch.equal(r.grad, d)
+
+
+# ---- arguments that are no tensors, behind the checks of those that are ----
+
+def test_arguments_that_are_no_tensors():
+    x, w, dy = rand((4, 256)), rand((256,), seed=1), rand((4, 256), seed=2)
+    wg, dh = rand((64, 256), seed=3), rand((4, 64), seed=4)
+    c, s = q.moe_quantize_fp8(x)
+    wc, ws = q.moe_quantize_fp8(wg, block_rows=128)
+    g = wg.clone().requires_grad_()
+    for call in (lambda: q.moe_rms_norm(x, 3.0), lambda: q.moe_rms_norm(x, w, residual=[1.0]), lambda: q.moe_rms_norm(x, w, out=[1.0]),
+                 lambda: q.moe_rms_norm(x, w, residual=x, total=5), lambda: q.moe_rms_norm_fp8(x, codes=[1], scales=s),
+                 lambda: q.moe_rms_norm_fp8(x, scales=[1]), lambda: q.moe_rms_norm_backward(x, w, [1.0]),
+                 lambda: q.moe_rms_norm_backward(x, w, dy, dtotal=[1.0]), lambda: q.moe_rms_norm_backward(x, w, dy, workspace=bytes(4096)),
+                 lambda: q.moe_rms_norm_backward(x, w, dy, dx=3), lambda: q.moe_rms_norm_backward(x, w, dy, dweight=3),
+                 lambda: q.moe_quantize_fp8(x, codes=[1]), lambda: q.moe_quantize_fp8(x, scales=[1]),
+                 lambda: q.moe_linear_fp8_forward(c, [1], wc, ws), lambda: q.moe_linear_fp8_forward(c, s, wc, [1]),
+                 lambda: q.moe_linear_fp8_forward(c, s, wc, ws, bias=[1.0]), lambda: q.moe_linear_fp8_forward(c, s, wc, ws, out=[1.0]),
+                 lambda: q.moe_linear_fp8_forward(c, s, wc, ws, workspace=bytes(64)), lambda: q.moe_glu(x, [1.0], wg),
+                 lambda: q.moe_glu(x, g, 3), lambda: q.moe_glu(x, [1.0], g), lambda: q.moe_glu(x, wg, wg, out=[1.0]),
+                 lambda: q.moe_glu(x, wg, wg, saved=[1.0]), lambda: q.moe_glu(x, wg, wg, workspace=bytes(64)),
+                 lambda: q.moe_glu_backward(x, wg, wg, [1.0]), lambda: q.moe_glu_backward(x, wg, wg, dh, dx=[1.0]),
+                 lambda: q.moe_glu_backward(x, wg, wg, dh, dwg=[1.0]), lambda: q.moe_glu_backward(x, wg, wg, dh, workspace=bytes(1 << 20))):
+        with pytest.raises(TypeError):
+            call()
