@@ -1,7 +1,8 @@
 """The gated block's gradient in fp16 where dg = dh u silu'(g) and du = dh
-silu(g) pass fp16's range and the gradients do not (needs an MI355X).
+silu(g) pass fp16's range and the gradients do not, and the weights' gradients
+of a few tokens far apart (needs an MI355X).
 
-dg and du are 16-bit numbers over a power of two that puts the call's largest
+fp16's dg and du are numbers over a power of two that puts the call's largest
 at 2^14 or above: half a step of fp16 each, and at least 2^-25 of that unit, so
 2^-39 of the largest one.  Everything else is as in around_refs."""
 
@@ -156,3 +157,33 @@ def test_graphs_take_the_scale_of_their_own_values():
         torch.cuda.synchronize()
         for a, b in zip(got, q.moe_glu_backward(x, wg, wu, dh)):
             assert torch.equal(a.isfinite(), b.isfinite()) and torch.equal(a[a.isfinite()], b[b.isfinite()])
+
+
+@pytest.mark.parametrize("T,H,I", [(300_000, 8192, 8), (5000, 264, 72), (700, 1032, 136)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_weight_gradients_of_a_few_tokens(T, H, I, dtype):
+    """dh is 0 but for a few tokens, at both ends and about 4 GB on in x: the weights' gradients are sums of that many
+    terms, and their bounds those terms'."""
+    print("[case] glu few tokens", T, H, I, dtype, flush=True)
+    mid = min(T // 2, (1 << 32) // (2 * H))
+    rows = torch.tensor([0, 1, mid - 1, mid, mid + 1, T - 65, T - 64, T - 2, T - 1])
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.empty(T, H, device="cuda", dtype=dtype)
+    for i in range(0, T, 20_000):
+        x[i:i + 20_000] = torch.randn(min(20_000, T - i), H, generator=g, device="cuda")
+    _, wg, wu, _ = problem(8, H, I, 1.0, 1.0, 1.0)
+    wg, wu = wg.to(dtype), wu.to(dtype)
+    some = torch.randn(len(rows), I, generator=g, device="cuda").to(dtype)
+    dh = torch.zeros(T, I, device="cuda", dtype=dtype)
+    dh[rows.cuda()] = some
+    dx, dwg, dwu = q.moe_glu_backward(x, wg.cuda(), wu.cuda(), dh)
+    few = x[rows.cuda()].cpu(), wg, wu, some.cpu()
+    refs, bounds = R.glu_backward(*few)
+    R.check(dx[rows.cuda()], refs[0], bounds[0], dtype)
+    for got, which in ((dwg, 1), (dwu, 2)):
+        R.check(got, refs[which], bounds[which], dtype)
+        for i in range(len(rows)):  # the check finds each token's loss (one element off is enough, and a tenth of them are)
+            keep = [j for j in range(len(rows)) if j != i]
+            lost = R.glu_backward(few[0][keep], wg, wu, few[3][keep])[0][which]
+            tol = bounds[which] + R.HALF[dtype] * (refs[which].abs() + bounds[which])
+            assert ((lost - refs[which]).abs() > tol).double().mean() > 0.1

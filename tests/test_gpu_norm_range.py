@@ -1,4 +1,5 @@
-"""Rounding of the norm's and the quantization's codes (needs an MI355X)."""
+"""Rounding of the norm's and the quantization's codes, and the norm's weight
+gradient where a few rows alone count (needs an MI355X)."""
 
 import pytest
 import torch
@@ -76,3 +77,23 @@ def test_values_beside_an_infinity():
     assert torch.isnan(c[0, 5]) and torch.isnan(c[1, 200]) and torch.isinf(s[0, 0]) and torch.isinf(s[1, 1])
     c[0, 5] = c[1, 200] = 0
     assert (c[0, :128] == 0).all() and (c[1, 128:] == 0).all() and (c[0, 128:] == 448).all() and (c[1, :128] == 448).all()
+
+
+# Rows of every launch shape: several a workgroup, one after another, and a last round that is not full.
+@pytest.mark.parametrize("T,H", [(20011, 100), (70000, 16), (9001, 500), (3000, 1030), (2500, 4090), (1500, 4104), (600, 9001)])
+@pytest.mark.parametrize("where", ["last", "first", "spread"])
+def test_weight_gradient_of_a_few_rows(T, H, where):
+    """dy is 0 but in a few rows, so dw is a sum of that many terms and its bound theirs: a lost row shows."""
+    g = torch.Generator().manual_seed(T + H)
+    rows = {"last": range(T - 4, T), "first": range(4), "spread": [0, T // 3, T // 2, T - 299, T - 17, T - 16, T - 2, T - 1]}[where]
+    rows = torch.tensor(list(rows))
+    r, w = torch.randn(T, H, generator=g), torch.randn(H, generator=g)
+    dy = torch.zeros(T, H)
+    dy[rows] = 2.0 ** torch.arange(len(rows)).float().unsqueeze(1) * (1 + torch.rand(len(rows), H, generator=g))
+    _, dw = q.moe_rms_norm_backward(r.cuda(), w.cuda(), dy.cuda())
+    _, _, ref, bound = R.norm_backward(r[rows], w, dy[rows], None, 1e-6, rounds=len(rows))
+    R.check(dw, ref, bound)
+    for i in range(len(rows)):  # the check finds each row's loss
+        rest = torch.cat((rows[:i], rows[i + 1:]))
+        lost = R.norm_backward(r[rest], w, dy[rest], None, 1e-6)[2]
+        assert ((lost - ref).abs() > bound + R.U * (ref.abs() + bound)).double().mean() > 0.9
