@@ -52,7 +52,8 @@ extern "C" {
 #define MOE_Q4_ERR_ALIGN 4       /* a pointer misses its alignment (see moe_swiglu_q4_forward) */
 #define MOE_Q4_ERR_WORKSPACE 5   /* workspace NULL or smaller than moe_swiglu_q4_workspace_bytes */
 #define MOE_Q4_ERR_LAUNCH 6      /* a HIP launch or runtime call failed                       */
-#define MOE_Q4_ERR_ALIAS 7       /* `out` overlaps an input or the workspace                  */
+#define MOE_Q4_ERR_ALIAS 7       /* `out` overlaps an input or the workspace: from the first
+                                  * element to the last, gaps between rows included           */
 #define MOE_Q4_ERR_SCRATCH 8     /* the shape needs more workspace than the allocation-free   */
                                  /* entry point's scratch holds (MOE_Q4_NOALLOC_SCRATCH_BYTES) */
 
@@ -476,7 +477,9 @@ int moe_balance_loss_backward(const void *logits, int logits_dtype, long long ld
  *
  * Either of y and codes may be left out.  Arrays need their elements'
  * alignment only.  Sums are fp32 (a row whose squares' sum passes fp32 gives
- * zeros), y is rounded once, codes are made of y in fp32.  A NaN has a NaN
+ * zeros, squares that vanish in fp32 count as 0 beside eps), y is rounded once,
+ * codes are made of y in fp32: of its quotient by s, rounded to fp32 and then
+ * to nearest even.  A NaN has a NaN
  * code; an infinite y makes its block's scale infinite and its values NaN.
  * Results are deterministic.  H <= MOE_Q4_NORM_MAX_H, T <= MOE_Q4_ROUTER_MAX_T;
  * eps >= 0.

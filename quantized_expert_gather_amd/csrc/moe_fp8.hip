@@ -4,8 +4,9 @@
 // one instruction and enters the fp32 accumulator by one multiply-add with
 // sx sw.  fp32 results, and those of few tokens, which memory bounds either
 // way, multiply the codes as bf16 (kGemmFp8Wide).
-// 8192 x 12288 x 6144: 533 us, 2320 TFLOP/s (a library product with one scale:
-// 468); 1 x 6144 x 6144: 8.3 us, 4.5 TB/s; 96 x 2050 x 4096 in fp32: 10.8 + 2.4.
+// 8192 x 12288 x 6144: 530 to 545 us, 2300 TFLOP/s, sustained 502 (a library
+// product with one scale 386), with fp32 results 1145; 1 x 6144 x 6144: 8.2 us, 4.6 TB/s;
+// 16 tokens 11.6, 24 tokens 12.5 + 1.8; 96 x 2050 x 4096 in fp32: 10.4 + 2.2.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -166,6 +167,7 @@ int fp8_status(int L, int N, int K) {
 // Measured with 256 tiles and with as many as are held at once, of 8, 32 and
 // 128 steps.
 constexpr GemmCosts kFp8Costs = {{1.62f, 0, 0, 0, 0.64f, 0.41f}, {0, 0, 0, 0, 0.47f, 0.32f}, {8.5f, 0, 0, 0, 4.3f, 3.5f}, {1, 0, 0, 0, 2, 3}};
+// (tiles of 256 x 256 were not built for it)
 constexpr GemmCosts kFp8WideCosts = {{0, 0, 0, 0, 1.02f, 0.69f}, {0, 0, 0, 0, 0.83f, 0.465f}, {0, 0, 0, 0, 7.0f, 5.0f}, {0, 0, 0, 0, 2, 3}};
 // Few tokens by rows, whose weights then pass the card once at the memory's
 // rate; from 17 tokens on the tiles' matrix instructions are the faster for

@@ -19,7 +19,9 @@ int glu_status(int T, int H, int I) {
 }
 
 // Few tokens by rows (us by rows with 32 tokens, by tiles with 33: 2056 x 1416 6.9
-// and 11.2, 6144 x 2048 14.2 and 16.9, 4096 x 4096 19.0 and 17.7).
+// and 11.2, 6144 x 2048 14.2 and 16.9, 4096 x 4096 19.0 and 17.7: with
+// such weights the tiles would be the faster before that; their size is not looked
+// at).
 bool glu_by_rows(int T) { return T <= 32; }
 int glu_steps(long k) { return (int)((2 * k + kGemmStep - 1) / kGemmStep); }
 GemmPlan glu_forward_plan(int T, int H, int I) { return gemm_plan(kGemmCosts16, T, 2 * I, glu_steps(H)); }

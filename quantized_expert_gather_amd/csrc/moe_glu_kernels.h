@@ -8,9 +8,10 @@
 //             dx = D [Wg; Wu], [dWg; dWu] = D^T x
 // The backward's products have their sums along the other axis of the weights,
 // or of both D and x, which the tiles read as they are.
-// 8192 x 6144 x 2048 bf16: forward 274 us (1500 TFLOP/s), with g and u kept 302,
-// dg and du 33, dx 291 (1420), dw 302 (1370), where a large library product
-// reaches 1411; 4 tokens 8.2 us, 6.1 TB/s.
+// 8192 x 6144 x 2048 bf16, each kernel by itself: forward with g and u kept 317
+// us (1300 TFLOP/s), dg and du 40, dx 317, dw 320, a call of all four 1031; the
+// forward alone, sustained, 274 to 281 (1470 to 1500), where a library product
+// of its size reaches 1598; 4 tokens 8.2 us, 6.1 TB/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
