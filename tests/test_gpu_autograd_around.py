@@ -130,3 +130,11 @@ def test_arguments_that_are_no_tensors():
                  lambda: q.moe_glu_backward(x, wg, wg, dh, dwg=[1.0]), lambda: q.moe_glu_backward(x, wg, wg, dh, workspace=bytes(1 << 20))):
         with pytest.raises(TypeError):
             call()
+
+
+def test_backward_of_a_captured_stream_is_refused(monkeypatch):
+    x, r = rand((4, 128)).requires_grad_(), rand((4, 128), seed=1)
+    total = q.moe_rms_norm_fp8(x, residual=r)[2]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="graph-captured"):
+        total.backward(r)
